@@ -16,6 +16,7 @@ import torch
 own = False
 
 DEV = "cuda"
+_OUT = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
 # ------------------------------------------------------------------ cases
@@ -37,10 +38,10 @@ def listed():
         {"name": "rows_tokens", "op": "rows", "S": 64, "E": 64, "active": 40, "K": 2048, "N": 1408, "transposed": False},
         # the data gradient of a middling batch (weights read transposed), sizes off the tiles
         {"name": "rows_dgrad", "op": "rows", "S": 5003, "E": 12, "active": 11, "K": 1400, "N": 1000, "transposed": True},
-        # the weight gradient of a training batch (fp32, for an optimiser that accumulates)
-        {"name": "wgrad_batch", "op": "wgrad", "S": 32768, "E": 16, "active": 16, "K": 2048, "N": 2048},
-        # the weight gradient of a short ragged micro-batch, an idle expert
-        {"name": "wgrad_ragged", "op": "wgrad", "S": 1003, "E": 8, "active": 7, "K": 640, "N": 384},
+        # the weight gradient of a training batch, in the weights' type
+        {"name": "wgrad_batch", "op": "wgrad", "S": 32768, "E": 16, "active": 16, "K": 2048, "N": 2048, "out": "bf16"},
+        # the weight gradient of a short ragged micro-batch, an idle expert; fp32, to be summed over micro-batches
+        {"name": "wgrad_ragged", "op": "wgrad", "S": 1003, "E": 8, "active": 7, "K": 640, "N": 384, "out": "f32"},
         # one decoded token through a large 4-bit projection
         {"name": "w4_token", "op": "w4", "S": 1, "E": 1, "active": 1, "K": 8192, "N": 28672, "format": "int4", "G": 128},
         # a few decoded tokens through 4-bit experts
@@ -76,6 +77,8 @@ def draw(rng):
                  "K": _width(rng, 128, 4096), "N": _width(rng, 128, 4096)}
             if op == "rows":
                 c["transposed"] = rng.random() < 0.5
+            else:  # short micro-batches keep their gradients in fp32, to be summed
+                c["out"] = "f32" if S // c["active"] < 256 else "bf16"
             if S * c["K"] * c["N"] > 32768 * 2048 * 4096 or E * c["K"] * c["N"] > 1 << 27:
                 continue
         else:
@@ -179,7 +182,7 @@ def prepare(case, seed):
     elif op == "wgrad":
         s["A"] = _bf16(g, S, K)
         s["B"] = _bf16(g, S, N)
-        s["D"] = torch.empty(E, K, N, dtype=torch.float32, device=DEV) if own else None
+        s["D"] = torch.empty(E, K, N, dtype=_OUT[case["out"]], device=DEV) if own else None
     else:
         G = case["G"]
         s["x"] = _bf16(g, S, K)
@@ -246,7 +249,7 @@ def _run_plain(s):
         for n in s["sizes"]:
             out.append(A[at:at + n].t() @ B[at:at + n])
             at += n
-        return {"D": torch.stack(out)}
+        return {"D": torch.stack(out).to(_OUT[s["out"]])}
     out, at = [], 0
     x = s["x"].float()
     for e, n in enumerate(s["sizes"]):
@@ -297,7 +300,8 @@ def work(case):
     if op == "rows":
         return {"bytes": 2 * S * K + 2 * used * K * N + 2 * S * N, "flops": 2 * S * K * N}
     if op == "wgrad":
-        return {"bytes": 2 * S * K + 2 * S * N + 4 * E * K * N, "flops": 2 * S * K * N}
+        size = 2 if case["out"] == "bf16" else 4
+        return {"bytes": 2 * S * K + 2 * S * N + size * E * K * N, "flops": 2 * S * K * N}
     per = {"int4": 2, "int4_zeros": 3, "e2m1": 1}[case["format"]]
     return {"bytes": 2 * S * K + used * N * (K // 2 + per * -(-K // case["G"])) + 2 * S * N, "flops": 2 * S * K * N}
 
