@@ -408,6 +408,57 @@ tg_status tg_gemm_splitk_static(const void *A, const void *B, float *C,
                                 int64_t batch, int64_t strideA, int64_t strideB,
                                 int64_t strideC, int32_t split_k, tg_stream_t stream);
 
+/* ---------------------------------------------------------------- experts
+ * Operators of a mixture-of-experts layer (no page of the method has a
+ * counterpart: the layer's products are this library's contraction over
+ * ragged groups of rows, the rest is what such a layer needs around them).
+ *
+ * An ORDER sorts the T x k assignments ids[t][j] (token t to expert
+ * ids[t][j]; flat number f = t*k + j) by expert, stably: three int32 device
+ * arrays
+ *     offsets[E + 1]  expert e's rows are offsets[e] .. offsets[e+1] - 1
+ *     source[T * k]   the flat assignment of sorted row s, -1 behind the last
+ *     slot[T][k]      the sorted row of assignment (t, j), -1 if dropped
+ * An id outside [0, E) drops its assignment.  ids is T x k with row pitch
+ * ld_ids (elements of id_bytes = 4 or 8).  T * k <= 2^31 - 1, E <= 1024
+ * (TG_ERR_UNSUPPORTED above).  Rows are D elements of a tg_dtype with a
+ * pitch in elements, any alignment of whole elements, D <= 2^22.  Rows that
+ * are 16-byte aligned multiples of 16 bytes are moved fastest.  Outputs may
+ * not overlap inputs or one another (TG_ERR_INVALID_ARG).  Slots out of
+ * range are treated as dropped and never read or written. */
+
+/* The order of ids.  T == 0 gives offsets of zeros. */
+tg_status tg_expert_sort(const void *ids, int32_t id_bytes, int64_t ld_ids, int64_t T, int64_t k, int64_t E,
+                         int32_t *offsets, int32_t *source, int32_t *slot, tg_stream_t stream);
+
+/* The order, and x's rows in it: xs[s] = x[source[s] / k] (s < T * k), rows
+ * behind the last expert zero. */
+tg_status tg_expert_dispatch(const void *ids, int32_t id_bytes, int64_t ld_ids, int64_t T, int64_t k, int64_t E,
+                             int32_t *offsets, int32_t *source, int32_t *slot, const void *x, int64_t ld_x,
+                             int64_t D, int32_t dtype, void *xs, int64_t ld_xs, tg_stream_t stream);
+
+/* The rows alone, in an order made before. */
+tg_status tg_expert_gather(const void *x, int64_t ld_x, int64_t D, int32_t dtype, int64_t T, int64_t k, int64_t E,
+                           const int32_t *offsets, const int32_t *slot, void *xs, int64_t ld_xs, tg_stream_t stream);
+
+/* y[t] = sum_j weights[t][j] * ys[slot[t][j]], summed in the order of j in
+ * fp32 and rounded once; a dropped assignment adds nothing, whatever its
+ * weight.  ys has S rows; weights (fp32, row pitch ld_w) may be NULL: ones,
+ * which is also the gradient of tg_expert_dispatch's row copy. */
+tg_status tg_expert_combine(const void *ys, int64_t ld_ys, int32_t ys_type, int64_t S, const int32_t *slot,
+                            const float *weights, int64_t ld_w, int64_t T, int64_t k, int64_t D, void *y, int64_t ld_y,
+                            int32_t y_type, tg_stream_t stream);
+
+/* The gradient of tg_expert_combine for dy = dL/dy:
+ *     dys[slot[t][j]] = weights[t][j] * dy[t]       (T * k rows; others zero)
+ *     dweights[t][j]  = sum_d dy[t][d] ys[slot[t][j]][d]     (dropped: zero)
+ * The sum is fp32 in a fixed order.  dweights may be NULL (ys is then not
+ * read and may be NULL), weights too (ones). */
+tg_status tg_expert_combine_grad(const void *dy, int64_t ld_dy, int32_t dy_type, const void *ys, int64_t ld_ys,
+                                 int32_t ys_type, const int32_t *offsets, const int32_t *slot, const float *weights,
+                                 int64_t ld_w, int64_t T, int64_t k, int64_t E, int64_t D, void *dys, int64_t ld_dys,
+                                 int32_t dys_type, float *dweights, int64_t ld_dw, tg_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the device error words that
  * the kernels' watchdog writes: the one of `stream`'s workspace, and the one
  * of tg_gemm_splitk_static on the current device.  TG_ERR_TIMEOUT if a wait

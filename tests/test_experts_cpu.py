@@ -1,0 +1,84 @@
+"""Refusals of the expert operators: every argument check of the C entry points
+runs before any CUDA call, so it is tested without a GPU; and the Python
+wrappers' checks of types and shapes on CPU tensors."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import tiled_gemm_codegen_gb300 as tg
+from tiled_gemm_codegen_gb300 import _abi
+
+INVALID, UNSUPPORTED = tg.TG_ERR_INVALID_ARG, tg.TG_ERR_UNSUPPORTED
+# placeholder addresses, far apart
+X, XS, IDS, OFF, SRC, SLOT, W, DW, DY = (0x1000000000 * i for i in range(1, 10))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _abi.load(build_if_missing=True)
+
+
+def _dispatch(lib, **kw):
+    a = dict(ids=IDS, id_bytes=8, ld_ids=4, T=10, k=4, E=8, offsets=OFF, source=SRC, slot=SLOT, x=X, ld_x=64, D=64,
+             dtype=tg.TG_BF16 if hasattr(tg, "TG_BF16") else 1, xs=XS, ld_xs=64)
+    a.update(kw)
+    return lib.tg_expert_dispatch(*a.values(), None)
+
+
+def test_dispatch_refusals(lib):
+    for kw in (dict(T=-1), dict(k=0), dict(E=0), dict(id_bytes=2), dict(ids=None), dict(ids=IDS + 4), dict(offsets=None),
+               dict(source=None), dict(slot=None), dict(ld_ids=3), dict(x=None), dict(xs=None), dict(ld_x=63),
+               dict(ld_xs=63), dict(x=X + 1), dict(xs=XS + 1), dict(dtype=2), dict(D=-1), dict(T=1 << 30),
+               dict(xs=X), dict(xs=X + 64), dict(slot=SRC), dict(offsets=XS + 100), dict(source=IDS), dict(T=1 << 40)):
+        assert _dispatch(lib, **kw) == INVALID, kw
+    assert _dispatch(lib, E=1025) == UNSUPPORTED
+    assert _dispatch(lib, D=(1 << 22) + 1, ld_x=1 << 23, ld_xs=1 << 23) == UNSUPPORTED
+
+
+def test_sort_and_gather_refusals(lib):
+    assert lib.tg_expert_sort(IDS, 4, 4, 10, 4, 1025, OFF, SRC, SLOT, None) == UNSUPPORTED
+    assert lib.tg_expert_sort(IDS, 4, 4, 10, 4, 8, OFF, SRC, SRC + 100, None) == INVALID
+    good = [X, 64, 64, 1, 10, 4, 8, OFF, SLOT, XS, 64]
+    for at, v in ((0, None), (1, 63), (2, -1), (3, 7), (5, 0), (7, None), (8, None), (9, None), (9, X + 128), (10, 3)):
+        args = list(good)
+        args[at] = v
+        assert lib.tg_expert_gather(*args, None) == INVALID, at
+    args = list(good)
+    args[4] = 0  # no tokens: nothing to do
+    assert lib.tg_expert_gather(*args, None) == tg.TG_OK
+
+
+def test_combine_refusals(lib):
+    good = [X, 64, 1, 40, SLOT, W, 4, 10, 4, 64, XS, 64, 1]
+    for at, v in ((0, None), (1, 63), (2, 5), (3, -1), (4, None), (6, 3), (7, -1), (8, 0), (9, -2), (10, None), (10, X),
+                  (11, 60), (12, 9), (10, XS + 1), (10, W)):
+        args = list(good)
+        args[at] = v
+        assert lib.tg_expert_combine(*args, None) == INVALID, (at, v)
+    args = list(good)
+    args[7] = 0
+    assert lib.tg_expert_combine(*args, None) == tg.TG_OK
+
+
+def test_combine_grad_refusals(lib):
+    good = [DY, 64, 1, X, 64, 1, OFF, SLOT, W, 4, 10, 4, 8, 64, XS, 64, 1, DW, 4]
+    for at, v in ((0, None), (1, 63), (2, 5), (3, None), (4, 63), (5, 5), (6, None), (7, None), (9, 3), (11, 0), (12, 0),
+                  (13, -1), (14, None), (14, DY), (14, X), (15, 63), (16, 3), (17, XS), (17, W), (18, 3)):
+        args = list(good)
+        args[at] = v
+        assert lib.tg_expert_combine_grad(*args, None) == INVALID, (at, v)
+
+
+def test_python_checks():
+    ids = torch.zeros(4, 2, dtype=torch.int64)
+    with pytest.raises(TypeError):
+        tg.expert_sort(ids, 3)  # not on the GPU
+    with pytest.raises(TypeError):
+        tg.expert_dispatch(torch.zeros(4, 8), ids, 3)
+    order = tg.ExpertOrder.empty(4, 2, 3, "cpu")
+    assert [tuple(t.shape) for t in order] == [(4,), (8,), (4, 2)]
+    with pytest.raises(TypeError):
+        tg.expert_combine(torch.zeros(8, 8), order)
+    with pytest.raises(AttributeError):
+        tg.no_such_name

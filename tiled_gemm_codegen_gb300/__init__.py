@@ -512,3 +512,19 @@ def plan(M, N, K, batch=1, *, lda=None, ldb=None, ldc=None, strideA=None, stride
 def device_error(stream=None) -> int:
     """Synchronise the stream and return (and clear) its watchdog status."""
     return tg_device_error(_stream_ptr(stream))
+
+
+_EXPERTS = ("ExpertOrder", "expert_sort", "expert_dispatch", "expert_gather", "expert_combine", "expert_combine_grad")
+__all__ += _EXPERTS
+
+
+def __getattr__(name):
+    # the expert operators' module imports torch, which the rest of the
+    # package only does inside its calls
+    if name in _EXPERTS:
+        from . import experts
+
+        value = getattr(experts, name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

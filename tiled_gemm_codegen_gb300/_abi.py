@@ -99,6 +99,7 @@ TG_ACT_NONE, TG_ACT_RELU, TG_ACT_GELU_TANH, TG_ACT_SILU = 0, 1, 2, 3
 TG_F32, TG_BF16 = 0, 1
 TG_FP8_E4M3, TG_FP8_E5M2 = 0, 1
 
+_i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 _GEMM_ARGS = [_vp, _vp, _vp] + [_i64] * 10 + [_vp]
@@ -124,6 +125,14 @@ SIGNATURES = {
     "tg_gemm_mxfp4": ([_vp, _vp, _vp] + [_i64] * 10 + [_vp, _i64, _i64, _vp, _i64, _i64,
                                                          ctypes.POINTER(tg_epilogue), _vp,
                                                          ctypes.POINTER(tg_options)], ctypes.c_int),
+    "tg_expert_sort": ([_vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "tg_expert_dispatch": ([_vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _i64,
+                            _vp], ctypes.c_int),
+    "tg_expert_gather": ([_vp, _i64, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "tg_expert_combine": ([_vp, _i64, _i32, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _i32, _vp],
+                          ctypes.c_int),
+    "tg_expert_combine_grad": ([_vp, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64,
+                                _vp, _i64, _i32, _vp, _i64, _vp], ctypes.c_int),
     "tg_device_error": ([_vp], ctypes.c_int),
     "tg_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "tg_shutdown": ([], None),

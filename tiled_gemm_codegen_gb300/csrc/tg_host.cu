@@ -16,6 +16,7 @@
 
 #include "tg_epilogue.cuh"
 #include "tg_gemm.h"
+#include "tg_host_api.h"
 #include "tg_internal.h"
 #include "tg_direct.h"
 #include "tg_plan.h"
@@ -26,7 +27,7 @@
 namespace tg {
 namespace {
 
-constexpr uint64_t DEFAULT_TIMEOUT_NS = 2000000000ull;  // 2 s
+constexpr uint64_t DEFAULT_TIMEOUT_NS = HOST_TIMEOUT_NS;
 
 // TG_TRACE=1 prints each call's plan to stderr (read once).
 bool trace_enabled()
@@ -968,6 +969,52 @@ cudaError_t shared_zero_fill(float *C, int64_t M, int64_t N, int64_t ldc, int64_
 {
     const int64_t total = batch * M * N;
     zero_c_kernel<<<grid_for(total, sms), 256, 0, s>>>(C, M, N, ldc, sC, total);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------ tg_host_api.h
+std::mutex &host_mutex() { return g_mutex; }
+
+tg_status host_cuda_status(cudaError_t e) { return cuda_status(e); }
+
+tg_status host_stream(cudaStream_t stream, HostStream *out)
+{
+    HostStream hs;
+    hs.stream = stream;
+    cudaError_t e = cudaGetDevice(&hs.dev);
+    if (e != cudaSuccess) return cuda_status(e);
+    tg_status st = device_sms(hs.dev, &hs.sms);
+    if (st != TG_OK) return st;
+    Workspace &w = workspace_for(hs.dev, stream);
+    st = ensure_err_word(w, stream);
+    if (st != TG_OK) return st;
+    hs.err = w.err;
+    *out = hs;
+    return TG_OK;
+}
+
+tg_status host_arena(const HostStream &hs, size_t bytes, void **out)
+{
+    Workspace &w = workspace_for(hs.dev, hs.stream);
+    const tg_status st = grow(&w.arena, &w.arena_cap, bytes, hs.stream);
+    *out = w.arena;
+    return st;
+}
+
+bool host_encode_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
+                    uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1, CUtensorMapSwizzle swz)
+{
+    return encode_3d(m, dt, base, d0, d1, d2, stride1, stride2, box0, box1, swz);
+}
+
+cudaError_t host_pack(const HostStream &hs, const HostPack *a, const HostPack *b)
+{
+    PackJob ja{}, jb{};
+    if (a) ja = pack_job(a->src, static_cast<uint16_t *>(a->dst), a->rows, a->cols, a->ld, a->nb, a->stride);
+    if (b) jb = pack_job(b->src, static_cast<uint16_t *>(b->dst), b->rows, b->cols, b->ld, b->nb, b->stride);
+    const int blocks_a = a ? grid_for(ja.chunks, hs.sms) : 0;
+    const int blocks_b = b ? grid_for(jb.chunks, hs.sms) : 0;
+    pack_bf16_kernel<<<blocks_a + blocks_b, 256, 0, hs.stream>>>(ja, jb, blocks_a);
     return cudaGetLastError();
 }
 

@@ -1,0 +1,190 @@
+"""Operators of a mixture-of-experts layer on torch tensors: tokens sorted by
+expert and back.
+
+As the rest of the package this is a thin binding of ``include/tg_gemm.h``:
+pointers, shapes and strides are read off the tensors, and all arithmetic
+happens in the CUDA library.  Calls are asynchronous on ``stream`` (default:
+torch's current stream).
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import TgError, _stream_ptr
+from ._abi import TG_BF16, TG_F32, TG_OK, load
+
+__all__ = ["ExpertOrder", "expert_sort", "expert_dispatch", "expert_gather", "expert_combine", "expert_combine_grad"]
+
+_DTYPES = {torch.float32: TG_F32, torch.bfloat16: TG_BF16}
+
+
+class ExpertOrder(NamedTuple):
+    """The stable order of T x k assignments by expert, int32 CUDA tensors:
+    ``offsets`` [E + 1] (expert e's rows), ``source`` [T * k] (the flat
+    assignment of each sorted row, -1 behind the last) and ``slot`` [T, k]
+    (the sorted row of each assignment, -1 if dropped)."""
+
+    offsets: torch.Tensor
+    source: torch.Tensor
+    slot: torch.Tensor
+
+    @classmethod
+    def empty(cls, tokens: int, k: int, num_experts: int, device="cuda") -> "ExpertOrder":
+        """An uninitialised order, to be filled by expert_sort or
+        expert_dispatch."""
+        n = dict(dtype=torch.int32, device=device)
+        return cls(torch.empty(num_experts + 1, **n), torch.empty(tokens * k, **n), torch.empty(tokens, k, **n))
+
+
+def _check(st: int, what: str) -> None:
+    if st != TG_OK:
+        raise TgError(st, what)
+
+
+def _rows(t, what, shape=None):
+    """(ptr, ld, tg_dtype) of a 2-D fp32 or bf16 CUDA tensor with unit
+    stride in its rows."""
+    dt = _DTYPES.get(t.dtype)
+    if dt is None or not t.is_cuda:
+        raise TypeError(f"{what} must be an fp32 or bf16 CUDA tensor")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{what} must have shape {tuple(shape) if shape is not None else '[rows, D]'}")
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1 and rows:
+        raise ValueError(f"{what} must have unit stride in its last dimension")
+    return t.data_ptr(), (ld if rows > 1 and ld > cols else cols), dt
+
+
+def _weights(w, shape, what="weights"):
+    if w is None:
+        return None, 0
+    if w.dtype != torch.float32 or not w.is_cuda:
+        raise TypeError(f"{what} must be an fp32 CUDA tensor")
+    if w.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}")
+    T, k = shape
+    if k > 1 and T and w.stride(1) != 1:
+        raise ValueError(f"{what} must have unit stride in its last dimension")
+    return w.data_ptr(), (max(w.stride(0), k) if T > 1 else k)
+
+
+def _order(order, T=None, k=None, E=None):
+    offsets, source, slot = order
+    for t, name in ((offsets, "offsets"), (source, "source"), (slot, "slot")):
+        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+            raise TypeError(f"order.{name} must be a contiguous int32 CUDA tensor")
+    if slot.dim() != 2 or offsets.dim() != 1 or source.shape != (slot.numel(),) or offsets.numel() < 2:
+        raise ValueError("order must hold offsets [E + 1], source [T * k] and slot [T, k]")
+    if T is not None and (slot.shape != (T, k) or offsets.numel() != E + 1):
+        raise ValueError(f"order does not fit {T} x {k} assignments to {E} experts")
+    return offsets, source, slot
+
+
+def _ids(ids):
+    if ids.dtype not in (torch.int32, torch.int64) or not ids.is_cuda:
+        raise TypeError("ids must be an int32 or int64 CUDA tensor")
+    if ids.dim() != 2 or ids.shape[1] < 1:
+        raise ValueError("ids must have shape [T, k], k >= 1")
+    T, k = ids.shape
+    if k > 1 and T and ids.stride(1) != 1:
+        raise ValueError("ids must have unit stride in their last dimension")
+    return T, k, (max(ids.stride(0), k) if T > 1 else k), ids.element_size()
+
+
+def expert_sort(ids, num_experts: int, *, order: ExpertOrder | None = None, stream=None) -> ExpertOrder:
+    """The order of ids [T, k] (int32 or int64; ids outside [0, num_experts)
+    drop their assignment) by expert, stable: equal ids keep their order."""
+    T, k, ld, size = _ids(ids)
+    if order is None:
+        order = ExpertOrder.empty(T, k, num_experts, ids.device)
+    offsets, source, slot = _order(order, T, k, num_experts)
+    _check(load().tg_expert_sort(ids.data_ptr(), size, ld, T, k, num_experts, offsets.data_ptr(), source.data_ptr(),
+                                 slot.data_ptr(), _stream_ptr(stream)), "tg_expert_sort")
+    return order
+
+
+def expert_dispatch(x, ids, num_experts: int, *, xs=None, order: ExpertOrder | None = None, stream=None):
+    """(xs, order): the order of ids [T, k] and the rows of x [T, D] (fp32 or
+    bf16) in it - xs [T * k, D], xs[s] = x[order.source[s] // k], rows behind
+    the last expert zero.  Its gradient is expert_combine(dxs, order)."""
+    T, k, ld, size = _ids(ids)
+    px, ld_x, dt = _rows(x, "x")
+    if x.shape[0] != T:
+        raise ValueError(f"x must have {T} rows")
+    D = x.shape[1]
+    if xs is None:
+        xs = torch.empty(T * k, D, dtype=x.dtype, device=x.device)
+    pxs, ld_xs, dxs = _rows(xs, "xs", (T * k, D))
+    if dxs != dt:
+        raise TypeError("xs must have x's dtype")
+    if order is None:
+        order = ExpertOrder.empty(T, k, num_experts, ids.device)
+    offsets, source, slot = _order(order, T, k, num_experts)
+    _check(load().tg_expert_dispatch(ids.data_ptr(), size, ld, T, k, num_experts, offsets.data_ptr(),
+                                     source.data_ptr(), slot.data_ptr(), px, ld_x, D, dt, pxs, ld_xs,
+                                     _stream_ptr(stream)), "tg_expert_dispatch")
+    return xs, order
+
+
+def expert_gather(x, order: ExpertOrder, xs=None, *, stream=None):
+    """xs [T * k, D]: the rows of x [T, D] in an order made before."""
+    offsets, _, slot = _order(order)
+    T, k = slot.shape
+    px, ld_x, dt = _rows(x, "x")
+    if x.shape[0] != T:
+        raise ValueError(f"x must have {T} rows")
+    D = x.shape[1]
+    if xs is None:
+        xs = torch.empty(T * k, D, dtype=x.dtype, device=x.device)
+    pxs, ld_xs, dxs = _rows(xs, "xs", (T * k, D))
+    if dxs != dt:
+        raise TypeError("xs must have x's dtype")
+    _check(load().tg_expert_gather(px, ld_x, D, dt, T, k, offsets.numel() - 1, offsets.data_ptr(), slot.data_ptr(),
+                                   pxs, ld_xs, _stream_ptr(stream)), "tg_expert_gather")
+    return xs
+
+
+def expert_combine(ys, order: ExpertOrder, weights=None, *, y=None, out_dtype=None, stream=None):
+    """y [T, D]: y[t] = sum_j weights[t, j] * ys[order.slot[t, j]] for ys
+    [T * k, D] (fp32 or bf16) and fp32 weights [T, k] (None: ones, the
+    gradient of expert_dispatch's rows), summed in fp32 and rounded once;
+    dropped assignments add nothing.  y: out_dtype, by default ys's."""
+    _, _, slot = _order(order)
+    T, k = slot.shape
+    pys, ld_ys, dt = _rows(ys, "ys")
+    S, D = ys.shape
+    pw, ld_w = _weights(weights, slot.shape)
+    if y is None:
+        y = torch.empty(T, D, dtype=out_dtype if out_dtype is not None else ys.dtype, device=ys.device)
+    py, ld_y, dty = _rows(y, "y", (T, D))
+    _check(load().tg_expert_combine(pys, ld_ys, dt, S, slot.data_ptr(), pw, ld_w, T, k, D, py, ld_y, dty,
+                                    _stream_ptr(stream)), "tg_expert_combine")
+    return y
+
+
+def expert_combine_grad(dy, ys, order: ExpertOrder, weights, *, dys=None, dweights=None, out_dtype=None, stream=None):
+    """(dys, dweights), the gradient of expert_combine for dy [T, D]:
+    dys[order.slot[t, j]] = weights[t, j] * dy[t] (rows of no assignment
+    zero; out_dtype, by default ys's) and dweights[t, j] = <dy[t],
+    ys[order.slot[t, j]]> (fp32; dropped: zero)."""
+    offsets, _, slot = _order(order)
+    T, k = slot.shape
+    pdy, ld_dy, t_dy = _rows(dy, "dy")
+    D = dy.shape[1]
+    if dy.shape[0] != T:
+        raise ValueError(f"dy must have {T} rows")
+    pys, ld_ys, t_ys = _rows(ys, "ys", (T * k, D))
+    pw, ld_w = _weights(weights, slot.shape)
+    if dys is None:
+        dys = torch.empty(T * k, D, dtype=out_dtype if out_dtype is not None else ys.dtype, device=dy.device)
+    if dweights is None:
+        dweights = torch.empty(T, k, dtype=torch.float32, device=dy.device)
+    pdys, ld_dys, t_dys = _rows(dys, "dys", (T * k, D))
+    pdw, ld_dw = _weights(dweights, slot.shape, "dweights")
+    _check(load().tg_expert_combine_grad(pdy, ld_dy, t_dy, pys, ld_ys, t_ys, offsets.data_ptr(), slot.data_ptr(), pw,
+                                         ld_w, T, k, offsets.numel() - 1, D, pdys, ld_dys, t_dys, pdw, ld_dw,
+                                         _stream_ptr(stream)), "tg_expert_combine_grad")
+    return dys, dweights
