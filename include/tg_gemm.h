@@ -459,6 +459,34 @@ tg_status tg_expert_combine_grad(const void *dy, int64_t ld_dy, int32_t dy_type,
                                  int64_t ld_w, int64_t T, int64_t k, int64_t E, int64_t D, void *dys, int64_t ld_dys,
                                  int32_t dys_type, float *dweights, int64_t ld_dw, tg_stream_t stream);
 
+/* The experts' products: one GEMM per group of consecutive rows, the groups'
+ * bounds in device memory (offsets[groups + 1], not decreasing, as an
+ * order's; the call does not wait for them):
+ *     D[s][j] = act(alpha * sum_{k<K} A[s][k] B_g[k][j] + bias_g[j])
+ * for the rows offsets[g] <= s < offsets[g + 1] of every group g, and zero
+ * for the rows of S that lie in no group.  A is S x K row-major bf16, B_g = B
+ * + g * strideB row-major K x N (opt->b_col_major: stored N x K - with the
+ * weights of the forward call and dL/dD for A, this is the gradient of A),
+ * D S x N (ldd).  ep may be NULL (fp32 D = A B); its residual must be NULL.
+ * K == 0 gives act(bias_g).  An empty group costs nothing.  Bounds outside
+ * [0, S] or decreasing are clamped, never followed out of range.
+ * opt: cta_pair (1 = 128 x 128 tiles, 2 = two-SM 256 x 256 tiles), force_pack,
+ * timeout_ns and b_col_major; the rest must be 0.  Other conventions as
+ * tg_gemm; extents below 2^31 - 1024. */
+tg_status tg_gemm_grouped(const void *A, const void *B, void *D, const int32_t *offsets, int64_t groups,
+                          int64_t S, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t strideB, int64_t ldd,
+                          const tg_epilogue *ep, tg_stream_t stream, const tg_options *opt);
+
+/* The gradient of the weights: D_g[i][j] = alpha * sum over the rows s of
+ * group g of A[s][i] * B[s][j], zero for an empty group.  A is S x M, B S x
+ * N, both row-major bf16; D_g = D + g * strideD row-major M x N.  Rows of no
+ * group are not used, whatever they hold.  ep may be NULL (fp32 D); only its
+ * alpha and out_type apply (the rest must be 0 or NULL).  opt as
+ * tg_gemm_grouped, without b_col_major. */
+tg_status tg_gemm_grouped_wgrad(const void *A, const void *B, void *D, const int32_t *offsets, int64_t groups,
+                                int64_t S, int64_t M, int64_t N, int64_t lda, int64_t ldb, int64_t ldd,
+                                int64_t strideD, const tg_epilogue *ep, tg_stream_t stream, const tg_options *opt);
+
 /* Synchronises `stream`, then reads and clears the device error words that
  * the kernels' watchdog writes: the one of `stream`'s workspace, and the one
  * of tg_gemm_splitk_static on the current device.  TG_ERR_TIMEOUT if a wait

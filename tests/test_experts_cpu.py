@@ -82,3 +82,39 @@ def test_python_checks():
         tg.expert_combine(torch.zeros(8, 8), order)
     with pytest.raises(AttributeError):
         tg.no_such_name
+
+
+def _ep(**kw):
+    ep = tg.tg_epilogue()
+    ep.alpha = 1.0
+    for k, v in kw.items():
+        setattr(ep, k, v)
+    return ep
+
+
+def test_grouped_refusals(lib):
+    import ctypes
+
+    def rows(opt=None, ep=None, **kw):
+        a = dict(A=X, B=XS, D=DY, offsets=OFF, groups=4, S=100, N=64, K=32, lda=32, ldb=64, strideB=2048, ldd=64)
+        a.update(kw)
+        return lib.tg_gemm_grouped(*a.values(), ctypes.byref(ep) if ep else None, None, ctypes.byref(opt) if opt else None)
+
+    def wgrad(opt=None, ep=None, **kw):
+        a = dict(A=X, B=XS, D=DY, offsets=OFF, groups=4, S=100, M=32, N=64, lda=32, ldb=64, ldd=64, strideD=2048)
+        a.update(kw)
+        return lib.tg_gemm_grouped_wgrad(*a.values(), ctypes.byref(ep) if ep else None, None, ctypes.byref(opt) if opt else None)
+
+    for kw in (dict(groups=0), dict(S=-1), dict(N=-1), dict(K=-1), dict(lda=31), dict(ldb=63), dict(ldd=63), dict(strideB=-1),
+               dict(A=None), dict(B=None), dict(D=None), dict(offsets=None), dict(D=X), dict(D=XS + 64), dict(D=OFF),
+               dict(A=X + 1), dict(D=DY + 2), dict(S=2 ** 31 - 1), dict(ep=_ep(residual=W)), dict(ep=_ep(activation=9)),
+               dict(ep=_ep(out_type=7)), dict(ep=_ep(bias=W, bias_stride=-1)), dict(opt=tg.make_options(split_k=2)),
+               dict(opt=tg.make_options(cta_pair=3)), dict(opt=tg.make_options(a_col_major=1)),
+               dict(opt=tg.make_options(b_col_major=1), ldb=31)):
+        assert rows(**kw) == INVALID, kw
+    for kw in (dict(groups=0), dict(S=-1), dict(M=-1), dict(N=-1), dict(lda=31), dict(ldb=63), dict(ldd=63), dict(strideD=100),
+               dict(A=None), dict(B=None), dict(D=None), dict(offsets=None), dict(D=X), dict(D=XS), dict(D=OFF),
+               dict(ep=_ep(bias=W)), dict(ep=_ep(activation=1)), dict(opt=tg.make_options(b_col_major=1)),
+               dict(opt=tg.make_options(direct=2))):
+        assert wgrad(**kw) == INVALID, kw
+    assert rows(S=0) == tg.TG_OK and rows(N=0, ldb=1, ldd=1) == tg.TG_OK and wgrad(M=0) == tg.TG_OK

@@ -514,7 +514,8 @@ def device_error(stream=None) -> int:
     return tg_device_error(_stream_ptr(stream))
 
 
-_EXPERTS = ("ExpertOrder", "expert_sort", "expert_dispatch", "expert_gather", "expert_combine", "expert_combine_grad")
+_EXPERTS = ("ExpertOrder", "expert_sort", "expert_dispatch", "expert_gather", "expert_combine", "expert_combine_grad",
+            "gemm_grouped", "gemm_grouped_wgrad")
 __all__ += _EXPERTS
 
 

@@ -133,6 +133,10 @@ SIGNATURES = {
                           ctypes.c_int),
     "tg_expert_combine_grad": ([_vp, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64,
                                 _vp, _i64, _i32, _vp, _i64, _vp], ctypes.c_int),
+    "tg_gemm_grouped": ([_vp, _vp, _vp, _vp] + [_i64] * 8 + [ctypes.POINTER(tg_epilogue), _vp,
+                                                               ctypes.POINTER(tg_options)], ctypes.c_int),
+    "tg_gemm_grouped_wgrad": ([_vp, _vp, _vp, _vp] + [_i64] * 8 + [ctypes.POINTER(tg_epilogue), _vp,
+                                                                     ctypes.POINTER(tg_options)], ctypes.c_int),
     "tg_device_error": ([_vp], ctypes.c_int),
     "tg_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "tg_shutdown": ([], None),

@@ -1,0 +1,668 @@
+// Persistent, warp-specialised grouped GEMM for sm_103a: one product per
+// group of consecutive rows, the groups' bounds on the device.
+//
+//   rows mode    D[s][:] = act(alpha * A[s][:] B[g] + bias[g]) for the rows s of group g: M is
+//                ragged.  A tile holds rows of one group only; it starts at any
+//                row (a TMA box may), the rows past the group's end are loaded but
+//                never stored (a row of D depends on its own row of A alone).
+//   wgrad mode   D[g] = alpha * A[rows g]^T B[rows g]: the contraction is ragged.  Both operands
+//                are read as stored (MN-major), 64 rows a k-block; the rows past the
+//                group's end in its last k-block (its fringe) belong to the next
+//                group, so a fixer warp overwrites them with zeros in shared memory
+//                before the MMA may read them (in both operands: 0 x NaN is NaN).
+//                A fringe's copies complete on the slot's fringe barrier, on which
+//                only the fixer waits; it then arrives on the slot's full barrier
+//                in the producer's place, so the MMA's own wait is one and the same.
+//
+// Roles, rings and the bounded waits are those of gemm_kernel (tg_kernel.cuh):
+// warp 0 loads, warp 1 issues tcgen05.mma, warps 2..5 drain tensor memory;
+// wgrad mode adds warp 6, the fixer, which runs as far ahead of the MMA as
+// the ring allows.  PAIR: a cluster of two CTAs computes 256 x BN.
+//
+// The list of tiles depends on offsets the host has not seen: every warp
+// walks it by itself, 32 groups at a time with a lane for each (a group's
+// tile count, a warp scan, a ballot), so that no table in shared memory and
+// no second kernel is needed.
+#pragma once
+
+#include "tg_kernel.cuh"
+
+namespace tg {
+
+struct GroupedParams {
+    const int32_t *offsets;  // [groups + 1]
+    int32_t groups;
+    int32_t S;               // rows of the ragged operands
+    int32_t M;               // wgrad mode: rows of D[g] (columns of A)
+    int32_t N, K;            // K: rows mode only
+    int32_t k_blocks;        // rows mode: ceil(K / BK)
+    int32_t tiles_m;         // wgrad mode
+    int32_t tiles_n;
+    int32_t group_m;         // row tiles a raster strip
+    int32_t b_k;             // rows mode: 1 = B stored N x K
+    int32_t b_shared;        // rows mode: 1 = every group has the same B
+    int32_t epi_tma;
+    void *D;
+    int64_t ldd, strideD;
+    int32_t out_bf16, act;
+    float alpha;
+    const float *bias;
+    int64_t bias_stride;
+    uint32_t *err;
+    uint64_t timeout_ns;
+};
+
+// One tile: group, first row of the group and the row behind it (rows mode:
+// rows of A and D; wgrad mode: rows of the contraction), tile coordinates.
+struct GroupUnit {
+    int32_t g, row0, row1, tm, tn, k_blocks;
+};
+
+// A warp's walk through the tiles in order.  Lane l holds group base + l:
+// its bounds and the number of tiles up to and including it.  Bounds are
+// clamped to [0, S] and never fall, whatever offsets holds, so that no row
+// is out of range and the number of tiles is bounded.
+struct GroupWalk {
+    int32_t base;      // group of lane 0
+    int32_t lo, hi;    // lane: bounds of its group
+    int32_t incl;      // lane: tiles of the chunk up to its group
+    int32_t before;    // tiles before the chunk
+    int32_t total;     // tiles of the chunk
+    int32_t last;      // the bound before the next chunk
+};
+
+template <int TILE_M>
+__device__ __forceinline__ void walk_load(const GroupedParams &p, int32_t base, GroupWalk &w)
+{
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const int32_t g = base + lane;
+    int32_t hi = g < p.groups ? __ldg(p.offsets + g + 1) : 0;
+    hi = max(0, min(hi, p.S));
+    hi = max(hi, w.last);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xffffffffu, hi, d);
+        if (lane >= d) hi = max(hi, o);
+    }
+    int32_t lo = __shfl_up_sync(0xffffffffu, hi, 1);
+    if (lane == 0) lo = w.last;
+    const int32_t units = g < p.groups ? (hi - lo + TILE_M - 1) / TILE_M * p.tiles_n : 0;
+    int32_t incl = units;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    w.base = base;
+    w.lo = lo;
+    w.hi = hi;
+    w.incl = incl;
+    w.total = __shfl_sync(0xffffffffu, incl, 31);
+    w.last = __shfl_sync(0xffffffffu, hi, 31);
+}
+
+template <int TILE_M, bool WGRAD>
+__device__ __forceinline__ void walk_begin(const GroupedParams &p, GroupWalk &w)
+{
+    w.before = 0;
+    w.last = max(0, min(__ldg(p.offsets), p.S));
+    if constexpr (!WGRAD) walk_load<TILE_M>(p, 0, w);
+}
+
+// Tile t of the list (t never falls from call to call); false past the end.
+template <int TILE_M, bool WGRAD>
+__device__ __forceinline__ bool walk_to(const GroupedParams &p, int64_t t64, GroupWalk &w, GroupUnit &u)
+{
+    if constexpr (WGRAD) {
+        const int64_t per = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+        if (t64 >= per * p.groups) return false;
+        u.g = static_cast<int32_t>(t64 / per);
+        const int32_t r = static_cast<int32_t>(t64 - u.g * per);
+        const int32_t strip = p.group_m * p.tiles_n;
+        const int32_t first = r / strip * p.group_m;
+        const int32_t rows = min(p.tiles_m - first, p.group_m);
+        u.tm = first + r % strip % rows;
+        u.tn = r % strip / rows;
+        u.row0 = max(0, min(__ldg(p.offsets + u.g), p.S));
+        u.row1 = max(u.row0, min(__ldg(p.offsets + u.g + 1), p.S));
+        u.k_blocks = (u.row1 - u.row0 + BK - 1) / BK;
+        return true;
+    } else {
+        if (t64 > INT32_MAX) return false;
+        const int32_t t = static_cast<int32_t>(t64);
+        while (t >= w.before + w.total) {
+            if (w.base + 32 >= p.groups) return false;
+            w.before += w.total;
+            walk_load<TILE_M>(p, w.base + 32, w);
+        }
+        const int32_t at = t - w.before;
+        const int idx = __popc(__ballot_sync(0xffffffffu, at >= w.incl));
+        u.g = w.base + idx;
+        u.row0 = __shfl_sync(0xffffffffu, w.lo, idx);
+        u.row1 = __shfl_sync(0xffffffffu, w.hi, idx);
+        const int32_t before = __shfl_sync(0xffffffffu, w.incl, idx > 0 ? idx - 1 : 0);
+        const int32_t r = at - (idx > 0 ? before : 0);
+        const int32_t tiles_m = (u.row1 - u.row0 + TILE_M - 1) / TILE_M;
+        const int32_t strip = p.group_m * p.tiles_n;
+        const int32_t first = r / strip * p.group_m;
+        const int32_t rows = min(tiles_m - first, p.group_m);
+        u.tm = first + r % strip % rows;
+        u.tn = r % strip / rows;
+        u.k_blocks = p.k_blocks;
+        return true;
+    }
+}
+
+// alpha, bias and activation on one thread's 32 columns of group g.
+__device__ __forceinline__ void grouped_epilogue(const GroupedParams &p, uint32_t (&v)[32], int32_t col0, int32_t g)
+{
+    float x[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] = __fmul_rn(p.alpha, __uint_as_float(v[j]));
+    if (p.bias) {
+        const float *bp = p.bias + static_cast<int64_t>(g) * p.bias_stride + col0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (col0 + j < p.N) x[j] = __fadd_rn(x[j], __ldg(bp + j));
+    }
+    switch (p.act) {
+        case 1:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = activation(x[j], 1);
+            break;
+        case 2:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = activation(x[j], 2);
+            break;
+        case 3:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = activation(x[j], 3);
+            break;
+        default:
+            break;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(x[j]);
+}
+
+constexpr int GROUPED_THREADS = 192;        // rows mode
+constexpr int GROUPED_WGRAD_THREADS = 224;  // and the fixer warp
+
+template <int BN, int STAGES, bool PAIR, bool WGRAD>
+__global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREADS, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmD, const GroupedParams p)
+{
+    using G = Geometry<BN, PAIR>;
+    constexpr int TILE_M = PAIR ? 2 * BM : BM;
+    constexpr int B_BOXES = G::B_COLS / 64;
+    constexpr uint32_t BOX_BYTES = BK * 64 * 2;                    // 64 k x 64 columns, 8 KB
+    constexpr uint32_t EPI_BOX_BYTES = EPI_CHUNK * EPI_CHUNK * 4;  // 4 KB
+    constexpr uint32_t EPI_WARPS_TOTAL = PAIR ? 8 : 4;
+    constexpr uint32_t TMEM_ALLOC = static_cast<uint32_t>(G::TMEM_COLS);
+    static_assert(8 * (4 * STAGES + 5) + 16 <= G::BAR_BYTES, "barrier area");
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sA = raw + pad;
+    const uint32_t sB = sA + STAGES * G::A_STAGE;
+    const uint32_t sE = sB + STAGES * G::B_STAGE;
+    uint8_t *bar_area = smem + STAGES * G::STAGE + G::EPI_BYTES;
+    const uint32_t bar0 = ptx::smem_addr(bar_area);
+    // barrier k at bar0 + 8k: [0, S) full, [S, 2S) empty, 2S+{0,1} tfull,
+    // 2S+{2,3} tempty, 2S+4 mma-done; wgrad mode: from 2S+5 fringe[S] (this
+    // CTA's copies of a group's last, partial k-block landed) and pfix[S]
+    // (pair, on the leader's: the peer has zeroed its share of it).
+    const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (4 * STAGES + 5));
+    volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
+    uint32_t *issued_slot = tmem_slot + 2;  // k-blocks this CTA's producer loaded; then a bit for
+                                            // each slot whose last load was a fringe
+    auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
+    auto tfull_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
+    auto tempty_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
+    auto fringe_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
+    auto pfix_bar = [&](uint32_t s) { return bar0 + 8u * (3 * STAGES + 5 + s); };
+
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int64_t worker = PAIR ? (blockIdx.x >> 1) : blockIdx.x;
+    const int64_t n_workers = PAIR ? (gridDim.x >> 1) : gridDim.x;
+
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+            if constexpr (WGRAD) {
+                ptx::mbar_init(fringe_bar(s), 1);
+                ptx::mbar_init(pfix_bar(s), 1);
+            }
+        }
+        for (uint32_t b = 0; b < 2; ++b) {
+            ptx::mbar_init(tfull_bar(b), 1);
+            ptx::mbar_init(tempty_bar(b), EPI_WARPS_TOTAL);
+        }
+        ptx::mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        issued_slot[0] = issued_slot[1] = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        if (WGRAD ? p.S > 0 : p.k_blocks > 0) {  // else there is nothing to load, and no map
+            ptx::prefetch_tensormap(&tmA);
+            ptx::prefetch_tensormap(&tmB);
+        }
+        if (p.epi_tma) ptx::prefetch_tensormap(&tmD);
+    }
+    if (warp == 1) {
+        if constexpr (PAIR) {
+            ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), TMEM_ALLOC);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_addr(tmem_slot), TMEM_ALLOC);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) ptx::cluster_sync_all();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    ptx::griddep_wait();
+    const uint32_t peer_abort =
+        PAIR ? ptx::map_to_cta(ptx::smem_addr(const_cast<int32_t *>(abort_flag)), rank ^ 1u) : 0u;
+    const Watchdog wd{p.timeout_ns, abort_flag, p.err, peer_abort};
+
+    GroupWalk walk;
+    GroupUnit w;
+    walk_begin<TILE_M, WGRAD>(p, walk);
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        uint32_t it = 0;
+        uint32_t fringe = 0, fringe_phase = 0;  // bit s: slot s's last load; parity of its next fringe
+        bool ok = true;
+        const uint32_t full0 = PAIR ? ptx::map_to_cta(full_bar(0), 0u) : full_bar(0);
+        const uint32_t fringe0 = PAIR ? ptx::map_to_cta(fringe_bar(0), rank) : fringe_bar(0);
+        for (int64_t t = worker; ok && walk_to<TILE_M, WGRAD>(p, t, walk, w); t += n_workers) {
+            if (!dbg_ok(w.g >= 0 && w.g < p.groups && w.row0 >= 0 && w.row0 <= w.row1 && w.row1 <= p.S && w.tm >= 0 &&
+                            w.tn >= 0 && w.tn < p.tiles_n,
+                        CHK_UNIT, wd))
+                break;
+            const int32_t m0 = (WGRAD ? 0 : w.row0) + w.tm * TILE_M + static_cast<int32_t>(rank) * BM;
+            const int32_t n0 = w.tn * BN + static_cast<int32_t>(rank) * G::B_COLS;
+            for (int32_t kb = 0; kb < w.k_blocks; ++kb, ++it) {
+                const uint32_t s = it % STAGES;
+                const uint32_t ph = (it / STAGES) & 1u;
+                const int r = wait_bounded_warp(empty_bar(s), ph ^ 1u, wd);
+                if (r != WAIT_OK) {
+                    if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_PRODUCER);
+                    ok = false;
+                    break;
+                }
+                const bool partial = WGRAD && w.row1 - w.row0 < (kb + 1) * BK;
+                if constexpr (WGRAD) {
+                    fringe = partial ? fringe | (1u << s) : fringe & ~(1u << s);
+                    if (partial) fringe_phase ^= 1u << s;
+                }
+                if (ptx::elect_one()) {
+                    uint32_t fb;
+                    if (partial) {
+                        ptx::mbar_arrive_expect_tx(fringe_bar(s), G::STAGE);
+                        fb = fringe0 + 8u * s;
+                    } else if constexpr (PAIR) {
+                        if (leader) ptx::mbar_arrive_expect_tx(full_bar(s), 2 * G::STAGE);
+                        fb = full0 + 8u * s;
+                    } else {
+                        ptx::mbar_arrive_expect_tx(full_bar(s), G::STAGE);
+                        fb = full_bar(s);
+                    }
+                    auto load = [&](uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2) {
+                        if constexpr (PAIR)
+                            ptx::tma_load_3d_pair(dst, map, fb, c0, c1, c2);
+                        else
+                            ptx::tma_load_3d(dst, map, fb, c0, c1, c2);
+                    };
+                    const uint32_t a_dst = sA + s * G::A_STAGE;
+                    const uint32_t b_dst = sB + s * G::B_STAGE;
+                    if constexpr (WGRAD) {
+                        const int32_t k0 = w.row0 + kb * BK;
+                        load(a_dst, &tmA, m0, k0, 0);
+                        load(a_dst + BOX_BYTES, &tmA, m0 + 64, k0, 0);
+#pragma unroll
+                        for (int j = 0; j < B_BOXES; ++j) load(b_dst + j * BOX_BYTES, &tmB, n0 + 64 * j, k0, 0);
+                    } else {
+                        load(a_dst, &tmA, kb * BK, m0, 0);
+                        if (!p.b_k) {
+#pragma unroll
+                            for (int j = 0; j < B_BOXES; ++j) load(b_dst + j * BOX_BYTES, &tmB, n0 + 64 * j, kb * BK, p.b_shared ? 0 : w.g);
+                        } else {
+                            load(b_dst, &tmB, kb * BK, n0, p.b_shared ? 0 : w.g);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0) {
+            issued_slot[0] = it;
+            issued_slot[1] = fringe;
+            const uint32_t first = it > STAGES ? it - STAGES : 0u;
+            for (uint32_t j = first; j < it; ++j) {
+                const uint32_t s = j % STAGES;
+                if ((fringe >> s) & 1u) {  // its copies, on this CTA's own barrier
+                    if (!wait_drain(fringe_bar(s), ((fringe_phase >> s) & 1u) ^ 1u, wd)) break;
+                } else if constexpr (!PAIR) {
+                    if (!wait_drain(full_bar(s), (j / STAGES) & 1u, wd)) break;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (!PAIR || leader) {
+            // ------------------------------------------------ MMA issuer
+            const uint32_t idesc = instr_desc_bf16<TILE_M, BN>(WGRAD, WGRAD || p.b_k == 0);
+            const uint64_t a_desc0 = smem_desc_sw128(0, WGRAD ? BK * 128 : 16, 1024);
+            const uint64_t b_desc0 = smem_desc_sw128(0, !WGRAD && p.b_k ? 16 : BK * 128, 1024);
+            const uint32_t a_step = WGRAD ? 2048u : 32u;
+            const uint32_t b_step = !WGRAD && p.b_k ? 32u : 2048u;
+            uint32_t it = 0, n = 0;
+            bool ok = true;
+            for (int64_t t = worker; ok && walk_to<TILE_M, WGRAD>(p, t, walk, w); t += n_workers) {
+                if (w.k_blocks == 0) continue;  // the epilogue writes the empty sum itself
+                const uint32_t buf = n & 1u;
+                const uint32_t tph = (n >> 1) & 1u;
+                ++n;
+                int r = wait_bounded_warp(tempty_bar(buf), tph ^ 1u, wd);
+                if (r != WAIT_OK) {
+                    if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_MMA);
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d_tmem = tmem_base + buf * BN;
+                for (int32_t kb = 0; kb < w.k_blocks; ++kb, ++it) {
+                    const uint32_t s = it % STAGES;
+                    const uint32_t ph = (it / STAGES) & 1u;
+                    r = wait_bounded_warp(full_bar(s), ph, wd);
+                    if (r != WAIT_OK) {
+                        if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_MMA);
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    if (ptx::elect_one()) {
+                        const uint32_t a_addr = sA + s * G::A_STAGE;
+                        const uint32_t b_addr = sB + s * G::B_STAGE;
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk) {
+                            const uint64_t ad = a_desc0 | (((a_addr + kk * a_step) >> 4) & 0x3FFFu);
+                            const uint64_t bd = b_desc0 | (((b_addr + kk * b_step) >> 4) & 0x3FFFu);
+                            const uint32_t acc = (kb > 0 || kk > 0) ? 1u : 0u;
+                            if constexpr (PAIR)
+                                ptx::mma_bf16_pair(d_tmem, ad, bd, idesc, acc);
+                            else
+                                ptx::mma_bf16(d_tmem, ad, bd, idesc, acc);
+                        }
+                        if constexpr (PAIR)
+                            ptx::mma_commit_pair_multicast(empty_bar(s), 0x3);
+                        else
+                            ptx::mma_commit(empty_bar(s));
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (ptx::elect_one()) {
+                    if constexpr (PAIR)
+                        ptx::mma_commit_pair_multicast(tfull_bar(buf), 0x3);
+                    else
+                        ptx::mma_commit(tfull_bar(buf));
+                }
+                __syncwarp();
+            }
+            if (ptx::elect_one()) {
+                if constexpr (PAIR)
+                    ptx::mma_commit_pair_multicast(done_bar, 0x1);
+                else
+                    ptx::mma_commit(done_bar);
+                wait_drain(done_bar, 0, wd);
+            }
+            __syncwarp();
+        }
+    } else if (WGRAD && warp == 6) {
+        // ------------------------------------------------ fixer
+        if constexpr (WGRAD) {
+            uint32_t it = 0;
+            uint32_t phase = 0;  // bit s: parity of the slot's next fringe
+            const uint32_t pfix_leader0 = PAIR ? ptx::map_to_cta(pfix_bar(0), 0u) : 0u;
+            for (int64_t t = worker; walk_to<TILE_M, WGRAD>(p, t, walk, w); t += n_workers) {
+                it += static_cast<uint32_t>(w.k_blocks);
+                const int32_t tail = (w.row1 - w.row0) % BK;
+                if (tail == 0) continue;  // also an empty group
+                const uint32_t s = (it - 1) % STAGES;
+                int r = wait_bounded_warp(fringe_bar(s), (phase >> s) & 1u, wd);
+                if (r != WAIT_OK) {
+                    if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_PRODUCER);
+                    break;
+                }
+                // k row r of a 64-column box is its bytes [128 r, 128 r + 128)
+                for (int box = 0; box < 2 + B_BOXES; ++box) {
+                    const uint32_t at = box < 2 ? sA + s * G::A_STAGE + box * BOX_BYTES
+                                                : sB + s * G::B_STAGE + (box - 2) * BOX_BYTES;
+                    for (uint32_t b = tail * 128u + lane * 16u; b < BOX_BYTES; b += 512u)
+                        ptx::st_shared_v4(at + b, 0u, 0u, 0u, 0u);
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if constexpr (PAIR) {
+                    if (!leader) {
+                        if (lane == 0) ptx::mbar_arrive_cluster(pfix_leader0 + 8u * s);
+                    } else {
+                        r = wait_bounded_warp(pfix_bar(s), (phase >> s) & 1u, wd);
+                        if (r != WAIT_OK) {
+                            if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_PRODUCER);
+                            break;
+                        }
+                        ptx::fence_acq_rel_cluster();
+                    }
+                }
+                if (leader && lane == 0) ptx::mbar_arrive(full_bar(s));
+                phase ^= 1u << s;
+                __syncwarp();
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue
+        const int q = warp & 3;
+        const uint32_t stage_base = sE + static_cast<uint32_t>(q * EPI_BUFS) * EPI_BOX_BYTES;
+        const uint32_t tempty_leader0 = PAIR ? ptx::map_to_cta(tempty_bar(0), 0u) : tempty_bar(0);
+        const bool plain = p.alpha == 1.0f && !p.bias && p.act == 0;
+        uint32_t st_cnt = 0;
+
+        // One 32 x 32 fp32 chunk -> rows row0 .. of D (those before `limit`),
+        // columns col0 ..  `whole`: the 32 rows may go out as one box.
+        auto store_chunk = [&](uint32_t (&v)[32], int32_t row0, int32_t limit, bool whole, int32_t col0, int32_t g) {
+            if (row0 >= limit || col0 >= p.N) return;  // warp-uniform
+            if (!plain) grouped_epilogue(p, v, col0, g);
+            const uint32_t box = stage_base + (st_cnt % EPI_BUFS) * EPI_BOX_BYTES;
+            ++st_cnt;
+            if (p.epi_tma && lane == 0) ptx::bulk_wait_group_read<EPI_BUFS - 1>();
+            __syncwarp();
+            const int32_t col = col0 + lane;
+            const int32_t nrows = min(32, limit - row0);
+            // (a box that the row's end cuts off its 16 bytes goes out plainly:
+            // a TMA store would write on to the next 16-byte boundary)
+            const bool tma = p.epi_tma && whole && (col0 + EPI_CHUNK <= p.N || p.N % (p.out_bf16 ? 8 : 4) == 0);
+            const int64_t at = (WGRAD ? static_cast<int64_t>(g) * p.strideD : 0) + static_cast<int64_t>(row0) * p.ldd + col;
+            if (!p.out_bf16) {
+#pragma unroll
+                for (int jj = 0; jj < 8; ++jj)
+                    ptx::st_shared_v4(box + lane * 128 + ((jj ^ (lane & 7)) << 4), v[4 * jj], v[4 * jj + 1], v[4 * jj + 2],
+                                      v[4 * jj + 3]);
+            } else {
+                uint32_t h[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) h[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    ptx::st_shared_v4(box + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4), h[4 * u], h[4 * u + 1], h[4 * u + 2],
+                                      h[4 * u + 3]);
+            }
+            if (tma) {
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::tma_store_3d(&tmD, box, col0, row0, WGRAD ? g : 0);
+                    ptx::bulk_commit_group();
+                }
+                return;
+            }
+            __syncwarp();
+            if (!p.out_bf16) {
+                const uint32_t src = box + ((lane >> 2) << 4) + ((lane & 3) << 2);
+                float *dst = static_cast<float *>(p.D) + at;
+#pragma unroll 1
+                for (int r0 = 0; r0 < nrows; r0 += 8) {
+                    float vals[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) vals[r] = ld_shared_f32((src ^ (((r0 + r) & 7) << 4)) + (r0 + r) * 128);
+                    if (col < p.N) {
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            if (r0 + r < nrows) dst[static_cast<int64_t>(r0 + r) * p.ldd] = vals[r];
+                    }
+                }
+            } else {
+                const uint32_t src = box + ((lane >> 3) << 4) + ((lane & 7) << 1);
+                uint16_t *dst = static_cast<uint16_t *>(p.D) + at;
+#pragma unroll 1
+                for (int r0 = 0; r0 < nrows; r0 += 8) {
+                    uint16_t vals[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        vals[r] = ld_shared_u16((src ^ ((((r0 + r) >> 1) & 3) << 4)) + (r0 + r) * 64);
+                    if (col < p.N) {
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            if (r0 + r < nrows) dst[static_cast<int64_t>(r0 + r) * p.ldd] = vals[r];
+                    }
+                }
+            }
+        };
+        auto release_tmem = [&](uint32_t buf) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR)
+                    ptx::mbar_arrive_cluster(tempty_leader0 + 8u * buf);
+                else
+                    ptx::mbar_arrive(tempty_bar(buf));
+            }
+        };
+
+        constexpr int NCH = BN / EPI_CHUNK;
+        uint32_t n = 0;
+        for (int64_t t = worker; walk_to<TILE_M, WGRAD>(p, t, walk, w); t += n_workers) {
+            const int32_t row0 = (WGRAD ? 0 : w.row0) + w.tm * TILE_M + static_cast<int32_t>(rank) * BM + q * 32;
+            const int32_t limit = WGRAD ? p.M : w.row1;
+            // the tensor's own end clips a box; a group's end does not
+            const bool whole = row0 + 32 <= limit || limit == (WGRAD ? p.M : p.S);
+            const int32_t col0 = w.tn * BN;
+            uint32_t va[32], vb[32];
+            if (w.k_blocks == 0) {  // the empty sum
+#pragma unroll 1
+                for (int c = 0; c < NCH; ++c) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) va[j] = 0u;
+                    store_chunk(va, row0, limit, whole, col0 + c * EPI_CHUNK, w.g);
+                }
+                continue;
+            }
+            const uint32_t buf = n & 1u;
+            const uint32_t tph = (n >> 1) & 1u;
+            ++n;
+            const int r = wait_bounded(tfull_bar(buf), tph, wd);
+            if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
+            if (!epi_all(r == WAIT_OK)) break;
+            ptx::tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
+            ptx::tmem_load_32cols(taddr, va);
+#pragma unroll 1
+            for (int c = 0; c < NCH; c += 2) {
+                ptx::tmem_load_32cols_async(taddr + (c + 1) * EPI_CHUNK, vb);
+                store_chunk(va, row0, limit, whole, col0 + c * EPI_CHUNK, w.g);
+                ptx::tmem_wait_ld(vb);
+                if (c + 2 < NCH)
+                    ptx::tmem_load_32cols_async(taddr + (c + 2) * EPI_CHUNK, va);
+                else
+                    release_tmem(buf);
+                store_chunk(vb, row0, limit, whole, col0 + (c + 1) * EPI_CHUNK, w.g);
+                if (c + 2 < NCH) ptx::tmem_wait_ld(va);
+            }
+        }
+        if constexpr (!WGRAD) {
+            // Rows of no group: zeros.  16-byte stores where D's rows allow.
+            const int32_t first = max(0, min(__ldg(p.offsets), p.S));
+            GroupWalk end = walk;
+            while (end.base + 32 < p.groups) {
+                end.before += end.total;
+                walk_load<TILE_M>(p, end.base + 32, end);
+            }
+            const int32_t eb = p.out_bf16 ? 2 : 4;
+            const bool vec = (reinterpret_cast<uintptr_t>(p.D) & 15u) == 0 && p.ldd * eb % 16 == 0;
+            const int64_t w0 = (static_cast<int64_t>(blockIdx.x) * 4 + q), nw = static_cast<int64_t>(gridDim.x) * 4;
+            for (int64_t i = w0; i < static_cast<int64_t>(first) + (p.S - end.last); i += nw) {
+                const int64_t row = i < first ? i : end.last + (i - first);
+                uint8_t *dst = static_cast<uint8_t *>(p.D) + row * p.ldd * eb;
+                const int64_t bytes = static_cast<int64_t>(p.N) * eb;
+                const int64_t body = vec ? bytes / 16 * 16 : 0;
+                for (int64_t b = lane * 16; b < body; b += 512)
+                    *reinterpret_cast<uint4 *>(dst + b) = make_uint4(0u, 0u, 0u, 0u);
+                for (int64_t b = body + lane * 2; b < bytes; b += 64) *reinterpret_cast<uint16_t *>(dst + b) = 0;
+            }
+        }
+        if (lane == 0) ptx::bulk_wait_group_read<0>();
+        __syncwarp();
+    }
+
+    __syncthreads();
+    if constexpr (PAIR) {
+        // as gemm_kernel: neither CTA leaves while copies, MMAs or arrivals
+        // of the other may still reach it; an abort's unequal issue counts
+        // are settled first
+        ptx::cluster_sync_all();
+        if (leader && warp == 0 && lane == 0) {
+            const uint32_t i_l = *issued_slot;
+            const uint32_t i_p = ptx::ld_cluster_u32(ptx::map_to_cta(ptx::smem_addr(issued_slot), 1u));
+            const uint32_t hi = i_l > i_p ? i_l : i_p;
+            const uint32_t lo = hi > STAGES ? hi - STAGES : 0u;
+            const uint32_t fringe_l = issued_slot[1];
+            const uint32_t fringe_p = ptx::ld_cluster_u32(ptx::map_to_cta(ptx::smem_addr(issued_slot + 1), 1u));
+            for (uint32_t j = lo; j < hi; ++j) {
+                const uint32_t s = j % STAGES;
+                // a fringe brings no bytes here (each CTA waited for its own)
+                if (((j < i_l ? fringe_l : fringe_p) >> s) & 1u) continue;
+                if (j < i_l && j >= i_p)
+                    ptx::mbar_complete_tx(full_bar(s), G::STAGE);
+                else if (j >= i_l && j < i_p)
+                    ptx::mbar_arrive_expect_tx(full_bar(s), G::STAGE);
+                if (!wait_drain(full_bar(s), (j / STAGES) & 1u, wd)) break;
+            }
+        }
+        ptx::cluster_sync_all();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        if constexpr (PAIR)
+            ptx::tmem_dealloc_pair(tmem_base, TMEM_ALLOC);
+        else
+            ptx::tmem_dealloc(tmem_base, TMEM_ALLOC);
+    }
+}
+
+}  // namespace tg

@@ -1,5 +1,5 @@
 """Operators of a mixture-of-experts layer on torch tensors: tokens sorted by
-expert and back.
+expert and back, and the experts' products over the sorted rows.
 
 As the rest of the package this is a thin binding of ``include/tg_gemm.h``:
 pointers, shapes and strides are read off the tensors, and all arithmetic
@@ -8,14 +8,16 @@ torch's current stream).
 """
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple
 
 import torch
 
-from . import TgError, _stream_ptr
-from ._abi import TG_BF16, TG_F32, TG_OK, load
+from . import ACTIVATIONS, TgError, _operand, _operand_geometry, _stream_ptr, _with_layout
+from ._abi import TG_BF16, TG_F32, TG_OK, load, tg_epilogue
 
-__all__ = ["ExpertOrder", "expert_sort", "expert_dispatch", "expert_gather", "expert_combine", "expert_combine_grad"]
+__all__ = ["ExpertOrder", "expert_sort", "expert_dispatch", "expert_gather", "expert_combine", "expert_combine_grad",
+           "gemm_grouped", "gemm_grouped_wgrad"]
 
 _DTYPES = {torch.float32: TG_F32, torch.bfloat16: TG_BF16}
 
@@ -188,3 +190,91 @@ def expert_combine_grad(dy, ys, order: ExpertOrder, weights, *, dys=None, dweigh
                                          ld_w, T, k, offsets.numel() - 1, D, pdys, ld_dys, t_dys, pdw, ld_dw,
                                          _stream_ptr(stream)), "tg_expert_combine_grad")
     return dys, dweights
+
+
+def _offsets(offsets, what="offsets"):
+    if offsets.dtype != torch.int32 or not offsets.is_cuda or not offsets.is_contiguous():
+        raise TypeError(f"{what} must be a contiguous int32 CUDA tensor")
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError(f"{what} must have shape [groups + 1]")
+    return offsets.data_ptr(), offsets.numel() - 1
+
+
+def _bf16_rows(t, what):
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{what} must be a bf16 CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have shape [rows, columns]")
+    p, rows, cols, ld, _, _ = _operand_geometry(t, -2, what)
+    return p, rows, cols, ld
+
+
+def _epilogue(D, alpha, activation="none", bias=None, groups=0, N=0):
+    ep = tg_epilogue()
+    ep.alpha = float(alpha)
+    ep.activation = ACTIVATIONS[activation]
+    ep.out_type = TG_BF16 if D.dtype == torch.bfloat16 else TG_F32
+    if bias is not None:
+        if bias.dtype != torch.float32 or not bias.is_cuda or (bias.shape[-1] > 1 and bias.stride(-1) != 1):
+            raise TypeError("bias must be an fp32 CUDA tensor with unit stride in its last dimension")
+        if bias.shape not in ((N,), (groups, N)):
+            raise ValueError(f"bias must have shape [{N}] or [{groups}, {N}]")
+        ep.bias = bias.data_ptr()
+        ep.bias_stride = bias.stride(0) if bias.dim() == 2 and groups > 1 else 0
+    return ep
+
+
+def _out(D, shape, out_dtype, device):
+    if D is None:
+        return torch.empty(shape, dtype=out_dtype if out_dtype is not None else torch.float32, device=device)
+    if D.dtype not in (torch.float32, torch.bfloat16) or not D.is_cuda:
+        raise TypeError("D must be an fp32 or bf16 CUDA tensor")
+    if D.shape != shape:
+        raise ValueError(f"D must have shape {tuple(shape)}")
+    return D
+
+
+def gemm_grouped(A, B, offsets, D=None, *, alpha: float = 1.0, bias=None, activation: str = "none", out_dtype=None,
+                 options=None, stream=None):
+    """D [S, N] = act(alpha * A @ B[g] + bias[g]) for the rows s of A [S, K]
+    with offsets[g] <= s < offsets[g + 1] (int32 [groups + 1] on the GPU, an
+    order's), zero for rows in no group.  A and B [groups, K, N] are bf16; a
+    transposed view of B is taken as it is, so the gradient of A is
+    gemm_grouped(dD, B.transpose(1, 2), offsets).  bias: fp32 [N] or
+    [groups, N]; D: fp32 (default) or bf16."""
+    po, groups = _offsets(offsets)
+    pa, S, K, lda = _bf16_rows(A, "A")
+    if B.dtype != torch.bfloat16 or not B.is_cuda:
+        raise TypeError("B must be a bf16 CUDA tensor")
+    if B.dim() != 3 or B.shape[0] != groups:
+        raise ValueError(f"B must have shape [{groups}, K, N]")
+    pb, K2, N, ldb, _, strideB, b_cm = _operand(B, "B")
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    D = _out(D, (S, N), out_dtype, A.device)
+    pd, _, _, ldd, _, _ = _operand_geometry(D, -2, "D")
+    options = _with_layout(options, False, b_cm)
+    ep = _epilogue(D, alpha, activation, bias, groups, N)
+    _check(load().tg_gemm_grouped(pa, pb, pd, po, groups, S, N, K, lda, ldb, strideB, ldd, ctypes.byref(ep),
+                                  _stream_ptr(stream), ctypes.byref(options) if options is not None else None),
+           "tg_gemm_grouped")
+    return D
+
+
+def gemm_grouped_wgrad(A, B, offsets, D=None, *, alpha: float = 1.0, out_dtype=None, options=None, stream=None):
+    """D [groups, M, N]: D[g] = alpha * A[rows g]^T @ B[rows g] for bf16 A
+    [S, M] and B [S, N], rows g = offsets[g] .. offsets[g + 1] - 1; zero for
+    an empty group.  With the forward call's A and dL/dD for B this is the
+    gradient of its weights.  D: fp32 (default) or bf16."""
+    po, groups = _offsets(offsets)
+    pa, S, M, lda = _bf16_rows(A, "A")
+    pb, S2, N, ldb = _bf16_rows(B, "B")
+    if S2 != S:
+        raise ValueError(f"A and B have {S} and {S2} rows")
+    D = _out(D, (groups, M, N), out_dtype, A.device)
+    pd, _, _, ldd, _, strideD = _operand_geometry(D, -2, "D")
+    ep = _epilogue(D, alpha)
+    _check(load().tg_gemm_grouped_wgrad(pa, pb, pd, po, groups, S, M, N, lda, ldb, ldd, strideD, ctypes.byref(ep),
+                                        _stream_ptr(stream), ctypes.byref(options) if options is not None else None),
+           "tg_gemm_grouped_wgrad")
+    return D
