@@ -487,6 +487,37 @@ tg_status tg_gemm_grouped_wgrad(const void *A, const void *B, void *D, const int
                                 int64_t S, int64_t M, int64_t N, int64_t lda, int64_t ldb, int64_t ldd,
                                 int64_t strideD, const tg_epilogue *ep, tg_stream_t stream, const tg_options *opt);
 
+/* 4-bit weight formats of tg_gemv_w4. */
+typedef enum { TG_W4_INT4 = 0, TG_W4_E2M1 = 1 } tg_w4_format;
+
+/* Products of a few 16-bit rows with 4-bit weights and group scales: the
+ * form for single tokens, where the weights are the traffic.
+ *     y[s][n] = sum_{k<K} x[s][k] * w_g[n][k]
+ * for the rows offsets[g] <= s < offsets[g + 1] of every group g (offsets in
+ * device memory, as in tg_gemm_grouped; rows of no group get zeros; NULL
+ * with groups = 1: all S rows are group 0's).  x is S x K bf16.  W_g = W + g *
+ * strideW holds N x K codes of 4 bits, two a byte, laid out as tg_gemm_mxfp4's
+ * operands (element k of a row in byte k / 2, the low nibble for even k); K,
+ * ldw and strideW count elements and must be even.  Every group_size
+ * consecutive codes of a row share a scale:
+ *   TG_W4_INT4  w = (code - z) * scale, codes 0 .. 15, scales bf16
+ *               (scales + g * stride_s, row pitch ld_s >= ceil(K/group_size),
+ *               in elements), z the low four bits of the byte in zeros (laid
+ *               out like the scales), 8 where zeros is NULL; group_size 32,
+ *               64 or 128
+ *   TG_W4_E2M1  w = e2m1(code) * 2^(e - 127), e the E8M0 byte in scales (255:
+ *               NaN), group_size 32, zeros NULL: tg_gemm_mxfp4's weights
+ * Products and sums are fp32 (a code's value is exact; a group's sum is
+ * scaled once), y is fp32 or bf16 (y_type), rounded once.  Any alignment of
+ * whole elements; weights and x with 16-byte rows are read fastest.  Any
+ * number of rows is computed; the weights are read again for every eight
+ * rows of a group.  At most 65535 groups may have rows
+ * (TG_ERR_UNSUPPORTED where min(groups, S) is more). */
+tg_status tg_gemv_w4(const void *x, int64_t ldx, const void *W, int64_t ldw, int64_t strideW, const void *scales,
+                     int64_t ld_s, int64_t stride_s, const uint8_t *zeros, int64_t ld_z, int64_t stride_z,
+                     int32_t format, int32_t group_size, const int32_t *offsets, int64_t groups, int64_t S, int64_t N,
+                     int64_t K, void *y, int64_t ldy, int32_t y_type, tg_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the device error words that
  * the kernels' watchdog writes: the one of `stream`'s workspace, and the one
  * of tg_gemm_splitk_static on the current device.  TG_ERR_TIMEOUT if a wait

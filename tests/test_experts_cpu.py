@@ -118,3 +118,20 @@ def test_grouped_refusals(lib):
                dict(opt=tg.make_options(direct=2))):
         assert wgrad(**kw) == INVALID, kw
     assert rows(S=0) == tg.TG_OK and rows(N=0, ldb=1, ldd=1) == tg.TG_OK and wgrad(M=0) == tg.TG_OK
+
+
+def test_w4_refusals(lib):
+    def call(**kw):
+        a = dict(x=X, ldx=128, W=XS, ldw=128, strideW=128 * 64, scales=SRC, ld_s=1, stride_s=64, zeros=None, ld_z=0, stride_z=0,
+                 format=0, group=128, offsets=OFF, groups=4, S=10, N=64, K=128, y=DY, ldy=64, y_type=0)
+        a.update(kw)
+        return lib.tg_gemv_w4(*a.values(), None)
+
+    for kw in (dict(groups=0), dict(S=-1), dict(N=-1), dict(K=-2), dict(K=127), dict(ldx=127), dict(ldw=126), dict(ldw=129),
+               dict(strideW=-2), dict(strideW=8191), dict(ld_s=0), dict(group=16), dict(group=48), dict(format=2),
+               dict(format=1), dict(format=1, group=32, ld_s=4, zeros=SLOT, ld_z=4), dict(zeros=SLOT, ld_z=0), dict(offsets=None),
+               dict(x=None), dict(W=None), dict(scales=None), dict(y=None), dict(y=X), dict(y=XS + 4), dict(y=SRC), dict(y=OFF),
+               dict(ldy=63), dict(y_type=2), dict(y=DY + 2), dict(x=X + 1), dict(scales=SRC + 1)):
+        assert call(**kw) == INVALID, kw
+    assert call(groups=70000, S=70000) == UNSUPPORTED
+    assert call(S=0) == tg.TG_OK and call(N=0) == tg.TG_OK

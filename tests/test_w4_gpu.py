@@ -1,0 +1,207 @@
+"""Products with 4-bit weights on the GPU against 64-bit products of the values
+the codes stand for: both formats, every group size, zero points, one to
+many rows, groups with and without rows, odd and misaligned extents.
+
+A code's value times an activation is exact in fp32 (5 and 8 bits), so a
+group's sum and the sum over groups round at most once for each of the K
+additions and once for each scale's product: |error| <= (K + runs + 2) 2^-24
+times the sum of the magnitudes (any order of summation).  The hardware's
+product of a 16-wide k step rounds its intermediate sum toward zero, a factor
+of two on that step: 2 (K + runs + 2) 2^-24 covers both.  bf16 outputs lie
+within one rounding of that."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import tiled_gemm_codegen_gb300 as tg
+from expert_ref import U32, within
+from gpu_helpers import dev
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6, 0, -0.5, -1, -1.5, -2, -3, -4, -6])
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    tg.load()
+    yield
+    assert tg.device_error() == tg.TG_OK
+
+
+def _weights(groups, N, K, fmt, G, seed, zeros=False, pitch=0):
+    """(W, scales, zeros) on the GPU and the values [groups, N, K] in 64 bits."""
+    g = np.random.default_rng(seed)
+    runs = -(-K // G)
+    W = torch.from_numpy(g.integers(0, 256, (groups, N, K // 2 + pitch), dtype=np.uint8)).to(dev())[..., :K // 2]
+    w = W.cpu().numpy()
+    q = np.stack((w & 15, w >> 4), -1).reshape(groups, N, K)
+    z = None
+    if fmt == "e2m1":
+        sc = torch.from_numpy(g.integers(118, 131, (groups, N, runs + pitch), dtype=np.uint8)).to(dev())[..., :runs]
+        v, s = E2M1[q], np.exp2(sc.cpu().double().numpy() - 127)
+    else:
+        sc = torch.from_numpy(g.random((groups, N, runs + pitch)) * 0.1 + 0.01).to(BF).to(dev())[..., :runs]
+        s = sc.cpu().double().numpy()
+        if zeros:
+            z = torch.from_numpy(g.integers(0, 16, (groups, N, runs + pitch), dtype=np.uint8)).to(dev())[..., :runs]
+            v = q - np.repeat(z.cpu().numpy().astype(np.int64), G, -1)[..., :K]
+        else:
+            v = q - 8.0
+    return W, sc, z, v * np.repeat(s, G, -1)[..., :K]
+
+
+def _x(S, K, seed, pitch=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(S, K + pitch, generator=g).to(BF)
+    return x.to(dev())[:, :K], x[:, :K].double().numpy()
+
+
+def _check(y, xv, wv, offsets, K, G, dtype):
+    S, N = y.shape
+    want, mag = np.zeros((S, N)), np.zeros((S, N))
+    for g in range(len(offsets) - 1):
+        r = slice(offsets[g], offsets[g + 1])
+        want[r] = xv[r] @ wv[g].T
+        mag[r] = np.abs(xv[r]) @ np.abs(wv[g]).T
+    assert within(y, want, 2 * (K + -(-K // G) + 2) * U32 * mag, dtype)
+
+
+FORMATS = [("int4", 32, False), ("int4", 64, True), ("int4", 128, False), ("int4", 128, True), ("int4", 32, True),
+           ("e2m1", 32, False)]
+
+
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+@pytest.mark.parametrize("K,N", [(2, 1), (32, 16), (128, 130), (256, 32), (1000, 40), (1024, 33), (2050, 70), (5000, 17), (8192, 48)])
+@pytest.mark.parametrize("S", [1, 3, 8, 21])
+def test_dense(fmt, G, zeros, K, N, S):
+    W, sc, z, wv = _weights(1, N, K, fmt, G, K + N, zeros)
+    x, xv = _x(S, K, S)
+    dtype = BF if S % 2 else F32
+    y = tg.gemv_w4(x, W[0], sc[0], zeros=z[0] if z is not None else None, format=fmt, group=G, out_dtype=dtype)
+    assert y.dtype == dtype
+    _check(y, xv, wv, [0, S], K, G, dtype)
+
+
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+@pytest.mark.parametrize("sizes", [[1], [0, 1, 0, 2], [9, 0, 0, 1, 17], [0] * 33 + [1] * 5 + [0] * 40 + [2], [0, 0]])
+@pytest.mark.parametrize("K,N", [(256, 72), (1100, 50)])
+def test_groups(fmt, G, zeros, sizes, K, N):
+    groups, tail, lead = len(sizes), 2, 1
+    W, sc, z, wv = _weights(groups, N, K, fmt, G, 5 * groups, zeros)
+    offsets = np.concatenate([[0], np.cumsum(sizes)]) + lead
+    S = int(offsets[-1]) + tail
+    x, xv = _x(S, K, 3)
+    off = torch.from_numpy(offsets).int().to(dev())
+    y = torch.full((S, N), float("nan"), device=dev())
+    tg.gemv_w4(x, W, sc, zeros=z, offsets=off, y=y, format=fmt, group=G)
+    _check(y, xv, wv, offsets, K, G, F32)
+
+
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+@pytest.mark.parametrize("pitch", [16, 4, 1])
+def test_pitches_and_guard_bands(fmt, G, zeros, pitch):
+    K, N, S = 480, 40, 5
+    W, sc, z, wv = _weights(2, N, K, fmt, G, pitch, zeros, pitch)
+    x, xv = _x(S, K, 4, pitch)
+    store = torch.full((S + 2, N + pitch), float("nan"), device=dev())
+    off = torch.tensor([0, 2, 5], dtype=torch.int32, device=dev())
+    y = store[1:-1, :N]
+    tg.gemv_w4(x, W, sc, zeros=z, offsets=off, y=y, format=fmt, group=G)
+    _check(y, xv, wv, [0, 2, 5], K, G, F32)
+    y.fill_(float("nan"))
+    assert bool(torch.isnan(store).all())
+
+
+@pytest.mark.parametrize("skip", [1, 2, 8])
+def test_operands_off_their_alignment(skip):
+    """Bases that are not 16-byte aligned."""
+    K, N, S = 512, 24, 2
+    W0, sc0, _, wv = _weights(1, N, K, "int4", 64, 9)
+    W = torch.empty(W0.numel() + 32, dtype=torch.uint8, device=dev())[skip:skip + W0.numel()].view(W0.shape[1:])
+    W.copy_(W0[0])
+    sc = torch.empty(sc0.numel() + 32, dtype=BF, device=dev())[skip:skip + sc0.numel()].view(sc0.shape[1:])
+    sc.copy_(sc0[0])
+    x0, xv = _x(S, K, 5)
+    x = torch.empty(S * K + 32, dtype=BF, device=dev())[skip:skip + S * K].view(S, K)
+    x.copy_(x0)
+    _check(tg.gemv_w4(x, W, sc, group=64), xv, wv, [0, S], K, 64, F32)
+
+
+def test_special_scales_and_activations():
+    """A NaN scale (E8M0 255) and infinite activations reach the outputs they
+    belong to and no others; the smallest scale is 2^-127."""
+    K, N = 96, 40
+    W, sc, _, wv = _weights(1, N, K, "e2m1", 32, 11)
+    W[0, 3] = 0x22  # every code 1
+    sc[0, 3] = 0
+    sc[0, 5, 1] = 255
+    x, xv = _x(3, K, 6)
+    x[1].fill_(1.0)
+    x[2, 40] = float("inf")
+    W[0, 7, 20] = 0x21  # w[7, 40] = 0.5: the infinity stays one
+    y = tg.gemv_w4(x, W[0], sc[0], format="e2m1")
+    yn = y.cpu().double().numpy()
+    assert np.isnan(yn[:, 5]).all()
+    good = [n for n in range(N) if n not in (3, 5)]
+    want = xv[0] @ wv[0].T
+    mag = np.abs(xv[0]) @ np.abs(wv[0]).T
+    assert np.all(np.abs(yn[0] - want)[[n for n in good if n != 7]] <= (2 * 105 * U32 * mag)[[n for n in good if n != 7]])
+    assert yn[1, 3] == 96 * 2.0 ** -127
+    assert np.isinf(yn[2, 7])
+    assert not np.isfinite(yn[2]).any()  # an infinity times a zero code is NaN, else infinite
+
+
+def test_no_terms_and_no_rows():
+    y = tg.gemv_w4(torch.empty(3, 0, dtype=BF, device=dev()), torch.empty(5, 0, dtype=torch.uint8, device=dev()),
+                   torch.empty(5, 0, dtype=BF, device=dev()))
+    assert torch.equal(y, torch.zeros(3, 5, device=dev()))
+    W, sc, _, _ = _weights(1, 8, 64, "int4", 64, 1)
+    assert tg.gemv_w4(torch.empty(0, 64, dtype=BF, device=dev()), W[0], sc[0], group=64).shape == (0, 8)
+
+
+def test_bounds_are_clamped():
+    K, N, S = 128, 24, 6
+    W, sc, _, wv = _weights(2, N, K, "int4", 128, 2)
+    x, xv = _x(S, K, 7)
+    for bounds in ([0, 2, 2 ** 31 - 1], [-9, 2, 6]):
+        off = torch.tensor(bounds, dtype=torch.int32, device=dev())
+        _check(tg.gemv_w4(x, W, sc, offsets=off), xv, wv, [0, 2, 6], K, 128, F32)
+
+
+def test_same_weights_as_the_block_scaled_gemm():
+    """gemv_w4 reads the very operands of gemm_mxfp4: activations that E2M1
+    holds exactly give equal products from both."""
+    K, N, S = 512, 128, 4
+    W, sc, _, _ = _weights(1, N, K, "e2m1", 32, 13)
+    sc.fill_(127)
+    a = torch.randint(0, 256, (S, K // 2), dtype=torch.uint8, device=dev())
+    an = a.cpu().numpy()
+    x = torch.from_numpy(E2M1[np.stack((an & 15, an >> 4), -1).reshape(S, K)]).to(BF).to(dev())
+    ones = torch.full((S, K // 32), 127, dtype=torch.uint8, device=dev())
+    assert torch.equal(tg.gemv_w4(x, W[0], sc[0], format="e2m1"), tg.gemm_mxfp4(a, W[0], ones, sc[0]))
+
+
+def test_same_bits_again_graph_and_stream():
+    K, N, groups = 1024, 200, 6
+    W, sc, z, _ = _weights(groups, N, K, "int4", 64, 17, True)
+    x, _ = _x(9, K, 8)
+    off = torch.tensor([0, 1, 1, 4, 4, 9, 9], dtype=torch.int32, device=dev())
+    first = tg.gemv_w4(x, W, sc, zeros=z, offsets=off, group=64)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y = torch.empty_like(first)
+    with torch.cuda.stream(s):
+        tg.gemv_w4(x, W, sc, zeros=z, offsets=off, group=64, y=y)
+    s.synchronize()
+    assert torch.equal(y, first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        tg.gemv_w4(x, W, sc, zeros=z, offsets=off, group=64, y=y)
+    off.copy_(torch.tensor([0, 0, 3, 3, 7, 7, 8], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, tg.gemv_w4(x, W, sc, zeros=z, offsets=off, group=64))

@@ -515,7 +515,7 @@ def device_error(stream=None) -> int:
 
 
 _EXPERTS = ("ExpertOrder", "expert_sort", "expert_dispatch", "expert_gather", "expert_combine", "expert_combine_grad",
-            "gemm_grouped", "gemm_grouped_wgrad")
+            "gemm_grouped", "gemm_grouped_wgrad", "gemv_w4", "W4_FORMATS")
 __all__ += _EXPERTS
 
 

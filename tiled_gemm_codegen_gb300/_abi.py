@@ -98,6 +98,7 @@ class tg_epilogue(ctypes.Structure):
 TG_ACT_NONE, TG_ACT_RELU, TG_ACT_GELU_TANH, TG_ACT_SILU = 0, 1, 2, 3
 TG_F32, TG_BF16 = 0, 1
 TG_FP8_E4M3, TG_FP8_E5M2 = 0, 1
+TG_W4_INT4, TG_W4_E2M1 = 0, 1
 
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
@@ -137,6 +138,8 @@ SIGNATURES = {
                                                                ctypes.POINTER(tg_options)], ctypes.c_int),
     "tg_gemm_grouped_wgrad": ([_vp, _vp, _vp, _vp] + [_i64] * 8 + [ctypes.POINTER(tg_epilogue), _vp,
                                                                      ctypes.POINTER(tg_options)], ctypes.c_int),
+    "tg_gemv_w4": ([_vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _vp, _i64, _i64, _i64,
+                    _i64, _vp, _i64, _i32, _vp], ctypes.c_int),
     "tg_device_error": ([_vp], ctypes.c_int),
     "tg_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "tg_shutdown": ([], None),

@@ -1,5 +1,6 @@
 """Operators of a mixture-of-experts layer on torch tensors: tokens sorted by
-expert and back, and the experts' products over the sorted rows.
+expert and back, the experts' products over the sorted rows, and products with
+4-bit weights for single tokens.
 
 As the rest of the package this is a thin binding of ``include/tg_gemm.h``:
 pointers, shapes and strides are read off the tensors, and all arithmetic
@@ -14,11 +15,12 @@ from typing import NamedTuple
 import torch
 
 from . import ACTIVATIONS, TgError, _operand, _operand_geometry, _stream_ptr, _with_layout
-from ._abi import TG_BF16, TG_F32, TG_OK, load, tg_epilogue
+from ._abi import TG_BF16, TG_F32, TG_OK, TG_W4_E2M1, TG_W4_INT4, load, tg_epilogue
 
 __all__ = ["ExpertOrder", "expert_sort", "expert_dispatch", "expert_gather", "expert_combine", "expert_combine_grad",
-           "gemm_grouped", "gemm_grouped_wgrad"]
+           "gemm_grouped", "gemm_grouped_wgrad", "gemv_w4", "W4_FORMATS"]
 
+W4_FORMATS = {"int4": TG_W4_INT4, "e2m1": TG_W4_E2M1}
 _DTYPES = {torch.float32: TG_F32, torch.bfloat16: TG_BF16}
 
 
@@ -278,3 +280,60 @@ def gemm_grouped_wgrad(A, B, offsets, D=None, *, alpha: float = 1.0, out_dtype=N
                                         _stream_ptr(stream), ctypes.byref(options) if options is not None else None),
            "tg_gemm_grouped_wgrad")
     return D
+
+
+def gemv_w4(x, W, scales, *, zeros=None, offsets=None, y=None, format: str = "int4", group: int | None = None,
+            out_dtype=None, stream=None):
+    """y [S, N] = x @ w^T for a few bf16 rows x [S, K] and 4-bit weights: W
+    [N, K / 2] or [groups, N, K / 2] uint8, two codes a byte (element k in
+    byte k // 2, the low nibble for even k).  With offsets (int32 [groups + 1],
+    an order's) rows offsets[g] .. offsets[g + 1] - 1 meet group g's weights
+    and rows of no group give zeros.  Every ``group`` codes of a row share a
+    scale:
+
+    - format "int4": w = (code - z) * scale, scales bf16 [.., N, ceil(K /
+      group)], z from zeros (uint8, the scales' shape; None: 8), group 32, 64
+      or 128 (the default);
+    - format "e2m1": w = e2m1(code) * 2^(e - 127), scales uint8 E8M0 codes,
+      group 32: the operands of gemm_mxfp4.
+
+    y: fp32 (default) or bf16."""
+    fmt = W4_FORMATS.get(format)
+    if fmt is None:
+        raise ValueError(f"format must be one of {sorted(W4_FORMATS)}")
+    if group is None:
+        group = 32 if fmt == TG_W4_E2M1 else 128
+    px, S, K, ldx = _bf16_rows(x, "x")
+    if W.dtype != torch.uint8 or not W.is_cuda:
+        raise TypeError("W must be a uint8 CUDA tensor (two codes a byte)")
+    if W.dim() not in (2, 3) or 2 * W.shape[-1] != K:
+        raise ValueError(f"W must have shape [.., N, {K // 2}] for x of {K} columns")
+    pW, N, _, ldw, groups, strideW = _operand_geometry(W, -2, "W")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    shape = (*W.shape[:-1], -(-K // group))
+    geo = []
+    want = torch.uint8 if fmt == TG_W4_E2M1 else torch.bfloat16
+    for t, dt, name in ((scales, want, "scales"), (zeros, torch.uint8, "zeros")):
+        if t is None:
+            geo.append((None, 0, 0))
+            continue
+        if t.dtype != dt or not t.is_cuda:
+            raise TypeError(f"{name} must be a {dt} CUDA tensor")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {list(shape)}")
+        p, _, _, ld, _, st = _operand_geometry(t, -2, name)
+        geo.append((p, ld, st))
+    po = None
+    if offsets is not None:
+        po, n = _offsets(offsets)
+        if n != groups:
+            raise ValueError(f"offsets must have shape [{groups + 1}]")
+    elif groups != 1:
+        raise ValueError("weights of several groups need offsets")
+    y = _out(y, (S, N), out_dtype, x.device)
+    py, _, _, ldy, _, _ = _operand_geometry(y, -2, "y")
+    (ps, ld_s, st_s), (pz, ld_z, st_z) = geo
+    _check(load().tg_gemv_w4(px, ldx, pW, 2 * ldw, 2 * strideW, ps, ld_s, st_s, pz, ld_z, st_z, fmt, group, po, groups, S, N, K,
+                             py, ldy, TG_BF16 if y.dtype == torch.bfloat16 else TG_F32, _stream_ptr(stream)), "tg_gemv_w4")
+    return y
