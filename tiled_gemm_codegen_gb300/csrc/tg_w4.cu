@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "tg_gemm.h"
@@ -158,6 +159,303 @@ __global__ void __launch_bounds__(ANY_COLS * 32) w4_any_kernel(const W4Args a)
     }
 }
 
+// ------------------------------------------------------------ tile kernel
+// A CTA computes W4_ROWS weight rows x up to 8 activation rows.  Its warps
+// share the rows and split K: a warp takes every WARPS-th step of 256 codes
+// (128 bytes of each weight row), so that together they read long pieces of
+// each row, and their fp32 sums are added in a fixed order at the end.
+//
+// The product is mma.sync m16n8k16 (bf16 in, fp32 sums) with the weights as
+// the 16-row operand: its operands are registers, so a code goes from its
+// staged word to the tensor core without another trip through shared memory,
+// which a tcgen05 operand would need; at one to eight rows the tensor work is
+// a small part of either's rate and HBM is the bound.
+//
+// A sum over k may take its terms in any order, so the k index of an operand
+// slot is chosen to suit the packing: within 32 consecutive codes lane (g, c)
+// = (lane / 4, lane % 4) owns the eight codes of one 32-bit word, c of the
+// four, and slots (2c, 2c + 1), (2c + 8, 2c + 9) of two k steps are its nibble
+// pairs (0, 4), (1, 5) and (2, 6), (3, 7) - the pairs that one mask of the
+// word leaves in the two halves of a register.  The activations are paired
+// the same way.
+//
+// A code becomes bf16 exactly: 0x4300 | q is 128 + q, minus 128 + z; an E2M1
+// code's three low bits sit on bf16's exponent and mantissa as its value times
+// 2^-126 (0.5 is a subnormal), and a product by 2^126 restores it.  The sum of
+// a group of codes is multiplied by its scale once, in fp32.
+//
+// Weights, activations, scales and zeros of a step travel through a ring of
+// STAGES slots per warp by cp.async; no warp waits for another before the end.
+constexpr int W4_WARPS = 8;                // 4 where the ring holds eight activation rows
+constexpr int W4_STAGES = 3;
+constexpr int W4_MT = 2;                   // 16-row blocks a warp
+constexpr int W4_ROWS = 16 * W4_MT;
+constexpr int W4_STEP = 256;               // codes of a step
+constexpr int W4_PITCH = W4_STEP / 2 + 16; // staged weight row: the 8 rows of a load fall in 32 different banks
+constexpr int W4_XPITCH = 2 * W4_STEP + 64;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Nibbles (i, i + 4) of a word as two bf16, i = 0 .. 3.  zz: (128 + zero) twice.
+template <bool E2M1>
+__device__ __forceinline__ void decode(uint32_t w, uint32_t zz, uint32_t (&p)[4])
+{
+    if constexpr (E2M1) {
+        const uint32_t big = 0x7E807E80u;  // 2^126 twice
+        p[0] = bf2_mul(((w << 6) & 0x01C001C0u) | ((w << 12) & 0x80008000u), big);
+        p[1] = bf2_mul(((w << 2) & 0x01C001C0u) | ((w << 8) & 0x80008000u), big);
+        p[2] = bf2_mul(((w >> 2) & 0x01C001C0u) | ((w << 4) & 0x80008000u), big);
+        p[3] = bf2_mul(((w >> 6) & 0x01C001C0u) | (w & 0x80008000u), big);
+    } else {
+        p[0] = bf2_sub((w & 0x000F000Fu) | 0x43004300u, zz);
+        p[1] = bf2_sub(((w >> 4) & 0x000F000Fu) | 0x43004300u, zz);
+        p[2] = bf2_sub(((w >> 8) & 0x000F000Fu) | 0x43004300u, zz);
+        p[3] = bf2_sub(((w >> 12) & 0x000F000Fu) | 0x43004300u, zz);
+    }
+}
+
+__host__ __device__ constexpr int w4_warps(int xt) { return xt > 4 ? W4_WARPS / 2 : W4_WARPS; }
+
+// Staged scale words of a row and step: its bytes from the 4-byte boundary
+// before them.
+template <bool E2M1, int RUN>
+struct W4Layout {
+    static constexpr int PER_STEP = W4_STEP / RUN;
+    static constexpr int SB = E2M1 ? 1 : 2;
+    static constexpr int S_WORDS = (PER_STEP * SB + 3) / 4 + 1;
+    static constexpr int Z_WORDS = (PER_STEP + 3) / 4 + 1;
+    static constexpr int stage(int xt, bool zeros)
+    {
+        return W4_ROWS * W4_PITCH + xt * W4_XPITCH + (W4_ROWS * 4 * (S_WORDS + (zeros ? Z_WORDS : 0)) + 15) / 16 * 16;
+    }
+    static constexpr int smem(int xt, bool zeros)  // the sums reuse the ring
+    {
+        return w4_warps(xt) * W4_STAGES * stage(xt, zeros);
+    }
+    static_assert(W4_STAGES * (W4_ROWS * W4_PITCH) >= W4_ROWS * 8 * 4, "room for a warp's sums");
+};
+
+// VEC: bytes of a copy of weights and activations (16, or 4 where rows are
+// only that aligned).  xt: activation rows the ring has room for (1 .. 8).
+template <bool E2M1, int RUN, bool ZEROS, int VEC>
+__global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, int xt)
+{
+    using L = W4Layout<E2M1, RUN>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lg = lane >> 2, lc = lane & 3;
+    const int warps = static_cast<int>(blockDim.x >> 5);
+    const int32_t n0 = static_cast<int32_t>(blockIdx.x) * W4_ROWS;
+    if (blockIdx.y == 0) zero_rows(a, n0, min(n0 + W4_ROWS, a.N));
+    int32_t grp, lo, hi;
+    if (!nth_group(a, static_cast<int32_t>(blockIdx.y), grp, lo, hi)) return;
+    const uint8_t *w0 = a.w + grp * a.stride_w + n0 * a.ldw;
+    const uint8_t *s0 = a.scales + (grp * a.stride_s + n0 * a.lds) * L::SB;
+    const uint8_t *z0 = ZEROS ? a.zeros + grp * a.stride_z + n0 * a.ldz : nullptr;
+    const int32_t rows = min(W4_ROWS, a.N - n0);
+    const int stage = L::stage(xt, ZEROS);
+    const uint32_t ring = ptx::smem_addr(smem) + static_cast<uint32_t>(warp * W4_STAGES * stage);
+    const uint32_t off_x = W4_ROWS * W4_PITCH, off_s = off_x + xt * W4_XPITCH, off_z = off_s + W4_ROWS * 4 * L::S_WORDS;
+    const int32_t steps = (a.K + W4_STEP - 1) / W4_STEP;
+    const int32_t mine = steps > warp ? (steps - warp + warps - 1) / warps : 0;
+    const int32_t row_bytes = a.K / 2;
+    const int32_t s_bytes = a.runs * L::SB;
+
+    for (int32_t r0 = lo; r0 < hi; r0 += xt) {
+        const int32_t nx = min(xt, hi - r0);
+        auto fill = [&](int32_t i) {  // step i of this warp -> slot i mod STAGES
+            const uint32_t dst = ring + static_cast<uint32_t>(i % W4_STAGES * stage);
+            const int32_t k0 = (warp + i * warps) * W4_STEP;
+            if constexpr (VEC == 16) {
+#pragma unroll
+                for (int j = 0; j < W4_ROWS / 4; ++j) {
+                    const int r = j * 4 + (lane >> 3), b = (lane & 7) * 16;
+                    const int32_t left = row_bytes - (k0 / 2 + b);
+                    if (r < rows)
+                        cp_async16(dst + r * W4_PITCH + b, w0 + r * a.ldw + (left > 0 ? k0 / 2 + b : 0), max(0, min(16, left)));
+                }
+                const int32_t xl = 2 * (a.K - k0) - lane * 16;
+                for (int t = 0; t < nx; ++t)
+                    cp_async16(dst + off_x + t * W4_XPITCH + lane * 16, a.x + (r0 + t) * a.ldx + (xl > 0 ? k0 + lane * 8 : 0),
+                               max(0, min(16, xl)));
+            } else {
+                for (int r = 0; r < rows; ++r) {
+                    const int32_t left = row_bytes - (k0 / 2 + lane * 4);
+                    cp_async4(dst + r * W4_PITCH + lane * 4, w0 + r * a.ldw + (left > 0 ? k0 / 2 + lane * 4 : 0), max(0, min(4, left)));
+                }
+                for (int t = 0; t < nx; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int32_t xl = 2 * (a.K - k0) - (j * 32 + lane) * 4;
+                        cp_async4(dst + off_x + t * W4_XPITCH + (j * 32 + lane) * 4,
+                                  a.x + (r0 + t) * a.ldx + (xl > 0 ? k0 + (j * 32 + lane) * 2 : 0), max(0, min(4, xl)));
+                    }
+            }
+            const int32_t at = k0 / RUN;
+            for (int j = lane; j < W4_ROWS * L::S_WORDS; j += 32) {
+                const int r = j / L::S_WORDS, word = j % L::S_WORDS;
+                if (r < rows) {
+                    const uint8_t *p = s0 + (r * a.lds + at) * L::SB;
+                    const uint8_t *src = p - (reinterpret_cast<uintptr_t>(p) & 3u) + word * 4;
+                    const int64_t left = (s0 + r * a.lds * L::SB + s_bytes) - src;
+                    cp_async4(dst + off_s + j * 4, left > 0 ? src : a.scales, static_cast<int>(left < 0 ? 0 : left > 4 ? 4 : left));
+                }
+            }
+            if constexpr (ZEROS) {
+                for (int j = lane; j < W4_ROWS * L::Z_WORDS; j += 32) {
+                    const int r = j / L::Z_WORDS, word = j % L::Z_WORDS;
+                    if (r < rows) {
+                        const uint8_t *p = z0 + r * a.ldz + at;
+                        const uint8_t *src = p - (reinterpret_cast<uintptr_t>(p) & 3u) + word * 4;
+                        const int64_t left = (z0 + r * a.ldz + a.runs) - src;
+                        cp_async4(dst + off_z + j * 4, left > 0 ? src : a.zeros, static_cast<int>(left < 0 ? 0 : left > 4 ? 4 : left));
+                    }
+                }
+            }
+        };
+        float acc[W4_MT][4] = {};
+#pragma unroll
+        for (int i = 0; i < W4_STAGES - 1; ++i) {
+            if (i < mine) fill(i);
+            cp_async_commit();
+        }
+        for (int32_t i = 0; i < mine; ++i) {
+            if (i + W4_STAGES - 1 < mine) fill(i + W4_STAGES - 1);
+            cp_async_commit();
+            cp_async_wait<W4_STAGES - 1>();
+            __syncwarp();
+            const uint32_t src = ring + static_cast<uint32_t>(i % W4_STAGES * stage);
+            const int32_t k0 = (warp + i * warps) * W4_STEP;
+            const int32_t at = k0 / RUN;
+            uint32_t s_row[2 * W4_MT], z_row[2 * W4_MT];
+#pragma unroll
+            for (int h = 0; h < 2 * W4_MT; ++h) {  // rows lg + 8h
+                const int r = lg + 8 * h;
+                s_row[h] = src + off_s + r * 4 * L::S_WORDS +
+                           static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s0 + (r * a.lds + at) * L::SB) & 3u);
+                if constexpr (ZEROS)
+                    z_row[h] = src + off_z + r * 4 * L::Z_WORDS + static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z0 + r * a.ldz + at) & 3u);
+            }
+#pragma unroll
+            for (int j = 0; j < L::PER_STEP; ++j) {
+                if (k0 + j * RUN >= a.K) break;
+                float part[W4_MT][4] = {};
+                uint32_t zz[2 * W4_MT];
+#pragma unroll
+                for (int h = 0; h < 2 * W4_MT; ++h)
+                    zz[h] = ZEROS ? (0x4300u | (lds_u8(z_row[h] + j) & 15u)) * 0x00010001u : 0x43084308u;
+#pragma unroll
+                for (int b = 0; b < RUN / 32; ++b) {
+                    const int blk = j * (RUN / 32) + b;
+                    uint4 xv = make_uint4(0u, 0u, 0u, 0u);
+                    if (lg < nx) xv = lds128(src + off_x + lg * W4_XPITCH + blk * 64 + lc * 16);
+                    const uint32_t x0 = __byte_perm(xv.x, xv.z, 0x5410), x1 = __byte_perm(xv.x, xv.z, 0x7632);
+                    const uint32_t x2 = __byte_perm(xv.y, xv.w, 0x5410), x3 = __byte_perm(xv.y, xv.w, 0x7632);
+#pragma unroll
+                    for (int m = 0; m < W4_MT; ++m) {
+                        uint32_t u[4], v[4];
+                        const uint32_t wa = src + (m * 16 + lg) * W4_PITCH + blk * 16 + lc * 4;
+                        decode<E2M1>(lds32(wa), zz[2 * m], u);
+                        decode<E2M1>(lds32(wa + 8 * W4_PITCH), zz[2 * m + 1], v);
+                        const uint32_t a0[4] = {u[0], v[0], u[1], v[1]}, a1[4] = {u[2], v[2], u[3], v[3]};
+                        mma_16816(part[m], a0, x0, x1);
+                        mma_16816(part[m], a1, x2, x3);
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < W4_MT; ++m) {
+                    float sa, sb;
+                    if constexpr (E2M1) {
+                        sa = e8m0_value(lds_u8(s_row[2 * m] + j));
+                        sb = e8m0_value(lds_u8(s_row[2 * m + 1] + j));
+                    } else {
+                        sa = bf16_value(static_cast<uint16_t>(lds_u16(s_row[2 * m] + 2 * j)));
+                        sb = bf16_value(static_cast<uint16_t>(lds_u16(s_row[2 * m + 1] + 2 * j)));
+                    }
+                    acc[m][0] = fmaf(sa, part[m][0], acc[m][0]);
+                    acc[m][1] = fmaf(sa, part[m][1], acc[m][1]);
+                    acc[m][2] = fmaf(sb, part[m][2], acc[m][2]);
+                    acc[m][3] = fmaf(sb, part[m][3], acc[m][3]);
+                }
+            }
+            __syncwarp();
+        }
+        cp_async_wait<0>();
+        __syncthreads();
+        // sums[warp][x row][weight row]; then added over the warps in order
+        float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+        for (int m = 0; m < W4_MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sums[(warp * 8 + 2 * lc + (i & 1)) * W4_ROWS + m * 16 + lg + 8 * (i >> 1)] = acc[m][i];
+        __syncthreads();
+        for (int i = threadIdx.x; i < nx * W4_ROWS; i += static_cast<int>(blockDim.x)) {
+            const int t = i / W4_ROWS, n = i % W4_ROWS;
+            float sum = 0.0f;
+            for (int v = 0; v < warps; ++v) sum += sums[(v * 8 + t) * W4_ROWS + n];
+            if (n < rows) store_y(a, r0 + t, n0 + n, sum);
+        }
+        if (r0 + xt < hi) __syncthreads();  // the ring is filled again
+    }
+}
+
 template <class... P, class... A>
 cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args)
 {
@@ -172,6 +470,37 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cuda
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
+template <bool E2M1, int RUN, bool ZEROS, int VEC>
+cudaError_t launch_tile(const W4Args &a, int64_t used, int xt, int dev, cudaStream_t s)
+{
+    using L = W4Layout<E2M1, RUN>;
+    auto kern = w4_tile_kernel<E2M1, RUN, ZEROS, VEC>;
+    static std::atomic<unsigned long long> configured{0};  // the shared-memory opt-in, once per device
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(8, ZEROS) > L::smem(4, ZEROS) ? L::smem(8, ZEROS) : L::smem(4, ZEROS));
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    static_assert(L::smem(8, ZEROS) <= SMEM_LIMIT && L::smem(4, ZEROS) <= SMEM_LIMIT, "shared memory");
+    const dim3 grid(static_cast<unsigned>((a.N + W4_ROWS - 1) / W4_ROWS), static_cast<unsigned>(used));
+    return launch(kern, grid, w4_warps(xt) * 32, static_cast<size_t>(L::smem(xt, ZEROS)), s, a, xt);
+}
+
+template <int VEC>
+cudaError_t launch_w4(const W4Args &a, bool e2m1, int64_t used, int xt, int dev, cudaStream_t s)
+{
+    if (e2m1) return launch_tile<true, 32, false, VEC>(a, used, xt, dev, s);
+    if (a.zeros) {
+        if (a.run == 32) return launch_tile<false, 32, true, VEC>(a, used, xt, dev, s);
+        if (a.run == 64) return launch_tile<false, 64, true, VEC>(a, used, xt, dev, s);
+        return launch_tile<false, 128, true, VEC>(a, used, xt, dev, s);
+    }
+    if (a.run == 32) return launch_tile<false, 32, false, VEC>(a, used, xt, dev, s);
+    if (a.run == 64) return launch_tile<false, 64, false, VEC>(a, used, xt, dev, s);
+    return launch_tile<false, 128, false, VEC>(a, used, xt, dev, s);
 }
 
 constexpr int64_t LIMIT = INT32_MAX - 1024;
@@ -248,8 +577,22 @@ TG_API tg_status tg_gemv_w4(const void *x, int64_t ldx, const void *W, int64_t l
         a.y_bf16 = y_type == TG_BF16;
         const int64_t used = offsets ? (groups < S ? groups : S) : 1;  // groups with rows, at most
         if (used > 65535) return TG_ERR_UNSUPPORTED;
-        const dim3 grid(static_cast<unsigned>((N + ANY_COLS - 1) / ANY_COLS), static_cast<unsigned>(used));
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        auto aligned = [&](uintptr_t n) {
+            return ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(W) | static_cast<uintptr_t>(2 * ldx) |
+                     static_cast<uintptr_t>(a.ldw) | static_cast<uintptr_t>(a.stride_w)) % n) == 0 &&
+                   (reinterpret_cast<uintptr_t>(scales) | reinterpret_cast<uintptr_t>(zeros)) % 4 == 0;
+        };
+        if (K > 0 && aligned(4)) {
+            int dev = 0;
+            const cudaError_t e = cudaGetDevice(&dev);
+            if (e != cudaSuccess) return host_cuda_status(e);
+            int xt = 1;  // activation rows a pass: no more than there are
+            while (xt < 8 && xt < S) xt *= 2;
+            const bool e2m1 = format == TG_W4_E2M1;
+            return host_cuda_status(aligned(16) ? launch_w4<16>(a, e2m1, used, xt, dev, s) : launch_w4<4>(a, e2m1, used, xt, dev, s));
+        }
+        const dim3 grid(static_cast<unsigned>((N + ANY_COLS - 1) / ANY_COLS), static_cast<unsigned>(used));
         return host_cuda_status(format == TG_W4_E2M1 ? launch(w4_any_kernel<true>, grid, ANY_COLS * 32, 0, s, a)
                                                      : launch(w4_any_kernel<false>, grid, ANY_COLS * 32, 0, s, a));
     });
