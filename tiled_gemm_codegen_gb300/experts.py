@@ -10,29 +10,60 @@ torch's current stream).
 from __future__ import annotations
 
 import ctypes
-from typing import NamedTuple
 
 import torch
 
-from . import ACTIVATIONS, TgError, _operand, _operand_geometry, _stream_ptr, _with_layout
-from ._abi import TG_BF16, TG_F32, TG_OK, TG_W4_E2M1, TG_W4_INT4, load, tg_epilogue
+from . import ACTIVATIONS, TgError, _stream_ptr, _with_layout
+from ._abi import TG_BF16, TG_F32, TG_OK, TG_W4_E2M1, TG_W4_INT4, load, tg_epilogue, tg_options
 
 __all__ = ["ExpertOrder", "expert_sort", "expert_dispatch", "expert_gather", "expert_combine", "expert_combine_grad",
            "gemm_grouped", "gemm_grouped_wgrad", "gemv_w4", "W4_FORMATS"]
 
 W4_FORMATS = {"int4": TG_W4_INT4, "e2m1": TG_W4_E2M1}
 _DTYPES = {torch.float32: TG_F32, torch.bfloat16: TG_BF16}
+_BF16, _U8 = torch.bfloat16, torch.uint8
+
+# A call for a few tokens costs the GPU 2-3 us, so these wrappers read each
+# property of a tensor once and keep nothing but the library's handle.
+_LIB = None
 
 
-class ExpertOrder(NamedTuple):
-    """The stable order of T x k assignments by expert, int32 CUDA tensors:
+def _lib():
+    global _LIB
+    if _LIB is None:
+        _LIB = load()
+    return _LIB
+
+
+def _stream(t, stream):
+    """The stream's handle; by default the current one of t's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream_ptr(stream)
+
+
+class ExpertOrder:
+    """The stable order of T x k assignments by expert: int32 tensors
     ``offsets`` [E + 1] (expert e's rows), ``source`` [T * k] (the flat
     assignment of each sorted row, -1 behind the last) and ``slot`` [T, k]
-    (the sorted row of each assignment, -1 if dropped)."""
+    (the sorted row of each assignment, -1 if dropped).  Unpacks as the
+    three of them."""
 
-    offsets: torch.Tensor
-    source: torch.Tensor
-    slot: torch.Tensor
+    __slots__ = ("offsets", "source", "slot", "shape", "_ptrs")
+
+    def __init__(self, offsets, source, slot):
+        for t, name in ((offsets, "offsets"), (source, "source"), (slot, "slot")):
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous int32 tensor")
+        if slot.dim() != 2 or slot.shape[1] < 1 or offsets.dim() != 1 or source.shape != (slot.numel(),) or offsets.numel() < 2:
+            raise ValueError("an order holds offsets [E + 1], source [T * k] and slot [T, k]")
+        self.offsets, self.source, self.slot = offsets, source, slot
+        self.shape = (*slot.shape, offsets.numel() - 1)  # T, k, E
+        on_gpu = offsets.is_cuda and source.is_cuda and slot.is_cuda
+        self._ptrs = (offsets.data_ptr(), source.data_ptr(), slot.data_ptr()) if on_gpu else None
+
+    def __iter__(self):
+        return iter((self.offsets, self.source, self.slot))
 
     @classmethod
     def empty(cls, tokens: int, k: int, num_experts: int, device="cuda") -> "ExpertOrder":
@@ -47,66 +78,65 @@ def _check(st: int, what: str) -> None:
         raise TgError(st, what)
 
 
-def _rows(t, what, shape=None):
-    """(ptr, ld, tg_dtype) of a 2-D fp32 or bf16 CUDA tensor with unit
-    stride in its rows."""
+def _order(order, shape=None):
+    """((T, k, E), pointers) of an order on the GPU."""
+    if order._ptrs is None:
+        raise TypeError("the order's tensors must be on the GPU")
+    if shape is not None and order.shape != shape:
+        raise ValueError(f"the order is one of {order.shape[0]} x {order.shape[1]} assignments to {order.shape[2]} experts, "
+                         f"not {shape[0]} x {shape[1]} to {shape[2]}")
+    return order.shape, order._ptrs
+
+
+def _rows(t, what, rows=None, cols=None):
+    """(ptr, rows, columns, ld, tg_dtype) of a 2-D fp32 or bf16 CUDA tensor
+    with unit stride in its rows."""
     dt = _DTYPES.get(t.dtype)
     if dt is None or not t.is_cuda:
         raise TypeError(f"{what} must be an fp32 or bf16 CUDA tensor")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{what} must have shape {tuple(shape) if shape is not None else '[rows, D]'}")
-    rows, cols = t.shape
-    ld, inner = t.stride()
-    if inner != 1 and cols > 1 and rows:
+    shape, st = t.shape, t.stride()
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
+        raise ValueError(f"{what} must have shape [{'rows' if rows is None else rows}, {'columns' if cols is None else cols}]")
+    n, c = shape
+    if st[1] != 1 and c > 1 and n:
         raise ValueError(f"{what} must have unit stride in its last dimension")
-    return t.data_ptr(), (ld if rows > 1 and ld > cols else cols), dt
+    return t.data_ptr(), n, c, (st[0] if n > 1 and st[0] > c else c), dt
 
 
-def _weights(w, shape, what="weights"):
+def _weights(w, T, k, what="weights"):
     if w is None:
         return None, 0
     if w.dtype != torch.float32 or not w.is_cuda:
         raise TypeError(f"{what} must be an fp32 CUDA tensor")
-    if w.shape != shape:
-        raise ValueError(f"{what} must have shape {tuple(shape)}")
-    T, k = shape
-    if k > 1 and T and w.stride(1) != 1:
+    if w.shape != (T, k):
+        raise ValueError(f"{what} must have shape [{T}, {k}]")
+    st = w.stride()
+    if k > 1 and T and st[1] != 1:
         raise ValueError(f"{what} must have unit stride in its last dimension")
-    return w.data_ptr(), (max(w.stride(0), k) if T > 1 else k)
-
-
-def _order(order, T=None, k=None, E=None):
-    offsets, source, slot = order
-    for t, name in ((offsets, "offsets"), (source, "source"), (slot, "slot")):
-        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
-            raise TypeError(f"order.{name} must be a contiguous int32 CUDA tensor")
-    if slot.dim() != 2 or offsets.dim() != 1 or source.shape != (slot.numel(),) or offsets.numel() < 2:
-        raise ValueError("order must hold offsets [E + 1], source [T * k] and slot [T, k]")
-    if T is not None and (slot.shape != (T, k) or offsets.numel() != E + 1):
-        raise ValueError(f"order does not fit {T} x {k} assignments to {E} experts")
-    return offsets, source, slot
+    return w.data_ptr(), (st[0] if T > 1 and st[0] > k else k)
 
 
 def _ids(ids):
-    if ids.dtype not in (torch.int32, torch.int64) or not ids.is_cuda:
+    dt = ids.dtype
+    if (dt != torch.int64 and dt != torch.int32) or not ids.is_cuda:
         raise TypeError("ids must be an int32 or int64 CUDA tensor")
-    if ids.dim() != 2 or ids.shape[1] < 1:
+    shape, st = ids.shape, ids.stride()
+    if len(shape) != 2 or shape[1] < 1:
         raise ValueError("ids must have shape [T, k], k >= 1")
-    T, k = ids.shape
-    if k > 1 and T and ids.stride(1) != 1:
+    T, k = shape
+    if k > 1 and T and st[1] != 1:
         raise ValueError("ids must have unit stride in their last dimension")
-    return T, k, (max(ids.stride(0), k) if T > 1 else k), ids.element_size()
+    return ids.data_ptr(), (8 if dt == torch.int64 else 4), (st[0] if T > 1 and st[0] > k else k), T, k
 
 
 def expert_sort(ids, num_experts: int, *, order: ExpertOrder | None = None, stream=None) -> ExpertOrder:
     """The order of ids [T, k] (int32 or int64; ids outside [0, num_experts)
     drop their assignment) by expert, stable: equal ids keep their order."""
-    T, k, ld, size = _ids(ids)
+    pid, size, ld, T, k = _ids(ids)
     if order is None:
         order = ExpertOrder.empty(T, k, num_experts, ids.device)
-    offsets, source, slot = _order(order, T, k, num_experts)
-    _check(load().tg_expert_sort(ids.data_ptr(), size, ld, T, k, num_experts, offsets.data_ptr(), source.data_ptr(),
-                                 slot.data_ptr(), _stream_ptr(stream)), "tg_expert_sort")
+    _, (po, pso, psl) = _order(order, (T, k, num_experts))
+    _check(_lib().tg_expert_sort(pid, size, ld, T, k, num_experts, po, pso, psl, _stream(ids, stream)), "tg_expert_sort")
     return order
 
 
@@ -114,40 +144,31 @@ def expert_dispatch(x, ids, num_experts: int, *, xs=None, order: ExpertOrder | N
     """(xs, order): the order of ids [T, k] and the rows of x [T, D] (fp32 or
     bf16) in it - xs [T * k, D], xs[s] = x[order.source[s] // k], rows behind
     the last expert zero.  Its gradient is expert_combine(dxs, order)."""
-    T, k, ld, size = _ids(ids)
-    px, ld_x, dt = _rows(x, "x")
-    if x.shape[0] != T:
-        raise ValueError(f"x must have {T} rows")
-    D = x.shape[1]
+    pid, size, ld, T, k = _ids(ids)
+    px, _, D, ld_x, dt = _rows(x, "x", T)
     if xs is None:
         xs = torch.empty(T * k, D, dtype=x.dtype, device=x.device)
-    pxs, ld_xs, dxs = _rows(xs, "xs", (T * k, D))
+    pxs, _, _, ld_xs, dxs = _rows(xs, "xs", T * k, D)
     if dxs != dt:
         raise TypeError("xs must have x's dtype")
     if order is None:
         order = ExpertOrder.empty(T, k, num_experts, ids.device)
-    offsets, source, slot = _order(order, T, k, num_experts)
-    _check(load().tg_expert_dispatch(ids.data_ptr(), size, ld, T, k, num_experts, offsets.data_ptr(),
-                                     source.data_ptr(), slot.data_ptr(), px, ld_x, D, dt, pxs, ld_xs,
-                                     _stream_ptr(stream)), "tg_expert_dispatch")
+    _, (po, pso, psl) = _order(order, (T, k, num_experts))
+    _check(_lib().tg_expert_dispatch(pid, size, ld, T, k, num_experts, po, pso, psl, px, ld_x, D, dt, pxs, ld_xs,
+                                     _stream(x, stream)), "tg_expert_dispatch")
     return xs, order
 
 
 def expert_gather(x, order: ExpertOrder, xs=None, *, stream=None):
     """xs [T * k, D]: the rows of x [T, D] in an order made before."""
-    offsets, _, slot = _order(order)
-    T, k = slot.shape
-    px, ld_x, dt = _rows(x, "x")
-    if x.shape[0] != T:
-        raise ValueError(f"x must have {T} rows")
-    D = x.shape[1]
+    (T, k, E), (po, _, psl) = _order(order)
+    px, _, D, ld_x, dt = _rows(x, "x", T)
     if xs is None:
         xs = torch.empty(T * k, D, dtype=x.dtype, device=x.device)
-    pxs, ld_xs, dxs = _rows(xs, "xs", (T * k, D))
+    pxs, _, _, ld_xs, dxs = _rows(xs, "xs", T * k, D)
     if dxs != dt:
         raise TypeError("xs must have x's dtype")
-    _check(load().tg_expert_gather(px, ld_x, D, dt, T, k, offsets.numel() - 1, offsets.data_ptr(), slot.data_ptr(),
-                                   pxs, ld_xs, _stream_ptr(stream)), "tg_expert_gather")
+    _check(_lib().tg_expert_gather(px, ld_x, D, dt, T, k, E, po, psl, pxs, ld_xs, _stream(x, stream)), "tg_expert_gather")
     return xs
 
 
@@ -156,16 +177,14 @@ def expert_combine(ys, order: ExpertOrder, weights=None, *, y=None, out_dtype=No
     [T * k, D] (fp32 or bf16) and fp32 weights [T, k] (None: ones, the
     gradient of expert_dispatch's rows), summed in fp32 and rounded once;
     dropped assignments add nothing.  y: out_dtype, by default ys's."""
-    _, _, slot = _order(order)
-    T, k = slot.shape
-    pys, ld_ys, dt = _rows(ys, "ys")
-    S, D = ys.shape
-    pw, ld_w = _weights(weights, slot.shape)
+    (T, k, _), (_, _, psl) = _order(order)
+    pys, S, D, ld_ys, dt = _rows(ys, "ys")
+    pw, ld_w = _weights(weights, T, k)
     if y is None:
         y = torch.empty(T, D, dtype=out_dtype if out_dtype is not None else ys.dtype, device=ys.device)
-    py, ld_y, dty = _rows(y, "y", (T, D))
-    _check(load().tg_expert_combine(pys, ld_ys, dt, S, slot.data_ptr(), pw, ld_w, T, k, D, py, ld_y, dty,
-                                    _stream_ptr(stream)), "tg_expert_combine")
+    py, _, _, ld_y, dty = _rows(y, "y", T, D)
+    _check(_lib().tg_expert_combine(pys, ld_ys, dt, S, psl, pw, ld_w, T, k, D, py, ld_y, dty, _stream(ys, stream)),
+           "tg_expert_combine")
     return y
 
 
@@ -174,48 +193,70 @@ def expert_combine_grad(dy, ys, order: ExpertOrder, weights, *, dys=None, dweigh
     dys[order.slot[t, j]] = weights[t, j] * dy[t] (rows of no assignment
     zero; out_dtype, by default ys's) and dweights[t, j] = <dy[t],
     ys[order.slot[t, j]]> (fp32; dropped: zero)."""
-    offsets, _, slot = _order(order)
-    T, k = slot.shape
-    pdy, ld_dy, t_dy = _rows(dy, "dy")
-    D = dy.shape[1]
-    if dy.shape[0] != T:
-        raise ValueError(f"dy must have {T} rows")
-    pys, ld_ys, t_ys = _rows(ys, "ys", (T * k, D))
-    pw, ld_w = _weights(weights, slot.shape)
+    (T, k, E), (po, _, psl) = _order(order)
+    pdy, _, D, ld_dy, t_dy = _rows(dy, "dy", T)
+    pys, _, _, ld_ys, t_ys = _rows(ys, "ys", T * k, D)
+    pw, ld_w = _weights(weights, T, k)
     if dys is None:
         dys = torch.empty(T * k, D, dtype=out_dtype if out_dtype is not None else ys.dtype, device=dy.device)
     if dweights is None:
         dweights = torch.empty(T, k, dtype=torch.float32, device=dy.device)
-    pdys, ld_dys, t_dys = _rows(dys, "dys", (T * k, D))
-    pdw, ld_dw = _weights(dweights, slot.shape, "dweights")
-    _check(load().tg_expert_combine_grad(pdy, ld_dy, t_dy, pys, ld_ys, t_ys, offsets.data_ptr(), slot.data_ptr(), pw,
-                                         ld_w, T, k, offsets.numel() - 1, D, pdys, ld_dys, t_dys, pdw, ld_dw,
-                                         _stream_ptr(stream)), "tg_expert_combine_grad")
+    pdys, _, _, ld_dys, t_dys = _rows(dys, "dys", T * k, D)
+    pdw, ld_dw = _weights(dweights, T, k, "dweights")
+    _check(_lib().tg_expert_combine_grad(pdy, ld_dy, t_dy, pys, ld_ys, t_ys, po, psl, pw, ld_w, T, k, E, D, pdys, ld_dys, t_dys,
+                                         pdw, ld_dw, _stream(dy, stream)), "tg_expert_combine_grad")
     return dys, dweights
 
 
-def _offsets(offsets, what="offsets"):
+def _offsets(offsets):
     if offsets.dtype != torch.int32 or not offsets.is_cuda or not offsets.is_contiguous():
-        raise TypeError(f"{what} must be a contiguous int32 CUDA tensor")
-    if offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError(f"{what} must have shape [groups + 1]")
-    return offsets.data_ptr(), offsets.numel() - 1
+        raise TypeError("offsets must be a contiguous int32 CUDA tensor")
+    shape = offsets.shape
+    if len(shape) != 1 or shape[0] < 2:
+        raise ValueError("offsets must have shape [groups + 1]")
+    return offsets.data_ptr(), shape[0] - 1
 
 
 def _bf16_rows(t, what):
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
+    if t.dtype != _BF16:
         raise TypeError(f"{what} must be a bf16 CUDA tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{what} must have shape [rows, columns]")
-    p, rows, cols, ld, _, _ = _operand_geometry(t, -2, what)
-    return p, rows, cols, ld
+    return _rows(t, what)[:4]
 
 
-def _epilogue(D, alpha, activation="none", bias=None, groups=0, N=0):
+def _matrices(t, what):
+    """(ptr, groups, rows, columns, ld, group stride, column-major) of a 3-D
+    CUDA tensor whose matrices are row-major or transposed views."""
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{what} must have shape [groups, rows, columns]")
+    g, r, c = shape
+    sg = st[0] if g > 1 else 0
+    if c > 1 and st[2] != 1 and (st[1] == 1 or r == 1):
+        return t.data_ptr(), g, r, c, (st[2] if st[2] > r else max(r, 1)), sg, True
+    if st[2] != 1 and c > 1 and t.numel():
+        raise ValueError(f"{what} must have unit stride in one of its last two dimensions")
+    return t.data_ptr(), g, r, c, (st[1] if r > 1 and st[1] > c else max(c, 1)), sg, False
+
+
+def _plain_epilogue(out_type):
+    ep = tg_epilogue()
+    ep.alpha = 1.0
+    ep.out_type = out_type
+    return ctypes.byref(ep)
+
+
+_PLAIN = {torch.float32: _plain_epilogue(TG_F32), torch.bfloat16: _plain_epilogue(TG_BF16)}
+_B_COL_MAJOR = ctypes.byref(tg_options(b_col_major=1))
+
+
+def _epilogue(dtype, alpha, activation="none", bias=None, groups=0, N=0):
+    """The epilogue, by reference."""
+    if alpha == 1.0 and activation == "none" and bias is None:
+        return _PLAIN[dtype]
     ep = tg_epilogue()
     ep.alpha = float(alpha)
     ep.activation = ACTIVATIONS[activation]
-    ep.out_type = TG_BF16 if D.dtype == torch.bfloat16 else TG_F32
+    ep.out_type = _DTYPES[dtype]
     if bias is not None:
         if bias.dtype != torch.float32 or not bias.is_cuda or (bias.shape[-1] > 1 and bias.stride(-1) != 1):
             raise TypeError("bias must be an fp32 CUDA tensor with unit stride in its last dimension")
@@ -223,17 +264,7 @@ def _epilogue(D, alpha, activation="none", bias=None, groups=0, N=0):
             raise ValueError(f"bias must have shape [{N}] or [{groups}, {N}]")
         ep.bias = bias.data_ptr()
         ep.bias_stride = bias.stride(0) if bias.dim() == 2 and groups > 1 else 0
-    return ep
-
-
-def _out(D, shape, out_dtype, device):
-    if D is None:
-        return torch.empty(shape, dtype=out_dtype if out_dtype is not None else torch.float32, device=device)
-    if D.dtype not in (torch.float32, torch.bfloat16) or not D.is_cuda:
-        raise TypeError("D must be an fp32 or bf16 CUDA tensor")
-    if D.shape != shape:
-        raise ValueError(f"D must have shape {tuple(shape)}")
-    return D
+    return ctypes.byref(ep)
 
 
 def gemm_grouped(A, B, offsets, D=None, *, alpha: float = 1.0, bias=None, activation: str = "none", out_dtype=None,
@@ -246,19 +277,22 @@ def gemm_grouped(A, B, offsets, D=None, *, alpha: float = 1.0, bias=None, activa
     [groups, N]; D: fp32 (default) or bf16."""
     po, groups = _offsets(offsets)
     pa, S, K, lda = _bf16_rows(A, "A")
-    if B.dtype != torch.bfloat16 or not B.is_cuda:
+    if B.dtype != _BF16 or not B.is_cuda:
         raise TypeError("B must be a bf16 CUDA tensor")
-    if B.dim() != 3 or B.shape[0] != groups:
+    pb, gb, K2, N, ldb, strideB, b_cm = _matrices(B, "B")
+    if gb != groups:
         raise ValueError(f"B must have shape [{groups}, K, N]")
-    pb, K2, N, ldb, _, strideB, b_cm = _operand(B, "B")
     if K2 != K:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
-    D = _out(D, (S, N), out_dtype, A.device)
-    pd, _, _, ldd, _, _ = _operand_geometry(D, -2, "D")
-    options = _with_layout(options, False, b_cm)
-    ep = _epilogue(D, alpha, activation, bias, groups, N)
-    _check(load().tg_gemm_grouped(pa, pb, pd, po, groups, S, N, K, lda, ldb, strideB, ldd, ctypes.byref(ep),
-                                  _stream_ptr(stream), ctypes.byref(options) if options is not None else None),
+    if D is None:
+        D = torch.empty(S, N, dtype=out_dtype if out_dtype is not None else torch.float32, device=A.device)
+    pd, _, _, ldd, _ = _rows(D, "D", S, N)
+    if options is not None:
+        options = ctypes.byref(_with_layout(options, False, b_cm))
+    elif b_cm:
+        options = _B_COL_MAJOR
+    _check(_lib().tg_gemm_grouped(pa, pb, pd, po, groups, S, N, K, lda, ldb, strideB, ldd,
+                                  _epilogue(D.dtype, alpha, activation, bias, groups, N), _stream(A, stream), options),
            "tg_gemm_grouped")
     return D
 
@@ -273,13 +307,30 @@ def gemm_grouped_wgrad(A, B, offsets, D=None, *, alpha: float = 1.0, out_dtype=N
     pb, S2, N, ldb = _bf16_rows(B, "B")
     if S2 != S:
         raise ValueError(f"A and B have {S} and {S2} rows")
-    D = _out(D, (groups, M, N), out_dtype, A.device)
-    pd, _, _, ldd, _, strideD = _operand_geometry(D, -2, "D")
-    ep = _epilogue(D, alpha)
-    _check(load().tg_gemm_grouped_wgrad(pa, pb, pd, po, groups, S, M, N, lda, ldb, ldd, strideD, ctypes.byref(ep),
-                                        _stream_ptr(stream), ctypes.byref(options) if options is not None else None),
+    if D is None:
+        D = torch.empty(groups, M, N, dtype=out_dtype if out_dtype is not None else torch.float32, device=A.device)
+    if D.dtype not in _DTYPES or not D.is_cuda:
+        raise TypeError("D must be an fp32 or bf16 CUDA tensor")
+    pd, gd, Md, Nd, ldd, strideD, d_cm = _matrices(D, "D")
+    if (gd, Md, Nd) != (groups, M, N) or d_cm:
+        raise ValueError(f"D must be row-major with shape [{groups}, {M}, {N}]")
+    _check(_lib().tg_gemm_grouped_wgrad(pa, pb, pd, po, groups, S, M, N, lda, ldb, ldd, strideD, _epilogue(D.dtype, alpha),
+                                        _stream(A, stream), ctypes.byref(options) if options is not None else None),
            "tg_gemm_grouped_wgrad")
     return D
+
+
+def _per_row(t, what, dtype, lead, cols):
+    """(ptr, ld, group stride) of scales or zeros [*lead, cols]."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{what} must be a {dtype} CUDA tensor")
+    if t.shape != (*lead, cols):
+        raise ValueError(f"{what} must have shape {[*lead, cols]}")
+    st = t.stride()
+    if cols > 1 and st[-1] != 1:
+        raise ValueError(f"{what} must have unit stride in its last dimension")
+    ld = st[-2] if lead[-1] > 1 and st[-2] > cols else max(cols, 1)
+    return t.data_ptr(), ld, (st[0] if len(lead) == 2 and lead[0] > 1 else 0)
 
 
 def gemv_w4(x, W, scales, *, zeros=None, offsets=None, y=None, format: str = "int4", group: int | None = None,
@@ -303,27 +354,19 @@ def gemv_w4(x, W, scales, *, zeros=None, offsets=None, y=None, format: str = "in
         raise ValueError(f"format must be one of {sorted(W4_FORMATS)}")
     if group is None:
         group = 32 if fmt == TG_W4_E2M1 else 128
-    px, S, K, ldx = _bf16_rows(x, "x")
-    if W.dtype != torch.uint8 or not W.is_cuda:
-        raise TypeError("W must be a uint8 CUDA tensor (two codes a byte)")
-    if W.dim() not in (2, 3) or 2 * W.shape[-1] != K:
-        raise ValueError(f"W must have shape [.., N, {K // 2}] for x of {K} columns")
-    pW, N, _, ldw, groups, strideW = _operand_geometry(W, -2, "W")
-    if group not in (32, 64, 128):
+    elif group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
-    shape = (*W.shape[:-1], -(-K // group))
-    geo = []
-    want = torch.uint8 if fmt == TG_W4_E2M1 else torch.bfloat16
-    for t, dt, name in ((scales, want, "scales"), (zeros, torch.uint8, "zeros")):
-        if t is None:
-            geo.append((None, 0, 0))
-            continue
-        if t.dtype != dt or not t.is_cuda:
-            raise TypeError(f"{name} must be a {dt} CUDA tensor")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {list(shape)}")
-        p, _, _, ld, _, st = _operand_geometry(t, -2, name)
-        geo.append((p, ld, st))
+    px, S, K, ldx = _bf16_rows(x, "x")
+    if W.dtype != _U8 or not W.is_cuda:
+        raise TypeError("W must be a uint8 CUDA tensor (two codes a byte)")
+    lead = tuple(W.shape[:-1])
+    if len(lead) not in (1, 2) or 2 * W.shape[-1] != K:
+        raise ValueError(f"W must have shape [.., N, {K // 2}] for x of {K} columns")
+    groups, N = (lead if len(lead) == 2 else (1, lead[0]))
+    pW, ldw, strideW = _per_row(W, "W", _U8, lead, K // 2)
+    runs = -(-K // group)
+    ps, ld_s, st_s = _per_row(scales, "scales", _U8 if fmt == TG_W4_E2M1 else _BF16, lead, runs)
+    pz, ld_z, st_z = _per_row(zeros, "zeros", _U8, lead, runs) if zeros is not None else (None, 0, 0)
     po = None
     if offsets is not None:
         po, n = _offsets(offsets)
@@ -331,9 +374,9 @@ def gemv_w4(x, W, scales, *, zeros=None, offsets=None, y=None, format: str = "in
             raise ValueError(f"offsets must have shape [{groups + 1}]")
     elif groups != 1:
         raise ValueError("weights of several groups need offsets")
-    y = _out(y, (S, N), out_dtype, x.device)
-    py, _, _, ldy, _, _ = _operand_geometry(y, -2, "y")
-    (ps, ld_s, st_s), (pz, ld_z, st_z) = geo
-    _check(load().tg_gemv_w4(px, ldx, pW, 2 * ldw, 2 * strideW, ps, ld_s, st_s, pz, ld_z, st_z, fmt, group, po, groups, S, N, K,
-                             py, ldy, TG_BF16 if y.dtype == torch.bfloat16 else TG_F32, _stream_ptr(stream)), "tg_gemv_w4")
+    if y is None:
+        y = torch.empty(S, N, dtype=out_dtype if out_dtype is not None else torch.float32, device=x.device)
+    py, _, _, ldy, ty = _rows(y, "y", S, N)
+    _check(_lib().tg_gemv_w4(px, ldx, pW, 2 * ldw, 2 * strideW, ps, ld_s, st_s, pz, ld_z, st_z, fmt, group, po, groups, S, N, K,
+                             py, ldy, ty, _stream(x, stream)), "tg_gemv_w4")
     return y
