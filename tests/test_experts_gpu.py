@@ -58,7 +58,7 @@ def _np(t):
 
 
 SORT = [(0, 3, 5), (1, 1, 1), (1, 8, 64), (5, 2, 8), (31, 4, 7), (128, 8, 1024), (1024, 1, 3), (1025, 1, 1023),
-        (700, 3, 17), (4096, 8, 60), (33333, 2, 256), (70000, 8, 128)]
+        (700, 3, 17), (900, 5, 1024), (2048, 8, 60), (5461, 3, 100), (4096, 8, 60), (33333, 2, 256), (70000, 8, 128)]
 
 
 @pytest.mark.parametrize("T,k,E", SORT)
@@ -112,7 +112,7 @@ ROWS = [(64, None, 0), (8, None, 0), (1, None, 0), (7, None, 0), (1001, None, 0)
 
 
 @pytest.mark.parametrize("D,pitch,offset", ROWS)
-@pytest.mark.parametrize("T,k,E", [(1, 8, 64), (37, 3, 9), (700, 2, 33)])
+@pytest.mark.parametrize("T,k,E", [(1, 8, 64), (37, 3, 9), (700, 2, 33), (9000, 2, 5)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_dispatch_and_gather(D, pitch, offset, T, k, E, dtype):
     ids = _ids(T, k, E, D + T)
@@ -234,8 +234,8 @@ def test_gather_gradient_is_the_unweighted_combine():
 
 
 def test_graph_capture_and_streams():
-    T, k, E, D = 3000, 2, 16, 128
-    for tokens in (T, 40):  # three launches; one
+    T, k, E, D = 9000, 2, 16, 128
+    for tokens in (T, 3000, 40):  # three sorting launches; one; one with the copy
         x = torch.randn(tokens, D, device=dev()).to(BF)
         ids = torch.randint(0, E, (tokens, k), device=dev())
         w = torch.rand(tokens, k, device=dev())

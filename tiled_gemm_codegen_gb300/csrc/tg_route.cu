@@ -19,12 +19,13 @@
 namespace tg {
 namespace {
 
-constexpr int MAX_EXPERTS = 1024;      // histograms of 8 warps x 1024 fit static shared memory
-constexpr int SORT_THREADS = 256;
-constexpr int SORT_WARPS = SORT_THREADS / 32;
-constexpr int SORT_BATCH = 4;          // ids a thread ranks at once
-constexpr int SORT_IDS = SORT_THREADS * SORT_BATCH;  // 1024 ids a block and step
-constexpr int MAX_SORT_BLOCKS = 512;   // rows of the count matrix every placing block sums
+constexpr int MAX_EXPERTS = 1024;
+constexpr int SORT_BATCH = 4;                 // ids a thread ranks at once
+constexpr int ONE_THREADS = 256;              // a block that ranks every id of a call
+constexpr int ONE_IDS = ONE_THREADS * SORT_BATCH;
+constexpr int PLACE_THREADS = 128;            // a block of the three-launch sort
+constexpr int PLACE_IDS = PLACE_THREADS * SORT_BATCH;
+constexpr int MAX_SORT_BLOCKS = 4096;         // columns of the count matrix
 
 // The ids of one call and where its order goes.
 struct SortArgs {
@@ -34,10 +35,11 @@ struct SortArgs {
     int32_t n;       // T * k
     int32_t k, E;
     int32_t *offsets, *source, *slot;
-    int32_t *counts;   // [blocks][epad], or null when one block holds every id
+    int32_t *counts;   // [E][blocks]: a block's ids of each expert, then those of the blocks before it
+    int32_t *totals;   // [E]
     int32_t epad;      // E rounded up to 4
     int32_t blocks;    // blocks of the count and place kernels
-    int32_t per_block; // ids of a block, a multiple of SORT_IDS
+    int32_t per_block; // ids of a block
 };
 
 // Rows copied into expert order, in bytes.
@@ -65,29 +67,39 @@ __device__ __forceinline__ int32_t load_id(const SortArgs &a, int32_t f)
     return v >= 0 && v < a.E ? v : -1;
 }
 
-// Ranks of up to SORT_IDS ids inside their experts, in the order of the ids.
-// Warp w holds ids [w * seg, (w + 1) * seg), 32 consecutive ones at a time:
-// an id's rank is the number of equal ids in lower lanes (match.any) plus
-// the warp's count so far.  On return hist[w][e] is warp w's count.
+// Ranks of up to THREADS * SORT_BATCH ids inside their experts, in the order
+// of the ids.  Warp w holds ids [w * seg, (w + 1) * seg), 32 consecutive ones
+// at a time: an id's rank is the number of equal ids in lower lanes
+// (match.any) plus the warp's count so far.  On return hist[w][e] is warp
+// w's count.
 struct Ranked {
     int32_t id[SORT_BATCH];
     int32_t rank[SORT_BATCH];
 };
 
+// Ids of a warp's segment: 32 times what the block's threads need each.
+template <int THREADS>
+__device__ __forceinline__ int32_t segment(int32_t n)
+{
+    return (n + THREADS - 1) / THREADS * 32;
+}
+
+template <int THREADS>
 __device__ __forceinline__ void rank_ids(const SortArgs &a, int32_t base, int32_t n, int32_t *hist, Ranked &r)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < SORT_WARPS * a.epad; i += SORT_THREADS) hist[i] = 0;
-    const int32_t seg = (n + SORT_THREADS - 1) / SORT_THREADS * 32;  // <= 32 * SORT_BATCH
+    const int32_t seg = segment<THREADS>(n);
 #pragma unroll
     for (int b = 0; b < SORT_BATCH; ++b) {
         const int32_t i = warp * seg + b * 32 + lane;
         r.id[b] = (b * 32 < seg && i < n) ? load_id(a, base + i) : -1;
     }
+    for (int i = threadIdx.x; i < THREADS / 32 * a.epad; i += THREADS) hist[i] = 0;
     __syncthreads();
     int32_t *mine = hist + warp * a.epad;
 #pragma unroll
     for (int b = 0; b < SORT_BATCH; ++b) {
+        if (b * 32 >= seg) break;
         const uint32_t peers = __match_any_sync(0xffffffffu, r.id[b]);
         const uint32_t before = peers & ((1u << lane) - 1u);
         const int32_t seen = r.id[b] >= 0 ? mine[r.id[b]] : 0;
@@ -100,27 +112,31 @@ __device__ __forceinline__ void rank_ids(const SortArgs &a, int32_t base, int32_
 }
 
 // hist[w][e] -> the count of the warps before w; returns expert e's total.
+template <int WARPS>
 __device__ __forceinline__ int32_t scan_warps(int32_t *hist, int32_t epad, int32_t e)
 {
-    int32_t sum = 0;
+    int32_t v[WARPS], sum = 0;  // all loads before the first store: one latency, not WARPS of them
 #pragma unroll
-    for (int w = 0; w < SORT_WARPS; ++w) {
-        const int32_t v = hist[w * epad + e];
+    for (int w = 0; w < WARPS; ++w) v[w] = hist[w * epad + e];
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
         hist[w * epad + e] = sum;
-        sum += v;
+        sum += v[w];
     }
     return sum;
 }
 
 // Exclusive scan of v[0 .. E) in shared memory, in place; v[E] = the sum.
-// Thread t owns entries 4t .. 4t+3 (E <= 4 * SORT_THREADS).
+// Thread t owns PER consecutive entries.
+template <int THREADS>
 __device__ __forceinline__ void scan_experts(int32_t *v, int32_t E, int32_t *warp_sums)
 {
+    constexpr int PER = MAX_EXPERTS / THREADS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int e0 = threadIdx.x * 4;
-    int32_t x[4], mine = 0;
+    const int e0 = static_cast<int>(threadIdx.x) * PER;
+    int32_t x[PER], mine = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < PER; ++i) {
         x[i] = e0 + i < E ? v[e0 + i] : 0;
         mine += x[i];
     }
@@ -132,114 +148,79 @@ __device__ __forceinline__ void scan_experts(int32_t *v, int32_t E, int32_t *war
     }
     if (lane == 31) warp_sums[warp] = incl;
     __syncthreads();
-    int32_t at = incl - mine;
-    for (int w = 0; w < warp; ++w) at += warp_sums[w];
+    int32_t at = lane < warp ? warp_sums[lane] : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int d = 16; d > 0; d >>= 1) at += __shfl_xor_sync(0xffffffffu, at, d);
+    at += incl - mine;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
         if (e0 + i <= E) v[e0 + i] = at;
         at += x[i];
     }
-    if (E == 4 * SORT_THREADS && e0 + 4 == E) v[E] = at;  // otherwise the owner of entry E wrote it
+    if (E == MAX_EXPERTS && threadIdx.x == THREADS - 1) v[E] = at;  // otherwise the owner of entry E wrote it
     __syncthreads();
 }
 
 // How many ids of each expert a block's share holds.
-__global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const SortArgs a)
+__global__ void __launch_bounds__(PLACE_THREADS) sort_count_kernel(const SortArgs a)
 {
     __shared__ int32_t hist[MAX_EXPERTS];
-    for (int i = threadIdx.x; i < a.epad; i += SORT_THREADS) hist[i] = 0;
+    for (int i = threadIdx.x; i < a.E; i += PLACE_THREADS) hist[i] = 0;
     __syncthreads();
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.per_block;
     const int64_t hi = lo + a.per_block < a.n ? lo + a.per_block : a.n;
-    for (int64_t f = lo + threadIdx.x; f < hi; f += SORT_THREADS) {
+#pragma unroll 4
+    for (int64_t f = lo + threadIdx.x; f < hi; f += PLACE_THREADS) {
         const int32_t e = load_id(a, static_cast<int32_t>(f));
         if (e >= 0) atomicAdd(&hist[e], 1);  // integers: the order does not show
     }
     __syncthreads();
-    int32_t *out = a.counts + static_cast<int64_t>(blockIdx.x) * a.epad;
-    for (int i = threadIdx.x; i < a.epad; i += SORT_THREADS) out[i] = hist[i];
+    for (int i = threadIdx.x; i < a.E; i += PLACE_THREADS) a.counts[static_cast<int64_t>(i) * a.blocks + blockIdx.x] = hist[i];
 }
 
-// Shared memory of a sorting block.
-struct SortSmem {
-    int32_t hist[SORT_WARPS * MAX_EXPERTS];
-    int32_t base[MAX_EXPERTS + 4];   // next slot of each expert
-    int32_t warp_sums[SORT_WARPS];
-};
-
-// The slots of a block's ids.  Every block sums the count matrix itself
-// (all rows: the experts' offsets; the rows before its own: where its ids
-// go), so that no kernel stands between the count and this one: at 128
-// blocks x 128 experts the 64 KB come from L2 in about 2 us, in every block
-// at once.
-__global__ void __launch_bounds__(SORT_THREADS) sort_place_kernel(const SortArgs a)
+// A warp per expert: its counts become the sums of the blocks before.
+__global__ void __launch_bounds__(128) sort_scan_kernel(const SortArgs a)
 {
-    __shared__ __align__(16) SortSmem sm;
-    int32_t *before = sm.hist;  // until the first step
-    for (int i = threadIdx.x; i < a.epad; i += SORT_THREADS) sm.base[i] = before[i] = 0;
-    __syncthreads();
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    {
-        const int nq = a.epad / 4;             // 16-byte quads of a row
-        const int rows = SORT_THREADS / nq;    // rows read side by side (>= 1: nq <= 256)
-        const int q = threadIdx.x % nq, r0 = threadIdx.x / nq;
-        if (r0 < rows) {
-            const int4 *src = reinterpret_cast<const int4 *>(a.counts) + q;
-            int4 all = make_int4(0, 0, 0, 0), bef = all;
-#pragma unroll 8
-            for (int r = r0; r < a.blocks; r += rows) {
-                const int4 v = __ldcg(src + static_cast<int64_t>(r) * nq);
-                all.x += v.x; all.y += v.y; all.z += v.z; all.w += v.w;
-                if (r < static_cast<int>(blockIdx.x)) { bef.x += v.x; bef.y += v.y; bef.z += v.z; bef.w += v.w; }
-            }
-            int32_t *t = sm.base + 4 * q, *b = before + 4 * q;
-            atomicAdd(t, all.x); atomicAdd(t + 1, all.y); atomicAdd(t + 2, all.z); atomicAdd(t + 3, all.w);
-            atomicAdd(b, bef.x); atomicAdd(b + 1, bef.y); atomicAdd(b + 2, bef.z); atomicAdd(b + 3, bef.w);
-        }
-    }
-    __syncthreads();
-    scan_experts(sm.base, a.E, sm.warp_sums);
-    if (blockIdx.x == 0)
-        for (int e = threadIdx.x; e <= a.E; e += SORT_THREADS) a.offsets[e] = sm.base[e];
-    const int32_t kept = sm.base[a.E];
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += SORT_THREADS) sm.base[e] += before[e];
-    __syncthreads();
-    // slots past the last kept assignment hold nothing
-    for (int64_t s = kept + static_cast<int64_t>(blockIdx.x) * SORT_THREADS + threadIdx.x; s < a.n;
-         s += static_cast<int64_t>(gridDim.x) * SORT_THREADS)
-        a.source[s] = -1;
-    const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.per_block;
-    const int64_t hi = lo + a.per_block < a.n ? lo + a.per_block : a.n;
-    for (int64_t at = lo; at < hi; at += SORT_IDS) {
-        const int32_t n = static_cast<int32_t>(hi - at < SORT_IDS ? hi - at : SORT_IDS);
-        Ranked r;
-        rank_ids(a, static_cast<int32_t>(at), n, sm.hist, r);
-        int32_t total[4];
-        for (int e = threadIdx.x, i = 0; e < a.E; e += SORT_THREADS, ++i) total[i] = scan_warps(sm.hist, a.epad, e);
-        __syncthreads();
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        const int32_t seg = (n + SORT_THREADS - 1) / SORT_THREADS * 32;
+    const int lane = threadIdx.x & 31;
+    const int32_t e = static_cast<int32_t>(blockIdx.x) * 4 + static_cast<int32_t>(threadIdx.x >> 5);
+    if (e >= a.E) return;
+    int32_t *row = a.counts + static_cast<int64_t>(e) * a.blocks;
+    int32_t sum = 0;
+    for (int32_t b0 = 0; b0 < a.blocks; b0 += 128) {
+        int32_t v[4], mine = 0;
 #pragma unroll
-        for (int b = 0; b < SORT_BATCH; ++b) {
-            const int32_t i = warp * seg + b * 32 + lane;
-            if (b * 32 >= seg || i >= n) continue;
-            const int32_t f = static_cast<int32_t>(at) + i;
-            int32_t s = -1;
-            if (r.id[b] >= 0) {
-                s = sm.base[r.id[b]] + sm.hist[warp * a.epad + r.id[b]] + r.rank[b];
-                a.source[s] = f;
-            }
-            a.slot[f] = s;
+        for (int i = 0; i < 4; ++i) {
+            const int32_t b = b0 + lane * 4 + i;
+            v[i] = b < a.blocks ? __ldcg(row + b) : 0;
+            mine += v[i];
         }
-        __syncthreads();
-        for (int e = threadIdx.x, i = 0; e < a.E; e += SORT_THREADS, ++i) sm.base[e] += total[i];
-        __syncthreads();
+        int32_t incl = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t t = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += t;
+        }
+        int32_t at = sum + incl - mine;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int32_t b = b0 + lane * 4 + i;
+            if (b < a.blocks) row[b] = at;
+            at += v[i];
+        }
+        sum += __shfl_sync(0xffffffffu, incl, 31);
     }
+    if (lane == 0) a.totals[e] = sum;
 }
+
+// Shared memory of a ranking block, hist[warps][epad] behind it.
+struct SortSmem {
+    int32_t base[MAX_EXPERTS + 4];   // next slot of each expert
+    int32_t warp_sums[32];
+};
 
 // ------------------------------------------------------------ row copies
 // The 16 bytes at p (any multiple of 2), which lie inside [lo, hi): one
@@ -342,24 +323,154 @@ __global__ void __launch_bounds__(256) gather_any_kernel(const CopyArgs a, int s
         copy_chunk(a.xs + (kept + i / a.chunks) * a.ld_xs, nullptr, a.row_bytes, i % a.chunks, a.x, hi);
 }
 
-// The whole dispatch of at most SORT_IDS assignments in one launch: every
-// block ranks all ids itself (they are few, and no block then waits for
-// another), block 0 writes the order, and the blocks share the row copies.
-// With copy.x null only the order is written.
-__global__ void __launch_bounds__(SORT_THREADS) dispatch_small_kernel(const SortArgs a, const CopyArgs cp)
+// The slots of a block's ids, PLACE_IDS at a time; the experts' starting slots
+// come from the scan.
+__global__ void __launch_bounds__(PLACE_THREADS) sort_place_kernel(const SortArgs a)
 {
     __shared__ __align__(16) SortSmem sm;
-    __shared__ int32_t source[SORT_IDS];
+    extern __shared__ int32_t hist[];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    for (int e = threadIdx.x; e < a.E; e += PLACE_THREADS) sm.base[e] = __ldcg(a.totals + e);
+    __syncthreads();
+    scan_experts<PLACE_THREADS>(sm.base, a.E, sm.warp_sums);
+    const int32_t kept = sm.base[a.E];
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= a.E; e += PLACE_THREADS) a.offsets[e] = sm.base[e];
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += PLACE_THREADS)
+        sm.base[e] += __ldcg(a.counts + static_cast<int64_t>(e) * a.blocks + blockIdx.x);
+    // slots past the last kept assignment hold nothing
+    for (int64_t s = kept + static_cast<int64_t>(blockIdx.x) * PLACE_THREADS + threadIdx.x; s < a.n;
+         s += static_cast<int64_t>(gridDim.x) * PLACE_THREADS)
+        a.source[s] = -1;
+    const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.per_block;
+    const int64_t hi = lo + a.per_block < a.n ? lo + a.per_block : a.n;
+    constexpr int WARPS = PLACE_THREADS / 32;
+    for (int64_t at = lo; at < hi; at += PLACE_IDS) {
+        const int32_t n = static_cast<int32_t>(hi - at < PLACE_IDS ? hi - at : PLACE_IDS);
+        Ranked r;
+        rank_ids<PLACE_THREADS>(a, static_cast<int32_t>(at), n, hist, r);
+        int32_t total[MAX_EXPERTS / PLACE_THREADS];
+#pragma unroll
+        for (int i = 0; i < MAX_EXPERTS / PLACE_THREADS; ++i) {
+            const int e = static_cast<int>(threadIdx.x) + i * PLACE_THREADS;
+            if (e < a.E) total[i] = scan_warps<WARPS>(hist, a.epad, e);
+        }
+        __syncthreads();
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int32_t seg = segment<PLACE_THREADS>(n);
+#pragma unroll
+        for (int b = 0; b < SORT_BATCH; ++b) {
+            const int32_t i = warp * seg + b * 32 + lane;
+            if (b * 32 >= seg || i >= n) continue;
+            const int32_t f = static_cast<int32_t>(at) + i;
+            int32_t s = -1;
+            if (r.id[b] >= 0) {
+                s = sm.base[r.id[b]] + hist[warp * a.epad + r.id[b]] + r.rank[b];
+                a.source[s] = f;
+            }
+            a.slot[f] = s;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MAX_EXPERTS / PLACE_THREADS; ++i) {
+            const int e = static_cast<int>(threadIdx.x) + i * PLACE_THREADS;
+            if (e < a.E) sm.base[e] += total[i];
+        }
+        __syncthreads();
+    }
+}
+
+// Up to CLUSTER_IDS ids in one launch: a cluster of CLUSTER blocks, each
+// ranking CLUSTER_THREADS * SORT_BATCH of them.  Every block's counts by
+// expert lie in its shared memory, where the others read them: the experts'
+// offsets from all, the place of a block's own ids from the blocks before it.
+constexpr int CLUSTER = 8;
+constexpr int CLUSTER_THREADS = 512;
+constexpr int CLUSTER_IDS = CLUSTER * CLUSTER_THREADS * SORT_BATCH;
+
+__global__ void __launch_bounds__(CLUSTER_THREADS) sort_cluster_kernel(const SortArgs a)
+{
+    __shared__ __align__(16) SortSmem sm;
+    __shared__ int32_t mine[MAX_EXPERTS];  // this block's counts
+    extern __shared__ int32_t hist[];
+    constexpr int WARPS = CLUSTER_THREADS / 32, EACH = MAX_EXPERTS / CLUSTER_THREADS;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int32_t rank = static_cast<int32_t>(ptx::cluster_ctarank());
+    const int32_t share = (a.n + CLUSTER - 1) / CLUSTER;
+    const int32_t lo = min(a.n, rank * share), n = min(a.n - lo, share);
+    Ranked r;
+    rank_ids<CLUSTER_THREADS>(a, lo, n, hist, r);
+    for (int e = threadIdx.x; e < a.E; e += CLUSTER_THREADS) mine[e] = scan_warps<WARPS>(hist, a.epad, e);
+    ptx::cluster_sync_all();
+    int32_t before[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int e = static_cast<int>(threadIdx.x) + i * CLUSTER_THREADS;
+        before[i] = 0;
+        if (e >= a.E) continue;
+        int32_t all = 0;
+        const uint32_t at = ptx::smem_addr(mine + e);
+#pragma unroll
+        for (int32_t c = 0; c < CLUSTER; ++c) {
+            const int32_t v = static_cast<int32_t>(ptx::ld_cluster_u32(ptx::map_to_cta(at, static_cast<uint32_t>(c))));
+            all += v;
+            if (c < rank) before[i] += v;
+        }
+        sm.base[e] = all;
+    }
+    ptx::cluster_sync_all();  // no block leaves while another still reads its counts
+    scan_experts<CLUSTER_THREADS>(sm.base, a.E, sm.warp_sums);
+    const int32_t kept = sm.base[a.E];
+    if (rank == 0)
+        for (int e = threadIdx.x; e <= a.E; e += CLUSTER_THREADS) a.offsets[e] = sm.base[e];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int e = static_cast<int>(threadIdx.x) + i * CLUSTER_THREADS;
+        if (e < a.E) sm.base[e] += before[i];
+    }
+    __syncthreads();
+    for (int32_t s = kept + rank * CLUSTER_THREADS + static_cast<int32_t>(threadIdx.x); s < a.n; s += CLUSTER * CLUSTER_THREADS)
+        a.source[s] = -1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t seg = segment<CLUSTER_THREADS>(n);
+#pragma unroll
+    for (int b = 0; b < SORT_BATCH; ++b) {
+        const int32_t i = warp * seg + b * 32 + lane;
+        if (b * 32 >= seg || i >= n) continue;
+        int32_t s = -1;
+        if (r.id[b] >= 0) {
+            s = sm.base[r.id[b]] + hist[warp * a.epad + r.id[b]] + r.rank[b];
+            a.source[s] = lo + i;
+        }
+        a.slot[lo + i] = s;
+    }
+}
+
+// The whole dispatch of at most ONE_IDS assignments in one launch: every
+// block ranks all ids itself (they are few, and no block then waits for
+// another), block 0 writes the order, and the blocks share the row copies.
+// With c.x null only the order is written.
+__global__ void __launch_bounds__(ONE_THREADS) dispatch_one_kernel(const SortArgs a, const CopyArgs c)
+{
+    constexpr int THREADS = ONE_THREADS;
+    __shared__ __align__(16) SortSmem sm;
+    __shared__ int32_t source[THREADS * SORT_BATCH];
+    extern __shared__ int32_t hist[];
+    constexpr int WARPS = THREADS / 32;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     Ranked r;
-    for (int i = threadIdx.x; i < a.n; i += SORT_THREADS) source[i] = -1;
-    rank_ids(a, 0, a.n, sm.hist, r);
-    for (int e = threadIdx.x; e < a.E; e += SORT_THREADS) sm.base[e] = scan_warps(sm.hist, a.epad, e);
+    for (int i = threadIdx.x; i < a.n; i += THREADS) source[i] = -1;
+    rank_ids<THREADS>(a, 0, a.n, hist, r);
+    for (int e = threadIdx.x; e < a.E; e += THREADS) sm.base[e] = scan_warps<WARPS>(hist, a.epad, e);
     __syncthreads();
-    scan_experts(sm.base, a.E, sm.warp_sums);
+    scan_experts<THREADS>(sm.base, a.E, sm.warp_sums);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t seg = (a.n + SORT_THREADS - 1) / SORT_THREADS * 32;
+    const int32_t seg = segment<THREADS>(a.n);
     const bool writes = blockIdx.x == 0;
 #pragma unroll
     for (int b = 0; b < SORT_BATCH; ++b) {
@@ -367,25 +478,35 @@ __global__ void __launch_bounds__(SORT_THREADS) dispatch_small_kernel(const Sort
         if (b * 32 >= seg || f >= a.n) continue;
         int32_t s = -1;
         if (r.id[b] >= 0) {
-            s = sm.base[r.id[b]] + sm.hist[warp * a.epad + r.id[b]] + r.rank[b];
+            s = sm.base[r.id[b]] + hist[warp * a.epad + r.id[b]] + r.rank[b];
             source[s] = f;
         }
         if (writes) a.slot[f] = s;
     }
     __syncthreads();
     if (writes) {
-        for (int e = threadIdx.x; e <= a.E; e += SORT_THREADS) a.offsets[e] = sm.base[e];
-        for (int i = threadIdx.x; i < a.n; i += SORT_THREADS) a.source[i] = source[i];
+        for (int e = threadIdx.x; e <= a.E; e += THREADS) a.offsets[e] = sm.base[e];
+        for (int i = threadIdx.x; i < a.n; i += THREADS) a.source[i] = source[i];
     }
-    if (!cp.x) return;
-    const uint8_t *hi = cp.x + (cp.T - 1) * cp.ld_x + cp.row_bytes;
-    const int64_t total = static_cast<int64_t>(a.n) * cp.chunks;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * SORT_THREADS + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * SORT_THREADS) {
-        const int32_t s = static_cast<int32_t>(i / cp.chunks);
+    if (!c.x) return;
+    const uint8_t *hi = c.x + (c.T - 1) * c.ld_x + c.row_bytes;
+    // sorted rows in turn: a block's threads cover whole rows
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * THREADS;
+    int64_t s = first / c.chunks;
+    int32_t ch = static_cast<int32_t>(first % c.chunks);
+    const int64_t ds = step / c.chunks;
+    const int32_t dch = static_cast<int32_t>(step % c.chunks);
+#pragma unroll 2
+    while (s < a.n) {
         const int32_t f = source[s];
-        copy_chunk(cp.xs + s * cp.ld_xs, f >= 0 ? cp.x + static_cast<int64_t>(f / a.k) * cp.ld_x : nullptr,
-                   cp.row_bytes, i % cp.chunks, cp.x, hi);
+        copy_chunk(c.xs + s * c.ld_xs, f >= 0 ? c.x + static_cast<int64_t>(f / a.k) * c.ld_x : nullptr, c.row_bytes, ch, c.x, hi);
+        s += ds;
+        ch += dch;
+        if (ch >= c.chunks) {
+            ch -= c.chunks;
+            ++s;
+        }
     }
 }
 
@@ -416,19 +537,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// Eight elements from a row at element e0, aligned (16-byte chunks).
-template <bool BF16>
-__device__ __forceinline__ void load8_aligned(const void *row, int64_t e0, float (&f)[8])
-{
-    if constexpr (BF16) {
-        unpack8(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + e0), f);
-    } else {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(row) + e0);
-        const float4 u = p[0], v = p[1];
-        f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w; f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
-    }
 }
 
 template <bool BF16>
@@ -498,6 +606,32 @@ __device__ __forceinline__ int64_t lead_of(const void *row, bool bf16)
 
 // y[t] = sum_j w[t, j] ys[slot[t, j]], in the order of j, in fp32, rounded
 // once.  A thread owns 8 elements of a token: KB rows' loads in flight.
+template <bool BF16>
+struct Raw8;  // eight elements as loaded
+template <>
+struct Raw8<true> {
+    uint4 v;
+    __device__ __forceinline__ void load(const void *row, int64_t e0)
+    {
+        v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + e0));
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const { unpack8(v, f); }
+};
+template <>
+struct Raw8<false> {
+    float4 u, v;
+    __device__ __forceinline__ void load(const void *row, int64_t e0)
+    {
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(row) + e0);
+        u = __ldg(p);
+        v = __ldg(p + 1);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+        f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w; f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+    }
+};
+
 template <bool YS_BF16, bool Y_BF16, int KB>
 __global__ void __launch_bounds__(256) combine_aligned_kernel(const CombineArgs a, int shift)
 {
@@ -511,22 +645,24 @@ __global__ void __launch_bounds__(256) combine_aligned_kernel(const CombineArgs 
     const float *w = a.weights ? a.weights + t * a.ld_w : nullptr;
     float acc[8] = {};
     for (int j0 = 0; j0 < a.k; j0 += KB) {
-        float v[KB][8], wj[KB];
-        bool on[KB];
+        Raw8<YS_BF16> v[KB];
+        uint32_t on = 0;
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
-            const int32_t s = j0 + j < a.k ? slot[j0 + j] : -1;
-            on[j] = s >= 0 && s < a.S;
-            if (on[j]) {
-                load8_aligned<YS_BF16>(row_of(a.ys, s, a.ld_ys, YS_BF16), c * 8, v[j]);
-                wj[j] = w ? w[j0 + j] : 1.0f;
+            const int32_t s = j0 + j < a.k ? __ldg(slot + j0 + j) : -1;
+            if (s >= 0 && s < a.S) {
+                on |= 1u << j;
+                v[j].load(row_of(a.ys, s, a.ld_ys, YS_BF16), c * 8);
             }
         }
 #pragma unroll
         for (int j = 0; j < KB; ++j)
-            if (on[j]) {  // a dropped assignment adds nothing, whatever its weight
+            if (on >> j & 1u) {  // a dropped assignment adds nothing, whatever its weight
+                const float wj = w ? __ldg(w + j0 + j) : 1.0f;
+                float f[8];
+                v[j].get(f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = fmaf(wj[j], v[j][i], acc[i]);
+                for (int i = 0; i < 8; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
             }
     }
     store8_aligned<Y_BF16>(const_cast<uint8_t *>(row_of(a.y, t, a.ld_y, Y_BF16)), c * 8, acc);
@@ -613,48 +749,56 @@ __device__ __forceinline__ float block_sums(float (&v)[KB], float (*part)[KB])
 }
 
 // One block a token: dys[slot[t, j]] = w[t, j] dy[t] and
-// dw[t, j] = <dy[t], ys[slot[t, j]]>.  dy is read once for KB rows; all bf16
-// and 16-byte rows.
+// dw[t, j] = <dy[t], ys[slot[t, j]]>.  dy is read once for KB assignments,
+// whose rows of ys are loaded four at a time; all bf16 and 16-byte rows.
 template <int KB>
-__global__ void __launch_bounds__(256) combine_grad_aligned_kernel(const GradArgs a)
+__global__ void __launch_bounds__(512) combine_grad_aligned_kernel(const GradArgs a)
 {
-    __shared__ float part[8][KB];
+    constexpr int LB = KB < 4 ? KB : 4;
+    __shared__ float part[16][KB];
+    __shared__ int32_t s[KB];
+    __shared__ float w[KB];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int64_t t = blockIdx.x;
     const uint16_t *dy = static_cast<const uint16_t *>(a.dy) + t * a.ld_dy;
     for (int j0 = 0; j0 < a.k; j0 += KB) {
-        int64_t s[KB];
-        float w[KB], dot[KB];
-#pragma unroll
-        for (int j = 0; j < KB; ++j) {
-            const int32_t v = j0 + j < a.k ? a.slot[t * a.k + j0 + j] : -1;
-            s[j] = v >= 0 && v < a.S ? v : -1;
-            w[j] = s[j] >= 0 && a.weights ? a.weights[t * a.ld_w + j0 + j] : 1.0f;
-            dot[j] = 0.0f;
+        if (threadIdx.x < KB) {
+            const int j = j0 + static_cast<int>(threadIdx.x);
+            const int32_t v = j < a.k ? a.slot[t * a.k + j] : -1;
+            s[threadIdx.x] = v < a.S ? v : -1;
+            w[threadIdx.x] = j < a.k && a.weights ? a.weights[t * a.ld_w + j] : 1.0f;
         }
-        for (int64_t c = threadIdx.x; c < a.chunks; c += blockDim.x) {
+        __syncthreads();
+        float dot[KB] = {};
+        for (int32_t c = threadIdx.x; c < a.chunks; c += static_cast<int32_t>(blockDim.x)) {
             float g[8];
-            load8_aligned<true>(dy, c * 8, g);
-            uint4 raw[KB];
-            if (a.dw) {
+            Raw8<true> d;
+            d.load(dy, c * 8);
+            uint4 raw[LB];
 #pragma unroll
-                for (int j = 0; j < KB; ++j)
-                    if (s[j] >= 0)
-                        raw[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.ys) + s[j] * a.ld_ys + c * 8);
-            }
-#pragma unroll
-            for (int j = 0; j < KB; ++j) {
-                if (s[j] < 0) continue;
-                float o[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = w[j] * g[i];
-                store8_aligned<true>(static_cast<uint16_t *>(a.dys) + s[j] * a.ld_dys, c * 8, o);
+            for (int jb = 0; jb < KB; jb += LB) {
                 if (a.dw) {
-                    float v[8];
-                    unpack8(raw[j], v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], v[i], dot[j]);
+                    for (int j = 0; j < LB; ++j)
+                        if (s[jb + j] >= 0)
+                            raw[j] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.ys) +
+                                                                           s[jb + j] * a.ld_ys + c * 8));
+                }
+                if (jb == 0) d.get(g);
+#pragma unroll
+                for (int j = 0; j < LB; ++j) {
+                    if (s[jb + j] < 0) continue;
+                    float o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = w[jb + j] * g[i];
+                    store8_aligned<true>(static_cast<uint16_t *>(a.dys) + s[jb + j] * a.ld_dys, c * 8, o);
+                    if (a.dw) {
+                        float v[8];
+                        unpack8(raw[j], v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dot[jb + j] = fmaf(g[i], v[i], dot[jb + j]);
+                    }
                 }
             }
         }
@@ -662,14 +806,15 @@ __global__ void __launch_bounds__(256) combine_grad_aligned_kernel(const GradArg
             const float sum = block_sums<KB>(dot, part);
             if (threadIdx.x < KB && j0 + threadIdx.x < a.k) a.dw[t * a.ld_dw + j0 + threadIdx.x] = sum;
         }
+        if (j0 + KB < a.k) __syncthreads();  // s and w are written again
     }
     zero_tail(a);
 }
 
 // The same for any type, pitch and alignment: one row of dys at a time.
-__global__ void __launch_bounds__(256) combine_grad_any_kernel(const GradArgs a)
+__global__ void __launch_bounds__(512) combine_grad_any_kernel(const GradArgs a)
 {
-    __shared__ float part[8][1];
+    __shared__ float part[16][1];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int64_t t = blockIdx.x;
@@ -710,20 +855,37 @@ __global__ void __launch_bounds__(256) combine_grad_any_kernel(const GradArgs a)
 
 // ------------------------------------------------------------ host
 template <class... P, class... A>
-cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, cudaStream_t s, A... args)
+cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, A... args)
 {
     // Programmatic dependent launch: the kernel waits (griddepcontrol.wait)
     // before its first access to memory another kernel may write.
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
+// The shared-memory opt-in of a kernel, once per device (under the host
+// mutex).
+template <auto KERN>
+cudaError_t opt_in(int dev, int bytes)
+{
+    static uint64_t configured = 0;
+    if (dev < 64 && ((configured >> dev) & 1u)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) configured |= 1ull << dev;
+    return e;
 }
 
 constexpr int64_t ROW_LIMIT = 1 << 22;            // elements of a row (segments fit grid.y)
@@ -801,7 +963,7 @@ cudaError_t launch_gather(const CopyArgs &c, bool aligned, cudaStream_t s)
     const int64_t per_block = 8 * (32 >> sh);
     const dim3 grid(static_cast<unsigned>((rows + per_block - 1) / per_block),
                     static_cast<unsigned>((c.chunks + (1 << sh) - 1) >> sh));
-    return aligned ? launch(gather_aligned_kernel, grid, 256, s, c, sh) : launch(gather_any_kernel, grid, 256, s, c, sh);
+    return aligned ? launch(gather_aligned_kernel, grid, 256, 0, s, 1, c, sh) : launch(gather_any_kernel, grid, 256, 0, s, 1, c, sh);
 }
 
 // The sort (and, with x, the copy of the rows into expert order).
@@ -846,23 +1008,40 @@ tg_status run_sort(const void *ids, int32_t id_bytes, int64_t ld_ids, int64_t T,
     bool aligned = false;
     CopyArgs c{};
     if (copies) c = copy_args(x, ld_x, D, eb, xs, ld_xs, T, k, E, offsets, slot, &aligned);
-    // Up to SORT_IDS assignments one launch does everything.
-    if (n <= SORT_IDS) {
+    const size_t warp_hist = static_cast<size_t>(a.epad) * 4;
+    // Up to ONE_IDS assignments one launch does everything (1024 of 64
+    // experts: 3.7 us, sorted by a cluster and copied by a second launch 5.8;
+    // blocks of 1024 threads for 4096 of them take 7.7, the cluster 3.7).
+    if (n <= ONE_IDS) {
         int64_t blocks = 1;
-        if (copies) blocks = (n * c.chunks + SORT_THREADS - 1) / SORT_THREADS;
+        if (copies) blocks = (n * c.chunks + ONE_THREADS - 1) / ONE_THREADS;
         if (blocks > 4 * hs.sms) blocks = 4 * hs.sms;
-        return host_cuda_status(launch(dispatch_small_kernel, dim3(static_cast<unsigned>(blocks)), SORT_THREADS, stream, a, c));
+        return host_cuda_status(launch(dispatch_one_kernel, dim3(static_cast<unsigned>(blocks)), ONE_THREADS,
+                                       ONE_THREADS / 32 * warp_hist, stream, 1, a, c));
     }
-    const int64_t steps = (n + SORT_IDS - 1) / SORT_IDS;
-    a.per_block = static_cast<int32_t>((steps + MAX_SORT_BLOCKS - 1) / MAX_SORT_BLOCKS * SORT_IDS);
-    a.blocks = static_cast<int32_t>((n + a.per_block - 1) / a.per_block);
-    void *arena = nullptr;
-    st = host_arena(hs, static_cast<size_t>(a.blocks) * a.epad * 4, &arena);
-    if (st != TG_OK) return st;
-    a.counts = static_cast<int32_t *>(arena);
-    const dim3 grid(static_cast<unsigned>(a.blocks));
-    cudaError_t e = launch(sort_count_kernel, grid, SORT_THREADS, stream, a);
-    if (e == cudaSuccess) e = launch(sort_place_kernel, grid, SORT_THREADS, stream, a);
+    // Up to CLUSTER_IDS one cluster sorts (5000 ids: 3.7 us); beyond, three
+    // launches over all SMs: count, scan and place (32768: 7.1, 262144: 12.3).
+    cudaError_t e;
+    if (n <= CLUSTER_IDS) {
+        constexpr int WARPS = CLUSTER_THREADS / 32;
+        e = opt_in<sort_cluster_kernel>(hs.dev, WARPS * MAX_EXPERTS * 4);
+        if (e == cudaSuccess)
+            e = launch(sort_cluster_kernel, dim3(CLUSTER), CLUSTER_THREADS, WARPS * warp_hist, stream, CLUSTER, a);
+    } else {
+        a.per_block = PLACE_IDS;
+        const int64_t least = (n + MAX_SORT_BLOCKS - 1) / MAX_SORT_BLOCKS;
+        if (a.per_block < least) a.per_block = static_cast<int32_t>((least + PLACE_IDS - 1) / PLACE_IDS * PLACE_IDS);
+        a.blocks = static_cast<int32_t>((n + a.per_block - 1) / a.per_block);
+        void *arena = nullptr;
+        st = host_arena(hs, (static_cast<size_t>(a.blocks) + 1) * a.E * 4, &arena);
+        if (st != TG_OK) return st;
+        a.counts = static_cast<int32_t *>(arena);
+        a.totals = a.counts + static_cast<int64_t>(a.blocks) * a.E;
+        const dim3 grid(static_cast<unsigned>(a.blocks));
+        e = launch(sort_count_kernel, grid, PLACE_THREADS, 0, stream, 1, a);
+        if (e == cudaSuccess) e = launch(sort_scan_kernel, dim3(static_cast<unsigned>((E + 3) / 4)), 128, 0, stream, 1, a);
+        if (e == cudaSuccess) e = launch(sort_place_kernel, grid, PLACE_THREADS, PLACE_THREADS / 32 * warp_hist, stream, 1, a);
+    }
     if (e == cudaSuccess && copies) e = launch_gather(c, aligned, stream);
     return host_cuda_status(e);
 }
@@ -873,9 +1052,9 @@ int64_t dtype_bytes(int32_t t) { return t == TG_BF16 ? 2 : 4; }
 template <bool YS_BF16, bool Y_BF16>
 cudaError_t launch_combine(const CombineArgs &a, dim3 grid, int sh, cudaStream_t s)
 {
-    if (a.k <= 2) return launch(combine_aligned_kernel<YS_BF16, Y_BF16, 2>, grid, 256, s, a, sh);
-    if (a.k <= 4) return launch(combine_aligned_kernel<YS_BF16, Y_BF16, 4>, grid, 256, s, a, sh);
-    return launch(combine_aligned_kernel<YS_BF16, Y_BF16, 8>, grid, 256, s, a, sh);
+    if (a.k <= 2) return launch(combine_aligned_kernel<YS_BF16, Y_BF16, 2>, grid, 256, 0, s, 1, a, sh);
+    if (a.k <= 4) return launch(combine_aligned_kernel<YS_BF16, Y_BF16, 4>, grid, 256, 0, s, 1, a, sh);
+    return launch(combine_aligned_kernel<YS_BF16, Y_BF16, 8>, grid, 256, 0, s, 1, a, sh);
 }
 
 }  // namespace
@@ -963,7 +1142,7 @@ TG_API tg_status tg_expert_combine(const void *ys, int64_t ld_ys, int32_t ys_typ
                         static_cast<unsigned>((a.chunks + (1 << sh) - 1) >> sh));
         cudaError_t e;
         if (!aligned)
-            e = launch(combine_any_kernel, grid, 256, stream, a, sh);
+            e = launch(combine_any_kernel, grid, 256, 0, stream, 1, a, sh);
         else if (a.ys_bf16)
             e = a.y_bf16 ? launch_combine<true, true>(a, grid, sh, stream) : launch_combine<true, false>(a, grid, sh, stream);
         else
@@ -1020,18 +1199,20 @@ TG_API tg_status tg_expert_combine_grad(const void *dy, int64_t ld_dy, int32_t d
         const bool aligned = a.dy_bf16 && a.dys_bf16 && (!dweights || a.ys_bf16) && D % 8 == 0 &&
                              mult16(dy, ld_dy * 2) && mult16(dys, ld_dys * 2) && (!dweights || mult16(ys, ld_ys * 2));
         a.chunks = static_cast<int32_t>(aligned ? D / 8 : (D + 7 + 7) / 8);
-        int threads = 32;
-        while (threads < 256 && threads < a.chunks) threads *= 2;
+        // one turn of the block's threads over a row where 512 of them
+        // suffice, else turns of 256
+        int threads = a.chunks <= 512 ? static_cast<int>((a.chunks + 31) / 32 * 32) : 256;
+        if (threads < 32) threads = 32;
         const dim3 grid(static_cast<unsigned>(T));
         cudaError_t e;
         if (!aligned)
-            e = launch(combine_grad_any_kernel, grid, threads, stream, a);
+            e = launch(combine_grad_any_kernel, grid, threads, 0, stream, 1, a);
         else if (k <= 2)
-            e = launch(combine_grad_aligned_kernel<2>, grid, threads, stream, a);
+            e = launch(combine_grad_aligned_kernel<2>, grid, threads, 0, stream, 1, a);
         else if (k <= 4)
-            e = launch(combine_grad_aligned_kernel<4>, grid, threads, stream, a);
+            e = launch(combine_grad_aligned_kernel<4>, grid, threads, 0, stream, 1, a);
         else
-            e = launch(combine_grad_aligned_kernel<8>, grid, threads, stream, a);
+            e = launch(combine_grad_aligned_kernel<8>, grid, threads, 0, stream, 1, a);
         return host_cuda_status(e);
     });
 }
