@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstdlib>
 #include <cstdint>
 
 #include "tg_gemm.h"
@@ -206,65 +207,70 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a)
+// Plain loads (not volatile): the compiler may move them ahead of the
+// products before them, though not across the waits, which clobber memory.
+__device__ __forceinline__ uint32_t lds32(const uint8_t *a) { return *reinterpret_cast<const uint32_t *>(a); }
+__device__ __forceinline__ uint4 lds128(const uint8_t *a) { return *reinterpret_cast<const uint4 *>(a); }
+__device__ __forceinline__ uint32_t lds_u16(const uint8_t *a) { return *reinterpret_cast<const uint16_t *>(a); }
+__device__ __forceinline__ uint32_t lds_u8(const uint8_t *a) { return *a; }
+
+// d (+)= a b; the first product of a sum takes no accumulator.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool first)
 {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t a)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
+    if (first)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+// A constant the compiler keeps in a register: (w & mask) | magic is one
+// instruction with one immediate and one register operand, two with two
+// immediates.
+__device__ __forceinline__ uint32_t in_register(uint32_t v)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    uint32_t r;
+    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
-
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t masked_or(uint32_t w, uint32_t c)  // (w & MASK) | c
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(c));
+    return r;
+}
 __device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b)
 {
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 __device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b)
 {
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// Nibbles (i, i + 4) of a word as two bf16, i = 0 .. 3.  zz: (128 + zero) twice.
+// Nibbles (i, i + 4) of a word as two bf16, i = 0 .. 3.  magic: 0x4300 twice
+// (int4) or 2^126 twice (e2m1); zz: (128 + zero) twice.
 template <bool E2M1>
-__device__ __forceinline__ void decode(uint32_t w, uint32_t zz, uint32_t (&p)[4])
+__device__ __forceinline__ void decode(uint32_t w, uint32_t magic, uint32_t zz, uint32_t (&p)[4])
 {
     if constexpr (E2M1) {
-        const uint32_t big = 0x7E807E80u;  // 2^126 twice
-        p[0] = bf2_mul(((w << 6) & 0x01C001C0u) | ((w << 12) & 0x80008000u), big);
-        p[1] = bf2_mul(((w << 2) & 0x01C001C0u) | ((w << 8) & 0x80008000u), big);
-        p[2] = bf2_mul(((w >> 2) & 0x01C001C0u) | ((w << 4) & 0x80008000u), big);
-        p[3] = bf2_mul(((w >> 6) & 0x01C001C0u) | (w & 0x80008000u), big);
+        p[0] = bf2_mul(masked_or<0x01C001C0u>(w << 6, (w << 12) & 0x80008000u), magic);
+        p[1] = bf2_mul(masked_or<0x01C001C0u>(w << 2, (w << 8) & 0x80008000u), magic);
+        p[2] = bf2_mul(masked_or<0x01C001C0u>(w >> 2, (w << 4) & 0x80008000u), magic);
+        p[3] = bf2_mul(masked_or<0x01C001C0u>(w >> 6, w & 0x80008000u), magic);
     } else {
-        p[0] = bf2_sub((w & 0x000F000Fu) | 0x43004300u, zz);
-        p[1] = bf2_sub(((w >> 4) & 0x000F000Fu) | 0x43004300u, zz);
-        p[2] = bf2_sub(((w >> 8) & 0x000F000Fu) | 0x43004300u, zz);
-        p[3] = bf2_sub(((w >> 12) & 0x000F000Fu) | 0x43004300u, zz);
+        p[0] = bf2_sub(masked_or<0x000F000Fu>(w, magic), zz);
+        p[1] = bf2_sub(masked_or<0x000F000Fu>(w >> 4, magic), zz);
+        p[2] = bf2_sub(masked_or<0x000F000Fu>(w >> 8, magic), zz);
+        p[3] = bf2_sub(masked_or<0x000F000Fu>(w >> 12, magic), zz);
     }
 }
 
@@ -300,6 +306,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
     ptx::griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lg = lane >> 2, lc = lane & 3;
+    const uint32_t magic = in_register(E2M1 ? 0x7E807E80u : 0x43004300u), eight = in_register(0x43084308u);
     const int warps = static_cast<int>(blockDim.x >> 5);
     const int32_t n0 = static_cast<int32_t>(blockIdx.x) * W4_ROWS;
     if (blockIdx.y == 0) zero_rows(a, n0, min(n0 + W4_ROWS, a.N));
@@ -310,7 +317,8 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
     const uint8_t *z0 = ZEROS ? a.zeros + grp * a.stride_z + n0 * a.ldz : nullptr;
     const int32_t rows = min(W4_ROWS, a.N - n0);
     const int stage = L::stage(xt, ZEROS);
-    const uint32_t ring = ptx::smem_addr(smem) + static_cast<uint32_t>(warp * W4_STAGES * stage);
+    uint8_t *const ring_p = smem + warp * W4_STAGES * stage;
+    const uint32_t ring = ptx::smem_addr(ring_p);
     const uint32_t off_x = W4_ROWS * W4_PITCH, off_s = off_x + xt * W4_XPITCH, off_z = off_s + W4_ROWS * 4 * L::S_WORDS;
     const int32_t steps = (a.K + W4_STEP - 1) / W4_STEP;
     const int32_t mine = steps > warp ? (steps - warp + warps - 1) / warps : 0;
@@ -380,10 +388,10 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
             cp_async_commit();
             cp_async_wait<W4_STAGES - 1>();
             __syncwarp();
-            const uint32_t src = ring + static_cast<uint32_t>(i % W4_STAGES * stage);
+            const uint8_t *src = ring_p + i % W4_STAGES * stage;
             const int32_t k0 = (warp + i * warps) * W4_STEP;
             const int32_t at = k0 / RUN;
-            uint32_t s_row[2 * W4_MT], z_row[2 * W4_MT];
+            const uint8_t *s_row[2 * W4_MT], *z_row[2 * W4_MT];
 #pragma unroll
             for (int h = 0; h < 2 * W4_MT; ++h) {  // rows lg + 8h
                 const int r = lg + 8 * h;
@@ -395,27 +403,27 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
 #pragma unroll
             for (int j = 0; j < L::PER_STEP; ++j) {
                 if (k0 + j * RUN >= a.K) break;
-                float part[W4_MT][4] = {};
+                float part[W4_MT][4];
                 uint32_t zz[2 * W4_MT];
 #pragma unroll
                 for (int h = 0; h < 2 * W4_MT; ++h)
-                    zz[h] = ZEROS ? (0x4300u | (lds_u8(z_row[h] + j) & 15u)) * 0x00010001u : 0x43084308u;
+                    zz[h] = ZEROS ? (0x4300u | (lds_u8(z_row[h] + j) & 15u)) * 0x00010001u : eight;
 #pragma unroll
                 for (int b = 0; b < RUN / 32; ++b) {
                     const int blk = j * (RUN / 32) + b;
-                    uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-                    if (lg < nx) xv = lds128(src + off_x + lg * W4_XPITCH + blk * 64 + lc * 16);
+                    // (an operand column of no row repeats row 0's: its sums are not stored)
+                    const uint4 xv = lds128(src + off_x + (lg < nx ? lg : 0) * W4_XPITCH + blk * 64 + lc * 16);
                     const uint32_t x0 = __byte_perm(xv.x, xv.z, 0x5410), x1 = __byte_perm(xv.x, xv.z, 0x7632);
                     const uint32_t x2 = __byte_perm(xv.y, xv.w, 0x5410), x3 = __byte_perm(xv.y, xv.w, 0x7632);
 #pragma unroll
                     for (int m = 0; m < W4_MT; ++m) {
                         uint32_t u[4], v[4];
-                        const uint32_t wa = src + (m * 16 + lg) * W4_PITCH + blk * 16 + lc * 4;
-                        decode<E2M1>(lds32(wa), zz[2 * m], u);
-                        decode<E2M1>(lds32(wa + 8 * W4_PITCH), zz[2 * m + 1], v);
+                        const uint8_t *wa = src + (m * 16 + lg) * W4_PITCH + blk * 16 + lc * 4;
+                        decode<E2M1>(lds32(wa), magic, zz[2 * m], u);
+                        decode<E2M1>(lds32(wa + 8 * W4_PITCH), magic, zz[2 * m + 1], v);
                         const uint32_t a0[4] = {u[0], v[0], u[1], v[1]}, a1[4] = {u[2], v[2], u[3], v[3]};
-                        mma_16816(part[m], a0, x0, x1);
-                        mma_16816(part[m], a1, x2, x3);
+                        mma_16816(part[m], a0, x0, x1, b == 0);
+                        mma_16816(part[m], a1, x2, x3, false);
                     }
                 }
 #pragma unroll
@@ -454,6 +462,350 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
         }
         if (r0 + xt < hi) __syncthreads();  // the ring is filled again
     }
+}
+
+// ------------------------------------------------------------ stream kernel
+// The same product for weights that TMA can address and activations that fit
+// shared memory whole.  One CTA per SM walks a contiguous range of tiles (16
+// weight rows for each of its teams of `wk` warps, which share K step by
+// step); each warp keeps `stages` TMA boxes of 16 rows x 256 codes in flight
+// across the ends of its tiles, so the weights never stop.  What a tile needs
+// besides is loaded once or ahead: the activations of a group in the order the
+// products want them (their pairs made once instead of at every use), the
+// scales of the next tile by cp.async during this one.
+//
+// A box lies in shared memory with the 128-byte swizzle (16-byte unit u of
+// row r at u ^ (r mod 8)), which puts the words of a block's eight rows in 32
+// different banks.
+struct W4Stream {
+    int32_t xt;        // activation rows a pass
+    int32_t warps, wk; // warps of the CTA, and of a team
+    int32_t stages;
+    int32_t steps;     // of 256 codes
+    int32_t tiles_n;   // tiles of a group
+    int32_t x_pitch;   // bytes of an activation row in shared memory
+    int32_t s_words, z_words;  // staged words of a row's scales and zeros
+    int32_t off_x, off_s, off_z, off_sum;  // bytes in shared memory after the rings
+    uint32_t *err;
+    uint64_t timeout_ns;
+};
+
+constexpr int W4S_ROWS = 16;
+constexpr int W4S_BOX = W4S_ROWS * W4_STEP / 2;  // 2 KB
+constexpr int W4S_WARPS = 16;
+constexpr int W4S_STAGES = 6;
+
+// Pass `nth` over the groups' rows, at most xt rows each: its group, first
+// row and number of rows; false past the last.  Whole warps.
+__device__ __forceinline__ bool nth_pass(const W4Args &a, int32_t xt, int32_t nth, int32_t &g, int32_t &r0, int32_t &nx)
+{
+    if (!a.offsets) {
+        g = 0;
+        r0 = nth * xt;
+        nx = min(xt, a.S - r0);
+        return r0 < a.S;
+    }
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    for (int32_t base = 0; base < a.groups; base += 32) {
+        const int32_t e = base + lane;
+        int32_t l = 0, h = 0;
+        if (e < a.groups) {
+            l = max(0, min(__ldg(a.offsets + e), a.S));
+            h = max(l, min(__ldg(a.offsets + e + 1), a.S));
+        }
+        const int32_t passes = (h - l + xt - 1) / xt;
+        int32_t incl = passes;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        const int32_t count = __shfl_sync(0xffffffffu, incl, 31);
+        if (nth >= count) {
+            nth -= count;
+            continue;
+        }
+        const int src = __popc(__ballot_sync(0xffffffffu, nth >= incl));
+        g = base + src;
+        const int32_t first = nth - (__shfl_sync(0xffffffffu, incl, src) - __shfl_sync(0xffffffffu, passes, src));
+        r0 = __shfl_sync(0xffffffffu, l, src) + first * xt;
+        nx = min(xt, __shfl_sync(0xffffffffu, h, src) - r0);
+        return true;
+    }
+    return false;
+}
+
+// All passes over the groups' rows.  Whole warps.
+__device__ __forceinline__ int32_t count_passes(const W4Args &a, int32_t xt)
+{
+    if (!a.offsets) return (a.S + xt - 1) / xt;
+    int32_t sum = 0;
+    for (int32_t e = static_cast<int32_t>(threadIdx.x & 31); e < a.groups; e += 32) {
+        const int32_t l = max(0, min(__ldg(a.offsets + e), a.S));
+        const int32_t h = max(l, min(__ldg(a.offsets + e + 1), a.S));
+        sum += (h - l + xt - 1) / xt;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    return sum;
+}
+
+template <bool E2M1, int RUN, bool ZEROS>
+__global__ void __launch_bounds__(W4S_WARPS * 32, 1)
+    w4_stream_kernel(const __grid_constant__ CUtensorMap tmW, const W4Args a, const W4Stream p)
+{
+    constexpr int SB = E2M1 ? 1 : 2;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[W4S_WARPS * W4S_STAGES];
+    __shared__ int32_t aborted;
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t base = ptx::smem_addr(smem);
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const int lg = lane >> 2, lc = lane & 3;
+    const uint32_t magic = in_register(E2M1 ? 0x7E807E80u : 0x43004300u), eight = in_register(0x43084308u);
+    const int team = warp / p.wk, part_k = warp % p.wk;
+    const int teams = p.warps / p.wk;
+    const int tile_rows = teams * W4S_ROWS;
+    const uint32_t ring = base + static_cast<uint32_t>(warp * p.stages * W4S_BOX);
+    const uint32_t bar0 = ptx::smem_addr(bars + warp * W4S_STAGES);
+    if (lane == 0) {
+        for (int s = 0; s < p.stages; ++s) ptx::mbar_init(bar0 + 8u * s, 1);
+        ptx::fence_barrier_init();
+    }
+    if (threadIdx.x == 0) {
+        aborted = 0;
+        ptx::prefetch_tensormap(&tmW);
+    }
+    __syncthreads();
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    auto clear = [&]() {  // this CTA's share of the rows of no group
+        for (int32_t n = static_cast<int32_t>(blockIdx.x) * 256; n < a.N; n += static_cast<int32_t>(gridDim.x) * 256)
+            zero_rows(a, n, min(n + 256, a.N));
+    };
+    const int64_t tiles = static_cast<int64_t>(count_passes(a, p.xt)) * p.tiles_n;
+    const int64_t first = blockIdx.x * tiles / gridDim.x, last = (blockIdx.x + 1) * tiles / gridDim.x;
+    if (first == last) {
+        clear();
+        return;
+    }
+    // A tile by its pass and its place in it, stepped without a division.
+    struct At {
+        int64_t t;
+        int32_t pass, n;
+    };
+    const int32_t pass0 = static_cast<int32_t>(first / p.tiles_n), place0 = static_cast<int32_t>(first % p.tiles_n);
+    auto step_tile = [&](At &at) {
+        ++at.t;
+        if (++at.n == p.tiles_n) {
+            at.n = 0;
+            ++at.pass;
+        }
+    };
+    // this warp's steps of a tile: part_k, part_k + wk, ...
+    const int32_t mine = p.steps > part_k ? (p.steps - part_k + p.wk - 1) / p.wk : 0;
+
+    // ---- producer: the next box to ask for
+    At pat{first, pass0, place0};
+    int32_t ps = 0, pg = 0, pg_pass = -1, pslot = 0;
+    uint32_t asked = 0;
+    auto ask = [&]() {  // one box, if any is left (warp-uniform)
+        if (pat.t >= last) return;
+        if (pat.pass != pg_pass) {
+            int32_t r, n;
+            nth_pass(a, p.xt, pat.pass, pg, r, n);
+            pg_pass = pat.pass;
+        }
+        if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(bar0 + 8u * pslot, W4S_BOX);
+            ptx::tma_load_3d(ring + pslot * W4S_BOX, &tmW, bar0 + 8u * pslot, (part_k + ps * p.wk) * (W4_STEP / 2),
+                             pat.n * tile_rows + team * W4S_ROWS, pg);
+        }
+        ++asked;
+        if (++pslot == p.stages) pslot = 0;
+        if (++ps == mine) {
+            ps = 0;
+            step_tile(pat);
+        }
+    };
+    for (int s = 0; s < p.stages; ++s) ask();
+
+    // ---- scales and zeros of a tile -> buffer b
+    auto stage_scales = [&](int32_t n0, int32_t g, int b) {
+        const int32_t rows = min(tile_rows, a.N - n0);
+        auto copy = [&](const uint8_t *src0, int64_t pitch, int32_t bytes, const uint8_t *any, int32_t words, uint32_t dst) {
+            for (int32_t r = warp; r < rows; r += p.warps) {
+                const uint8_t *row = src0 + r * pitch;
+                const int32_t off = static_cast<int32_t>(reinterpret_cast<uintptr_t>(row) & 3u);
+                for (int32_t w = lane; w < words; w += 32) {
+                    const int32_t left = bytes + off - w * 4;
+                    cp_async4(dst + (r * words + w) * 4, left > 0 ? row - off + w * 4 : any, max(0, min(4, left)));
+                }
+            }
+        };
+        copy(a.scales + (g * a.stride_s + n0 * a.lds) * SB, a.lds * SB, a.runs * SB, a.scales, p.s_words,
+             base + p.off_s + b * tile_rows * p.s_words * 4);
+        if constexpr (ZEROS)
+            copy(a.zeros + g * a.stride_z + n0 * a.ldz, a.ldz, a.runs, a.zeros, p.z_words,
+                 base + p.off_z + b * tile_rows * p.z_words * 4);
+    };
+    // ---- activations of a pass: eight of them become (0,4) (1,5) (2,6) (3,7)
+    auto stage_x = [&](int32_t r0, int32_t nx) {
+        const int32_t chunks = p.steps * (W4_STEP / 8);
+        const bool aligned = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(2 * a.ldx)) & 15u) == 0;
+        for (int32_t t = 0; t < nx; ++t) {
+            const uint16_t *row = a.x + (r0 + t) * a.ldx;
+            for (int32_t c = static_cast<int32_t>(threadIdx.x); c < chunks; c += static_cast<int32_t>(blockDim.x)) {
+                uint4 v;
+                if (aligned && c * 8 + 8 <= a.K) {
+                    v = *reinterpret_cast<const uint4 *>(row + c * 8);
+                } else {
+                    uint32_t h[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[i] = c * 8 + i < a.K ? row[c * 8 + i] : 0u;
+                    v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+                }
+                *reinterpret_cast<uint4 *>(smem + p.off_x + t * p.x_pitch + c * 16) =
+                    make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                               __byte_perm(v.y, v.w, 0x7632));
+            }
+        }
+    };
+
+    At at{first, pass0, place0};
+    int32_t g, r0, nx;              // the tile's pass
+    int32_t g_next, r0_next, nx_next;  // the pass of the tile behind it
+    nth_pass(a, p.xt, pass0, g_next, r0_next, nx_next);
+    stage_scales(place0 * tile_rows, g_next, 0);
+    uint32_t got = 0;               // boxes read
+    uint32_t slot = 0, parity = 0;  // of the next one
+    bool fresh = true;  // the tile's activations are not in shared memory yet
+    for (int b = 0; at.t < last; b ^= 1) {
+        if (fresh) {  // every warp is past its last use of the old ones: the barrier below
+            g = g_next;
+            r0 = r0_next;
+            nx = nx_next;
+            stage_x(r0, nx);
+            cp_async_commit();
+            cp_async_wait<0>();
+            __syncthreads();
+        }
+        const int32_t n0 = at.n * tile_rows;
+        step_tile(at);  // from here on the tile behind this one
+        fresh = at.n == 0;
+        if (at.t < last) {
+            if (fresh) nth_pass(a, p.xt, at.pass, g_next, r0_next, nx_next);
+            stage_scales(at.n * tile_rows, fresh ? g_next : g, b ^ 1);
+        }
+        cp_async_commit();
+        float acc[4] = {};
+        // scale bytes of rows lg and lg + 8 of this team's 16
+        const uint8_t *s_row[2], *z_row[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int32_t r = team * W4S_ROWS + lg + 8 * h;
+            const uintptr_t src = reinterpret_cast<uintptr_t>(a.scales) + static_cast<uintptr_t>((g * a.stride_s + (n0 + r) * a.lds) * SB);
+            s_row[h] = smem + p.off_s + (b * tile_rows + r) * p.s_words * 4 + static_cast<uint32_t>(src & 3u);
+            if constexpr (ZEROS) {
+                const uintptr_t zsrc = reinterpret_cast<uintptr_t>(a.zeros) + static_cast<uintptr_t>(g * a.stride_z + (n0 + r) * a.ldz);
+                z_row[h] = smem + p.off_z + (b * tile_rows + r) * p.z_words * 4 + static_cast<uint32_t>(zsrc & 3u);
+            }
+        }
+        // (an operand column of no row repeats row 0's: its sums are not stored)
+        const uint8_t *x_lane = smem + p.off_x + (lg < nx ? lg : 0) * p.x_pitch + lc * 16;
+        for (int32_t i = 0; i < mine; ++i, ++got) {
+            if (!ptx::mbar_try_wait(bar0 + 8u * slot, parity)) {
+                const uint64_t t0 = ptx::global_timer_ns();
+                while (!ptx::mbar_try_wait(bar0 + 8u * slot, parity)) {
+                    if (*reinterpret_cast<volatile int32_t *>(&aborted)) break;
+                    if (ptx::global_timer_ns() - t0 > p.timeout_ns) {
+                        atomicCAS(p.err, 0u, static_cast<uint32_t>(ERR_TIMEOUT_PRODUCER));
+                        *reinterpret_cast<volatile int32_t *>(&aborted) = 1;
+                        break;
+                    }
+                }
+            }
+            __syncwarp();
+            const int32_t step = part_k + i * p.wk;
+            const int32_t k0 = step * W4_STEP;
+            const uint32_t w_lane = (ring - base + slot * W4S_BOX + lg * 128 + lc * 4) ^ static_cast<uint32_t>(lg << 4);
+            const uint8_t *x_step = x_lane + step * (2 * W4_STEP);
+            const int32_t run0 = k0 / RUN;
+#pragma unroll
+            for (int j = 0; j < W4_STEP / RUN; ++j) {
+                if (j > 0 && k0 + j * RUN >= a.K) break;
+                float part[4];
+                uint32_t zz[2] = {eight, eight};
+                if constexpr (ZEROS) {
+                    zz[0] = (0x4300u | (lds_u8(z_row[0] + run0 + j) & 15u)) * 0x00010001u;
+                    zz[1] = (0x4300u | (lds_u8(z_row[1] + run0 + j) & 15u)) * 0x00010001u;
+                }
+#pragma unroll
+                for (int q = 0; q < RUN / 32; ++q) {
+                    const int blk = j * (RUN / 32) + q;
+                    const uint4 xv = lds128(x_step + blk * 64);
+                    uint32_t u[4], v[4];
+                    const uint8_t *wa = smem + (w_lane ^ static_cast<uint32_t>(blk << 4));
+                    decode<E2M1>(lds32(wa), magic, zz[0], u);
+                    decode<E2M1>(lds32(wa + 1024), magic, zz[1], v);
+                    const uint32_t a0[4] = {u[0], v[0], u[1], v[1]}, a1[4] = {u[2], v[2], u[3], v[3]};
+                    mma_16816(part, a0, xv.x, xv.y, q == 0);
+                    mma_16816(part, a1, xv.z, xv.w, false);
+                }
+                float sa, sb;
+                if constexpr (E2M1) {
+                    sa = e8m0_value(lds_u8(s_row[0] + run0 + j));
+                    sb = e8m0_value(lds_u8(s_row[1] + run0 + j));
+                } else {
+                    sa = bf16_value(static_cast<uint16_t>(lds_u16(s_row[0] + 2 * (run0 + j))));
+                    sb = bf16_value(static_cast<uint16_t>(lds_u16(s_row[1] + 2 * (run0 + j))));
+                }
+                acc[0] = fmaf(sa, part[0], acc[0]);
+                acc[1] = fmaf(sa, part[1], acc[1]);
+                acc[2] = fmaf(sb, part[2], acc[2]);
+                acc[3] = fmaf(sb, part[3], acc[3]);
+            }
+            if (++slot == static_cast<uint32_t>(p.stages)) {
+                slot = 0;
+                parity ^= 1u;
+            }
+            __syncwarp();  // every lane has read the box: the slot may be filled again
+            ask();
+        }
+        // sums[buffer][warp][x row][weight row], added over a team's warps in order
+        float *sums = reinterpret_cast<float *>(smem + p.off_sum) + b * p.warps * 8 * W4S_ROWS;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[(warp * 8 + 2 * lc + (i & 1)) * W4S_ROWS + lg + 8 * (i >> 1)] = acc[i];
+        cp_async_wait<0>();
+        __syncthreads();  // the sums, and the next tile's scales
+        if (aborted) {
+            // the boxes still on their way land (or the limit runs out) before the CTA leaves
+            const uint64_t t0 = ptx::global_timer_ns();
+            for (; got < asked; ++got) {
+                while (!ptx::mbar_try_wait(bar0 + 8u * slot, parity))
+                    if (ptx::global_timer_ns() - t0 > p.timeout_ns) return;
+                if (++slot == static_cast<uint32_t>(p.stages)) {
+                    slot = 0;
+                    parity ^= 1u;
+                }
+            }
+            return;
+        }
+        // warp: 16 weight rows of a team x two activation rows a turn
+        for (int32_t i = warp; i < teams * 4; i += p.warps) {
+            const int32_t tm = i >> 2, tok = (i & 3) * 2 + (lane >> 4), n = tm * W4S_ROWS + (lane & 15);
+            if (tok >= nx || n0 + n >= a.N) continue;
+            const float *src = sums + (tm * p.wk * 8 + tok) * W4S_ROWS + (lane & 15);
+            float sum = 0.0f;
+#pragma unroll 4
+            for (int v = 0; v < p.wk; ++v) sum += src[v * 8 * W4S_ROWS];
+            store_y(a, r0 + tok, n0 + n, sum);
+        }
+    }
+    clear();
 }
 
 template <class... P, class... A>
@@ -501,6 +853,76 @@ cudaError_t launch_w4(const W4Args &a, bool e2m1, int64_t used, int xt, int dev,
     if (a.run == 32) return launch_tile<false, 32, false, VEC>(a, used, xt, dev, s);
     if (a.run == 64) return launch_tile<false, 64, false, VEC>(a, used, xt, dev, s);
     return launch_tile<false, 128, false, VEC>(a, used, xt, dev, s);
+}
+
+int w4_env(const char *k, int d) { const char *v = std::getenv(k); return v ? std::atoi(v) : d; }
+// The stream kernel's plan; false where its activations do not fit.
+bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &p, int &grid, size_t &smem)
+{
+    p.xt = 1;
+    while (p.xt < 8 && p.xt < a.S) p.xt *= 2;
+    p.steps = (a.K + W4_STEP - 1) / W4_STEP;
+    p.warps = W4S_WARPS;
+    p.wk = 1;
+    auto tiles = [&]() {
+        const int64_t rows = static_cast<int64_t>(p.warps / p.wk) * W4S_ROWS;
+        p.tiles_n = static_cast<int32_t>((a.N + rows - 1) / rows);
+        return p.tiles_n * used;
+    };
+    // Teams share K while a warp keeps four steps of a tile (a tile's end
+    // costs a warp about a step's time) and the tiles are fewer than six an
+    // SM, or fewer than two an SM and the warp keeps one step; then CTAs of
+    // fewer warps where the tiles do not fill the SMs.
+    while (p.wk < p.warps && 2 * p.wk <= p.steps && tiles() < (8 * p.wk <= p.steps ? w4_env("W4A", 6) : w4_env("W4B", 2)) * sms) p.wk *= 2;
+    if (w4_env("W4WK", 0)) p.wk = w4_env("W4WK", 0);
+    while (p.warps > p.wk && p.warps > 2 && tiles() < sms) p.warps /= 2;
+    const int64_t n = tiles();
+    grid = static_cast<int>(n < sms ? n : sms);
+    const int sb = e2m1 ? 1 : 2;
+    const int tile_rows = p.warps / p.wk * W4S_ROWS;
+    p.x_pitch = p.steps * W4_STEP * 2 + 64;
+    p.s_words = (a.runs * sb + 3) / 4 + 1;
+    p.z_words = a.zeros ? (a.runs + 3) / 4 + 1 : 0;
+    const int64_t fixed = static_cast<int64_t>(p.xt) * p.x_pitch + 2 * static_cast<int64_t>(tile_rows) * (p.s_words + p.z_words) * 4 +
+                          2 * p.warps * 8 * W4S_ROWS * 4;
+    const int64_t room = SMEM_LIMIT - 2048 - fixed;  // 1 KB of alignment, the static barriers
+    p.stages = static_cast<int32_t>(room / (p.warps * W4S_BOX));
+    if (room < 0 || p.stages < 2) return false;
+    if (p.stages > W4S_STAGES) p.stages = W4S_STAGES;
+    p.off_x = p.warps * p.stages * W4S_BOX;
+    p.off_s = p.off_x + p.xt * p.x_pitch;
+    p.off_z = p.off_s + 2 * tile_rows * p.s_words * 4;
+    p.off_sum = p.off_z + 2 * tile_rows * p.z_words * 4;
+    smem = static_cast<size_t>(p.off_sum + 2 * p.warps * 8 * W4S_ROWS * 4 + 1024);
+    return true;
+}
+
+template <bool E2M1, int RUN, bool ZEROS>
+cudaError_t launch_stream(const CUtensorMap &tm, const W4Args &a, const W4Stream &p, int grid, size_t smem, int dev, cudaStream_t s)
+{
+    auto kern = w4_stream_kernel<E2M1, RUN, ZEROS>;
+    static std::atomic<unsigned long long> configured{0};
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT - 1024);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    return launch(kern, dim3(static_cast<unsigned>(grid)), p.warps * 32, smem, s, tm, a, p);
+}
+
+cudaError_t launch_stream_of(bool e2m1, const CUtensorMap &tm, const W4Args &a, const W4Stream &p, int grid, size_t smem, int dev,
+                             cudaStream_t s)
+{
+    if (e2m1) return launch_stream<true, 32, false>(tm, a, p, grid, smem, dev, s);
+    if (a.zeros) {
+        if (a.run == 32) return launch_stream<false, 32, true>(tm, a, p, grid, smem, dev, s);
+        if (a.run == 64) return launch_stream<false, 64, true>(tm, a, p, grid, smem, dev, s);
+        return launch_stream<false, 128, true>(tm, a, p, grid, smem, dev, s);
+    }
+    if (a.run == 32) return launch_stream<false, 32, false>(tm, a, p, grid, smem, dev, s);
+    if (a.run == 64) return launch_stream<false, 64, false>(tm, a, p, grid, smem, dev, s);
+    return launch_stream<false, 128, false>(tm, a, p, grid, smem, dev, s);
 }
 
 constexpr int64_t LIMIT = INT32_MAX - 1024;
@@ -583,13 +1005,36 @@ TG_API tg_status tg_gemv_w4(const void *x, int64_t ldx, const void *W, int64_t l
                      static_cast<uintptr_t>(a.ldw) | static_cast<uintptr_t>(a.stride_w)) % n) == 0 &&
                    (reinterpret_cast<uintptr_t>(scales) | reinterpret_cast<uintptr_t>(zeros)) % 4 == 0;
         };
+        const bool e2m1 = format == TG_W4_E2M1;
+        // Weights that TMA can address (16-byte rows; the activations may
+        // have any alignment).
+        if (K > 0 && (reinterpret_cast<uintptr_t>(W) | static_cast<uintptr_t>(a.ldw) | static_cast<uintptr_t>(a.stride_w)) % 16 == 0 &&
+            (reinterpret_cast<uintptr_t>(scales) | reinterpret_cast<uintptr_t>(zeros)) % 4 == 0) {
+            std::lock_guard<std::mutex> lock(host_mutex());
+            HostStream hs;
+            const tg_status st = host_stream(s, &hs);
+            if (st != TG_OK) return st;
+            W4Stream p{};
+            int grid = 0;
+            size_t smem = 0;
+            CUtensorMap tm;
+            const uint64_t s2 = static_cast<uint64_t>(groups > 1 && a.stride_w > 0 ? a.stride_w : (N * a.ldw + 15) / 16 * 16);
+            const bool shared_w = groups > 1 && a.stride_w == 0;
+            if (!shared_w && plan_stream(a, e2m1, used, hs.sms, p, grid, smem) &&
+                host_encode_3d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, static_cast<uint64_t>(K / 2), static_cast<uint64_t>(N),
+                               static_cast<uint64_t>(groups), static_cast<uint64_t>(a.ldw), s2, W4_STEP / 2, W4S_ROWS,
+                               CU_TENSOR_MAP_SWIZZLE_128B)) {
+                p.err = hs.err;
+                p.timeout_ns = HOST_TIMEOUT_NS;
+                return host_cuda_status(launch_stream_of(e2m1, tm, a, p, grid, smem, hs.dev, s));
+            }
+        }
         if (K > 0 && aligned(4)) {
             int dev = 0;
             const cudaError_t e = cudaGetDevice(&dev);
             if (e != cudaSuccess) return host_cuda_status(e);
             int xt = 1;  // activation rows a pass: no more than there are
             while (xt < 8 && xt < S) xt *= 2;
-            const bool e2m1 = format == TG_W4_E2M1;
             return host_cuda_status(aligned(16) ? launch_w4<16>(a, e2m1, used, xt, dev, s) : launch_w4<4>(a, e2m1, used, xt, dev, s));
         }
         const dim3 grid(static_cast<unsigned>((N + ANY_COLS - 1) / ANY_COLS), static_cast<unsigned>(used));
