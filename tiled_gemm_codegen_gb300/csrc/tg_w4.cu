@@ -5,10 +5,13 @@
 // The weights are the traffic (half a byte each, read once), so the bound is
 // HBM; at that rate an SM has to turn about 47 codes a clock into products.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
 #include <cstdlib>
+#include <cstdio>
 #include <cstdint>
 
 #include "tg_gemm.h"
@@ -87,6 +90,22 @@ __device__ __forceinline__ float e2m1_value(uint32_t q)
     return (q & 8u) ? -v : v;
 }
 
+// The two weights of a byte of codes; s and z: where its scale and zero lie.
+template <bool E2M1>
+__device__ __forceinline__ void byte_values(const W4Args &a, uint32_t q, int64_t s, int64_t z, float &v0, float &v1)
+{
+    if constexpr (E2M1) {
+        const float f = e8m0_value(a.scales[s]);
+        v0 = e2m1_value(q & 15u) * f;
+        v1 = e2m1_value(q >> 4) * f;
+    } else {
+        const float f = bf16_value(reinterpret_cast<const uint16_t *>(a.scales)[s]);
+        const float zero = a.zeros ? static_cast<float>(a.zeros[z] & 15u) : 8.0f;
+        v0 = (static_cast<float>(q & 15u) - zero) * f;
+        v1 = (static_cast<float>(q >> 4) - zero) * f;
+    }
+}
+
 __device__ __forceinline__ void store_y(const W4Args &a, int64_t row, int64_t n, float v)
 {
     if (a.y_bf16)
@@ -130,18 +149,8 @@ __global__ void __launch_bounds__(ANY_COLS * 32) w4_any_kernel(const W4Args a)
         float acc[4] = {};
         for (int32_t b = lane; b < a.K / 2; b += 32) {
             const uint32_t q = w[b];
-            const int32_t r = 2 * b / a.run;
             float v0, v1;
-            if constexpr (E2M1) {
-                const float s = e8m0_value(a.scales[s0 + r]);
-                v0 = e2m1_value(q & 15u) * s;
-                v1 = e2m1_value(q >> 4) * s;
-            } else {
-                const float s = bf16_value(reinterpret_cast<const uint16_t *>(a.scales)[s0 + r]);
-                const float z = a.zeros ? static_cast<float>(a.zeros[z0 + r] & 15u) : 8.0f;
-                v0 = (static_cast<float>(q & 15u) - z) * s;
-                v1 = (static_cast<float>(q >> 4) - z) * s;
-            }
+            byte_values<E2M1>(a, q, s0 + 2 * b / a.run, z0 + 2 * b / a.run, v0, v1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (r0 + i < hi) {
@@ -275,6 +284,39 @@ __device__ __forceinline__ void decode(uint32_t w, uint32_t magic, uint32_t zz, 
 }
 
 __host__ __device__ constexpr int w4_warps(int xt) { return xt > 4 ? W4_WARPS / 2 : W4_WARPS; }
+
+// Nibbles (i, i + 4) of a word as two fp16, i = 0 .. 3: int4 as code * 2^-24
+// (odd i: * 2^-20), E2M1 as value * 2^-14.
+template <bool E2M1>
+__device__ __forceinline__ void decode_half(uint32_t w, uint32_t (&p)[4])
+{
+    if constexpr (E2M1) {
+        p[0] = masked_or<0x0E000E00u>(w << 9, (w << 12) & 0x80008000u);
+        p[1] = masked_or<0x0E000E00u>(w << 5, (w << 8) & 0x80008000u);
+        p[2] = masked_or<0x0E000E00u>(w << 1, (w << 4) & 0x80008000u);
+        p[3] = masked_or<0x0E000E00u>(w >> 3, w & 0x80008000u);
+    } else {
+        const uint32_t v = w >> 8;
+        p[0] = w & 0x000F000Fu;
+        p[1] = w & 0x00F000F0u;
+        p[2] = v & 0x000F000Fu;
+        p[3] = v & 0x00F000F0u;
+    }
+}
+constexpr float W4_UNIT_INT4 = 0x1p-24f, W4_UNIT_E2M1 = 0x1p-14f;
+
+// d (+)= a b in fp16 with fp32 sums.
+__device__ __forceinline__ void mma_16816_half(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool first)
+{
+    if (first)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
 // Staged scale words of a row and step: its bytes from the 4-byte boundary
 // before them.
@@ -466,13 +508,29 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
 
 // ------------------------------------------------------------ stream kernel
 // The same product for weights that TMA can address and activations that fit
-// shared memory whole.  One CTA per SM walks a contiguous range of tiles (16
+// shared memory whole.  One CTA per SM walks a contiguous range of tiles (32
 // weight rows for each of its teams of `wk` warps, which share K step by
-// step); each warp keeps `stages` TMA boxes of 16 rows x 256 codes in flight
+// step); each warp keeps `stages` TMA boxes of 32 rows x 256 codes in flight
 // across the ends of its tiles, so the weights never stop.  What a tile needs
-// besides is loaded once or ahead: the activations of a group in the order the
-// products want them (their pairs made once instead of at every use), the
-// scales of the next tile by cp.async during this one.
+// besides is loaded once or ahead: the activations of a group in the order and
+// type the products want, the scales of the next tile by cp.async during this
+// one.
+//
+// What bounds it is taking the codes apart, so both operands are fp16 here,
+// where that takes least: a masked code is an fp16 subnormal as it lies, q
+// 2^-24 in the low four bits of a half and 16 q 2^-24 in the next four (the
+// activations that meet those are divided by 16), so eight codes cost four
+// masks and one shift, and the tensor cores take subnormals as they are.  Zero
+// points leave the product: sum (q - z) x = sum q x - z sum x, with the sums
+// of a group's activations made once.  An E2M1 code's three low bits on fp16's
+// exponent and mantissa are its value times 2^-14.
+//
+// Activations become fp16 by a power of two for each row, which brings its
+// largest finite magnitude to [2^11, 2^12); the sums are multiplied back.  A
+// value of bf16's eight bits loses some only below 2^-17 (2^-13 where it is
+// divided by 16) of its row's largest, by 2^-25 of that at most: less than
+// the rounding of the fp32 sum.  A row with an infinity or NaN, for which the
+// difference of two sums is not the sum, is computed value by value instead.
 //
 // A box lies in shared memory with the 128-byte swizzle (16-byte unit u of
 // row r at u ^ (r mod 8)), which puts the words of a block's eight rows in 32
@@ -485,15 +543,16 @@ struct W4Stream {
     int32_t tiles_n;   // tiles of a group
     int32_t x_pitch;   // bytes of an activation row in shared memory
     int32_t s_words, z_words;  // staged words of a row's scales and zeros
-    int32_t off_x, off_s, off_z, off_sum;  // bytes in shared memory after the rings
+    int32_t off_x, off_xs, off_s, off_z, off_sum;  // bytes in shared memory after the rings
+    int32_t s_vec;             // every row of scales starts on 4 bytes
     uint32_t *err;
     uint64_t timeout_ns;
 };
 
-constexpr int W4S_ROWS = 16;
-constexpr int W4S_BOX = W4S_ROWS * W4_STEP / 2;  // 2 KB
+constexpr int W4S_ROWS = 32;
+constexpr int W4S_BOX = W4S_ROWS * W4_STEP / 2;  // 4 KB
 constexpr int W4S_WARPS = 16;
-constexpr int W4S_STAGES = 6;
+constexpr int W4S_STAGES = 4;
 
 // Pass `nth` over the groups' rows, at most xt rows each: its group, first
 // row and number of rows; false past the last.  Whole warps.
@@ -550,21 +609,53 @@ __device__ __forceinline__ int32_t count_passes(const W4Args &a, int32_t xt)
     return sum;
 }
 
+// The power of two (or its inverse) that brings a row's largest finite
+// magnitude, given as bf16 bits, to [2^11, 2^12); at most 2^126.
+__device__ __forceinline__ float x_scale(int32_t most, bool inverse)
+{
+    const int32_t up = min(138 - (most >> 7), 126);
+    return __uint_as_float(static_cast<uint32_t>(127 + (inverse ? -up : up)) << 23);
+}
+
+// Whole warp: <x[row], w_g[n]> value by value, for any values.
+template <bool E2M1>
+__device__ __forceinline__ float row_dot(const W4Args &a, int32_t g, int32_t n, int32_t row)
+{
+    const uint8_t *w = a.w + g * a.stride_w + n * a.ldw;
+    const int64_t s0 = g * a.stride_s + n * a.lds, z0 = g * a.stride_z + n * a.ldz;
+    const uint16_t *x = a.x + row * a.ldx;
+    float acc = 0.0f;
+    for (int32_t b = static_cast<int32_t>(threadIdx.x & 31); b < a.K / 2; b += 32) {
+        const uint32_t q = w[b];
+        float v0, v1;
+        byte_values<E2M1>(a, q, s0 + 2 * b / a.run, z0 + 2 * b / a.run, v0, v1);
+        acc = fmaf(v0, bf16_value(x[2 * b]), acc);
+        acc = fmaf(v1, bf16_value(x[2 * b + 1]), acc);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
+    return acc;
+}
+
 template <bool E2M1, int RUN, bool ZEROS>
 __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
     w4_stream_kernel(const __grid_constant__ CUtensorMap tmW, const W4Args a, const W4Stream p)
 {
     constexpr int SB = E2M1 ? 1 : 2;
+    constexpr int RUNS = W4_STEP / RUN;        // of a step
+    constexpr int SW = (RUNS * 2 + 3) / 4;     // registers of a step's scales of a row, bf16
+    constexpr int SBYTES = RUNS * SB;          // as staged
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[W4S_WARPS * W4S_STAGES];
     __shared__ int32_t aborted;
+    __shared__ int32_t x_max[8];  // largest finite magnitude of a row, bf16 bits
+    __shared__ int32_t x_odd[8];  // the row holds an infinity or NaN
     const uint32_t raw = ptx::smem_addr(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_addr(smem);
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = static_cast<int>(threadIdx.x & 31);
     const int lg = lane >> 2, lc = lane & 3;
-    const uint32_t magic = in_register(E2M1 ? 0x7E807E80u : 0x43004300u), eight = in_register(0x43084308u);
     const int team = warp / p.wk, part_k = warp % p.wk;
     const int teams = p.warps / p.wk;
     const int tile_rows = teams * W4S_ROWS;
@@ -594,97 +685,171 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
     }
     // A tile by its pass and its place in it, stepped without a division.
     struct At {
-        int64_t t;
-        int32_t pass, n;
-    };
-    const int32_t pass0 = static_cast<int32_t>(first / p.tiles_n), place0 = static_cast<int32_t>(first % p.tiles_n);
-    auto step_tile = [&](At &at) {
-        ++at.t;
-        if (++at.n == p.tiles_n) {
-            at.n = 0;
-            ++at.pass;
+        int32_t left, pass, n;
+        __device__ __forceinline__ void next(int32_t tiles_n)
+        {
+            --left;
+            if (++n == tiles_n) {
+                n = 0;
+                ++pass;
+            }
         }
     };
-    // this warp's steps of a tile: part_k, part_k + wk, ...
-    const int32_t mine = p.steps > part_k ? (p.steps - part_k + p.wk - 1) / p.wk : 0;
+    const At at0{static_cast<int32_t>(last - first), static_cast<int32_t>(first / p.tiles_n), static_cast<int32_t>(first % p.tiles_n)};
+    // this warp's steps of a tile: part_k, part_k + wk, ... (wk <= steps)
+    const int32_t mine = (p.steps - part_k + p.wk - 1) / p.wk;
+
+    int32_t g_next, r0_next, nx_next;  // the pass of the next tile
+    nth_pass(a, p.xt, at0.pass, g_next, r0_next, nx_next);
 
     // ---- producer: the next box to ask for
-    At pat{first, pass0, place0};
-    int32_t ps = 0, pg = 0, pg_pass = -1, pslot = 0;
+    At pat = at0;
+    int32_t pk = part_k * (W4_STEP / 2), pn = pat.n * tile_rows + team * W4S_ROWS, pg = g_next;  // its coordinates
+    int32_t p_left = mine, pslot = 0;
     uint32_t asked = 0;
     auto ask = [&]() {  // one box, if any is left (warp-uniform)
-        if (pat.t >= last) return;
-        if (pat.pass != pg_pass) {
-            int32_t r, n;
-            nth_pass(a, p.xt, pat.pass, pg, r, n);
-            pg_pass = pat.pass;
-        }
+        if (p_left == 0) return;
         if (lane == 0) {
             ptx::mbar_arrive_expect_tx(bar0 + 8u * pslot, W4S_BOX);
-            ptx::tma_load_3d(ring + pslot * W4S_BOX, &tmW, bar0 + 8u * pslot, (part_k + ps * p.wk) * (W4_STEP / 2),
-                             pat.n * tile_rows + team * W4S_ROWS, pg);
+            ptx::tma_load_3d(ring + pslot * W4S_BOX, &tmW, bar0 + 8u * pslot, pk, pn, pg);
         }
         ++asked;
         if (++pslot == p.stages) pslot = 0;
-        if (++ps == mine) {
-            ps = 0;
-            step_tile(pat);
+        pk += p.wk * (W4_STEP / 2);
+        if (--p_left == 0) {  // the next tile's first
+            const int32_t pass = pat.pass;
+            pat.next(p.tiles_n);
+            if (pat.left == 0) return;
+            if (pat.pass != pass) {
+                int32_t r, n;
+                nth_pass(a, p.xt, pat.pass, pg, r, n);
+            }
+            p_left = mine;
+            pk = part_k * (W4_STEP / 2);
+            pn = pat.n * tile_rows + team * W4S_ROWS;
         }
     };
     for (int s = 0; s < p.stages; ++s) ask();
 
-    // ---- scales and zeros of a tile -> buffer b
+    // ---- scales and zeros of a tile -> buffer b; a thread's first word and
+    // its step to the next are the same for every tile
+    const int32_t s_used = (a.runs * SB + 3) / 4 + (p.s_vec ? 0 : 1), z_used = ZEROS ? (a.runs + 3) / 4 + 1 : 1;
+    const int32_t s_r = static_cast<int32_t>(threadIdx.x) / s_used, s_w = static_cast<int32_t>(threadIdx.x) - s_r * s_used;
+    const int32_t s_dr = static_cast<int32_t>(blockDim.x) / s_used, s_dw = static_cast<int32_t>(blockDim.x) - s_dr * s_used;
+    const int32_t z_r = static_cast<int32_t>(threadIdx.x) / z_used, z_w = static_cast<int32_t>(threadIdx.x) - z_r * z_used;
+    const int32_t z_dr = static_cast<int32_t>(blockDim.x) / z_used, z_dw = static_cast<int32_t>(blockDim.x) - z_dr * z_used;
     auto stage_scales = [&](int32_t n0, int32_t g, int b) {
         const int32_t rows = min(tile_rows, a.N - n0);
-        auto copy = [&](const uint8_t *src0, int64_t pitch, int32_t bytes, const uint8_t *any, int32_t words, uint32_t dst) {
-            for (int32_t r = warp; r < rows; r += p.warps) {
+        auto copy = [&](const uint8_t *src0, int64_t pitch, int32_t bytes, const uint8_t *any, int32_t used, int32_t words, uint32_t dst,
+                        int32_t r, int32_t w, int32_t dr, int32_t dw) {
+            while (r < rows) {
                 const uint8_t *row = src0 + r * pitch;
                 const int32_t off = static_cast<int32_t>(reinterpret_cast<uintptr_t>(row) & 3u);
-                for (int32_t w = lane; w < words; w += 32) {
-                    const int32_t left = bytes + off - w * 4;
-                    cp_async4(dst + (r * words + w) * 4, left > 0 ? row - off + w * 4 : any, max(0, min(4, left)));
+                const int32_t left = bytes + off - w * 4;
+                cp_async4(dst + (r * words + w) * 4, left > 0 ? row - off + w * 4 : any, max(0, min(4, left)));
+                r += dr;
+                w += dw;
+                if (w >= used) {
+                    w -= used;
+                    ++r;
                 }
             }
         };
-        copy(a.scales + (g * a.stride_s + n0 * a.lds) * SB, a.lds * SB, a.runs * SB, a.scales, p.s_words,
-             base + p.off_s + b * tile_rows * p.s_words * 4);
+        copy(a.scales + (g * a.stride_s + n0 * a.lds) * SB, a.lds * SB, a.runs * SB, a.scales, s_used, p.s_words,
+             base + p.off_s + b * tile_rows * p.s_words * 4, s_r, s_w, s_dr, s_dw);
         if constexpr (ZEROS)
-            copy(a.zeros + g * a.stride_z + n0 * a.ldz, a.ldz, a.runs, a.zeros, p.z_words,
-                 base + p.off_z + b * tile_rows * p.z_words * 4);
+            copy(a.zeros + g * a.stride_z + n0 * a.ldz, a.ldz, a.runs, a.zeros, z_used, p.z_words,
+                 base + p.off_z + b * tile_rows * p.z_words * 4, z_r, z_w, z_dr, z_dw);
     };
-    // ---- activations of a pass: eight of them become (0,4) (1,5) (2,6) (3,7)
+
+    // ---- activations of a pass, as fp16 times a power of two: eight
+    // consecutive ones paired as the codes of a word are; and their sums by
+    // group of codes, times the code's unit (and the zero point where it is 8)
     auto stage_x = [&](int32_t r0, int32_t nx) {
         const int32_t chunks = p.steps * (W4_STEP / 8);
+        const int32_t items = nx * chunks;  // 16-byte pieces, 32 a warp and turn: all of one row
         const bool aligned = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(2 * a.ldx)) & 15u) == 0;
-        for (int32_t t = 0; t < nx; ++t) {
-            const uint16_t *row = a.x + (r0 + t) * a.ldx;
-            for (int32_t c = static_cast<int32_t>(threadIdx.x); c < chunks; c += static_cast<int32_t>(blockDim.x)) {
-                uint4 v;
+        if (threadIdx.x < 8) x_max[threadIdx.x] = x_odd[threadIdx.x] = 0;
+        __syncthreads();
+        constexpr int U = 4;  // turns whose loads are in flight together
+        for (int32_t i0 = static_cast<int32_t>(threadIdx.x); i0 < items; i0 += U * static_cast<int32_t>(blockDim.x)) {
+            uint4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int32_t i = i0 + u * static_cast<int32_t>(blockDim.x);
+                v[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (i >= items) continue;
+                const int32_t t = i / chunks, c = i - t * chunks;
+                const uint16_t *row = a.x + (r0 + t) * a.ldx + c * 8;
                 if (aligned && c * 8 + 8 <= a.K) {
-                    v = *reinterpret_cast<const uint4 *>(row + c * 8);
-                } else {
+                    v[u] = *reinterpret_cast<const uint4 *>(row);
+                } else if (c * 8 < a.K) {
                     uint32_t h[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) h[i] = c * 8 + i < a.K ? row[c * 8 + i] : 0u;
-                    v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+                    for (int e = 0; e < 8; ++e) h[e] = c * 8 + e < a.K ? row[e] : 0u;
+                    v[u] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
                 }
-                *reinterpret_cast<uint4 *>(smem + p.off_x + t * p.x_pitch + c * 16) =
-                    make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                               __byte_perm(v.y, v.w, 0x7632));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int32_t i = i0 + u * static_cast<int32_t>(blockDim.x);
+                if (i >= items) break;  // warp-uniform: items and the block are multiples of 32
+                const int32_t t = i / chunks, c = i - t * chunks;
+                const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                int32_t most = 0;
+                bool odd = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int32_t lo = static_cast<int32_t>(w[e] & 0x7fffu), hi = static_cast<int32_t>(w[e] >> 16 & 0x7fffu);
+                    odd |= lo >= 0x7f80 || hi >= 0x7f80;
+                    if (lo < 0x7f80) most = max(most, lo);
+                    if (hi < 0x7f80) most = max(most, hi);
+                }
+                *reinterpret_cast<uint4 *>(smem + p.off_x + t * p.x_pitch + c * 16) = v[u];
+                most = __reduce_max_sync(0xffffffffu, most);
+                if (lane == 0) atomicMax(&x_max[t], most);
+                if (odd) x_odd[t] = 1;
+            }
+        }
+        __syncthreads();
+        for (int32_t i = static_cast<int32_t>(threadIdx.x); i < items; i += static_cast<int32_t>(blockDim.x)) {
+            const int32_t t = i / chunks, c = i - t * chunks;
+            const float mul = x_scale(x_max[t], false);
+            uint4 *at = reinterpret_cast<uint4 *>(smem + p.off_x + t * p.x_pitch + c * 16);
+            const uint4 v = *at;  // this thread's own
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            float f[8], sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) * mul;
+                f[e] = __half2float(__float2half_rn(!E2M1 && (e & 1) ? x * 0.0625f : x));
+                sum += !E2M1 && (e & 1) ? f[e] * 16.0f : f[e];
+            }
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __half2 q = __floats2half2_rn(f[e], f[e + 4]);
+                h[e] = *reinterpret_cast<const uint32_t *>(&q);
+            }
+            *at = make_uint4(h[0], h[1], h[2], h[3]);
+            if constexpr (!E2M1) {
+#pragma unroll
+                for (int d = 1; d < RUN / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (lane % (RUN / 8) == 0)
+                    *reinterpret_cast<float *>(smem + p.off_xs + (c / (RUN / 8) * 8 + t) * 4) = sum * (ZEROS ? W4_UNIT_INT4 : 8.0f * W4_UNIT_INT4);
             }
         }
     };
 
-    At at{first, pass0, place0};
-    int32_t g, r0, nx;              // the tile's pass
-    int32_t g_next, r0_next, nx_next;  // the pass of the tile behind it
-    nth_pass(a, p.xt, pass0, g_next, r0_next, nx_next);
-    stage_scales(place0 * tile_rows, g_next, 0);
+    At at = at0;
+    int32_t g, r0, nx;  // the tile's pass
+    stage_scales(at.n * tile_rows, g_next, 0);
     uint32_t got = 0;               // boxes read
     uint32_t slot = 0, parity = 0;  // of the next one
     bool fresh = true;  // the tile's activations are not in shared memory yet
-    for (int b = 0; at.t < last; b ^= 1) {
-        if (fresh) {  // every warp is past its last use of the old ones: the barrier below
+    for (int b = 0; at.left > 0; b ^= 1) {
+        if (fresh) {
+            __syncthreads();  // every warp is done with the old ones
             g = g_next;
             r0 = r0_next;
             nx = nx_next;
@@ -694,18 +859,18 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
             __syncthreads();
         }
         const int32_t n0 = at.n * tile_rows;
-        step_tile(at);  // from here on the tile behind this one
+        at.next(p.tiles_n);  // from here on the tile behind this one
         fresh = at.n == 0;
-        if (at.t < last) {
+        if (at.left > 0) {
             if (fresh) nth_pass(a, p.xt, at.pass, g_next, r0_next, nx_next);
             stage_scales(at.n * tile_rows, fresh ? g_next : g, b ^ 1);
         }
         cp_async_commit();
-        float acc[4] = {};
-        // scale bytes of rows lg and lg + 8 of this team's 16
-        const uint8_t *s_row[2], *z_row[2];
+        float acc[2][4] = {};
+        // scale and zero bytes of this team's rows lg + 8 h
+        const uint8_t *s_row[4], *z_row[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 4; ++h) {
             const int32_t r = team * W4S_ROWS + lg + 8 * h;
             const uintptr_t src = reinterpret_cast<uintptr_t>(a.scales) + static_cast<uintptr_t>((g * a.stride_s + (n0 + r) * a.lds) * SB);
             s_row[h] = smem + p.off_s + (b * tile_rows + r) * p.s_words * 4 + static_cast<uint32_t>(src & 3u);
@@ -715,8 +880,11 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
             }
         }
         // (an operand column of no row repeats row 0's: its sums are not stored)
-        const uint8_t *x_lane = smem + p.off_x + (lg < nx ? lg : 0) * p.x_pitch + lc * 16;
-        for (int32_t i = 0; i < mine; ++i, ++got) {
+        const uint8_t *x_step = smem + p.off_x + (lg < nx ? lg : 0) * p.x_pitch + lc * 16 + part_k * (2 * W4_STEP);
+        const float2 *xs_step = reinterpret_cast<const float2 *>(smem + p.off_xs) + part_k * RUNS * 4 + lc;
+        int32_t k_left = a.K - part_k * W4_STEP;  // codes from the step's first
+        int32_t run0 = part_k * RUNS;
+        for (int32_t i = 0; i < mine; ++i) {
             if (!ptx::mbar_try_wait(bar0 + 8u * slot, parity)) {
                 const uint64_t t0 = ptx::global_timer_ns();
                 while (!ptx::mbar_try_wait(bar0 + 8u * slot, parity)) {
@@ -729,45 +897,89 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
                 }
             }
             __syncwarp();
-            const int32_t step = part_k + i * p.wk;
-            const int32_t k0 = step * W4_STEP;
             const uint32_t w_lane = (ring - base + slot * W4S_BOX + lg * 128 + lc * 4) ^ static_cast<uint32_t>(lg << 4);
-            const uint8_t *x_step = x_lane + step * (2 * W4_STEP);
-            const int32_t run0 = k0 / RUN;
+            // the step's scales, as bf16 pairs
+            uint32_t sc[4][SW];
 #pragma unroll
-            for (int j = 0; j < W4_STEP / RUN; ++j) {
-                if (j > 0 && k0 + j * RUN >= a.K) break;
-                float part[4];
-                uint32_t zz[2] = {eight, eight};
-                if constexpr (ZEROS) {
-                    zz[0] = (0x4300u | (lds_u8(z_row[0] + run0 + j) & 15u)) * 0x00010001u;
-                    zz[1] = (0x4300u | (lds_u8(z_row[1] + run0 + j) & 15u)) * 0x00010001u;
+            for (int h = 0; h < 4; ++h) {
+                const uint8_t *src = s_row[h] + run0 * SB;
+                uint32_t in[(SBYTES + 3) / 4];
+                if (p.s_vec) {
+                    if constexpr (SBYTES == 16) {
+                        const uint4 v = lds128(src);
+                        in[0] = v.x, in[1] = v.y, in[2] = v.z, in[3] = v.w;
+                    } else if constexpr (SBYTES == 8) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                        in[0] = v.x, in[1] = v.y;
+                    } else {
+                        in[0] = lds32(src);
+                    }
+                } else {
+#pragma unroll
+                    for (int w = 0; w < SBYTES / 4; ++w) {
+                        if constexpr (E2M1)
+                            in[w] = lds_u8(src + 4 * w) | lds_u8(src + 4 * w + 1) << 8 | lds_u8(src + 4 * w + 2) << 16 | lds_u8(src + 4 * w + 3) << 24;
+                        else
+                            in[w] = lds_u16(src + 4 * w) | lds_u16(src + 4 * w + 2) << 16;
+                    }
                 }
+#pragma unroll
+                for (int w = 0; w < SW; ++w) {
+                    if constexpr (E2M1) {
+                        const __nv_bfloat162_raw v = __nv_cvt_e8m0x2_to_bf162raw(static_cast<__nv_fp8x2_storage_t>(in[w >> 1] >> (16 * (w & 1))));
+                        sc[h][w] = static_cast<uint32_t>(v.x) | static_cast<uint32_t>(v.y) << 16;
+                    } else {
+                        sc[h][w] = in[w];
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < RUNS; ++j) {
+                if (j > 0 && j * RUN >= k_left) break;
+                float part[2][4];
 #pragma unroll
                 for (int q = 0; q < RUN / 32; ++q) {
                     const int blk = j * (RUN / 32) + q;
                     const uint4 xv = lds128(x_step + blk * 64);
-                    uint32_t u[4], v[4];
                     const uint8_t *wa = smem + (w_lane ^ static_cast<uint32_t>(blk << 4));
-                    decode<E2M1>(lds32(wa), magic, zz[0], u);
-                    decode<E2M1>(lds32(wa + 1024), magic, zz[1], v);
-                    const uint32_t a0[4] = {u[0], v[0], u[1], v[1]}, a1[4] = {u[2], v[2], u[3], v[3]};
-                    mma_16816(part, a0, xv.x, xv.y, q == 0);
-                    mma_16816(part, a1, xv.z, xv.w, false);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t u[4], v[4];
+                        decode_half<E2M1>(lds32(wa + m * 2048), u);
+                        decode_half<E2M1>(lds32(wa + m * 2048 + 1024), v);
+                        const uint32_t a0[4] = {u[0], v[0], u[1], v[1]}, a1[4] = {u[2], v[2], u[3], v[3]};
+                        mma_16816_half(part[m], a0, xv.x, xv.y, q == 0);
+                        mma_16816_half(part[m], a1, xv.z, xv.w, false);
+                    }
                 }
-                float sa, sb;
-                if constexpr (E2M1) {
-                    sa = e8m0_value(lds_u8(s_row[0] + run0 + j));
-                    sb = e8m0_value(lds_u8(s_row[1] + run0 + j));
-                } else {
-                    sa = bf16_value(static_cast<uint16_t>(lds_u16(s_row[0] + 2 * (run0 + j))));
-                    sb = bf16_value(static_cast<uint16_t>(lds_u16(s_row[1] + 2 * (run0 + j))));
+                if constexpr (!E2M1) {  // - z sum x
+                    const float2 xs = xs_step[j * 4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        float &c0 = part[h >> 1][2 * (h & 1)], &c1 = part[h >> 1][2 * (h & 1) + 1];
+                        if constexpr (ZEROS) {
+                            const float z = -static_cast<float>(lds_u8(z_row[h] + run0 + j) & 15u);
+                            c0 = fmaf(z, xs.x, c0);
+                            c1 = fmaf(z, xs.y, c1);
+                        } else {
+                            c0 -= xs.x;
+                            c1 -= xs.y;
+                        }
+                    }
                 }
-                acc[0] = fmaf(sa, part[0], acc[0]);
-                acc[1] = fmaf(sa, part[1], acc[1]);
-                acc[2] = fmaf(sb, part[2], acc[2]);
-                acc[3] = fmaf(sb, part[3], acc[3]);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const float sv = (j & 1) ? __uint_as_float(sc[h][j >> 1] & 0xffff0000u) : __uint_as_float(sc[h][j >> 1] << 16);
+                    float &a0 = acc[h >> 1][2 * (h & 1)], &a1 = acc[h >> 1][2 * (h & 1) + 1];
+                    a0 = fmaf(sv, part[h >> 1][2 * (h & 1)], a0);
+                    a1 = fmaf(sv, part[h >> 1][2 * (h & 1) + 1], a1);
+                }
             }
+            x_step += p.wk * (2 * W4_STEP);
+            xs_step += p.wk * RUNS * 4;
+            k_left -= p.wk * W4_STEP;
+            run0 += p.wk * RUNS;
+            ++got;
             if (++slot == static_cast<uint32_t>(p.stages)) {
                 slot = 0;
                 parity ^= 1u;
@@ -776,9 +988,18 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
             ask();
         }
         // sums[buffer][warp][x row][weight row], added over a team's warps in order
-        float *sums = reinterpret_cast<float *>(smem + p.off_sum) + b * p.warps * 8 * W4S_ROWS;
+        float *sums = reinterpret_cast<float *>(smem + p.off_sum) + b * p.warps * p.xt * W4S_ROWS;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sums[(warp * 8 + 2 * lc + (i & 1)) * W4S_ROWS + lg + 8 * (i >> 1)] = acc[i];
+        for (int i = 0; i < 2; ++i) {
+            const int tok = 2 * lc + i;
+            if (tok >= nx) continue;
+            float *dst = sums + (warp * p.xt + tok) * W4S_ROWS + lg;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                dst[16 * m] = acc[m][i];
+                dst[16 * m + 8] = acc[m][2 + i];
+            }
+        }
         cp_async_wait<0>();
         __syncthreads();  // the sums, and the next tile's scales
         if (aborted) {
@@ -794,15 +1015,22 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
             }
             return;
         }
-        // warp: 16 weight rows of a team x two activation rows a turn
-        for (int32_t i = warp; i < teams * 4; i += p.warps) {
-            const int32_t tm = i >> 2, tok = (i & 3) * 2 + (lane >> 4), n = tm * W4S_ROWS + (lane & 15);
-            if (tok >= nx || n0 + n >= a.N) continue;
-            const float *src = sums + (tm * p.wk * 8 + tok) * W4S_ROWS + (lane & 15);
+        // a warp: the 32 weight rows of a team for one activation row a turn
+        for (int i = warp; i < teams * nx; i += p.warps) {
+            const int tm = i / nx, tok = i - tm * nx, n = tm * W4S_ROWS + lane;
+            if (!E2M1 && x_odd[tok]) {
+                for (int r = 0; r < W4S_ROWS && n0 + tm * W4S_ROWS + r < a.N; ++r) {
+                    const float v = row_dot<E2M1>(a, g, n0 + tm * W4S_ROWS + r, r0 + tok);
+                    if (lane == 0) store_y(a, r0 + tok, n0 + tm * W4S_ROWS + r, v);
+                }
+                continue;
+            }
+            if (n0 + n >= a.N) continue;
+            const float *src = sums + (tm * p.wk * p.xt + tok) * W4S_ROWS + lane;
             float sum = 0.0f;
 #pragma unroll 4
-            for (int v = 0; v < p.wk; ++v) sum += src[v * 8 * W4S_ROWS];
-            store_y(a, r0 + tok, n0 + n, sum);
+            for (int v = 0; v < p.wk; ++v) sum += src[v * p.xt * W4S_ROWS];
+            store_y(a, r0 + tok, n0 + n, sum * (1.0f / (E2M1 ? W4_UNIT_E2M1 : W4_UNIT_INT4)) * x_scale(x_max[tok], true));
         }
     }
     clear();
@@ -869,31 +1097,43 @@ bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &p,
         p.tiles_n = static_cast<int32_t>((a.N + rows - 1) / rows);
         return p.tiles_n * used;
     };
-    // Teams share K while a warp keeps four steps of a tile (a tile's end
-    // costs a warp about a step's time) and the tiles are fewer than six an
-    // SM, or fewer than two an SM and the warp keeps one step; then CTAs of
-    // fewer warps where the tiles do not fill the SMs.
-    while (p.wk < p.warps && 2 * p.wk <= p.steps && tiles() < (8 * p.wk <= p.steps ? w4_env("W4A", 6) : w4_env("W4B", 2)) * sms) p.wk *= 2;
+    // Teams share K while the tiles are fewer than six an SM and a warp keeps
+    // two steps of a tile, or fewer than two an SM and it keeps one; then CTAs
+    // of fewer warps where the tiles do not fill the SMs.
+    while (p.wk < p.warps && 2 * p.wk <= p.steps && tiles() < (4 * p.wk <= p.steps ? w4_env("W4A", 6) : w4_env("W4B", 2)) * sms) p.wk *= 2;
     if (w4_env("W4WK", 0)) p.wk = w4_env("W4WK", 0);
-    while (p.warps > p.wk && p.warps > 2 && tiles() < sms) p.warps /= 2;
+    while (p.warps > p.wk && p.warps > 4 && tiles() < sms) p.warps /= 2;
+    // ... and where two boxes a warp do not fit beside the activations.
+    p.x_pitch = p.steps * W4_STEP * 2 + 64;
+    const int sb = e2m1 ? 1 : 2;
+    // A lane reads a step's scales of a row at once, 4 to 16 bytes: rows lie
+    // an odd number of such pieces apart, in different banks.
+    const int unit = (W4_STEP / a.run * sb + 3) / 4;
+    const int pieces = (p.steps * unit + 1 + unit - 1) / unit | 1;
+    p.s_words = pieces * unit;
+    p.s_vec = (reinterpret_cast<uintptr_t>(a.scales) | static_cast<uintptr_t>(a.lds * sb) | static_cast<uintptr_t>(a.stride_s * sb)) % 4 == 0;
+    p.z_words = a.zeros ? (a.runs + 3) / 4 + 1 : 0;
+    const int xs_bytes = e2m1 ? 0 : p.steps * (W4_STEP / a.run) * 8 * 4;
+    int64_t room;
+    for (;; p.warps /= 2) {
+        if (p.wk > p.warps) p.wk = p.warps;
+        room = SMEM_LIMIT - 2048 - static_cast<int64_t>(p.xt) * p.x_pitch - xs_bytes - 32 -  // 1 KB of alignment, the static part
+               2 * static_cast<int64_t>(p.warps / p.wk) * W4S_ROWS * (p.s_words + p.z_words) * 4 - 2 * p.warps * p.xt * W4S_ROWS * 4;
+        if (room >= 2 * p.warps * W4S_BOX) break;
+        if (p.warps <= 4) return false;
+    }
+    if (w4_env("W4DBG", 0)) std::fprintf(stderr, "w4 warps %d wk %d\n", p.warps, p.wk);
     const int64_t n = tiles();
     grid = static_cast<int>(n < sms ? n : sms);
-    const int sb = e2m1 ? 1 : 2;
     const int tile_rows = p.warps / p.wk * W4S_ROWS;
-    p.x_pitch = p.steps * W4_STEP * 2 + 64;
-    p.s_words = (a.runs * sb + 3) / 4 + 1;
-    p.z_words = a.zeros ? (a.runs + 3) / 4 + 1 : 0;
-    const int64_t fixed = static_cast<int64_t>(p.xt) * p.x_pitch + 2 * static_cast<int64_t>(tile_rows) * (p.s_words + p.z_words) * 4 +
-                          2 * p.warps * 8 * W4S_ROWS * 4;
-    const int64_t room = SMEM_LIMIT - 2048 - fixed;  // 1 KB of alignment, the static barriers
     p.stages = static_cast<int32_t>(room / (p.warps * W4S_BOX));
-    if (room < 0 || p.stages < 2) return false;
     if (p.stages > W4S_STAGES) p.stages = W4S_STAGES;
     p.off_x = p.warps * p.stages * W4S_BOX;
-    p.off_s = p.off_x + p.xt * p.x_pitch;
+    p.off_xs = p.off_x + p.xt * p.x_pitch;
+    p.off_s = (p.off_xs + xs_bytes + 15) / 16 * 16;
     p.off_z = p.off_s + 2 * tile_rows * p.s_words * 4;
     p.off_sum = p.off_z + 2 * tile_rows * p.z_words * 4;
-    smem = static_cast<size_t>(p.off_sum + 2 * p.warps * 8 * W4S_ROWS * 4 + 1024);
+    smem = static_cast<size_t>(p.off_sum + 2 * p.warps * p.xt * W4S_ROWS * 4 + 1024);
     return true;
 }
 
