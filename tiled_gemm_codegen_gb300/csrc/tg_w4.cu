@@ -9,9 +9,9 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
-#include <cstdlib>
-#include <cstdio>
+#include <cmath>
 #include <cstdint>
 
 #include "tg_gemm.h"
@@ -115,14 +115,14 @@ __device__ __forceinline__ void store_y(const W4Args &a, int64_t row, int64_t n,
 }
 
 // Rows of no group: zeros in columns [n0, n1).
-__device__ __forceinline__ void zero_rows(const W4Args &a, int32_t n0, int32_t n1)
+__device__ __forceinline__ void zero_rows(const W4Args &a, int32_t n0, int32_t n1, int32_t threads)
 {
     if (!a.offsets) return;
     const int32_t first = max(0, min(__ldg(a.offsets), a.S));
     const int32_t last = max(first, min(__ldg(a.offsets + a.groups), a.S));
     for (int32_t i = 0; i < first + (a.S - last); ++i) {
         const int64_t row = i < first ? i : last + (i - first);
-        for (int32_t n = n0 + static_cast<int32_t>(threadIdx.x); n < n1; n += static_cast<int32_t>(blockDim.x))
+        for (int32_t n = n0 + static_cast<int32_t>(threadIdx.x); n < n1; n += threads)
             store_y(a, row, n, 0.0f);
     }
 }
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(ANY_COLS * 32) w4_any_kernel(const W4Args a)
     const int lane = threadIdx.x & 31;
     const int32_t n0 = static_cast<int32_t>(blockIdx.x) * ANY_COLS;
     const int32_t n = n0 + static_cast<int32_t>(threadIdx.x >> 5);
-    if (blockIdx.y == 0) zero_rows(a, n0, min(n0 + ANY_COLS, a.N));
+    if (blockIdx.y == 0) zero_rows(a, n0, min(n0 + ANY_COLS, a.N), static_cast<int32_t>(blockDim.x));
     int32_t g, lo, hi;
     if (!nth_group(a, static_cast<int32_t>(blockIdx.y), g, lo, hi) || n >= a.N) return;
     const uint8_t *w = a.w + g * a.stride_w + n * a.ldw;
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
     const uint32_t magic = in_register(E2M1 ? 0x7E807E80u : 0x43004300u), eight = in_register(0x43084308u);
     const int warps = static_cast<int>(blockDim.x >> 5);
     const int32_t n0 = static_cast<int32_t>(blockIdx.x) * W4_ROWS;
-    if (blockIdx.y == 0) zero_rows(a, n0, min(n0 + W4_ROWS, a.N));
+    if (blockIdx.y == 0) zero_rows(a, n0, min(n0 + W4_ROWS, a.N), static_cast<int32_t>(blockDim.x));
     int32_t grp, lo, hi;
     if (!nth_group(a, static_cast<int32_t>(blockIdx.y), grp, lo, hi)) return;
     const uint8_t *w0 = a.w + grp * a.stride_w + n0 * a.ldw;
@@ -510,8 +510,9 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
 // The same product for weights that TMA can address and activations that fit
 // shared memory whole.  One CTA per SM walks a contiguous range of tiles (32
 // weight rows for each of its teams of `wk` warps, which share K step by
-// step); each warp keeps `stages` TMA boxes of 32 rows x 256 codes in flight
-// across the ends of its tiles, so the weights never stop.  What a tile needs
+// step); a producer warp keeps `stages` TMA boxes of 32 rows x 256 codes in
+// flight for each of them, across the ends of tiles, so the weights never stop
+// and a step costs the others one wait and one arrival.  What a tile needs
 // besides is loaded once or ahead: the activations of a group in the order and
 // type the products want, the scales of the next tile by cp.async during this
 // one.
@@ -525,11 +526,11 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
 // of a group's activations made once.  An E2M1 code's three low bits on fp16's
 // exponent and mantissa are its value times 2^-14.
 //
-// Activations become fp16 by a power of two for each row, which brings its
-// largest finite magnitude to [2^11, 2^12); the sums are multiplied back.  A
-// value of bf16's eight bits loses some only below 2^-17 (2^-13 where it is
-// divided by 16) of its row's largest, by 2^-25 of that at most: less than
-// the rounding of the fp32 sum.  A row with an infinity or NaN, for which the
+// Activations become fp16 by a power of two for each row and step of 256, which
+// brings their largest finite magnitude to [2^11, 2^12); a step's sums are
+// multiplied back.  A value of bf16's eight bits loses some only below 2^-28
+// (2^-24 where it is divided by 16) of the step's largest, by 2^-32 of that at
+// most: less than the rounding of the fp32 sum.  A row with an infinity or NaN, for which the
 // difference of two sums is not the sum, is computed value by value instead.
 //
 // A box lies in shared memory with the 128-byte swizzle (16-byte unit u of
@@ -553,6 +554,7 @@ constexpr int W4S_ROWS = 32;
 constexpr int W4S_BOX = W4S_ROWS * W4_STEP / 2;  // 4 KB
 constexpr int W4S_WARPS = 16;
 constexpr int W4S_STAGES = 4;
+constexpr int W4S_STATIC = 2048;  // static shared memory, rounded up
 
 // Pass `nth` over the groups' rows, at most xt rows each: its group, first
 // row and number of rows; false past the last.  Whole warps.
@@ -609,8 +611,23 @@ __device__ __forceinline__ int32_t count_passes(const W4Args &a, int32_t xt)
     return sum;
 }
 
-// The power of two (or its inverse) that brings a row's largest finite
-// magnitude, given as bf16 bits, to [2^11, 2^12); at most 2^126.
+// Shared memory at a + OFF, neither volatile nor a memory access to the
+// compiler: the caller orders them by what a and the results hang on.
+__device__ __forceinline__ uint32_t shared_u32(uint32_t a, int off)
+{
+    uint32_t v;
+    asm("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a + off));
+    return v;
+}
+__device__ __forceinline__ uint4 shared_u128(uint32_t a, int off)
+{
+    uint4 v;
+    asm("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a + off));
+    return v;
+}
+
+// The power of two (or its inverse) that brings the largest finite magnitude of
+// 256 activations, given as bf16 bits, to [2^11, 2^12); at most 2^126.
 __device__ __forceinline__ float x_scale(int32_t most, bool inverse)
 {
     const int32_t up = min(138 - (most >> 7), 126);
@@ -638,7 +655,7 @@ __device__ __forceinline__ float row_dot(const W4Args &a, int32_t g, int32_t n, 
 }
 
 template <bool E2M1, int RUN, bool ZEROS>
-__global__ void __launch_bounds__(W4S_WARPS * 32, 1)
+__global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
     w4_stream_kernel(const __grid_constant__ CUtensorMap tmW, const W4Args a, const W4Stream p)
 {
     constexpr int SB = E2M1 ? 1 : 2;
@@ -646,9 +663,8 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
     constexpr int SW = (RUNS * 2 + 3) / 4;     // registers of a step's scales of a row, bf16
     constexpr int SBYTES = RUNS * SB;          // as staged
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[W4S_WARPS * W4S_STAGES];
+    __shared__ __align__(8) uint64_t bars[2 * W4S_WARPS * W4S_STAGES];  // a warp's full, then its empty ones
     __shared__ int32_t aborted;
-    __shared__ int32_t x_max[8];  // largest finite magnitude of a row, bf16 bits
     __shared__ int32_t x_odd[8];  // the row holds an infinity or NaN
     const uint32_t raw = ptx::smem_addr(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -660,9 +676,13 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
     const int teams = p.warps / p.wk;
     const int tile_rows = teams * W4S_ROWS;
     const uint32_t ring = base + static_cast<uint32_t>(warp * p.stages * W4S_BOX);
-    const uint32_t bar0 = ptx::smem_addr(bars + warp * W4S_STAGES);
-    if (lane == 0) {
-        for (int s = 0; s < p.stages; ++s) ptx::mbar_init(bar0 + 8u * s, 1);
+    const uint32_t bars0 = ptx::smem_addr(bars), bar0 = bars0 + 16u * W4S_STAGES * warp;
+    const int threads = p.warps * 32;  // without the producer's
+    if (warp < p.warps && lane == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            ptx::mbar_init(bar0 + 8u * s, 1);
+            ptx::mbar_init(bar0 + 8u * (W4S_STAGES + s), 1);
+        }
         ptx::fence_barrier_init();
     }
     if (threadIdx.x == 0) {
@@ -675,12 +695,12 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
 
     auto clear = [&]() {  // this CTA's share of the rows of no group
         for (int32_t n = static_cast<int32_t>(blockIdx.x) * 256; n < a.N; n += static_cast<int32_t>(gridDim.x) * 256)
-            zero_rows(a, n, min(n + 256, a.N));
+            zero_rows(a, n, min(n + 256, a.N), threads);
     };
     const int64_t tiles = static_cast<int64_t>(count_passes(a, p.xt)) * p.tiles_n;
     const int64_t first = blockIdx.x * tiles / gridDim.x, last = (blockIdx.x + 1) * tiles / gridDim.x;
     if (first == last) {
-        clear();
+        if (warp < p.warps) clear();
         return;
     }
     // A tile by its pass and its place in it, stepped without a division.
@@ -696,48 +716,81 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
         }
     };
     const At at0{static_cast<int32_t>(last - first), static_cast<int32_t>(first / p.tiles_n), static_cast<int32_t>(first % p.tiles_n)};
+    if (warp == p.warps) {
+        // ------------------------------------------------ producer
+        // Lane l keeps warp l's ring full: a box at a time, whenever the
+        // warp has freed its slot.
+        const bool used = lane < p.warps;
+        const int l_team = lane / p.wk, l_part = lane % p.wk;
+        const int32_t each = (p.steps - l_part + p.wk - 1) / p.wk;
+        const uint32_t l_ring = base + static_cast<uint32_t>(lane * p.stages * W4S_BOX);
+        const uint32_t l_full = bars0 + 16u * W4S_STAGES * lane, l_empty = l_full + 8u * W4S_STAGES;
+        int32_t pass = at0.pass - 1, g = 0;
+        uint32_t slot = 0, parity = 1;
+        uint64_t t0 = 0;
+        bool ok = true;
+        for (At at = at0; ok && at.left > 0; at.next(p.tiles_n)) {
+            if (at.pass != pass) {
+                int32_t r, n;
+                nth_pass(a, p.xt, at.pass, g, r, n);
+                pass = at.pass;
+            }
+            const int32_t n0 = at.n * tile_rows + l_team * W4S_ROWS;
+            int32_t i = used ? 0 : each;  // boxes of the tile asked for
+            while (__any_sync(0xffffffffu, i < each)) {
+                bool moved = false;
+                if (i < each && ptx::mbar_try_wait(l_empty + 8u * slot, parity)) {
+                    ptx::mbar_arrive_expect_tx(l_full + 8u * slot, W4S_BOX);
+                    ptx::tma_load_3d(l_ring + slot * W4S_BOX, &tmW, l_full + 8u * slot, (l_part + i * p.wk) * (W4_STEP / 2), n0, g);
+                    ++i;
+                    moved = true;
+                    if (++slot == static_cast<uint32_t>(p.stages)) {
+                        slot = 0;
+                        parity ^= 1u;
+                    }
+                }
+                if (__any_sync(0xffffffffu, moved)) {
+                    t0 = 0;
+                } else {
+                    const uint64_t now = ptx::global_timer_ns();
+                    if (t0 == 0) t0 = now;
+                    const bool late = now - t0 > p.timeout_ns;
+                    if (late && lane == 0) {
+                        atomicCAS(p.err, 0u, static_cast<uint32_t>(ERR_TIMEOUT_PRODUCER));
+                        *reinterpret_cast<volatile int32_t *>(&aborted) = 1;
+                    }
+                    if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int32_t *>(&aborted) != 0)) {
+                        ok = false;
+                        break;
+                    }
+                }
+            }
+        }
+        // every box asked for has landed (bounded) before the CTA may leave
+        t0 = ptx::global_timer_ns();
+        if (used) {
+            for (int s = 0; s < p.stages; ++s) {
+                // the slot's last copy completed the phase before the one its
+                // next use would wait for: slots before `slot` were used once more
+                const uint32_t done = static_cast<uint32_t>(s) < slot ? parity ^ 1u : parity;
+                while (!ptx::mbar_try_wait(l_full + 8u * s, done))
+                    if (ptx::global_timer_ns() - t0 > p.timeout_ns) break;
+            }
+        }
+        return;
+    }
     // this warp's steps of a tile: part_k, part_k + wk, ... (wk <= steps)
     const int32_t mine = (p.steps - part_k + p.wk - 1) / p.wk;
-
     int32_t g_next, r0_next, nx_next;  // the pass of the next tile
     nth_pass(a, p.xt, at0.pass, g_next, r0_next, nx_next);
-
-    // ---- producer: the next box to ask for
-    At pat = at0;
-    int32_t pk = part_k * (W4_STEP / 2), pn = pat.n * tile_rows + team * W4S_ROWS, pg = g_next;  // its coordinates
-    int32_t p_left = mine, pslot = 0;
-    uint32_t asked = 0;
-    auto ask = [&]() {  // one box, if any is left (warp-uniform)
-        if (p_left == 0) return;
-        if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(bar0 + 8u * pslot, W4S_BOX);
-            ptx::tma_load_3d(ring + pslot * W4S_BOX, &tmW, bar0 + 8u * pslot, pk, pn, pg);
-        }
-        ++asked;
-        if (++pslot == p.stages) pslot = 0;
-        pk += p.wk * (W4_STEP / 2);
-        if (--p_left == 0) {  // the next tile's first
-            const int32_t pass = pat.pass;
-            pat.next(p.tiles_n);
-            if (pat.left == 0) return;
-            if (pat.pass != pass) {
-                int32_t r, n;
-                nth_pass(a, p.xt, pat.pass, pg, r, n);
-            }
-            p_left = mine;
-            pk = part_k * (W4_STEP / 2);
-            pn = pat.n * tile_rows + team * W4S_ROWS;
-        }
-    };
-    for (int s = 0; s < p.stages; ++s) ask();
 
     // ---- scales and zeros of a tile -> buffer b; a thread's first word and
     // its step to the next are the same for every tile
     const int32_t s_used = (a.runs * SB + 3) / 4 + (p.s_vec ? 0 : 1), z_used = ZEROS ? (a.runs + 3) / 4 + 1 : 1;
     const int32_t s_r = static_cast<int32_t>(threadIdx.x) / s_used, s_w = static_cast<int32_t>(threadIdx.x) - s_r * s_used;
-    const int32_t s_dr = static_cast<int32_t>(blockDim.x) / s_used, s_dw = static_cast<int32_t>(blockDim.x) - s_dr * s_used;
+    const int32_t s_dr = threads / s_used, s_dw = threads - s_dr * s_used;
     const int32_t z_r = static_cast<int32_t>(threadIdx.x) / z_used, z_w = static_cast<int32_t>(threadIdx.x) - z_r * z_used;
-    const int32_t z_dr = static_cast<int32_t>(blockDim.x) / z_used, z_dw = static_cast<int32_t>(blockDim.x) - z_dr * z_used;
+    const int32_t z_dr = threads / z_used, z_dw = threads - z_dr * z_used;
     auto stage_scales = [&](int32_t n0, int32_t g, int b) {
         const int32_t rows = min(tile_rows, a.N - n0);
         auto copy = [&](const uint8_t *src0, int64_t pitch, int32_t bytes, const uint8_t *any, int32_t used, int32_t words, uint32_t dst,
@@ -762,24 +815,22 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
                  base + p.off_z + b * tile_rows * p.z_words * 4, z_r, z_w, z_dr, z_dw);
     };
 
-    // ---- activations of a pass, as fp16 times a power of two: eight
-    // consecutive ones paired as the codes of a word are; and their sums by
-    // group of codes, times the code's unit (and the zero point where it is 8)
+    // ---- activations of a pass, as fp16 times a power of two for each row
+    // and step: eight consecutive ones paired as the codes of a word are; and
+    // their sums by group of codes, times the code's unit (and by 8, the zero
+    // point, where there is no other).  A warp takes the 256 of a row and step.
     auto stage_x = [&](int32_t r0, int32_t nx) {
-        const int32_t chunks = p.steps * (W4_STEP / 8);
-        const int32_t items = nx * chunks;  // 16-byte pieces, 32 a warp and turn: all of one row
         const bool aligned = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(2 * a.ldx)) & 15u) == 0;
-        if (threadIdx.x < 8) x_max[threadIdx.x] = x_odd[threadIdx.x] = 0;
-        __syncthreads();
         constexpr int U = 4;  // turns whose loads are in flight together
-        for (int32_t i0 = static_cast<int32_t>(threadIdx.x); i0 < items; i0 += U * static_cast<int32_t>(blockDim.x)) {
+        const int32_t turns = nx * p.steps;
+        for (int32_t i0 = warp; i0 < turns; i0 += U * p.warps) {
             uint4 v[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int32_t i = i0 + u * static_cast<int32_t>(blockDim.x);
+                const int32_t i = i0 + u * p.warps;
                 v[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (i >= items) continue;
-                const int32_t t = i / chunks, c = i - t * chunks;
+                if (i >= turns) continue;
+                const int32_t t = i / p.steps, c = (i - t * p.steps) * 32 + lane;
                 const uint16_t *row = a.x + (r0 + t) * a.ldx + c * 8;
                 if (aligned && c * 8 + 8 <= a.K) {
                     v[u] = *reinterpret_cast<const uint4 *>(row);
@@ -792,9 +843,9 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int32_t i = i0 + u * static_cast<int32_t>(blockDim.x);
-                if (i >= items) break;  // warp-uniform: items and the block are multiples of 32
-                const int32_t t = i / chunks, c = i - t * chunks;
+                const int32_t i = i0 + u * p.warps;
+                if (i >= turns) break;
+                const int32_t t = i / p.steps, step = i - t * p.steps, c = step * 32 + lane;
                 const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
                 int32_t most = 0;
                 bool odd = false;
@@ -802,41 +853,33 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
                 for (int e = 0; e < 4; ++e) {
                     const int32_t lo = static_cast<int32_t>(w[e] & 0x7fffu), hi = static_cast<int32_t>(w[e] >> 16 & 0x7fffu);
                     odd |= lo >= 0x7f80 || hi >= 0x7f80;
-                    if (lo < 0x7f80) most = max(most, lo);
-                    if (hi < 0x7f80) most = max(most, hi);
+                    most = max(most, max(lo < 0x7f80 ? lo : 0, hi < 0x7f80 ? hi : 0));
                 }
-                *reinterpret_cast<uint4 *>(smem + p.off_x + t * p.x_pitch + c * 16) = v[u];
-                most = __reduce_max_sync(0xffffffffu, most);
-                if (lane == 0) atomicMax(&x_max[t], most);
                 if (odd) x_odd[t] = 1;
-            }
-        }
-        __syncthreads();
-        for (int32_t i = static_cast<int32_t>(threadIdx.x); i < items; i += static_cast<int32_t>(blockDim.x)) {
-            const int32_t t = i / chunks, c = i - t * chunks;
-            const float mul = x_scale(x_max[t], false);
-            uint4 *at = reinterpret_cast<uint4 *>(smem + p.off_x + t * p.x_pitch + c * 16);
-            const uint4 v = *at;  // this thread's own
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            float f[8], sum = 0.0f;
+                most = __reduce_max_sync(0xffffffffu, most);
+                const float mul = x_scale(most, false);
+                float f[8], sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) * mul;
-                f[e] = __half2float(__float2half_rn(!E2M1 && (e & 1) ? x * 0.0625f : x));
-                sum += !E2M1 && (e & 1) ? f[e] * 16.0f : f[e];
-            }
-            uint32_t h[4];
+                for (int e = 0; e < 8; ++e) {
+                    const float x = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) * mul;
+                    f[e] = __half2float(__float2half_rn(!E2M1 && (e & 1) ? x * 0.0625f : x));
+                    sum += !E2M1 && (e & 1) ? f[e] * 16.0f : f[e];
+                }
+                uint32_t h[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __half2 q = __floats2half2_rn(f[e], f[e + 4]);
-                h[e] = *reinterpret_cast<const uint32_t *>(&q);
-            }
-            *at = make_uint4(h[0], h[1], h[2], h[3]);
-            if constexpr (!E2M1) {
+                for (int e = 0; e < 4; ++e) {
+                    const __half2 q = __floats2half2_rn(f[e], f[e + 4]);
+                    h[e] = *reinterpret_cast<const uint32_t *>(&q);
+                }
+                *reinterpret_cast<uint4 *>(smem + p.off_x + t * p.x_pitch + c * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                float *xs = reinterpret_cast<float *>(smem + p.off_xs);
+                if (lane == 0) xs[step * 8 + t] = x_scale(most, true);
+                if constexpr (!E2M1) {
 #pragma unroll
-                for (int d = 1; d < RUN / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                if (lane % (RUN / 8) == 0)
-                    *reinterpret_cast<float *>(smem + p.off_xs + (c / (RUN / 8) * 8 + t) * 4) = sum * (ZEROS ? W4_UNIT_INT4 : 8.0f * W4_UNIT_INT4);
+                    for (int d = 1; d < RUN / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    if (lane % (RUN / 8) == 0)
+                        xs[p.steps * 8 + c / (RUN / 8) * 8 + t] = sum * (ZEROS ? W4_UNIT_INT4 : 8.0f * W4_UNIT_INT4);
+                }
             }
         }
     };
@@ -844,19 +887,19 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
     At at = at0;
     int32_t g, r0, nx;  // the tile's pass
     stage_scales(at.n * tile_rows, g_next, 0);
-    uint32_t got = 0;               // boxes read
-    uint32_t slot = 0, parity = 0;  // of the next one
+    uint32_t slot = 0, parity = 0;  // of the next box
     bool fresh = true;  // the tile's activations are not in shared memory yet
     for (int b = 0; at.left > 0; b ^= 1) {
         if (fresh) {
-            __syncthreads();  // every warp is done with the old ones
+            if (threadIdx.x < 8) x_odd[threadIdx.x] = 0;
+            ptx::named_barrier_sync(1, threads);  // every warp is done with the old ones
             g = g_next;
             r0 = r0_next;
             nx = nx_next;
             stage_x(r0, nx);
             cp_async_commit();
             cp_async_wait<0>();
-            __syncthreads();
+            ptx::named_barrier_sync(1, threads);
         }
         const int32_t n0 = at.n * tile_rows;
         at.next(p.tiles_n);  // from here on the tile behind this one
@@ -880,8 +923,9 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
             }
         }
         // (an operand column of no row repeats row 0's: its sums are not stored)
-        const uint8_t *x_step = smem + p.off_x + (lg < nx ? lg : 0) * p.x_pitch + lc * 16 + part_k * (2 * W4_STEP);
-        const float2 *xs_step = reinterpret_cast<const float2 *>(smem + p.off_xs) + part_k * RUNS * 4 + lc;
+        uint32_t x_step = base + p.off_x + (lg < nx ? lg : 0) * p.x_pitch + lc * 16 + part_k * (2 * W4_STEP);
+        const float2 *xs_step = reinterpret_cast<const float2 *>(smem + p.off_xs) + (p.steps + part_k * RUNS) * 4 + lc;
+        const float2 *inv_step = reinterpret_cast<const float2 *>(smem + p.off_xs) + part_k * 4 + lc;
         int32_t k_left = a.K - part_k * W4_STEP;  // codes from the step's first
         int32_t run0 = part_k * RUNS;
         for (int32_t i = 0; i < mine; ++i) {
@@ -897,7 +941,11 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
                 }
             }
             __syncwarp();
-            const uint32_t w_lane = (ring - base + slot * W4S_BOX + lg * 128 + lc * 4) ^ static_cast<uint32_t>(lg << 4);
+            uint32_t w_lane = (ring + slot * W4S_BOX + lg * 128 + lc * 4) ^ static_cast<uint32_t>(lg << 4);
+            // (the loads below are not volatile, so that they mix with the
+            // products; they hang on w_lane, which exists from here on)
+            asm volatile("" : "+r"(w_lane), "+r"(x_step)::"memory");
+            float sum[2][4];  // of the step
             // the step's scales, as bf16 pairs
             uint32_t sc[4][SW];
 #pragma unroll
@@ -940,13 +988,13 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
 #pragma unroll
                 for (int q = 0; q < RUN / 32; ++q) {
                     const int blk = j * (RUN / 32) + q;
-                    const uint4 xv = lds128(x_step + blk * 64);
-                    const uint8_t *wa = smem + (w_lane ^ static_cast<uint32_t>(blk << 4));
+                    const uint4 xv = shared_u128(x_step, blk * 64);
+                    const uint32_t wa = w_lane ^ static_cast<uint32_t>(blk << 4);
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         uint32_t u[4], v[4];
-                        decode_half<E2M1>(lds32(wa + m * 2048), u);
-                        decode_half<E2M1>(lds32(wa + m * 2048 + 1024), v);
+                        decode_half<E2M1>(shared_u32(wa, m * 2048), u);
+                        decode_half<E2M1>(shared_u32(wa, m * 2048 + 1024), v);
                         const uint32_t a0[4] = {u[0], v[0], u[1], v[1]}, a1[4] = {u[2], v[2], u[3], v[3]};
                         mma_16816_half(part[m], a0, xv.x, xv.y, q == 0);
                         mma_16816_half(part[m], a1, xv.z, xv.w, false);
@@ -970,22 +1018,29 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     const float sv = (j & 1) ? __uint_as_float(sc[h][j >> 1] & 0xffff0000u) : __uint_as_float(sc[h][j >> 1] << 16);
-                    float &a0 = acc[h >> 1][2 * (h & 1)], &a1 = acc[h >> 1][2 * (h & 1) + 1];
-                    a0 = fmaf(sv, part[h >> 1][2 * (h & 1)], a0);
-                    a1 = fmaf(sv, part[h >> 1][2 * (h & 1) + 1], a1);
+                    float &a0 = sum[h >> 1][2 * (h & 1)], &a1 = sum[h >> 1][2 * (h & 1) + 1];
+                    a0 = j == 0 ? sv * part[h >> 1][2 * (h & 1)] : fmaf(sv, part[h >> 1][2 * (h & 1)], a0);
+                    a1 = j == 0 ? sv * part[h >> 1][2 * (h & 1) + 1] : fmaf(sv, part[h >> 1][2 * (h & 1) + 1], a1);
                 }
             }
+            const float2 inv = *inv_step;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e >> 2][e & 3] = fmaf(e & 1 ? inv.y : inv.x, sum[e >> 2][e & 3], acc[e >> 2][e & 3]);
             x_step += p.wk * (2 * W4_STEP);
             xs_step += p.wk * RUNS * 4;
             k_left -= p.wk * W4_STEP;
             run0 += p.wk * RUNS;
-            ++got;
+            inv_step += p.wk * 4;
+            // the box has been read into these sums: its slot may be filled again
+            asm volatile(""
+                         : "+f"(acc[0][0]), "+f"(acc[0][1]), "+f"(acc[0][2]), "+f"(acc[0][3]), "+f"(acc[1][0]), "+f"(acc[1][1]), "+f"(acc[1][2]),
+                           "+f"(acc[1][3])::"memory");
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar0 + 8u * (W4S_STAGES + slot));
             if (++slot == static_cast<uint32_t>(p.stages)) {
                 slot = 0;
                 parity ^= 1u;
             }
-            __syncwarp();  // every lane has read the box: the slot may be filled again
-            ask();
         }
         // sums[buffer][warp][x row][weight row], added over a team's warps in order
         float *sums = reinterpret_cast<float *>(smem + p.off_sum) + b * p.warps * p.xt * W4S_ROWS;
@@ -1001,20 +1056,8 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
             }
         }
         cp_async_wait<0>();
-        __syncthreads();  // the sums, and the next tile's scales
-        if (aborted) {
-            // the boxes still on their way land (or the limit runs out) before the CTA leaves
-            const uint64_t t0 = ptx::global_timer_ns();
-            for (; got < asked; ++got) {
-                while (!ptx::mbar_try_wait(bar0 + 8u * slot, parity))
-                    if (ptx::global_timer_ns() - t0 > p.timeout_ns) return;
-                if (++slot == static_cast<uint32_t>(p.stages)) {
-                    slot = 0;
-                    parity ^= 1u;
-                }
-            }
-            return;
-        }
+        ptx::named_barrier_sync(1, threads);  // the sums, and the next tile's scales
+        if (aborted) return;  // (the producer waits for the boxes on their way)
         // a warp: the 32 weight rows of a team for one activation row a turn
         for (int i = warp; i < teams * nx; i += p.warps) {
             const int tm = i / nx, tok = i - tm * nx, n = tm * W4S_ROWS + lane;
@@ -1030,7 +1073,7 @@ __global__ void __launch_bounds__(W4S_WARPS * 32, 1)
             float sum = 0.0f;
 #pragma unroll 4
             for (int v = 0; v < p.wk; ++v) sum += src[v * p.xt * W4S_ROWS];
-            store_y(a, r0 + tok, n0 + n, sum * (1.0f / (E2M1 ? W4_UNIT_E2M1 : W4_UNIT_INT4)) * x_scale(x_max[tok], true));
+            store_y(a, r0 + tok, n0 + n, sum * (1.0f / (E2M1 ? W4_UNIT_E2M1 : W4_UNIT_INT4)));
         }
     }
     clear();
@@ -1083,27 +1126,13 @@ cudaError_t launch_w4(const W4Args &a, bool e2m1, int64_t used, int xt, int dev,
     return launch_tile<false, 128, false, VEC>(a, used, xt, dev, s);
 }
 
-int w4_env(const char *k, int d) { const char *v = std::getenv(k); return v ? std::atoi(v) : d; }
-// The stream kernel's plan; false where its activations do not fit.
+// The stream kernel's plan; false where its activations do not fit.  `used`:
+// the groups that have rows, at most.
 bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &p, int &grid, size_t &smem)
 {
     p.xt = 1;
     while (p.xt < 8 && p.xt < a.S) p.xt *= 2;
     p.steps = (a.K + W4_STEP - 1) / W4_STEP;
-    p.warps = W4S_WARPS;
-    p.wk = 1;
-    auto tiles = [&]() {
-        const int64_t rows = static_cast<int64_t>(p.warps / p.wk) * W4S_ROWS;
-        p.tiles_n = static_cast<int32_t>((a.N + rows - 1) / rows);
-        return p.tiles_n * used;
-    };
-    // Teams share K while the tiles are fewer than six an SM and a warp keeps
-    // two steps of a tile, or fewer than two an SM and it keeps one; then CTAs
-    // of fewer warps where the tiles do not fill the SMs.
-    while (p.wk < p.warps && 2 * p.wk <= p.steps && tiles() < (4 * p.wk <= p.steps ? w4_env("W4A", 6) : w4_env("W4B", 2)) * sms) p.wk *= 2;
-    if (w4_env("W4WK", 0)) p.wk = w4_env("W4WK", 0);
-    while (p.warps > p.wk && p.warps > 4 && tiles() < sms) p.warps /= 2;
-    // ... and where two boxes a warp do not fit beside the activations.
     p.x_pitch = p.steps * W4_STEP * 2 + 64;
     const int sb = e2m1 ? 1 : 2;
     // A lane reads a step's scales of a row at once, 4 to 16 bytes: rows lie
@@ -1113,21 +1142,42 @@ bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &p,
     p.s_words = pieces * unit;
     p.s_vec = (reinterpret_cast<uintptr_t>(a.scales) | static_cast<uintptr_t>(a.lds * sb) | static_cast<uintptr_t>(a.stride_s * sb)) % 4 == 0;
     p.z_words = a.zeros ? (a.runs + 3) / 4 + 1 : 0;
-    const int xs_bytes = e2m1 ? 0 : p.steps * (W4_STEP / a.run) * 8 * 4;
-    int64_t room;
-    for (;; p.warps /= 2) {
-        if (p.wk > p.warps) p.wk = p.warps;
-        room = SMEM_LIMIT - 2048 - static_cast<int64_t>(p.xt) * p.x_pitch - xs_bytes - 32 -  // 1 KB of alignment, the static part
-               2 * static_cast<int64_t>(p.warps / p.wk) * W4S_ROWS * (p.s_words + p.z_words) * 4 - 2 * p.warps * p.xt * W4S_ROWS * 4;
-        if (room >= 2 * p.warps * W4S_BOX) break;
-        if (p.warps <= 4) return false;
+    const int xs_bytes = p.steps * (1 + (e2m1 ? 0 : W4_STEP / a.run)) * 8 * 4;
+    // The passes to expect: rows that fall on groups at random leave some
+    // groups empty (S of them reach groups (1 - (1 - 1/groups)^S)).
+    double passes = static_cast<double>((a.S + p.xt - 1) / p.xt);
+    if (a.offsets && a.groups > 1) {
+        const double hit = a.groups * (1.0 - std::pow(1.0 - 1.0 / a.groups, static_cast<double>(a.S)));
+        passes = std::fmax(passes, std::fmin(hit, static_cast<double>(used)));
     }
-    if (w4_env("W4DBG", 0)) std::fprintf(stderr, "w4 warps %d wk %d\n", p.warps, p.wk);
-    const int64_t n = tiles();
+    // A CTA's time: for each of its tiles a turn of `warps` boxes for every
+    // step a warp has, and the tile's end.  Measured on 28672 rows of 8192
+    // codes (16 warps; teams of 16, 8, 4 and 2 warps: 27.4, 27.1, 31.0 and
+    // 33.7 us): a turn costs 1.5 times the end.  Fewer warps only shorten a
+    // turn to a half, where latency is what is left of it.
+    double best = 0.0;
+    for (int warps = W4S_WARPS; warps >= 4; warps /= 2) {
+        for (int wk = 1; wk <= warps && wk <= p.steps; wk *= 2) {
+            const int rows = warps / wk * W4S_ROWS;
+            const int64_t room = SMEM_LIMIT - W4S_STATIC - 1024 - static_cast<int64_t>(p.xt) * p.x_pitch - xs_bytes - 32 -  // (1 KB: alignment)
+                                 2 * static_cast<int64_t>(rows) * (p.s_words + p.z_words) * 4 - 2 * warps * p.xt * W4S_ROWS * 4;
+            if (room < 2 * warps * W4S_BOX) continue;
+            const int64_t tiles_n = (a.N + rows - 1) / rows;
+            const double rounds = std::ceil(passes * tiles_n / sms);
+            const double cost = rounds * (1.5 * ((p.steps + wk - 1) / wk) * std::fmax(warps, 8) / 16.0 + 1.0);
+            if (best != 0.0 && cost >= best) continue;
+            best = cost;
+            p.warps = warps;
+            p.wk = wk;
+            p.tiles_n = static_cast<int32_t>(tiles_n);
+            p.stages = static_cast<int32_t>(room / (warps * W4S_BOX));
+        }
+    }
+    if (best == 0.0) return false;
+    if (p.stages > W4S_STAGES) p.stages = W4S_STAGES;
+    const int64_t n = p.tiles_n * (a.offsets ? std::max<int64_t>(used, (a.S + p.xt - 1) / p.xt) : (a.S + p.xt - 1) / p.xt);
     grid = static_cast<int>(n < sms ? n : sms);
     const int tile_rows = p.warps / p.wk * W4S_ROWS;
-    p.stages = static_cast<int32_t>(room / (p.warps * W4S_BOX));
-    if (p.stages > W4S_STAGES) p.stages = W4S_STAGES;
     p.off_x = p.warps * p.stages * W4S_BOX;
     p.off_xs = p.off_x + p.xt * p.x_pitch;
     p.off_s = (p.off_xs + xs_bytes + 15) / 16 * 16;
@@ -1144,11 +1194,11 @@ cudaError_t launch_stream(const CUtensorMap &tm, const W4Args &a, const W4Stream
     static std::atomic<unsigned long long> configured{0};
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
     if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT - 1024);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT - W4S_STATIC);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch(kern, dim3(static_cast<unsigned>(grid)), p.warps * 32, smem, s, tm, a, p);
+    return launch(kern, dim3(static_cast<unsigned>(grid)), (p.warps + 1) * 32, smem, s, tm, a, p);
 }
 
 cudaError_t launch_stream_of(bool e2m1, const CUtensorMap &tm, const W4Args &a, const W4Stream &p, int grid, size_t smem, int dev,
