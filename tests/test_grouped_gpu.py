@@ -157,6 +157,37 @@ def test_non_finite_rows_stay_in_their_group(pair):
     assert not np.isfinite(G[3]).any()
 
 
+# Few tiles and a long contraction: the tiles are shared between workers
+SHARED = [([5000], 130, 70), ([3000, 0, 17, 2500], 64, 128), ([1, 6000], 300, 260), ([64 * 9 - 1], 40, 40)]
+
+
+@pytest.mark.parametrize("sizes,M,N", SHARED)
+@pytest.mark.parametrize("pair", [0, 1, 2])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_shared_tiles_of_wgrad(sizes, M, N, pair, dtype):
+    S = sum(sizes)
+    A, av = _rand((S, M), 30, True)
+    B, bv = _rand((S, N), 31, True)
+    off, opts = _offsets(sizes), tg.make_options(cta_pair=pair)
+    want = torch.from_numpy(_wgrad_ref(av, bv, sizes, 0)).to(dtype).double().numpy()
+    for _ in range(2):  # the arrival counters are left ready for the next call
+        assert np.array_equal(_np(tg.gemm_grouped_wgrad(A, B, off, out_dtype=dtype, options=opts)), want)
+
+
+@pytest.mark.parametrize("sizes", [[1], [3, 0, 2], [0, 40], [130]])
+@pytest.mark.parametrize("K,N", [(4096, 64), (5000, 200), (1100, 129)])
+@pytest.mark.parametrize("pair", [0, 1, 2])
+def test_shared_tiles_of_rows(sizes, K, N, pair):
+    S = sum(sizes)
+    A, av = _rand((S, K), 32, True)
+    B, bv = _rand((len(sizes), K, N), 33, True)
+    bias = torch.randint(-4, 5, (len(sizes), N), device=dev()).float()
+    want = np.maximum(_rows_ref(av, bv, sizes, 0, S) + np.repeat(_np(bias), sizes, axis=0), 0)
+    for _ in range(2):
+        D = tg.gemm_grouped(A, B, _offsets(sizes), bias=bias, activation="relu", options=tg.make_options(cta_pair=pair))
+        assert np.array_equal(_np(D), want)
+
+
 RANDOM = [([0, 300, 17, 1000, 256], 1024, 640), ([2000, 96], 512, 1408), ([2] * 40 + [0] * 9, 2048, 200)]
 
 

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int64_t GROUPED_EXTENT = INT32_MAX - 1024;  // a tile past the end stays in range
 constexpr int64_t PITCH_LIMIT = int64_t(1) << 40;
+constexpr int64_t SPLIT_DEPTH = 8;  // k-blocks a worker has at least of a shared tile
 
 using GroupedKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const GroupedParams);
 
@@ -111,14 +112,17 @@ size_t pack_bytes(const Operand &o)
 }
 
 // Copies the operands that TMA cannot address to aligned scratch.
-tg_status realign(const HostStream &hs, Operand &a, Operand &b)
+// (part_bytes of the scratch in front of the copies are for partial tiles.)
+tg_status realign(const HostStream &hs, Operand &a, Operand &b, size_t part_bytes, float **partials)
 {
-    if (!a.pack && !b.pack) return TG_OK;
+    if (!a.pack && !b.pack && !part_bytes) return TG_OK;
     void *arena = nullptr;
-    tg_status st = host_arena(hs, pack_bytes(a) + pack_bytes(b), &arena);
+    tg_status st = host_arena(hs, part_bytes + pack_bytes(a) + pack_bytes(b), &arena);
     if (st != TG_OK) return st;
+    *partials = static_cast<float *>(arena);
+    if (!a.pack && !b.pack) return TG_OK;
     HostPack ja, jb;
-    uint8_t *at = static_cast<uint8_t *>(arena);
+    uint8_t *at = static_cast<uint8_t *>(arena) + part_bytes;
     auto move = [&](Operand &o, HostPack &j) {
         if (!o.pack) return;
         j = HostPack{o.p, at, o.rows, o.cols, o.ld, o.nb, o.stride};
@@ -185,7 +189,7 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     const int64_t tiles_m = cdiv(M, tile_m);
     const int64_t row_tiles = S / tile_m + (groups < S ? groups : S);  // at most, over all groups
     const int64_t units = wgrad ? groups * tiles_m * tiles_n : row_tiles * tiles_n;
-    if (row_tiles * tiles_n > INT32_MAX || tiles_m * tiles_n > INT32_MAX) return TG_ERR_UNSUPPORTED;
+    if (units > INT32_MAX) return TG_ERR_UNSUPPORTED;
 
     GroupedParams p{};
     p.offsets = offsets;
@@ -212,6 +216,17 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     p.err = hs.err;
     p.timeout_ns = opt && opt->timeout_ns ? opt->timeout_ns : HOST_TIMEOUT_NS;
 
+    // Few tiles and a long contraction: workers share tiles, each at least
+    // eight k-blocks of the average group, while a wave holds them all.
+    const int64_t workers = pair ? hs.sms / 2 : hs.sms;
+    const int64_t depth = wgrad ? cdiv(S / groups, BK) : cdiv(K, BK);
+    int64_t splits = units > 0 ? workers / units : 1;
+    if (splits > depth / SPLIT_DEPTH) splits = depth / SPLIT_DEPTH;
+    if (splits < 1) splits = 1;
+    p.splits = static_cast<int32_t>(splits);
+    const int64_t part_tiles = splits > 1 ? units * (pair ? 2 : 1) : 0;
+    const size_t part_bytes = static_cast<size_t>(part_tiles) * splits * BM * bn * 4;
+
     const bool reads = S > 0 && (wgrad || K > 0);
     if (b.nb > 1 && b.stride == 0) {  // one matrix for every group
         b.nb = 1;
@@ -222,7 +237,7 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
         const bool force = opt && opt->force_pack;
         a.pack = force || !tma_ok(a.p, a.ld, 0, 2);
         b.pack = force || !tma_ok(b.p, b.ld, b.nb > 1 ? b.stride : 0, 2);
-        if ((st = realign(hs, a, b)) != TG_OK) return st;
+        if ((st = realign(hs, a, b, part_bytes, &p.partials)) != TG_OK) return st;
         const uint32_t a_box1 = wgrad ? BK : BM;
         const uint32_t b_box1 = b_k ? static_cast<uint32_t>(pair ? bn / 2 : bn) : BK;
         if (!host_encode_3d(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.p, a.cols, a.rows, a.nb, a.ld * 2, problem_stride(a), 64,
@@ -244,7 +259,8 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
                                     shape<128, 6, false, true>(), shape<256, 6, true, true>()};
     static ShapeState states[4];
     const int which = (wgrad ? 2 : 0) + (pair ? 1 : 0);
-    return host_cuda_status(launch_shape(shapes[which], states[which], hs, units, ta, tb, td, p));
+    if (splits > 1 && (st = host_counters(hs, static_cast<size_t>(part_tiles) * 4, &p.counters)) != TG_OK) return st;
+    return host_cuda_status(launch_shape(shapes[which], states[which], hs, units * splits, ta, tb, td, p));
 }
 
 }  // namespace

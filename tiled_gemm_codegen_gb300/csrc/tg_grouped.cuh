@@ -19,6 +19,10 @@
 // wgrad mode adds warp 6, the fixer, which runs as far ahead of the MMA as
 // the ring allows.  PAIR: a cluster of two CTAs computes 256 x BN.
 //
+// Where there are fewer tiles than workers, `splits` of them share a tile's
+// contraction: each writes its fp32 partial tile to scratch, and the last to
+// arrive adds them in the order of k, as gemm_kernel's split-K does.
+//
 // The list of tiles depends on offsets the host has not seen: every warp
 // walks it by itself, 32 groups at a time with a lane for each (a group's
 // tile count, a warp scan, a ballot), so that no table in shared memory and
@@ -48,6 +52,9 @@ struct GroupedParams {
     float alpha;
     const float *bias;
     int64_t bias_stride;
+    int32_t splits;          // workers that share a tile (at most one per k-block)
+    float *partials;         // splits > 1: [tile][CTA of the pair][splits][BM x BN]
+    int32_t *counters;       // splits > 1: arrivals per [tile][CTA], zero between calls
     uint32_t *err;
     uint64_t timeout_ns;
 };
@@ -56,6 +63,9 @@ struct GroupedParams {
 // rows of A and D; wgrad mode: rows of the contraction), tile coordinates.
 struct GroupUnit {
     int32_t g, row0, row1, tm, tn, k_blocks;
+    int32_t kb0, kb1;      // this worker's k-blocks of it
+    int32_t part, nparts;  // (part >= nparts: nothing to do)
+    int32_t tile;
 };
 
 // A warp's walk through the tiles in order.  Lane l holds group base + l:
@@ -110,26 +120,30 @@ __device__ __forceinline__ void walk_begin(const GroupedParams &p, GroupWalk &w)
 }
 
 // Tile t of the list (t never falls from call to call); false past the end.
+// Tile t / splits of the list and share t % splits of it (t never falls from
+// call to call); false past the end.
 template <int TILE_M, bool WGRAD>
 __device__ __forceinline__ bool walk_to(const GroupedParams &p, int64_t t64, GroupWalk &w, GroupUnit &u)
 {
+    u.part = 0;
+    if (p.splits > 1) {
+        u.part = static_cast<int32_t>(t64 % p.splits);
+        t64 /= p.splits;
+    }
+    if (t64 > INT32_MAX) return false;
+    const int32_t t = static_cast<int32_t>(t64);
+    u.tile = t;
+    int32_t r, tiles_m;
     if constexpr (WGRAD) {
-        const int64_t per = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-        if (t64 >= per * p.groups) return false;
-        u.g = static_cast<int32_t>(t64 / per);
-        const int32_t r = static_cast<int32_t>(t64 - u.g * per);
-        const int32_t strip = p.group_m * p.tiles_n;
-        const int32_t first = r / strip * p.group_m;
-        const int32_t rows = min(p.tiles_m - first, p.group_m);
-        u.tm = first + r % strip % rows;
-        u.tn = r % strip / rows;
+        tiles_m = p.tiles_m;
+        const int32_t per = tiles_m * p.tiles_n;
+        u.g = t / per;
+        if (u.g >= p.groups) return false;
+        r = t - u.g * per;
         u.row0 = max(0, min(__ldg(p.offsets + u.g), p.S));
         u.row1 = max(u.row0, min(__ldg(p.offsets + u.g + 1), p.S));
         u.k_blocks = (u.row1 - u.row0 + BK - 1) / BK;
-        return true;
     } else {
-        if (t64 > INT32_MAX) return false;
-        const int32_t t = static_cast<int32_t>(t64);
         while (t >= w.before + w.total) {
             if (w.base + 32 >= p.groups) return false;
             w.before += w.total;
@@ -141,16 +155,24 @@ __device__ __forceinline__ bool walk_to(const GroupedParams &p, int64_t t64, Gro
         u.row0 = __shfl_sync(0xffffffffu, w.lo, idx);
         u.row1 = __shfl_sync(0xffffffffu, w.hi, idx);
         const int32_t before = __shfl_sync(0xffffffffu, w.incl, idx > 0 ? idx - 1 : 0);
-        const int32_t r = at - (idx > 0 ? before : 0);
-        const int32_t tiles_m = (u.row1 - u.row0 + TILE_M - 1) / TILE_M;
-        const int32_t strip = p.group_m * p.tiles_n;
-        const int32_t first = r / strip * p.group_m;
-        const int32_t rows = min(tiles_m - first, p.group_m);
-        u.tm = first + r % strip % rows;
-        u.tn = r % strip / rows;
+        r = at - (idx > 0 ? before : 0);
+        tiles_m = (u.row1 - u.row0 + TILE_M - 1) / TILE_M;
         u.k_blocks = p.k_blocks;
-        return true;
     }
+    const int32_t strip = p.group_m * p.tiles_n;
+    const int32_t first = r / strip * p.group_m;
+    const int32_t in = r % strip, rows = min(tiles_m - first, p.group_m);
+    u.tm = first + in % rows;
+    u.tn = in / rows;
+    u.nparts = max(1, min(p.splits, u.k_blocks));
+    u.kb0 = 0;
+    u.kb1 = u.k_blocks;
+    if (p.splits > 1) {
+        const bool idle = u.part >= u.nparts;
+        u.kb0 = idle ? 0 : static_cast<int32_t>(static_cast<int64_t>(u.part) * u.k_blocks / u.nparts);
+        u.kb1 = idle ? 0 : static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * u.k_blocks / u.nparts);
+    }
+    return true;
 }
 
 // alpha, bias and activation on one thread's 32 columns of group g.
@@ -200,7 +222,7 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
     constexpr uint32_t EPI_BOX_BYTES = EPI_CHUNK * EPI_CHUNK * 4;  // 4 KB
     constexpr uint32_t EPI_WARPS_TOTAL = PAIR ? 8 : 4;
     constexpr uint32_t TMEM_ALLOC = static_cast<uint32_t>(G::TMEM_COLS);
-    static_assert(8 * (4 * STAGES + 5) + 16 <= G::BAR_BYTES, "barrier area");
+    static_assert(8 * (4 * STAGES + 5) + 24 <= G::BAR_BYTES, "barrier area");
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -218,7 +240,8 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
     const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (4 * STAGES + 5));
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
-    uint32_t *issued_slot = tmem_slot + 2;  // k-blocks this CTA's producer loaded; then a bit for
+    volatile int32_t *last_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 2);
+    uint32_t *issued_slot = tmem_slot + 4;  // k-blocks this CTA's producer loaded; then a bit for
                                             // each slot whose last load was a fringe
     auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
     auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
@@ -296,7 +319,7 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                 break;
             const int32_t m0 = (WGRAD ? 0 : w.row0) + w.tm * TILE_M + static_cast<int32_t>(rank) * BM;
             const int32_t n0 = w.tn * BN + static_cast<int32_t>(rank) * G::B_COLS;
-            for (int32_t kb = 0; kb < w.k_blocks; ++kb, ++it) {
+            for (int32_t kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const uint32_t s = it % STAGES;
                 const uint32_t ph = (it / STAGES) & 1u;
                 const int r = wait_bounded_warp(empty_bar(s), ph ^ 1u, wd);
@@ -374,7 +397,7 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             uint32_t it = 0, n = 0;
             bool ok = true;
             for (int64_t t = worker; ok && walk_to<TILE_M, WGRAD>(p, t, walk, w); t += n_workers) {
-                if (w.k_blocks == 0) continue;  // the epilogue writes the empty sum itself
+                if (w.kb0 == w.kb1) continue;  // the epilogue writes an empty sum itself
                 const uint32_t buf = n & 1u;
                 const uint32_t tph = (n >> 1) & 1u;
                 ++n;
@@ -385,7 +408,7 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + buf * BN;
-                for (int32_t kb = 0; kb < w.k_blocks; ++kb, ++it) {
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                     const uint32_t s = it % STAGES;
                     const uint32_t ph = (it / STAGES) & 1u;
                     r = wait_bounded_warp(full_bar(s), ph, wd);
@@ -402,7 +425,7 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                         for (int kk = 0; kk < BK / 16; ++kk) {
                             const uint64_t ad = a_desc0 | (((a_addr + kk * a_step) >> 4) & 0x3FFFu);
                             const uint64_t bd = b_desc0 | (((b_addr + kk * b_step) >> 4) & 0x3FFFu);
-                            const uint32_t acc = (kb > 0 || kk > 0) ? 1u : 0u;
+                            const uint32_t acc = (kb > w.kb0 || kk > 0) ? 1u : 0u;
                             if constexpr (PAIR)
                                 ptx::mma_bf16_pair(d_tmem, ad, bd, idesc, acc);
                             else
@@ -440,9 +463,10 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             uint32_t phase = 0;  // bit s: parity of the slot's next fringe
             const uint32_t pfix_leader0 = PAIR ? ptx::map_to_cta(pfix_bar(0), 0u) : 0u;
             for (int64_t t = worker; walk_to<TILE_M, WGRAD>(p, t, walk, w); t += n_workers) {
-                it += static_cast<uint32_t>(w.k_blocks);
+                it += static_cast<uint32_t>(w.kb1 - w.kb0);
                 const int32_t tail = (w.row1 - w.row0) % BK;
-                if (tail == 0) continue;  // also an empty group
+                // (no tail: also an empty group; the fringe is in the last share)
+                if (tail == 0 || w.kb0 == w.kb1 || w.kb1 != w.k_blocks) continue;
                 const uint32_t s = (it - 1) % STAGES;
                 int r = wait_bounded_warp(fringe_bar(s), (phase >> s) & 1u, wd);
                 if (r != WAIT_OK) {
@@ -522,36 +546,63 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                 return;
             }
             __syncwarp();
-            if (!p.out_bf16) {
+            // Plain stores, read back from the box.  Rows of D on 16 bytes: 16
+            // at a time (a group's last rows take this path); else an element
+            // a lane, eight rows a step.
+            const int32_t cols = min(EPI_CHUNK, p.N - col0);
+            if (p.epi_tma) {
+                const int eb = p.out_bf16 ? 2 : 4;
+                const int upr = p.out_bf16 ? 4 : 8;  // 16-byte units of a box row
+                const int u = lane & (upr - 1), rstep = 32 / upr;
+                const int per = 16 / eb;
+                uint8_t *dst = static_cast<uint8_t *>(p.D) + (at - lane + u * per) * eb;
+                const int n = min(per, cols - u * per);  // elements of this unit
+#pragma unroll 1
+                for (int r = lane / upr; r < nrows; r += rstep) {
+                    const uint32_t src = p.out_bf16 ? box + r * 64 + ((u ^ ((r >> 1) & 3)) << 4) : box + r * 128 + ((u ^ (r & 7)) << 4);
+                    uint32_t v[4];
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(src) : "memory");
+                    uint8_t *q = dst + static_cast<int64_t>(r) * p.ldd * eb;
+                    if (n == per) {
+                        *reinterpret_cast<uint4 *>(q) = make_uint4(v[0], v[1], v[2], v[3]);
+                    } else if (p.out_bf16) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (e < n) reinterpret_cast<uint16_t *>(q)[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (e < n) reinterpret_cast<uint32_t *>(q)[e] = v[e];
+                    }
+                }
+            } else if (!p.out_bf16) {
                 const uint32_t src = box + ((lane >> 2) << 4) + ((lane & 3) << 2);
                 float *dst = static_cast<float *>(p.D) + at;
 #pragma unroll 1
-                for (int r0 = 0; r0 < nrows; r0 += 8) {
+                for (int r0 = 0; r0 < nrows; r0 += 8, dst += 8 * p.ldd) {
                     float vals[8];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) vals[r] = ld_shared_f32((src ^ (((r0 + r) & 7) << 4)) + (r0 + r) * 128);
-                    if (col < p.N) {
+                    for (int r = 0; r < 8; ++r) vals[r] = ld_shared_f32((src ^ (r << 4)) + (r0 + r) * 128);
+                    float *q = dst;
 #pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            if (r0 + r < nrows) dst[static_cast<int64_t>(r0 + r) * p.ldd] = vals[r];
-                    }
+                    for (int r = 0; r < 8; ++r, q += p.ldd)
+                        if (r0 + r < nrows && lane < cols) *q = vals[r];
                 }
             } else {
                 const uint32_t src = box + ((lane >> 3) << 4) + ((lane & 7) << 1);
                 uint16_t *dst = static_cast<uint16_t *>(p.D) + at;
 #pragma unroll 1
-                for (int r0 = 0; r0 < nrows; r0 += 8) {
+                for (int r0 = 0; r0 < nrows; r0 += 8, dst += 8 * p.ldd) {
                     uint16_t vals[8];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        vals[r] = ld_shared_u16((src ^ ((((r0 + r) >> 1) & 3) << 4)) + (r0 + r) * 64);
-                    if (col < p.N) {
+                    for (int r = 0; r < 8; ++r) vals[r] = ld_shared_u16((src ^ (((r >> 1) & 3) << 4)) + (r0 + r) * 64);
+                    uint16_t *q = dst;
 #pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            if (r0 + r < nrows) dst[static_cast<int64_t>(r0 + r) * p.ldd] = vals[r];
-                    }
+                    for (int r = 0; r < 8; ++r, q += p.ldd)
+                        if (r0 + r < nrows && lane < cols) *q = vals[r];
                 }
             }
+            __syncwarp();  // the box may be written again
         };
         auto release_tmem = [&](uint32_t buf) {
             ptx::tc_fence_before();
@@ -573,6 +624,7 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             const bool whole = row0 + 32 <= limit || limit == (WGRAD ? p.M : p.S);
             const int32_t col0 = w.tn * BN;
             uint32_t va[32], vb[32];
+            if (w.part >= w.nparts) continue;
             if (w.k_blocks == 0) {  // the empty sum
 #pragma unroll 1
                 for (int c = 0; c < NCH; ++c) {
@@ -590,6 +642,65 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             if (!epi_all(r == WAIT_OK)) break;
             ptx::tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
+            if (w.nparts > 1) {
+                // The partial tile -> scratch [chunk][column quad][row][4
+                // columns]: 16 coalesced bytes a thread.
+                constexpr int64_t PART4 = BM * BN / 4;  // float4s a part
+                const int64_t half = static_cast<int64_t>(w.tile) * (PAIR ? 2 : 1) + rank;
+                float4 *parts = reinterpret_cast<float4 *>(p.partials) + half * p.splits * PART4 + q * 32 + lane;
+                float4 *mine = parts + w.part * PART4;
+#pragma unroll 1
+                for (int c = 0; c < NCH; ++c) {
+                    ptx::tmem_load_32cols(taddr + c * EPI_CHUNK, va);
+                    if (c == NCH - 1) release_tmem(buf);
+                    if (row0 < limit) {
+#pragma unroll
+                        for (int j4 = 0; j4 < 8; ++j4)
+                            __stcg(mine + (c * 8 + j4) * BM,
+                                   make_float4(__uint_as_float(va[4 * j4]), __uint_as_float(va[4 * j4 + 1]),
+                                               __uint_as_float(va[4 * j4 + 2]), __uint_as_float(va[4 * j4 + 3])));
+                    }
+                }
+                __threadfence();
+                ptx::named_barrier_sync(1, 128);
+                if (warp == 2 && lane == 0) {
+                    const int32_t old = atomicAdd(p.counters + half, 1);
+                    *last_flag = old == w.nparts - 1 ? 1 : 0;
+                    if (old == w.nparts - 1) atomicExch(p.counters + half, 0);  // ready for the next call
+                }
+                ptx::named_barrier_sync(1, 128);
+                if (*last_flag) {
+                    __threadfence();
+#pragma unroll 1
+                    for (int c = 0; c < NCH; ++c) {
+                        if (row0 >= limit || col0 + c * EPI_CHUNK >= p.N) break;  // warp-uniform
+                        float4 acc[8];
+#pragma unroll
+                        for (int j4 = 0; j4 < 8; ++j4) acc[j4] = __ldcg(parts + (c * 8 + j4) * BM);
+#pragma unroll 2
+                        for (int s = 1; s < w.nparts; ++s) {
+                            float4 t4[8];
+#pragma unroll
+                            for (int j4 = 0; j4 < 8; ++j4) t4[j4] = __ldcg(parts + s * PART4 + (c * 8 + j4) * BM);
+#pragma unroll
+                            for (int j4 = 0; j4 < 8; ++j4) {
+                                acc[j4].x += t4[j4].x; acc[j4].y += t4[j4].y;
+                                acc[j4].z += t4[j4].z; acc[j4].w += t4[j4].w;
+                            }
+                        }
+#pragma unroll
+                        for (int j4 = 0; j4 < 8; ++j4) {
+                            va[4 * j4] = __float_as_uint(acc[j4].x);
+                            va[4 * j4 + 1] = __float_as_uint(acc[j4].y);
+                            va[4 * j4 + 2] = __float_as_uint(acc[j4].z);
+                            va[4 * j4 + 3] = __float_as_uint(acc[j4].w);
+                        }
+                        store_chunk(va, row0, limit, whole, col0 + c * EPI_CHUNK, w.g);
+                    }
+                }
+                ptx::named_barrier_sync(1, 128);  // the flag may be written again
+                continue;
+            }
             ptx::tmem_load_32cols(taddr, va);
 #pragma unroll 1
             for (int c = 0; c < NCH; c += 2) {

@@ -1001,6 +1001,14 @@ tg_status host_arena(const HostStream &hs, size_t bytes, void **out)
     return st;
 }
 
+tg_status host_counters(const HostStream &hs, size_t bytes, int32_t **out)
+{
+    Workspace &w = workspace_for(hs.dev, hs.stream);
+    const tg_status st = ensure_counters(w, bytes, hs.stream);
+    *out = w.counters;
+    return st;
+}
+
 bool host_encode_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
                     uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1, CUtensorMapSwizzle swz)
 {

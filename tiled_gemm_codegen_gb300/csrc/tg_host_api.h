@@ -30,6 +30,10 @@ tg_status host_stream(cudaStream_t stream, HostStream *out);
 // of earlier calls are stale; later calls on the stream reuse it).
 tg_status host_arena(const HostStream &hs, size_t bytes, void **out);
 
+// At least `bytes` of the stream's arrival counters, all zero (their kernel
+// leaves them so; tg_device_error resets them after an abort).
+tg_status host_counters(const HostStream &hs, size_t bytes, int32_t **out);
+
 tg_status host_cuda_status(cudaError_t e);
 
 // A rank-3 tensor map (dim0 contiguous, dim1 rows, dim2 problems; strides in

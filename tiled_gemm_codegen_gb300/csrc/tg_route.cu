@@ -811,43 +811,131 @@ __global__ void __launch_bounds__(512) combine_grad_aligned_kernel(const GradArg
     zero_tail(a);
 }
 
-// The same for any type, pitch and alignment: one row of dys at a time.
+// The same with a warp a token, for short rows (a block a token would be mostly
+// its own start and barriers).
+constexpr int GRAD_WARP_CHUNKS = 64;
+
+template <int KB>
+__global__ void __launch_bounds__(256) combine_grad_warp_kernel(const GradArgs a)
+{
+    constexpr int LB = KB < 4 ? KB : 4;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (t < a.T) {
+        const uint16_t *dy = static_cast<const uint16_t *>(a.dy) + t * a.ld_dy;
+        for (int j0 = 0; j0 < a.k; j0 += KB) {
+            int32_t sl = -1;
+            float wl = 1.0f;
+            if (lane < KB && j0 + lane < a.k) {
+                sl = a.slot[t * a.k + j0 + lane];
+                if (sl >= a.S) sl = -1;
+                if (a.weights) wl = a.weights[t * a.ld_w + j0 + lane];
+            }
+            int32_t s[KB];
+            float w[KB], dot[KB];
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                s[j] = __shfl_sync(0xffffffffu, sl, j);
+                w[j] = __shfl_sync(0xffffffffu, wl, j);
+                dot[j] = 0.0f;
+            }
+            for (int32_t c = lane; c < a.chunks; c += 32) {
+                float g[8];
+                Raw8<true> d;
+                d.load(dy, c * 8);
+                uint4 raw[LB];
+#pragma unroll
+                for (int jb = 0; jb < KB; jb += LB) {
+                    if (a.dw) {
+#pragma unroll
+                        for (int j = 0; j < LB; ++j)
+                            if (s[jb + j] >= 0)
+                                raw[j] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.ys) +
+                                                                               s[jb + j] * a.ld_ys + c * 8));
+                    }
+                    if (jb == 0) d.get(g);
+#pragma unroll
+                    for (int j = 0; j < LB; ++j) {
+                        if (s[jb + j] < 0) continue;
+                        float o[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = w[jb + j] * g[i];
+                        store8_aligned<true>(static_cast<uint16_t *>(a.dys) + s[jb + j] * a.ld_dys, c * 8, o);
+                        if (a.dw) {
+                            float v[8];
+                            unpack8(raw[j], v);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) dot[jb + j] = fmaf(g[i], v[i], dot[jb + j]);
+                        }
+                    }
+                }
+            }
+            if (a.dw) {
+                float mine = 0.0f;
+#pragma unroll
+                for (int j = 0; j < KB; ++j) {
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
+                    if (lane == j) mine = dot[j];
+                }
+                if (lane < KB && j0 + lane < a.k) a.dw[t * a.ld_dw + j0 + lane] = mine;
+            }
+        }
+    }
+    zero_tail(a);
+}
+
+// The same for any type, pitch and alignment: one row of dys at a time, by a
+// warp (short rows) or a block.
+template <bool WARP>
 __global__ void __launch_bounds__(512) combine_grad_any_kernel(const GradArgs a)
 {
     __shared__ float part[16][1];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int64_t t = blockIdx.x;
-    const uint8_t *dy = row_of(a.dy, t, a.ld_dy, a.dy_bf16);
-    const uint8_t *dy_lo = static_cast<const uint8_t *>(a.dy);
-    const uint8_t *dy_hi = row_of(a.dy, a.T - 1, a.ld_dy, a.dy_bf16) + a.D * (a.dy_bf16 ? 2 : 4);
-    const uint8_t *ys_lo = static_cast<const uint8_t *>(a.ys);
-    const uint8_t *ys_hi = a.ys ? row_of(a.ys, a.S - 1, a.ld_ys, a.ys_bf16) + a.D * (a.ys_bf16 ? 2 : 4) : nullptr;
-    for (int j = 0; j < a.k; ++j) {
-        const int32_t s = a.slot[t * a.k + j];
-        float dot[1] = {0.0f};
-        if (s >= 0 && s < a.S) {
-            const float w = a.weights ? a.weights[t * a.ld_w + j] : 1.0f;
-            uint8_t *out = const_cast<uint8_t *>(row_of(a.dys, s, a.ld_dys, a.dys_bf16));
-            const int64_t lead = lead_of(out, a.dys_bf16);
-            for (int64_t c = threadIdx.x; c * 8 - lead < a.D; c += blockDim.x) {
-                const int64_t e0 = c * 8 - lead;
-                float g[8], o[8];
-                load8_any(dy, a.dy_bf16, e0, a.D, dy_lo, dy_hi, g);
-                if (a.dw) {
-                    float v[8];
-                    load8_any(row_of(a.ys, s, a.ld_ys, a.ys_bf16), a.ys_bf16, e0, a.D, ys_lo, ys_hi, v);
+    const int64_t t = WARP ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t first = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
+    if (t < a.T) {
+        const uint8_t *dy = row_of(a.dy, t, a.ld_dy, a.dy_bf16);
+        const uint8_t *dy_lo = static_cast<const uint8_t *>(a.dy);
+        const uint8_t *dy_hi = row_of(a.dy, a.T - 1, a.ld_dy, a.dy_bf16) + a.D * (a.dy_bf16 ? 2 : 4);
+        const uint8_t *ys_lo = static_cast<const uint8_t *>(a.ys);
+        const uint8_t *ys_hi = a.ys ? row_of(a.ys, a.S - 1, a.ld_ys, a.ys_bf16) + a.D * (a.ys_bf16 ? 2 : 4) : nullptr;
+        for (int j = 0; j < a.k; ++j) {
+            const int32_t s = a.slot[t * a.k + j];
+            float dot[1] = {0.0f};
+            if (s >= 0 && s < a.S) {
+                const float w = a.weights ? a.weights[t * a.ld_w + j] : 1.0f;
+                uint8_t *out = const_cast<uint8_t *>(row_of(a.dys, s, a.ld_dys, a.dys_bf16));
+                const int64_t lead = lead_of(out, a.dys_bf16);
+                for (int64_t c = first; c * 8 - lead < a.D; c += step) {
+                    const int64_t e0 = c * 8 - lead;
+                    float g[8], o[8];
+                    load8_any(dy, a.dy_bf16, e0, a.D, dy_lo, dy_hi, g);
+                    if (a.dw) {
+                        float v[8];
+                        load8_any(row_of(a.ys, s, a.ld_ys, a.ys_bf16), a.ys_bf16, e0, a.D, ys_lo, ys_hi, v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dot[0] = fmaf(g[i], v[i], dot[0]);
+                        for (int i = 0; i < 8; ++i) dot[0] = fmaf(g[i], v[i], dot[0]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = w * g[i];
+                    store8_any(out, a.dys_bf16, e0, a.D, o);
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = w * g[i];
-                store8_any(out, a.dys_bf16, e0, a.D, o);
             }
-        }
-        if (a.dw) {
-            const float sum = block_sums<1>(dot, part);
-            if (threadIdx.x == 0) a.dw[t * a.ld_dw + j] = sum;
+            if (a.dw) {
+                if constexpr (WARP) {
+                    __syncwarp();
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], d);
+                    if (first == 0) a.dw[t * a.ld_dw + j] = dot[0];
+                } else {
+                    const float sum = block_sums<1>(dot, part);
+                    if (threadIdx.x == 0) a.dw[t * a.ld_dw + j] = sum;
+                }
+            }
         }
     }
     zero_tail(a);
@@ -1203,16 +1291,21 @@ TG_API tg_status tg_expert_combine_grad(const void *dy, int64_t ld_dy, int32_t d
         // suffice, else turns of 256
         int threads = a.chunks <= 512 ? static_cast<int>((a.chunks + 31) / 32 * 32) : 256;
         if (threads < 32) threads = 32;
-        const dim3 grid(static_cast<unsigned>(T));
+        const dim3 grid(static_cast<unsigned>(T)), warps(static_cast<unsigned>((T + 7) / 8));
+        const bool narrow = a.chunks <= GRAD_WARP_CHUNKS;
         cudaError_t e;
         if (!aligned)
-            e = launch(combine_grad_any_kernel, grid, threads, 0, stream, 1, a);
+            e = narrow ? launch(combine_grad_any_kernel<true>, warps, 256, 0, stream, 1, a)
+                       : launch(combine_grad_any_kernel<false>, grid, threads, 0, stream, 1, a);
         else if (k <= 2)
-            e = launch(combine_grad_aligned_kernel<2>, grid, threads, 0, stream, 1, a);
+            e = narrow ? launch(combine_grad_warp_kernel<2>, warps, 256, 0, stream, 1, a)
+                       : launch(combine_grad_aligned_kernel<2>, grid, threads, 0, stream, 1, a);
         else if (k <= 4)
-            e = launch(combine_grad_aligned_kernel<4>, grid, threads, 0, stream, 1, a);
+            e = narrow ? launch(combine_grad_warp_kernel<4>, warps, 256, 0, stream, 1, a)
+                       : launch(combine_grad_aligned_kernel<4>, grid, threads, 0, stream, 1, a);
         else
-            e = launch(combine_grad_aligned_kernel<8>, grid, threads, 0, stream, 1, a);
+            e = narrow ? launch(combine_grad_warp_kernel<8>, warps, 256, 0, stream, 1, a)
+                       : launch(combine_grad_aligned_kernel<8>, grid, threads, 0, stream, 1, a);
         return host_cuda_status(e);
     });
 }
