@@ -176,18 +176,23 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     tg_status st = host_stream(stream, &hs);
     if (st != TG_OK) return st;
 
-    // Tiles: pairs (256 x 256) where the groups' rows fill them, else one
-    // CTA's 128 x 128.
+    // Tiles.  wgrad: pairs (256 x 256) where they fill half the SMs, else one
+    // CTA's 128 x 128.  Rows: 256 of a group by 256 columns for a pair where
+    // groups have that many on average and the tiles fill half the SMs; else
+    // one CTA's 128 columns by 128 rows, or 32 where groups have few (the ring
+    // is then deeper: weights are the traffic).
+    const int64_t hit = groups < S ? groups : S;  // groups that have rows, at most
     bool pair;
     if (wgrad)
         pair = M > 128 && N > 128 && groups * cdiv(M, 256) * cdiv(N, 256) >= hs.sms / 2;
     else
         pair = N > 128 && S >= 192 * groups && cdiv(S, 256) * cdiv(N, 256) >= hs.sms / 2;
     if (opt && opt->cta_pair) pair = opt->cta_pair == 2;
-    const int64_t tile_m = pair ? 256 : 128, bn = pair ? 256 : 128;
-    const int64_t tiles_n = cdiv(N, bn);
+    const bool few = !wgrad && !pair && S <= 32 * hit;
+    const int64_t tile_m = pair ? 256 : 128, bn = pair ? 256 : few ? 32 : 128;
+    const int64_t tiles_n = cdiv(N, wgrad ? bn : tile_m);
     const int64_t tiles_m = cdiv(M, tile_m);
-    const int64_t row_tiles = S / tile_m + (groups < S ? groups : S);  // at most, over all groups
+    const int64_t row_tiles = S / bn + hit;  // rows mode: at most, over all groups
     const int64_t units = wgrad ? groups * tiles_m * tiles_n : row_tiles * tiles_n;
     if (units > INT32_MAX) return TG_ERR_UNSUPPORTED;
 
@@ -238,8 +243,10 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
         a.pack = force || !tma_ok(a.p, a.ld, 0, 2);
         b.pack = force || !tma_ok(b.p, b.ld, b.nb > 1 ? b.stride : 0, 2);
         if ((st = realign(hs, a, b, part_bytes, &p.partials)) != TG_OK) return st;
-        const uint32_t a_box1 = wgrad ? BK : BM;
-        const uint32_t b_box1 = b_k ? static_cast<uint32_t>(pair ? bn / 2 : bn) : BK;
+        // rows mode: A is the MMA's N operand (this CTA's rows x 64 k), B[g] its
+        // M operand (64 k x 64 columns, or 128 columns x 64 k)
+        const uint32_t a_box1 = wgrad ? BK : static_cast<uint32_t>(pair ? bn / 2 : bn);
+        const uint32_t b_box1 = b_k ? BM : BK;
         if (!host_encode_3d(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.p, a.cols, a.rows, a.nb, a.ld * 2, problem_stride(a), 64,
                             a_box1, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !host_encode_3d(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b.p, b.cols, b.rows, b.nb, b.ld * 2, problem_stride(b), 64,
@@ -248,17 +255,19 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     }
     if (tma_ok(D, ldd, wgrad && groups > 1 ? strideD : 0, eb)) {
         const Operand d{D, wgrad ? M : S, N, ldd, wgrad ? groups : 1, strideD};
+        const EpiBox box = epi_box(wgrad, out_bf16);
         const uint64_t s2 = static_cast<uint64_t>(d.nb > 1 ? strideD * eb : cdiv(d.rows * ldd * eb, 16) * 16);
         p.epi_tma = host_encode_3d(&td, out_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, D, d.cols,
-                                   d.rows, d.nb, ldd * eb, s2, EPI_CHUNK, EPI_CHUNK,
-                                   out_bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)
+                                   d.rows, d.nb, ldd * eb, s2, static_cast<uint32_t>(box.row_bytes / eb),
+                                   static_cast<uint32_t>(box.rows),
+                                   box.row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)
                         ? 1
                         : 0;
     }
-    static const Shape shapes[4] = {shape<128, 6, false, false>(), shape<256, 6, true, false>(),
-                                    shape<128, 6, false, true>(), shape<256, 6, true, true>()};
-    static ShapeState states[4];
-    const int which = (wgrad ? 2 : 0) + (pair ? 1 : 0);
+    static const Shape shapes[5] = {shape<128, 6, false, false>(), shape<256, 6, true, false>(),
+                                    shape<128, 6, false, true>(), shape<256, 6, true, true>(), shape<32, 9, false, false>()};
+    static ShapeState states[5];
+    const int which = few ? 4 : (wgrad ? 2 : 0) + (pair ? 1 : 0);
     if (splits > 1 && (st = host_counters(hs, static_cast<size_t>(part_tiles) * 4, &p.counters)) != TG_OK) return st;
     return host_cuda_status(launch_shape(shapes[which], states[which], hs, units * splits, ta, tb, td, p));
 }

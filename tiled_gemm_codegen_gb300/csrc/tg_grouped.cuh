@@ -1,10 +1,15 @@
 // Persistent, warp-specialised grouped GEMM for sm_103a: one product per
 // group of consecutive rows, the groups' bounds on the device.
 //
-//   rows mode    D[s][:] = act(alpha * A[s][:] B[g] + bias[g]) for the rows s of group g: M is
-//                ragged.  A tile holds rows of one group only; it starts at any
-//                row (a TMA box may), the rows past the group's end are loaded but
-//                never stored (a row of D depends on its own row of A alone).
+//   rows mode    D[s][:] = act(alpha * A[s][:] B[g] + bias[g]) for the rows s of group g: the rows
+//                are ragged.  The tile is computed transposed - the columns of B[g] are the
+//                MMA's M (256 or 128 of them), the rows of A its N - because N is a field
+//                of each instruction: a group's last tile takes as many rows as are left,
+//                rounded up to 32, where an M of 256 would compute 128 rows of padding a
+//                group on average (uneven groups of 1024 rows, 2048 x 4096: an eighth
+//                of the work).  A tile's box of A may start at any row; rows past the
+//                group's end are loaded but never stored (a row of D depends on its
+//                own row of A alone).
 //   wgrad mode   D[g] = alpha * A[rows g]^T B[rows g]: the contraction is ragged.  Both operands
 //                are read as stored (MN-major), 64 rows a k-block; the rows past the
 //                group's end in its last k-block (its fringe) belong to the next
@@ -15,9 +20,12 @@
 //                in the producer's place, so the MMA's own wait is one and the same.
 //
 // Roles, rings and the bounded waits are those of gemm_kernel (tg_kernel.cuh):
-// warp 0 loads, warp 1 issues tcgen05.mma, warps 2..5 drain tensor memory;
-// wgrad mode adds warp 6, the fixer, which runs as far ahead of the MMA as
-// the ring allows.  PAIR: a cluster of two CTAs computes 256 x BN.
+// warp 0 loads, warp 1 issues tcgen05.mma, warps 2..9 drain tensor memory;
+// wgrad mode adds warp 10, the fixer, which runs as far ahead of the MMA as
+// the ring allows.  PAIR: a cluster of two CTAs computes one tile, each half
+// of its M, and loads half of its N.  Eight warps drain (two for each lane
+// quadrant, taking boxes in turn) because short contractions leave little but
+// the stores to do: 4 KB boxes, one in flight a warp, outrun HBM.
 //
 // Where there are fewer tiles than workers, `splits` of them share a tile's
 // contraction: each writes its fp32 partial tile to scratch, and the last to
@@ -40,9 +48,9 @@ struct GroupedParams {
     int32_t M;               // wgrad mode: rows of D[g] (columns of A)
     int32_t N, K;            // K: rows mode only
     int32_t k_blocks;        // rows mode: ceil(K / BK)
-    int32_t tiles_m;         // wgrad mode
-    int32_t tiles_n;
-    int32_t group_m;         // row tiles a raster strip
+    int32_t tiles_m;         // wgrad mode: tiles of M
+    int32_t tiles_n;         // tiles of D's columns
+    int32_t group_m;         // tiles of rows a raster strip
     int32_t b_k;             // rows mode: 1 = B stored N x K
     int32_t b_shared;        // rows mode: 1 = every group has the same B
     int32_t epi_tma;
@@ -81,7 +89,7 @@ struct GroupWalk {
     int32_t last;      // the bound before the next chunk
 };
 
-template <int TILE_M>
+template <int TILE_R>  // rows of A a tile takes
 __device__ __forceinline__ void walk_load(const GroupedParams &p, int32_t base, GroupWalk &w)
 {
     const int lane = static_cast<int>(threadIdx.x & 31);
@@ -96,7 +104,7 @@ __device__ __forceinline__ void walk_load(const GroupedParams &p, int32_t base, 
     }
     int32_t lo = __shfl_up_sync(0xffffffffu, hi, 1);
     if (lane == 0) lo = w.last;
-    const int32_t units = g < p.groups ? (hi - lo + TILE_M - 1) / TILE_M * p.tiles_n : 0;
+    const int32_t units = g < p.groups ? (hi - lo + TILE_R - 1) / TILE_R * p.tiles_n : 0;
     int32_t incl = units;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -111,18 +119,18 @@ __device__ __forceinline__ void walk_load(const GroupedParams &p, int32_t base, 
     w.last = __shfl_sync(0xffffffffu, hi, 31);
 }
 
-template <int TILE_M, bool WGRAD>
+template <int TILE_R, bool WGRAD>
 __device__ __forceinline__ void walk_begin(const GroupedParams &p, GroupWalk &w)
 {
     w.before = 0;
     w.last = max(0, min(__ldg(p.offsets), p.S));
-    if constexpr (!WGRAD) walk_load<TILE_M>(p, 0, w);
+    if constexpr (!WGRAD) walk_load<TILE_R>(p, 0, w);
 }
 
 // Tile t of the list (t never falls from call to call); false past the end.
 // Tile t / splits of the list and share t % splits of it (t never falls from
 // call to call); false past the end.
-template <int TILE_M, bool WGRAD>
+template <int TILE_R, bool WGRAD>
 __device__ __forceinline__ bool walk_to(const GroupedParams &p, int64_t t64, GroupWalk &w, GroupUnit &u)
 {
     u.part = 0;
@@ -147,7 +155,7 @@ __device__ __forceinline__ bool walk_to(const GroupedParams &p, int64_t t64, Gro
         while (t >= w.before + w.total) {
             if (w.base + 32 >= p.groups) return false;
             w.before += w.total;
-            walk_load<TILE_M>(p, w.base + 32, w);
+            walk_load<TILE_R>(p, w.base + 32, w);
         }
         const int32_t at = t - w.before;
         const int idx = __popc(__ballot_sync(0xffffffffu, at >= w.incl));
@@ -156,7 +164,7 @@ __device__ __forceinline__ bool walk_to(const GroupedParams &p, int64_t t64, Gro
         u.row1 = __shfl_sync(0xffffffffu, w.hi, idx);
         const int32_t before = __shfl_sync(0xffffffffu, w.incl, idx > 0 ? idx - 1 : 0);
         r = at - (idx > 0 ? before : 0);
-        tiles_m = (u.row1 - u.row0 + TILE_M - 1) / TILE_M;
+        tiles_m = (u.row1 - u.row0 + TILE_R - 1) / TILE_R;
         u.k_blocks = p.k_blocks;
     }
     const int32_t strip = p.group_m * p.tiles_n;
@@ -175,17 +183,24 @@ __device__ __forceinline__ bool walk_to(const GroupedParams &p, int64_t t64, Gro
     return true;
 }
 
-// alpha, bias and activation on one thread's 32 columns of group g.
-__device__ __forceinline__ void grouped_epilogue(const GroupedParams &p, uint32_t (&v)[32], int32_t col0, int32_t g)
+// rows mode: the MMA's N for a tile, its rows rounded up to 32 (16 a CTA of a
+// pair).
+template <int BN>
+__device__ __forceinline__ int32_t rows_n(const GroupUnit &u)
+{
+    return min(BN, (u.row1 - u.row0 - u.tm * BN + 31) / 32 * 32);
+}
+
+// alpha, bias and activation on 32 values (of one column of D in rows mode,
+// whose bias is `bias`).
+__device__ __forceinline__ void grouped_epilogue(const GroupedParams &p, uint32_t (&v)[32], float bias)
 {
     float x[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) x[j] = __fmul_rn(p.alpha, __uint_as_float(v[j]));
     if (p.bias) {
-        const float *bp = p.bias + static_cast<int64_t>(g) * p.bias_stride + col0;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (col0 + j < p.N) x[j] = __fadd_rn(x[j], __ldg(bp + j));
+        for (int j = 0; j < 32; ++j) x[j] = __fadd_rn(x[j], bias);
     }
     switch (p.act) {
         case 1:
@@ -207,8 +222,36 @@ __device__ __forceinline__ void grouped_epilogue(const GroupedParams &p, uint32_
     for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(x[j]);
 }
 
-constexpr int GROUPED_THREADS = 192;        // rows mode
-constexpr int GROUPED_WGRAD_THREADS = 224;  // and the fixer warp
+// All 256 epilogue threads agree on a predicate (named barrier 1).
+__device__ __forceinline__ bool grouped_epi_all(bool pred)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(pred))
+        : "memory");
+    return r != 0;
+}
+
+constexpr int GROUPED_EPI_WARPS = 8;
+// A box of D in shared memory: 4 KB, `rows` of row_bytes with the swizzle of
+// that width.
+struct EpiBox {
+    int rows, row_bytes;
+};
+// rows mode: 32 columns of 32 fp32 or 64 bf16 rows; wgrad mode: 32 rows of 32
+// fp32 or 64 bf16 columns.
+__host__ __device__ constexpr EpiBox epi_box(bool wgrad, bool bf16)
+{
+    return wgrad ? EpiBox{32, 128} : bf16 ? EpiBox{64, 64} : EpiBox{32, 128};
+}
+
+constexpr int GROUPED_THREADS = 64 + 32 * GROUPED_EPI_WARPS;  // rows mode
+constexpr int GROUPED_WGRAD_THREADS = GROUPED_THREADS + 32;   // and the fixer warp
 
 template <int BN, int STAGES, bool PAIR, bool WGRAD>
 __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREADS, 1)
@@ -216,11 +259,14 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                    const __grid_constant__ CUtensorMap tmD, const GroupedParams p)
 {
     using G = Geometry<BN, PAIR>;
-    constexpr int TILE_M = PAIR ? 2 * BM : BM;
+    constexpr int TILE_M = PAIR ? 2 * BM : BM;  // the MMA's M
+    constexpr int TILE_R = WGRAD ? TILE_M : BN; // rows of D a tile takes
     constexpr int B_BOXES = G::B_COLS / 64;
     constexpr uint32_t BOX_BYTES = BK * 64 * 2;                    // 64 k x 64 columns, 8 KB
     constexpr uint32_t EPI_BOX_BYTES = EPI_CHUNK * EPI_CHUNK * 4;  // 4 KB
-    constexpr uint32_t EPI_WARPS_TOTAL = PAIR ? 8 : 4;
+    constexpr uint32_t EPI_WARPS_TOTAL = (PAIR ? 2 : 1) * GROUPED_EPI_WARPS;
+    static_assert(GROUPED_EPI_WARPS * EPI_BOX_BYTES <= G::EPI_BYTES, "epilogue boxes");
+    static_assert(!WGRAD || BN % 64 == 0, "wgrad mode loads 64-column boxes");
     constexpr uint32_t TMEM_ALLOC = static_cast<uint32_t>(G::TMEM_COLS);
     static_assert(8 * (4 * STAGES + 5) + 24 <= G::BAR_BYTES, "barrier area");
 
@@ -303,7 +349,7 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
 
     GroupWalk walk;
     GroupUnit w;
-    walk_begin<TILE_M, WGRAD>(p, walk);
+    walk_begin<TILE_R, WGRAD>(p, walk);
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
@@ -312,13 +358,20 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
         bool ok = true;
         const uint32_t full0 = PAIR ? ptx::map_to_cta(full_bar(0), 0u) : full_bar(0);
         const uint32_t fringe0 = PAIR ? ptx::map_to_cta(fringe_bar(0), rank) : fringe_bar(0);
-        for (int64_t t = worker; ok && walk_to<TILE_M, WGRAD>(p, t, walk, w); t += n_workers) {
+        for (int64_t t = worker; ok && walk_to<TILE_R, WGRAD>(p, t, walk, w); t += n_workers) {
             if (!dbg_ok(w.g >= 0 && w.g < p.groups && w.row0 >= 0 && w.row0 <= w.row1 && w.row1 <= p.S && w.tm >= 0 &&
                             w.tn >= 0 && w.tn < p.tiles_n,
                         CHK_UNIT, wd))
                 break;
-            const int32_t m0 = (WGRAD ? 0 : w.row0) + w.tm * TILE_M + static_cast<int32_t>(rank) * BM;
-            const int32_t n0 = w.tn * BN + static_cast<int32_t>(rank) * G::B_COLS;
+            // this CTA's part of the MMA's M and N operands
+            int32_t m0, n0;
+            if constexpr (WGRAD) {
+                m0 = w.tm * TILE_M + static_cast<int32_t>(rank) * BM;
+                n0 = w.tn * BN + static_cast<int32_t>(rank) * G::B_COLS;
+            } else {
+                m0 = w.tn * TILE_M + static_cast<int32_t>(rank) * BM;
+                n0 = w.row0 + w.tm * BN + static_cast<int32_t>(rank) * (rows_n<BN>(w) / 2);
+            }
             for (int32_t kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const uint32_t s = it % STAGES;
                 const uint32_t ph = (it / STAGES) & 1u;
@@ -360,13 +413,14 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
 #pragma unroll
                         for (int j = 0; j < B_BOXES; ++j) load(b_dst + j * BOX_BYTES, &tmB, n0 + 64 * j, k0, 0);
                     } else {
-                        load(a_dst, &tmA, kb * BK, m0, 0);
-                        if (!p.b_k) {
-#pragma unroll
-                            for (int j = 0; j < B_BOXES; ++j) load(b_dst + j * BOX_BYTES, &tmB, n0 + 64 * j, kb * BK, p.b_shared ? 0 : w.g);
-                        } else {
-                            load(b_dst, &tmB, kb * BK, n0, p.b_shared ? 0 : w.g);
+                        const int32_t z = p.b_shared ? 0 : w.g;
+                        if (!p.b_k) {  // B[g] is K x N: 64 k x 64 columns, twice
+                            load(a_dst, &tmB, m0, kb * BK, z);
+                            load(a_dst + BOX_BYTES, &tmB, m0 + 64, kb * BK, z);
+                        } else {  // stored N x K: 128 columns x 64 k
+                            load(a_dst, &tmB, kb * BK, m0, z);
                         }
+                        load(b_dst, &tmA, kb * BK, n0, 0);
                     }
                 }
                 __syncwarp();
@@ -389,14 +443,15 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
     } else if (warp == 1) {
         if (!PAIR || leader) {
             // ------------------------------------------------ MMA issuer
-            const uint32_t idesc = instr_desc_bf16<TILE_M, BN>(WGRAD, WGRAD || p.b_k == 0);
-            const uint64_t a_desc0 = smem_desc_sw128(0, WGRAD ? BK * 128 : 16, 1024);
-            const uint64_t b_desc0 = smem_desc_sw128(0, !WGRAD && p.b_k ? 16 : BK * 128, 1024);
-            const uint32_t a_step = WGRAD ? 2048u : 32u;
-            const uint32_t b_step = !WGRAD && p.b_k ? 32u : 2048u;
+            const bool m_mn = WGRAD || p.b_k == 0;  // the M operand's M is contiguous (N's only in wgrad mode)
+            uint32_t idesc = instr_desc_bf16<TILE_M, BN>(m_mn, WGRAD);
+            const uint64_t a_desc0 = smem_desc_sw128(0, m_mn ? BK * 128 : 16, 1024);
+            const uint64_t b_desc0 = smem_desc_sw128(0, WGRAD ? BK * 128 : 16, 1024);
+            const uint32_t a_step = m_mn ? 2048u : 32u;
+            const uint32_t b_step = WGRAD ? 2048u : 32u;
             uint32_t it = 0, n = 0;
             bool ok = true;
-            for (int64_t t = worker; ok && walk_to<TILE_M, WGRAD>(p, t, walk, w); t += n_workers) {
+            for (int64_t t = worker; ok && walk_to<TILE_R, WGRAD>(p, t, walk, w); t += n_workers) {
                 if (w.kb0 == w.kb1) continue;  // the epilogue writes an empty sum itself
                 const uint32_t buf = n & 1u;
                 const uint32_t tph = (n >> 1) & 1u;
@@ -408,6 +463,8 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + buf * BN;
+                if constexpr (!WGRAD)
+                    idesc = (idesc & ~(0x3Fu << 17)) | (static_cast<uint32_t>(rows_n<BN>(w)) >> 3 << 17);
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                     const uint32_t s = it % STAGES;
                     const uint32_t ph = (it / STAGES) & 1u;
@@ -456,13 +513,13 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             }
             __syncwarp();
         }
-    } else if (WGRAD && warp == 6) {
+    } else if (WGRAD && warp == 2 + GROUPED_EPI_WARPS) {
         // ------------------------------------------------ fixer
         if constexpr (WGRAD) {
             uint32_t it = 0;
             uint32_t phase = 0;  // bit s: parity of the slot's next fringe
             const uint32_t pfix_leader0 = PAIR ? ptx::map_to_cta(pfix_bar(0), 0u) : 0u;
-            for (int64_t t = worker; walk_to<TILE_M, WGRAD>(p, t, walk, w); t += n_workers) {
+            for (int64_t t = worker; walk_to<TILE_R, WGRAD>(p, t, walk, w); t += n_workers) {
                 it += static_cast<uint32_t>(w.kb1 - w.kb0);
                 const int32_t tail = (w.row1 - w.row0) % BK;
                 // (no tail: also an empty group; the fringe is in the last share)
@@ -501,42 +558,27 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
         }
     } else {
         // ------------------------------------------------ epilogue
-        const int q = warp & 3;
-        const uint32_t stage_base = sE + static_cast<uint32_t>(q * EPI_BUFS) * EPI_BOX_BYTES;
+        const int q = warp & 3;              // tensor-memory lane quadrant of this warp
+        const int turn = (warp - 2) >> 2;    // which of the quadrant's two warps
+        const uint32_t box = sE + static_cast<uint32_t>(warp - 2) * EPI_BOX_BYTES;
         const uint32_t tempty_leader0 = PAIR ? ptx::map_to_cta(tempty_bar(0), 0u) : tempty_bar(0);
         const bool plain = p.alpha == 1.0f && !p.bias && p.act == 0;
-        uint32_t st_cnt = 0;
+        const EpiBox eb = epi_box(WGRAD, p.out_bf16 != 0);
+        const int size = p.out_bf16 ? 2 : 4;
+        // Address of 16-byte unit u of box row r.
+        auto unit_at = [&](int r, int u) {
+            return eb.row_bytes == 128 ? box + r * 128 + ((u ^ (r & 7)) << 4) : box + r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
+        };
 
-        // One 32 x 32 fp32 chunk -> rows row0 .. of D (those before `limit`),
-        // columns col0 ..  `whole`: the 32 rows may go out as one box.
-        auto store_chunk = [&](uint32_t (&v)[32], int32_t row0, int32_t limit, bool whole, int32_t col0, int32_t g) {
-            if (row0 >= limit || col0 >= p.N) return;  // warp-uniform
-            if (!plain) grouped_epilogue(p, v, col0, g);
-            const uint32_t box = stage_base + (st_cnt % EPI_BUFS) * EPI_BOX_BYTES;
-            ++st_cnt;
-            if (p.epi_tma && lane == 0) ptx::bulk_wait_group_read<EPI_BUFS - 1>();
-            __syncwarp();
-            const int32_t col = col0 + lane;
-            const int32_t nrows = min(32, limit - row0);
+        // The box -> rows row0 .. of D (those before `limit`), columns col0 ..
+        // `whole`: a TMA store may write all of its rows (the tensor's own end
+        // clips a box, a group's end does not).
+        auto flush = [&](int32_t row0, int32_t limit, bool whole, int32_t col0, int32_t g) {
+            const int32_t width = eb.row_bytes / size;
+            const int32_t cols = min(width, p.N - col0);
             // (a box that the row's end cuts off its 16 bytes goes out plainly:
             // a TMA store would write on to the next 16-byte boundary)
-            const bool tma = p.epi_tma && whole && (col0 + EPI_CHUNK <= p.N || p.N % (p.out_bf16 ? 8 : 4) == 0);
-            const int64_t at = (WGRAD ? static_cast<int64_t>(g) * p.strideD : 0) + static_cast<int64_t>(row0) * p.ldd + col;
-            if (!p.out_bf16) {
-#pragma unroll
-                for (int jj = 0; jj < 8; ++jj)
-                    ptx::st_shared_v4(box + lane * 128 + ((jj ^ (lane & 7)) << 4), v[4 * jj], v[4 * jj + 1], v[4 * jj + 2],
-                                      v[4 * jj + 3]);
-            } else {
-                uint32_t h[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) h[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    ptx::st_shared_v4(box + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4), h[4 * u], h[4 * u + 1], h[4 * u + 2],
-                                      h[4 * u + 3]);
-            }
-            if (tma) {
+            if (p.epi_tma && whole && (cols == width || p.N % (16 / size) == 0)) {
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -546,63 +588,77 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                 return;
             }
             __syncwarp();
-            // Plain stores, read back from the box.  Rows of D on 16 bytes: 16
-            // at a time (a group's last rows take this path); else an element
-            // a lane, eight rows a step.
-            const int32_t cols = min(EPI_CHUNK, p.N - col0);
-            if (p.epi_tma) {
-                const int eb = p.out_bf16 ? 2 : 4;
-                const int upr = p.out_bf16 ? 4 : 8;  // 16-byte units of a box row
-                const int u = lane & (upr - 1), rstep = 32 / upr;
-                const int per = 16 / eb;
-                uint8_t *dst = static_cast<uint8_t *>(p.D) + (at - lane + u * per) * eb;
-                const int n = min(per, cols - u * per);  // elements of this unit
-#pragma unroll 1
-                for (int r = lane / upr; r < nrows; r += rstep) {
-                    const uint32_t src = p.out_bf16 ? box + r * 64 + ((u ^ ((r >> 1) & 3)) << 4) : box + r * 128 + ((u ^ (r & 7)) << 4);
+            const int32_t nrows = min(eb.rows, limit - row0);
+            uint8_t *dst = static_cast<uint8_t *>(p.D) +
+                           ((WGRAD ? static_cast<int64_t>(g) * p.strideD : 0) + static_cast<int64_t>(row0) * p.ldd + col0) * size;
+            const int64_t pitch = p.ldd * size;
+            if (p.epi_tma) {  // rows of D on 16 bytes
+                const int upr = eb.row_bytes / 16, per = 16 / size;
+                const int u = lane & (upr - 1), n = min(per, cols - u * per);
+#pragma unroll 2
+                for (int r = lane / upr; r < nrows; r += 32 / upr) {
                     uint32_t v[4];
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(src) : "memory");
-                    uint8_t *q = dst + static_cast<int64_t>(r) * p.ldd * eb;
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(unit_at(r, u)) : "memory");
+                    uint8_t *o = dst + r * pitch + u * 16;
                     if (n == per) {
-                        *reinterpret_cast<uint4 *>(q) = make_uint4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<uint4 *>(o) = make_uint4(v[0], v[1], v[2], v[3]);
                     } else if (p.out_bf16) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            if (e < n) reinterpret_cast<uint16_t *>(q)[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+                            if (e < n) reinterpret_cast<uint16_t *>(o)[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (e < n) reinterpret_cast<uint32_t *>(q)[e] = v[e];
+                            if (e < n) reinterpret_cast<uint32_t *>(o)[e] = v[e];
                     }
                 }
-            } else if (!p.out_bf16) {
-                const uint32_t src = box + ((lane >> 2) << 4) + ((lane & 3) << 2);
-                float *dst = static_cast<float *>(p.D) + at;
-#pragma unroll 1
-                for (int r0 = 0; r0 < nrows; r0 += 8, dst += 8 * p.ldd) {
-                    float vals[8];
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) vals[r] = ld_shared_f32((src ^ (r << 4)) + (r0 + r) * 128);
-                    float *q = dst;
-#pragma unroll
-                    for (int r = 0; r < 8; ++r, q += p.ldd)
-                        if (r0 + r < nrows && lane < cols) *q = vals[r];
-                }
-            } else {
-                const uint32_t src = box + ((lane >> 3) << 4) + ((lane & 7) << 1);
-                uint16_t *dst = static_cast<uint16_t *>(p.D) + at;
-#pragma unroll 1
-                for (int r0 = 0; r0 < nrows; r0 += 8, dst += 8 * p.ldd) {
-                    uint16_t vals[8];
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) vals[r] = ld_shared_u16((src ^ (((r >> 1) & 3) << 4)) + (r0 + r) * 64);
-                    uint16_t *q = dst;
-#pragma unroll
-                    for (int r = 0; r < 8; ++r, q += p.ldd)
-                        if (r0 + r < nrows && lane < cols) *q = vals[r];
+            } else {  // an element a lane
+                for (int c = lane; c < cols; c += 32) {
+                    const int u = c * size >> 4, in = c * size & 15;
+                    uint8_t *o = dst + c * size;
+#pragma unroll 8
+                    for (int r = 0; r < nrows; ++r, o += pitch) {
+                        if (p.out_bf16)
+                            *reinterpret_cast<uint16_t *>(o) = ld_shared_u16(unit_at(r, u) + in);
+                        else
+                            *reinterpret_cast<float *>(o) = ld_shared_f32(unit_at(r, u) + in);
+                    }
                 }
             }
             __syncwarp();  // the box may be written again
+        };
+        // The box's last TMA store has read it.
+        auto box_free = [&]() {
+            if (p.epi_tma && lane == 0) ptx::bulk_wait_group_read<0>();
+            __syncwarp();
+        };
+        // 32 values of lane `lane` into the box.  rows mode: column `lane` of
+        // box rows r0 .. r0 + 31; wgrad mode: row `lane`, columns c0 .. c0 + 31.
+        auto stage = [&](const uint32_t (&v)[32], int at) {
+            if constexpr (WGRAD) {
+                if (p.out_bf16) {
+                    uint32_t h[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) h[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        ptx::st_shared_v4(unit_at(lane, at / 8 + u), h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        ptx::st_shared_v4(unit_at(lane, u), v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+                }
+            } else if (p.out_bf16) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j])));
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(unit_at(at + j, lane >> 3) + (lane & 7) * 2), "h"(h) : "memory");
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(unit_at(j, lane >> 2) + (lane & 3) * 4), "r"(v[j]) : "memory");
+            }
         };
         auto release_tmem = [&](uint32_t buf) {
             ptx::tc_fence_before();
@@ -615,22 +671,36 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             }
         };
 
-        constexpr int NCH = BN / EPI_CHUNK;
         uint32_t n = 0;
-        for (int64_t t = worker; walk_to<TILE_M, WGRAD>(p, t, walk, w); t += n_workers) {
-            const int32_t row0 = (WGRAD ? 0 : w.row0) + w.tm * TILE_M + static_cast<int32_t>(rank) * BM + q * 32;
-            const int32_t limit = WGRAD ? p.M : w.row1;
-            // the tensor's own end clips a box; a group's end does not
-            const bool whole = row0 + 32 <= limit || limit == (WGRAD ? p.M : p.S);
-            const int32_t col0 = w.tn * BN;
-            uint32_t va[32], vb[32];
+        const int per_box = p.out_bf16 ? 2 : 1;  // 32-column pieces of the accumulator a box takes
+        for (int64_t t = worker; walk_to<TILE_R, WGRAD>(p, t, walk, w); t += n_workers) {
+            // Accumulator column `32 c` and this warp's lanes in D.
+            const int32_t lanes0 = (WGRAD ? w.tm : w.tn) * TILE_M + static_cast<int32_t>(rank) * BM + q * 32;
+            const int32_t cols0 = WGRAD ? w.tn * BN : w.row0 + w.tm * BN;
+            const int32_t end = WGRAD ? p.N : min(w.row1, cols0 + BN);  // of the accumulator's columns
+            const int32_t limit = WGRAD ? p.M : end;                     // of D's rows
+            const int32_t pieces = (min(BN, end - cols0) + 31) / 32;
+            const bool lanes_in = lanes0 < (WGRAD ? p.M : p.N);  // warp-uniform
+            const float bias = !WGRAD && p.bias && lanes0 + lane < p.N
+                                   ? __ldg(p.bias + static_cast<int64_t>(w.g) * p.bias_stride + lanes0 + lane)
+                                   : 0.0f;
+            // pieces c .. of box c / per_box -> D
+            auto put = [&](int c) {
+                const int32_t row0 = WGRAD ? lanes0 : cols0 + 32 * c;
+                const int32_t col0 = WGRAD ? cols0 + 32 * c : lanes0;
+                flush(row0, limit, row0 + eb.rows <= limit || limit == (WGRAD ? p.M : p.S), col0, w.g);
+            };
             if (w.part >= w.nparts) continue;
+            uint32_t va[32], vb[32];
             if (w.k_blocks == 0) {  // the empty sum
-#pragma unroll 1
-                for (int c = 0; c < NCH; ++c) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) va[j] = 0u;
-                    store_chunk(va, row0, limit, whole, col0 + c * EPI_CHUNK, w.g);
+                for (int j = 0; j < 32; ++j) va[j] = 0u;
+                if (!plain) grouped_epilogue(p, va, bias);
+                for (int c = turn * per_box; lanes_in && c < pieces; c += 2 * per_box) {
+                    box_free();
+                    stage(va, 0);
+                    if (per_box == 2) stage(va, 32);
+                    put(c);
                 }
                 continue;
             }
@@ -639,81 +709,85 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             ++n;
             const int r = wait_bounded(tfull_bar(buf), tph, wd);
             if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
-            if (!epi_all(r == WAIT_OK)) break;
+            if (!grouped_epi_all(r == WAIT_OK)) break;
             ptx::tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
             if (w.nparts > 1) {
-                // The partial tile -> scratch [chunk][column quad][row][4
+                // The partial tile -> scratch [piece][column quad][lane][4
                 // columns]: 16 coalesced bytes a thread.
                 constexpr int64_t PART4 = BM * BN / 4;  // float4s a part
                 const int64_t half = static_cast<int64_t>(w.tile) * (PAIR ? 2 : 1) + rank;
                 float4 *parts = reinterpret_cast<float4 *>(p.partials) + half * p.splits * PART4 + q * 32 + lane;
                 float4 *mine = parts + w.part * PART4;
-#pragma unroll 1
-                for (int c = 0; c < NCH; ++c) {
-                    ptx::tmem_load_32cols(taddr + c * EPI_CHUNK, va);
-                    if (c == NCH - 1) release_tmem(buf);
-                    if (row0 < limit) {
+                for (int c = turn; lanes_in && c < pieces; c += 2) {
+                    ptx::tmem_load_32cols(taddr + c * 32, va);
 #pragma unroll
-                        for (int j4 = 0; j4 < 8; ++j4)
-                            __stcg(mine + (c * 8 + j4) * BM,
-                                   make_float4(__uint_as_float(va[4 * j4]), __uint_as_float(va[4 * j4 + 1]),
-                                               __uint_as_float(va[4 * j4 + 2]), __uint_as_float(va[4 * j4 + 3])));
-                    }
+                    for (int j4 = 0; j4 < 8; ++j4)
+                        __stcg(mine + (c * 8 + j4) * BM,
+                               make_float4(__uint_as_float(va[4 * j4]), __uint_as_float(va[4 * j4 + 1]),
+                                           __uint_as_float(va[4 * j4 + 2]), __uint_as_float(va[4 * j4 + 3])));
                 }
+                release_tmem(buf);
                 __threadfence();
-                ptx::named_barrier_sync(1, 128);
+                ptx::named_barrier_sync(1, 32 * GROUPED_EPI_WARPS);
                 if (warp == 2 && lane == 0) {
                     const int32_t old = atomicAdd(p.counters + half, 1);
                     *last_flag = old == w.nparts - 1 ? 1 : 0;
                     if (old == w.nparts - 1) atomicExch(p.counters + half, 0);  // ready for the next call
                 }
-                ptx::named_barrier_sync(1, 128);
+                ptx::named_barrier_sync(1, 32 * GROUPED_EPI_WARPS);
                 if (*last_flag) {
                     __threadfence();
-#pragma unroll 1
-                    for (int c = 0; c < NCH; ++c) {
-                        if (row0 >= limit || col0 + c * EPI_CHUNK >= p.N) break;  // warp-uniform
-                        float4 acc[8];
+                    for (int c0 = turn * per_box; lanes_in && c0 < pieces; c0 += 2 * per_box) {
+                        box_free();
+                        for (int c = c0; c < min(pieces, c0 + per_box); ++c) {
+                            float4 acc[8];
 #pragma unroll
-                        for (int j4 = 0; j4 < 8; ++j4) acc[j4] = __ldcg(parts + (c * 8 + j4) * BM);
+                            for (int j4 = 0; j4 < 8; ++j4) acc[j4] = __ldcg(parts + (c * 8 + j4) * BM);
 #pragma unroll 2
-                        for (int s = 1; s < w.nparts; ++s) {
-                            float4 t4[8];
+                            for (int s = 1; s < w.nparts; ++s) {
+                                float4 t4[8];
 #pragma unroll
-                            for (int j4 = 0; j4 < 8; ++j4) t4[j4] = __ldcg(parts + s * PART4 + (c * 8 + j4) * BM);
+                                for (int j4 = 0; j4 < 8; ++j4) t4[j4] = __ldcg(parts + s * PART4 + (c * 8 + j4) * BM);
+#pragma unroll
+                                for (int j4 = 0; j4 < 8; ++j4) {
+                                    acc[j4].x += t4[j4].x; acc[j4].y += t4[j4].y;
+                                    acc[j4].z += t4[j4].z; acc[j4].w += t4[j4].w;
+                                }
+                            }
 #pragma unroll
                             for (int j4 = 0; j4 < 8; ++j4) {
-                                acc[j4].x += t4[j4].x; acc[j4].y += t4[j4].y;
-                                acc[j4].z += t4[j4].z; acc[j4].w += t4[j4].w;
+                                va[4 * j4] = __float_as_uint(acc[j4].x);
+                                va[4 * j4 + 1] = __float_as_uint(acc[j4].y);
+                                va[4 * j4 + 2] = __float_as_uint(acc[j4].z);
+                                va[4 * j4 + 3] = __float_as_uint(acc[j4].w);
                             }
+                            if (!plain) grouped_epilogue(p, va, bias);
+                            stage(va, (c - c0) * 32);
                         }
-#pragma unroll
-                        for (int j4 = 0; j4 < 8; ++j4) {
-                            va[4 * j4] = __float_as_uint(acc[j4].x);
-                            va[4 * j4 + 1] = __float_as_uint(acc[j4].y);
-                            va[4 * j4 + 2] = __float_as_uint(acc[j4].z);
-                            va[4 * j4 + 3] = __float_as_uint(acc[j4].w);
-                        }
-                        store_chunk(va, row0, limit, whole, col0 + c * EPI_CHUNK, w.g);
+                        put(c0);
                     }
                 }
-                ptx::named_barrier_sync(1, 128);  // the flag may be written again
+                ptx::named_barrier_sync(1, 32 * GROUPED_EPI_WARPS);  // the flag may be written again
                 continue;
             }
-            ptx::tmem_load_32cols(taddr, va);
-#pragma unroll 1
-            for (int c = 0; c < NCH; c += 2) {
-                ptx::tmem_load_32cols_async(taddr + (c + 1) * EPI_CHUNK, vb);
-                store_chunk(va, row0, limit, whole, col0 + c * EPI_CHUNK, w.g);
-                ptx::tmem_wait_ld(vb);
-                if (c + 2 < NCH)
-                    ptx::tmem_load_32cols_async(taddr + (c + 2) * EPI_CHUNK, va);
-                else
-                    release_tmem(buf);
-                store_chunk(vb, row0, limit, whole, col0 + (c + 1) * EPI_CHUNK, w.g);
-                if (c + 2 < NCH) ptx::tmem_wait_ld(va);
+            // Both pieces of a box are on their way before the first is used.
+            for (int c = turn * per_box; lanes_in && c < pieces; c += 2 * per_box) {
+                const bool two = per_box == 2 && c + 1 < pieces;
+                ptx::tmem_load_32cols_async(taddr + c * 32, va);
+                if (two) ptx::tmem_load_32cols_async(taddr + c * 32 + 32, vb);
+                box_free();
+                ptx::tmem_wait_ld(va);
+                if (!plain) grouped_epilogue(p, va, bias);
+                stage(va, 0);
+                if (two) {
+                    ptx::tmem_wait_ld(vb);
+                    if (!plain) grouped_epilogue(p, vb, bias);
+                    stage(vb, 32);
+                }
+                put(c);
             }
+            release_tmem(buf);
         }
         if constexpr (!WGRAD) {
             // Rows of no group: zeros.  16-byte stores where D's rows allow.
@@ -721,15 +795,15 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             GroupWalk end = walk;
             while (end.base + 32 < p.groups) {
                 end.before += end.total;
-                walk_load<TILE_M>(p, end.base + 32, end);
+                walk_load<TILE_R>(p, end.base + 32, end);
             }
-            const int32_t eb = p.out_bf16 ? 2 : 4;
-            const bool vec = (reinterpret_cast<uintptr_t>(p.D) & 15u) == 0 && p.ldd * eb % 16 == 0;
-            const int64_t w0 = (static_cast<int64_t>(blockIdx.x) * 4 + q), nw = static_cast<int64_t>(gridDim.x) * 4;
+            const bool vec = (reinterpret_cast<uintptr_t>(p.D) & 15u) == 0 && p.ldd * size % 16 == 0;
+            const int64_t w0 = static_cast<int64_t>(blockIdx.x) * GROUPED_EPI_WARPS + (warp - 2);
+            const int64_t nw = static_cast<int64_t>(gridDim.x) * GROUPED_EPI_WARPS;
             for (int64_t i = w0; i < static_cast<int64_t>(first) + (p.S - end.last); i += nw) {
                 const int64_t row = i < first ? i : end.last + (i - first);
-                uint8_t *dst = static_cast<uint8_t *>(p.D) + row * p.ldd * eb;
-                const int64_t bytes = static_cast<int64_t>(p.N) * eb;
+                uint8_t *dst = static_cast<uint8_t *>(p.D) + row * p.ldd * size;
+                const int64_t bytes = static_cast<int64_t>(p.N) * size;
                 const int64_t body = vec ? bytes / 16 * 16 : 0;
                 for (int64_t b = lane * 16; b < body; b += 512)
                     *reinterpret_cast<uint4 *>(dst + b) = make_uint4(0u, 0u, 0u, 0u);
