@@ -1,6 +1,6 @@
 // Entry points of the grouped GEMM (include/tg_gemm.h): argument checks, the
 // tile choice, tensor maps and launches of grouped_kernel (tg_grouped.cuh).
-#include <atomic>
+#include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -182,9 +182,10 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     // one CTA's 128 columns by 128 rows, or 32 where groups have few (the ring
     // is then deeper: weights are the traffic).
     const int64_t hit = groups < S ? groups : S;  // groups that have rows, at most
+    const int64_t depth = wgrad ? cdiv(S / groups, BK) : cdiv(K, BK);  // k-blocks of an (average) tile
     bool pair;
-    if (wgrad)
-        pair = M > 128 && N > 128 && groups * cdiv(M, 256) * cdiv(N, 256) >= hs.sms / 2;
+    if (wgrad)  // (or shares of them do)
+        pair = M > 128 && N > 128 && groups * cdiv(M, 256) * cdiv(N, 256) * std::max<int64_t>(1, depth / SPLIT_DEPTH) >= hs.sms / 2;
     else
         pair = N > 128 && S >= 192 * groups && cdiv(S, 256) * cdiv(N, 256) >= hs.sms / 2;
     if (opt && opt->cta_pair) pair = opt->cta_pair == 2;
@@ -222,10 +223,11 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     p.timeout_ns = opt && opt->timeout_ns ? opt->timeout_ns : HOST_TIMEOUT_NS;
 
     // Few tiles and a long contraction: workers share tiles, each at least
-    // eight k-blocks of the average group, while a wave holds them all.
+    // SPLIT_DEPTH k-blocks of the average group.  wgrad: three shares a worker,
+    // because groups differ (28118 rows in 4 groups, 552 x 550: 75 us with one
+    // tile a worker); rows mode, whose tiles are alike: one.
     const int64_t workers = pair ? hs.sms / 2 : hs.sms;
-    const int64_t depth = wgrad ? cdiv(S / groups, BK) : cdiv(K, BK);
-    int64_t splits = units > 0 ? workers / units : 1;
+    int64_t splits = units > 0 ? (wgrad ? 3 : 1) * workers / units : 1;
     if (splits > depth / SPLIT_DEPTH) splits = depth / SPLIT_DEPTH;
     if (splits < 1) splits = 1;
     p.splits = static_cast<int32_t>(splits);
@@ -255,12 +257,10 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     }
     if (tma_ok(D, ldd, wgrad && groups > 1 ? strideD : 0, eb)) {
         const Operand d{D, wgrad ? M : S, N, ldd, wgrad ? groups : 1, strideD};
-        const EpiBox box = epi_box(wgrad, out_bf16);
         const uint64_t s2 = static_cast<uint64_t>(d.nb > 1 ? strideD * eb : cdiv(d.rows * ldd * eb, 16) * 16);
         p.epi_tma = host_encode_3d(&td, out_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, D, d.cols,
-                                   d.rows, d.nb, ldd * eb, s2, static_cast<uint32_t>(box.row_bytes / eb),
-                                   static_cast<uint32_t>(box.rows),
-                                   box.row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)
+                                   d.rows, d.nb, ldd * eb, s2, static_cast<uint32_t>(EPI_ROW_BYTES / eb), EPI_ROWS,
+                                   CU_TENSOR_MAP_SWIZZLE_128B)
                         ? 1
                         : 0;
     }

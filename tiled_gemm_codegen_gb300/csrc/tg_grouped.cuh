@@ -24,8 +24,10 @@
 // wgrad mode adds warp 10, the fixer, which runs as far ahead of the MMA as
 // the ring allows.  PAIR: a cluster of two CTAs computes one tile, each half
 // of its M, and loads half of its N.  Eight warps drain (two for each lane
-// quadrant, taking boxes in turn) because short contractions leave little but
-// the stores to do: 4 KB boxes, one in flight a warp, outrun HBM.
+// quadrant, taking boxes in turn), because short contractions leave little but
+// the stores to do.  Every box of D is 32 rows of 128 bytes: in rows mode with
+// bf16 a warp's 32 lanes are half of that, so the warps of two neighbouring
+// quadrants fill two boxes together, one while the other is stored.
 //
 // Where there are fewer tiles than workers, `splits` of them share a tile's
 // contraction: each writes its fp32 partial tile to scratch, and the last to
@@ -222,33 +224,24 @@ __device__ __forceinline__ void grouped_epilogue(const GroupedParams &p, uint32_
     for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(x[j]);
 }
 
-// All 256 epilogue threads agree on a predicate (named barrier 1).
-__device__ __forceinline__ bool grouped_epi_all(bool pred)
+// `threads` epilogue threads agree on a predicate (named barrier `id`).
+__device__ __forceinline__ bool agree(bool pred, uint32_t id, uint32_t threads)
 {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.and.pred q, 1, 256, p;\n\t"
+        "bar.red.and.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(pred))
+        : "r"(static_cast<uint32_t>(pred)), "r"(id), "r"(threads)
         : "memory");
     return r != 0;
 }
 
 constexpr int GROUPED_EPI_WARPS = 8;
-// A box of D in shared memory: 4 KB, `rows` of row_bytes with the swizzle of
-// that width.
-struct EpiBox {
-    int rows, row_bytes;
-};
-// rows mode: 32 columns of 32 fp32 or 64 bf16 rows; wgrad mode: 32 rows of 32
-// fp32 or 64 bf16 columns.
-__host__ __device__ constexpr EpiBox epi_box(bool wgrad, bool bf16)
-{
-    return wgrad ? EpiBox{32, 128} : bf16 ? EpiBox{64, 64} : EpiBox{32, 128};
-}
+// A box of D in shared memory: 32 rows of 128 bytes with the 128-byte swizzle.
+constexpr int EPI_ROWS = 32, EPI_ROW_BYTES = 128;
 
 constexpr int GROUPED_THREADS = 64 + 32 * GROUPED_EPI_WARPS;  // rows mode
 constexpr int GROUPED_WGRAD_THREADS = GROUPED_THREADS + 32;   // and the fixer warp
@@ -560,45 +553,64 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
         // ------------------------------------------------ epilogue
         const int q = warp & 3;              // tensor-memory lane quadrant of this warp
         const int turn = (warp - 2) >> 2;    // which of the quadrant's two warps
-        const uint32_t box = sE + static_cast<uint32_t>(warp - 2) * EPI_BOX_BYTES;
+        const bool duo = !WGRAD && p.out_bf16;  // two quadrants' warps share boxes
+        const int sub = q & 1;                  // duo: the half of a box row that is this warp's
+        const uint32_t duo_bar = 2u + static_cast<uint32_t>((warp - 2) >> 1);
+        const uint32_t boxes = duo ? sE + static_cast<uint32_t>((warp - 2) >> 1) * 2u * EPI_BOX_BYTES
+                                   : sE + static_cast<uint32_t>(warp - 2) * EPI_BOX_BYTES;
+        uint32_t box = boxes;
         const uint32_t tempty_leader0 = PAIR ? ptx::map_to_cta(tempty_bar(0), 0u) : tempty_bar(0);
         const bool plain = p.alpha == 1.0f && !p.bias && p.act == 0;
-        const EpiBox eb = epi_box(WGRAD, p.out_bf16 != 0);
         const int size = p.out_bf16 ? 2 : 4;
+        const int width = EPI_ROW_BYTES / size;
         // Address of 16-byte unit u of box row r.
-        auto unit_at = [&](int r, int u) {
-            return eb.row_bytes == 128 ? box + r * 128 + ((u ^ (r & 7)) << 4) : box + r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
-        };
+        auto unit_at = [&](int r, int u) { return box + r * EPI_ROW_BYTES + ((u ^ (r & 7)) << 4); };
 
+        // The next box may be written: its last TMA store has read it.
+        auto box_free = [&]() {
+            if (duo) {
+                box = box == boxes ? boxes + EPI_BOX_BYTES : boxes;
+                if (p.epi_tma && sub == 0 && lane == 0) ptx::bulk_wait_group_read<1>();
+                ptx::named_barrier_sync(duo_bar, 64);
+            } else {
+                if (p.epi_tma && lane == 0) ptx::bulk_wait_group_read<0>();
+                __syncwarp();
+            }
+        };
         // The box -> rows row0 .. of D (those before `limit`), columns col0 ..
         // `whole`: a TMA store may write all of its rows (the tensor's own end
         // clips a box, a group's end does not).
         auto flush = [&](int32_t row0, int32_t limit, bool whole, int32_t col0, int32_t g) {
-            const int32_t width = eb.row_bytes / size;
             const int32_t cols = min(width, p.N - col0);
             // (a box that the row's end cuts off its 16 bytes goes out plainly:
             // a TMA store would write on to the next 16-byte boundary)
-            if (p.epi_tma && whole && (cols == width || p.N % (16 / size) == 0)) {
-                ptx::fence_proxy_async_smem();
+            const bool tma = p.epi_tma && whole && (cols == width || p.N % (16 / size) == 0);
+            if (tma) ptx::fence_proxy_async_smem();
+            if (duo)
+                ptx::named_barrier_sync(duo_bar, 64);
+            else
                 __syncwarp();
-                if (lane == 0) {
+            if (tma) {
+                if (lane == 0 && (!duo || sub == 0)) {
                     ptx::tma_store_3d(&tmD, box, col0, row0, WGRAD ? g : 0);
                     ptx::bulk_commit_group();
                 }
                 return;
             }
-            __syncwarp();
-            const int32_t nrows = min(eb.rows, limit - row0);
+            const int32_t nrows = min(EPI_ROWS, limit - row0);
+            const int r_first = duo ? sub : 0, r_step = duo ? 2 : 1;  // duo: every other row (or four) each
             uint8_t *dst = static_cast<uint8_t *>(p.D) +
                            ((WGRAD ? static_cast<int64_t>(g) * p.strideD : 0) + static_cast<int64_t>(row0) * p.ldd + col0) * size;
             const int64_t pitch = p.ldd * size;
             if (p.epi_tma) {  // rows of D on 16 bytes
-                const int upr = eb.row_bytes / 16, per = 16 / size;
-                const int u = lane & (upr - 1), n = min(per, cols - u * per);
+                const int per = 16 / size, u = lane & 7, n = min(per, cols - u * per);
 #pragma unroll 2
-                for (int r = lane / upr; r < nrows; r += 32 / upr) {
+                for (int r = r_first * 4 + (lane >> 3); r < nrows; r += 4 * r_step) {
                     uint32_t v[4];
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(unit_at(r, u)) : "memory");
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                 : "r"(unit_at(r, u))
+                                 : "memory");
                     uint8_t *o = dst + r * pitch + u * 16;
                     if (n == per) {
                         *reinterpret_cast<uint4 *>(o) = make_uint4(v[0], v[1], v[2], v[3]);
@@ -615,9 +627,9 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             } else {  // an element a lane
                 for (int c = lane; c < cols; c += 32) {
                     const int u = c * size >> 4, in = c * size & 15;
-                    uint8_t *o = dst + c * size;
+                    uint8_t *o = dst + c * size + r_first * pitch;
 #pragma unroll 8
-                    for (int r = 0; r < nrows; ++r, o += pitch) {
+                    for (int r = r_first; r < nrows; r += r_step, o += r_step * pitch) {
                         if (p.out_bf16)
                             *reinterpret_cast<uint16_t *>(o) = ld_shared_u16(unit_at(r, u) + in);
                         else
@@ -625,15 +637,10 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                     }
                 }
             }
-            __syncwarp();  // the box may be written again
+            if (!duo) __syncwarp();  // the box may be written again
         };
-        // The box's last TMA store has read it.
-        auto box_free = [&]() {
-            if (p.epi_tma && lane == 0) ptx::bulk_wait_group_read<0>();
-            __syncwarp();
-        };
-        // 32 values of lane `lane` into the box.  rows mode: column `lane` of
-        // box rows r0 .. r0 + 31; wgrad mode: row `lane`, columns c0 .. c0 + 31.
+        // 32 values of lane `lane` into the box.  rows mode: one column of its
+        // 32 rows; wgrad mode: row `lane`, columns from `at`.
         auto stage = [&](const uint32_t (&v)[32], int at) {
             if constexpr (WGRAD) {
                 if (p.out_bf16) {
@@ -649,10 +656,11 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                         ptx::st_shared_v4(unit_at(lane, u), v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
                 }
             } else if (p.out_bf16) {
+                const int u = sub * 4 + (lane >> 3), in = (lane & 7) * 2;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     const uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j])));
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(unit_at(at + j, lane >> 3) + (lane & 7) * 2), "h"(h) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(unit_at(j, u) + in), "h"(h) : "memory");
                 }
             } else {
 #pragma unroll
@@ -672,25 +680,24 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
         };
 
         uint32_t n = 0;
-        const int per_box = p.out_bf16 ? 2 : 1;  // 32-column pieces of the accumulator a box takes
+        const int per_box = WGRAD && p.out_bf16 ? 2 : 1;  // 32-column pieces of the accumulator a box takes
         for (int64_t t = worker; walk_to<TILE_R, WGRAD>(p, t, walk, w); t += n_workers) {
+            if (w.part >= w.nparts) continue;
             // Accumulator column `32 c` and this warp's lanes in D.
             const int32_t lanes0 = (WGRAD ? w.tm : w.tn) * TILE_M + static_cast<int32_t>(rank) * BM + q * 32;
+            const int32_t box0 = duo ? lanes0 - 32 * sub : lanes0;  // the box's first lane
             const int32_t cols0 = WGRAD ? w.tn * BN : w.row0 + w.tm * BN;
             const int32_t end = WGRAD ? p.N : min(w.row1, cols0 + BN);  // of the accumulator's columns
             const int32_t limit = WGRAD ? p.M : end;                     // of D's rows
             const int32_t pieces = (min(BN, end - cols0) + 31) / 32;
-            const bool lanes_in = lanes0 < (WGRAD ? p.M : p.N);  // warp-uniform
+            const bool lanes_in = box0 < (WGRAD ? p.M : p.N);  // uniform in a warp (and in a duo)
             const float bias = !WGRAD && p.bias && lanes0 + lane < p.N
                                    ? __ldg(p.bias + static_cast<int64_t>(w.g) * p.bias_stride + lanes0 + lane)
                                    : 0.0f;
-            // pieces c .. of box c / per_box -> D
             auto put = [&](int c) {
                 const int32_t row0 = WGRAD ? lanes0 : cols0 + 32 * c;
-                const int32_t col0 = WGRAD ? cols0 + 32 * c : lanes0;
-                flush(row0, limit, row0 + eb.rows <= limit || limit == (WGRAD ? p.M : p.S), col0, w.g);
+                flush(row0, limit, row0 + EPI_ROWS <= limit || limit == (WGRAD ? p.M : p.S), WGRAD ? cols0 + 32 * c : box0, w.g);
             };
-            if (w.part >= w.nparts) continue;
             uint32_t va[32], vb[32];
             if (w.k_blocks == 0) {  // the empty sum
 #pragma unroll
@@ -707,9 +714,10 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             const uint32_t buf = n & 1u;
             const uint32_t tph = (n >> 1) & 1u;
             ++n;
+            // (the warps that meet at barriers below leave together)
             const int r = wait_bounded(tfull_bar(buf), tph, wd);
             if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
-            if (!grouped_epi_all(r == WAIT_OK)) break;
+            if (!(p.splits > 1 ? agree(r == WAIT_OK, 1, 32 * GROUPED_EPI_WARPS) : agree(r == WAIT_OK, duo_bar, 64))) break;
             ptx::tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
             if (w.nparts > 1) {
@@ -771,23 +779,33 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                 ptx::named_barrier_sync(1, 32 * GROUPED_EPI_WARPS);  // the flag may be written again
                 continue;
             }
-            // Both pieces of a box are on their way before the first is used.
-            for (int c = turn * per_box; lanes_in && c < pieces; c += 2 * per_box) {
-                const bool two = per_box == 2 && c + 1 < pieces;
+            // The next pieces' loads are on their way while these are stored.
+            const int step = 2 * per_box;
+            int c = turn * per_box;
+            if (lanes_in && c < pieces) {
                 ptx::tmem_load_32cols_async(taddr + c * 32, va);
-                if (two) ptx::tmem_load_32cols_async(taddr + c * 32 + 32, vb);
+                if (per_box == 2 && c + 1 < pieces) ptx::tmem_load_32cols_async(taddr + c * 32 + 32, vb);
+            } else {
+                release_tmem(buf);
+            }
+            for (; lanes_in && c < pieces; c += step) {
                 box_free();
                 ptx::tmem_wait_ld(va);
                 if (!plain) grouped_epilogue(p, va, bias);
                 stage(va, 0);
-                if (two) {
+                if (per_box == 2 && c + 1 < pieces) {
                     ptx::tmem_wait_ld(vb);
                     if (!plain) grouped_epilogue(p, vb, bias);
                     stage(vb, 32);
                 }
+                if (c + step < pieces) {
+                    ptx::tmem_load_32cols_async(taddr + (c + step) * 32, va);
+                    if (per_box == 2 && c + step + 1 < pieces) ptx::tmem_load_32cols_async(taddr + (c + step) * 32 + 32, vb);
+                } else {
+                    release_tmem(buf);
+                }
                 put(c);
             }
-            release_tmem(buf);
         }
         if constexpr (!WGRAD) {
             // Rows of no group: zeros.  16-byte stores where D's rows allow.
