@@ -15,7 +15,8 @@ namespace {
 
 constexpr int64_t GROUPED_EXTENT = INT32_MAX - 1024;  // a tile past the end stays in range
 constexpr int64_t PITCH_LIMIT = int64_t(1) << 40;
-constexpr int64_t SPLIT_DEPTH = 8;  // k-blocks a worker has at least of a shared tile
+constexpr int64_t SPLIT_DEPTH = 16;  // k-blocks of a share at least (pairs: twice that)
+constexpr int64_t SPLIT_MOST = 16;   // shares of a tile at most
 
 using GroupedKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const GroupedParams);
 
@@ -185,7 +186,7 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     const int64_t depth = wgrad ? cdiv(S / groups, BK) : cdiv(K, BK);  // k-blocks of an (average) tile
     bool pair;
     if (wgrad)  // (or shares of them do)
-        pair = M > 128 && N > 128 && groups * cdiv(M, 256) * cdiv(N, 256) * std::max<int64_t>(1, depth / SPLIT_DEPTH) >= hs.sms / 2;
+        pair = M > 128 && N > 128 && groups * cdiv(M, 256) * cdiv(N, 256) * std::max<int64_t>(1, depth / (2 * SPLIT_DEPTH)) >= hs.sms / 2;
     else
         pair = N > 128 && S >= 192 * groups && cdiv(S, 256) * cdiv(N, 256) >= hs.sms / 2;
     if (opt && opt->cta_pair) pair = opt->cta_pair == 2;
@@ -222,14 +223,18 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     p.err = hs.err;
     p.timeout_ns = opt && opt->timeout_ns ? opt->timeout_ns : HOST_TIMEOUT_NS;
 
-    // Few tiles and a long contraction: workers share tiles, each at least
-    // SPLIT_DEPTH k-blocks of the average group.  wgrad: three shares a worker,
-    // because groups differ (28118 rows in 4 groups, 552 x 550: 75 us with one
-    // tile a worker); rows mode, whose tiles are alike: one.
+    // Few tiles and a long contraction: workers share tiles, as many shares as
+    // there are workers for the average group's (the one that arrives last adds
+    // them, 128 or 64 KB each, so a share is 32 or 16 k-blocks at least), and
+    // a longer group's tiles more of the same length.
     const int64_t workers = pair ? hs.sms / 2 : hs.sms;
-    int64_t splits = units > 0 ? (wgrad ? 3 : 1) * workers / units : 1;
-    if (splits > depth / SPLIT_DEPTH) splits = depth / SPLIT_DEPTH;
-    if (splits < 1) splits = 1;
+    const int64_t least = pair ? 2 * SPLIT_DEPTH : SPLIT_DEPTH;
+    int64_t splits = 1, share = depth;
+    if (units < (wgrad ? 2 * workers : workers) && depth >= 2 * least) {
+        share = std::max(least, units <= workers ? cdiv(depth, workers / units) : cdiv(units * depth, workers));
+        splits = std::min<int64_t>(SPLIT_MOST, cdiv(wgrad ? cdiv(S, BK) : depth, share));
+    }
+    p.part_blocks = static_cast<int32_t>(share);
     p.splits = static_cast<int32_t>(splits);
     const int64_t part_tiles = splits > 1 ? units * (pair ? 2 : 1) : 0;
     const size_t part_bytes = static_cast<size_t>(part_tiles) * splits * BM * bn * 4;

@@ -29,8 +29,8 @@
 // bf16 a warp's 32 lanes are half of that, so the warps of two neighbouring
 // quadrants fill two boxes together, one while the other is stored.
 //
-// Where there are fewer tiles than workers, `splits` of them share a tile's
-// contraction: each writes its fp32 partial tile to scratch, and the last to
+// Where there are few tiles, workers share a tile's contraction (a group of more
+// rows between more of them): each writes its fp32 partial tile to scratch, and the last to
 // arrive adds them in the order of k, as gemm_kernel's split-K does.
 //
 // The list of tiles depends on offsets the host has not seen: every warp
@@ -62,7 +62,8 @@ struct GroupedParams {
     float alpha;
     const float *bias;
     int64_t bias_stride;
-    int32_t splits;          // workers that share a tile (at most one per k-block)
+    int32_t splits;          // workers that share a tile, at most
+    int32_t part_blocks;     // k-blocks a share has, about: a tile has as many shares as that takes
     float *partials;         // splits > 1: [tile][CTA of the pair][splits][BM x BN]
     int32_t *counters;       // splits > 1: arrivals per [tile][CTA], zero between calls
     uint32_t *err;
@@ -174,7 +175,7 @@ __device__ __forceinline__ bool walk_to(const GroupedParams &p, int64_t t64, Gro
     const int32_t in = r % strip, rows = min(tiles_m - first, p.group_m);
     u.tm = first + in % rows;
     u.tn = in / rows;
-    u.nparts = max(1, min(p.splits, u.k_blocks));
+    u.nparts = p.splits > 1 ? max(1, min(p.splits, (u.k_blocks + p.part_blocks - 1) / p.part_blocks)) : 1;
     u.kb0 = 0;
     u.kb1 = u.k_blocks;
     if (p.splits > 1) {
