@@ -470,8 +470,8 @@ tg_status tg_expert_combine_grad(const void *dy, int64_t ld_dy, int32_t dy_type,
  * D S x N (ldd).  ep may be NULL (fp32 D = A B); its residual must be NULL.
  * K == 0 gives act(bias_g).  An empty group costs nothing.  Bounds outside
  * [0, S] or decreasing are clamped, never followed out of range.
- * opt: cta_pair (1 = 128 x 128 tiles, 2 = two-SM 256 x 256 tiles), force_pack,
- * timeout_ns and b_col_major; the rest must be 0.  Other conventions as
+ * opt: cta_pair (1 = one-CTA tiles, 2 = two-SM 256 x 256 tiles), force_pack,
+ * timeout_ns, debug_stall (1) and b_col_major; the rest must be 0.  Other conventions as
  * tg_gemm; extents below 2^31 - 1024. */
 tg_status tg_gemm_grouped(const void *A, const void *B, void *D, const int32_t *offsets, int64_t groups,
                           int64_t S, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t strideB, int64_t ldd,

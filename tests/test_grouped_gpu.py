@@ -307,3 +307,45 @@ def test_same_bits_again_graph_and_stream():
         torch.cuda.synchronize()
         assert torch.equal(D, tg.gemm_grouped(A, B, _offsets(moved)))
         assert torch.equal(W, tg.gemm_grouped_wgrad(A, A, _offsets(moved)))
+
+
+@pytest.mark.parametrize("wgrad", [False, True])
+@pytest.mark.parametrize("pair", [1, 2])
+@pytest.mark.parametrize("sizes", [[300, 5, 170], [6000]])  # whole tiles; shared ones
+def test_watchdog(wgrad, pair, sizes):
+    """A wait that nothing ends runs out after its limit, is reported by
+    tg_device_error, and leaves the device and the next call's counters sound."""
+    S, K, N = sum(sizes), 128, 192
+    A, av = _rand((S, K), 40, True)
+    B, bv = _rand((S, N) if wgrad else (len(sizes), K, N), 41, True)
+    off = _offsets(sizes)
+    call = tg.gemm_grouped_wgrad if wgrad else tg.gemm_grouped
+    call(A, B, off, options=tg.make_options(cta_pair=pair, debug_stall=1, timeout_ns=20_000_000))
+    assert tg.device_error() == tg.TG_ERR_TIMEOUT
+    assert tg.device_error() == tg.TG_OK
+    got = call(A, B, off, options=tg.make_options(cta_pair=pair))
+    assert tg.device_error() == tg.TG_OK
+    assert np.array_equal(_np(got), _wgrad_ref(av, bv, sizes, 0) if wgrad else _rows_ref(av, bv, sizes, 0, S))
+
+
+def test_checks_build_gives_the_same_bits():
+    """The library built with device-side checks: the same results, and no
+    check fails."""
+    import ctypes
+
+    lib = tg.load_checks()
+    sizes, K, N = [300, 0, 45, 700], 200, 264
+    S, off = sum(sizes), _offsets(sizes)
+    A, _ = _rand((S, K), 42, False)
+    B, _ = _rand((4, K, N), 43, False)
+    D, W = tg.gemm_grouped(A, B, off), tg.gemm_grouped_wgrad(A, A, off)
+    D2, W2 = torch.empty_like(D), torch.empty_like(W)
+    ep = tg.tg_epilogue()
+    ep.alpha = 1.0
+    s = torch.cuda.current_stream().cuda_stream
+    assert lib.tg_gemm_grouped(A.data_ptr(), B.data_ptr(), D2.data_ptr(), off.data_ptr(), 4, S, N, K, K, N, K * N, N,
+                               ctypes.byref(ep), s, None) == tg.TG_OK
+    assert lib.tg_gemm_grouped_wgrad(A.data_ptr(), A.data_ptr(), W2.data_ptr(), off.data_ptr(), 4, S, K, K, K, K, K, K * K,
+                                     ctypes.byref(ep), s, None) == tg.TG_OK
+    assert lib.tg_device_error(s) == tg.TG_OK
+    assert torch.equal(D, D2) and torch.equal(W, W2)

@@ -156,12 +156,12 @@ bool span_ok(int64_t nb, int64_t stride, int64_t rows, int64_t ld)
     return static_cast<__int128>(nb) * stride + static_cast<__int128>(rows) * ld < (static_cast<__int128>(1) << 56);
 }
 
-// The options that apply here: cta_pair (1 or 2), timeout_ns, b_col_major;
-// everything else has to be 0.
+// The options that apply here: cta_pair (1 or 2), force_pack, timeout_ns,
+// debug_stall (1), b_col_major; everything else has to be 0.
 bool options_ok(const tg_options *o, bool wgrad)
 {
     if (!o) return true;
-    return !o->block_n && !o->stages && !o->split_k && !o->epilogue && !o->max_ctas && !o->debug_stall && !o->stream_k &&
+    return !o->block_n && !o->stages && !o->split_k && !o->epilogue && !o->max_ctas && (o->debug_stall == 0 || o->debug_stall == 1) && !o->stream_k &&
            !o->operands && !o->trace_buffer && !o->a_col_major && !o->direct && o->cta_pair >= 0 && o->cta_pair <= 2 &&
            (!wgrad || !o->b_col_major);
 }
@@ -222,6 +222,7 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     }
     p.err = hs.err;
     p.timeout_ns = opt && opt->timeout_ns ? opt->timeout_ns : HOST_TIMEOUT_NS;
+    p.debug_stall = opt ? opt->debug_stall : 0;
 
     // Few tiles and a long contraction: workers share tiles, as many shares as
     // there are workers for the average group's (the one that arrives last adds

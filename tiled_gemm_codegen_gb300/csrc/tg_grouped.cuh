@@ -68,6 +68,7 @@ struct GroupedParams {
     int32_t *counters;       // splits > 1: arrivals per [tile][CTA], zero between calls
     uint32_t *err;
     uint64_t timeout_ns;
+    int32_t debug_stall;     // watchdog self-test
 };
 
 // One tile: group, first row of the group and the row behind it (rows mode:
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
     static_assert(GROUPED_EPI_WARPS * EPI_BOX_BYTES <= G::EPI_BYTES, "epilogue boxes");
     static_assert(!WGRAD || BN % 64 == 0, "wgrad mode loads 64-column boxes");
     constexpr uint32_t TMEM_ALLOC = static_cast<uint32_t>(G::TMEM_COLS);
-    static_assert(8 * (4 * STAGES + 5) + 24 <= G::BAR_BYTES, "barrier area");
+    static_assert(8 * (4 * STAGES + 6) + 24 <= G::BAR_BYTES, "barrier area");
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -278,7 +279,8 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
     // CTA's copies of a group's last, partial k-block landed) and pfix[S]
     // (pair, on the leader's: the peer has zeroed its share of it).
     const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (4 * STAGES + 5));
+    const uint32_t stall_bar = bar0 + 8u * (4 * STAGES + 5);  // never completed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (4 * STAGES + 6));
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
     volatile int32_t *last_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 2);
     uint32_t *issued_slot = tmem_slot + 4;  // k-blocks this CTA's producer loaded; then a bit for
@@ -311,6 +313,7 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             ptx::mbar_init(tempty_bar(b), EPI_WARPS_TOTAL);
         }
         ptx::mbar_init(done_bar, 1);
+        ptx::mbar_init(stall_bar, 1);
         *abort_flag = 0;
         issued_slot[0] = issued_slot[1] = 0;
         ptx::fence_barrier_init();
@@ -680,9 +683,15 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
             }
         };
 
+        bool ok = true;
+        if (p.debug_stall) {  // watchdog self-test: a barrier that nothing completes
+            const int r = wait_bounded(stall_bar, 0, wd);
+            if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
+            ok = agree(r == WAIT_OK, 1, 32 * GROUPED_EPI_WARPS);
+        }
         uint32_t n = 0;
         const int per_box = WGRAD && p.out_bf16 ? 2 : 1;  // 32-column pieces of the accumulator a box takes
-        for (int64_t t = worker; walk_to<TILE_R, WGRAD>(p, t, walk, w); t += n_workers) {
+        for (int64_t t = worker; ok && walk_to<TILE_R, WGRAD>(p, t, walk, w); t += n_workers) {
             if (w.part >= w.nparts) continue;
             // Accumulator column `32 c` and this warp's lanes in D.
             const int32_t lanes0 = (WGRAD ? w.tm : w.tn) * TILE_M + static_cast<int32_t>(rank) * BM + q * 32;

@@ -127,10 +127,27 @@ __device__ __forceinline__ void zero_rows(const W4Args &a, int32_t n0, int32_t n
     }
 }
 
-// Any layout and alignment: a warp per column n, a lane per byte of codes,
+// Any layout and alignment: a warp per column n, eight codes a lane and turn,
 // four rows at a time.  (code - zero) * scale and its product with an
 // activation are exact in fp32 (5 + 8 and 8 bits), so only the sum rounds.
 constexpr int ANY_COLS = 8;
+
+// The four bytes at p, of which the first `n` exist: one or two aligned words
+// where they lie inside [lo, hi), else byte by byte.
+__device__ __forceinline__ uint32_t load4_any(const uint8_t *p, int n, const uint8_t *lo, const uint8_t *hi)
+{
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+    const uint8_t *a = p - off;
+    if (n == 4 && a >= lo && a + 8 <= hi) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(a);
+        return off ? __funnelshift_r(w[0], w[1], 8 * off) : w[0];
+    }
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n) v |= static_cast<uint32_t>(p[i]) << (8 * i);
+    return v;
+}
 
 template <bool E2M1>
 __global__ void __launch_bounds__(ANY_COLS * 32) w4_any_kernel(const W4Args a)
@@ -144,19 +161,36 @@ __global__ void __launch_bounds__(ANY_COLS * 32) w4_any_kernel(const W4Args a)
     int32_t g, lo, hi;
     if (!nth_group(a, static_cast<int32_t>(blockIdx.y), g, lo, hi) || n >= a.N) return;
     const uint8_t *w = a.w + g * a.stride_w + n * a.ldw;
+    const uint8_t *w_lo = a.w, *w_hi = a.w + (a.groups - 1) * a.stride_w + (a.N - 1) * a.ldw + a.K / 2;
     const int64_t s0 = g * a.stride_s + n * a.lds, z0 = g * a.stride_z + n * a.ldz;
+    const bool x4 = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(2 * a.ldx)) & 3u) == 0;
     for (int32_t r0 = lo; r0 < hi; r0 += 4) {
         float acc[4] = {};
-        for (int32_t b = lane; b < a.K / 2; b += 32) {
-            const uint32_t q = w[b];
-            float v0, v1;
-            byte_values<E2M1>(a, q, s0 + 2 * b / a.run, z0 + 2 * b / a.run, v0, v1);
+#pragma unroll 2
+        for (int32_t k = lane * 8; k < a.K; k += 256) {
+            const int32_t left = min(8, a.K - k);
+            const uint32_t q = load4_any(w + k / 2, left / 2, w_lo, w_hi);
+            const int32_t r = k / a.run;
+            float v[8];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) byte_values<E2M1>(a, q >> (8 * b) & 255u, s0 + r, z0 + r, v[2 * b], v[2 * b + 1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (r0 + i < hi) {
-                    const uint16_t *x = a.x + (r0 + i) * a.ldx + 2 * b;
-                    acc[i] = fmaf(v0, bf16_value(x[0]), acc[i]);
-                    acc[i] = fmaf(v1, bf16_value(x[1]), acc[i]);
+                if (r0 + i >= hi) break;
+                const uint16_t *x = a.x + (r0 + i) * a.ldx + k;
+                if (x4 && left == 8) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) h[b] = __ldg(reinterpret_cast<const uint32_t *>(x) + b);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        acc[i] = fmaf(v[2 * b], __uint_as_float(h[b] << 16), acc[i]);
+                        acc[i] = fmaf(v[2 * b + 1], __uint_as_float(h[b] & 0xffff0000u), acc[i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 8; ++b)
+                        if (b < left) acc[i] = fmaf(v[b], bf16_value(x[b]), acc[i]);
                 }
             }
         }
@@ -1042,8 +1076,9 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
                 parity ^= 1u;
             }
         }
-        // sums[buffer][warp][x row][weight row], added over a team's warps in order
-        float *sums = reinterpret_cast<float *>(smem + p.off_sum) + b * p.warps * p.xt * W4S_ROWS;
+        // sums[warp][x row][weight row], added over a team's warps in order
+        float *sums = reinterpret_cast<float *>(smem + p.off_sum);
+        ptx::named_barrier_sync(1, threads);  // the last tile's have been added
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int tok = 2 * lc + i;
@@ -1160,7 +1195,7 @@ bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &p,
         for (int wk = 1; wk <= warps && wk <= p.steps; wk *= 2) {
             const int rows = warps / wk * W4S_ROWS;
             const int64_t room = SMEM_LIMIT - W4S_STATIC - 1024 - static_cast<int64_t>(p.xt) * p.x_pitch - xs_bytes - 32 -  // (1 KB: alignment)
-                                 2 * static_cast<int64_t>(rows) * (p.s_words + p.z_words) * 4 - 2 * warps * p.xt * W4S_ROWS * 4;
+                                 2 * static_cast<int64_t>(rows) * (p.s_words + p.z_words) * 4 - warps * p.xt * W4S_ROWS * 4;
             if (room < 2 * warps * W4S_BOX) continue;
             const int64_t tiles_n = (a.N + rows - 1) / rows;
             const double rounds = std::ceil(passes * tiles_n / sms);
@@ -1183,7 +1218,7 @@ bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &p,
     p.off_s = (p.off_xs + xs_bytes + 15) / 16 * 16;
     p.off_z = p.off_s + 2 * tile_rows * p.s_words * 4;
     p.off_sum = p.off_z + 2 * tile_rows * p.z_words * 4;
-    smem = static_cast<size_t>(p.off_sum + 2 * p.warps * p.xt * W4S_ROWS * 4 + 1024);
+    smem = static_cast<size_t>(p.off_sum + p.warps * p.xt * W4S_ROWS * 4 + 1024);
     return true;
 }
 
