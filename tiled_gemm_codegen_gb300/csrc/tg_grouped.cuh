@@ -43,6 +43,9 @@
 
 namespace tg {
 
+// Orders this thread's accesses before and after it for the whole cluster.
+__device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
 struct GroupedParams {
     const int32_t *offsets;  // [groups + 1]
     int32_t groups;
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                             if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_PRODUCER);
                             break;
                         }
-                        ptx::fence_acq_rel_cluster();
+                        fence_acq_rel_cluster();
                     }
                 }
                 if (leader && lane == 0) ptx::mbar_arrive(full_bar(s));
