@@ -277,3 +277,27 @@ def test_repeated_calls_give_the_same_bits():
         if first is not None:
             assert all(torch.equal(a, b) for a, b in zip(first, now))
         first = now
+
+
+def test_rows_past_two_billion_elements():
+    """Offsets of rows beyond 32 bits: the last tokens and slots of a batch
+    whose sorted rows hold 2.3 x 10^9 elements, aligned and not."""
+    T, k, E = 140000, 2, 3
+    ids = torch.randint(0, E, (T, k), device=dev())
+    w = torch.rand(T, k, device=dev())
+    for D in (8192, 8193):
+        x = torch.zeros(T, D, dtype=BF, device=dev())
+        x[:, -16:] = torch.arange(T, device=dev())[:, None] % 251
+        xs, order = tg.expert_dispatch(x, ids, E)
+        s = torch.arange(T * k - 500, T * k, device=dev())
+        src = order.source[s].long()
+        assert torch.equal(xs[s], x[src // k])
+        y = tg.expert_combine(xs, order, w)
+        t = torch.arange(T - 500, T, device=dev())
+        want = _np(x[t]) * _np(w[t].sum(1, keepdim=True))
+        assert within(y[t], want, 4 * U32 * np.abs(want) + 1e-30, BF)
+        del y
+        dys, dw = tg.expert_combine_grad(x, xs, order, w)
+        assert within(dys[s], _np(x[src // k]) * _np(w.reshape(-1)[src])[:, None], U32 * 300, BF)
+        assert torch.equal(dw[t, 0], (x[t].float() ** 2).sum(1))
+        del dys, xs, x

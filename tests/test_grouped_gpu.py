@@ -349,3 +349,27 @@ def test_checks_build_gives_the_same_bits():
                                      ctypes.byref(ep), s, None) == tg.TG_OK
     assert lib.tg_device_error(s) == tg.TG_OK
     assert torch.equal(D, D2) and torch.equal(W, W2)
+
+
+def test_rows_past_two_billion_elements():
+    """A and D of more than 2^31 elements: the last group's rows, and the
+    weight gradient of rows that lie behind them all."""
+    S, K = 270000, 8192
+    A = torch.zeros(S, K, dtype=BF, device=dev())
+    tail, tv = _rand((700, K), 50, True)
+    A[-700:] = tail
+    B, bv = _rand((2, K, 24), 51, True)
+    off = torch.tensor([0, S - 700, S], dtype=torch.int32, device=dev())
+    D = tg.gemm_grouped(A, B, off)
+    assert np.array_equal(_np(D[-700:]), tv @ bv[1])
+    assert not bool(D[:-700].any())
+    W = tg.gemm_grouped_wgrad(A, A[:, :40], off)
+    assert np.array_equal(_np(W[1]), tv.T @ tv[:, :40])
+    assert not bool(W[0].any())
+    del D, W
+    X, xv = _rand((300, 32), 52, True)
+    x = torch.zeros(S, 32, dtype=BF, device=dev())
+    x[-300:] = X
+    V, vv = _rand((1, 32, K), 53, True)
+    out = tg.gemm_grouped(x, V, torch.tensor([0, S], dtype=torch.int32, device=dev()), out_dtype=BF)
+    assert np.array_equal(_np(out[-300:]), torch.from_numpy(xv @ vv[0]).to(BF).double().numpy())

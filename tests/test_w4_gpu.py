@@ -205,3 +205,72 @@ def test_same_bits_again_graph_and_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, tg.gemv_w4(x, W, sc, zeros=z, offsets=off, group=64))
+
+
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+@pytest.mark.parametrize("S", [5, 9])
+def test_activations_that_do_not_fit_shared_memory(fmt, G, zeros, S):
+    K, N = 16640, 40
+    W, sc, z, wv = _weights(1, N, K, fmt, G, 31, zeros)
+    x, xv = _x(S, K, 12)
+    y = tg.gemv_w4(x, W[0], sc[0], zeros=z[0] if z is not None else None, format=fmt, group=G)
+    _check(y, xv, wv, [0, S], K, G, F32)
+
+
+def test_one_matrix_for_every_group():
+    K, N, G = 512, 48, 64
+    W, sc, z, wv = _weights(1, N, K, "int4", G, 32, True)
+    x, xv = _x(6, K, 13)
+    off = torch.tensor([0, 4, 4, 6], dtype=torch.int32, device=dev())
+    y = tg.gemv_w4(x, W.expand(3, N, K // 2), sc.expand(3, N, K // G), zeros=z.expand(3, N, K // G), offsets=off, group=G)
+    _check(y, xv, wv, [0, 6], K, G, F32)
+
+
+def test_infinite_activations_reach_int4_as_the_formula_says():
+    """x w is an infinity of w's sign, NaN where the weight is zero; other rows
+    of the same pass are untouched."""
+    K, N = 1024, 70
+    W, sc, _, wv = _weights(1, N, K, "int4", 128, 33)
+    x, xv = _x(4, K, 14)
+    x[1, 700] = float("inf")
+    x[3, 5] = float("nan")
+    y = tg.gemv_w4(x, W[0], sc[0]).cpu().double().numpy()
+    w = wv[0][:, 700]
+    assert np.array_equal(np.isnan(y[1]), w == 0)
+    assert np.array_equal(y[1][w != 0], np.where(w > 0, np.inf, -np.inf)[w != 0])
+    assert np.isnan(y[3]).all()
+    for t in (0, 2):
+        want, mag = xv[t] @ wv[0].T, np.abs(xv[t]) @ np.abs(wv[0]).T
+        assert np.all(np.abs(y[t] - want) <= 2 * (K + 10) * U32 * mag)
+
+
+@pytest.mark.parametrize("power", [-120, -60, 60, 110])
+def test_activations_of_any_magnitude(power):
+    """Rows scaled by powers of two give results scaled by the same, exactly
+    (no step of the product depends on their magnitude); where bf16 cannot hold
+    the scaled rows (below 2^-126 it has fewer bits), the product of the rows
+    as they were rounded."""
+    K, N = 768, 40
+    W, sc, _, wv = _weights(1, N, K, "int4", 128, 34)
+    x, _ = _x(2, K, 15)
+    scaled = (x.double() * 2.0 ** power).bfloat16()
+    z = tg.gemv_w4(scaled, W[0], sc[0])
+    if torch.equal(scaled.double(), x.double() * 2.0 ** power):
+        assert torch.equal(z.double(), tg.gemv_w4(x, W[0], sc[0]).double() * 2.0 ** power)
+    else:
+        assert power < -110
+        _check(z, scaled.cpu().double().numpy(), wv, [0, 2], K, 128, F32)
+
+
+def test_codes_past_four_gigabytes():
+    K, N, groups = 8192, 8192, 140  # 32 MiB a group, 4.7 GB in all
+    W = torch.zeros(groups, N, K // 2, dtype=torch.uint8, device=dev())
+    sc = torch.ones(groups, N, K // 128, dtype=BF, device=dev())
+    last, slc, _, wv = _weights(1, N, K, "int4", 128, 35)
+    W[-1], sc[-1] = last[0], slc[0]
+    off = torch.zeros(groups + 1, dtype=torch.int32, device=dev())
+    off[-1] = 2
+    x, xv = _x(2, K, 16)
+    y = tg.gemv_w4(x, W, sc, offsets=off)
+    _check(y[:, -64:], xv, wv[:, -64:], [0, 2], K, 128, F32)
+    _check(y[:, :64], xv, wv[:, :64], [0, 2], K, 128, F32)
