@@ -244,21 +244,21 @@ def test_infinite_activations_reach_int4_as_the_formula_says():
         assert np.all(np.abs(y[t] - want) <= 2 * (K + 10) * U32 * mag)
 
 
-@pytest.mark.parametrize("power", [-120, -60, 60, 110])
+@pytest.mark.parametrize("power", [-120, -60, 60, 110, 124])
 def test_activations_of_any_magnitude(power):
     """Rows scaled by powers of two give results scaled by the same, exactly
     (no step of the product depends on their magnitude); where bf16 cannot hold
     the scaled rows (below 2^-126 it has fewer bits), the product of the rows
-    as they were rounded."""
+    as they were rounded; and from 2^114, where rows are summed in another
+    order, the product within its bound."""
     K, N = 768, 40
     W, sc, _, wv = _weights(1, N, K, "int4", 128, 34)
     x, _ = _x(2, K, 15)
     scaled = (x.double() * 2.0 ** power).bfloat16()
     z = tg.gemv_w4(scaled, W[0], sc[0])
-    if torch.equal(scaled.double(), x.double() * 2.0 ** power):
+    if power < 114 and torch.equal(scaled.double(), x.double() * 2.0 ** power):
         assert torch.equal(z.double(), tg.gemv_w4(x, W[0], sc[0]).double() * 2.0 ** power)
     else:
-        assert power < -110
         _check(z, scaled.cpu().double().numpy(), wv, [0, 2], K, 128, F32)
 
 
@@ -274,3 +274,24 @@ def test_codes_past_four_gigabytes():
     y = tg.gemv_w4(x, W, sc, offsets=off)
     _check(y[:, -64:], xv, wv[:, -64:], [0, 2], K, 128, F32)
     _check(y[:, :64], xv, wv[:, :64], [0, 2], K, 128, F32)
+
+
+@pytest.mark.parametrize("power", [-120, 116, 125])
+def test_e2m1_activations_of_any_magnitude(power):
+    K, N = 768, 40
+    W, sc, _, wv = _weights(1, N, K, "e2m1", 32, 36)
+    x, _ = _x(2, K, 17)
+    scaled = (x.double() * 2.0 ** power).clamp(-2.0 ** 127, 2.0 ** 127).bfloat16()
+    scaled[0] = x[0]
+    s = torch.full_like(sc[0], 123)
+    g = np.exp2(123.0 - 127) * wv / np.repeat(np.exp2(sc.cpu().double().numpy() - 127), 32, -1)
+    y = tg.gemv_w4(scaled, W[0], s, format="e2m1", group=32).cpu().double().numpy()
+    xv = scaled.cpu().double().numpy()
+    want, mag = xv @ g[0].T, np.abs(xv) @ np.abs(g[0]).T
+    top = torch.finfo(F32).max
+    assert (np.abs(want) > top).any() == (power == 125)
+    with np.errstate(invalid="ignore"):
+        near = np.abs(y - want) <= 2 * (K + -(-K // 32) + 2) * U32 * mag
+    # where the magnitudes add up to more than fp32 holds, some orders of summation overflow
+    assert np.all(near | (~np.isfinite(y) & (mag > top)))
+    assert np.isfinite(y[np.abs(want) < 0.5 * top]).sum() > 0

@@ -337,7 +337,8 @@ __device__ __forceinline__ void decode_half(uint32_t w, uint32_t (&p)[4])
         p[3] = v & 0x00F000F0u;
     }
 }
-constexpr float W4_UNIT_INT4 = 0x1p-24f, W4_UNIT_E2M1 = 0x1p-14f;
+template <bool E2M1>
+constexpr int32_t W4_UNIT_UP = E2M1 ? 14 : 24;
 
 // d (+)= a b in fp16 with fp32 sums.
 __device__ __forceinline__ void mma_16816_half(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool first)
@@ -562,10 +563,14 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
 //
 // Activations become fp16 by a power of two for each row and step of 256, which
 // brings their largest finite magnitude to [2^11, 2^12); a step's sums are
-// multiplied back.  A value of bf16's eight bits loses some only below 2^-28
-// (2^-24 where it is divided by 16) of the step's largest, by 2^-32 of that at
-// most: less than the rounding of the fp32 sum.  A row with an infinity or NaN, for which the
-// difference of two sums is not the sum, is computed value by value instead.
+// multiplied back, and by the code's unit, before they are added up, so that
+// small results keep their bits (scales below 2^-112 would cost a step's sum
+// some).  A value of bf16's eight bits loses some only below 2^-28 (2^-24
+// where it is divided by 16) of the step's largest, by 2^-32 of that at most:
+// less than the rounding of the fp32 sum.  A row with an infinity or NaN, for
+// which the difference of two sums is not the sum, or with a magnitude from
+// 2^114 (E2M1: 2^124) that no fp32 power of two would bring back, is computed
+// value by value instead.
 //
 // A box lies in shared memory with the 128-byte swizzle (16-byte unit u of
 // row r at u ^ (r mod 8)), which puts the words of a block's eight rows in 32
@@ -660,13 +665,10 @@ __device__ __forceinline__ uint4 shared_u128(uint32_t a, int off)
     return v;
 }
 
-// The power of two (or its inverse) that brings the largest finite magnitude of
-// 256 activations, given as bf16 bits, to [2^11, 2^12); at most 2^126.
-__device__ __forceinline__ float x_scale(int32_t most, bool inverse)
-{
-    const int32_t up = min(138 - (most >> 7), 126);
-    return __uint_as_float(static_cast<uint32_t>(127 + (inverse ? -up : up)) << 23);
-}
+// The exponent of the power of two that brings the largest finite magnitude of
+// 256 activations, given as bf16 bits, to [2^11, 2^12); at most 126.
+__device__ __forceinline__ int32_t x_up(int32_t most) { return min(138 - (most >> 7), 126); }
+__device__ __forceinline__ float power_of_two(int32_t e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // Whole warp: <x[row], w_g[n]> value by value, for any values.
 template <bool E2M1>
@@ -699,7 +701,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * W4S_WARPS * W4S_STAGES];  // a warp's full, then its empty ones
     __shared__ int32_t aborted;
-    __shared__ int32_t x_odd[8];  // the row holds an infinity or NaN
+    __shared__ int32_t x_odd[8];  // the row holds an infinity, NaN or a magnitude too large
     const uint32_t raw = ptx::smem_addr(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_addr(smem);
@@ -889,9 +891,10 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
                     odd |= lo >= 0x7f80 || hi >= 0x7f80;
                     most = max(most, max(lo < 0x7f80 ? lo : 0, hi < 0x7f80 ? hi : 0));
                 }
-                if (odd) x_odd[t] = 1;
                 most = __reduce_max_sync(0xffffffffu, most);
-                const float mul = x_scale(most, false);
+                const int32_t up = x_up(most), back = W4_UNIT_UP<E2M1> - up;
+                if (odd || back > 127) x_odd[t] = 1;
+                const float mul = power_of_two(up);
                 float f[8], sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -907,12 +910,12 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
                 }
                 *reinterpret_cast<uint4 *>(smem + p.off_x + t * p.x_pitch + c * 16) = make_uint4(h[0], h[1], h[2], h[3]);
                 float *xs = reinterpret_cast<float *>(smem + p.off_xs);
-                if (lane == 0) xs[step * 8 + t] = x_scale(most, true);
+                if (lane == 0) xs[step * 8 + t] = power_of_two(min(back, 127));
                 if constexpr (!E2M1) {
 #pragma unroll
                     for (int d = 1; d < RUN / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                     if (lane % (RUN / 8) == 0)
-                        xs[p.steps * 8 + c / (RUN / 8) * 8 + t] = sum * (ZEROS ? W4_UNIT_INT4 : 8.0f * W4_UNIT_INT4);
+                        xs[p.steps * 8 + c / (RUN / 8) * 8 + t] = sum * power_of_two((ZEROS ? 0 : 3) - W4_UNIT_UP<false>);
                 }
             }
         }
@@ -1096,7 +1099,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
         // a warp: the 32 weight rows of a team for one activation row a turn
         for (int i = warp; i < teams * nx; i += p.warps) {
             const int tm = i / nx, tok = i - tm * nx, n = tm * W4S_ROWS + lane;
-            if (!E2M1 && x_odd[tok]) {
+            if (x_odd[tok]) {
                 for (int r = 0; r < W4S_ROWS && n0 + tm * W4S_ROWS + r < a.N; ++r) {
                     const float v = row_dot<E2M1>(a, g, n0 + tm * W4S_ROWS + r, r0 + tok);
                     if (lane == 0) store_y(a, r0 + tok, n0 + tm * W4S_ROWS + r, v);
@@ -1108,7 +1111,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             float sum = 0.0f;
 #pragma unroll 4
             for (int v = 0; v < p.wk; ++v) sum += src[v * p.xt * W4S_ROWS];
-            store_y(a, r0 + tok, n0 + n, sum * (1.0f / (E2M1 ? W4_UNIT_E2M1 : W4_UNIT_INT4)));
+            store_y(a, r0 + tok, n0 + n, sum);
         }
     }
     clear();
