@@ -70,6 +70,17 @@ def _check(y, xv, wv, offsets, K, G, dtype):
     assert within(y, want, 2 * (K + -(-K // G) + 2) * U32 * mag, dtype)
 
 
+def _check_wide(y, xv, wv, K, G):
+    """The same near fp32's largest value: where the magnitudes add up to more
+    than it, some orders of summation overflow."""
+    y, want, mag = y.cpu().double().numpy(), xv @ wv[0].T, np.abs(xv) @ np.abs(wv[0]).T
+    top = torch.finfo(F32).max
+    assert np.all(~np.isfinite(y[np.abs(want) > top * (1 + U32)]))
+    with np.errstate(invalid="ignore"):
+        near = np.abs(y - want) <= 2 * (K + -(-K // G) + 2) * U32 * mag
+    assert np.all(near | (~np.isfinite(y) & (mag > top)))
+
+
 FORMATS = [("int4", 32, False), ("int4", 64, True), ("int4", 128, False), ("int4", 128, True), ("int4", 32, True),
            ("e2m1", 32, False)]
 
@@ -259,7 +270,7 @@ def test_activations_of_any_magnitude(power):
     if power < 114 and torch.equal(scaled.double(), x.double() * 2.0 ** power):
         assert torch.equal(z.double(), tg.gemv_w4(x, W[0], sc[0]).double() * 2.0 ** power)
     else:
-        _check(z, scaled.cpu().double().numpy(), wv, [0, 2], K, 128, F32)
+        _check_wide(z, scaled.cpu().double().numpy(), wv, K, 128)
 
 
 def test_codes_past_four_gigabytes():
@@ -285,13 +296,30 @@ def test_e2m1_activations_of_any_magnitude(power):
     scaled[0] = x[0]
     s = torch.full_like(sc[0], 123)
     g = np.exp2(123.0 - 127) * wv / np.repeat(np.exp2(sc.cpu().double().numpy() - 127), 32, -1)
-    y = tg.gemv_w4(scaled, W[0], s, format="e2m1", group=32).cpu().double().numpy()
-    xv = scaled.cpu().double().numpy()
-    want, mag = xv @ g[0].T, np.abs(xv) @ np.abs(g[0]).T
-    top = torch.finfo(F32).max
-    assert (np.abs(want) > top).any() == (power == 125)
-    with np.errstate(invalid="ignore"):
-        near = np.abs(y - want) <= 2 * (K + -(-K // 32) + 2) * U32 * mag
-    # where the magnitudes add up to more than fp32 holds, some orders of summation overflow
-    assert np.all(near | (~np.isfinite(y) & (mag > top)))
-    assert np.isfinite(y[np.abs(want) < 0.5 * top]).sum() > 0
+    y = tg.gemv_w4(scaled, W[0], s, format="e2m1", group=32)
+    assert bool(torch.isinf(y).any()) == (power == 125)  # three values lie past fp32's largest
+    _check_wide(y, scaled.cpu().double().numpy(), g, K, 32)
+
+
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+def test_slices_of_the_contraction(fmt, G, zeros):
+    """Long rows are cut into slices that a second kernel adds: groups with and
+    without rows, rows of no group, infinities in one slice, the same bits again."""
+    K, N, S = 9000, 136, 23
+    K += K % 32 and 32 - K % 32
+    W, sc, z, wv = _weights(4, N, K, fmt, G, 37, zeros)
+    x, xv = _x(S, K, 18)
+    offsets = [1, 12, 12, 20, 22]
+    off = torch.tensor(offsets, dtype=torch.int32, device=dev())
+    y = tg.gemv_w4(x, W, sc, zeros=z, offsets=off, format=fmt, group=G)
+    _check(y, xv, wv, offsets, K, G, F32)
+    assert torch.equal(y, tg.gemv_w4(x, W, sc, zeros=z, offsets=off, format=fmt, group=G))
+    assert not bool(y[0].any()) and not bool(y[22].any())
+    b = tg.gemv_w4(x, W, sc, zeros=z, offsets=off, format=fmt, group=G, out_dtype=BF)
+    assert torch.equal(b, y.to(BF))
+    x[13, K - 3] = float("inf")
+    v = tg.gemv_w4(x, W, sc, zeros=z, offsets=off, format=fmt, group=G)
+    w = wv[2][:, K - 3]
+    assert torch.equal(torch.isnan(v[13]).cpu(), torch.from_numpy(w == 0))
+    keep = [i for i in range(S) if i != 13]
+    assert torch.equal(v[keep], y[keep])

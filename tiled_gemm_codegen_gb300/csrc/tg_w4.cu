@@ -238,10 +238,6 @@ constexpr int W4_STEP = 256;               // codes of a step
 constexpr int W4_PITCH = W4_STEP / 2 + 16; // staged weight row: the 8 rows of a load fall in 32 different banks
 constexpr int W4_XPITCH = 2 * W4_STEP + 64;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -372,9 +368,8 @@ struct W4Layout {
     static_assert(W4_STAGES * (W4_ROWS * W4_PITCH) >= W4_ROWS * 8 * 4, "room for a warp's sums");
 };
 
-// VEC: bytes of a copy of weights and activations (16, or 4 where rows are
-// only that aligned).  xt: activation rows the ring has room for (1 .. 8).
-template <bool E2M1, int RUN, bool ZEROS, int VEC>
+// xt: activation rows the ring has room for (1 .. 8).
+template <bool E2M1, int RUN, bool ZEROS>
 __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, int xt)
 {
     using L = W4Layout<E2M1, RUN>;
@@ -407,31 +402,17 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
         auto fill = [&](int32_t i) {  // step i of this warp -> slot i mod STAGES
             const uint32_t dst = ring + static_cast<uint32_t>(i % W4_STAGES * stage);
             const int32_t k0 = (warp + i * warps) * W4_STEP;
-            if constexpr (VEC == 16) {
-#pragma unroll
-                for (int j = 0; j < W4_ROWS / 4; ++j) {
-                    const int r = j * 4 + (lane >> 3), b = (lane & 7) * 16;
-                    const int32_t left = row_bytes - (k0 / 2 + b);
-                    if (r < rows)
-                        cp_async16(dst + r * W4_PITCH + b, w0 + r * a.ldw + (left > 0 ? k0 / 2 + b : 0), max(0, min(16, left)));
-                }
-                const int32_t xl = 2 * (a.K - k0) - lane * 16;
-                for (int t = 0; t < nx; ++t)
-                    cp_async16(dst + off_x + t * W4_XPITCH + lane * 16, a.x + (r0 + t) * a.ldx + (xl > 0 ? k0 + lane * 8 : 0),
-                               max(0, min(16, xl)));
-            } else {
-                for (int r = 0; r < rows; ++r) {
-                    const int32_t left = row_bytes - (k0 / 2 + lane * 4);
-                    cp_async4(dst + r * W4_PITCH + lane * 4, w0 + r * a.ldw + (left > 0 ? k0 / 2 + lane * 4 : 0), max(0, min(4, left)));
-                }
-                for (int t = 0; t < nx; ++t)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int32_t xl = 2 * (a.K - k0) - (j * 32 + lane) * 4;
-                        cp_async4(dst + off_x + t * W4_XPITCH + (j * 32 + lane) * 4,
-                                  a.x + (r0 + t) * a.ldx + (xl > 0 ? k0 + (j * 32 + lane) * 2 : 0), max(0, min(4, xl)));
-                    }
+            for (int r = 0; r < rows; ++r) {
+                const int32_t left = row_bytes - (k0 / 2 + lane * 4);
+                cp_async4(dst + r * W4_PITCH + lane * 4, w0 + r * a.ldw + (left > 0 ? k0 / 2 + lane * 4 : 0), max(0, min(4, left)));
             }
+            for (int t = 0; t < nx; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int32_t xl = 2 * (a.K - k0) - (j * 32 + lane) * 4;
+                    cp_async4(dst + off_x + t * W4_XPITCH + (j * 32 + lane) * 4,
+                              a.x + (r0 + t) * a.ldx + (xl > 0 ? k0 + (j * 32 + lane) * 2 : 0), max(0, min(4, xl)));
+                }
             const int32_t at = k0 / RUN;
             for (int j = lane; j < W4_ROWS * L::S_WORDS; j += 32) {
                 const int r = j / L::S_WORDS, word = j % L::S_WORDS;
@@ -542,10 +523,11 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
 }
 
 // ------------------------------------------------------------ stream kernel
-// The same product for weights that TMA can address and activations that fit
-// shared memory whole.  One CTA per SM walks a contiguous range of tiles (32
-// weight rows for each of its teams of `wk` warps, which share K step by
-// step); a producer warp keeps `stages` TMA boxes of 32 rows x 256 codes in
+// The same product for weights that TMA can address.  K is cut into slices
+// (one where that is best) whose activations fit shared memory; products of a
+// slice are added by w4_join_kernel.  One CTA per SM walks a contiguous range
+// of tiles (32 weight rows for each of its teams of `wk` warps, which share a
+// slice of K step by step); a producer warp keeps `stages` TMA boxes of 32 rows x 256 codes in
 // flight for each of them, across the ends of tiles, so the weights never stop
 // and a step costs the others one wait and one arrival.  What a tile needs
 // besides is loaded once or ahead: the activations of a group in the order and
@@ -579,12 +561,15 @@ struct W4Stream {
     int32_t xt;        // activation rows a pass
     int32_t warps, wk; // warps of the CTA, and of a team
     int32_t stages;
-    int32_t steps;     // of 256 codes
+    int32_t steps;     // of 256 codes, of a slice
+    int32_t all_steps, slices;
     int32_t tiles_n;   // tiles of a group
+    int32_t w_shared;  // every group has the same weights
     int32_t x_pitch;   // bytes of an activation row in shared memory
     int32_t s_words, z_words;  // staged words of a row's scales and zeros
     int32_t off_x, off_xs, off_s, off_z, off_sum;  // bytes in shared memory after the rings
     int32_t s_vec;             // every row of scales starts on 4 bytes
+    float *partials;           // slices > 1: [slice][S][N]
     uint32_t *err;
     uint64_t timeout_ns;
 };
@@ -594,6 +579,8 @@ constexpr int W4S_BOX = W4S_ROWS * W4_STEP / 2;  // 4 KB
 constexpr int W4S_WARPS = 16;
 constexpr int W4S_STAGES = 4;
 constexpr int W4S_STATIC = 2048;  // static shared memory, rounded up
+constexpr int W4S_SLICES = 32;
+constexpr int64_t W4S_SCRATCH = int64_t(64) << 20;  // of partial sums, at most
 
 // Pass `nth` over the groups' rows, at most xt rows each: its group, first
 // row and number of rows; false past the last.  Whole warps.
@@ -670,15 +657,15 @@ __device__ __forceinline__ uint4 shared_u128(uint32_t a, int off)
 __device__ __forceinline__ int32_t x_up(int32_t most) { return min(138 - (most >> 7), 126); }
 __device__ __forceinline__ float power_of_two(int32_t e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
-// Whole warp: <x[row], w_g[n]> value by value, for any values.
+// Whole warp: <x[row], w_g[n]> over [k0, k1) value by value, for any values.
 template <bool E2M1>
-__device__ __forceinline__ float row_dot(const W4Args &a, int32_t g, int32_t n, int32_t row)
+__device__ __forceinline__ float row_dot(const W4Args &a, int32_t g, int32_t n, int32_t row, int32_t k0, int32_t k1)
 {
     const uint8_t *w = a.w + g * a.stride_w + n * a.ldw;
     const int64_t s0 = g * a.stride_s + n * a.lds, z0 = g * a.stride_z + n * a.ldz;
     const uint16_t *x = a.x + row * a.ldx;
     float acc = 0.0f;
-    for (int32_t b = static_cast<int32_t>(threadIdx.x & 31); b < a.K / 2; b += 32) {
+    for (int32_t b = k0 / 2 + static_cast<int32_t>(threadIdx.x & 31); b < k1 / 2; b += 32) {
         const uint32_t q = w[b];
         float v0, v1;
         byte_values<E2M1>(a, q, s0 + 2 * b / a.run, z0 + 2 * b / a.run, v0, v1);
@@ -733,51 +720,58 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
         for (int32_t n = static_cast<int32_t>(blockIdx.x) * 256; n < a.N; n += static_cast<int32_t>(gridDim.x) * 256)
             zero_rows(a, n, min(n + 256, a.N), threads);
     };
-    const int64_t tiles = static_cast<int64_t>(count_passes(a, p.xt)) * p.tiles_n;
+    const int64_t tiles = static_cast<int64_t>(count_passes(a, p.xt)) * p.slices * p.tiles_n;
     const int64_t first = blockIdx.x * tiles / gridDim.x, last = (blockIdx.x + 1) * tiles / gridDim.x;
     if (first == last) {
         if (warp < p.warps) clear();
         return;
     }
-    // A tile by its pass and its place in it, stepped without a division.
+    // A tile by its pass, slice and place in it, stepped without a division.
     struct At {
-        int32_t left, pass, n;
-        __device__ __forceinline__ void next(int32_t tiles_n)
+        int32_t left, pass, slice, n;
+        __device__ __forceinline__ void next(const W4Stream &p)
         {
             --left;
-            if (++n == tiles_n) {
+            if (++n == p.tiles_n) {
                 n = 0;
-                ++pass;
+                if (++slice == p.slices) {
+                    slice = 0;
+                    ++pass;
+                }
             }
         }
     };
-    const At at0{static_cast<int32_t>(last - first), static_cast<int32_t>(first / p.tiles_n), static_cast<int32_t>(first % p.tiles_n)};
+    const int64_t first_slice = first / p.tiles_n;
+    const At at0{static_cast<int32_t>(last - first), static_cast<int32_t>(first_slice / p.slices), static_cast<int32_t>(first_slice % p.slices),
+                 static_cast<int32_t>(first % p.tiles_n)};
     if (warp == p.warps) {
         // ------------------------------------------------ producer
         // Lane l keeps warp l's ring full: a box at a time, whenever the
         // warp has freed its slot.
         const bool used = lane < p.warps;
         const int l_team = lane / p.wk, l_part = lane % p.wk;
-        const int32_t each = (p.steps - l_part + p.wk - 1) / p.wk;
         const uint32_t l_ring = base + static_cast<uint32_t>(lane * p.stages * W4S_BOX);
         const uint32_t l_full = bars0 + 16u * W4S_STAGES * lane, l_empty = l_full + 8u * W4S_STAGES;
         int32_t pass = at0.pass - 1, g = 0;
         uint32_t slot = 0, parity = 1;
         uint64_t t0 = 0;
         bool ok = true;
-        for (At at = at0; ok && at.left > 0; at.next(p.tiles_n)) {
+        for (At at = at0; ok && at.left > 0; at.next(p)) {
             if (at.pass != pass) {
                 int32_t r, n;
                 nth_pass(a, p.xt, at.pass, g, r, n);
+                if (p.w_shared) g = 0;
                 pass = at.pass;
             }
+            const int32_t step0 = at.slice * p.steps;
+            const int32_t each = (min(p.steps, p.all_steps - step0) - l_part + p.wk - 1) / p.wk;
             const int32_t n0 = at.n * tile_rows + l_team * W4S_ROWS;
             int32_t i = used ? 0 : each;  // boxes of the tile asked for
             while (__any_sync(0xffffffffu, i < each)) {
                 bool moved = false;
                 if (i < each && ptx::mbar_try_wait(l_empty + 8u * slot, parity)) {
                     ptx::mbar_arrive_expect_tx(l_full + 8u * slot, W4S_BOX);
-                    ptx::tma_load_3d(l_ring + slot * W4S_BOX, &tmW, l_full + 8u * slot, (l_part + i * p.wk) * (W4_STEP / 2), n0, g);
+                    ptx::tma_load_3d(l_ring + slot * W4S_BOX, &tmW, l_full + 8u * slot, (step0 + l_part + i * p.wk) * (W4_STEP / 2), n0, g);
                     ++i;
                     moved = true;
                     if (++slot == static_cast<uint32_t>(p.stages)) {
@@ -815,20 +809,19 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
         }
         return;
     }
-    // this warp's steps of a tile: part_k, part_k + wk, ... (wk <= steps)
-    const int32_t mine = (p.steps - part_k + p.wk - 1) / p.wk;
     int32_t g_next, r0_next, nx_next;  // the pass of the next tile
     nth_pass(a, p.xt, at0.pass, g_next, r0_next, nx_next);
 
     // ---- scales and zeros of a tile -> buffer b; a thread's first word and
     // its step to the next are the same for every tile
-    const int32_t s_used = (a.runs * SB + 3) / 4 + (p.s_vec ? 0 : 1), z_used = ZEROS ? (a.runs + 3) / 4 + 1 : 1;
+    const int32_t slice_runs = min(a.runs, p.steps * RUNS);
+    const int32_t s_used = (slice_runs * SB + 3) / 4 + (p.s_vec ? 0 : 1), z_used = ZEROS ? (slice_runs + 3) / 4 + 1 : 1;
     const int32_t s_r = static_cast<int32_t>(threadIdx.x) / s_used, s_w = static_cast<int32_t>(threadIdx.x) - s_r * s_used;
     const int32_t s_dr = threads / s_used, s_dw = threads - s_dr * s_used;
     const int32_t z_r = static_cast<int32_t>(threadIdx.x) / z_used, z_w = static_cast<int32_t>(threadIdx.x) - z_r * z_used;
     const int32_t z_dr = threads / z_used, z_dw = threads - z_dr * z_used;
-    auto stage_scales = [&](int32_t n0, int32_t g, int b) {
-        const int32_t rows = min(tile_rows, a.N - n0);
+    auto stage_scales = [&](int32_t n0, int32_t g, int32_t slice, int b) {
+        const int32_t rows = min(tile_rows, a.N - n0), from = slice * p.steps * RUNS, runs = min(slice_runs, a.runs - from);
         auto copy = [&](const uint8_t *src0, int64_t pitch, int32_t bytes, const uint8_t *any, int32_t used, int32_t words, uint32_t dst,
                         int32_t r, int32_t w, int32_t dr, int32_t dw) {
             while (r < rows) {
@@ -844,10 +837,10 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
                 }
             }
         };
-        copy(a.scales + (g * a.stride_s + n0 * a.lds) * SB, a.lds * SB, a.runs * SB, a.scales, s_used, p.s_words,
+        copy(a.scales + (g * a.stride_s + n0 * a.lds + from) * SB, a.lds * SB, runs * SB, a.scales, s_used, p.s_words,
              base + p.off_s + b * tile_rows * p.s_words * 4, s_r, s_w, s_dr, s_dw);
         if constexpr (ZEROS)
-            copy(a.zeros + g * a.stride_z + n0 * a.ldz, a.ldz, a.runs, a.zeros, z_used, p.z_words,
+            copy(a.zeros + g * a.stride_z + n0 * a.ldz + from, a.ldz, runs, a.zeros, z_used, p.z_words,
                  base + p.off_z + b * tile_rows * p.z_words * 4, z_r, z_w, z_dr, z_dw);
     };
 
@@ -855,10 +848,10 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
     // and step: eight consecutive ones paired as the codes of a word are; and
     // their sums by group of codes, times the code's unit (and by 8, the zero
     // point, where there is no other).  A warp takes the 256 of a row and step.
-    auto stage_x = [&](int32_t r0, int32_t nx) {
+    auto stage_x = [&](int32_t r0, int32_t nx, int32_t k0, int32_t steps) {
         const bool aligned = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(2 * a.ldx)) & 15u) == 0;
         constexpr int U = 4;  // turns whose loads are in flight together
-        const int32_t turns = nx * p.steps;
+        const int32_t turns = nx * steps;
         for (int32_t i0 = warp; i0 < turns; i0 += U * p.warps) {
             uint4 v[U];
 #pragma unroll
@@ -866,14 +859,14 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
                 const int32_t i = i0 + u * p.warps;
                 v[u] = make_uint4(0u, 0u, 0u, 0u);
                 if (i >= turns) continue;
-                const int32_t t = i / p.steps, c = (i - t * p.steps) * 32 + lane;
-                const uint16_t *row = a.x + (r0 + t) * a.ldx + c * 8;
-                if (aligned && c * 8 + 8 <= a.K) {
+                const int32_t t = i / steps, k = k0 + ((i - t * steps) * 32 + lane) * 8;
+                const uint16_t *row = a.x + (r0 + t) * a.ldx + k;
+                if (aligned && k + 8 <= a.K) {
                     v[u] = *reinterpret_cast<const uint4 *>(row);
-                } else if (c * 8 < a.K) {
+                } else if (k < a.K) {
                     uint32_t h[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) h[e] = c * 8 + e < a.K ? row[e] : 0u;
+                    for (int e = 0; e < 8; ++e) h[e] = k + e < a.K ? row[e] : 0u;
                     v[u] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
                 }
             }
@@ -881,7 +874,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             for (int u = 0; u < U; ++u) {
                 const int32_t i = i0 + u * p.warps;
                 if (i >= turns) break;
-                const int32_t t = i / p.steps, step = i - t * p.steps, c = step * 32 + lane;
+                const int32_t t = i / steps, step = i - t * steps, c = step * 32 + lane;
                 const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
                 int32_t most = 0;
                 bool odd = false;
@@ -923,7 +916,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
 
     At at = at0;
     int32_t g, r0, nx;  // the tile's pass
-    stage_scales(at.n * tile_rows, g_next, 0);
+    stage_scales(at.n * tile_rows, g_next, at.slice, 0);
     uint32_t slot = 0, parity = 0;  // of the next box
     bool fresh = true;  // the tile's activations are not in shared memory yet
     for (int b = 0; at.left > 0; b ^= 1) {
@@ -933,17 +926,19 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             g = g_next;
             r0 = r0_next;
             nx = nx_next;
-            stage_x(r0, nx);
+            stage_x(r0, nx, at.slice * p.steps * W4_STEP, min(p.steps, p.all_steps - at.slice * p.steps));
             cp_async_commit();
             cp_async_wait<0>();
             ptx::named_barrier_sync(1, threads);
         }
-        const int32_t n0 = at.n * tile_rows;
-        at.next(p.tiles_n);  // from here on the tile behind this one
+        const int32_t n0 = at.n * tile_rows, slice = at.slice, k0 = slice * p.steps * W4_STEP;
+        // this warp's steps of the tile: part_k, part_k + wk, ...
+        const int32_t mine = (min(p.steps, p.all_steps - slice * p.steps) - part_k + p.wk - 1) / p.wk;
+        at.next(p);  // from here on the tile behind this one
         fresh = at.n == 0;
         if (at.left > 0) {
             if (fresh) nth_pass(a, p.xt, at.pass, g_next, r0_next, nx_next);
-            stage_scales(at.n * tile_rows, fresh ? g_next : g, b ^ 1);
+            stage_scales(at.n * tile_rows, fresh ? g_next : g, at.slice, b ^ 1);
         }
         cp_async_commit();
         float acc[2][4] = {};
@@ -955,7 +950,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             const uintptr_t src = reinterpret_cast<uintptr_t>(a.scales) + static_cast<uintptr_t>((g * a.stride_s + (n0 + r) * a.lds) * SB);
             s_row[h] = smem + p.off_s + (b * tile_rows + r) * p.s_words * 4 + static_cast<uint32_t>(src & 3u);
             if constexpr (ZEROS) {
-                const uintptr_t zsrc = reinterpret_cast<uintptr_t>(a.zeros) + static_cast<uintptr_t>(g * a.stride_z + (n0 + r) * a.ldz);
+                const uintptr_t zsrc = reinterpret_cast<uintptr_t>(a.zeros) + static_cast<uintptr_t>(g * a.stride_z + (n0 + r) * a.ldz + slice * p.steps * RUNS);
                 z_row[h] = smem + p.off_z + (b * tile_rows + r) * p.z_words * 4 + static_cast<uint32_t>(zsrc & 3u);
             }
         }
@@ -963,7 +958,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
         uint32_t x_step = base + p.off_x + (lg < nx ? lg : 0) * p.x_pitch + lc * 16 + part_k * (2 * W4_STEP);
         const float2 *xs_step = reinterpret_cast<const float2 *>(smem + p.off_xs) + (p.steps + part_k * RUNS) * 4 + lc;
         const float2 *inv_step = reinterpret_cast<const float2 *>(smem + p.off_xs) + part_k * 4 + lc;
-        int32_t k_left = a.K - part_k * W4_STEP;  // codes from the step's first
+        int32_t k_left = a.K - k0 - part_k * W4_STEP;  // codes from the step's first
         int32_t run0 = part_k * RUNS;
         for (int32_t i = 0; i < mine; ++i) {
             if (!ptx::mbar_try_wait(bar0 + 8u * slot, parity)) {
@@ -1096,13 +1091,20 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
         cp_async_wait<0>();
         ptx::named_barrier_sync(1, threads);  // the sums, and the next tile's scales
         if (aborted) return;  // (the producer waits for the boxes on their way)
-        // a warp: the 32 weight rows of a team for one activation row a turn
+        // A warp: the 32 weight rows of a team for one activation row a turn,
+        // to y or, where there are more slices, to scratch.
+        auto put = [&](int tok, int n, float v) {
+            if (p.slices == 1)
+                store_y(a, r0 + tok, n0 + n, v);
+            else
+                __stcg(p.partials + (static_cast<int64_t>(slice) * a.S + r0 + tok) * a.N + n0 + n, v);
+        };
         for (int i = warp; i < teams * nx; i += p.warps) {
             const int tm = i / nx, tok = i - tm * nx, n = tm * W4S_ROWS + lane;
             if (x_odd[tok]) {
                 for (int r = 0; r < W4S_ROWS && n0 + tm * W4S_ROWS + r < a.N; ++r) {
-                    const float v = row_dot<E2M1>(a, g, n0 + tm * W4S_ROWS + r, r0 + tok);
-                    if (lane == 0) store_y(a, r0 + tok, n0 + tm * W4S_ROWS + r, v);
+                    const float v = row_dot<E2M1>(a, g, n0 + tm * W4S_ROWS + r, r0 + tok, k0, min(a.K, k0 + p.steps * W4_STEP));
+                    if (lane == 0) put(tok, tm * W4S_ROWS + r, v);
                 }
                 continue;
             }
@@ -1111,10 +1113,27 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             float sum = 0.0f;
 #pragma unroll 4
             for (int v = 0; v < p.wk; ++v) sum += src[v * p.xt * W4S_ROWS];
-            store_y(a, r0 + tok, n0 + n, sum);
+            put(tok, n, sum);
         }
     }
     clear();
+}
+
+// The slices' partial products, added in their order.
+__global__ void __launch_bounds__(256) w4_join_kernel(const W4Args a, const float *partials, int32_t slices)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int32_t n = static_cast<int32_t>(blockIdx.x) * 256 + static_cast<int32_t>(threadIdx.x);
+    if (n >= a.N) return;
+    const int32_t first = a.offsets ? max(0, min(__ldg(a.offsets), a.S)) : 0;
+    const int32_t last = a.offsets ? max(first, min(__ldg(a.offsets + a.groups), a.S)) : a.S;
+    for (int32_t r = first + static_cast<int32_t>(blockIdx.y); r < last; r += static_cast<int32_t>(gridDim.y)) {
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int32_t v = 0; v < slices; ++v) sum += __ldcg(partials + (static_cast<int64_t>(v) * a.S + r) * a.N + n);
+        store_y(a, r, n, sum);
+    }
 }
 
 template <class... P, class... A>
@@ -1133,11 +1152,11 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cuda
     return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
-template <bool E2M1, int RUN, bool ZEROS, int VEC>
+template <bool E2M1, int RUN, bool ZEROS>
 cudaError_t launch_tile(const W4Args &a, int64_t used, int xt, int dev, cudaStream_t s)
 {
     using L = W4Layout<E2M1, RUN>;
-    auto kern = w4_tile_kernel<E2M1, RUN, ZEROS, VEC>;
+    auto kern = w4_tile_kernel<E2M1, RUN, ZEROS>;
     static std::atomic<unsigned long long> configured{0};  // the shared-memory opt-in, once per device
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
     if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
@@ -1150,40 +1169,33 @@ cudaError_t launch_tile(const W4Args &a, int64_t used, int xt, int dev, cudaStre
     return launch(kern, grid, w4_warps(xt) * 32, static_cast<size_t>(L::smem(xt, ZEROS)), s, a, xt);
 }
 
-template <int VEC>
 cudaError_t launch_w4(const W4Args &a, bool e2m1, int64_t used, int xt, int dev, cudaStream_t s)
 {
-    if (e2m1) return launch_tile<true, 32, false, VEC>(a, used, xt, dev, s);
+    if (e2m1) return launch_tile<true, 32, false>(a, used, xt, dev, s);
     if (a.zeros) {
-        if (a.run == 32) return launch_tile<false, 32, true, VEC>(a, used, xt, dev, s);
-        if (a.run == 64) return launch_tile<false, 64, true, VEC>(a, used, xt, dev, s);
-        return launch_tile<false, 128, true, VEC>(a, used, xt, dev, s);
+        if (a.run == 32) return launch_tile<false, 32, true>(a, used, xt, dev, s);
+        if (a.run == 64) return launch_tile<false, 64, true>(a, used, xt, dev, s);
+        return launch_tile<false, 128, true>(a, used, xt, dev, s);
     }
-    if (a.run == 32) return launch_tile<false, 32, false, VEC>(a, used, xt, dev, s);
-    if (a.run == 64) return launch_tile<false, 64, false, VEC>(a, used, xt, dev, s);
-    return launch_tile<false, 128, false, VEC>(a, used, xt, dev, s);
+    if (a.run == 32) return launch_tile<false, 32, false>(a, used, xt, dev, s);
+    if (a.run == 64) return launch_tile<false, 64, false>(a, used, xt, dev, s);
+    return launch_tile<false, 128, false>(a, used, xt, dev, s);
 }
 
-// The stream kernel's plan; false where its activations do not fit.  `used`:
+// The stream kernel's plan; false where no slice's activations fit.  `used`:
 // the groups that have rows, at most.
-bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &p, int &grid, size_t &smem)
+bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &best_p, int &grid, size_t &smem)
 {
+    W4Stream p{};
     p.xt = 1;
     while (p.xt < 8 && p.xt < a.S) p.xt *= 2;
-    p.steps = (a.K + W4_STEP - 1) / W4_STEP;
-    p.x_pitch = p.steps * W4_STEP * 2 + 64;
-    const int sb = e2m1 ? 1 : 2;
-    // A lane reads a step's scales of a row at once, 4 to 16 bytes: rows lie
-    // an odd number of such pieces apart, in different banks.
-    const int unit = (W4_STEP / a.run * sb + 3) / 4;
-    const int pieces = (p.steps * unit + 1 + unit - 1) / unit | 1;
-    p.s_words = pieces * unit;
+    p.all_steps = (a.K + W4_STEP - 1) / W4_STEP;
+    const int sb = e2m1 ? 1 : 2, runs = W4_STEP / a.run;
     p.s_vec = (reinterpret_cast<uintptr_t>(a.scales) | static_cast<uintptr_t>(a.lds * sb) | static_cast<uintptr_t>(a.stride_s * sb)) % 4 == 0;
-    p.z_words = a.zeros ? (a.runs + 3) / 4 + 1 : 0;
-    const int xs_bytes = p.steps * (1 + (e2m1 ? 0 : W4_STEP / a.run)) * 8 * 4;
     // The passes to expect: rows that fall on groups at random leave some
     // groups empty (S of them reach groups (1 - (1 - 1/groups)^S)).
-    double passes = static_cast<double>((a.S + p.xt - 1) / p.xt);
+    const int64_t even = (a.S + p.xt - 1) / p.xt;
+    double passes = static_cast<double>(even);
     if (a.offsets && a.groups > 1) {
         const double hit = a.groups * (1.0 - std::pow(1.0 - 1.0 / a.groups, static_cast<double>(a.S)));
         passes = std::fmax(passes, std::fmin(hit, static_cast<double>(used)));
@@ -1192,36 +1204,55 @@ bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &p,
     // step a warp has, and the tile's end.  Measured on 28672 rows of 8192
     // codes (16 warps; teams of 16, 8, 4 and 2 warps: 27.4, 27.1, 31.0 and
     // 33.7 us): a turn costs 1.5 times the end.  Fewer warps only shorten a
-    // turn to a half, where latency is what is left of it.
+    // turn to a half, where latency is what is left of it, and a ring of
+    // fewer than 32 boxes (128 KB) stretches it: the activations of a slice
+    // of K take its room.  More slices mean a second launch that adds them,
+    // activations staged for each (its share of the CTA's tiles) and partial
+    // products.  Measured (us; 1, 2, 4 and 8 slices, int4): 8 rows of 9216
+    // onto 8192 49, 29, 27, 25; 4 of 14336 onto 4096 29, 25, 21, 21; 8 of
+    // 8192 onto 28672 49, 45, 41, 47; 1 of 8192 onto 28672 33, 33, 35, 39.
     double best = 0.0;
-    for (int warps = W4S_WARPS; warps >= 4; warps /= 2) {
-        for (int wk = 1; wk <= warps && wk <= p.steps; wk *= 2) {
-            const int rows = warps / wk * W4S_ROWS;
-            const int64_t room = SMEM_LIMIT - W4S_STATIC - 1024 - static_cast<int64_t>(p.xt) * p.x_pitch - xs_bytes - 32 -  // (1 KB: alignment)
-                                 2 * static_cast<int64_t>(rows) * (p.s_words + p.z_words) * 4 - warps * p.xt * W4S_ROWS * 4;
-            if (room < 2 * warps * W4S_BOX) continue;
-            const int64_t tiles_n = (a.N + rows - 1) / rows;
-            const double rounds = std::ceil(passes * tiles_n / sms);
-            const double cost = rounds * (1.5 * ((p.steps + wk - 1) / wk) * std::fmax(warps, 8) / 16.0 + 1.0);
-            if (best != 0.0 && cost >= best) continue;
-            best = cost;
-            p.warps = warps;
-            p.wk = wk;
-            p.tiles_n = static_cast<int32_t>(tiles_n);
-            p.stages = static_cast<int32_t>(room / (warps * W4S_BOX));
+    for (int32_t slices = 1; slices <= W4S_SLICES && slices <= p.all_steps; slices *= 2) {
+        p.steps = (p.all_steps + slices - 1) / slices;
+        p.slices = (p.all_steps + p.steps - 1) / p.steps;
+        if (p.slices != slices) continue;
+        if (slices > 1 && static_cast<int64_t>(a.S) * a.N * slices * 4 > W4S_SCRATCH) break;
+        p.x_pitch = p.steps * W4_STEP * 2 + 64;
+        // A lane reads a step's scales of a row at once, 4 to 16 bytes: rows lie
+        // an odd number of such pieces apart, in different banks.
+        const int unit = (runs * sb + 3) / 4;
+        const int pieces = (p.steps * unit + 1 + unit - 1) / unit | 1;
+        p.s_words = pieces * unit;
+        p.z_words = a.zeros ? (std::min(a.runs, p.steps * runs) + 3) / 4 + 1 : 0;
+        const int xs_bytes = p.steps * (1 + (e2m1 ? 0 : runs)) * 8 * 4;
+        for (p.warps = W4S_WARPS; p.warps >= 4; p.warps /= 2) {
+            for (p.wk = 1; p.wk <= p.warps && p.wk <= p.steps; p.wk *= 2) {
+                const int rows = p.warps / p.wk * W4S_ROWS;
+                const int64_t room = SMEM_LIMIT - W4S_STATIC - 1024 - static_cast<int64_t>(p.xt) * p.x_pitch - xs_bytes - 32 -  // (1 KB: alignment)
+                                     2 * static_cast<int64_t>(rows) * (p.s_words + p.z_words) * 4 - p.warps * p.xt * W4S_ROWS * 4;
+                if (room < 2 * p.warps * W4S_BOX) continue;
+                p.tiles_n = static_cast<int32_t>((a.N + rows - 1) / rows);
+                p.stages = static_cast<int32_t>(std::min<int64_t>(W4S_STAGES, room / (p.warps * W4S_BOX)));
+                const double rounds = std::ceil(passes * slices * p.tiles_n / sms);
+                const double starved = std::fmax(1.0, 32.0 / (p.warps * p.stages));
+                const double turn = 1.5 * std::fmax(p.warps, 8) / 16.0 * starved;
+                const double fresh = std::fmin(1.0 + rounds / p.tiles_n, rounds);
+                const double cost = rounds * (turn * ((p.steps + p.wk - 1) / p.wk) + 1.0) + fresh * 0.015 * p.xt * p.steps + (slices > 1 ? 2.0 + 1.6e-6 * slices * a.S * a.N : 0.0);
+                if (best != 0.0 && cost >= best) continue;
+                best = cost;
+                best_p = p;
+                best_p.off_x = p.warps * p.stages * W4S_BOX;
+                best_p.off_xs = best_p.off_x + p.xt * p.x_pitch;
+                best_p.off_s = (best_p.off_xs + xs_bytes + 15) / 16 * 16;
+                best_p.off_z = best_p.off_s + 2 * rows * p.s_words * 4;
+                best_p.off_sum = best_p.off_z + 2 * rows * p.z_words * 4;
+                smem = static_cast<size_t>(best_p.off_sum + p.warps * p.xt * W4S_ROWS * 4 + 1024);
+            }
         }
     }
     if (best == 0.0) return false;
-    if (p.stages > W4S_STAGES) p.stages = W4S_STAGES;
-    const int64_t n = p.tiles_n * (a.offsets ? std::max<int64_t>(used, (a.S + p.xt - 1) / p.xt) : (a.S + p.xt - 1) / p.xt);
+    const int64_t n = std::max(a.offsets ? used : 0, even) * best_p.slices * best_p.tiles_n;
     grid = static_cast<int>(n < sms ? n : sms);
-    const int tile_rows = p.warps / p.wk * W4S_ROWS;
-    p.off_x = p.warps * p.stages * W4S_BOX;
-    p.off_xs = p.off_x + p.xt * p.x_pitch;
-    p.off_s = (p.off_xs + xs_bytes + 15) / 16 * 16;
-    p.off_z = p.off_s + 2 * tile_rows * p.s_words * 4;
-    p.off_sum = p.off_z + 2 * tile_rows * p.z_words * 4;
-    smem = static_cast<size_t>(p.off_sum + p.warps * p.xt * W4S_ROWS * 4 + 1024);
     return true;
 }
 
@@ -1328,16 +1359,13 @@ TG_API tg_status tg_gemv_w4(const void *x, int64_t ldx, const void *W, int64_t l
         const int64_t used = offsets ? (groups < S ? groups : S) : 1;  // groups with rows, at most
         if (used > 65535) return TG_ERR_UNSUPPORTED;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-        auto aligned = [&](uintptr_t n) {
-            return ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(W) | static_cast<uintptr_t>(2 * ldx) |
-                     static_cast<uintptr_t>(a.ldw) | static_cast<uintptr_t>(a.stride_w)) % n) == 0 &&
-                   (reinterpret_cast<uintptr_t>(scales) | reinterpret_cast<uintptr_t>(zeros)) % 4 == 0;
-        };
         const bool e2m1 = format == TG_W4_E2M1;
         // Weights that TMA can address (16-byte rows; the activations may
-        // have any alignment).
-        if (K > 0 && (reinterpret_cast<uintptr_t>(W) | static_cast<uintptr_t>(a.ldw) | static_cast<uintptr_t>(a.stride_w)) % 16 == 0 &&
-            (reinterpret_cast<uintptr_t>(scales) | reinterpret_cast<uintptr_t>(zeros)) % 4 == 0) {
+        // have any alignment); 4-byte rows of both; anything else.
+        const uintptr_t w_at = reinterpret_cast<uintptr_t>(W) | static_cast<uintptr_t>(a.ldw) | static_cast<uintptr_t>(a.stride_w);
+        const uintptr_t x_at = reinterpret_cast<uintptr_t>(x) | static_cast<uintptr_t>(2 * ldx);
+        const bool words = (reinterpret_cast<uintptr_t>(scales) | reinterpret_cast<uintptr_t>(zeros)) % 4 == 0;
+        if (K > 0 && w_at % 16 == 0 && words) {
             std::lock_guard<std::mutex> lock(host_mutex());
             HostStream hs;
             const tg_status st = host_stream(s, &hs);
@@ -1348,22 +1376,33 @@ TG_API tg_status tg_gemv_w4(const void *x, int64_t ldx, const void *W, int64_t l
             CUtensorMap tm;
             const uint64_t s2 = static_cast<uint64_t>(groups > 1 && a.stride_w > 0 ? a.stride_w : (N * a.ldw + 15) / 16 * 16);
             const bool shared_w = groups > 1 && a.stride_w == 0;
-            if (!shared_w && plan_stream(a, e2m1, used, hs.sms, p, grid, smem) &&
+            if (plan_stream(a, e2m1, used, hs.sms, p, grid, smem) &&
                 host_encode_3d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, static_cast<uint64_t>(K / 2), static_cast<uint64_t>(N),
-                               static_cast<uint64_t>(groups), static_cast<uint64_t>(a.ldw), s2, W4_STEP / 2, W4S_ROWS,
+                               shared_w ? 1 : static_cast<uint64_t>(groups), static_cast<uint64_t>(a.ldw), s2, W4_STEP / 2, W4S_ROWS,
                                CU_TENSOR_MAP_SWIZZLE_128B)) {
+                p.w_shared = shared_w;
                 p.err = hs.err;
                 p.timeout_ns = HOST_TIMEOUT_NS;
-                return host_cuda_status(launch_stream_of(e2m1, tm, a, p, grid, smem, hs.dev, s));
+                if (p.slices > 1) {
+                    void *scratch = nullptr;
+                    const tg_status ws = host_arena(hs, static_cast<size_t>(p.slices) * S * N * 4, &scratch);
+                    if (ws != TG_OK) return ws;
+                    p.partials = static_cast<float *>(scratch);
+                }
+                cudaError_t e = launch_stream_of(e2m1, tm, a, p, grid, smem, hs.dev, s);
+                if (e == cudaSuccess && p.slices > 1)
+                    e = launch(w4_join_kernel, dim3(static_cast<unsigned>((N + 255) / 256), static_cast<unsigned>(S < 1024 ? S : 1024)), 256, 0, s,
+                               a, p.partials, p.slices);
+                return host_cuda_status(e);
             }
         }
-        if (K > 0 && aligned(4)) {
+        if (K > 0 && (w_at | x_at) % 4 == 0 && words) {
             int dev = 0;
             const cudaError_t e = cudaGetDevice(&dev);
             if (e != cudaSuccess) return host_cuda_status(e);
             int xt = 1;  // activation rows a pass: no more than there are
             while (xt < 8 && xt < S) xt *= 2;
-            return host_cuda_status(aligned(16) ? launch_w4<16>(a, e2m1, used, xt, dev, s) : launch_w4<4>(a, e2m1, used, xt, dev, s));
+            return host_cuda_status(launch_w4(a, e2m1, used, xt, dev, s));
         }
         const dim3 grid(static_cast<unsigned>((N + ANY_COLS - 1) / ANY_COLS), static_cast<unsigned>(used));
         return host_cuda_status(format == TG_W4_E2M1 ? launch(w4_any_kernel<true>, grid, ANY_COLS * 32, 0, s, a)
