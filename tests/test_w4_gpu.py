@@ -317,6 +317,20 @@ def test_slices_of_the_contraction(fmt, G, zeros):
     assert not bool(y[0].any()) and not bool(y[22].any())
     b = tg.gemv_w4(x, W, sc, zeros=z, offsets=off, format=fmt, group=G, out_dtype=BF)
     assert torch.equal(b, y.to(BF))
+    stream, g2 = torch.cuda.Stream(), torch.empty_like(y)
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):  # another stream's scratch, then a captured call
+        tg.gemv_w4(x, W, sc, zeros=z, offsets=off, format=fmt, group=G, y=g2)
+    stream.synchronize()
+    assert torch.equal(g2, y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        tg.gemv_w4(x, W, sc, zeros=z, offsets=off, format=fmt, group=G, y=g2)
+    off.copy_(torch.tensor([0, 3, 15, 15, 23], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    _check(g2, xv, wv, [0, 3, 15, 15, 23], K, G, F32)
+    off.copy_(torch.tensor(offsets, dtype=torch.int32))
     x[13, K - 3] = float("inf")
     v = tg.gemv_w4(x, W, sc, zeros=z, offsets=off, format=fmt, group=G)
     w = wv[2][:, K - 3]
