@@ -156,6 +156,47 @@ bool span_ok(int64_t nb, int64_t stride, int64_t rows, int64_t ld)
     return static_cast<__int128>(nb) * stride + static_cast<__int128>(rows) * ld < (static_cast<__int128>(1) << 56);
 }
 
+// Few tiles and a long contraction: workers share tiles.  The k-blocks of a
+// share, or 0 where tiles are not shared: as many shares as there are workers
+// for the average group's tiles (the one that arrives last adds them, 128 or
+// 64 KB each, so a share is 32 or 16 k-blocks at least), and a longer group's
+// tiles more of the same length.  (Two, three or four times as many, to even
+// out groups of unknown lengths, measured the same or more: wgrad, 32768 rows
+// of 8 groups, 256 x 1000: 35, 38, 46 and 49 us.)
+int64_t share_of(bool wgrad, bool pair, int64_t units, int64_t depth, int sms)
+{
+    const int64_t workers = pair ? sms / 2 : sms;
+    const int64_t least = pair ? 2 * SPLIT_DEPTH : SPLIT_DEPTH;
+    if (depth < 2 * least || units >= (wgrad ? 2 * workers : workers)) return 0;
+    return std::max(least, units <= workers ? cdiv(depth, workers / units) : cdiv(units * depth, workers));
+}
+
+// What a call takes with one-CTA tiles (128 x 128) or pairs (256 x 256), in
+// microseconds: turns of the workers over the tiles (rows mode: those of
+// groups that end anywhere in a tile) or shares, each a start, so much a
+// k-block, and where tiles are shared the adding.  The constants were fitted
+// to 350 calls of both kinds (1 to 32 uneven groups of 64 to 4096 rows, rows
+// mode K 64 to 4096 and N 256 to 4096, gradients 256 to 2048 x 256 to 4096):
+// the tiles it chooses take 0.4% longer than the better ones on average,
+// those of a rule by size (256 rows and enough pair tiles to fill half the
+// SMs) 4%, and up to half as long again: 8 groups of 256 rows, 4096 x 1000:
+// 42.9 us in one-CTA tiles, 28.1 in pairs; 32 of 192, 64 x 1000: 10.1, 15.4.
+double tiles_cost(bool wgrad, bool pair, int64_t S, int64_t M, int64_t N, int64_t K, int64_t groups, int sms)
+{
+    const double start = pair ? 4.3 : 0.7, block = pair ? 0.143 : 0.27, adding = pair ? 9.5 : 2.1;
+    const int64_t t = pair ? 256 : 128, workers = pair ? sms / 2 : sms;
+    const int64_t hit = std::max<int64_t>(1, groups < S ? groups : S);
+    const int64_t depth = wgrad ? cdiv(S / groups, BK) : cdiv(K, BK);
+    int64_t units = cdiv(N, t);
+    if (wgrad)
+        units *= groups * cdiv(M, t);
+    else
+        units *= groups > 1 ? std::max(hit, S / t + (hit + 1) / 2) : cdiv(S, t);
+    const int64_t share = share_of(wgrad, pair, units, depth, sms);
+    if (share == 0) return static_cast<double>(cdiv(units, workers)) * (start + block * depth);
+    return static_cast<double>(cdiv(units * cdiv(depth, share), workers)) * (start + block * share + (share < depth ? adding : 0.0));
+}
+
 // The options that apply here: cta_pair (1 or 2), force_pack, timeout_ns,
 // debug_stall (1), b_col_major; everything else has to be 0.
 bool options_ok(const tg_options *o, bool wgrad)
@@ -177,18 +218,12 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     tg_status st = host_stream(stream, &hs);
     if (st != TG_OK) return st;
 
-    // Tiles.  wgrad: pairs (256 x 256) where they fill half the SMs, else one
-    // CTA's 128 x 128.  Rows: 256 of a group by 256 columns for a pair where
-    // groups have that many on average and the tiles fill half the SMs; else
-    // one CTA's 128 columns by 128 rows, or 32 where groups have few (the ring
-    // is then deeper: weights are the traffic).
     const int64_t hit = groups < S ? groups : S;  // groups that have rows, at most
-    const int64_t depth = wgrad ? cdiv(S / groups, BK) : cdiv(K, BK);  // k-blocks of an (average) tile
-    bool pair;
-    if (wgrad)  // (or shares of them do)
-        pair = M > 128 && N > 128 && groups * cdiv(M, 256) * cdiv(N, 256) * std::max<int64_t>(1, depth / (2 * SPLIT_DEPTH)) >= hs.sms / 2;
-    else
-        pair = N > 128 && S >= 192 * groups && cdiv(S, 256) * cdiv(N, 256) >= hs.sms / 2;
+    // Tiles: 256 x 256 for a pair or 128 x 128 for one CTA, whichever is
+    // quicker by tiles_cost; rows mode takes 128 columns x 32 rows where groups
+    // have few (the ring is then deeper: weights are the traffic).
+    bool pair = N > 128 && (wgrad ? M > 128 : S > 32 * hit) &&
+                tiles_cost(wgrad, true, S, M, N, K, groups, hs.sms) < tiles_cost(wgrad, false, S, M, N, K, groups, hs.sms);
     if (opt && opt->cta_pair) pair = opt->cta_pair == 2;
     const bool few = !wgrad && !pair && S <= 32 * hit;
     const int64_t tile_m = pair ? 256 : 128, bn = pair ? 256 : few ? 32 : 128;
@@ -224,17 +259,9 @@ tg_status run_grouped(bool wgrad, Operand a, Operand b, bool b_k, void *D, const
     p.timeout_ns = opt && opt->timeout_ns ? opt->timeout_ns : HOST_TIMEOUT_NS;
     p.debug_stall = opt ? opt->debug_stall : 0;
 
-    // Few tiles and a long contraction: workers share tiles, as many shares as
-    // there are workers for the average group's (the one that arrives last adds
-    // them, 128 or 64 KB each, so a share is 32 or 16 k-blocks at least), and
-    // a longer group's tiles more of the same length.
-    const int64_t workers = pair ? hs.sms / 2 : hs.sms;
-    const int64_t least = pair ? 2 * SPLIT_DEPTH : SPLIT_DEPTH;
-    int64_t splits = 1, share = depth;
-    if (units < (wgrad ? 2 * workers : workers) && depth >= 2 * least) {
-        share = std::max(least, units <= workers ? cdiv(depth, workers / units) : cdiv(units * depth, workers));
-        splits = std::min<int64_t>(SPLIT_MOST, cdiv(wgrad ? cdiv(S, BK) : depth, share));
-    }
+    const int64_t depth = wgrad ? cdiv(S / groups, BK) : cdiv(K, BK);
+    const int64_t share = share_of(wgrad, pair, units, depth, hs.sms);
+    const int64_t splits = share == 0 ? 1 : std::min<int64_t>(SPLIT_MOST, cdiv(wgrad ? cdiv(S, BK) : depth, share));
     p.part_blocks = static_cast<int32_t>(share);
     p.splits = static_cast<int32_t>(splits);
     const int64_t part_tiles = splits > 1 ? units * (pair ? 2 : 1) : 0;
