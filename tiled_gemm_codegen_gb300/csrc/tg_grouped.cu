@@ -15,7 +15,7 @@ namespace {
 
 constexpr int64_t GROUPED_EXTENT = INT32_MAX - 1024;  // a tile past the end stays in range
 constexpr int64_t PITCH_LIMIT = int64_t(1) << 40;
-constexpr int64_t SPLIT_DEPTH = 16;  // k-blocks of a share at least (pairs: twice that)
+constexpr int64_t SPLIT_DEPTH = 12;  // k-blocks of a share at least (pairs: twice that)
 constexpr int64_t SPLIT_MOST = 16;   // shares of a tile at most
 
 using GroupedKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const GroupedParams);
@@ -159,7 +159,8 @@ bool span_ok(int64_t nb, int64_t stride, int64_t rows, int64_t ld)
 // Few tiles and a long contraction: workers share tiles.  The k-blocks of a
 // share, or 0 where tiles are not shared: as many shares as there are workers
 // for the average group's tiles (the one that arrives last adds them, 128 or
-// 64 KB each, so a share is 32 or 16 k-blocks at least), and a longer group's
+// 64 KB each, so a share is 24 or 12 k-blocks at least: with 16, 8 or 4 for 12,
+// 22 short calls take 3%, 5% and 10% longer), and a longer group's
 // tiles more of the same length.  (Two, three or four times as many, to even
 // out groups of unknown lengths, measured the same or more: wgrad, 32768 rows
 // of 8 groups, 256 x 1000: 35, 38, 46 and 49 us.)
