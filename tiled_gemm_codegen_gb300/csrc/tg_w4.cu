@@ -560,11 +560,11 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
 // 2^114 (E2M1: 2^124) that no fp32 power of two would bring back, is computed
 // value by value instead.
 //
-// Measured: 1 row, 8192 x 28672 int4 by 128, 121 MB: 27.6 us on the GPU; between
+// Measured: 1 row, 8192 x 28672 int4 by 128, 121 MB: 27.4 us on the GPU; between
 // sizes the weights stream at 6.0 TB/s (88% of a plain copy), and start, first
 // boxes, activations and last tiles are 5.7 us of it.  E2M1 has a scale for every
 // 32 codes: 43 us for the same codes.  32 rows over 20 of 64 experts, 2048 x
-// 1408 E2M1, 31 MB: 17.6-18 us, of which the start and a CTA's few turns are
+// 1408 E2M1, 31 MB: 18-18.8 us, of which the start and a CTA's few turns are
 // most.  Tried: eight turns' activation loads in flight instead of four (3-4
 // us slower, registers), E2M1's sign moved by a multiply-add instead of a
 // shift and mask (no change), the hardware's E2M1 conversion (twice the time).
@@ -736,7 +736,16 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             zero_rows(a, n, min(n + 256, a.N), threads);
     };
     const int64_t tiles = static_cast<int64_t>(count_passes(a, p.xt)) * p.slices * p.tiles_n;
-    const int64_t first = blockIdx.x * tiles / gridDim.x, last = (blockIdx.x + 1) * tiles / gridDim.x;
+    // (a 64-bit division costs some hundred cycles of every call's start)
+    int64_t first, last;
+    if (tiles <= 0xFFFFFFFFll / 1024 && gridDim.x < 1024) {
+        const uint32_t n = static_cast<uint32_t>(tiles);
+        first = blockIdx.x * n / gridDim.x;
+        last = (blockIdx.x + 1) * n / gridDim.x;
+    } else {
+        first = blockIdx.x * tiles / gridDim.x;
+        last = (blockIdx.x + 1) * tiles / gridDim.x;
+    }
     if (first == last) {
         if (warp < p.warps) clear();
         return;
@@ -756,9 +765,10 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             }
         }
     };
-    const int64_t first_slice = first / p.tiles_n;
-    const At at0{static_cast<int32_t>(last - first), static_cast<int32_t>(first_slice / p.slices), static_cast<int32_t>(first_slice % p.slices),
-                 static_cast<int32_t>(first % p.tiles_n)};
+    const int32_t first_slice = static_cast<int32_t>(first <= INT32_MAX ? static_cast<int32_t>(first) / p.tiles_n : first / p.tiles_n);
+    const int32_t first_pass = p.slices == 1 ? first_slice : first_slice / p.slices;
+    const At at0{static_cast<int32_t>(last - first), first_pass, first_slice - first_pass * p.slices,
+                 static_cast<int32_t>(first - static_cast<int64_t>(first_slice) * p.tiles_n)};
     if (warp == p.warps) {
         // ------------------------------------------------ producer
         // Lane l keeps warp l's ring full: a box at a time, whenever the
