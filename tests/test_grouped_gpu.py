@@ -209,6 +209,28 @@ def test_random_values(sizes, K, N, dtype):
             assert within(got, want, PER_ELEM * np.sqrt(depth) * np.abs(want).max(), dtype)
 
 
+@pytest.mark.parametrize("size", [200, 33, 95])
+@pytest.mark.parametrize("N", [384, 392, 700])
+@pytest.mark.parametrize("pair", [1, 2])
+def test_bf16_boxes_stored_plainly_between_boxes_stored_by_tma(size, N, pair):
+    """A group's last rows, and a box cut off by the row's end, leave their
+    staging box by plain stores, the others by asynchronous ones that may
+    still read theirs: short products over many groups, several tiles a
+    worker, every element of every call."""
+    groups, K = 160, 64
+    S, off = groups * size, _offsets([size] * groups)
+    A, _ = _rand((S, K), 60, True)
+    B, _ = _rand((groups, K, N), 61, True)
+    want = torch.bmm(A.float().view(groups, size, K), B.float()).view(S, N).to(BF)  # integers: exact before the rounding
+    opts, D = tg.make_options(cta_pair=pair), torch.empty(S, N, dtype=BF, device=dev())
+    wrong = torch.zeros((), dtype=torch.int64, device=dev())
+    for _ in range(200):
+        D.fill_(float("nan"))
+        tg.gemm_grouped(A, B, off, D, options=opts)
+        wrong += (D != want).sum()
+    assert int(wrong) == 0
+
+
 @pytest.mark.parametrize("activation", ["none", "relu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("per_group", [False, True])
 @pytest.mark.parametrize("dtype", [F32, BF])

@@ -601,7 +601,9 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
         // Address of 16-byte unit u of box row r.
         auto unit_at = [&](int r, int u) { return box + r * EPI_ROW_BYTES + ((u ^ (r & 7)) << 4); };
 
-        // The next box may be written: its last TMA store has read it.
+        // The next box may be written: its last TMA store has read it.  A duo
+        // has two boxes in turn and lets the other one's store run on, which
+        // counts on one bulk group a box (see flush).
         auto box_free = [&]() {
             if (duo) {
                 box = box == boxes ? boxes + EPI_BOX_BYTES : boxes;
@@ -632,6 +634,9 @@ __global__ void __launch_bounds__(WGRAD ? GROUPED_WGRAD_THREADS : GROUPED_THREAD
                 }
                 return;
             }
+            // a plain box commits a group too, an empty one: without it the one
+            // group that box_free leaves running could be of the box it hands out
+            if (duo && p.epi_tma && sub == 0 && lane == 0) ptx::bulk_commit_group();
             const int32_t nrows = min(EPI_ROWS, limit - row0);
             const int r_first = duo ? sub : 0, r_step = duo ? 2 : 1;  // duo: every other row (or four) each
             uint8_t *dst = static_cast<uint8_t *>(p.D) +
