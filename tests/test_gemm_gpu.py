@@ -617,6 +617,28 @@ def test_store_never_writes_row_padding(N, out, direct):
         assert np.array_equal(got, torch.from_numpy(want).to(torch.bfloat16).double().numpy())
 
 
+@pytest.mark.parametrize("cfg", CONFIGS, ids=_cfg_id)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_boxes_stored_plainly_between_boxes_stored_by_tma(cfg, out):
+    """A row that ends off 16 bytes: its last box leaves by plain stores, the
+    boxes before and after it by asynchronous ones that may still read
+    theirs.  Several short tiles a CTA, every element of every call."""
+    bn, pair = cfg
+    M, N, K, ldc = 2560, 1413, 64, 1424
+    A, B = (t.to(dev()) for t in synth.make_int_inputs(1, M, N, K, seed=_seed(M, N, K, bn)))
+    dt = torch.float32 if out == "f32" else torch.bfloat16
+    want = (A.float() @ B.float()).to(dt)  # integers: exact before the rounding
+    store = torch.empty(M, ldc, dtype=dt, device=dev())
+    opts = tg.make_options(block_n=bn, cta_pair=pair, direct=1)
+    wrong = torch.zeros((), dtype=torch.int64, device=dev())
+    for _ in range(100):
+        store.fill_(float("nan"))
+        (tg.gemm if out == "f32" else tg.gemm_fused)(A, B, store[:, :N], options=opts)
+        wrong += (store[:, :N] != want).sum() + (~torch.isnan(store[:, N:])).sum()
+    assert tg.device_error() == tg.TG_OK
+    assert int(wrong) == 0
+
+
 # Outputs of at most 64 rows take ring slots of 64 rows of A (8 slots at
 # width 128, 6 at width 192); the MMA reads the upper 64 rows from the memory
 # after the slot and their accumulator rows are never stored.

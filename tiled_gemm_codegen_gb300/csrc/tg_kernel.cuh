@@ -791,6 +791,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // That box goes out with plain stores instead.
             const int32_t per16 = p.out_bf16 ? 8 : 4;
             const bool tma = p.epi_tma && (col0 + EPI_CHUNK <= p.N || p.N % per16 == 0);
+            // (it commits a bulk group all the same, an empty one: the wait
+            // above counts one group a box)
+            if (p.epi_tma && !tma && lane == 0) ptx::bulk_commit_group();
             if (!p.out_bf16) {
                 // Row `lane` of the box; its 16-byte unit jj is stored at unit
                 // jj ^ (lane mod 8): the 128B swizzle (Swizzle(2,3,3) on fp32).
