@@ -255,6 +255,41 @@ def test_infinite_activations_reach_int4_as_the_formula_says():
         assert np.all(np.abs(y[t] - want) <= 2 * (K + 10) * U32 * mag)
 
 
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS[:5])
+@pytest.mark.parametrize("K,N,sizes", [(512, 28672, [16]), (512, 28672, [64]), (256, 9000, [16, 0, 1, 8, 40]), (9216, 2048, [40])])
+def test_infinities_and_large_values_in_the_rows_of_several_passes(fmt, G, zeros, K, N, sizes):
+    """Workers go on from one pass of eight rows, or slice of K, to the next:
+    infinities and magnitudes from 2^116 in some rows of each, every column
+    of every row, several calls alike."""
+    S, groups = sum(sizes), len(sizes)
+    W, sc, z, wv = _weights(groups, N, K, fmt, G, K + N, zeros)
+    x, xv = _x(S, K, 19)
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    inf, large = list(range(3, S, 8)), list(range(5, S, 16))
+    at = [(t * 37) % K for t in range(S)]
+    for t in inf:
+        x[t, at[t]] = xv[t, at[t]] = float("inf") if t % 3 else float("-inf")
+    for t in large:
+        x[t, at[t]] = 2.0 ** 116
+        xv[t, at[t]] = 2.0 ** 116
+    offsets = torch.from_numpy(off).int().to(dev())
+    y = tg.gemv_w4(x, W, sc, zeros=z, offsets=offsets, format=fmt, group=G)
+    for _ in range(3):
+        again = tg.gemv_w4(x, W, sc, zeros=z, offsets=offsets, format=fmt, group=G)
+        assert torch.equal(torch.nan_to_num(again, nan=7e30), torch.nan_to_num(y, nan=7e30))
+    y = y.cpu().double().numpy()
+    bound = 2 * (K + -(-K // G) + 2) * U32
+    for g in range(groups):
+        for t in range(off[g], off[g + 1]):
+            if t in inf:
+                w = wv[g][:, at[t]] * np.sign(xv[t, at[t]])
+                assert np.array_equal(np.isnan(y[t]), w == 0)
+                assert np.array_equal(y[t][w != 0], np.where(w > 0, np.inf, -np.inf)[w != 0])
+            else:
+                want, mag = xv[t] @ wv[g].T, np.abs(xv[t]) @ np.abs(wv[g]).T
+                assert np.all(np.abs(y[t] - want) <= bound * mag)
+
+
 @pytest.mark.parametrize("power", [-120, -60, 60, 110, 124])
 def test_activations_of_any_magnitude(power):
     """Rows scaled by powers of two give results scaled by the same, exactly

@@ -703,7 +703,10 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * W4S_WARPS * W4S_STAGES];  // a warp's full, then its empty ones
     __shared__ int32_t aborted;
-    __shared__ int32_t x_odd[8];  // the row holds an infinity, NaN or a magnitude too large
+    // The row holds an infinity, NaN or a magnitude too large.  Two sets in turn:
+    // the next pass's is cleared while warps may still be storing the last tile
+    // of this one, which read this one's.
+    __shared__ int32_t x_odd[2][8];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_addr(smem);
@@ -873,6 +876,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
     // and step: eight consecutive ones paired as the codes of a word are; and
     // their sums by group of codes, times the code's unit (and by 8, the zero
     // point, where there is no other).  A warp takes the 256 of a row and step.
+    int32_t odd_set = 0;  // the set of x_odd in use
     auto stage_x = [&](int32_t r0, int32_t nx, int32_t k0, int32_t steps) {
         const bool aligned = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(2 * a.ldx)) & 15u) == 0;
         constexpr int U = 4;  // turns whose loads are in flight together
@@ -911,7 +915,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
                 }
                 most = __reduce_max_sync(0xffffffffu, most);
                 const int32_t up = x_up(most), back = W4_UNIT_UP<E2M1> - up;
-                if (odd || back > 127) x_odd[t] = 1;
+                if (odd || back > 127) x_odd[odd_set][t] = 1;
                 const float mul = power_of_two(up);
                 float f[8], sum = 0.0f;
 #pragma unroll
@@ -946,7 +950,8 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
     bool fresh = true;  // the tile's activations are not in shared memory yet
     for (int b = 0; at.left > 0; b ^= 1) {
         if (fresh) {
-            if (threadIdx.x < 8) x_odd[threadIdx.x] = 0;
+            odd_set ^= 1;
+            if (threadIdx.x < 8) x_odd[odd_set][threadIdx.x] = 0;
             ptx::named_barrier_sync(1, threads);  // every warp is done with the old ones
             g = g_next;
             r0 = r0_next;
@@ -1126,7 +1131,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
         };
         for (int i = warp; i < teams * nx; i += p.warps) {
             const int tm = i / nx, tok = i - tm * nx, n = tm * W4S_ROWS + lane;
-            if (x_odd[tok]) {
+            if (x_odd[odd_set][tok]) {
                 for (int r = 0; r < W4S_ROWS && n0 + tm * W4S_ROWS + r < a.N; ++r) {
                     const float v = row_dot<E2M1>(a, g, n0 + tm * W4S_ROWS + r, r0 + tok, k0, min(a.K, k0 + p.steps * W4_STEP));
                     if (lane == 0) put(tok, tm * W4S_ROWS + r, v);
