@@ -372,3 +372,39 @@ def test_slices_of_the_contraction(fmt, G, zeros):
     assert torch.equal(torch.isnan(v[13]).cpu(), torch.from_numpy(w == 0))
     keep = [i for i in range(S) if i != 13]
     assert torch.equal(v[keep], y[keep])
+
+
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+@pytest.mark.parametrize("K,N,sizes", [(512, 9000, [16]), (4096, 600, [3, 0, 9]), (9216, 2048, [40])])
+def test_watchdog(fmt, G, zeros, K, N, sizes):
+    """The checks build, whose first warp's weights are never loaded: the waits
+    run out after their limit, whole blocks leave (whoever noticed first),
+    tg_device_error says so, and the next call is right."""
+    import ctypes
+
+    lib = tg.load_checks()
+    lib.tg_gemv_w4_watchdog.argtypes, lib.tg_gemv_w4_watchdog.restype = [ctypes.c_int32, ctypes.c_uint64], None
+    S, groups, runs = sum(sizes), len(sizes), -(-K // G)
+    W, sc, z, wv = _weights(groups, N, K, fmt, G, 39, zeros)
+    x, xv = _x(S, K, 20)
+    offsets = np.concatenate([[0], np.cumsum(sizes)])
+    off = torch.from_numpy(offsets).int().to(dev())
+    y = torch.empty(S, N, device=dev())
+    s = torch.cuda.current_stream().cuda_stream
+
+    def call():
+        return lib.tg_gemv_w4(x.data_ptr(), K, W.data_ptr(), K, N * K, sc.data_ptr(), runs, N * runs,
+                              z.data_ptr() if z is not None else None, runs, N * runs, tg.W4_FORMATS[fmt], G, off.data_ptr(), groups,
+                              S, N, K, y.data_ptr(), N, 0, s)
+
+    try:
+        for _ in range(10):
+            lib.tg_gemv_w4_watchdog(1, 2_000_000)
+            assert call() == tg.TG_OK
+            assert lib.tg_device_error(s) == tg.TG_ERR_TIMEOUT
+    finally:
+        lib.tg_gemv_w4_watchdog(0, 0)
+    assert lib.tg_device_error(s) == tg.TG_OK
+    assert call() == tg.TG_OK
+    assert lib.tg_device_error(s) == tg.TG_OK
+    _check(y, xv, wv, offsets, K, G, F32)

@@ -56,6 +56,7 @@
 #pragma once
 
 #include "tg_kernel.cuh"
+#include "tg_sync.cuh"
 
 namespace tg {
 
@@ -255,21 +256,6 @@ __device__ __forceinline__ void grouped_epilogue(const GroupedParams &p, uint32_
     }
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(x[j]);
-}
-
-// `threads` epilogue threads agree on a predicate (named barrier `id`).
-__device__ __forceinline__ bool agree(bool pred, uint32_t id, uint32_t threads)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.and.pred q, %2, %3, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(pred)), "r"(id), "r"(threads)
-        : "memory");
-    return r != 0;
 }
 
 constexpr int GROUPED_EPI_WARPS = 8;

@@ -17,6 +17,7 @@
 #include "tg_gemm.h"
 #include "tg_host_api.h"
 #include "tg_ptx.cuh"
+#include "tg_sync.cuh"
 
 #define TG_API extern "C" __attribute__((visibility("default")))
 
@@ -587,6 +588,9 @@ struct W4Stream {
     float *partials;           // slices > 1: [slice][S][N]
     uint32_t *err;
     uint64_t timeout_ns;
+#ifdef TG_DEBUG_CHECKS
+    int32_t stall;  // watchdog self-test: the first warp's boxes are never asked for
+#endif
 };
 
 constexpr int W4S_ROWS = 32;
@@ -798,8 +802,13 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             while (__any_sync(0xffffffffu, i < each)) {
                 bool moved = false;
                 if (i < each && ptx::mbar_try_wait(l_empty + 8u * slot, parity)) {
-                    ptx::mbar_arrive_expect_tx(l_full + 8u * slot, W4S_BOX);
-                    ptx::tma_load_3d(l_ring + slot * W4S_BOX, &tmW, l_full + 8u * slot, (step0 + l_part + i * p.wk) * (W4_STEP / 2), n0, g);
+#ifdef TG_DEBUG_CHECKS
+                    if (!p.stall || lane > 0)
+#endif
+                    {
+                        ptx::mbar_arrive_expect_tx(l_full + 8u * slot, W4S_BOX);
+                        ptx::tma_load_3d(l_ring + slot * W4S_BOX, &tmW, l_full + 8u * slot, (step0 + l_part + i * p.wk) * (W4_STEP / 2), n0, g);
+                    }
                     ++i;
                     moved = true;
                     if (++slot == static_cast<uint32_t>(p.stages)) {
@@ -1119,8 +1128,10 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             }
         }
         cp_async_wait<0>();
-        ptx::named_barrier_sync(1, threads);  // the sums, and the next tile's scales
-        if (aborted) return;  // (the producer waits for the boxes on their way)
+        // The sums, and the next tile's scales, are there.  The warps leave as one
+        // where a wait has run out: the producer may say so between two warps'
+        // reads of it.  (It waits for the boxes on their way itself.)
+        if (!agree(*reinterpret_cast<volatile int32_t *>(&aborted) == 0, 1, threads)) return;
         // A warp: the 32 weight rows of a team for one activation row a turn,
         // to y or, where there are more slices, to scratch.
         auto put = [&](int tok, int n, float v) {
@@ -1328,6 +1339,14 @@ Bytes bytes_of(const void *p, int64_t nb, int64_t stride, int64_t rows, int64_t 
 }
 bool meets(const Bytes &a, const Bytes &b) { return a.lo < b.hi && b.lo < a.hi; }
 
+#ifdef TG_DEBUG_CHECKS
+// What tg_gemv_w4_watchdog set for the calls after it (under the host mutex).
+struct {
+    int32_t stall = 0;
+    uint64_t timeout_ns = 0;
+} g_watchdog;
+#endif
+
 bool pitch_ok(int64_t ld, int64_t cols, int64_t stride)
 {
     return ld >= cols && ld <= PITCH_LIMIT && stride >= 0 && stride <= PITCH_LIMIT;
@@ -1337,6 +1356,17 @@ bool pitch_ok(int64_t ld, int64_t cols, int64_t stride)
 }  // namespace tg
 
 using namespace tg;
+
+#ifdef TG_DEBUG_CHECKS
+// Of the checks build alone, as tg_gemv_w4 takes no options: the watchdog limit
+// of later calls (0: the usual one) and whether their waits are made to run out.
+TG_API void tg_gemv_w4_watchdog(int32_t stall, uint64_t timeout_ns)
+{
+    std::lock_guard<std::mutex> lock(host_mutex());
+    g_watchdog.stall = stall;
+    g_watchdog.timeout_ns = timeout_ns;
+}
+#endif
 
 TG_API tg_status tg_gemv_w4(const void *x, int64_t ldx, const void *W, int64_t ldw, int64_t strideW, const void *scales,
                             int64_t ld_s, int64_t stride_s, const uint8_t *zeros, int64_t ld_z, int64_t stride_z,
@@ -1413,6 +1443,10 @@ TG_API tg_status tg_gemv_w4(const void *x, int64_t ldx, const void *W, int64_t l
                 p.w_shared = shared_w;
                 p.err = hs.err;
                 p.timeout_ns = HOST_TIMEOUT_NS;
+#ifdef TG_DEBUG_CHECKS
+                p.stall = g_watchdog.stall;
+                if (g_watchdog.timeout_ns) p.timeout_ns = g_watchdog.timeout_ns;
+#endif
                 if (p.slices > 1) {
                     void *scratch = nullptr;
                     const tg_status ws = host_arena(hs, static_cast<size_t>(p.slices) * S * N * 4, &scratch);
