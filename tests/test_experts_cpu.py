@@ -135,3 +135,113 @@ def test_w4_refusals(lib):
         assert call(**kw) == INVALID, kw
     assert call(groups=70000, S=70000) == UNSUPPORTED
     assert call(S=0) == tg.TG_OK and call(N=0) == tg.TG_OK
+
+
+class _OnGpu:
+    """A CPU tensor that says it is on the GPU: what the wrappers read off it
+    before a call."""
+
+    def __init__(self, t):
+        self._t = t
+
+    is_cuda = True
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+    def get_device(self):
+        return 0
+
+
+BF, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _order(T, k, E):
+    n = dict(dtype=I32)
+    return tg.ExpertOrder(*(_OnGpu(t) for t in (torch.zeros(E + 1, **n), torch.zeros(T * k, **n), torch.zeros(T, k, **n))))
+
+
+def _shared_rows(rows, cols, dtype):
+    """The ways rows may share memory, the first two made by expand."""
+    yield torch.zeros(cols, dtype=dtype).expand(rows, cols)
+    yield torch.zeros(1, cols, dtype=dtype).expand(rows, cols)
+    yield torch.zeros(rows * cols, dtype=dtype).as_strided((rows, cols), (cols - 1, 1))
+
+
+def test_rows_that_share_memory_are_refused():
+    """Read with the row length for a pitch they would be read, or written,
+    past their storage: an expanded gradient, expanded weights, one row of
+    scales for all.  The refusal comes before any CUDA call."""
+    T, k, E, D = 6, 3, 4, 8
+    z = lambda *s, dtype=BF: _OnGpu(torch.zeros(*s, dtype=dtype))  # noqa: E731
+    order, ids = _order(T, k, E), z(T, k, dtype=torch.int64)
+    off = z(E + 1, dtype=I32)
+
+    def check(call, rows, cols, dtype):
+        for t in _shared_rows(rows, cols, dtype):
+            with pytest.raises(ValueError, match="contiguous"):
+                call(_OnGpu(t))
+
+    for c in (D, 1):
+        check(lambda t, c=c: tg.expert_combine_grad(t, z(T * k, c), order, None), T, c, BF)
+        check(lambda t, c=c: tg.expert_combine_grad(z(T, c), t, order, None), T * k, c, BF)
+        check(lambda t, c=c: tg.expert_combine_grad(z(T, c), z(T * k, c), order, None, dys=t), T * k, c, BF)
+        check(lambda t: tg.expert_combine(t, order), T * k, c, F32)
+        check(lambda t, c=c: tg.expert_combine(z(T * k, c), order, y=t), T, c, BF)
+        check(lambda t: tg.expert_gather(t, order), T, c, BF)
+        check(lambda t, c=c: tg.expert_dispatch(z(T, c), ids, E, xs=t, order=order), T * k, c, BF)
+        check(lambda t, c=c: tg.gemm_grouped(t, z(E, c, 16), off), 20, c, BF)
+        check(lambda t, c=c: tg.gemm_grouped(z(20, 16), z(E, 16, c), off, t), 20, c, F32)
+        check(lambda t, c=c: tg.gemm_grouped_wgrad(t, z(20, 16), off), 20, c, BF)
+    check(lambda t: tg.expert_combine(z(T * k, D), order, t), T, k, F32)
+    check(lambda t: tg.expert_combine_grad(z(T, D), z(T * k, D), order, t), T, k, F32)
+    check(lambda t: tg.expert_combine_grad(z(T, D), z(T * k, D), order, None, dys=z(T * k, D), dweights=t), T, k, F32)
+    check(lambda t: tg.expert_sort(t, E, order=order), T, k, torch.int64)
+    check(lambda t: tg.expert_sort(t, E, order=_order(T, 1, E)), T, 1, I32)
+    check(lambda t: tg.gemv_w4(t, z(5, 32, dtype=U8), z(5, 1), group=64), 4, 64, BF)
+    check(lambda t: tg.gemv_w4(z(4, 64), t, z(5, 1), group=64), 5, 32, U8)
+    check(lambda t: tg.gemv_w4(z(4, 64), z(5, 32, dtype=U8), t, group=32), 5, 2, BF)
+    check(lambda t: tg.gemv_w4(z(4, 64), z(5, 32, dtype=U8), t, group=64), 5, 1, BF)
+    check(lambda t: tg.gemv_w4(z(4, 64), z(5, 32, dtype=U8), z(5, 2), zeros=t, group=32), 5, 2, U8)
+    check(lambda t: tg.gemv_w4(z(4, 64), z(5, 32, dtype=U8), z(5, 2), y=t, group=32), 4, 5, F32)
+    # matrices of a stack whose rows (or, stored the other way, columns) lie 0 apart
+    for B in (torch.zeros(16, dtype=BF).expand(E, 8, 16), torch.zeros(8, 1, dtype=BF).expand(E, 8, 16),
+              torch.zeros(E, 8, 1, dtype=BF).expand(E, 8, 16), torch.zeros(E, 1, 1, dtype=BF).expand(E, 1, 16),
+              torch.zeros(E, 1, 1, dtype=BF).expand(E, 8, 1)):
+        with pytest.raises(ValueError):
+            tg.gemm_grouped(z(20, B.shape[1]), _OnGpu(B), off)
+    with pytest.raises(ValueError):
+        tg.gemm_grouped_wgrad(z(20, 8), z(20, 16), off, _OnGpu(torch.zeros(E, 1, 16).expand(E, 8, 16)))
+
+
+def test_pitches_that_are_read_off_tensors():
+    """Rows apart by their length or more keep their pitch, single rows and
+    columns any; the matrices of a stack may be one."""
+    from tiled_gemm_codegen_gb300 import experts as ex
+
+    t = lambda *s: torch.zeros(*s, dtype=BF)  # noqa: E731
+    rows = lambda v: ex._rows(_OnGpu(v), "x")[1:4]  # noqa: E731
+    assert rows(t(5, 8)) == (5, 8, 8) and rows(t(5, 12)[:, 2:10]) == (5, 8, 12) and rows(t(10, 8)[::2]) == (5, 8, 16)
+    assert rows(t(8).expand(1, 8)) == (1, 8, 8) and rows(t(5, 7)[:, :1]) == (5, 1, 7) and rows(t(5, 1)) == (5, 1, 1)
+    assert rows(t(0, 8)) == (0, 8, 8) and rows(t(5, 0))[:2] == (5, 0)
+    mats = lambda v: ex._matrices(_OnGpu(v), "B")[1:]  # noqa: E731
+    assert mats(t(3, 4, 6)) == (3, 4, 6, 6, 24, False) and mats(t(3, 6, 4).transpose(1, 2)) == (3, 4, 6, 4, 24, True)
+    assert mats(t(4, 6).expand(3, 4, 6)) == (3, 4, 6, 6, 0, False) and mats(t(3, 6, 9).transpose(1, 2)[:, :4]) == (3, 4, 6, 9, 54, True)
+    assert mats(t(3, 6, 1).transpose(1, 2)) in ((3, 1, 6, 1, 6, True), (3, 1, 6, 6, 6, False))
+    assert mats(t(3, 1, 6)) == (3, 1, 6, 6, 6, False) and mats(t(3, 4, 1)) == (3, 4, 1, 1, 4, False)
+
+
+def test_gemm_operands_whose_rows_share_memory_are_refused():
+    A, B = torch.zeros(8, dtype=BF).expand(4, 8), torch.zeros(8, 16, dtype=BF)
+    for a, b, c in ((A, B, None), (B.t().contiguous(), A.contiguous().t()[:, :1].expand(8, 4), None),
+                    (torch.zeros(4, 8, dtype=BF), B, torch.zeros(16).expand(4, 16))):
+        with pytest.raises(ValueError):
+            tg.gemm_host(a, b, c)
+    with pytest.raises(ValueError, match="contiguous"):
+        tg.gemm(_OnGpu(A), _OnGpu(B))
+    with pytest.raises(ValueError, match="contiguous"):  # stored column-major, columns 0 apart
+        tg.gemm(_OnGpu(torch.zeros(4, 8, dtype=BF)), _OnGpu(torch.zeros(8, 1, dtype=BF).expand(8, 16)))
+    with pytest.raises(ValueError, match="contiguous"):
+        tg.gemm(_OnGpu(torch.zeros(4, 8, dtype=BF)), _OnGpu(B), _OnGpu(torch.zeros(16).expand(4, 16)))
+    with pytest.raises(ValueError, match="contiguous"):
+        tg.gemm_fp8(_OnGpu(torch.zeros(32).to(torch.float8_e4m3fn).expand(4, 32)), _OnGpu(torch.zeros(16, 32).to(torch.float8_e4m3fn)))

@@ -143,6 +143,16 @@ def _stream_ptr(stream):
     return stream.cuda_stream
 
 
+def _pitch(stride, rows, cols, what):
+    """The pitch of `rows` rows of `cols` elements.  Rows that share memory (an
+    expanded tensor's lie 0 apart) have none that the library takes."""
+    if rows <= 1:
+        return cols if cols > 1 else 1
+    if stride >= cols:
+        return stride
+    raise ValueError(f"{what} has rows of {cols} elements {stride} apart: pass a copy (contiguous())")
+
+
 def _geometry(t, shape, st, what):
     """_operand_geometry on the tensor's shape and strides, read once (each
     read is a call into the framework)."""
@@ -152,12 +162,12 @@ def _geometry(t, shape, st, what):
     rows, cols = shape[-2], shape[-1]
     if st[-1] != 1 and cols > 1:
         raise ValueError(f"{what} must have unit stride in its last dimension")
-    ld = st[-2] if rows > 1 else max(cols, 1)
+    ld = _pitch(st[-2], rows, cols, what)
     if nd == 3:
         batch, sb = shape[0], (st[0] if shape[0] > 1 else 0)
     else:
         batch, sb = 1, 0
-    return t.data_ptr(), rows, cols, max(ld, cols), batch, sb
+    return t.data_ptr(), rows, cols, ld, batch, sb
 
 
 def _operand_geometry(t, rows_dim, what):
@@ -174,7 +184,7 @@ def _operand(t, what):
     nd = len(shape)
     rows, cols = shape[-2], shape[-1]
     if nd in (2, 3) and cols > 1 and st[-1] != 1 and (st[-2] == 1 or rows == 1):
-        ld = max(st[-1], rows, 1)
+        ld = _pitch(st[-1], cols, max(rows, 1), what)
         batch, sb = (shape[0], st[0] if shape[0] > 1 else 0) if nd == 3 else (1, 0)
         return t.data_ptr(), rows, cols, ld, batch, sb, True
     return (*_geometry(t, shape, st, what), False)

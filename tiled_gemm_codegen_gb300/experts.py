@@ -5,7 +5,10 @@ expert and back, the experts' products over the sorted rows, and products with
 As the rest of the package this is a thin binding of ``include/tg_gemm.h``:
 pointers, shapes and strides are read off the tensors, and all arithmetic
 happens in the CUDA library.  Calls are asynchronous on ``stream`` (default:
-torch's current stream).
+torch's current stream).  A row starts behind the one before it: tensors whose
+rows share memory, as ``expand`` makes them (the gradient of a sum over
+tokens, uniform weights), are refused and go in as a copy (``contiguous()``);
+the matrices of a stack may share theirs.
 """
 from __future__ import annotations
 
@@ -13,7 +16,7 @@ import ctypes
 
 import torch
 
-from . import ACTIVATIONS, TgError, _stream_ptr, _with_layout
+from . import ACTIVATIONS, TgError, _pitch, _stream_ptr, _with_layout
 from ._abi import TG_BF16, TG_F32, TG_OK, TG_W4_E2M1, TG_W4_INT4, load, tg_epilogue, tg_options
 
 __all__ = ["ExpertOrder", "expert_sort", "expert_dispatch", "expert_gather", "expert_combine", "expert_combine_grad",
@@ -100,7 +103,7 @@ def _rows(t, what, rows=None, cols=None):
     n, c = shape
     if st[1] != 1 and c > 1 and n:
         raise ValueError(f"{what} must have unit stride in its last dimension")
-    return t.data_ptr(), n, c, (st[0] if n > 1 and st[0] > c else c), dt
+    return t.data_ptr(), n, c, _pitch(st[0], n, c, what), dt
 
 
 def _weights(w, T, k, what="weights"):
@@ -113,7 +116,7 @@ def _weights(w, T, k, what="weights"):
     st = w.stride()
     if k > 1 and T and st[1] != 1:
         raise ValueError(f"{what} must have unit stride in its last dimension")
-    return w.data_ptr(), (st[0] if T > 1 and st[0] > k else k)
+    return w.data_ptr(), _pitch(st[0], T, k, what)
 
 
 def _ids(ids):
@@ -126,7 +129,7 @@ def _ids(ids):
     T, k = shape
     if k > 1 and T and st[1] != 1:
         raise ValueError("ids must have unit stride in their last dimension")
-    return ids.data_ptr(), (8 if dt == torch.int64 else 4), (st[0] if T > 1 and st[0] > k else k), T, k
+    return ids.data_ptr(), (8 if dt == torch.int64 else 4), _pitch(st[0], T, k, "ids"), T, k
 
 
 def expert_sort(ids, num_experts: int, *, order: ExpertOrder | None = None, stream=None) -> ExpertOrder:
@@ -232,10 +235,10 @@ def _matrices(t, what):
     g, r, c = shape
     sg = st[0] if g > 1 else 0
     if c > 1 and st[2] != 1 and (st[1] == 1 or r == 1):
-        return t.data_ptr(), g, r, c, (st[2] if st[2] > r else max(r, 1)), sg, True
+        return t.data_ptr(), g, r, c, _pitch(st[2], c, max(r, 1), what), sg, True
     if st[2] != 1 and c > 1 and t.numel():
         raise ValueError(f"{what} must have unit stride in one of its last two dimensions")
-    return t.data_ptr(), g, r, c, (st[1] if r > 1 and st[1] > c else max(c, 1)), sg, False
+    return t.data_ptr(), g, r, c, _pitch(st[1], r, c, what), sg, False
 
 
 def _plain_epilogue(out_type):
@@ -329,8 +332,7 @@ def _per_row(t, what, dtype, lead, cols):
     st = t.stride()
     if cols > 1 and st[-1] != 1:
         raise ValueError(f"{what} must have unit stride in its last dimension")
-    ld = st[-2] if lead[-1] > 1 and st[-2] > cols else max(cols, 1)
-    return t.data_ptr(), ld, (st[0] if len(lead) == 2 and lead[0] > 1 else 0)
+    return t.data_ptr(), _pitch(st[-2], lead[-1], cols, what), (st[0] if len(lead) == 2 and lead[0] > 1 else 0)
 
 
 def gemv_w4(x, W, scales, *, zeros=None, offsets=None, y=None, format: str = "int4", group: int | None = None,
