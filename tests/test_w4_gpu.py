@@ -322,6 +322,22 @@ def test_codes_past_four_gigabytes():
     _check(y[:, :64], xv, wv[:, :64], [0, 2], K, 128, F32)
 
 
+@pytest.mark.parametrize("K", [2 ** 30 + 1024, 2 ** 30 + 520, 2 ** 30 + 26])
+def test_rows_of_more_than_a_billion_codes(K):
+    """Byte counts of a row past 31 bits, for rows on 16, 4 and 1 bytes: few
+    activations are not zero, so the sums are exact."""
+    N, G = 2, 128
+    g = torch.Generator(device=dev()).manual_seed(40)
+    W = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, generator=g, device=dev())
+    sc = torch.ones(N, -(-K // G), dtype=BF, device=dev())
+    x = torch.zeros(1, K, dtype=BF, device=dev())
+    at = torch.tensor([0, 1, 300, 513, 2 ** 20 + 7, 2 ** 29, 2 ** 30 - 1, 2 ** 30, K - 1], device=dev())
+    x[0, at] = torch.arange(1, 10, device=dev()).to(BF)
+    q = (W[:, at // 2].int() >> (4 * (at % 2))) & 15
+    want = ((q - 8) * torch.arange(1, 10, device=dev())).sum(1).float()
+    assert torch.equal(tg.gemv_w4(x, W, sc)[0], want)
+
+
 @pytest.mark.parametrize("power", [-120, 116, 125])
 def test_e2m1_activations_of_any_magnitude(power):
     K, N = 768, 40

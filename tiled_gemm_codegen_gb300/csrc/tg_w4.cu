@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
             for (int t = 0; t < nx; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int32_t xl = 2 * (a.K - k0) - (j * 32 + lane) * 4;
+                    const int32_t xl = 2 * min(a.K - k0, W4_STEP) - (j * 32 + lane) * 4;
                     cp_async4(dst + off_x + t * W4_XPITCH + (j * 32 + lane) * 4,
                               a.x + (r0 + t) * a.ldx + (xl > 0 ? k0 + (j * 32 + lane) * 2 : 0), max(0, min(4, xl)));
                 }
@@ -1258,6 +1258,7 @@ bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &be
         p.slices = (p.all_steps + p.steps - 1) / p.steps;
         if (p.slices != slices) continue;
         if (slices > 1 && static_cast<int64_t>(a.S) * a.N * slices * 4 > W4S_SCRATCH) break;
+        if (p.steps > SMEM_LIMIT / (W4_STEP * 2)) continue;  // not one row of activations fits (and 32 bits hold what follows)
         p.x_pitch = p.steps * W4_STEP * 2 + 64;
         // A lane reads a step's scales of a row at once, 4 to 16 bytes: rows lie
         // an odd number of such pieces apart, in different banks.
