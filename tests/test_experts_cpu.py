@@ -245,3 +245,18 @@ def test_gemm_operands_whose_rows_share_memory_are_refused():
         tg.gemm(_OnGpu(torch.zeros(4, 8, dtype=BF)), _OnGpu(B), _OnGpu(torch.zeros(16).expand(4, 16)))
     with pytest.raises(ValueError, match="contiguous"):
         tg.gemm_fp8(_OnGpu(torch.zeros(32).to(torch.float8_e4m3fn).expand(4, 32)), _OnGpu(torch.zeros(16, 32).to(torch.float8_e4m3fn)))
+
+
+def test_an_order_uses_the_tensors_it_shows():
+    """Its tensors cannot be replaced, and their addresses are read at each
+    call (storage that has moved is found where it is)."""
+    from tiled_gemm_codegen_gb300 import experts as ex
+
+    order = _order(4, 2, 3)
+    for name in ("offsets", "source", "slot"):
+        with pytest.raises(AttributeError):
+            setattr(order, name, getattr(order, name))
+    order.slot._t.set_(torch.ones(4, 2, dtype=I32))
+    assert ex._order(order)[1] == tuple(t.data_ptr() for t in order)
+    offsets, source, slot = order
+    assert offsets is order.offsets and source is order.source and slot is order.slot

@@ -50,9 +50,9 @@ class ExpertOrder:
     ``offsets`` [E + 1] (expert e's rows), ``source`` [T * k] (the flat
     assignment of each sorted row, -1 behind the last) and ``slot`` [T, k]
     (the sorted row of each assignment, -1 if dropped).  Unpacks as the
-    three of them."""
+    three of them, which stay the ones it was made of."""
 
-    __slots__ = ("offsets", "source", "slot", "shape", "_ptrs")
+    __slots__ = ("_tensors", "shape", "_on_gpu")
 
     def __init__(self, offsets, source, slot):
         for t, name in ((offsets, "offsets"), (source, "source"), (slot, "slot")):
@@ -60,13 +60,16 @@ class ExpertOrder:
                 raise TypeError(f"{name} must be a contiguous int32 tensor")
         if slot.dim() != 2 or slot.shape[1] < 1 or offsets.dim() != 1 or source.shape != (slot.numel(),) or offsets.numel() < 2:
             raise ValueError("an order holds offsets [E + 1], source [T * k] and slot [T, k]")
-        self.offsets, self.source, self.slot = offsets, source, slot
+        self._tensors = (offsets, source, slot)
         self.shape = (*slot.shape, offsets.numel() - 1)  # T, k, E
-        on_gpu = offsets.is_cuda and source.is_cuda and slot.is_cuda
-        self._ptrs = (offsets.data_ptr(), source.data_ptr(), slot.data_ptr()) if on_gpu else None
+        self._on_gpu = offsets.is_cuda and source.is_cuda and slot.is_cuda
+
+    offsets = property(lambda self: self._tensors[0])
+    source = property(lambda self: self._tensors[1])
+    slot = property(lambda self: self._tensors[2])
 
     def __iter__(self):
-        return iter((self.offsets, self.source, self.slot))
+        return iter(self._tensors)
 
     @classmethod
     def empty(cls, tokens: int, k: int, num_experts: int, device="cuda") -> "ExpertOrder":
@@ -83,12 +86,13 @@ def _check(st: int, what: str) -> None:
 
 def _order(order, shape=None):
     """((T, k, E), pointers) of an order on the GPU."""
-    if order._ptrs is None:
+    if not order._on_gpu:
         raise TypeError("the order's tensors must be on the GPU")
     if shape is not None and order.shape != shape:
         raise ValueError(f"the order is one of {order.shape[0]} x {order.shape[1]} assignments to {order.shape[2]} experts, "
                          f"not {shape[0]} x {shape[1]} to {shape[2]}")
-    return order.shape, order._ptrs
+    offsets, source, slot = order._tensors
+    return order.shape, (offsets.data_ptr(), source.data_ptr(), slot.data_ptr())
 
 
 def _rows(t, what, rows=None, cols=None):
