@@ -57,8 +57,11 @@
  *     workspace and set kernel attributes; a later call of the same or a
  *     smaller plan on the stream enqueues only kernel launches, so it can be
  *     captured into a CUDA graph and replayed (each replay reads the
- *     operands' current contents).  tg_gemm_host and tg_tune synchronise
- *     and cannot be captured.
+ *     operands' current contents).  A larger call on the stream later on
+ *     leaves the workspace that captured calls use in place (until
+ *     tg_shutdown); replays use the capturing stream's workspace, so they
+ *     and that stream's calls follow one another.  tg_gemm_host and tg_tune
+ *     synchronise and cannot be captured.
  */
 #ifndef TG_GEMM_H
 #define TG_GEMM_H

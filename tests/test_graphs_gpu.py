@@ -84,3 +84,57 @@ def test_graph_of_a_fused_epilogue_call():
     assert tg.device_error(s) == tg.TG_OK
     want = np.maximum(oracle_dense(A1, B1) + np.arange(N, dtype=np.float64), 0.0)
     assert np.array_equal(D.cpu().double().numpy(), want)
+
+
+def test_graphs_outlive_the_growth_of_their_streams_workspace():
+    """Calls with scratch and counters captured small, then the same calls
+    larger on the same stream, which outgrow its workspace, then what took
+    the place of freed memory; the first graph's replays give the first
+    results, touch nothing else, and so do the second's."""
+    s = torch.cuda.Stream()
+    E, k = 8, 2
+
+    def case(scale, seed):
+        M, N, K = 128 * scale, 250, 2048 * scale
+        A, B = (t.to(dev()) for t in synth.make_int_inputs(1, M, N, K, seed=seed))
+        T = 10000 * scale
+        ids = torch.randint(0, E, (T, k), generator=torch.Generator().manual_seed(seed)).to(dev())
+        return dict(A=A, B=B, ids=ids, C=torch.empty(M, N, device=dev()), order=tg.ExpertOrder.empty(T, k, E),
+                    off=torch.tensor([0, M], dtype=torch.int32, device=dev()),
+                    R=torch.empty(M, N, device=dev()), o=tg.make_options(direct=1, block_n=64 * scale, split_k=4))
+
+    def calls(c):
+        tg.gemm(c["A"], c["B"], c["C"], options=c["o"], stream=s)              # a split contraction, packed operands
+        tg.expert_sort(c["ids"], E, order=c["order"], stream=s)                # three launches with scratch between them
+        tg.gemm_grouped(c["A"], c["B"].unsqueeze(0), c["off"], c["R"], stream=s)  # shared tiles
+
+    def check(c):
+        want = torch.from_numpy(oracle_dense(c["A"].cpu(), c["B"].cpu())).float().to(dev())
+        assert torch.equal(c["C"], want) and torch.equal(c["R"], want)
+        assert torch.equal(c["order"].source, torch.argsort(c["ids"].flatten(), stable=True).int())
+
+    def capture(c):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            calls(c)
+        s.synchronize()
+        check(c)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            calls(c)
+        return g
+
+    small, large = case(1, 1), case(3, 2)
+    first = capture(small)
+    second = capture(large)
+    guard = [torch.full((1 << 22,), 7, dtype=torch.int32, device=dev()) for _ in range(8)]
+    for _ in range(3):
+        for g, c in ((first, small), (second, large)):
+            for name in ("C", "R"):
+                c[name].fill_(float("nan"))
+            c["order"].source.fill_(-9)
+            g.replay()
+            torch.cuda.synchronize()
+            assert tg.device_error(s) == tg.TG_OK
+            check(c)
+    assert all(bool((t == 7).all()) for t in guard)

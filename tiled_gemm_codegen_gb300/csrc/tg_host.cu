@@ -13,6 +13,7 @@
 #include <mutex>
 #include <tuple>
 #include <utility>
+#include <vector>
 
 #include "tg_epilogue.cuh"
 #include "tg_gemm.h"
@@ -400,6 +401,10 @@ struct Workspace {
     int32_t *counters = nullptr;  // split-K arrival counters (kept zero between calls)
     size_t counters_cap = 0;
     uint32_t *err = nullptr;  // device error word of this stream
+    // A call of this stream was captured into a CUDA graph: the graph's replays
+    // use the buffers that it met, so those outlive their growth.
+    bool captured = false;
+    std::vector<std::pair<void *, size_t>> kept;  // grown since; bytes of counters, 0 for an arena
     void *host_arena = nullptr;  // device copies of tg_gemm_host operands
     size_t host_cap = 0;
     // tg_gemm_host's copy streams and events (created on first use)
@@ -442,13 +447,28 @@ Workspace &workspace_for(int dev, cudaStream_t stream)
 }
 
 // Grows a device buffer; waits for the stream first so that no kernel still
-// uses the old one.
-tg_status grow(void **buf, size_t *cap, size_t need, cudaStream_t stream)
+// uses the old one.  A buffer that a captured call has met is kept for the
+// graph's replays (a quarter of room to grow bounds what is kept by four times
+// the largest).
+tg_status grow(Workspace &w, void **buf, size_t *cap, size_t need, cudaStream_t stream, bool counters = false)
 {
-    if (need <= *cap) return TG_OK;
+    if (need <= *cap) {
+        cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+        if (!w.captured && cudaStreamIsCapturing(stream, &st) == cudaSuccess && st != cudaStreamCaptureStatusNone)
+            w.captured = true;
+        return TG_OK;
+    }
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_status(e);
-    if (*buf) cudaFree(*buf);
+    if (*buf && w.captured) {
+        try {
+            w.kept.emplace_back(*buf, counters ? *cap : 0);
+        } catch (...) {
+            return TG_ERR_OOM;
+        }
+    } else if (*buf) {
+        cudaFree(*buf);
+    }
     *buf = nullptr;
     *cap = 0;
     const size_t want = need + need / 4;
@@ -475,11 +495,11 @@ tg_status ensure_err_word(Workspace &w, cudaStream_t stream)
 
 tg_status ensure_counters(Workspace &w, size_t bytes, cudaStream_t stream)
 {
-    if (bytes <= w.counters_cap) return TG_OK;
+    const bool fits = bytes <= w.counters_cap;
     void *p = w.counters;
-    tg_status st = grow(&p, &w.counters_cap, bytes, stream);
+    tg_status st = grow(w, &p, &w.counters_cap, bytes, stream, true);
     w.counters = static_cast<int32_t *>(p);
-    if (st != TG_OK) return st;
+    if (st != TG_OK || fits) return st;
     return cuda_status(cudaMemsetAsync(w.counters, 0, w.counters_cap, stream));
 }
 
@@ -803,7 +823,7 @@ tg_status run_gemm(const Args &a, cudaStream_t stream, const tg_options *opt,
     const size_t arena_need = static_cast<size_t>(plan.ws_pack_a + plan.ws_pack_b + plan.ws_partials +
                                                   plan.ws_scales_a + plan.ws_scales_b);
     if (arena_need > 0) {
-        st = grow(&w.arena, &w.arena_cap, arena_need, stream);
+        st = grow(w, &w.arena, &w.arena_cap, arena_need, stream);
         if (st != TG_OK) return st;
     }
     if (plan.ws_counters > 0) {
@@ -996,7 +1016,7 @@ tg_status host_stream(cudaStream_t stream, HostStream *out)
 tg_status host_arena(const HostStream &hs, size_t bytes, void **out)
 {
     Workspace &w = workspace_for(hs.dev, hs.stream);
-    const tg_status st = grow(&w.arena, &w.arena_cap, bytes, hs.stream);
+    const tg_status st = grow(w, &w.arena, &w.arena_cap, bytes, hs.stream);
     *out = w.arena;
     return st;
 }
@@ -1557,7 +1577,7 @@ TG_API tg_status tg_gemm_host(const void *A_host, const void *B_host, float *C_h
     {
         std::lock_guard<std::mutex> lock(g_mutex);
         Workspace &w = workspace_for(dev, stream);
-        st = grow(&w.host_arena, &w.host_cap, off, stream);
+        st = grow(w, &w.host_arena, &w.host_cap, off, stream);
         if (st == TG_OK) st = host_streams(w);
         if (st != TG_OK) return st;
         dbuf = static_cast<uint8_t *>(w.host_arena);
@@ -1690,6 +1710,8 @@ TG_API tg_status tg_device_error(tg_stream_t stream_)
     // counters an aborted kernel may have left part-way.
     cudaMemsetAsync(w.err, 0, 8, stream);
     if (w.counters) cudaMemsetAsync(w.counters, 0, w.counters_cap, stream);
+    for (const auto &k : w.kept)
+        if (k.second) cudaMemsetAsync(k.first, 0, k.second, stream);
     cudaStreamSynchronize(stream);
     return word == ERR_DEBUG_CHECK ? TG_ERR_DEVICE_CHECK : TG_ERR_TIMEOUT;
 }
@@ -1704,6 +1726,7 @@ TG_API void tg_shutdown(void)
         cudaSetDevice(w.device);
         if (w.arena) cudaFree(w.arena);
         if (w.counters) cudaFree(w.counters);
+        for (const auto &k : w.kept) cudaFree(k.first);
         if (w.err) cudaFree(w.err);
         if (w.host_arena) cudaFree(w.host_arena);
         if (w.h2d) cudaStreamDestroy(w.h2d);
