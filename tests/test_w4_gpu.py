@@ -290,6 +290,24 @@ def test_infinities_and_large_values_in_the_rows_of_several_passes(fmt, G, zeros
                 assert np.all(np.abs(y[t] - want) <= bound * mag)
 
 
+@pytest.mark.parametrize("K", [1022])
+@pytest.mark.parametrize("code", [0, 1, 120, 250, 254])
+def test_e2m1_scales_of_any_size(K, code):
+    """Scales from 2^-127 to 2^127 with activations that keep the results in
+    range; what a product below 2^-126 loses (2^-150 at most, half a unit of
+    fp32 there) is allowed for each of them."""
+    N, S = 40, 3
+    W, sc, _, wv = _weights(1, N, K, "e2m1", 32, 43)
+    x, xv = _x(S, K, 23)
+    up = 2.0 ** min(100, max(-100, 127 - code))
+    x, xv = (x.double() * up).to(BF), xv * up
+    wv = wv / np.repeat(np.exp2(sc.cpu().double().numpy() - 127), 32, -1)[..., :K] * 2.0 ** (code - 127)
+    sc.fill_(code)
+    y = tg.gemv_w4(x, W[0], sc[0], format="e2m1")
+    want, mag = xv @ wv[0].T, np.abs(xv) @ np.abs(wv[0]).T
+    assert np.all(np.abs(y.cpu().double().numpy() - want) <= 2 * (K + -(-K // 32) + 2) * U32 * mag + 2 * K * 2.0 ** -150)
+
+
 @pytest.mark.parametrize("power", [-120, -60, 60, 110, 124])
 def test_activations_of_any_magnitude(power):
     """Rows scaled by powers of two give results scaled by the same, exactly

@@ -91,21 +91,33 @@ __device__ __forceinline__ float e2m1_value(uint32_t q)
     return (q & 8u) ? -v : v;
 }
 
-// The two weights of a byte of codes; s and z: where its scale and zero lie.
+// A run's scale f and its zero; s and z: where they lie.  A code's weight is
+// code_value * f, which is exact in fp32, but past its largest value for the
+// largest f; `late` is the part of f that goes on after the activation instead:
+// all of it from 2^64, where only a product that overflows itself still does.
 template <bool E2M1>
-__device__ __forceinline__ void byte_values(const W4Args &a, uint32_t q, int64_t s, int64_t z, float &v0, float &v1)
-{
-    if constexpr (E2M1) {
-        const float f = e8m0_value(a.scales[s]);
-        v0 = e2m1_value(q & 15u) * f;
-        v1 = e2m1_value(q >> 4) * f;
-    } else {
-        const float f = bf16_value(reinterpret_cast<const uint16_t *>(a.scales)[s]);
-        const float zero = a.zeros ? static_cast<float>(a.zeros[z] & 15u) : 8.0f;
-        v0 = (static_cast<float>(q & 15u) - zero) * f;
-        v1 = (static_cast<float>(q >> 4) - zero) * f;
+struct W4Run {
+    float f, late, zero;
+    __device__ __forceinline__ W4Run(const W4Args &a, int64_t s, int64_t z)
+    {
+        if constexpr (E2M1) {
+            f = e8m0_value(a.scales[s]);
+            zero = 0.0f;
+        } else {
+            f = bf16_value(reinterpret_cast<const uint16_t *>(a.scales)[s]);
+            zero = a.zeros ? static_cast<float>(a.zeros[z] & 15u) : 8.0f;
+        }
+        late = fabsf(f) > 0x1p64f ? f : 1.0f;
+        if (late != 1.0f) f = 1.0f;
     }
-}
+    __device__ __forceinline__ float weight(uint32_t q) const  // without `late`
+    {
+        if constexpr (E2M1)
+            return e2m1_value(q) * f;
+        else
+            return (static_cast<float>(q) - zero) * f;
+    }
+};
 
 __device__ __forceinline__ void store_y(const W4Args &a, int64_t row, int64_t n, float v)
 {
@@ -132,7 +144,7 @@ __device__ __forceinline__ void zero_rows(const W4Args &a, int32_t n0, int32_t n
 // four rows at a time.  (code - zero) * scale and its product with an
 // activation are exact in fp32 (5 + 8 and 8 bits), so only the sum rounds.
 // Bound by its conversions and multiply-adds: 6 rows of 1964 codes (982-byte
-// rows) x 2976, int4: 26.8 us.
+// rows) x 2976, int4: 28.1 us.
 constexpr int ANY_COLS = 8;
 
 // The four bytes at p, of which the first `n` exist: one or two aligned words
@@ -175,13 +187,16 @@ __global__ void __launch_bounds__(ANY_COLS * 32) w4_any_kernel(const W4Args a)
             const uint32_t q = load4_any(w + k / 2, left / 2, w_lo, w_hi);
             const int32_t r = k / a.run;
             float v[8];
+            const W4Run<E2M1> run(a, s0 + r, z0 + r);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) byte_values<E2M1>(a, q >> (8 * b) & 255u, s0 + r, z0 + r, v[2 * b], v[2 * b + 1]);
+            for (int b = 0; b < 8; ++b) v[b] = run.weight(q >> (4 * b) & 15u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (r0 + i >= hi) break;
                 const uint16_t *x = a.x + (r0 + i) * a.ldx + k;
-                if (x4 && left == 8) {
+                if (run.late != 1.0f) {
+                    for (int b = 0; b < left; ++b) acc[i] = fmaf(run.weight(q >> (4 * b) & 15u) * bf16_value(x[b]), run.late, acc[i]);
+                } else if (x4 && left == 8) {
                     uint32_t h[4];
 #pragma unroll
                     for (int b = 0; b < 4; ++b) h[b] = __ldg(reinterpret_cast<const uint32_t *>(x) + b);
@@ -686,10 +701,9 @@ __device__ __forceinline__ float row_dot(const W4Args &a, int32_t g, int32_t n, 
     float acc = 0.0f;
     for (int32_t b = k0 / 2 + static_cast<int32_t>(threadIdx.x & 31); b < k1 / 2; b += 32) {
         const uint32_t q = w[b];
-        float v0, v1;
-        byte_values<E2M1>(a, q, s0 + 2 * b / a.run, z0 + 2 * b / a.run, v0, v1);
-        acc = fmaf(v0, bf16_value(x[2 * b]), acc);
-        acc = fmaf(v1, bf16_value(x[2 * b + 1]), acc);
+        const W4Run<E2M1> run(a, s0 + 2 * b / a.run, z0 + 2 * b / a.run);
+        acc = fmaf(run.weight(q & 15u) * bf16_value(x[2 * b]), run.late, acc);
+        acc = fmaf(run.weight(q >> 4) * bf16_value(x[2 * b + 1]), run.late, acc);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
