@@ -510,10 +510,10 @@ typedef enum { TG_W4_INT4 = 0, TG_W4_E2M1 = 1 } tg_w4_format;
  *               64 or 128
  *   TG_W4_E2M1  w = e2m1(code) * 2^(e - 127), e the E8M0 byte in scales (255:
  *               NaN), group_size 32, zeros NULL: tg_gemm_mxfp4's weights
- * Products and sums are fp32 (a code's value is exact; a group's sum is
- * scaled once; below 2^-112 a scale costs that sum some of its bits), y is
- * fp32 or bf16 (y_type), rounded once.  An infinity or NaN in x gives what
- * the formula gives.  Any alignment of whole elements; weights with 16-byte
+ * Products and sums are fp32 (a weight's code - z, or e2m1, is exact; a group's
+ * sum is scaled once, or each product), whatever the alignment, y is fp32 or
+ * bf16 (y_type), rounded once.  An infinity or NaN in x gives what the formula
+ * gives, a weight of zero gives zero for every finite x and scale.  Any alignment of whole elements; weights with 16-byte
  * rows are read fastest.  Any number of rows is computed; the weights are
  * read again for every eight rows of a group.  At most 65535 groups may have rows
  * (TG_ERR_UNSUPPORTED where min(groups, S) is more). */

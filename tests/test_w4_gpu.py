@@ -255,7 +255,7 @@ def test_infinite_activations_reach_int4_as_the_formula_says():
         assert np.all(np.abs(y[t] - want) <= 2 * (K + 10) * U32 * mag)
 
 
-@pytest.mark.parametrize("fmt,G,zeros", FORMATS[:5])
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
 @pytest.mark.parametrize("K,N,sizes", [(512, 28672, [16]), (512, 28672, [64]), (256, 9000, [16, 0, 1, 8, 40]), (9216, 2048, [40])])
 def test_infinities_and_large_values_in_the_rows_of_several_passes(fmt, G, zeros, K, N, sizes):
     """Workers go on from one pass of eight rows, or slice of K, to the next:
@@ -290,7 +290,45 @@ def test_infinities_and_large_values_in_the_rows_of_several_passes(fmt, G, zeros
                 assert np.all(np.abs(y[t] - want) <= bound * mag)
 
 
-@pytest.mark.parametrize("K", [1022])
+# K whose rows lie on 16 bytes, 4 bytes and neither
+ROWS_ON = [1024, 1000, 1022]
+
+
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+@pytest.mark.parametrize("K", ROWS_ON)
+@pytest.mark.parametrize("S", [1, 9])
+def test_codes_of_zero_weights_give_zero(fmt, G, zeros, K, S):
+    """A code at its zero point is the weight 0: no activation, of whatever size,
+    leaves anything of it."""
+    N = 70
+    W, sc, z, _ = _weights(1, N, K, fmt, G, 41, zeros)
+    code = np.zeros((1, N, K), np.uint8) if fmt == "e2m1" else np.repeat(z.cpu().numpy() if zeros else np.full(sc.shape, 8, np.uint8), G, -1)[..., :K]
+    W = torch.from_numpy(code[..., 0::2] | code[..., 1::2] << 4).to(dev())
+    x, _ = _x(S, K, 21)
+    x[:, 5::7] *= 1000
+    y = tg.gemv_w4(x, W[0], sc[0], zeros=z[0] if zeros else None, format=fmt, group=G)
+    assert torch.equal(y, torch.zeros(S, N, device=dev()))
+
+
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+@pytest.mark.parametrize("K", ROWS_ON)
+@pytest.mark.parametrize("power", [20, 40, 100, 117, 125])
+def test_large_activations_over_zero_weights(fmt, G, zeros, K, power):
+    """A channel of large activations whose weights are zero leaves the others'
+    products as they are."""
+    N, S, at = 70, 3, 333
+    W, sc, z, wv = _weights(1, N, K, fmt, G, 42, zeros)
+    code = torch.zeros_like(sc[..., at // G]).to(torch.uint8) if fmt == "e2m1" else z[..., at // G] if zeros else torch.full_like(W[..., 0], 8)
+    W[..., at // 2] = (W[..., at // 2] & 15) | code << 4
+    x, xv = _x(S, K, 22)
+    x[:, at] = 2.0 ** power
+    xv[:, at] = 2.0 ** power
+    wv[..., at] = 0
+    y = tg.gemv_w4(x, W[0], sc[0], zeros=z[0] if zeros else None, format=fmt, group=G)
+    _check(y, xv, wv, [0, S], K, G, F32)
+
+
+@pytest.mark.parametrize("K", ROWS_ON)
 @pytest.mark.parametrize("code", [0, 1, 120, 250, 254])
 def test_e2m1_scales_of_any_size(K, code):
     """Scales from 2^-127 to 2^127 with activations that keep the results in

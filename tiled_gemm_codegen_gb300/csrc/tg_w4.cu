@@ -5,7 +5,6 @@
 // The weights are the traffic (half a byte each, read once), so the bound is
 // HBM; at that rate an SM has to turn about 47 codes a clock into products.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -337,40 +336,6 @@ __device__ __forceinline__ void decode(uint32_t w, uint32_t magic, uint32_t zz, 
 
 __host__ __device__ constexpr int w4_warps(int xt) { return xt > 4 ? W4_WARPS / 2 : W4_WARPS; }
 
-// Nibbles (i, i + 4) of a word as two fp16, i = 0 .. 3: int4 as code * 2^-24
-// (odd i: * 2^-20), E2M1 as value * 2^-14.
-template <bool E2M1>
-__device__ __forceinline__ void decode_half(uint32_t w, uint32_t (&p)[4])
-{
-    if constexpr (E2M1) {
-        p[0] = masked_or<0x0E000E00u>(w << 9, (w << 12) & 0x80008000u);
-        p[1] = masked_or<0x0E000E00u>(w << 5, (w << 8) & 0x80008000u);
-        p[2] = masked_or<0x0E000E00u>(w << 1, (w << 4) & 0x80008000u);
-        p[3] = masked_or<0x0E000E00u>(w >> 3, w & 0x80008000u);
-    } else {
-        const uint32_t v = w >> 8;
-        p[0] = w & 0x000F000Fu;
-        p[1] = w & 0x00F000F0u;
-        p[2] = v & 0x000F000Fu;
-        p[3] = v & 0x00F000F0u;
-    }
-}
-template <bool E2M1>
-constexpr int32_t W4_UNIT_UP = E2M1 ? 14 : 24;
-
-// d (+)= a b in fp16 with fp32 sums.
-__device__ __forceinline__ void mma_16816_half(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool first)
-{
-    if (first)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Staged scale words of a row and step: its bytes from the 4-byte boundary
 // before them.
 template <bool E2M1, int RUN>
@@ -552,35 +517,26 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
 // slice of K step by step); a producer warp keeps `stages` TMA boxes of 32 rows x 256 codes in
 // flight for each of them, across the ends of tiles, so the weights never stop
 // and a step costs the others one wait and one arrival.  What a tile needs
-// besides is loaded once or ahead: the activations of a group in the order and
-// type the products want, the scales of the next tile by cp.async during this
+// besides is loaded once or ahead: the activations of a group in the order
+// the products want, the scales of the next tile by cp.async during this
 // one.
 //
-// What bounds it is taking the codes apart, so both operands are fp16 here,
-// where that takes least: a masked code is an fp16 subnormal as it lies, q
-// 2^-24 in the low four bits of a half and 16 q 2^-24 in the next four (the
-// activations that meet those are divided by 16), so eight codes cost four
-// masks and one shift, and the tensor cores take subnormals as they are.  Zero
-// points leave the product: sum (q - z) x = sum q x - z sum x, with the sums
-// of a group's activations made once.  An E2M1 code's three low bits on fp16's
-// exponent and mantissa are its value times 2^-14.
+// The arithmetic is the tile kernel's: a code becomes the exact bf16 value of q -
+// z, or of E2M1, activations stay the bf16 they are, a group's products are summed
+// in fp32 and multiplied by its scale once.  So nothing depends on the size of
+// other values: weights of zero leave nothing of their activations, and infinities and
+// NaN go through the products.  (fp16 operands take fewer steps apart - codes as
+// subnormals, zero points as a difference of two sums - and 4 to 9% less time on
+// int4, 1 to 3% on E2M1, but their error goes with sum |q x| and with the largest
+// activation of 256: a channel of 2^40 over zero weights hid the others.)
+// Rows with a finite magnitude from W4_LARGE are computed value by value, scale
+// first.
 //
-// Activations become fp16 by a power of two for each row and step of 256, which
-// brings their largest finite magnitude to [2^11, 2^12); a step's sums are
-// multiplied back, and by the code's unit, before they are added up, so that
-// small results keep their bits (scales below 2^-112 would cost a step's sum
-// some).  A value of bf16's eight bits loses some only below 2^-28 (2^-24
-// where it is divided by 16) of the step's largest, by 2^-32 of that at most:
-// less than the rounding of the fp32 sum.  A row with an infinity or NaN, for
-// which the difference of two sums is not the sum, or with a magnitude from
-// 2^114 (E2M1: 2^124) that no fp32 power of two would bring back, is computed
-// value by value instead.
-//
-// Measured: 1 row, 8192 x 28672 int4 by 128, 121 MB: 27.4 us on the GPU; between
-// sizes the weights stream at 6.0 TB/s (88% of a plain copy), and start, first
-// boxes, activations and last tiles are 5.7 us of it.  E2M1 has a scale for every
-// 32 codes: 43 us for the same codes.  32 rows over 20 of 64 experts, 2048 x
-// 1408 E2M1, 31 MB: 18-18.8 us, of which the start and a CTA's few turns are
+// What bounds it is taking the codes apart.  Measured (calls on a graph, weights
+// not in L2): 1 row, 8192 x 28672 int4 by 128, 121 MB: 28.8 us, of which start,
+// first boxes, activations and last tiles are 5.7; with zero points 31.4; E2M1,
+// which has a scale for every 32 codes, 39.0.  32 rows over 20 of 64 experts, 2048 x
+// 1408 E2M1, 31 MB: 19.4 us, of which the start and a CTA's few turns are
 // most.  Tried: eight turns' activation loads in flight instead of four (3-4
 // us slower, registers), E2M1's sign moved by a multiply-add instead of a
 // shift and mask (no change), the hardware's E2M1 conversion (twice the time).
@@ -598,7 +554,7 @@ struct W4Stream {
     int32_t w_shared;  // every group has the same weights
     int32_t x_pitch;   // bytes of an activation row in shared memory
     int32_t s_words, z_words;  // staged words of a row's scales and zeros
-    int32_t off_x, off_xs, off_s, off_z, off_sum;  // bytes in shared memory after the rings
+    int32_t off_x, off_s, off_z, off_sum;  // bytes in shared memory after the rings
     int32_t s_vec;             // every row of scales starts on 4 bytes
     float *partials;           // slices > 1: [slice][S][N]
     uint32_t *err;
@@ -686,10 +642,11 @@ __device__ __forceinline__ uint4 shared_u128(uint32_t a, int off)
     return v;
 }
 
-// The exponent of the power of two that brings the largest finite magnitude of
-// 256 activations, given as bf16 bits, to [2^11, 2^12); at most 126.
-__device__ __forceinline__ int32_t x_up(int32_t most) { return min(138 - (most >> 7), 126); }
-__device__ __forceinline__ float power_of_two(int32_t e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+// Activations from this magnitude, as bf16 bits, may add up to more than fp32's
+// largest before their group's scale brings them back: 2^116 where a group of
+// 128 has weights up to 15, 2^119 for 32 up to 6.
+template <bool E2M1>
+constexpr int32_t W4_LARGE = (127 + (E2M1 ? 119 : 116)) << 7;
 
 // Whole warp: <x[row], w_g[n]> over [k0, k1) value by value, for any values.
 template <bool E2M1>
@@ -721,7 +678,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * W4S_WARPS * W4S_STAGES];  // a warp's full, then its empty ones
     __shared__ int32_t aborted;
-    // The row holds an infinity, NaN or a magnitude too large.  Two sets in turn:
+    // The row holds a finite magnitude from W4_LARGE.  Two sets in turn:
     // the next pass's is cleared while warps may still be storing the last tile
     // of this one, which read this one's.
     __shared__ int32_t x_odd[2][8];
@@ -731,6 +688,7 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = static_cast<int>(threadIdx.x & 31);
     const int lg = lane >> 2, lc = lane & 3;
+    const uint32_t magic = in_register(E2M1 ? 0x7E807E80u : 0x43004300u), eight = in_register(0x43084308u);
     const int team = warp / p.wk, part_k = warp % p.wk;
     const int teams = p.warps / p.wk;
     const int tile_rows = teams * W4S_ROWS;
@@ -895,10 +853,8 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
                  base + p.off_z + b * tile_rows * p.z_words * 4, z_r, z_w, z_dr, z_dw);
     };
 
-    // ---- activations of a pass, as fp16 times a power of two for each row
-    // and step: eight consecutive ones paired as the codes of a word are; and
-    // their sums by group of codes, times the code's unit (and by 8, the zero
-    // point, where there is no other).  A warp takes the 256 of a row and step.
+    // ---- activations of a pass: eight consecutive ones paired as the codes of a
+    // word are.  A warp takes the 256 of a row and step.
     int32_t odd_set = 0;  // the set of x_odd in use
     auto stage_x = [&](int32_t r0, int32_t nx, int32_t k0, int32_t steps) {
         const bool aligned = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(2 * a.ldx)) & 15u) == 0;
@@ -926,42 +882,18 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             for (int u = 0; u < U; ++u) {
                 const int32_t i = i0 + u * p.warps;
                 if (i >= turns) break;
-                const int32_t t = i / steps, step = i - t * steps, c = step * 32 + lane;
+                const int32_t t = i / steps, c = (i - t * steps) * 32 + lane;
                 const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-                int32_t most = 0;
-                bool odd = false;
+                bool large = false;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int32_t lo = static_cast<int32_t>(w[e] & 0x7fffu), hi = static_cast<int32_t>(w[e] >> 16 & 0x7fffu);
-                    odd |= lo >= 0x7f80 || hi >= 0x7f80;
-                    most = max(most, max(lo < 0x7f80 ? lo : 0, hi < 0x7f80 ? hi : 0));
+                    large |= (lo >= W4_LARGE<E2M1> && lo < 0x7f80) || (hi >= W4_LARGE<E2M1> && hi < 0x7f80);
                 }
-                most = __reduce_max_sync(0xffffffffu, most);
-                const int32_t up = x_up(most), back = W4_UNIT_UP<E2M1> - up;
-                if (odd || back > 127) x_odd[odd_set][t] = 1;
-                const float mul = power_of_two(up);
-                float f[8], sum = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float x = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) * mul;
-                    f[e] = __half2float(__float2half_rn(!E2M1 && (e & 1) ? x * 0.0625f : x));
-                    sum += !E2M1 && (e & 1) ? f[e] * 16.0f : f[e];
-                }
-                uint32_t h[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __half2 q = __floats2half2_rn(f[e], f[e + 4]);
-                    h[e] = *reinterpret_cast<const uint32_t *>(&q);
-                }
-                *reinterpret_cast<uint4 *>(smem + p.off_x + t * p.x_pitch + c * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-                float *xs = reinterpret_cast<float *>(smem + p.off_xs);
-                if (lane == 0) xs[step * 8 + t] = power_of_two(min(back, 127));
-                if constexpr (!E2M1) {
-#pragma unroll
-                    for (int d = 1; d < RUN / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                    if (lane % (RUN / 8) == 0)
-                        xs[p.steps * 8 + c / (RUN / 8) * 8 + t] = sum * power_of_two((ZEROS ? 0 : 3) - W4_UNIT_UP<false>);
-                }
+                if (large) x_odd[odd_set][t] = 1;
+                *reinterpret_cast<uint4 *>(smem + p.off_x + t * p.x_pitch + c * 16) =
+                    make_uint4(__byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632), __byte_perm(w[1], w[3], 0x5410),
+                               __byte_perm(w[1], w[3], 0x7632));
             }
         }
     };
@@ -1009,8 +941,6 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
         }
         // (an operand column of no row repeats row 0's: its sums are not stored)
         uint32_t x_step = base + p.off_x + (lg < nx ? lg : 0) * p.x_pitch + lc * 16 + part_k * (2 * W4_STEP);
-        const float2 *xs_step = reinterpret_cast<const float2 *>(smem + p.off_xs) + (p.steps + part_k * RUNS) * 4 + lc;
-        const float2 *inv_step = reinterpret_cast<const float2 *>(smem + p.off_xs) + part_k * 4 + lc;
         int32_t k_left = a.K - k0 - part_k * W4_STEP;  // codes from the step's first
         int32_t run0 = part_k * RUNS;
         for (int32_t i = 0; i < mine; ++i) {
@@ -1030,7 +960,6 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             // (the loads below are not volatile, so that they mix with the
             // products; they hang on w_lane, which exists from here on)
             asm volatile("" : "+r"(w_lane), "+r"(x_step)::"memory");
-            float sum[2][4];  // of the step
             // the step's scales, as bf16 pairs
             uint32_t sc[4][SW];
 #pragma unroll
@@ -1070,6 +999,9 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
             for (int j = 0; j < RUNS; ++j) {
                 if (j > 0 && j * RUN >= k_left) break;
                 float part[2][4];
+                uint32_t zz[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) zz[h] = ZEROS ? (0x4300u | (lds_u8(z_row[h] + run0 + j) & 15u)) * 0x00010001u : eight;
 #pragma unroll
                 for (int q = 0; q < RUN / 32; ++q) {
                     const int blk = j * (RUN / 32) + q;
@@ -1078,44 +1010,24 @@ __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         uint32_t u[4], v[4];
-                        decode_half<E2M1>(shared_u32(wa, m * 2048), u);
-                        decode_half<E2M1>(shared_u32(wa, m * 2048 + 1024), v);
+                        decode<E2M1>(shared_u32(wa, m * 2048), magic, zz[2 * m], u);
+                        decode<E2M1>(shared_u32(wa, m * 2048 + 1024), magic, zz[2 * m + 1], v);
                         const uint32_t a0[4] = {u[0], v[0], u[1], v[1]}, a1[4] = {u[2], v[2], u[3], v[3]};
-                        mma_16816_half(part[m], a0, xv.x, xv.y, q == 0);
-                        mma_16816_half(part[m], a1, xv.z, xv.w, false);
-                    }
-                }
-                if constexpr (!E2M1) {  // - z sum x
-                    const float2 xs = xs_step[j * 4];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        float &c0 = part[h >> 1][2 * (h & 1)], &c1 = part[h >> 1][2 * (h & 1) + 1];
-                        if constexpr (ZEROS) {
-                            const float z = -static_cast<float>(lds_u8(z_row[h] + run0 + j) & 15u);
-                            c0 = fmaf(z, xs.x, c0);
-                            c1 = fmaf(z, xs.y, c1);
-                        } else {
-                            c0 -= xs.x;
-                            c1 -= xs.y;
-                        }
+                        mma_16816(part[m], a0, xv.x, xv.y, q == 0);
+                        mma_16816(part[m], a1, xv.z, xv.w, false);
                     }
                 }
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     const float sv = (j & 1) ? __uint_as_float(sc[h][j >> 1] & 0xffff0000u) : __uint_as_float(sc[h][j >> 1] << 16);
-                    float &a0 = sum[h >> 1][2 * (h & 1)], &a1 = sum[h >> 1][2 * (h & 1) + 1];
-                    a0 = j == 0 ? sv * part[h >> 1][2 * (h & 1)] : fmaf(sv, part[h >> 1][2 * (h & 1)], a0);
-                    a1 = j == 0 ? sv * part[h >> 1][2 * (h & 1) + 1] : fmaf(sv, part[h >> 1][2 * (h & 1) + 1], a1);
+                    float &a0 = acc[h >> 1][2 * (h & 1)], &a1 = acc[h >> 1][2 * (h & 1) + 1];
+                    a0 = fmaf(sv, part[h >> 1][2 * (h & 1)], a0);
+                    a1 = fmaf(sv, part[h >> 1][2 * (h & 1) + 1], a1);
                 }
             }
-            const float2 inv = *inv_step;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e >> 2][e & 3] = fmaf(e & 1 ? inv.y : inv.x, sum[e >> 2][e & 3], acc[e >> 2][e & 3]);
             x_step += p.wk * (2 * W4_STEP);
-            xs_step += p.wk * RUNS * 4;
             k_left -= p.wk * W4_STEP;
             run0 += p.wk * RUNS;
-            inv_step += p.wk * 4;
             // the box has been read into these sums: its slot may be filled again
             asm volatile(""
                          : "+f"(acc[0][0]), "+f"(acc[0][1]), "+f"(acc[0][2]), "+f"(acc[0][3]), "+f"(acc[1][0]), "+f"(acc[1][1]), "+f"(acc[1][2]),
@@ -1280,11 +1192,10 @@ bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &be
         const int pieces = (p.steps * unit + 1 + unit - 1) / unit | 1;
         p.s_words = pieces * unit;
         p.z_words = a.zeros ? (std::min(a.runs, p.steps * runs) + 3) / 4 + 1 : 0;
-        const int xs_bytes = p.steps * (1 + (e2m1 ? 0 : runs)) * 8 * 4;
         for (p.warps = W4S_WARPS; p.warps >= 4; p.warps /= 2) {
             for (p.wk = 1; p.wk <= p.warps && p.wk <= p.steps; p.wk *= 2) {
                 const int rows = p.warps / p.wk * W4S_ROWS;
-                const int64_t room = SMEM_LIMIT - W4S_STATIC - 1024 - static_cast<int64_t>(p.xt) * p.x_pitch - xs_bytes - 32 -  // (1 KB: alignment)
+                const int64_t room = SMEM_LIMIT - W4S_STATIC - 1024 - static_cast<int64_t>(p.xt) * p.x_pitch - 32 -  // (1 KB: alignment)
                                      2 * static_cast<int64_t>(rows) * (p.s_words + p.z_words) * 4 - p.warps * p.xt * W4S_ROWS * 4;
                 if (room < 2 * p.warps * W4S_BOX) continue;
                 p.tiles_n = static_cast<int32_t>((a.N + rows - 1) / rows);
@@ -1298,8 +1209,7 @@ bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &be
                 best = cost;
                 best_p = p;
                 best_p.off_x = p.warps * p.stages * W4S_BOX;
-                best_p.off_xs = best_p.off_x + p.xt * p.x_pitch;
-                best_p.off_s = (best_p.off_xs + xs_bytes + 15) / 16 * 16;
+                best_p.off_s = best_p.off_x + p.xt * p.x_pitch;
                 best_p.off_z = best_p.off_s + 2 * rows * p.s_words * 4;
                 best_p.off_sum = best_p.off_z + 2 * rows * p.z_words * 4;
                 smem = static_cast<size_t>(best_p.off_sum + p.warps * p.xt * W4S_ROWS * 4 + 1024);
