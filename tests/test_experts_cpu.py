@@ -260,3 +260,33 @@ def test_an_order_uses_the_tensors_it_shows():
     assert ex._order(order)[1] == tuple(t.data_ptr() for t in order)
     offsets, source, slot = order
     assert offsets is order.offsets and source is order.source and slot is order.slot
+
+
+def test_layouts_are_the_tensors_own(monkeypatch):
+    """Options tuned on transposed operands, used with row-major ones: the layout
+    they hold would have the operands read past their storage."""
+    from tiled_gemm_codegen_gb300 import experts as ex
+
+    seen = []
+    monkeypatch.setattr(tg, "tg_gemm_ex", lambda *a: seen.append((a[-1] and (a[-1].a_col_major, a[-1].b_col_major, a[-1].stages))) or tg.TG_OK)
+    A, B, C = torch.zeros(24, 64, dtype=BF), torch.zeros(64, 40, dtype=BF), torch.zeros(24, 40)
+    At, Bt = torch.zeros(64, 24, dtype=BF).t(), torch.zeros(40, 64, dtype=BF).t()
+    for o in (None, dict(stages=4), dict(stages=4, a_col_major=1), dict(stages=4, a_col_major=1, b_col_major=1)):
+        for a, b, want in ((A, B, (0, 0)), (At, B, (1, 0)), (A, Bt, (0, 1)), (At, Bt, (1, 1))):
+            opts = None if o is None else tg.make_options(**o)
+            tg.gemm(_OnGpu(a), _OnGpu(b), _OnGpu(C), options=opts, stream=0)
+            assert seen[-1] == (None if o is None and want == (0, 0) else (*want, 0 if o is None else 4))
+            assert opts is None or (opts.a_col_major, opts.b_col_major) == (o.get("a_col_major", 0), o.get("b_col_major", 0))
+
+    class Lib:
+        @staticmethod
+        def tg_gemm_grouped(*a):
+            seen.append(a[-1] and a[-1]._obj.b_col_major)
+            return tg.TG_OK
+
+    monkeypatch.setattr(ex, "_lib", lambda: Lib)
+    W, Wt = torch.zeros(4, 64, 40, dtype=BF), torch.zeros(4, 40, 64, dtype=BF).transpose(1, 2)
+    off, opts = _OnGpu(torch.zeros(5, dtype=I32)), tg.make_options(cta_pair=1, b_col_major=1)
+    for b, o, want in ((W, opts, 0), (Wt, opts, 1), (W, None, None), (Wt, None, 1)):
+        tg.gemm_grouped(_OnGpu(A), _OnGpu(b), off, _OnGpu(C), options=o, stream=0)
+        assert seen[-1] == want

@@ -191,7 +191,12 @@ def _operand(t, what):
 
 
 def _with_layout(options, a_cm, b_cm):
-    if not (a_cm or b_cm):
+    """The options with the operands' layouts, which are the tensors' own,
+    whatever the options hold (a tuned plan's have its operands')."""
+    if options is None:
+        if not (a_cm or b_cm):
+            return None
+    elif (options.a_col_major, options.b_col_major) == (int(a_cm), int(b_cm)):
         return options
     o = tg_options()
     if options is not None:
