@@ -290,3 +290,25 @@ def test_layouts_are_the_tensors_own(monkeypatch):
     for b, o, want in ((W, opts, 0), (Wt, opts, 1), (W, None, None), (Wt, None, 1)):
         tg.gemm_grouped(_OnGpu(A), _OnGpu(b), off, _OnGpu(C), options=o, stream=0)
         assert seen[-1] == want
+
+
+def test_words_off_their_alignment_are_refused(lib):
+    """Bounds, slots, weights and bias are read in 4-byte words: a kernel given
+    others would fault."""
+    for kw in (dict(offsets=OFF + 2), dict(source=SRC + 1), dict(slot=SLOT + 2)):
+        assert _dispatch(lib, **kw) == INVALID, kw
+    assert lib.tg_expert_sort(IDS, 4, 4, 10, 4, 8, OFF + 2, SRC, SLOT, None) == INVALID
+    for off, slot in ((OFF + 2, SLOT), (OFF, SLOT + 1)):
+        assert lib.tg_expert_gather(X, 64, 64, 1, 10, 4, 8, off, slot, XS, 64, None) == INVALID
+    for slot, w in ((SLOT + 2, W), (SLOT, W + 2)):
+        assert lib.tg_expert_combine(X, 64, 1, 40, slot, w, 4, 10, 4, 64, XS, 64, 1, None) == INVALID
+    for off, slot, w, dw in ((OFF + 2, SLOT, W, DW), (OFF, SLOT + 2, W, DW), (OFF, SLOT, W + 1, DW), (OFF, SLOT, W, DW + 2)):
+        assert lib.tg_expert_combine_grad(DY, 64, 1, X, 64, 1, off, slot, w, 4, 10, 4, 8, 64, XS, 64, 1, dw, 4, None) == INVALID
+    import ctypes
+
+    def grouped(off, ep):
+        return lib.tg_gemm_grouped(X, XS, DY, off, 4, 100, 64, 32, 32, 64, 2048, 64, ctypes.byref(ep), None, None)
+
+    assert grouped(OFF + 2, _ep()) == INVALID and grouped(OFF, _ep(bias=W + 2)) == INVALID
+    assert lib.tg_gemm_grouped_wgrad(X, XS, DY, OFF + 2, 4, 100, 32, 64, 32, 64, 64, 2048, None, None, None) == INVALID
+    assert lib.tg_gemv_w4(X, 128, XS, 128, 128 * 64, SRC, 1, 64, None, 0, 0, 0, 128, OFF + 2, 4, 10, 64, 128, DY, 64, 0, None) == INVALID

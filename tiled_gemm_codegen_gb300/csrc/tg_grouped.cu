@@ -329,7 +329,8 @@ TG_API tg_status tg_gemm_grouped(const void *A, const void *B, void *D, const in
         if (S == 0 || N == 0) return TG_OK;
         if (!offsets || !D || (K > 0 && (!A || !B))) return TG_ERR_INVALID_ARG;
         const int64_t eb = ep && ep->out_type == TG_BF16 ? 2 : 4;
-        if (reinterpret_cast<uintptr_t>(D) % eb || reinterpret_cast<uintptr_t>(A) % 2 || reinterpret_cast<uintptr_t>(B) % 2)
+        if (reinterpret_cast<uintptr_t>(D) % eb || reinterpret_cast<uintptr_t>(A) % 2 || reinterpret_cast<uintptr_t>(B) % 2 ||
+            !host_words_ok(offsets, ep ? ep->bias : nullptr))
             return TG_ERR_INVALID_ARG;
         const Bytes d = bytes_of(D, 1, 0, S, ldd, N, eb);
         if (meets(d, bytes_of(A, 1, 0, S, lda, K, 2)) || meets(d, bytes_of(B, groups, strideB, b_rows, ldb, b_cols, 2)) ||
@@ -357,7 +358,8 @@ TG_API tg_status tg_gemm_grouped_wgrad(const void *A, const void *B, void *D, co
         if (groups > 1 && strideD < (M - 1) * ldd + N) return TG_ERR_INVALID_ARG;
         if (!offsets || !D || (S > 0 && (!A || !B))) return TG_ERR_INVALID_ARG;
         const int64_t eb = ep && ep->out_type == TG_BF16 ? 2 : 4;
-        if (reinterpret_cast<uintptr_t>(D) % eb || reinterpret_cast<uintptr_t>(A) % 2 || reinterpret_cast<uintptr_t>(B) % 2)
+        if (reinterpret_cast<uintptr_t>(D) % eb || reinterpret_cast<uintptr_t>(A) % 2 || reinterpret_cast<uintptr_t>(B) % 2 ||
+            !host_words_ok(offsets))
             return TG_ERR_INVALID_ARG;
         const Bytes d = bytes_of(D, groups, strideD, M, ldd, N, eb);
         if (meets(d, bytes_of(A, 1, 0, S, lda, M, 2)) || meets(d, bytes_of(B, 1, 0, S, ldb, N, 2)) ||

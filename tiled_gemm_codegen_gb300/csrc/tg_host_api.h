@@ -36,6 +36,13 @@ tg_status host_counters(const HostStream &hs, size_t bytes, int32_t **out);
 
 tg_status host_cuda_status(cudaError_t e);
 
+// Whether arrays of 4-byte values (bounds, slots, weights, bias) lie on 4 bytes.
+template <class... P>
+bool host_words_ok(const P *...p)
+{
+    return ((reinterpret_cast<uintptr_t>(p) | ... | uintptr_t(0)) & 3u) == 0;
+}
+
 // A rank-3 tensor map (dim0 contiguous, dim1 rows, dim2 problems; strides in
 // bytes; box {box0, box1, 1}); false if the driver refuses it.
 bool host_encode_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,

@@ -1085,7 +1085,8 @@ tg_status run_sort(const void *ids, int32_t id_bytes, int64_t ld_ids, int64_t T,
                    int32_t *source, int32_t *slot, const void *x, int64_t ld_x, int64_t D, int32_t eb, void *xs,
                    int64_t ld_xs, cudaStream_t stream)
 {
-    if (!counts_ok(T, k, E) || (id_bytes != 4 && id_bytes != 8) || !offsets) return TG_ERR_INVALID_ARG;
+    if (!counts_ok(T, k, E) || (id_bytes != 4 && id_bytes != 8) || !offsets || !host_words_ok(offsets, source, slot))
+        return TG_ERR_INVALID_ARG;
     const int64_t n = T * k;
     if (n > 0 && (!ids || !source || !slot || ld_ids < k || ld_ids > PITCH_LIMIT ||
                   reinterpret_cast<uintptr_t>(ids) % static_cast<uintptr_t>(id_bytes) != 0))
@@ -1204,7 +1205,8 @@ TG_API tg_status tg_expert_gather(const void *x, int64_t ld_x, int64_t D, int32_
         if (!counts_ok(T, k, E) || D < 0 || !dtype_ok(dtype)) return TG_ERR_INVALID_ARG;
         const int64_t n = T * k, eb = dtype_bytes(dtype);
         if (n == 0 || D == 0) return TG_OK;
-        if (!offsets || !slot || !row_ok(x, T, ld_x, D, eb) || !row_ok(xs, n, ld_xs, D, eb)) return TG_ERR_INVALID_ARG;
+        if (!offsets || !slot || !host_words_ok(offsets, slot) || !row_ok(x, T, ld_x, D, eb) || !row_ok(xs, n, ld_xs, D, eb))
+            return TG_ERR_INVALID_ARG;
         const Span out = span_of(xs, n, ld_xs, D, eb);
         if (meets(out, span_of(x, T, ld_x, D, eb)) || meets(out, span_of(offsets, 1, 0, E + 1, 4)) ||
             meets(out, span_of(slot, 1, 0, n, 4)))
@@ -1226,7 +1228,7 @@ TG_API tg_status tg_expert_combine(const void *ys, int64_t ld_ys, int32_t ys_typ
             return TG_ERR_INVALID_ARG;
         if (T == 0 || D == 0) return TG_OK;
         const int64_t yb = dtype_bytes(y_type), ysb = dtype_bytes(ys_type);
-        if (!slot || !row_ok(ys, S, ld_ys, D, ysb) || !row_ok(y, T, ld_y, D, yb) || (weights && ld_w < k) ||
+        if (!slot || !host_words_ok(slot, weights) || !row_ok(ys, S, ld_ys, D, ysb) || !row_ok(y, T, ld_y, D, yb) || (weights && ld_w < k) ||
             (weights && ld_w > PITCH_LIMIT))
             return TG_ERR_INVALID_ARG;
         const Span out = span_of(y, T, ld_y, D, yb);
@@ -1278,7 +1280,7 @@ TG_API tg_status tg_expert_combine_grad(const void *dy, int64_t ld_dy, int32_t d
         const int64_t n = T * k;
         if (n == 0) return TG_OK;
         const int64_t b_dy = dtype_bytes(dy_type), b_ys = dtype_bytes(ys_type), b_dys = dtype_bytes(dys_type);
-        if (!offsets || !slot || !row_ok(dy, T, ld_dy, D, b_dy) || !row_ok(dys, n, ld_dys, D, b_dys) ||
+        if (!offsets || !slot || !host_words_ok(offsets, slot, weights, dweights) || !row_ok(dy, T, ld_dy, D, b_dy) || !row_ok(dys, n, ld_dys, D, b_dys) ||
             (dweights && !row_ok(ys, n, ld_ys, D, b_ys)) || (weights && (ld_w < k || ld_w > PITCH_LIMIT)) ||
             (dweights && (ld_dw < k || ld_dw > PITCH_LIMIT)))
             return TG_ERR_INVALID_ARG;

@@ -1312,7 +1312,8 @@ TG_API tg_status tg_gemv_w4(const void *x, int64_t ldx, const void *W, int64_t l
         if (S == 0 || N == 0) return TG_OK;
         if (!y || (K > 0 && (!x || !W || !scales))) return TG_ERR_INVALID_ARG;
         const int64_t yb = y_type == TG_BF16 ? 2 : 4, sb = format == TG_W4_E2M1 ? 1 : 2;
-        if (reinterpret_cast<uintptr_t>(y) % yb || reinterpret_cast<uintptr_t>(x) % 2 || reinterpret_cast<uintptr_t>(scales) % sb)
+        if (reinterpret_cast<uintptr_t>(y) % yb || reinterpret_cast<uintptr_t>(x) % 2 || reinterpret_cast<uintptr_t>(scales) % sb ||
+            !host_words_ok(offsets))
             return TG_ERR_INVALID_ARG;
         const Bytes out = bytes_of(y, 1, 0, S, ldy, N, yb);
         if (meets(out, bytes_of(x, 1, 0, S, ldx, K, 2)) || meets(out, bytes_of(W, groups, strideW / 2, N, ldw / 2, K / 2, 1)) ||
