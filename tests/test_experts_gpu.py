@@ -301,3 +301,18 @@ def test_rows_past_two_billion_elements():
         assert within(dys[s], _np(x[src // k]) * _np(w.reshape(-1)[src])[:, None], U32 * 300, BF)
         assert torch.equal(dw[t, 0], (x[t].float() ** 2).sum(1))
         del dys, xs, x
+
+
+@pytest.mark.parametrize("T,k,E", [(1300001, 2, 33), (2 ** 21, 2, 1024)])
+def test_sort_of_millions_of_ids(T, k, E):
+    """More ids than the largest number of blocks places in one turn each."""
+    ids = torch.randint(-1, E + 1, (T, k), generator=torch.Generator().manual_seed(T)).to(dev())
+    order = tg.expert_sort(ids, E)
+    key = torch.where((ids >= 0) & (ids < E), ids, E).flatten()
+    by = torch.argsort(key, stable=True)
+    kept = int((key < E).sum())
+    assert torch.equal(order.offsets, torch.searchsorted(key[by], torch.arange(E + 1, device=dev())).int())
+    assert torch.equal(order.source[:kept], by[:kept].int()) and bool((order.source[kept:] == -1).all())
+    slot = torch.full((T * k,), -1, dtype=torch.int32, device=dev())
+    slot[by[:kept]] = torch.arange(kept, dtype=torch.int32, device=dev())
+    assert torch.equal(order.slot.flatten(), slot)
