@@ -172,16 +172,19 @@ int64_t share_of(bool wgrad, bool pair, int64_t units, int64_t depth, int sms)
     return std::max(least, units <= workers ? cdiv(depth, workers / units) : cdiv(units * depth, workers));
 }
 
-// What a call takes with one-CTA tiles (128 x 128) or pairs (256 x 256), in
-// microseconds: turns of the workers over the tiles (rows mode: those of
-// groups that end anywhere in a tile) or shares, each a start, so much a
-// k-block, and where tiles are shared the adding.  The constants were fitted
-// to 350 calls of both kinds (1 to 32 uneven groups of 64 to 4096 rows, rows
-// mode K 64 to 4096 and N 256 to 4096, gradients 256 to 2048 x 256 to 4096):
-// the tiles it chooses take 0.4% longer than the better ones on average,
-// those of a rule by size (256 rows and enough pair tiles to fill half the
-// SMs) 4%, and up to half as long again: 8 groups of 256 rows, 4096 x 1000:
-// 42.9 us in one-CTA tiles, 28.1 in pairs; 32 of 192, 64 x 1000: 10.1, 15.4.
+// A measure of what a call takes with one-CTA tiles (128 x 128) or pairs (256 x
+// 256): turns of the workers over the tiles (rows mode: those of groups that end
+// anywhere in a tile) or shares, each a start, so much a k-block, and where tiles
+// are shared the adding.  Its constants choose, they do not foretell: they were fitted,
+// in microseconds, to the choice in 350 calls of both kinds (1 to 32 uneven groups of
+// 64 to 4096 rows, rows mode K 64 to 4096 and N 256 to 4096, gradients 256 to 2048 x
+// 256 to 4096), and a pair's start carries a part of its k-blocks (which take 0.33 at
+// the tensor cores' measured rate, not 0.143), so that contractions deeper than those
+// look too short in pairs.  The tiles it
+// chooses take 0.4% longer than the better ones on average, those of a rule by
+// size (256 rows and enough pair tiles to fill half the SMs) 4%, and up to half as
+// long again: 8 groups of 256 rows, 4096 x 1000: 42.9 us in one-CTA tiles, 28.1
+// in pairs; 32 of 192, 64 x 1000: 10.1, 15.4.
 double tiles_cost(bool wgrad, bool pair, int64_t S, int64_t M, int64_t N, int64_t K, int64_t groups, int sms)
 {
     const double start = pair ? 4.3 : 0.7, block = pair ? 0.143 : 0.27, adding = pair ? 9.5 : 2.1;

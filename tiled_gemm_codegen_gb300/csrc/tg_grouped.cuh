@@ -35,17 +35,17 @@
 //
 // What bounds it, measured (bf16 in and out, cold L2):
 //   32768 rows of 32 even groups, 2048 x 4096: 314 us in short runs (1751
-//     TFLOP/s, 94% of the 1861 of a plain library product in short runs; tensor
-//     pipe 88-95% active), 368-381 us when run for seconds, where the
-//     board's power limit lowers the clock (library: 1686 TFLOP/s).
-//   64 rows of 40 of 64 experts, 2048 x 1408: 37.8 us, 231 MB of weights at
-//     6.1 TB/s (90% of a plain copy): HBM.
+//     TFLOP/s, 91% of the 1931 of a plain library product in short runs; tensor
+//     pipe 88-95% active), 363-387 us when run for seconds, where the
+//     board's power limit lowers the clock (library: 1740 TFLOP/s).
+//   64 rows of 40 of 64 experts, 2048 x 1408: 37.3-37.8 us, 231 MB of weights at
+//     6.1 TB/s (92% of a plain copy): HBM.
 //   5003 rows of 11 groups, 1400 x 1000, weights N x K: 28.3 us; about a
 //     hundred pair tiles on 76 pairs are two turns, of which the second is a
 //     third full, and a tile of 22 k-blocks is half start and stores.  (Pair tiles
 //     of 128 rows: 30.8.)
 //   wgrad, 32768 rows of 16 groups, 2048 x 2048: 174 us short (1580
-//     TFLOP/s, 85%), 193 sustained: MN-major operands and fringe blocks.
+//     TFLOP/s, 82%), 189-198 sustained: MN-major operands and fringe blocks.
 //   wgrad, 1003 rows of 7 of 8 groups, 640 x 384, fp32: 5.7-6.2 us on the GPU:
 //     latency (start, two or three k-blocks, stores of 7.9 MB).
 //

@@ -6,7 +6,7 @@
 // All of it moves bytes (two flops a value): the bound is HBM for batches
 // and launch latency for a few tokens.  Offsets of rows are 64-bit.
 // Bandwidths below are the bytes a call cannot do without over its time, and
-// their fraction of a plain copy's 6791 GB/s on the same GPU.
+// their fraction of a plain copy's 6685 GB/s on the same GPU.
 //
 // The sort is a counting sort by expert, stable because an id's place is
 //     offsets[e] + (ids of e in earlier blocks) + (in earlier warps of the
@@ -286,7 +286,7 @@ __device__ __forceinline__ void copy_chunk(uint8_t *dst, const uint8_t *src, int
 // Block (32 >> shift tokens per warp) x 8 warps; grid.y: segments of a row.
 // Bound by HBM's writes (k times the reads), so a token's reads are not
 // repeated for its k slots: 16384 tokens of 2048 bf16, k 8, 604 MB: 90.5 us,
-// 6.67 TB/s (98%).  Copying inside the sort's last launch instead, so that it
+// 6.67 TB/s (100%).  Copying inside the sort's last launch instead, so that it
 // starts a launch earlier, made dispatch 118 us instead of 106: a block's
 // copies then wait for its own ranks.
 __global__ void __launch_bounds__(256) gather_aligned_kernel(const CopyArgs a, int shift)
@@ -652,7 +652,7 @@ struct Raw8<false> {
 // y[t] = sum_j w[t, j] ys[slot[t, j]], in the order of j, in fp32, rounded
 // once.  A thread owns 8 elements of a token: KB rows' loads in flight, which
 // is what keeps HBM busy at 48 registers and half the SM's warps.  16384
-// tokens of 4096 bf16, k 4, 661 MB: 103 us, 6.42 TB/s (95%); five tokens of
+// tokens of 4096 bf16, k 4, 661 MB: 103 us, 6.42 TB/s (96%); five tokens of
 // 1001: 2.5 us on the GPU.
 template <bool YS_BF16, bool Y_BF16, int KB>
 __global__ void __launch_bounds__(256) combine_aligned_kernel(const CombineArgs a, int shift)
@@ -776,7 +776,7 @@ __device__ __forceinline__ float block_sums(float (&v)[KB], float (*part)[KB])
 // whose rows of ys are loaded four at a time; all bf16 and 16-byte rows.  The
 // dot products are summed lane by lane, warp by warp, in a fixed order.  Reads
 // and writes share HBM about evenly, which costs it more than either alone:
-// 8191 tokens of 2056, k 8, 568 MB: 99.5 us, 5.70 TB/s (84%); the kernel
+// 8191 tokens of 2056, k 8, 568 MB: 99.5 us, 5.70 TB/s (85%); the kernel
 // itself moves 520 MB, as dys partly stays in L2.
 template <int KB>
 __global__ void __launch_bounds__(512) combine_grad_aligned_kernel(const GradArgs a)

@@ -241,7 +241,9 @@ __global__ void __launch_bounds__(ANY_COLS * 32) w4_any_kernel(const W4Args a)
 // word leaves in the two halves of a register.  The activations are paired
 // the same way.
 //
-// A code becomes bf16 exactly: 0x4300 | q is 128 + q, minus 128 + z; an E2M1
+// A code becomes bf16 exactly: 0x4300 | q is 128 + q, minus 128 + z (the integer
+// as mantissa bits of a constant that is then subtracted, the usual conversion by
+// a magic number; for weights of few bits see Kim et al., arXiv 2211.10017); an E2M1
 // code's three low bits sit on bf16's exponent and mantissa as its value times
 // 2^-126 (0.5 is a subnormal), and a product by 2^126 restores it.  The sum of
 // a group of codes is multiplied by its scale once, in fp32.
@@ -532,9 +534,10 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
 // Rows with a finite magnitude from W4_LARGE are computed value by value, scale
 // first.
 //
-// What bounds it is taking the codes apart.  Measured (calls on a graph, weights
-// not in L2): 1 row, 8192 x 28672 int4 by 128, 121 MB: 28.8 us, of which start,
-// first boxes, activations and last tiles are 5.7; with zero points 31.4; E2M1,
+// What bounds it is taking the codes apart (56% of issue slots).  Measured (calls
+// on a graph, weights not in L2): 1 row, 8192 x 28672 int4 by 128, 121 MB: 28.8 us,
+// a quarter of those 12.0: 5.4 TB/s between the two, and 6.4 us of start,
+// first boxes, activations and last tiles; with zero points 31.4; E2M1,
 // which has a scale for every 32 codes, 39.0.  32 rows over 20 of 64 experts, 2048 x
 // 1408 E2M1, 31 MB: 19.4 us, of which the start and a CTA's few turns are
 // most.  Tried: eight turns' activation loads in flight instead of four (3-4

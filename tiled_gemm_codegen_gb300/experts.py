@@ -8,7 +8,9 @@ happens in the CUDA library.  Calls are asynchronous on ``stream`` (default:
 torch's current stream).  A row starts behind the one before it: tensors whose
 rows share memory, as ``expand`` makes them (the gradient of a sum over
 tokens, uniform weights), are refused and go in as a copy (``contiguous()``);
-the matrices of a stack may share theirs.
+the matrices of a stack may share theirs.  As the rest of the package the
+calls record no gradients (``examples/moe_layer.py`` makes an autograd function
+of them), and outputs that they make belong to torch's current stream.
 """
 from __future__ import annotations
 
