@@ -1172,15 +1172,15 @@ bool plan_stream(const W4Args &a, bool e2m1, int64_t used, int sms, W4Stream &be
     }
     // A CTA's time: for each of its tiles a turn of `warps` boxes for every
     // step a warp has, and the tile's end.  Measured on 28672 rows of 8192
-    // codes (16 warps; teams of 16, 8, 4 and 2 warps: 27.4, 27.1, 31.0 and
-    // 33.7 us): a turn costs 1.5 times the end.  Fewer warps only shorten a
+    // codes (16 warps; teams of 16, 8, 4 and 2 warps: 31.6, 28.8, 35.1 and
+    // 33.2 us): a turn costs about 1.5 times the end.  Fewer warps only shorten a
     // turn to a half, where latency is what is left of it, and a ring of
     // fewer than 32 boxes (128 KB) stretches it: the activations of a slice
     // of K take its room.  More slices mean a second launch that adds them,
     // activations staged for each (its share of the CTA's tiles) and partial
     // products.  Measured (us; 1, 2, 4 and 8 slices, int4): 8 rows of 9216
-    // onto 8192 49, 29, 27, 25; 4 of 14336 onto 4096 29, 25, 21, 21; 8 of
-    // 8192 onto 28672 49, 45, 41, 47; 1 of 8192 onto 28672 33, 33, 35, 39.
+    // onto 8192 39, 24, 21, 21; 4 of 14336 onto 4096 21, 17, 15, 15; 8 of
+    // 8192 onto 28672 44, 41, 38, 44; 1 of 8192 onto 28672 29, 30, 31, 36.
     double best = 0.0;
     for (int32_t slices = 1; slices <= W4S_SLICES && slices <= p.all_steps; slices *= 2) {
         p.steps = (p.all_steps + slices - 1) / slices;
