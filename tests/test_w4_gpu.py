@@ -328,6 +328,34 @@ def test_large_activations_over_zero_weights(fmt, G, zeros, K, power):
     _check(y, xv, wv, [0, S], K, G, F32)
 
 
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+@pytest.mark.parametrize("K", ROWS_ON)
+@pytest.mark.parametrize("power", [115, 118, 121, 126])
+def test_large_activations_with_small_scales(fmt, G, zeros, K, power):
+    """A group's codes times its activations may add up to more than fp32's
+    largest value where its scale brings them back; rows of usual size and
+    a row with an infinity lie beside."""
+    N, S = 70, 6
+    W, sc, z, wv = _weights(1, N, K, fmt, G, 44, zeros)
+    if fmt == "e2m1":
+        sc -= 40
+    else:
+        sc *= 2.0 ** -40
+    wv = wv * 2.0 ** -40
+    x, xv = _x(S, K, 24)
+    for t in (1, 4):
+        x[t] = xv[t] = 2.0 ** power
+        x[t, ::3] = -1.5 * 2.0 ** power
+        xv[t, ::3] = -1.5 * 2.0 ** power
+    x[3, 77] = float("inf")
+    y = tg.gemv_w4(x, W[0], sc[0], zeros=z[0] if zeros else None, format=fmt, group=G)
+    keep = [0, 1, 2, 4, 5]
+    _check(y[keep], xv[keep], wv, [0, 5], K, G, F32)
+    w = wv[0][:, 77]
+    assert torch.equal(torch.isnan(y[3]).cpu(), torch.from_numpy(w == 0))
+    assert torch.equal(y[3].cpu()[w != 0], torch.from_numpy(np.where(w > 0, np.inf, -np.inf)[w != 0]).float())
+
+
 @pytest.mark.parametrize("K", ROWS_ON)
 @pytest.mark.parametrize("code", [0, 1, 120, 250, 254])
 def test_e2m1_scales_of_any_size(K, code):

@@ -220,6 +220,25 @@ __global__ void __launch_bounds__(ANY_COLS * 32) w4_any_kernel(const W4Args a)
     }
 }
 
+// Whole warp: <x[row], w_g[n]> over [k0, k1) value by value, for any values.
+template <bool E2M1>
+__device__ __forceinline__ float row_dot(const W4Args &a, int32_t g, int32_t n, int32_t row, int32_t k0, int32_t k1)
+{
+    const uint8_t *w = a.w + g * a.stride_w + n * a.ldw;
+    const int64_t s0 = g * a.stride_s + n * a.lds, z0 = g * a.stride_z + n * a.ldz;
+    const uint16_t *x = a.x + row * a.ldx;
+    float acc = 0.0f;
+    for (int32_t b = k0 / 2 + static_cast<int32_t>(threadIdx.x & 31); b < k1 / 2; b += 32) {
+        const uint32_t q = w[b];
+        const W4Run<E2M1> run(a, s0 + 2 * b / a.run, z0 + 2 * b / a.run);
+        acc = fmaf(run.weight(q & 15u) * bf16_value(x[2 * b]), run.late, acc);
+        acc = fmaf(run.weight(q >> 4) * bf16_value(x[2 * b + 1]), run.late, acc);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
+    return acc;
+}
+
 // ------------------------------------------------------------ tile kernel
 // For weights and activations whose rows lie on 4 bytes but not on TMA's 16.
 // A CTA computes W4_ROWS weight rows x up to 8 activation rows.  Its warps
@@ -359,7 +378,7 @@ struct W4Layout {
 
 // xt: activation rows the ring has room for (1 .. 8).
 template <bool E2M1, int RUN, bool ZEROS>
-__global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, int xt)
+__global__ void __launch_bounds__(W4_WARPS * 32, 1) w4_tile_kernel(const W4Args a, int xt)
 {
     using L = W4Layout<E2M1, RUN>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -505,6 +524,13 @@ __global__ void __launch_bounds__(W4_WARPS * 32) w4_tile_kernel(const W4Args a, 
             const int t = i / W4_ROWS, n = i % W4_ROWS;
             float sum = 0.0f;
             for (int v = 0; v < warps; ++v) sum += sums[(v * 8 + t) * W4_ROWS + n];
+            // A group's sum may overflow before its scale brings it back: what is not
+            // finite (a warp holds one activation row's) is summed value by value.
+            for (uint32_t left = __ballot_sync(0xffffffffu, n < rows && !isfinite(sum)); left; left &= left - 1) {
+                const int at = __ffs(left) - 1;
+                const float v = row_dot<E2M1>(a, grp, n0 + at, r0 + t, 0, a.K);
+                if (n == at) sum = v;
+            }
             if (n < rows) store_y(a, r0 + t, n0 + n, sum);
         }
         if (r0 + xt < hi) __syncthreads();  // the ring is filled again
@@ -650,25 +676,6 @@ __device__ __forceinline__ uint4 shared_u128(uint32_t a, int off)
 // 128 has weights up to 15, 2^119 for 32 up to 6.
 template <bool E2M1>
 constexpr int32_t W4_LARGE = (127 + (E2M1 ? 119 : 116)) << 7;
-
-// Whole warp: <x[row], w_g[n]> over [k0, k1) value by value, for any values.
-template <bool E2M1>
-__device__ __forceinline__ float row_dot(const W4Args &a, int32_t g, int32_t n, int32_t row, int32_t k0, int32_t k1)
-{
-    const uint8_t *w = a.w + g * a.stride_w + n * a.ldw;
-    const int64_t s0 = g * a.stride_s + n * a.lds, z0 = g * a.stride_z + n * a.ldz;
-    const uint16_t *x = a.x + row * a.ldx;
-    float acc = 0.0f;
-    for (int32_t b = k0 / 2 + static_cast<int32_t>(threadIdx.x & 31); b < k1 / 2; b += 32) {
-        const uint32_t q = w[b];
-        const W4Run<E2M1> run(a, s0 + 2 * b / a.run, z0 + 2 * b / a.run);
-        acc = fmaf(run.weight(q & 15u) * bf16_value(x[2 * b]), run.late, acc);
-        acc = fmaf(run.weight(q >> 4) * bf16_value(x[2 * b + 1]), run.late, acc);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-    return acc;
-}
 
 template <bool E2M1, int RUN, bool ZEROS>
 __global__ void __launch_bounds__((W4S_WARPS + 1) * 32, 1)
