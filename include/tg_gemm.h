@@ -522,6 +522,65 @@ tg_status tg_gemv_w4(const void *x, int64_t ldx, const void *W, int64_t ldw, int
                      int32_t format, int32_t group_size, const int32_t *offsets, int64_t groups, int64_t S, int64_t N,
                      int64_t K, void *y, int64_t ldy, int32_t y_type, tg_stream_t stream);
 
+/* ------------------------------------------------------------- projections
+ * A transformer block's projections with what stands around them fused in (no
+ * page of the method has a counterpart: as for the experts, the contraction is
+ * this library's).  Rows are dense - offsets NULL with groups = 1: all S rows
+ * meet the one W - or ragged, as in tg_gemm_grouped: the rows
+ * offsets[g] <= s < offsets[g + 1] meet W_g = W + g * strideW, bounds are
+ * clamped, an empty group costs nothing, and outputs' rows of no group are
+ * zeros.  Operands and outputs are bf16 unless said otherwise, sums fp32, any
+ * alignment of whole elements.  Outputs may not overlap inputs or one another.
+ * opt: cta_pair (1 = one-CTA tiles, 2 = two-SM tiles), force_pack, timeout_ns,
+ * debug_stall (1) and b_col_major (the weights stored N x K); the rest must be
+ * 0.  Other conventions as tg_gemm; extents below 2^31 - 1024 (2 F for a
+ * gated block's features). */
+
+/* A feed-forward block's gated projection: with z = X[s] W_g, 2 F values of
+ * which the first F are the gate,
+ *     H[s][f] = act(z[f]) * z[F + f]
+ * (S x F) and, where Z is not NULL, Z[s] = z (S x 2 F), both rounded once from
+ * fp32.  W_g is K x 2 F (b_col_major: stored 2 F x K, as a linear layer
+ * stores it).  activation is a tg_activation.  K == 0: zeros. */
+tg_status tg_gemm_gated(const void *X, const void *W, void *H, void *Z, const int32_t *offsets, int64_t groups,
+                        int64_t S, int64_t F, int64_t K, int64_t ldx, int64_t ldw, int64_t strideW, int64_t ldh,
+                        int64_t ldz, int32_t activation, tg_stream_t stream, const tg_options *opt);
+
+/* The gradient through it: with dh = dY[s] V_g, which stays in fp32 and is
+ * never stored,
+ *     dZ[s][f]     = dh[f] * Z[s][F + f] * act'(Z[s][f])
+ *     dZ[s][F + f] = dh[f] * act(Z[s][f])
+ * and, where H is not NULL, H[s][f] = act(Z[s][f]) * Z[s][F + f] again (what
+ * the next projection's weight gradient needs).  V_g is K x F: the next
+ * projection's weights transposed (b_col_major: stored F x K, those weights
+ * as they are), dY S x K, Z as tg_gemm_gated left it.  The gradients of X and
+ * W are products with dZ (tg_gemm_ex or tg_gemm_grouped with W transposed,
+ * tg_gemm_grouped_wgrad).  relu's slope at 0 is 0. */
+tg_status tg_gemm_gated_grad(const void *dY, const void *V, const void *Z, void *dZ, void *H, const int32_t *offsets,
+                             int64_t groups, int64_t S, int64_t F, int64_t K, int64_t lddy, int64_t ldv,
+                             int64_t strideV, int64_t ldz, int64_t lddz, int64_t ldh, int32_t activation,
+                             tg_stream_t stream, const tg_options *opt);
+
+/* A projection with low-rank adapters of many requests beside its shared
+ * weights: for the rows offsets[g] <= s < offsets[g + 1] of adapter g
+ *     u = scales[g] * X[s] A_g^T        (R values)
+ *     Y[s] = X[s] W + u B_g
+ * and Y[s] = X[s] W for rows of no adapter.  W is K x N (b_col_major: stored
+ * N x K), A_g = A + g * strideA is R x K, B_g = B + g * strideB R x N, both
+ * row-major; scales (fp32) may be NULL: ones.  Y is fp32 or bf16 (y_type),
+ * rounded once; u enters the second product as two bf16 parts (its first 17
+ * bits or more).  Where U is not NULL it receives u rounded to bf16 (S x R,
+ * zero for rows of no adapter).  An adapter's rows depend on its own matrices
+ * alone, whatever the others hold.  The gradient of X is the same call on dY,
+ * W transposed, B for A and A for B; with its U as dU the gradient of A is
+ * tg_gemm_grouped_wgrad(dU, X), that of B (U, dY).  offsets must be given;
+ * groups <= 4096 and R <= 256 (TG_ERR_UNSUPPORTED above). */
+tg_status tg_gemm_adapted(const void *X, const void *W, const void *A, const void *B, void *Y, void *U,
+                          const int32_t *offsets, const float *scales, int64_t groups, int64_t S, int64_t N, int64_t K,
+                          int64_t R, int64_t ldx, int64_t ldw, int64_t lda, int64_t strideA, int64_t ldb,
+                          int64_t strideB, int64_t ldy, int64_t ldu, int32_t y_type, tg_stream_t stream,
+                          const tg_options *opt);
+
 /* Synchronises `stream`, then reads and clears the device error words that
  * the kernels' watchdog writes: the one of `stream`'s workspace, and the one
  * of tg_gemm_splitk_static on the current device.  TG_ERR_TIMEOUT if a wait

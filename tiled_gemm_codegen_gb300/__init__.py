@@ -531,16 +531,17 @@ def device_error(stream=None) -> int:
 
 _EXPERTS = ("ExpertOrder", "expert_sort", "expert_dispatch", "expert_gather", "expert_combine", "expert_combine_grad",
             "gemm_grouped", "gemm_grouped_wgrad", "gemv_w4", "W4_FORMATS")
-__all__ += _EXPERTS
+_PROJECTIONS = ("gemm_gated", "gemm_gated_grad", "gemm_adapted")
+__all__ += _EXPERTS + _PROJECTIONS
 
 
 def __getattr__(name):
-    # the expert operators' module imports torch, which the rest of the
-    # package only does inside its calls
-    if name in _EXPERTS:
-        from . import experts
+    # these operators' modules import torch, which the rest of the package
+    # only does inside its calls
+    if name in _EXPERTS or name in _PROJECTIONS:
+        from . import experts, projections
 
-        value = getattr(experts, name)
+        value = getattr(experts if name in _EXPERTS else projections, name)
         globals()[name] = value
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

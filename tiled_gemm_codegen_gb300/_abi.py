@@ -140,6 +140,9 @@ SIGNATURES = {
                                                                      ctypes.POINTER(tg_options)], ctypes.c_int),
     "tg_gemv_w4": ([_vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _vp, _i64, _i64, _i64,
                     _i64, _vp, _i64, _i32, _vp], ctypes.c_int),
+    "tg_gemm_gated": ([_vp] * 5 + [_i64] * 9 + [_i32, _vp, ctypes.POINTER(tg_options)], ctypes.c_int),
+    "tg_gemm_gated_grad": ([_vp] * 6 + [_i64] * 10 + [_i32, _vp, ctypes.POINTER(tg_options)], ctypes.c_int),
+    "tg_gemm_adapted": ([_vp] * 8 + [_i64] * 13 + [_i32, _vp, ctypes.POINTER(tg_options)], ctypes.c_int),
     "tg_device_error": ([_vp], ctypes.c_int),
     "tg_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "tg_shutdown": ([], None),

@@ -10,6 +10,9 @@ Translation units (compiled in parallel, one ``-gencode`` for sm_103a):
 * ``csrc/tg_direct.cu``  - the direct-load kernel for small problems;
 * ``csrc/tg_route.cu``   - tokens sorted by expert and back, and the gradient;
 * ``csrc/tg_grouped.cu`` - the grouped GEMM (ragged rows, ragged contraction);
+* ``csrc/tg_block.cu``   - a block's projections (gated, its gradient, adapters),
+                           their kernel in ``csrc/tg_block_kernels.cu``, once a
+                           mode (-DTG_BLOCK_MODE=0 .. 3);
 * ``csrc/tg_w4.cu``      - products with 4-bit weights for a few rows.
 The CUDA runtime is linked statically, so the library loads on a machine
 without a GPU (every CUDA call then returns an error) and exports only the
@@ -90,10 +93,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             (os.path.join(CSRC, "tg_direct.cu"), os.path.join(BUILD, f"tg_direct_{machine}.o"), []),
             (os.path.join(CSRC, "tg_route.cu"), os.path.join(BUILD, f"tg_route_{machine}.o"), []),
             (os.path.join(CSRC, "tg_grouped.cu"), os.path.join(BUILD, f"tg_grouped_{machine}.o"), []),
+            (os.path.join(CSRC, "tg_block.cu"), os.path.join(BUILD, f"tg_block_{machine}.o"), []),
             (os.path.join(CSRC, "tg_w4.cu"), os.path.join(BUILD, f"tg_w4_{machine}.o"), [])]
     for bn in WIDTHS:
         jobs.append((os.path.join(CSRC, "tg_kernels.cu"),
                      os.path.join(BUILD, f"tg_kernels_bn{bn}_{machine}.o"), [f"-DTG_BN={bn}"]))
+    for mode in range(4):
+        jobs.append((os.path.join(CSRC, "tg_block_kernels.cu"),
+                     os.path.join(BUILD, f"tg_block_mode{mode}_{machine}.o"), [f"-DTG_BLOCK_MODE={mode}"]))
     flags = (["-DTG_DEBUG_CHECKS"] if checks else []) + list(extra_flags or [])
     if flags:
         jobs = [(s, o, d + flags) for (s, o, d) in jobs]

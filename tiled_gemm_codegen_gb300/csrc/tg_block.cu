@@ -1,0 +1,583 @@
+// Entry points of the block projections (include/tg_gemm.h): argument checks,
+// the tile choice, tensor maps and launches of block_kernel (tg_block.cuh),
+// and the tables of adapters that its extended contraction goes by.
+#include <algorithm>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "tg_block.h"
+#include "tg_gemm.h"
+#include "tg_host_api.h"
+#include "tg_tiles.h"
+
+#define TG_API extern "C" __attribute__((visibility("default")))
+
+namespace tg {
+namespace {
+
+constexpr int64_t ADAPT_GROUPS = 4096;  // adapters a call takes at most
+constexpr int64_t ADAPT_RANK = 256;
+
+// ------------------------------------------------------------ adapter tables
+constexpr int TABLE_THREADS = 1024;
+
+// Inclusive scan over the block (max or sum); `part` holds 33 words.
+template <bool MAX>
+__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t *part)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v = MAX ? max(v, o) : v + o;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        int32_t t = part[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, t, d);
+            if (lane >= d) t = MAX ? max(t, o) : t + o;
+        }
+        part[lane] = t;
+    }
+    __syncthreads();
+    if (warp > 0) v = MAX ? max(v, part[warp - 1]) : v + part[warp - 1];
+    return v;
+}
+
+// Block 0: the tables of AdapterTables but the flags (bounds clamped as the
+// walks clamp them: inside [0, S], never falling).  The others: a share of one
+// group's B each, flagged if it holds an infinity or NaN.
+__global__ void __launch_bounds__(TABLE_THREADS) adapter_tables_kernel(const BlockParams p, int32_t bn, int32_t tiles, int32_t N,
+                                                                       int32_t vec)
+{
+    __shared__ int32_t part[32];
+    const int tid = static_cast<int>(threadIdx.x);
+    if (blockIdx.x > 0) {
+        const int32_t g = static_cast<int32_t>(blockIdx.x - 1) / ADAPT_FLAGS, c = static_cast<int32_t>(blockIdx.x - 1) % ADAPT_FLAGS;
+        int32_t bad = 0;
+        if (p.offsets[g + 1] > p.offsets[g]) {
+            for (int32_t r = c; r < p.R; r += ADAPT_FLAGS) {
+                const uint16_t *row = p.b + g * p.strideB + r * p.ldb;
+                const int32_t body = vec ? N / 8 : 0;
+                for (int32_t i = tid; i < body; i += TABLE_THREADS) {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row) + i);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        bad |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+                }
+                for (int32_t i = body * 8 + tid; i < N; i += TABLE_THREADS) bad |= (row[i] & 0x7f80u) == 0x7f80u;
+            }
+        }
+        bad = __syncthreads_or(bad);
+        if (tid == 0) p.tab.flags[g * ADAPT_FLAGS + c] = bad;
+        return;
+    }
+    int32_t last = max(0, min(p.offsets[0], p.S)), used = 0;
+    for (int32_t g0 = 0; g0 < p.groups; g0 += TABLE_THREADS) {
+        const int32_t g = g0 + tid;
+        int32_t hi = g < p.groups ? max(0, min(p.offsets[g + 1], p.S)) : 0;
+        hi = block_scan<true>(max(hi, last), part);
+        __shared__ int32_t his[TABLE_THREADS];
+        his[tid] = hi;
+        __syncthreads();
+        const int32_t lo = tid > 0 ? his[tid - 1] : last;
+        const int32_t has = g < p.groups && hi > lo ? 1 : 0;
+        const int32_t at = used + block_scan<false>(has, part) - has;
+        if (has) {
+            p.tab.ids[at] = g;
+            p.tab.lo[at] = lo;
+            p.tab.hi[at] = hi;
+            p.tab.rank[g] = at;
+        }
+        last = his[TABLE_THREADS - 1];
+        used += part[31];
+        __syncthreads();
+    }
+    int32_t blocks = 0;
+    for (int32_t t0 = 0; t0 < tiles; t0 += TABLE_THREADS) {
+        const int32_t t = t0 + tid;
+        int32_t n = 0;
+        if (t < tiles) {
+            const int64_t r0 = static_cast<int64_t>(t) * bn, r1 = r0 + bn;
+            int32_t a = 0, b = used;  // first with hi > r0
+            while (a < b) {
+                const int32_t m = (a + b) / 2;
+                if (p.tab.hi[m] > r0)
+                    b = m;
+                else
+                    a = m + 1;
+            }
+            const int32_t first = a;
+            b = used;  // first with lo >= r1
+            while (a < b) {
+                const int32_t m = (a + b) / 2;
+                if (p.tab.lo[m] >= r1)
+                    b = m;
+                else
+                    a = m + 1;
+            }
+            p.tab.first[t] = first;
+            p.tab.count[t] = a - first;
+            n = adapter_blocks(a - first, p.Rp);
+        }
+        const int32_t at = blocks + block_scan<false>(n, part);
+        if (t < tiles) p.tab.blocks[t + 1] = at;
+        blocks += part[31];
+        __syncthreads();
+    }
+    if (tid == 0) p.tab.blocks[0] = 0;
+}
+
+// ------------------------------------------------------------ launches
+struct BlockMaps {
+    CUtensorMap x{}, w{}, v{}, e{}, o{}, g{}, u{};
+};
+
+// Per kernel: the devices whose shared-memory opt-in is made and the number of
+// co-resident pairs there (under the host mutex).
+struct BlockShapeState {
+    uint64_t configured = 0;
+    int pairs[64] = {};
+};
+
+const BlockShape &shape_of(int mode, BlockTiles tiles, BlockShapeState **state)
+{
+    static const BlockShape shapes[4][3] = {
+        {block_shape_gated(TILES_PAIR), block_shape_gated(TILES_ONE), block_shape_gated(TILES_FEW)},
+        {block_shape_grad(TILES_PAIR), block_shape_grad(TILES_ONE), block_shape_grad(TILES_FEW)},
+        {block_shape_shrink(TILES_ONE), block_shape_shrink(TILES_ONE), block_shape_shrink(TILES_FEW)},
+        {block_shape_adapt(TILES_PAIR), block_shape_adapt(TILES_ONE), block_shape_adapt(TILES_FEW)}};
+    static BlockShapeState states[4][3];
+    *state = &states[mode][tiles];
+    return shapes[mode][tiles];
+}
+
+cudaLaunchConfig_t block_config(const BlockShape &k, int grid, cudaStream_t s, cudaLaunchAttribute (&attr)[2])
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(BLOCK_THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(k.smem);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = k.pair ? 2 : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+cudaError_t launch_block(int mode, BlockTiles tiles, const HostStream &hs, int64_t units, const BlockMaps &m, const BlockParams &p)
+{
+    BlockShapeState *st;
+    const BlockShape &k = shape_of(mode, tiles, &st);
+    cudaLaunchAttribute attr[2];
+    const bool known = hs.dev < 64 && ((st->configured >> hs.dev) & 1u);
+    int pairs = known ? st->pairs[hs.dev] : 0;
+    if (!known) {
+        cudaError_t e = cudaFuncSetAttribute(k.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+        if (e != cudaSuccess) return e;
+        if (k.pair) {
+            cudaLaunchConfig_t cfg = block_config(k, 2, hs.stream, attr);
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&pairs, k.kern, &cfg);
+            if (e != cudaSuccess) return e;
+            if (pairs < 1) return cudaErrorInvalidConfiguration;
+        }
+        if (hs.dev < 64) {
+            st->pairs[hs.dev] = pairs;
+            st->configured |= 1ull << hs.dev;
+        }
+    }
+    const int64_t workers = std::max<int64_t>(1, std::min<int64_t>(units, k.pair ? pairs : hs.sms));
+    const cudaLaunchConfig_t cfg = block_config(k, static_cast<int>(workers) * (k.pair ? 2 : 1), hs.stream, attr);
+    return cudaLaunchKernelEx(&cfg, k.kern, m.x, m.w, m.v, m.e, m.o, m.g, m.u, p);
+}
+
+// How a product over ragged rows is cut: tiles of `features` x bn rows, shares.
+struct Cut {
+    BlockTiles tiles;
+    int64_t bn, features, units, splits;
+    int64_t part_tiles() const { return splits > 1 ? units * (tiles == TILES_PAIR ? 2 : 1) : 0; }
+    size_t part_bytes() const { return static_cast<size_t>(part_tiles()) * splits * BM * bn * 4; }
+};
+
+// `lanes`: accumulator lanes a feature takes (GATED: 2).  Tiles as grouped
+// rows choose them (tiles_cost): pairs or one CTA, and 32 rows where
+// groups have few, whose ring is deeper (weights are the traffic).
+Cut cut_rows(int mode, int64_t S, int64_t N, int64_t K, int64_t groups, int sms, const tg_options *opt)
+{
+    const int64_t lanes = mode == BLOCK_GATED ? 2 : 1, hit = std::min(groups, S);
+    bool pair = N * lanes > 128 && S > 32 * hit &&
+                tiles_cost(false, true, S, 0, N * lanes, K, groups, sms) < tiles_cost(false, false, S, 0, N * lanes, K, groups, sms);
+    if (opt && opt->cta_pair) pair = opt->cta_pair == 2;
+    if (mode == BLOCK_SHRINK) pair = false;
+    Cut c;
+    c.tiles = pair ? TILES_PAIR : S <= 32 * hit ? TILES_FEW : TILES_ONE;
+    c.bn = pair ? 256 : c.tiles == TILES_FEW ? 32 : 128;
+    c.features = (pair ? 256 : 128) / lanes;
+    c.units = (S / c.bn + hit) * cdiv(N, c.features);
+    if (groups == 1) c.units = cdiv(S, c.bn) * cdiv(N, c.features);
+    const int64_t depth = cdiv(K, BK);
+    const int64_t share = share_of(false, pair, c.units, depth, sms);
+    c.splits = share == 0 ? 1 : std::min(SPLIT_MOST, cdiv(depth, share));
+    return c;
+}
+
+void set_cut(BlockParams &p, const Cut &c, int64_t N)
+{
+    p.tiles_n = static_cast<int32_t>(cdiv(N, c.features));
+    p.splits = static_cast<int32_t>(c.splits);
+}
+
+// The options that apply here: cta_pair (1 or 2), force_pack, timeout_ns,
+// debug_stall (1), b_col_major; everything else has to be 0.
+bool options_ok(const tg_options *o)
+{
+    if (!o) return true;
+    return !o->block_n && !o->stages && !o->split_k && !o->epilogue && !o->max_ctas && (o->debug_stall == 0 || o->debug_stall == 1) &&
+           !o->stream_k && !o->operands && !o->trace_buffer && !o->a_col_major && !o->direct && o->cta_pair >= 0 && o->cta_pair <= 2;
+}
+
+bool map_operand(CUtensorMap *m, const Operand &o, uint32_t box1)
+{
+    return host_encode_3d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, o.p, o.cols, o.rows, o.nb, o.ld * 2, problem_stride(o), 64, box1,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// An output's description, and a tensor map of it where TMA can address it.
+BlockOut output(CUtensorMap *m, void *ptr, int64_t rows, int64_t cols, int64_t ld, int64_t size)
+{
+    BlockOut o{ptr, ld, 0};
+    if (ptr && tma_ok(ptr, ld, 0, size))
+        o.tma = host_encode_3d(m, size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ptr, cols, rows, 1,
+                               ld * size, cdiv(rows * ld * size, 16) * 16, static_cast<uint32_t>(128 / size), 32, CU_TENSOR_MAP_SWIZZLE_128B)
+                    ? 1
+                    : 0;
+    return o;
+}
+
+// Scratch of a call: pieces of the stream's arena.
+struct Scratch {
+    size_t size = 0;
+    size_t take(size_t bytes)
+    {
+        const size_t at = size;
+        size += (bytes + 255) / 256 * 256;
+        return at;
+    }
+};
+
+// Copies operands that TMA cannot address to their places in the arena, two a
+// launch; they become the copies.
+cudaError_t pack_operands(const HostStream &hs, uint8_t *arena, Operand *const *ops, const size_t *at, int n)
+{
+    HostPack job;
+    bool have = false;
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i <= n && e == cudaSuccess; ++i) {
+        HostPack next;
+        bool more = false;
+        if (i < n && ops[i]->pack) {
+            Operand &o = *ops[i];
+            next = HostPack{o.p, arena + at[i], o.rows, o.cols, o.ld, o.nb, o.stride};
+            o.p = next.dst;
+            o.ld = cdiv(o.cols, 64) * 64;
+            o.stride = o.rows * o.ld;
+            more = true;
+        }
+        if (have && (more || i == n)) {
+            e = host_pack(hs, &job, more ? &next : nullptr);
+            have = false;
+        } else if (more) {
+            job = next;
+            have = true;
+        }
+    }
+    return e;
+}
+
+void set_common(BlockParams &p, const HostStream &hs, const tg_options *opt)
+{
+    p.group_m = 8;
+    p.err = hs.err;
+    p.timeout_ns = opt && opt->timeout_ns ? opt->timeout_ns : HOST_TIMEOUT_NS;
+    p.debug_stall = opt ? opt->debug_stall : 0;
+}
+
+// GATED and GRAD.  w: GATED the gate half of the weights, v its up half.
+tg_status run_gated(int mode, Operand x, Operand w, Operand v, bool w_k, uint16_t *H, int64_t ldh, uint16_t *zout, int64_t ldzout,
+                    const uint16_t *z, int64_t ldz, const int32_t *offsets, int64_t groups, int64_t S, int64_t F, int64_t K,
+                    int32_t act, const tg_options *opt, cudaStream_t stream)
+{
+    std::lock_guard<std::mutex> lock(host_mutex());
+    HostStream hs;
+    tg_status st = host_stream(stream, &hs);
+    if (st != TG_OK) return st;
+    const Cut c = cut_rows(mode, S, F, K, groups, hs.sms, opt);
+    if (c.units * c.splits > INT32_MAX) return TG_ERR_UNSUPPORTED;
+
+    BlockParams p{};
+    BlockMaps m;
+    p.offsets = offsets;
+    p.groups = static_cast<int32_t>(groups);
+    p.S = static_cast<int32_t>(S);
+    p.N = static_cast<int32_t>(F);
+    p.k_blocks = static_cast<int32_t>(cdiv(K, BK));
+    p.w_k = w_k ? 1 : 0;
+    p.act = act;
+    p.out_bf16 = 1;
+    p.z = z;
+    p.ldz = ldz;
+    set_cut(p, c, F);
+    set_common(p, hs, opt);
+
+    const bool gated = mode == BLOCK_GATED;
+    if (w.nb > 1 && w.stride == 0) {  // one matrix for every group
+        w.nb = v.nb = 1;
+        p.w_shared = 1;
+    }
+    const bool force = opt && opt->force_pack;
+    if (K > 0) {
+        x.pack = force || !tma_ok(x.p, x.ld, 0, 2);
+        w.pack = force || !tma_ok(w.p, w.ld, w.nb > 1 ? w.stride : 0, 2);
+        v.pack = gated && (force || !tma_ok(v.p, v.ld, v.nb > 1 ? v.stride : 0, 2));
+    }
+    Scratch s;
+    const size_t at_part = s.take(c.part_bytes());
+    Operand *ops[3] = {&x, &w, &v};
+    const size_t at[3] = {s.take(pack_bytes(x)), s.take(pack_bytes(w)), s.take(pack_bytes(v))};
+    void *arena = nullptr;
+    if (s.size && (st = host_arena(hs, s.size, &arena)) != TG_OK) return st;
+    if (c.splits > 1) {
+        p.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(arena) + at_part);
+        if ((st = host_counters(hs, static_cast<size_t>(c.part_tiles()) * 4, &p.counters)) != TG_OK) return st;
+    }
+    cudaError_t e = pack_operands(hs, static_cast<uint8_t *>(arena), ops, at, 3);
+    if (e != cudaSuccess) return host_cuda_status(e);
+    if (K > 0) {
+        const uint32_t x_box = static_cast<uint32_t>(c.tiles == TILES_PAIR ? c.bn / 2 : c.bn);
+        const uint32_t w_box = w_k ? (gated ? BM / 2 : BM) : BK;
+        if (!map_operand(&m.x, x, x_box) || !map_operand(&m.w, w, w_box) || (gated && !map_operand(&m.v, v, w_box))) return TG_ERR_CUDA;
+    }
+    p.out0 = output(&m.o, H, S, F, ldh, 2);
+    p.gate = output(&m.g, zout, S, F, ldzout, 2);
+    p.up = output(&m.u, zout ? zout + F : nullptr, S, F, ldzout, 2);
+    return host_cuda_status(launch_block(mode, c.tiles, hs, c.units * c.splits, m, p));
+}
+
+tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void *Y, int64_t ldy, bool out_bf16, uint16_t *U,
+                      int64_t ldu, const int32_t *offsets, const float *scales, int64_t groups, int64_t S, int64_t N, int64_t K,
+                      int64_t R, const tg_options *opt, cudaStream_t stream)
+{
+    std::lock_guard<std::mutex> lock(host_mutex());
+    HostStream hs;
+    tg_status st = host_stream(stream, &hs);
+    if (st != TG_OK) return st;
+    const int64_t Rp = R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : cdiv(R, 64) * 64;
+    const int64_t hit = std::min(groups, S);
+    // the adapters' first product, by group; the shared one, all rows
+    const Cut ca = cut_rows(BLOCK_SHRINK, S, R, K, groups, hs.sms, opt);
+    const Cut cy = cut_rows(BLOCK_ADAPT, S, N, K, 1, hs.sms, opt);
+    if (ca.units * ca.splits > INT32_MAX || cy.units * cy.splits > INT32_MAX) return TG_ERR_UNSUPPORTED;
+    const int64_t tiles = cdiv(S, cy.bn);
+    // A tile's blocks round its adapters up; together at most so many.
+    const int64_t blocks = Rp <= 32 ? std::min(tiles + hit, tiles + cdiv((tiles + hit) * Rp, 32)) : (tiles + hit) * (Rp / 32);
+    if (blocks * cy.bn > INT32_MAX) return TG_ERR_UNSUPPORTED;
+
+    BlockParams p{};
+    BlockMaps m;
+    set_common(p, hs, opt);
+    p.S = static_cast<int32_t>(S);
+    p.k_blocks = static_cast<int32_t>(cdiv(K, BK));
+    p.R = static_cast<int32_t>(R);
+    p.Rp = static_cast<int32_t>(Rp);
+    p.wide_bn = static_cast<int32_t>(cy.bn);
+    p.scales = scales;
+    p.b = static_cast<const uint16_t *>(b.p);
+    p.ldb = b.ld;
+    p.strideB = b.nb > 1 ? b.stride : 0;
+
+    const bool force = opt && opt->force_pack;
+    const bool a_shared = a.nb > 1 && a.stride == 0;
+    if (a_shared) a.nb = 1;
+    if (K > 0) {
+        x.pack = force || !tma_ok(x.p, x.ld, 0, 2);
+        w.pack = force || !tma_ok(w.p, w.ld, 0, 2);
+        a.pack = force || !tma_ok(a.p, a.ld, a.nb > 1 ? a.stride : 0, 2);
+    }
+    const bool b_vec = tma_ok(b.p, b.ld, b.nb > 1 ? b.stride : 0, 2);
+    b.pack = force || !b_vec;
+    if (b.nb > 1 && b.stride == 0) {  // one matrix for every adapter
+        b.nb = 1;
+        p.b_shared = 1;
+    }
+    Scratch s;
+    const size_t at_part = s.take(std::max(ca.part_bytes(), cy.part_bytes()));
+    Operand *ops[4] = {&x, &w, &a, &b};
+    const size_t at[4] = {s.take(pack_bytes(x)), s.take(pack_bytes(w)), s.take(pack_bytes(a)), s.take(pack_bytes(b))};
+    const size_t at_wide = s.take(static_cast<size_t>(blocks) * cy.bn * 128);
+    const size_t words[7] = {static_cast<size_t>(hit), static_cast<size_t>(hit), static_cast<size_t>(hit), static_cast<size_t>(groups),
+                             static_cast<size_t>(tiles), static_cast<size_t>(tiles), static_cast<size_t>(tiles + 1)};
+    size_t at_tab[7];
+    for (int i = 0; i < 7; ++i) at_tab[i] = s.take(words[i] * 4);
+    const size_t at_flags = s.take(static_cast<size_t>(groups) * ADAPT_FLAGS * 4);
+    void *mem = nullptr;
+    if ((st = host_arena(hs, s.size, &mem)) != TG_OK) return st;
+    uint8_t *arena = static_cast<uint8_t *>(mem);
+    auto table = [&](size_t off) { return reinterpret_cast<int32_t *>(arena + off); };
+    p.tab = AdapterTables{table(at_tab[0]), table(at_tab[1]), table(at_tab[2]), table(at_tab[3]),
+                          table(at_tab[4]), table(at_tab[5]), table(at_tab[6]), table(at_flags)};
+    p.wide = reinterpret_cast<uint16_t *>(arena + at_wide);
+    p.partials = reinterpret_cast<float *>(arena + at_part);
+    if (ca.splits > 1 || cy.splits > 1) {
+        if ((st = host_counters(hs, static_cast<size_t>(std::max(ca.part_tiles(), cy.part_tiles())) * 4, &p.counters)) != TG_OK) return st;
+    }
+    cudaError_t e = pack_operands(hs, arena, ops, at, 4);
+    if (e != cudaSuccess) return host_cuda_status(e);
+
+    p.offsets = offsets;
+    p.groups = static_cast<int32_t>(groups);
+    p.N = static_cast<int32_t>(R);
+    adapter_tables_kernel<<<static_cast<unsigned>(1 + groups * ADAPT_FLAGS), TABLE_THREADS, 0, hs.stream>>>(
+        p, static_cast<int32_t>(cy.bn), static_cast<int32_t>(tiles), static_cast<int32_t>(N), b_vec ? 1 : 0);
+    if ((e = cudaGetLastError()) != cudaSuccess) return host_cuda_status(e);
+
+    // u
+    BlockParams pa = p;
+    pa.w_k = 1;
+    pa.w_shared = a_shared ? 1 : 0;
+    pa.out_bf16 = 1;
+    pa.out0 = BlockOut{U, ldu, 0};
+    set_cut(pa, ca, R);
+    if (K > 0 && (!map_operand(&m.x, x, static_cast<uint32_t>(ca.bn)) || !map_operand(&m.w, a, BM))) return TG_ERR_CUDA;
+    if ((e = launch_block(BLOCK_SHRINK, ca.tiles, hs, ca.units * ca.splits, m, pa)) != cudaSuccess) return host_cuda_status(e);
+
+    // Y
+    const bool pair = cy.tiles == TILES_PAIR;
+    p.offsets = nullptr;
+    p.groups = 1;
+    p.N = static_cast<int32_t>(N);
+    p.w_k = w_k ? 1 : 0;
+    p.out_bf16 = out_bf16 ? 1 : 0;
+    p.out0 = output(&m.o, Y, S, N, ldy, out_bf16 ? 2 : 4);
+    set_cut(p, cy, N);
+    const uint32_t rows_box = static_cast<uint32_t>(pair ? cy.bn / 2 : cy.bn);
+    if (K > 0 && (!map_operand(&m.x, x, rows_box) || !map_operand(&m.w, w, w_k ? BM : BK))) return TG_ERR_CUDA;
+    const Operand wide{p.wide, blocks * cy.bn, 64, 64, 1, 0};
+    if (!map_operand(&m.v, b, static_cast<uint32_t>(std::min<int64_t>(Rp, 64))) || !map_operand(&m.e, wide, rows_box)) return TG_ERR_CUDA;
+    return host_cuda_status(launch_block(BLOCK_ADAPT, cy.tiles, hs, cy.units * cy.splits, m, p));
+}
+
+bool act_ok(int32_t act) { return act >= TG_ACT_NONE && act <= TG_ACT_SILU; }
+bool halves_ok(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+}  // namespace
+}  // namespace tg
+
+using namespace tg;
+
+TG_API tg_status tg_gemm_gated(const void *X, const void *W, void *H, void *Z, const int32_t *offsets, int64_t groups, int64_t S,
+                               int64_t F, int64_t K, int64_t ldx, int64_t ldw, int64_t strideW, int64_t ldh, int64_t ldz,
+                               int32_t activation, tg_stream_t stream, const tg_options *opt)
+{
+    return host_guard([&] {
+        if (groups < 1 || groups > GROUPED_EXTENT || !extent_ok(S) || F < 0 || F > GROUPED_EXTENT / 2 || !extent_ok(K))
+            return TG_ERR_INVALID_ARG;
+        if (!options_ok(opt) || !act_ok(activation) || (!offsets && groups > 1)) return TG_ERR_INVALID_ARG;
+        const bool w_k = opt && opt->b_col_major;
+        const int64_t w_rows = w_k ? 2 * F : K, w_cols = w_k ? K : 2 * F;
+        if (!pitch_ok(ldx, K) || !pitch_ok(ldw, w_cols) || !pitch_ok(ldh, F) || (Z && !pitch_ok(ldz, 2 * F)) || strideW < 0 ||
+            strideW > PITCH_LIMIT || !span_ok(1, 0, S, ldx) || !span_ok(groups, strideW, w_rows, ldw) || !span_ok(1, 0, S, ldh) ||
+            (Z && !span_ok(1, 0, S, ldz)))
+            return TG_ERR_INVALID_ARG;
+        if (S == 0 || F == 0) return TG_OK;
+        if (!H || (K > 0 && (!X || !W))) return TG_ERR_INVALID_ARG;
+        if (!halves_ok(X) || !halves_ok(W) || !halves_ok(H) || !halves_ok(Z) || !host_words_ok(offsets)) return TG_ERR_INVALID_ARG;
+        const Bytes h = bytes_of(H, 1, 0, S, ldh, F, 2), z = bytes_of(Z, 1, 0, S, ldz, 2 * F, 2);
+        const Bytes in[3] = {bytes_of(X, 1, 0, S, ldx, K, 2), bytes_of(W, groups, strideW, w_rows, ldw, w_cols, 2),
+                             bytes_of(offsets, 1, 0, 1, 0, groups + 1, 4)};
+        for (const Bytes &i : in)
+            if (meets(h, i) || meets(z, i)) return TG_ERR_INVALID_ARG;
+        if (meets(h, z)) return TG_ERR_INVALID_ARG;
+        const uint16_t *up = static_cast<const uint16_t *>(W) + (W ? (w_k ? F * ldw : F) : 0);
+        const Operand w{W, w_k ? F : K, w_k ? K : F, ldw, groups, strideW}, v{up, w.rows, w.cols, ldw, groups, strideW};
+        return run_gated(BLOCK_GATED, Operand{X, S, K, ldx, 1, 0}, w, v, w_k, static_cast<uint16_t *>(H), ldh,
+                         static_cast<uint16_t *>(Z), ldz, nullptr, 0, offsets, groups, S, F, K, activation, opt,
+                         reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+TG_API tg_status tg_gemm_gated_grad(const void *dY, const void *V, const void *Z, void *dZ, void *H, const int32_t *offsets,
+                                    int64_t groups, int64_t S, int64_t F, int64_t K, int64_t lddy, int64_t ldv, int64_t strideV,
+                                    int64_t ldz, int64_t lddz, int64_t ldh, int32_t activation, tg_stream_t stream,
+                                    const tg_options *opt)
+{
+    return host_guard([&] {
+        if (groups < 1 || groups > GROUPED_EXTENT || !extent_ok(S) || F < 0 || F > GROUPED_EXTENT / 2 || !extent_ok(K))
+            return TG_ERR_INVALID_ARG;
+        if (!options_ok(opt) || !act_ok(activation) || (!offsets && groups > 1)) return TG_ERR_INVALID_ARG;
+        const bool v_k = opt && opt->b_col_major;
+        const int64_t v_rows = v_k ? F : K, v_cols = v_k ? K : F;
+        if (!pitch_ok(lddy, K) || !pitch_ok(ldv, v_cols) || !pitch_ok(ldz, 2 * F) || !pitch_ok(lddz, 2 * F) ||
+            (H && !pitch_ok(ldh, F)) || strideV < 0 || strideV > PITCH_LIMIT || !span_ok(1, 0, S, lddy) ||
+            !span_ok(groups, strideV, v_rows, ldv) || !span_ok(1, 0, S, ldz) || !span_ok(1, 0, S, lddz) || (H && !span_ok(1, 0, S, ldh)))
+            return TG_ERR_INVALID_ARG;
+        if (S == 0 || F == 0) return TG_OK;
+        if (!Z || !dZ || (K > 0 && (!dY || !V))) return TG_ERR_INVALID_ARG;
+        if (!halves_ok(dY) || !halves_ok(V) || !halves_ok(Z) || !halves_ok(dZ) || !halves_ok(H) || !host_words_ok(offsets))
+            return TG_ERR_INVALID_ARG;
+        const Bytes h = bytes_of(H, 1, 0, S, ldh, F, 2), dz = bytes_of(dZ, 1, 0, S, lddz, 2 * F, 2);
+        const Bytes in[4] = {bytes_of(dY, 1, 0, S, lddy, K, 2), bytes_of(V, groups, strideV, v_rows, ldv, v_cols, 2),
+                             bytes_of(Z, 1, 0, S, ldz, 2 * F, 2), bytes_of(offsets, 1, 0, 1, 0, groups + 1, 4)};
+        for (const Bytes &i : in)
+            if (meets(h, i) || meets(dz, i)) return TG_ERR_INVALID_ARG;
+        if (meets(h, dz)) return TG_ERR_INVALID_ARG;
+        return run_gated(BLOCK_GRAD, Operand{dY, S, K, lddy, 1, 0}, Operand{V, v_rows, v_cols, ldv, groups, strideV}, Operand{}, v_k,
+                         static_cast<uint16_t *>(H), ldh, static_cast<uint16_t *>(dZ), lddz, static_cast<const uint16_t *>(Z), ldz,
+                         offsets, groups, S, F, K, activation, opt, reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+TG_API tg_status tg_gemm_adapted(const void *X, const void *W, const void *A, const void *B, void *Y, void *U,
+                                 const int32_t *offsets, const float *scales, int64_t groups, int64_t S, int64_t N, int64_t K,
+                                 int64_t R, int64_t ldx, int64_t ldw, int64_t lda, int64_t strideA, int64_t ldb, int64_t strideB,
+                                 int64_t ldy, int64_t ldu, int32_t y_type, tg_stream_t stream, const tg_options *opt)
+{
+    return host_guard([&] {
+        if (groups < 1 || !extent_ok(S) || !extent_ok(N) || !extent_ok(K) || R < 1) return TG_ERR_INVALID_ARG;
+        if (groups > ADAPT_GROUPS || R > ADAPT_RANK) return TG_ERR_UNSUPPORTED;
+        if (!options_ok(opt) || (y_type != TG_F32 && y_type != TG_BF16)) return TG_ERR_INVALID_ARG;
+        const bool w_k = opt && opt->b_col_major;
+        const int64_t w_rows = w_k ? N : K, w_cols = w_k ? K : N, eb = y_type == TG_BF16 ? 2 : 4;
+        if (!pitch_ok(ldx, K) || !pitch_ok(ldw, w_cols) || !pitch_ok(lda, K) || !pitch_ok(ldb, N) || !pitch_ok(ldy, N) ||
+            (U && !pitch_ok(ldu, R)) || strideA < 0 || strideA > PITCH_LIMIT || strideB < 0 || strideB > PITCH_LIMIT ||
+            !span_ok(1, 0, S, ldx) || !span_ok(1, 0, w_rows, ldw) || !span_ok(groups, strideA, R, lda) ||
+            !span_ok(groups, strideB, R, ldb) || !span_ok(1, 0, S, ldy) || (U && !span_ok(1, 0, S, ldu)))
+            return TG_ERR_INVALID_ARG;
+        if (S == 0 || N == 0) return TG_OK;
+        if (!offsets || !Y || !B || (K > 0 && (!X || !W || !A))) return TG_ERR_INVALID_ARG;
+        if (!halves_ok(X) || !halves_ok(W) || !halves_ok(A) || !halves_ok(B) || !halves_ok(U) ||
+            reinterpret_cast<uintptr_t>(Y) % eb || !host_words_ok(offsets, scales))
+            return TG_ERR_INVALID_ARG;
+        const Bytes y = bytes_of(Y, 1, 0, S, ldy, N, eb), u = bytes_of(U, 1, 0, S, ldu, R, 2);
+        const Bytes in[6] = {bytes_of(X, 1, 0, S, ldx, K, 2), bytes_of(W, 1, 0, w_rows, ldw, w_cols, 2),
+                             bytes_of(A, groups, strideA, R, lda, K, 2), bytes_of(B, groups, strideB, R, ldb, N, 2),
+                             bytes_of(offsets, 1, 0, 1, 0, groups + 1, 4), bytes_of(scales, 1, 0, 1, 0, groups, 4)};
+        for (const Bytes &i : in)
+            if (meets(y, i) || meets(u, i)) return TG_ERR_INVALID_ARG;
+        if (meets(y, u)) return TG_ERR_INVALID_ARG;
+        return run_adapted(Operand{X, S, K, ldx, 1, 0}, Operand{W, w_rows, w_cols, ldw, 1, 0}, w_k,
+                           Operand{A, R, K, lda, groups, strideA}, Operand{B, R, N, ldb, groups, strideB}, Y, ldy, y_type == TG_BF16,
+                           static_cast<uint16_t *>(U), ldu, offsets, scales, groups, S, N, K, R, opt,
+                           reinterpret_cast<cudaStream_t>(stream));
+    });
+}

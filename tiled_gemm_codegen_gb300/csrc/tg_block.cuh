@@ -1,0 +1,995 @@
+// Persistent, warp-specialised products of a transformer block's projections
+// for sm_103a: a product over ragged (grouped) or dense rows whose epilogue, or
+// whose contraction, holds what usually takes more passes.  With s a row, g
+// its group, f a feature:
+//
+//   GATED   z = X[s] W_g (gate features, then as many up features),
+//           H[s][f] = act(z[f]) * z[F + f]; z is stored (bf16) where the
+//           backward pass wants it, and never read back here.
+//   GRAD    dh = dY[s] V_g stays in registers:
+//           dZ[s][f] = dh[f] * up * act'(gate), dZ[s][F + f] = dh[f] * act(gate),
+//           H[s][f] = act(gate) * up again for the next product's gradient.
+//   SHRINK  u = scale_g X[s] A_g^T (R values a row), in the layout that ADAPT's
+//           contraction reads (below), and plainly.
+//   ADAPT   Y[s] = X[s] W + u[s] B_g: the adapters' part is further k-blocks of
+//           the shared projection's contraction, so it costs no pass over Y.
+//
+// The tile is computed transposed as in grouped_kernel (tg_grouped.cuh), whose
+// roles, rings, bounded waits and shares of few tiles these are: features on
+// the MMA's M, rows on its N.
+//
+// GATED: of a CTA's 128 accumulator lanes the first 64 are gate features and
+// the last 64 the up features of the same index: one box of each half of W a
+// k-block, no re-arranged weights, and the full MMA shape.  A warp reads only
+// its own 32 lanes of tensor memory, so the warps of a gate quadrant and
+// an up quadrant exchange half of their 32 x 32 values through shared memory
+// (16 bytes a lane, no bank conflicts) and each computes 16 rows.
+//
+// ADAPT: rows of several adapters share a tile (decoding: a row or two each).
+// For a row tile with c adapters the contraction is extended by blocks of 64 k
+// in which every adapter has columns of its own; a row's u stands in its
+// adapter's columns and zeros in the others'.  u is fp32 and meets bf16 B, so
+// it goes in as two bf16 parts, hi + lo (17 bits or more): columns [hi | lo] of Rp = R
+// rounded up to 8, 16 or 32 each, both against the same rows of B (32 / Rp
+// adapters a block), or for R > 32 blocks of 64 of hi, then of lo.  The zeros
+// of other adapters' rows must not meet an infinity or NaN in B (0 x NaN is
+// NaN): B_g that hold one are flagged by the table kernel, go in as zeros and
+// are added by the epilogue, row by row of their own.
+#pragma once
+
+#include "tg_block.h"
+#include "tg_kernel.cuh"
+#include "tg_sync.cuh"
+
+namespace tg {
+
+struct BlockUnit {
+    int32_t g, row0, row1, tm, tn;
+    int32_t k_blocks;      // of the tile
+    int32_t kb0, kb1;      // this worker's of them
+    int32_t part, nparts, tile;
+};
+
+// A warp's walk through the tiles (or shares of tiles): grouped_kernel's, for
+// one group (no bounds to read) or many, 32 groups at a time with a lane each.
+struct BlockWalk {
+    int32_t base, lo, hi, incl, before, total, last;
+};
+
+template <int BN>
+__device__ __forceinline__ void block_walk_load(const BlockParams &p, int32_t base, BlockWalk &w)
+{
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const int32_t g = base + lane;
+    int32_t hi = 0;
+    if (g < p.groups) hi = p.offsets ? max(0, min(__ldg(p.offsets + g + 1), p.S)) : p.S;
+    hi = max(hi, w.last);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xffffffffu, hi, d);
+        if (lane >= d) hi = max(hi, o);
+    }
+    int32_t lo = __shfl_up_sync(0xffffffffu, hi, 1);
+    if (lane == 0) lo = w.last;
+    int32_t incl = g < p.groups ? (hi - lo + BN - 1) / BN * p.tiles_n * p.splits : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    w.base = base;
+    w.lo = lo;
+    w.hi = hi;
+    w.incl = incl;
+    w.total = __shfl_sync(0xffffffffu, incl, 31);
+    w.last = __shfl_sync(0xffffffffu, hi, 31);
+}
+
+template <int BN>
+__device__ __forceinline__ void block_walk_begin(const BlockParams &p, BlockWalk &w)
+{
+    w.before = 0;
+    w.last = p.offsets ? max(0, min(__ldg(p.offsets), p.S)) : 0;
+    block_walk_load<BN>(p, 0, w);
+}
+
+// Item t of the list, where t never falls from call to call; false past the
+// end.  A group's first shares of all its tiles come first: they read the same
+// rows.
+template <int MODE, int BN>
+__device__ __forceinline__ bool block_walk_to(const BlockParams &p, int64_t t64, BlockWalk &w, BlockUnit &u)
+{
+    if (t64 > INT32_MAX) return false;
+    const int32_t t = static_cast<int32_t>(t64);
+    while (t >= w.before + w.total) {
+        if (w.base + 32 >= p.groups) return false;
+        w.before += w.total;
+        block_walk_load<BN>(p, w.base + 32, w);
+    }
+    const int32_t at = t - w.before;
+    const int idx = __popc(__ballot_sync(0xffffffffu, at >= w.incl));
+    u.g = w.base + idx;
+    u.row0 = __shfl_sync(0xffffffffu, w.lo, idx);
+    u.row1 = __shfl_sync(0xffffffffu, w.hi, idx);
+    int32_t before = __shfl_sync(0xffffffffu, w.incl, idx > 0 ? idx - 1 : 0);
+    if (idx == 0) before = 0;
+    int32_t r = at - before;
+    const int32_t tiles_m = (u.row1 - u.row0 + BN - 1) / BN;
+    const int32_t per = tiles_m * p.tiles_n;
+    u.nparts = p.splits;
+    u.part = r / per;
+    r -= u.part * per;
+    u.tile = (w.before + before) / p.splits + r;
+    const int32_t strip = p.group_m * p.tiles_n;
+    const int32_t first = r / strip * p.group_m;
+    const int32_t in = r % strip, rows = min(tiles_m - first, p.group_m);
+    u.tm = first + in % rows;
+    u.tn = in / rows;
+    u.k_blocks = p.k_blocks;
+    if (MODE == BLOCK_ADAPT) u.k_blocks += __ldcg(p.tab.blocks + u.tm + 1) - __ldcg(p.tab.blocks + u.tm);
+    u.kb0 = static_cast<int32_t>(static_cast<int64_t>(u.part) * u.k_blocks / u.nparts);
+    u.kb1 = static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * u.k_blocks / u.nparts);
+    return true;
+}
+
+// The MMA's N for a tile: its rows rounded up to 32 (16 a CTA of a pair).
+template <int BN>
+__device__ __forceinline__ int32_t block_rows_n(const BlockUnit &u)
+{
+    return min(BN, (u.row1 - u.row0 - u.tm * BN + 31) / 32 * 32);
+}
+
+// act(g) and its slope.
+template <int ACT>
+__device__ __forceinline__ void act_slope(float g, float &a, float &d)
+{
+    if (ACT == 1) {
+        a = fmaxf(g, 0.0f);
+        d = g > 0.0f ? 1.0f : 0.0f;
+    } else if (ACT == 2) {  // gelu, tanh form
+        const float c = 0.7978845608028654f, g2 = g * g;
+        const float t = tanhf(c * (g + 0.044715f * g2 * g));
+        a = 0.5f * g * (1.0f + t);
+        d = 0.5f * (1.0f + t) + 0.5f * g * (1.0f - t * t) * c * (1.0f + 3.0f * 0.044715f * g2);
+    } else if (ACT == 3) {  // silu
+        const float s = 1.0f / (1.0f + expf(-g));
+        a = g * s;
+        d = s * (1.0f + g * (1.0f - s));
+    } else {
+        a = g;
+        d = 1.0f;
+    }
+}
+
+// 16 of act(gate) * up.  One unrolled loop an activation behind one branch.
+template <int ACT>
+__device__ __forceinline__ void gated16(const uint32_t (&g)[16], const uint32_t (&u)[16], uint32_t (&h)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        h[j] = __float_as_uint(activation(__uint_as_float(g[j]), ACT) * __uint_as_float(u[j]));
+}
+
+// GRAD's 32 rows: dh and z (gate in the low half) -> dZ's two halves, packed
+// the same way, and H.
+template <int ACT>
+__device__ __forceinline__ void gated_grad32(const uint32_t (&dh)[32], const uint32_t (&z)[32], uint32_t (&dz)[32], uint32_t (&h)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        float hv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float g = __uint_as_float(z[j + e] << 16), u = __uint_as_float(z[j + e] & 0xffff0000u);
+            const float d = __uint_as_float(dh[j + e]);
+            float a, slope;
+            act_slope<ACT>(g, a, slope);
+            dz[j + e] = pack_bf16x2(__float_as_uint(d * u * slope), __float_as_uint(d * a));
+            hv[e] = a * u;
+        }
+        h[j / 2] = pack_bf16x2(__float_as_uint(hv[0]), __float_as_uint(hv[1]));
+    }
+}
+
+template <int MODE, int BN, int STAGES, bool PAIR>
+__global__ void __launch_bounds__(BLOCK_THREADS, 1)
+    block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                 const __grid_constant__ CUtensorMap tmV,  // GATED: the up half of W; ADAPT: B
+                 const __grid_constant__ CUtensorMap tmE,  // ADAPT: u's parts
+                 const __grid_constant__ CUtensorMap tmO,  // H, Y
+                 const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU,  // halves of Z, dZ
+                 const BlockParams p)
+{
+    using G = Geometry<BN, PAIR>;
+    constexpr int LANES = MODE == BLOCK_GATED ? BM / 2 : BM;  // features a CTA's accumulator holds
+    constexpr int TILE_F = PAIR ? 2 * LANES : LANES;
+    constexpr uint32_t BOX_BYTES = BK * 64 * 2;               // 64 k x 64 features, 8 KB
+    constexpr uint32_t EPI_BOX_BYTES = 4096;                  // 32 rows of 128 bytes
+    constexpr uint32_t EPI_WARPS_TOTAL = (PAIR ? 2 : 1) * BLOCK_EPI_WARPS;
+    constexpr int EPI_ROWS = 32, EPI_ROW_BYTES = 128;
+    static_assert(BLOCK_EPI_WARPS * EPI_BOX_BYTES <= G::EPI_BYTES, "epilogue boxes");
+    static_assert(MODE != BLOCK_SHRINK || !PAIR, "adapters' first products take one-CTA tiles");
+    constexpr uint32_t TMEM_ALLOC = static_cast<uint32_t>(G::TMEM_COLS);
+    static_assert(8 * (2 * STAGES + 6) + 20 <= G::BAR_BYTES, "barrier area");
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sA = raw + pad;
+    const uint32_t sB = sA + STAGES * G::A_STAGE;
+    const uint32_t sE = sB + STAGES * G::B_STAGE;
+    uint8_t *bar_area = smem + STAGES * G::STAGE + G::EPI_BYTES;
+    const uint32_t bar0 = ptx::smem_addr(bar_area);
+    // barrier k at bar0 + 8k: [0, S) full, [S, 2S) empty, 2S+{0,1} tfull,
+    // 2S+{2,3} tempty, 2S+4 mma-done, 2S+5 never completed
+    const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
+    const uint32_t stall_bar = bar0 + 8u * (2 * STAGES + 5);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (2 * STAGES + 6));
+    volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
+    volatile int32_t *last_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 2);
+    uint32_t *issued_slot = tmem_slot + 3;  // k-blocks this CTA's producer loaded
+    auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
+    auto tfull_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
+    auto tempty_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
+
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int64_t worker = PAIR ? (blockIdx.x >> 1) : blockIdx.x;
+    const int64_t n_workers = PAIR ? (gridDim.x >> 1) : gridDim.x;
+
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        for (uint32_t b = 0; b < 2; ++b) {
+            ptx::mbar_init(tfull_bar(b), 1);
+            ptx::mbar_init(tempty_bar(b), EPI_WARPS_TOTAL);
+        }
+        ptx::mbar_init(done_bar, 1);
+        ptx::mbar_init(stall_bar, 1);
+        *abort_flag = 0;
+        *issued_slot = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        if (p.k_blocks > 0) {
+            ptx::prefetch_tensormap(&tmX);
+            ptx::prefetch_tensormap(&tmW);
+            if (MODE == BLOCK_GATED) ptx::prefetch_tensormap(&tmV);
+        }
+        if (MODE == BLOCK_ADAPT) {
+            ptx::prefetch_tensormap(&tmV);
+            ptx::prefetch_tensormap(&tmE);
+        }
+        if (MODE != BLOCK_SHRINK && p.out0.tma) ptx::prefetch_tensormap(&tmO);
+    }
+    if (warp == 1) {
+        if constexpr (PAIR) {
+            ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), TMEM_ALLOC);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_addr(tmem_slot), TMEM_ALLOC);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) ptx::cluster_sync_all();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    ptx::griddep_wait();
+    const uint32_t peer_abort =
+        PAIR ? ptx::map_to_cta(ptx::smem_addr(const_cast<int32_t *>(abort_flag)), rank ^ 1u) : 0u;
+    const Watchdog wd{p.timeout_ns, abort_flag, p.err, peer_abort};
+
+    BlockWalk walk;
+    BlockUnit w;
+    block_walk_begin<BN>(p, walk);
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        uint32_t it = 0;
+        bool ok = true;
+        const uint32_t full0 = PAIR ? ptx::map_to_cta(full_bar(0), 0u) : full_bar(0);
+        for (int64_t t = worker; ok && block_walk_to<MODE, BN>(p, t, walk, w); t += n_workers) {
+            if (!dbg_ok(w.g >= 0 && w.g < p.groups && w.row0 >= 0 && w.row0 <= w.row1 && w.row1 <= p.S && w.tm >= 0 &&
+                            w.tn >= 0 && w.tn < p.tiles_n,
+                        CHK_UNIT, wd))
+                break;
+            const int32_t m0 = w.tn * TILE_F + static_cast<int32_t>(rank) * LANES;
+            const int32_t n_half = static_cast<int32_t>(rank) * (block_rows_n<BN>(w) / 2);
+            const int32_t n0 = w.row0 + w.tm * BN + n_half;
+            // ADAPT: lane l holds the tile's adapter ad0 + l (-1: none, or flagged)
+            int32_t ad0 = 0, ad = -1, ad_first = 0, ad_count = 0, ext_row = 0;
+            auto adapters = [&](int32_t from) {
+                ad0 = from;
+                ad = -1;
+                if (from + lane < ad_count) {
+                    ad = __ldcg(p.tab.ids + ad_first + from + lane);
+                    int32_t bad = 0;
+                    for (int i = 0; i < ADAPT_FLAGS; ++i) bad |= __ldcg(p.tab.flags + ad * ADAPT_FLAGS + i);
+                    if (bad) ad = -1;
+                }
+            };
+            if (MODE == BLOCK_ADAPT && w.kb1 > p.k_blocks) {
+                ad_first = __ldcg(p.tab.first + w.tm);
+                ad_count = __ldcg(p.tab.count + w.tm);
+                ext_row = __ldcg(p.tab.blocks + w.tm) * BN + n_half;
+            }
+            for (int32_t kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                const uint32_t s = it % STAGES;
+                const uint32_t ph = (it / STAGES) & 1u;
+                const int r = wait_bounded_warp(empty_bar(s), ph ^ 1u, wd);
+                if (r != WAIT_OK) {
+                    if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_PRODUCER);
+                    ok = false;
+                    break;
+                }
+                const uint32_t a_dst = sA + s * G::A_STAGE;
+                const uint32_t b_dst = sB + s * G::B_STAGE;
+                const uint32_t fb = PAIR ? full0 + 8u * s : full_bar(s);
+                auto load = [&](uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2) {
+                    if constexpr (PAIR)
+                        ptx::tma_load_3d_pair(dst, map, fb, c0, c1, c2);
+                    else
+                        ptx::tma_load_3d(dst, map, fb, c0, c1, c2);
+                };
+                auto expect = [&]() {
+                    if constexpr (PAIR) {
+                        if (leader) ptx::mbar_arrive_expect_tx(full_bar(s), 2 * G::STAGE);
+                    } else {
+                        ptx::mbar_arrive_expect_tx(full_bar(s), G::STAGE);
+                    }
+                };
+                if (MODE == BLOCK_ADAPT && kb >= p.k_blocks) {
+                    const int32_t e = kb - p.k_blocks;
+                    // the block's first adapter, and for R > 32 the rows of B
+                    const int32_t per = p.Rp <= 32 ? 32 / p.Rp : 1;
+                    const int32_t bpa = p.Rp <= 32 ? 1 : p.Rp / 32;
+                    const int32_t a0 = p.Rp <= 32 ? e * per : e / bpa;
+                    const int32_t chunk = p.Rp <= 32 ? 0 : (e % bpa) / 2 * 64;
+                    if (kb == w.kb0 || kb == p.k_blocks || a0 + per > ad0 + 32) adapters(a0);
+                    int32_t ids[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ids[i] = __shfl_sync(0xffffffffu, ad, min(31, a0 - ad0 + i));
+                    if (ptx::elect_one()) {
+                        expect();
+                        const int32_t rows = min(p.Rp, 64);
+                        const int32_t subs = 64 / rows;
+                        for (int i = 0; i < subs; ++i) {
+                            const int k = p.Rp <= 32 ? i >> 1 : 0;
+                            int32_t id = ids[0];
+                            if (k == 1) id = ids[1];
+                            if (k == 2) id = ids[2];
+                            if (k == 3) id = ids[3];
+                            // rows past R read as zeros
+                            const int32_t r0 = id < 0 ? p.Rp : chunk, z = p.b_shared ? 0 : max(id, 0);
+                            const uint32_t dst = a_dst + static_cast<uint32_t>(i * rows) * 128u;
+                            load(dst, &tmV, m0, r0, z);
+                            load(dst + BOX_BYTES, &tmV, m0 + 64, r0, z);
+                        }
+                        load(b_dst, &tmE, 0, ext_row + e * BN, 0);
+                    }
+                } else if (ptx::elect_one()) {
+                    expect();
+                    const int32_t z = p.w_shared ? 0 : w.g;
+                    if constexpr (MODE == BLOCK_GATED) {
+                        if (!p.w_k) {
+                            load(a_dst, &tmW, m0, kb * BK, z);
+                            load(a_dst + BOX_BYTES, &tmV, m0, kb * BK, z);
+                        } else {
+                            load(a_dst, &tmW, kb * BK, m0, z);
+                            load(a_dst + BOX_BYTES, &tmV, kb * BK, m0, z);
+                        }
+                    } else if (!p.w_k) {  // W[g] is K x N: 64 k x 64 features, twice
+                        load(a_dst, &tmW, m0, kb * BK, z);
+                        load(a_dst + BOX_BYTES, &tmW, m0 + 64, kb * BK, z);
+                    } else {  // stored N x K: 128 features x 64 k
+                        load(a_dst, &tmW, kb * BK, m0, z);
+                    }
+                    load(b_dst, &tmX, kb * BK, n0, 0);
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0) {
+            *issued_slot = it;
+            if constexpr (!PAIR) {
+                const uint32_t first = it > STAGES ? it - STAGES : 0u;
+                for (uint32_t j = first; j < it; ++j)
+                    if (!wait_drain(full_bar(j % STAGES), (j / STAGES) & 1u, wd)) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (!PAIR || leader) {
+            // ------------------------------------------------ MMA issuer
+            // the weights' features are contiguous (k-major otherwise); u's partner B always so
+            constexpr int TILE_M = PAIR ? 2 * BM : BM;
+            const uint32_t idesc_mn = instr_desc_bf16<TILE_M, BN>(true, false);
+            const uint32_t idesc_k = instr_desc_bf16<TILE_M, BN>(false, false);
+            const uint64_t desc_mn = smem_desc_sw128(0, BK * 128, 1024);
+            const uint64_t desc_k = smem_desc_sw128(0, 16, 1024);
+            uint32_t it = 0, n = 0;
+            bool ok = true;
+            for (int64_t t = worker; ok && block_walk_to<MODE, BN>(p, t, walk, w); t += n_workers) {
+                if (w.kb0 == w.kb1) continue;  // the epilogue writes an empty sum itself
+                const uint32_t buf = n & 1u;
+                const uint32_t tph = (n >> 1) & 1u;
+                ++n;
+                int r = wait_bounded_warp(tempty_bar(buf), tph ^ 1u, wd);
+                if (r != WAIT_OK) {
+                    if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_MMA);
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d_tmem = tmem_base + buf * BN;
+                const uint32_t n_field = static_cast<uint32_t>(block_rows_n<BN>(w)) >> 3 << 17;
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    const uint32_t s = it % STAGES;
+                    const uint32_t ph = (it / STAGES) & 1u;
+                    r = wait_bounded_warp(full_bar(s), ph, wd);
+                    if (r != WAIT_OK) {
+                        if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_MMA);
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    if (ptx::elect_one()) {
+                        const bool mn = !p.w_k || (MODE == BLOCK_ADAPT && kb >= p.k_blocks);
+                        const uint32_t idesc = ((mn ? idesc_mn : idesc_k) & ~(0x3Fu << 17)) | n_field;
+                        const uint64_t a_desc0 = mn ? desc_mn : desc_k;
+                        const uint32_t a_step = mn ? 2048u : 32u;
+                        const uint32_t a_addr = sA + s * G::A_STAGE;
+                        const uint32_t b_addr = sB + s * G::B_STAGE;
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk) {
+                            const uint64_t ad = a_desc0 | (((a_addr + kk * a_step) >> 4) & 0x3FFFu);
+                            const uint64_t bd = desc_k | (((b_addr + kk * 32u) >> 4) & 0x3FFFu);
+                            const uint32_t acc = (kb > w.kb0 || kk > 0) ? 1u : 0u;
+                            if constexpr (PAIR)
+                                ptx::mma_bf16_pair(d_tmem, ad, bd, idesc, acc);
+                            else
+                                ptx::mma_bf16(d_tmem, ad, bd, idesc, acc);
+                        }
+                        if constexpr (PAIR)
+                            ptx::mma_commit_pair_multicast(empty_bar(s), 0x3);
+                        else
+                            ptx::mma_commit(empty_bar(s));
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (ptx::elect_one()) {
+                    if constexpr (PAIR)
+                        ptx::mma_commit_pair_multicast(tfull_bar(buf), 0x3);
+                    else
+                        ptx::mma_commit(tfull_bar(buf));
+                }
+                __syncwarp();
+            }
+            if (ptx::elect_one()) {
+                if constexpr (PAIR)
+                    ptx::mma_commit_pair_multicast(done_bar, 0x1);
+                else
+                    ptx::mma_commit(done_bar);
+                wait_drain(done_bar, 0, wd);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------ epilogue
+        const int q = warp & 3;             // tensor-memory lane quadrant of this warp
+        const int turn = (warp - 2) >> 2;   // which of the quadrant's two warps
+        const uint32_t tempty_leader0 = PAIR ? ptx::map_to_cta(tempty_bar(0), 0u) : tempty_bar(0);
+
+        // Warps that fill and flush boxes together: GATED the four of a turn,
+        // GRAD and a bf16 Y two neighbouring quadrants (64 features are the 128
+        // bytes of a box row), an fp32 Y one warp.
+        const int team = MODE == BLOCK_GATED ? 4 : MODE == BLOCK_GRAD || p.out_bf16 ? 2 : 1;
+        const int sub = q & 1;              // which half of a box row is this warp's
+        const int member = MODE == BLOCK_GATED ? q : team == 2 ? sub : 0;
+        const uint32_t team_id = 2u + (MODE == BLOCK_GATED ? turn : (warp - 2) >> 1);
+        auto team_sync = [&]() {
+            if (team == 1)
+                __syncwarp();
+            else
+                ptx::named_barrier_sync(team_id, 32 * team);
+        };
+        const bool issues = member == 0 && lane == 0;  // all the team's bulk stores
+        const uint32_t area = sE + (MODE == BLOCK_GATED ? static_cast<uint32_t>(turn) * 4u * EPI_BOX_BYTES
+                                    : team == 2         ? static_cast<uint32_t>((warp - 2) >> 1) * 2u * EPI_BOX_BYTES
+                                                        : static_cast<uint32_t>(warp - 2) * EPI_BOX_BYTES);
+        // Address of 16-byte unit u of row r of the box at `box`.
+        auto unit_at = [&](uint32_t box, int r, int u) { return box + r * EPI_ROW_BYTES + ((u ^ (r & 7)) << 4); };
+        // This lane's bf16 of 32 rows of a box (r: first row).
+        auto put16 = [&](uint32_t box, int r, uint16_t v) {
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(unit_at(box, r, sub * 4 + (lane >> 3)) + (lane & 7) * 2), "h"(v) : "memory");
+        };
+        auto bf16_bits = [](uint32_t v) { return __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v))); };
+
+        // The box -> rows row0 .. of an output (those before `limit`), columns
+        // col0 ..  `whole`: a TMA store may write all of its rows (the tensor's
+        // own end clips a box, a group's end does not).  Called by the team
+        // between team_syncs; true where a bulk store was issued.
+        auto flush = [&](uint32_t box, const CUtensorMap *map, const BlockOut &o, int size, int32_t row0, int32_t limit, bool whole,
+                         int32_t col0) {
+            const int32_t cols = min(EPI_ROW_BYTES / size, p.N - col0);
+            if (cols <= 0) return;
+            const bool full = cols == EPI_ROW_BYTES / size || p.N % (16 / size) == 0;
+            if (o.tma && whole && full) {
+                if (issues) ptx::tma_store_3d(map, box, col0, row0, 0);
+                return;
+            }
+            const int32_t nrows = min(EPI_ROWS, limit - row0);
+            uint8_t *dst = static_cast<uint8_t *>(o.p) + (static_cast<int64_t>(row0) * o.ld + col0) * size;
+            const int64_t pitch = o.ld * size;
+            if (o.tma) {  // rows on 16 bytes
+                const int per = 16 / size, u = lane & 7, n = min(per, cols - u * per);
+                for (int r = member * 4 + (lane >> 3); r < nrows; r += 4 * team) {
+                    uint32_t v[4];
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                 : "r"(unit_at(box, r, u))
+                                 : "memory");
+                    uint8_t *d = dst + r * pitch + u * 16;
+                    if (n == per) {
+                        *reinterpret_cast<uint4 *>(d) = make_uint4(v[0], v[1], v[2], v[3]);
+                    } else if (size == 2) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (e < n) reinterpret_cast<uint16_t *>(d)[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (e < n) reinterpret_cast<uint32_t *>(d)[e] = v[e];
+                    }
+                }
+            } else {  // an element a lane
+                for (int c = lane; c < cols; c += 32) {
+                    const int u = c * size >> 4, in = c * size & 15;
+                    uint8_t *d = dst + c * size + member * pitch;
+#pragma unroll 4
+                    for (int r = member; r < nrows; r += team, d += team * pitch) {
+                        if (size == 2)
+                            *reinterpret_cast<uint16_t *>(d) = ld_shared_u16(unit_at(box, r, u) + in);
+                        else
+                            *reinterpret_cast<float *>(d) = ld_shared_f32(unit_at(box, r, u) + in);
+                    }
+                }
+            }
+        };
+        auto release_tmem = [&](uint32_t buf) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR)
+                    ptx::mbar_arrive_cluster(tempty_leader0 + 8u * buf);
+                else
+                    ptx::mbar_arrive(tempty_bar(buf));
+            }
+        };
+
+        bool ok = true;
+        if (p.debug_stall) {  // watchdog self-test: a barrier that nothing completes
+            const int r = wait_bounded(stall_bar, 0, wd);
+            if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
+            ok = agree(r == WAIT_OK, 1, 32 * BLOCK_EPI_WARPS);
+        }
+        uint32_t n = 0;
+        uint32_t flip = 0;  // which of two boxes is next
+        for (int64_t t = worker; ok && block_walk_to<MODE, BN>(p, t, walk, w); t += n_workers) {
+            const int32_t f0 = w.tn * TILE_F + static_cast<int32_t>(rank) * LANES;  // the CTA's first feature
+            const int32_t f_warp = f0 + 32 * (MODE == BLOCK_GATED ? sub : q);       // the warp's
+            const int32_t f_box = MODE == BLOCK_GATED ? f0 : team == 2 ? f_warp - 32 * sub : f_warp;
+            const int32_t row_tile = w.row0 + w.tm * BN;
+            const int32_t limit = min(w.row1, row_tile + BN);
+            const int32_t pieces = (limit - row_tile + 31) / 32;
+            const bool lanes_in = MODE == BLOCK_SHRINK ? f_warp < p.Rp : f_box < p.N;  // uniform in a team
+
+            // GRAD: 32 rows of z, gate in the low half; rows and features past
+            // the end read the last one's.
+            uint32_t z[32];
+            auto load_z = [&](int c) {
+                if constexpr (MODE == BLOCK_GRAD) {
+                    const uint16_t *at = p.z + min(f_warp + lane, p.N - 1);
+                    const int32_t r0 = row_tile + 32 * c;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const uint16_t *row = at + static_cast<int64_t>(min(r0 + j, limit - 1)) * p.ldz;
+                        z[j] = static_cast<uint32_t>(row[0]) | static_cast<uint32_t>(row[p.N]) << 16;
+                    }
+                }
+            };
+
+            // 32 rows of the accumulator (v: row j of this lane's feature) ->
+            // the outputs.  `next` is called once v is used up.
+            auto piece = [&](int c, uint32_t (&v)[32], auto &&next) {
+                const int32_t row0 = row_tile + 32 * c;
+                [[maybe_unused]] const bool whole = row0 + EPI_ROWS <= limit || limit == p.S;
+                if constexpr (MODE == BLOCK_GATED) {
+                    const uint32_t zbox = area;  // gate half, up half; also the exchange
+                    const uint32_t hbox = area + (2u + flip) * EPI_BOX_BYTES;
+                    flip ^= 1u;
+                    // the boxes' last stores have read them (H's of the piece before may run on)
+                    if (issues) {
+                        if (p.gate.p)
+                            ptx::bulk_wait_group_read<0>();
+                        else
+                            ptx::bulk_wait_group_read<1>();
+                    }
+                    team_sync();
+                    const bool is_up = q >= 2;  // computes rows 16 .. 31, else 0 .. 15
+                    const uint32_t give = area + static_cast<uint32_t>(q) * 2048u + lane * 16u;
+                    const uint32_t take = area + static_cast<uint32_t>(q ^ 2) * 2048u + lane * 16u;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (is_up)
+                            ptx::st_shared_v4(give + k * 512u, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        else
+                            ptx::st_shared_v4(give + k * 512u, v[16 + 4 * k], v[17 + 4 * k], v[18 + 4 * k], v[19 + 4 * k]);
+                    }
+                    team_sync();
+                    uint32_t o[16], mine[16], h[16];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(o[4 * k]), "=r"(o[4 * k + 1]), "=r"(o[4 * k + 2]), "=r"(o[4 * k + 3])
+                                     : "r"(take + k * 512u)
+                                     : "memory");
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) mine[j] = is_up ? v[16 + j] : v[j];
+                    if (p.gate.p) {
+                        team_sync();  // the exchange was read
+                        const uint32_t box = zbox + (is_up ? EPI_BOX_BYTES : 0u);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) put16(box, j, bf16_bits(v[j]));
+                    }
+                    next();
+                    uint32_t g[16], u[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        g[j] = is_up ? o[j] : mine[j];
+                        u[j] = is_up ? mine[j] : o[j];
+                    }
+                    switch (p.act) {
+                        case 1: gated16<1>(g, u, h); break;
+                        case 2: gated16<2>(g, u, h); break;
+                        case 3: gated16<3>(g, u, h); break;
+                        default: gated16<0>(g, u, h); break;
+                    }
+                    const int j0 = is_up ? 16 : 0;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) put16(hbox, j0 + j, bf16_bits(h[j]));
+                    ptx::fence_proxy_async_smem();
+                    team_sync();
+                    flush(hbox, &tmO, p.out0, 2, row0, limit, whole, f_box);
+                    if (p.gate.p) {
+                        flush(zbox, &tmG, p.gate, 2, row0, limit, whole, f_box);
+                        flush(zbox + EPI_BOX_BYTES, &tmU, p.up, 2, row0, limit, whole, f_box);
+                    }
+                    // one group a piece, empty where nothing was issued
+                    if (issues) ptx::bulk_commit_group();
+                } else if constexpr (MODE == BLOCK_GRAD) {
+                    uint32_t dz[32], h[16];
+                    switch (p.act) {
+                        case 1: gated_grad32<1>(v, z, dz, h); break;
+                        case 2: gated_grad32<2>(v, z, dz, h); break;
+                        case 3: gated_grad32<3>(v, z, dz, h); break;
+                        default: gated_grad32<0>(v, z, dz, h); break;
+                    }
+                    next();
+                    auto send = [&](const CUtensorMap *map, const BlockOut &out, auto &&value) {
+                        const uint32_t box = area + flip * EPI_BOX_BYTES;
+                        flip ^= 1u;
+                        if (issues) ptx::bulk_wait_group_read<1>();
+                        team_sync();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) put16(box, j, value(j));
+                        ptx::fence_proxy_async_smem();
+                        team_sync();
+                        flush(box, map, out, 2, row0, limit, whole, f_box);
+                        if (issues) ptx::bulk_commit_group();
+                    };
+                    send(&tmG, p.gate, [&](int j) { return static_cast<uint16_t>(dz[j]); });
+                    send(&tmU, p.up, [&](int j) { return static_cast<uint16_t>(dz[j] >> 16); });
+                    if (p.out0.p) send(&tmO, p.out0, [&](int j) { return static_cast<uint16_t>(h[j >> 1] >> (16 * (j & 1))); });
+                } else if constexpr (MODE == BLOCK_ADAPT) {
+                    const uint32_t box = area + (team == 2 ? flip * EPI_BOX_BYTES : 0u);
+                    flip ^= 1u;
+                    if (issues) {
+                        if (team == 2)
+                            ptx::bulk_wait_group_read<1>();
+                        else
+                            ptx::bulk_wait_group_read<0>();
+                    }
+                    team_sync();
+                    if (team == 2) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) put16(box, j, bf16_bits(v[j]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(unit_at(box, j, lane >> 2) + (lane & 3) * 4), "r"(v[j]) : "memory");
+                    }
+                    next();
+                    ptx::fence_proxy_async_smem();
+                    team_sync();
+                    flush(box, &tmO, p.out0, p.out_bf16 ? 2 : 4, row0, limit, whole, f_box);
+                    if (issues) ptx::bulk_commit_group();
+                } else {  // SHRINK
+                    const float scale = p.scales ? __ldg(p.scales + w.g) : 1.0f;
+                    const int32_t r = f_warp + lane;
+                    const int32_t place = __ldcg(p.tab.rank + w.g);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int32_t row = row0 + j;
+                        if (row >= limit || r >= p.Rp) continue;
+                        // (columns past R meet zeros, whatever X holds)
+                        const float x = r < p.R ? __fmul_rn(scale, __uint_as_float(v[j])) : 0.0f;
+                        const __nv_bfloat16 rounded = __float2bfloat16_rn(x);
+                        // u = hi + lo; hi rounds down where rounding would make an infinity
+                        __nv_bfloat16 hi = rounded;
+                        if (fabsf(x) <= 3.402823466e38f && fabsf(__bfloat162float(hi)) > 3.402823466e38f)
+                            hi = __ushort_as_bfloat16(static_cast<uint16_t>(__float_as_uint(x) >> 16));
+                        const __nv_bfloat16 lo = fabsf(x) <= 3.402823466e38f
+                                                     ? __float2bfloat16_rn(__fsub_rn(x, __bfloat162float(hi)))
+                                                     : __ushort_as_bfloat16(0);
+                        const int32_t tile = row / p.wide_bn, in = row % p.wide_bn;
+                        const int32_t i = place - __ldcg(p.tab.first + tile);
+                        const int32_t per = p.Rp <= 32 ? 32 / p.Rp : 1;
+                        const int64_t blk = __ldcg(p.tab.blocks + tile) + (p.Rp <= 32 ? i / per : i * (p.Rp / 32) + r / 64 * 2);
+                        uint16_t *at = p.wide + (blk * p.wide_bn + in) * 64 + (p.Rp <= 32 ? i % per * 2 * p.Rp + r : r & 63);
+                        at[0] = __bfloat16_as_ushort(hi);
+                        at[p.Rp <= 32 ? p.Rp : static_cast<int64_t>(p.wide_bn) * 64] = __bfloat16_as_ushort(lo);
+                        if (p.out0.p && r < p.R)
+                            static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = __bfloat16_as_ushort(rounded);
+                    }
+                    next();
+                }
+            };
+            // SHRINK: zeros in the other adapters' columns of this tile's rows.
+            auto zero_others = [&]() {
+                if constexpr (MODE == BLOCK_SHRINK) {
+                    if (w.tn != 0) return;
+                    const int32_t place = __ldcg(p.tab.rank + w.g);
+                    for (int32_t row = row_tile + (warp - 2); row < limit; row += BLOCK_EPI_WARPS) {
+                        const int32_t tile = row / p.wide_bn, in = row % p.wide_bn;
+                        const int32_t blk0 = __ldcg(p.tab.blocks + tile), nb = __ldcg(p.tab.blocks + tile + 1) - blk0;
+                        const int32_t i = place - __ldcg(p.tab.first + tile);
+                        // its own 16-byte units of the tile's blocks: [own, own_end)
+                        const int32_t units = adapter_blocks(1, p.Rp) == 1 ? p.Rp / 4 : p.Rp / 32 * 8;
+                        const int32_t own = i * units, own_end = own + units;
+                        for (int32_t k = lane; k < nb * 8; k += 32)
+                            if (k < own || k >= own_end)
+                                *reinterpret_cast<uint4 *>(p.wide + (static_cast<int64_t>(blk0 + (k >> 3)) * p.wide_bn + in) * 64 + (k & 7) * 8) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+            };
+            // ADAPT: adds the adapters whose B holds an infinity or NaN to
+            // their own rows.
+            bool flagged = false;
+            if constexpr (MODE == BLOCK_ADAPT) {
+                const int32_t first = __ldcg(p.tab.first + w.tm), most = __ldcg(p.tab.count + w.tm);
+                int32_t bad = 0;
+                for (int32_t i = lane; i < most; i += 32) {
+                    const int32_t *flag = p.tab.flags + __ldcg(p.tab.ids + first + i) * ADAPT_FLAGS;
+#pragma unroll
+                    for (int k = 0; k < ADAPT_FLAGS; ++k) bad |= __ldcg(flag + k);
+                }
+                flagged = __any_sync(0xffffffffu, bad != 0);
+            }
+            auto add_flagged = [&](int c, uint32_t (&v)[32]) {
+                if constexpr (MODE == BLOCK_ADAPT) {
+                    if (!flagged) return;
+                    const int32_t first = __ldcg(p.tab.first + w.tm), most = __ldcg(p.tab.count + w.tm);
+                    const int32_t blk0 = __ldcg(p.tab.blocks + w.tm);
+                    const int32_t f = f_warp + lane;
+                    const int32_t r0 = row_tile + 32 * c;
+                    const int32_t per = p.Rp <= 32 ? 32 / p.Rp : 1;
+                    for (int32_t i = 0; i < most; ++i) {
+                        const int32_t id = __ldcg(p.tab.ids + first + i);
+                        const int32_t bad = lane < ADAPT_FLAGS ? __ldcg(p.tab.flags + id * ADAPT_FLAGS + lane) : 0;
+                        if (!__any_sync(0xffffffffu, bad != 0)) continue;
+                        const int32_t lo = max(__ldcg(p.tab.lo + first + i), r0), hi = min(__ldcg(p.tab.hi + first + i), min(limit, r0 + 32));
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int32_t row = r0 + j;
+                            if (row < lo || row >= hi) continue;
+                            float sum = 0.0f;
+#pragma unroll 1
+                            for (int32_t r = 0; f < p.N && r < p.R; ++r) {
+                                const int64_t blk = blk0 + (p.Rp <= 32 ? i / per : i * (p.Rp / 32) + r / 64 * 2);
+                                const uint16_t *at = p.wide + (blk * BN + (row - row_tile)) * 64 + (p.Rp <= 32 ? i % per * 2 * p.Rp + r : r & 63);
+                                const float u = __uint_as_float(static_cast<uint32_t>(at[0]) << 16) +
+                                                __uint_as_float(static_cast<uint32_t>(at[p.Rp <= 32 ? p.Rp : BN * 64]) << 16);
+                                const float bv = __uint_as_float(static_cast<uint32_t>(p.b[id * p.strideB + r * p.ldb + f]) << 16);
+                                sum = __fmaf_rn(u, bv, sum);
+                            }
+                            v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), sum));
+                        }
+                    }
+                }
+            };
+
+            uint32_t v[32];
+            if (w.k_blocks == 0) {  // the empty sum
+                for (int c = turn; lanes_in && c < pieces; c += 2) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0u;
+                    load_z(c);
+                    add_flagged(c, v);
+                    piece(c, v, [] {});
+                }
+                zero_others();
+                continue;
+            }
+            if (lanes_in && turn < pieces && w.nparts == 1) load_z(turn);
+            const uint32_t buf = n & 1u;
+            const uint32_t tph = (n >> 1) & 1u;
+            ++n;
+            // (the warps that meet at barriers below leave together)
+            const int r = wait_bounded(tfull_bar(buf), tph, wd);
+            if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
+            const bool here = r == WAIT_OK;
+            if (!(w.nparts > 1 ? agree(here, 1, 32 * BLOCK_EPI_WARPS)
+                  : team == 1  ? __all_sync(0xffffffffu, here) != 0
+                               : agree(here, team_id, 32 * team)))
+                break;
+            ptx::tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
+            if (w.nparts > 1) {
+                // The partial tile -> scratch [piece][column quad][lane][4
+                // columns]: 16 coalesced bytes a thread.
+                constexpr int64_t PART4 = BM * BN / 4;  // float4s a part
+                const int64_t half = static_cast<int64_t>(w.tile) * (PAIR ? 2 : 1) + rank;
+                float4 *parts = reinterpret_cast<float4 *>(p.partials) + half * p.splits * PART4 + q * 32 + lane;
+                float4 *mine = parts + w.part * PART4;
+                for (int c = turn; lanes_in && c < pieces; c += 2) {
+                    ptx::tmem_load_32cols(taddr + c * 32, v);
+#pragma unroll
+                    for (int j4 = 0; j4 < 8; ++j4)
+                        __stcg(mine + (c * 8 + j4) * BM, make_float4(__uint_as_float(v[4 * j4]), __uint_as_float(v[4 * j4 + 1]),
+                                                                     __uint_as_float(v[4 * j4 + 2]), __uint_as_float(v[4 * j4 + 3])));
+                }
+                release_tmem(buf);
+                __threadfence();
+                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
+                if (warp == 2 && lane == 0) {
+                    const int32_t old = atomicAdd(p.counters + half, 1);
+                    *last_flag = old == w.nparts - 1 ? 1 : 0;
+                    if (old == w.nparts - 1) atomicExch(p.counters + half, 0);  // ready for the next call
+                }
+                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
+                if (*last_flag) {
+                    __threadfence();
+                    for (int c = turn; lanes_in && c < pieces; c += 2) {
+                        load_z(c);
+                        float4 acc[8];
+#pragma unroll
+                        for (int j4 = 0; j4 < 8; ++j4) acc[j4] = __ldcg(parts + (c * 8 + j4) * BM);
+#pragma unroll 2
+                        for (int s = 1; s < w.nparts; ++s) {
+                            float4 t4[8];
+#pragma unroll
+                            for (int j4 = 0; j4 < 8; ++j4) t4[j4] = __ldcg(parts + s * PART4 + (c * 8 + j4) * BM);
+#pragma unroll
+                            for (int j4 = 0; j4 < 8; ++j4) {
+                                acc[j4].x += t4[j4].x; acc[j4].y += t4[j4].y;
+                                acc[j4].z += t4[j4].z; acc[j4].w += t4[j4].w;
+                            }
+                        }
+#pragma unroll
+                        for (int j4 = 0; j4 < 8; ++j4) {
+                            v[4 * j4] = __float_as_uint(acc[j4].x);
+                            v[4 * j4 + 1] = __float_as_uint(acc[j4].y);
+                            v[4 * j4 + 2] = __float_as_uint(acc[j4].z);
+                            v[4 * j4 + 3] = __float_as_uint(acc[j4].w);
+                        }
+                        add_flagged(c, v);
+                        piece(c, v, [] {});
+                    }
+                    zero_others();
+                }
+                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);  // the flag may be written again
+                continue;
+            }
+            // The next piece's loads are on their way while one is stored.
+            int c = turn;
+            if (lanes_in && c < pieces)
+                ptx::tmem_load_32cols_async(taddr + c * 32, v);
+            else
+                release_tmem(buf);
+            for (; lanes_in && c < pieces; c += 2) {
+                ptx::tmem_wait_ld(v);
+                add_flagged(c, v);
+                piece(c, v, [&] {
+                    if (c + 2 < pieces) {
+                        ptx::tmem_load_32cols_async(taddr + (c + 2) * 32, v);
+                        load_z(c + 2);
+                    } else {
+                        release_tmem(buf);
+                    }
+                });
+            }
+            zero_others();
+        }
+        // Rows of no group: zeros (SHRINK: of u and its parts).
+        if (p.offsets) {
+            const int32_t first = max(0, min(__ldg(p.offsets), p.S));
+            BlockWalk end = walk;
+            while (end.base + 32 < p.groups) {
+                end.before += end.total;
+                block_walk_load<BN>(p, end.base + 32, end);
+            }
+            const int64_t w0 = static_cast<int64_t>(blockIdx.x) * BLOCK_EPI_WARPS + (warp - 2);
+            const int64_t nw = static_cast<int64_t>(gridDim.x) * BLOCK_EPI_WARPS;
+            auto zero = [&](const BlockOut &o, int64_t row, int32_t cols) {
+                if (!o.p) return;
+                uint8_t *dst = static_cast<uint8_t *>(o.p) + row * o.ld * 2;
+                const int64_t bytes = static_cast<int64_t>(cols) * 2;
+                const bool vec = (reinterpret_cast<uintptr_t>(o.p) & 15u) == 0 && o.ld % 8 == 0;
+                const int64_t body = vec ? bytes / 16 * 16 : 0;
+                for (int64_t b = lane * 16; b < body; b += 512)
+                    *reinterpret_cast<uint4 *>(dst + b) = make_uint4(0u, 0u, 0u, 0u);
+                for (int64_t b = body + lane * 2; b < bytes; b += 64) *reinterpret_cast<uint16_t *>(dst + b) = 0;
+            };
+            for (int64_t i = w0; i < static_cast<int64_t>(first) + (p.S - end.last); i += nw) {
+                const int64_t row = i < first ? i : end.last + (i - first);
+                if constexpr (MODE == BLOCK_SHRINK) {
+                    zero(p.out0, row, p.R);
+                    const int32_t tile = static_cast<int32_t>(row / p.wide_bn), in = static_cast<int32_t>(row % p.wide_bn);
+                    const int32_t blk0 = __ldcg(p.tab.blocks + tile), nb = __ldcg(p.tab.blocks + tile + 1) - blk0;
+                    for (int32_t k = lane; k < nb * 8; k += 32)
+                        *reinterpret_cast<uint4 *>(p.wide + (static_cast<int64_t>(blk0 + (k >> 3)) * p.wide_bn + in) * 64 + (k & 7) * 8) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    zero(p.out0, row, p.N);
+                    zero(p.gate, row, p.N);
+                    zero(p.up, row, p.N);
+                }
+            }
+        }
+        if (lane == 0) ptx::bulk_wait_group_read<0>();
+        __syncwarp();
+    }
+
+    __syncthreads();
+    if constexpr (PAIR) {
+        // as gemm_kernel: neither CTA leaves while copies, MMAs or arrivals
+        // of the other may still reach it; an abort's unequal issue counts
+        // are settled first
+        ptx::cluster_sync_all();
+        if (leader && warp == 0 && lane == 0) {
+            const uint32_t i_l = *issued_slot;
+            const uint32_t i_p = ptx::ld_cluster_u32(ptx::map_to_cta(ptx::smem_addr(issued_slot), 1u));
+            const uint32_t hi = i_l > i_p ? i_l : i_p;
+            const uint32_t lo = hi > STAGES ? hi - STAGES : 0u;
+            for (uint32_t j = lo; j < hi; ++j) {
+                const uint32_t s = j % STAGES;
+                if (j < i_l && j >= i_p)
+                    ptx::mbar_complete_tx(full_bar(s), G::STAGE);
+                else if (j >= i_l && j < i_p)
+                    ptx::mbar_arrive_expect_tx(full_bar(s), G::STAGE);
+                if (!wait_drain(full_bar(s), (j / STAGES) & 1u, wd)) break;
+            }
+        }
+        ptx::cluster_sync_all();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        if constexpr (PAIR)
+            ptx::tmem_dealloc_pair(tmem_base, TMEM_ALLOC);
+        else
+            ptx::tmem_dealloc(tmem_base, TMEM_ALLOC);
+    }
+}
+
+}  // namespace tg

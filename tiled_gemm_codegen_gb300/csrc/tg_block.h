@@ -1,0 +1,88 @@
+// What the block projections' entry points (tg_block.cu) and their kernel's
+// translation units (tg_block_kernels.cu, one a mode) share.  Not part of the
+// public ABI.
+#pragma once
+
+#include "tg_internal.h"
+
+namespace tg {
+
+enum : int { BLOCK_GATED = 0, BLOCK_GRAD = 1, BLOCK_SHRINK = 2, BLOCK_ADAPT = 3 };
+
+// One output: rows of D's features (a half of Z or dZ is one).
+struct BlockOut {
+    void *p;       // null: not wanted
+    int64_t ld;    // elements
+    int32_t tma;   // a tensor map of it exists (rows on 16 bytes)
+};
+
+// Where a row's u stands for ADAPT, written by the table kernel.
+struct AdapterTables {
+    int32_t *ids;      // [min(groups, S)] groups that have rows, in order
+    int32_t *lo, *hi;  // [min(groups, S)] their rows
+    int32_t *rank;     // [groups] place in ids (of groups that have rows)
+    int32_t *first;    // [row tiles] place of the tile's first adapter
+    int32_t *count;    // [row tiles] adapters of its rows
+    int32_t *blocks;   // [row tiles + 1] blocks before the tile's
+    int32_t *flags;    // [groups][ADAPT_FLAGS] B_g holds an infinity or NaN
+};
+constexpr int ADAPT_FLAGS = 8;
+
+struct BlockParams {
+    const int32_t *offsets;  // [groups + 1]; null: one group of all rows
+    int32_t groups, S;
+    int32_t N;               // features of an output row (GATED and GRAD: of a half of z)
+    int32_t k_blocks;
+    int32_t tiles_n;
+    int32_t group_m;         // tiles of rows a raster strip
+    int32_t w_k;             // 1 = weights stored N x K
+    int32_t w_shared;        // 1 = every group has the same weights
+    int32_t act, out_bf16;
+    BlockOut out0;           // H (GATED, GRAD), Y (ADAPT), U (SHRINK)
+    BlockOut gate, up;       // halves of Z (GATED) or dZ (GRAD)
+    const uint16_t *z;       // GRAD: Z
+    int64_t ldz;
+    // SHRINK, ADAPT
+    AdapterTables tab;
+    const float *scales;     // [groups] or null
+    uint16_t *wide;          // u's parts: [block][bn rows][64]
+    int32_t R, Rp;
+    int32_t wide_bn;         // rows of ADAPT's tiles
+    const uint16_t *b;       // B (as the caller gave it), for flagged adapters
+    int64_t ldb, strideB;
+    int32_t b_shared;        // 1 = every adapter has the same B
+    // shares of tiles
+    int32_t splits;
+    float *partials;         // [tile][CTA of the pair][splits][BM x BN]
+    int32_t *counters;       // arrivals per [tile][CTA], zero between calls
+    uint32_t *err;
+    uint64_t timeout_ns;
+    int32_t debug_stall;
+};
+
+// Blocks of 64 k that a row tile's adapters take.
+__host__ __device__ inline int32_t adapter_blocks(int32_t count, int32_t Rp)
+{
+    return Rp <= 32 ? (count * Rp + 31) / 32 : count * (Rp / 32);
+}
+
+constexpr int BLOCK_EPI_WARPS = 8;
+constexpr int BLOCK_THREADS = 64 + 32 * BLOCK_EPI_WARPS;
+
+using BlockKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                             const CUtensorMap, const CUtensorMap, const BlockParams);
+
+struct BlockShape {
+    BlockKernel kern;
+    int bn, smem;
+    bool pair;
+};
+
+// Tiles of a mode: pairs, one CTA, one CTA for few rows.
+enum BlockTiles : int { TILES_PAIR = 0, TILES_ONE = 1, TILES_FEW = 2 };
+BlockShape block_shape_gated(BlockTiles t);
+BlockShape block_shape_grad(BlockTiles t);
+BlockShape block_shape_shrink(BlockTiles t);
+BlockShape block_shape_adapt(BlockTiles t);
+
+}  // namespace tg

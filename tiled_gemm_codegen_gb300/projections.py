@@ -1,0 +1,158 @@
+"""A transformer block's projections on torch tensors, with what stands around
+them fused in: the gated projection of a feed-forward block, the gradient
+through it, and a projection with low-rank adapters of many requests beside its
+shared weights.
+
+As ``experts`` this is a thin binding of ``include/tg_gemm.h``: pointers, shapes
+and strides are read off the tensors, all arithmetic happens in the CUDA
+library, calls are asynchronous on ``stream`` (default: torch's current
+stream), rows that share memory are refused, and no gradients are recorded
+(``examples/gated_block.py`` makes an autograd function of the calls).
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import ACTIVATIONS, _with_layout
+from .experts import _B_COL_MAJOR, _BF16, _bf16_rows, _check, _lib, _matrices, _offsets, _pitch, _rows, _stream
+
+__all__ = ["gemm_gated", "gemm_gated_grad", "gemm_adapted"]
+
+
+def _activation(name):
+    code = ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    return code
+
+
+def _weights(W, offsets, what):
+    """((offsets' ptr, groups), _matrices' tuple) of weights [K, N] without
+    offsets or [groups, K, N] with them."""
+    if W.dtype != _BF16 or not W.is_cuda:
+        raise TypeError(f"{what} must be a bf16 CUDA tensor")
+    if offsets is None:
+        if W.dim() != 2:
+            raise ValueError(f"{what} must have shape [K, N] (weights of several groups need offsets)")
+        return (None, 1), _matrices(W.unsqueeze(0), what)
+    po, groups = _offsets(offsets)
+    m = _matrices(W, what)
+    if m[1] != groups:
+        raise ValueError(f"{what} must have shape [{groups}, K, N]")
+    return (po, groups), m
+
+
+def _options(options, col_major):
+    if options is not None:
+        return ctypes.byref(_with_layout(options, False, col_major))
+    return _B_COL_MAJOR if col_major else None
+
+
+def _wanted(t, shape, like, what):
+    """(tensor or None, ptr, ld) of an optional bf16 output: None, True (one is
+    made) or a tensor."""
+    if t is None or t is False:
+        return None, None, 0
+    if t is True:
+        t = torch.empty(shape, dtype=_BF16, device=like.device)
+    if t.dtype != _BF16:
+        raise TypeError(f"{what} must be a bf16 CUDA tensor")
+    p, _, _, ld, _ = _rows(t, what, *shape)
+    return t, p, ld
+
+
+def gemm_gated(X, W, offsets=None, H=None, *, Z=None, activation: str = "silu", options=None, stream=None):
+    """H [S, F] = act(z[:, :F]) * z[:, F:] with z = X @ W for bf16 X [S, K] and
+    W [K, 2 F] (the gate's columns first), or W [groups, K, 2 F] with offsets
+    (int32 [groups + 1] on the GPU, an order's): rows offsets[g] ..
+    offsets[g + 1] - 1 meet W[g], rows of no group give zeros.  A transposed
+    view of W (a linear layer's weights) is taken as it is.  Z: True, or a
+    bf16 tensor [S, 2 F], to have z too, as gemm_gated_grad wants it; the call
+    then returns (H, Z).  H is bf16; activation: "silu", "gelu_tanh", "relu" or
+    "none"."""
+    act = _activation(activation)
+    px, S, K, ldx = _bf16_rows(X, "X")
+    (po, groups), (pw, _, K2, N2, ldw, strideW, w_cm) = _weights(W, offsets, "W")
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    if N2 % 2:
+        raise ValueError("W must have an even number of columns: the gate's, then as many of the other factor")
+    F = N2 // 2
+    if H is None:
+        H = torch.empty(S, F, dtype=_BF16, device=X.device)
+    H, ph, ldh = _wanted(H, (S, F), X, "H")
+    Z, pz, ldz = _wanted(Z, (S, N2), X, "Z")
+    _check(_lib().tg_gemm_gated(px, pw, ph, pz, po, groups, S, F, K, ldx, ldw, strideW, ldh, ldz, act, _stream(X, stream),
+                                _options(options, w_cm)), "tg_gemm_gated")
+    return H if Z is None else (H, Z)
+
+
+def gemm_gated_grad(dY, V, Z, offsets=None, dZ=None, *, H=None, activation: str = "silu", options=None, stream=None):
+    """dZ [S, 2 F], the gradient of gemm_gated's z where dL/dH = dY @ V, for
+    bf16 dY [S, K], V [K, F] (or [groups, K, F] with offsets) and the Z [S,
+    2 F] that gemm_gated gave: with y = H @ down, dY is dL/dy and V is
+    down.transpose(-1, -2).  dL/dH is never stored.  The other gradients are
+    products with dZ: dX = gemm(dZ, W.t()), dW = dZ's with X (gemm_grouped
+    and gemm_grouped_wgrad by group).  H: True, or a bf16 tensor [S, F], to
+    have gemm_gated's H again (for down's gradient); the call then returns
+    (dZ, H).  Rows of no group give zeros."""
+    act = _activation(activation)
+    py, S, K, lddy = _bf16_rows(dY, "dY")
+    (po, groups), (pv, _, K2, F, ldv, strideV, v_cm) = _weights(V, offsets, "V")
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    if Z.dtype != _BF16:
+        raise TypeError("Z must be a bf16 CUDA tensor")
+    pz, _, _, ldz, _ = _rows(Z, "Z", S, 2 * F)
+    dZ, pdz, lddz = _wanted(True if dZ is None else dZ, (S, 2 * F), dY, "dZ")
+    H, ph, ldh = _wanted(H, (S, F), dY, "H")
+    _check(_lib().tg_gemm_gated_grad(py, pv, pz, pdz, ph, po, groups, S, F, K, lddy, ldv, strideV, ldz, lddz, ldh, act,
+                                     _stream(dY, stream), _options(options, v_cm)), "tg_gemm_gated_grad")
+    return dZ if H is None else (dZ, H)
+
+
+def _adapters(t, what, groups, R, cols):
+    """(ptr, rows, ld, group stride) of adapters' matrices [groups, R, cols]."""
+    if t.dtype != _BF16 or not t.is_cuda:
+        raise TypeError(f"{what} must be a bf16 CUDA tensor")
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != groups or (R is not None and shape[1] != R) or shape[2] != cols:
+        raise ValueError(f"{what} must have shape [{groups}, {'R' if R is None else R}, {cols}]")
+    if cols > 1 and st[2] != 1 and t.numel():
+        raise ValueError(f"{what} must have unit stride in its last dimension")
+    return t.data_ptr(), shape[1], _pitch(st[1], shape[1], cols, what), st[0] if groups > 1 else 0
+
+
+def gemm_adapted(X, W, A, B, offsets, Y=None, *, scales=None, U=None, out_dtype=None, options=None, stream=None):
+    """Y [S, N] = X @ W + u @ B[g] with u = scales[g] * X @ A[g].T, for the rows
+    offsets[g] .. offsets[g + 1] - 1 of adapter g (int32 [groups + 1] on the
+    GPU, an order's); rows of no adapter give X @ W.  X [S, K], W [K, N] (or a
+    transposed view), A [groups, R, K] and B [groups, R, N] are bf16, scales
+    fp32 [groups] (None: ones).  Y: fp32 (default) or bf16.  U: True, or a bf16
+    tensor [S, R], to have u too; the call then returns (Y, U).
+
+    The gradient of X is the same call the other way: dX, dU =
+    gemm_adapted(dY, W.t(), B, A, offsets, scales=scales, U=True); then dA =
+    gemm_grouped_wgrad(dU, X, offsets) and dB = gemm_grouped_wgrad(U, dY,
+    offsets)."""
+    po, groups = _offsets(offsets)
+    px, S, K, ldx = _bf16_rows(X, "X")
+    (_, _), (pw, _, K2, N, ldw, _, w_cm) = _weights(W, None, "W")
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    pa, R, lda, strideA = _adapters(A, "A", groups, None, K)
+    pb, _, ldb, strideB = _adapters(B, "B", groups, R, N)
+    ps = None
+    if scales is not None:
+        if scales.dtype != torch.float32 or not scales.is_cuda or scales.shape != (groups,) or not scales.is_contiguous():
+            raise TypeError(f"scales must be a contiguous fp32 CUDA tensor of shape [{groups}]")
+        ps = scales.data_ptr()
+    if Y is None:
+        Y = torch.empty(S, N, dtype=out_dtype if out_dtype is not None else torch.float32, device=X.device)
+    py, _, _, ldy, ty = _rows(Y, "Y", S, N)
+    U, pu, ldu = _wanted(U, (S, R), X, "U")
+    _check(_lib().tg_gemm_adapted(px, pw, pa, pb, py, pu, po, ps, groups, S, N, K, R, ldx, ldw, lda, strideA, ldb, strideB, ldy,
+                                  ldu, ty, _stream(X, stream), _options(options, w_cm)), "tg_gemm_adapted")
+    return Y if U is None else (Y, U)
