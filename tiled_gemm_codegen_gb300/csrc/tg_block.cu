@@ -5,9 +5,10 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include "tg_block.h"
+#include "tg_adapter.cuh"
 #include "tg_gemm.h"
 #include "tg_host_api.h"
+#include "tg_ptx.cuh"
 #include "tg_tiles.h"
 
 #define TG_API extern "C" __attribute__((visibility("default")))
@@ -17,14 +18,16 @@ namespace {
 
 constexpr int64_t ADAPT_GROUPS = 4096;  // adapters a call takes at most
 constexpr int64_t ADAPT_RANK = 256;
+constexpr int64_t ADAPT_FEW_ROWS = 2048;
+constexpr int64_t ADAPT_FEW_BYTES = 32 << 20;
 
 // ------------------------------------------------------------ adapter tables
-constexpr int TABLE_THREADS = 1024;
-
-// Inclusive scan over the block (max or sum); `part` holds 33 words.
-template <bool MAX>
+// Inclusive scan over a block of THREADS (max or sum); part holds 32 words,
+// the last of THREADS / 32 the total.
+template <int THREADS, bool MAX>
 __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t *part)
 {
+    constexpr int WARPS = THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -35,75 +38,64 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t *part)
     if (lane == 31) part[warp] = v;
     __syncthreads();
     if (warp == 0) {
-        int32_t t = part[lane];
+        int32_t t = lane < WARPS ? part[lane] : 0;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
+        for (int d = 1; d < WARPS; d <<= 1) {
             const int32_t o = __shfl_up_sync(0xffffffffu, t, d);
             if (lane >= d) t = MAX ? max(t, o) : t + o;
         }
-        part[lane] = t;
+        if (lane < WARPS) part[lane] = t;
     }
     __syncthreads();
     if (warp > 0) v = MAX ? max(v, part[warp - 1]) : v + part[warp - 1];
     return v;
 }
 
-// Block 0: the tables of AdapterTables but the flags (bounds clamped as the
-// walks clamp them: inside [0, S], never falling).  The others: a share of one
-// group's B each, flagged if it holds an infinity or NaN.
-__global__ void __launch_bounds__(TABLE_THREADS) adapter_tables_kernel(const BlockParams p, int32_t bn, int32_t tiles, int32_t N,
-                                                                       int32_t vec)
+// The block's walk over the groups, THREADS at a time: each(g, lo, hi, place)
+// for every group that has rows, by the thread that holds it; bounds clamped
+// as block_walk_load clamps them (inside [0, S], never falling).  Returns the
+// number of such groups.
+template <int THREADS, class F>
+__device__ __forceinline__ int32_t each_group(const BlockParams &p, int32_t *part, int32_t *his, F &&each)
 {
-    __shared__ int32_t part[32];
     const int tid = static_cast<int>(threadIdx.x);
-    if (blockIdx.x > 0) {
-        const int32_t g = static_cast<int32_t>(blockIdx.x - 1) / ADAPT_FLAGS, c = static_cast<int32_t>(blockIdx.x - 1) % ADAPT_FLAGS;
-        int32_t bad = 0;
-        if (p.offsets[g + 1] > p.offsets[g]) {
-            for (int32_t r = c; r < p.R; r += ADAPT_FLAGS) {
-                const uint16_t *row = p.b + g * p.strideB + r * p.ldb;
-                const int32_t body = vec ? N / 8 : 0;
-                for (int32_t i = tid; i < body; i += TABLE_THREADS) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row) + i);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        bad |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
-                }
-                for (int32_t i = body * 8 + tid; i < N; i += TABLE_THREADS) bad |= (row[i] & 0x7f80u) == 0x7f80u;
-            }
-        }
-        bad = __syncthreads_or(bad);
-        if (tid == 0) p.tab.flags[g * ADAPT_FLAGS + c] = bad;
-        return;
-    }
-    int32_t last = max(0, min(p.offsets[0], p.S)), used = 0;
-    for (int32_t g0 = 0; g0 < p.groups; g0 += TABLE_THREADS) {
+    int32_t last = max(0, min(__ldg(p.offsets), p.S)), used = 0;
+    for (int32_t g0 = 0; g0 < p.groups; g0 += THREADS) {
         const int32_t g = g0 + tid;
-        int32_t hi = g < p.groups ? max(0, min(p.offsets[g + 1], p.S)) : 0;
-        hi = block_scan<true>(max(hi, last), part);
-        __shared__ int32_t his[TABLE_THREADS];
+        int32_t hi = g < p.groups ? max(0, min(__ldg(p.offsets + g + 1), p.S)) : 0;
+        hi = block_scan<THREADS, true>(max(hi, last), part);
         his[tid] = hi;
         __syncthreads();
         const int32_t lo = tid > 0 ? his[tid - 1] : last;
         const int32_t has = g < p.groups && hi > lo ? 1 : 0;
-        const int32_t at = used + block_scan<false>(has, part) - has;
-        if (has) {
-            p.tab.ids[at] = g;
-            p.tab.lo[at] = lo;
-            p.tab.hi[at] = hi;
-            p.tab.rank[g] = at;
-        }
-        last = his[TABLE_THREADS - 1];
-        used += part[31];
+        const int32_t place = used + block_scan<THREADS, false>(has, part) - has;
+        if (has) each(g, lo, hi, place);
+        last = his[THREADS - 1];
+        used += part[THREADS / 32 - 1];
         __syncthreads();
     }
+    return used;
+}
+
+// By one block: the tables of AdapterTables but the flags.  stride: blocks of
+// a tile (0: as many as it needs, tiles one behind another).  Returns the
+// number of groups that have rows.
+template <int THREADS>
+__device__ __forceinline__ int32_t write_tables(const BlockParams &p, int32_t tiles, int32_t stride, int32_t *part, int32_t *his)
+{
+    const int tid = static_cast<int>(threadIdx.x);
+    const int32_t used = each_group<THREADS>(p, part, his, [&](int32_t g, int32_t lo, int32_t hi, int32_t place) {
+        p.tab.ids[place] = g;
+        p.tab.lo[place] = lo;
+        p.tab.hi[place] = hi;
+        p.tab.rank[g] = place;
+    });
     int32_t blocks = 0;
-    for (int32_t t0 = 0; t0 < tiles; t0 += TABLE_THREADS) {
+    for (int32_t t0 = 0; t0 < tiles; t0 += THREADS) {
         const int32_t t = t0 + tid;
         int32_t n = 0;
         if (t < tiles) {
-            const int64_t r0 = static_cast<int64_t>(t) * bn, r1 = r0 + bn;
+            const int64_t r0 = static_cast<int64_t>(t) * p.wide_bn, r1 = r0 + p.wide_bn;
             int32_t a = 0, b = used;  // first with hi > r0
             while (a < b) {
                 const int32_t m = (a + b) / 2;
@@ -123,14 +115,241 @@ __global__ void __launch_bounds__(TABLE_THREADS) adapter_tables_kernel(const Blo
             }
             p.tab.first[t] = first;
             p.tab.count[t] = a - first;
-            n = adapter_blocks(a - first, p.Rp);
+            n = stride > 0 ? stride : adapter_blocks(a - first, p.Rp);
         }
-        const int32_t at = blocks + block_scan<false>(n, part);
-        if (t < tiles) p.tab.blocks[t + 1] = at;
-        blocks += part[31];
+        const int32_t before = blocks + block_scan<THREADS, false>(n, part) - n;
+        if (t < tiles) p.tab.blocks[t] = before;
+        blocks += part[THREADS / 32 - 1];
         __syncthreads();
     }
-    if (tid == 0) p.tab.blocks[0] = 0;
+    return used;
+}
+
+// By one block: share `c` of ADAPT_FLAGS of B_g's rows, flagged if it holds an
+// infinity or NaN (groups without rows are not looked at).
+template <int THREADS>
+__device__ __forceinline__ void write_flag(const BlockParams &p, int32_t g, int32_t c, int32_t N, int32_t vec)
+{
+    const int tid = static_cast<int>(threadIdx.x);
+    if (__ldg(p.offsets + g + 1) <= __ldg(p.offsets + g)) return;
+    int32_t bad = 0;
+    for (int32_t r = c; r < p.R; r += ADAPT_FLAGS) {
+        const uint16_t *row = p.b + g * p.strideB + r * p.ldb;
+        const int32_t body = vec ? N / 8 : 0;
+        for (int32_t i = tid; i < body; i += THREADS) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row) + i);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+        }
+        for (int32_t i = body * 8 + tid; i < N; i += THREADS) bad |= (row[i] & 0x7f80u) == 0x7f80u;
+    }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) p.tab.flags[g * ADAPT_FLAGS + c] = bad;
+}
+
+constexpr int TABLE_THREADS = 1024;
+constexpr int ROWS_THREADS = 512;
+
+// Block 0: the tables.  The others: flags.
+__global__ void __launch_bounds__(TABLE_THREADS) adapter_tables_kernel(const BlockParams p, int32_t tiles, int32_t N, int32_t vec)
+{
+    ptx::griddep_launch_dependents();
+    __shared__ int32_t part[32], his[TABLE_THREADS];
+    if (blockIdx.x == 0)
+        write_tables<TABLE_THREADS>(p, tiles, 0, part, his);
+    else
+        write_flag<TABLE_THREADS>(p, static_cast<int32_t>(blockIdx.x - 1) / ADAPT_FLAGS,
+                                  static_cast<int32_t>(blockIdx.x - 1) % ADAPT_FLAGS, N, vec);
+}
+
+// ------------------------------------------------------------ u of few rows
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Values k .. k + 7 of a row on 16 bytes, zeros from K.
+__device__ __forceinline__ uint4 load8(const uint16_t *row, int32_t k, int32_t K)
+{
+    if (k + 8 <= K) return __ldg(reinterpret_cast<const uint4 *>(row + k));
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (k + e < K) w[e >> 1] |= static_cast<uint32_t>(row[k + e]) << (16 * (e & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Few rows an adapter (decoding): the tables, the flags and u in one launch, so
+// that ADAPT's shared projection, which starts beside it, waits for
+// little.  Block 0: the tables; blocks 1 .. chunks: 16 rows of one group each,
+// K split over the block's 16 warps, 32 R at a time; the rest: flags.  A lane's
+// 16 bytes of X and of A are two MMAs' fragments: any order of k will do where
+// both operands have the same.  Bound by latency: offsets, one
+// round of loads, the warps' sums.
+__global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockParams p, const uint16_t *X, int64_t ldx, const uint16_t *A,
+                                                                    int64_t lda, int64_t strideA, int32_t K, int32_t chunks,
+                                                                    int32_t tiles, int32_t stride, int32_t N, int32_t vec)
+{
+    ptx::griddep_launch_dependents();
+    constexpr int WARPS = ROWS_THREADS / 32;
+    __shared__ int32_t part[32], his[ROWS_THREADS];
+    __shared__ int32_t found[8];  // group, first row, rows, place; adapters before and in the (two) tiles
+    __shared__ float sums[WARPS][16][33];
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    if (blockIdx.x == 0) {
+        const int32_t used = write_tables<ROWS_THREADS>(p, tiles, stride, part, his);
+        // rows of no group: zeros
+        const int32_t first = max(0, min(__ldg(p.offsets), p.S)), last = used > 0 ? p.tab.hi[used - 1] : first;
+        for (int32_t i = warp; i < first + p.S - last; i += WARPS) {
+            const int32_t row = i < first ? i : last + i - first, tile = row / p.wide_bn;
+            zero_columns(p, row % p.wide_bn, tile * stride, p.tab.count[tile], -1, lane);
+            for (int32_t r = lane; p.out0.p && r < p.R; r += 32)
+                static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = 0;
+        }
+        return;
+    }
+    if (static_cast<int32_t>(blockIdx.x) > chunks) {
+        const int32_t i = static_cast<int32_t>(blockIdx.x) - 1 - chunks;
+        write_flag<ROWS_THREADS>(p, i / ADAPT_FLAGS, i % ADAPT_FLAGS, N, vec);
+        return;
+    }
+    // the chunk's group: chunks are counted group by group
+    const int32_t want = static_cast<int32_t>(blockIdx.x) - 1;
+    if (tid < 8) found[tid] = tid == 0 ? -1 : 0;
+    __syncthreads();
+    {
+        int32_t before = 0;  // chunks of the groups before this turn's
+        int32_t last = max(0, min(__ldg(p.offsets), p.S)), used = 0;
+        for (int32_t g0 = 0; g0 < p.groups; g0 += ROWS_THREADS) {
+            const int32_t g = g0 + tid;
+            int32_t hi = g < p.groups ? max(0, min(__ldg(p.offsets + g + 1), p.S)) : 0;
+            hi = block_scan<ROWS_THREADS, true>(max(hi, last), part);
+            his[tid] = hi;
+            __syncthreads();
+            const int32_t lo = tid > 0 ? his[tid - 1] : last;
+            const int32_t rows = g < p.groups ? hi - lo : 0;
+            // chunks in the low bits' place, groups with rows above: one scan
+            const int32_t n = (rows + 15) / 16, has = rows > 0;
+            const int32_t at_n = before + block_scan<ROWS_THREADS, false>(n, part) - n;
+            const int32_t all_n = part[WARPS - 1];
+            const int32_t at = used + block_scan<ROWS_THREADS, false>(has, part) - has;
+            if (want >= at_n && want < at_n + n) {
+                found[0] = g;
+                found[1] = lo + (want - at_n) * 16;
+                found[2] = min(16, hi - found[1]);
+                found[3] = at;
+            }
+            last = his[ROWS_THREADS - 1];
+            before += all_n;
+            used += part[WARPS - 1];
+            __syncthreads();
+        }
+    }
+    const int32_t g = found[0], row0 = found[1], rows = found[2];
+    if (g < 0) return;
+    // the adapters before and in the tiles of its rows (two at most)
+    const int32_t t0 = row0 / p.wide_bn, t1 = (row0 + rows - 1) / p.wide_bn;
+    if (p.groups <= ROWS_THREADS) {
+        // (every group's bounds are in his, and its own thread counts it)
+        const int32_t first_row = max(0, min(__ldg(p.offsets), p.S));
+        const int32_t hi = his[tid], lo = tid > 0 ? his[tid - 1] : first_row;
+        const bool has = tid < p.groups && hi > lo;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int32_t r0 = (k ? t1 : t0) * p.wide_bn, r1 = r0 + p.wide_bn;
+            const int32_t b = __syncthreads_count(has && hi <= r0), c = __syncthreads_count(has && hi > r0 && lo < r1);
+            if (tid == 0) {
+                found[4 + 2 * k] = b;
+                found[5 + 2 * k] = c;
+            }
+        }
+    } else {
+        int32_t b[2] = {0, 0}, c[2] = {0, 0};
+        each_group<ROWS_THREADS>(p, part, his, [&](int32_t, int32_t lo, int32_t hi, int32_t) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int32_t r0 = (k ? t1 : t0) * p.wide_bn, r1 = r0 + p.wide_bn;
+                b[k] += hi <= r0;
+                c[k] += hi > r0 && lo < r1;
+            }
+        });
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (b[k]) atomicAdd(&found[4 + 2 * k], b[k]);
+            if (c[k]) atomicAdd(&found[5 + 2 * k], c[k]);
+        }
+    }
+    __syncthreads();
+    const int32_t place = found[3];
+
+    // sums over this warp's share of K
+    const int gid = lane >> 2, t = lane & 3;
+    const uint16_t *x0 = X + static_cast<int64_t>(row0 + min(gid, rows - 1)) * ldx;
+    const uint16_t *x1 = X + static_cast<int64_t>(row0 + min(gid + 8, rows - 1)) * ldx;
+    const float scale = p.scales ? __ldg(p.scales + g) : 1.0f;
+    const int32_t steps = (K + 31) / 32;
+    for (int32_t r0 = 0; r0 < p.R; r0 += 32) {
+        const int tiles_r = min(4, (p.R - r0 + 7) / 8);
+        float c[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[i][e] = 0.0f;
+        const uint16_t *w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = A + g * strideA + static_cast<int64_t>(min(r0 + 8 * i + gid, p.R - 1)) * lda;
+#pragma unroll 4
+        for (int32_t s = warp; s < steps; s += WARPS) {
+            const int32_t k = s * 32 + 8 * t;
+            const uint4 xa = load8(x0, k, K), xb = load8(x1, k, K);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i >= tiles_r) break;
+                const uint4 wv = load8(w[i], k, K);
+                mma_16x8x16(c[i], xa.x, xb.x, xa.y, xb.y, wv.x, wv.y);
+                mma_16x8x16(c[i], xa.z, xb.z, xa.w, xb.w, wv.z, wv.w);
+            }
+        }
+        __syncthreads();  // the sums of the turn before were read
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sums[warp][gid + (e >> 1) * 8][8 * i + 2 * t + (e & 1)] = c[i][e];
+        __syncthreads();
+        // a thread a value
+        const int32_t in = tid >> 5, r = r0 + lane;
+        if (in < rows && r < p.Rp) {
+            float x = 0.0f;
+#pragma unroll
+            for (int k = 0; k < WARPS; ++k) x = __fadd_rn(x, sums[k][in][lane]);
+            x = r < p.R ? __fmul_rn(scale, x) : 0.0f;  // (columns past R meet zeros)
+            __nv_bfloat16 hi, lo;
+            split_parts(x, hi, lo);
+            const int32_t row = row0 + in, tile = row / p.wide_bn, k = tile == t0 ? 0 : 1;
+            const int32_t unit = adapter_unit(place - found[4 + 2 * k], tile * stride, row % p.wide_bn, p.wide_bn, p.Rp);
+            uint16_t *at = p.wide + static_cast<int64_t>(unit) * 8 + (p.Rp <= 32 ? r : r / 64 * 2 * p.wide_bn * 64 + (r & 63));
+            at[0] = __bfloat16_as_ushort(hi);
+            at[p.Rp <= 32 ? p.Rp : static_cast<int64_t>(p.wide_bn) * 64] = __bfloat16_as_ushort(lo);
+            if (p.out0.p && r < p.R)
+                static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+        }
+    }
+    // columns from R's last 32 to Rp's end, and the other adapters'
+    for (int32_t in = warp; in < rows; in += WARPS) {
+        const int32_t row = row0 + in, tile = row / p.wide_bn, k = tile == t0 ? 0 : 1;
+        const int32_t i = place - found[4 + 2 * k];
+        zero_columns(p, row % p.wide_bn, tile * stride, found[5 + 2 * k], i, lane);
+        for (int32_t r = (p.R + 31) / 32 * 32 + lane; r < p.Rp; r += 32) {
+            uint16_t *at = p.wide + static_cast<int64_t>(adapter_unit(i, tile * stride, row % p.wide_bn, p.wide_bn, p.Rp)) * 8 +
+                           r / 64 * 2 * p.wide_bn * 64 + (r & 63);
+            at[0] = 0;
+            at[static_cast<int64_t>(p.wide_bn) * 64] = 0;
+        }
+    }
 }
 
 // ------------------------------------------------------------ launches
@@ -371,6 +590,10 @@ tg_status run_gated(int mode, Operand x, Operand w, Operand v, bool w_k, uint16_
     p.out0 = output(&m.o, H, S, F, ldh, 2);
     p.gate = output(&m.g, zout, S, F, ldzout, 2);
     p.up = output(&m.u, zout ? zout + F : nullptr, S, F, ldzout, 2);
+    if (z && tma_ok(z, ldz, 0, 2) && F % 8 == 0) {
+        const BlockOut g = output(&m.e, const_cast<uint16_t *>(z), S, F, ldz, 2), u = output(&m.v, const_cast<uint16_t *>(z) + F, S, F, ldz, 2);
+        p.z_tma = g.tma && u.tma ? 1 : 0;
+    }
     return host_cuda_status(launch_block(mode, c.tiles, hs, c.units * c.splits, m, p));
 }
 
@@ -389,9 +612,13 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     const Cut cy = cut_rows(BLOCK_ADAPT, S, N, K, 1, hs.sms, opt);
     if (ca.units * ca.splits > INT32_MAX || cy.units * cy.splits > INT32_MAX) return TG_ERR_UNSUPPORTED;
     const int64_t tiles = cdiv(S, cy.bn);
-    // A tile's blocks round its adapters up; together at most so many.
-    const int64_t blocks = Rp <= 32 ? std::min(tiles + hit, tiles + cdiv((tiles + hit) * Rp, 32)) : (tiles + hit) * (Rp / 32);
-    if (blocks * cy.bn > INT32_MAX) return TG_ERR_UNSUPPORTED;
+    // Few rows: u by adapter_rows_kernel, a fixed number of blocks a tile.
+    const int64_t stride = adapter_blocks(static_cast<int32_t>(std::min(cy.bn, hit)), static_cast<int32_t>(Rp));
+    const bool few = S <= ADAPT_FEW_ROWS && tiles * stride * cy.bn * 128 <= ADAPT_FEW_BYTES;
+    // Else a tile's blocks round its adapters up; together at most so many.
+    const int64_t blocks = few ? tiles * stride
+                           : Rp <= 32 ? std::min(tiles + hit, tiles + cdiv((tiles + hit) * Rp, 32)) : (tiles + hit) * (Rp / 32);
+    if (blocks * cy.bn > INT32_MAX / 8) return TG_ERR_UNSUPPORTED;
 
     BlockParams p{};
     BlockMaps m;
@@ -421,12 +648,13 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
         p.b_shared = 1;
     }
     Scratch s;
-    const size_t at_part = s.take(std::max(ca.part_bytes(), cy.part_bytes()));
+    // (the two products' shares apart: their kernels overlap)
+    const size_t at_part_a = s.take(few ? 0 : ca.part_bytes()), at_part = s.take(cy.part_bytes());
     Operand *ops[4] = {&x, &w, &a, &b};
     const size_t at[4] = {s.take(pack_bytes(x)), s.take(pack_bytes(w)), s.take(pack_bytes(a)), s.take(pack_bytes(b))};
     const size_t at_wide = s.take(static_cast<size_t>(blocks) * cy.bn * 128);
     const size_t words[7] = {static_cast<size_t>(hit), static_cast<size_t>(hit), static_cast<size_t>(hit), static_cast<size_t>(groups),
-                             static_cast<size_t>(tiles), static_cast<size_t>(tiles), static_cast<size_t>(tiles + 1)};
+                             static_cast<size_t>(tiles), static_cast<size_t>(tiles), static_cast<size_t>(tiles)};
     size_t at_tab[7];
     for (int i = 0; i < 7; ++i) at_tab[i] = s.take(words[i] * 4);
     const size_t at_flags = s.take(static_cast<size_t>(groups) * ADAPT_FLAGS * 4);
@@ -438,28 +666,38 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
                           table(at_tab[4]), table(at_tab[5]), table(at_tab[6]), table(at_flags)};
     p.wide = reinterpret_cast<uint16_t *>(arena + at_wide);
     p.partials = reinterpret_cast<float *>(arena + at_part);
-    if (ca.splits > 1 || cy.splits > 1) {
-        if ((st = host_counters(hs, static_cast<size_t>(std::max(ca.part_tiles(), cy.part_tiles())) * 4, &p.counters)) != TG_OK) return st;
-    }
+    const int64_t parts_a = few ? 0 : ca.part_tiles(), parts_y = cy.part_tiles();
+    int32_t *counters = nullptr;
+    if (parts_a + parts_y > 0 && (st = host_counters(hs, static_cast<size_t>(parts_a + parts_y) * 4, &counters)) != TG_OK) return st;
+    p.counters = counters + parts_a;
     cudaError_t e = pack_operands(hs, arena, ops, at, 4);
     if (e != cudaSuccess) return host_cuda_status(e);
 
     p.offsets = offsets;
     p.groups = static_cast<int32_t>(groups);
     p.N = static_cast<int32_t>(R);
-    adapter_tables_kernel<<<static_cast<unsigned>(1 + groups * ADAPT_FLAGS), TABLE_THREADS, 0, hs.stream>>>(
-        p, static_cast<int32_t>(cy.bn), static_cast<int32_t>(tiles), static_cast<int32_t>(N), b_vec ? 1 : 0);
-    if ((e = cudaGetLastError()) != cudaSuccess) return host_cuda_status(e);
-
-    // u
-    BlockParams pa = p;
-    pa.w_k = 1;
-    pa.w_shared = a_shared ? 1 : 0;
-    pa.out_bf16 = 1;
-    pa.out0 = BlockOut{U, ldu, 0};
-    set_cut(pa, ca, R);
-    if (K > 0 && (!map_operand(&m.x, x, static_cast<uint32_t>(ca.bn)) || !map_operand(&m.w, a, BM))) return TG_ERR_CUDA;
-    if ((e = launch_block(BLOCK_SHRINK, ca.tiles, hs, ca.units * ca.splits, m, pa)) != cudaSuccess) return host_cuda_status(e);
+    p.out0 = BlockOut{U, ldu, 0};
+    const unsigned flag_blocks = static_cast<unsigned>(groups * ADAPT_FLAGS);
+    const int32_t vec = b_vec ? 1 : 0;
+    if (few) {
+        const int32_t chunks = static_cast<int32_t>(S / 16 + hit);
+        adapter_rows_kernel<<<1u + chunks + flag_blocks, ROWS_THREADS, 0, hs.stream>>>(
+            p, static_cast<const uint16_t *>(x.p), x.ld, static_cast<const uint16_t *>(a.p), a.ld, a_shared ? 0 : a.stride,
+            static_cast<int32_t>(K), chunks, static_cast<int32_t>(tiles), static_cast<int32_t>(stride), static_cast<int32_t>(N), vec);
+        if ((e = cudaGetLastError()) != cudaSuccess) return host_cuda_status(e);
+    } else {
+        adapter_tables_kernel<<<1u + flag_blocks, TABLE_THREADS, 0, hs.stream>>>(p, static_cast<int32_t>(tiles), static_cast<int32_t>(N), vec);
+        if ((e = cudaGetLastError()) != cudaSuccess) return host_cuda_status(e);
+        BlockParams pa = p;
+        pa.w_k = 1;
+        pa.w_shared = a_shared ? 1 : 0;
+        pa.out_bf16 = 1;
+        pa.partials = reinterpret_cast<float *>(arena + at_part_a);
+        pa.counters = counters;
+        set_cut(pa, ca, R);
+        if (K > 0 && (!map_operand(&m.x, x, static_cast<uint32_t>(ca.bn)) || !map_operand(&m.w, a, BM))) return TG_ERR_CUDA;
+        if ((e = launch_block(BLOCK_SHRINK, ca.tiles, hs, ca.units * ca.splits, m, pa)) != cudaSuccess) return host_cuda_status(e);
+    }
 
     // Y
     const bool pair = cy.tiles == TILES_PAIR;

@@ -37,7 +37,7 @@
 // are added by the epilogue, row by row of their own.
 #pragma once
 
-#include "tg_block.h"
+#include "tg_adapter.cuh"
 #include "tg_kernel.cuh"
 #include "tg_sync.cuh"
 
@@ -45,8 +45,8 @@ namespace tg {
 
 struct BlockUnit {
     int32_t g, row0, row1, tm, tn;
-    int32_t k_blocks;      // of the tile
-    int32_t kb0, kb1;      // this worker's of them
+    int32_t kb0, kb1;      // this worker's k-blocks of the tile (ADAPT: of X W)
+    int32_t e0, e1;        // ADAPT: its blocks of u B, once known (ext_range)
     int32_t part, nparts, tile;
 };
 
@@ -96,7 +96,7 @@ __device__ __forceinline__ void block_walk_begin(const BlockParams &p, BlockWalk
 // Item t of the list, where t never falls from call to call; false past the
 // end.  A group's first shares of all its tiles come first: they read the same
 // rows.
-template <int MODE, int BN>
+template <int BN>
 __device__ __forceinline__ bool block_walk_to(const BlockParams &p, int64_t t64, BlockWalk &w, BlockUnit &u)
 {
     if (t64 > INT32_MAX) return false;
@@ -125,11 +125,19 @@ __device__ __forceinline__ bool block_walk_to(const BlockParams &p, int64_t t64,
     const int32_t in = r % strip, rows = min(tiles_m - first, p.group_m);
     u.tm = first + in % rows;
     u.tn = in / rows;
-    u.k_blocks = p.k_blocks;
-    if (MODE == BLOCK_ADAPT) u.k_blocks += __ldcg(p.tab.blocks + u.tm + 1) - __ldcg(p.tab.blocks + u.tm);
-    u.kb0 = static_cast<int32_t>(static_cast<int64_t>(u.part) * u.k_blocks / u.nparts);
-    u.kb1 = static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * u.k_blocks / u.nparts);
+    u.kb0 = static_cast<int32_t>(static_cast<int64_t>(u.part) * p.k_blocks / u.nparts);
+    u.kb1 = static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * p.k_blocks / u.nparts);
+    u.e0 = u.e1 = 0;
     return true;
+}
+
+// ADAPT: this worker's blocks of u B; waits for the kernel that wrote the tables.
+__device__ __forceinline__ void ext_range(const BlockParams &p, BlockUnit &u)
+{
+    ptx::griddep_wait();
+    const int32_t n = adapter_blocks(__ldcg(p.tab.count + u.tm), p.Rp);
+    u.e0 = static_cast<int32_t>(static_cast<int64_t>(u.part) * n / u.nparts);
+    u.e1 = static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * n / u.nparts);
 }
 
 // The MMA's N for a tile: its rows rounded up to 32 (16 a CTA of a pair).
@@ -139,63 +147,134 @@ __device__ __forceinline__ int32_t block_rows_n(const BlockUnit &u)
     return min(BN, (u.row1 - u.row0 - u.tm * BN + 31) / 32 * 32);
 }
 
-// act(g) and its slope.
+// 1 / (1 + exp(-g)) by the fast exponential and reciprocal (a few units off:
+// far below a bf16 rounding of what it goes into).
+__device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+// act(g) and its slope.  tanh(y) = 2 / (1 + exp(-2 y)) - 1.
 template <int ACT>
 __device__ __forceinline__ void act_slope(float g, float &a, float &d)
 {
     if (ACT == 1) {
-        a = fmaxf(g, 0.0f);
+        a = g < 0.0f ? 0.0f : g;  // (NaN stays NaN)
         d = g > 0.0f ? 1.0f : 0.0f;
-    } else if (ACT == 2) {  // gelu, tanh form
+    } else if (ACT == 2) {  // gelu, tanh form: s = (1 + tanh(c (g + 0.044715 g^3))) / 2
         const float c = 0.7978845608028654f, g2 = g * g;
-        const float t = tanhf(c * (g + 0.044715f * g2 * g));
-        a = 0.5f * g * (1.0f + t);
-        d = 0.5f * (1.0f + t) + 0.5f * g * (1.0f - t * t) * c * (1.0f + 3.0f * 0.044715f * g2);
-    } else if (ACT == 3) {  // silu
-        const float s = 1.0f / (1.0f + expf(-g));
+        const float s = fast_sigmoid(2.0f * c * g * (1.0f + 0.044715f * g2));
         a = g * s;
-        d = s * (1.0f + g * (1.0f - s));
+        d = s + 2.0f * a * (1.0f - s) * c * (1.0f + 3.0f * 0.044715f * g2);
+    } else if (ACT == 3) {  // silu
+        const float s = fast_sigmoid(g);
+        a = g * s;
+        d = s + a * (1.0f - s);
     } else {
         a = g;
         d = 1.0f;
     }
 }
 
-// 16 of act(gate) * up.  One unrolled loop an activation behind one branch.
-template <int ACT>
-__device__ __forceinline__ void gated16(const uint32_t (&g)[16], const uint32_t (&u)[16], uint32_t (&h)[16])
+// An epilogue warp's 32 features x 32 rows of the accumulator come as
+// fragments (tcgen05.ld 16x256b): lane t holds, as v[16 half + 4 oct + 2 f8 + e],
+// feature 16 half + 8 f8 + t / 4 and row 8 oct + 2 (t % 4) + e.  Two
+// neighbouring rows of a feature packed to bf16 are a fragment of an 8 x 8
+// matrix that stmatrix (ldmatrix) transposes into (out of) the boxes' rows of
+// features: 4 instructions a box for a warp, where an element a lane takes 32.
+__device__ __forceinline__ int frag_feature(int i, int lane) { return (i >> 4) * 16 + ((i >> 1) & 1) * 8 + (lane >> 2); }
+__device__ __forceinline__ int frag_row(int i, int lane) { return ((i >> 2) & 3) * 8 + (lane & 3) * 2 + (i & 1); }
+
+__device__ __forceinline__ void load_fragments(uint32_t taddr, uint32_t (&v)[32])
 {
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-        h[j] = __float_as_uint(activation(__uint_as_float(g[j]), ACT) * __uint_as_float(u[j]));
+    for (int h = 0; h < 2; ++h)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(v[16 * h]), "=r"(v[16 * h + 1]), "=r"(v[16 * h + 2]), "=r"(v[16 * h + 3]), "=r"(v[16 * h + 4]),
+              "=r"(v[16 * h + 5]), "=r"(v[16 * h + 6]), "=r"(v[16 * h + 7]), "=r"(v[16 * h + 8]), "=r"(v[16 * h + 9]),
+              "=r"(v[16 * h + 10]), "=r"(v[16 * h + 11]), "=r"(v[16 * h + 12]), "=r"(v[16 * h + 13]),
+              "=r"(v[16 * h + 14]), "=r"(v[16 * h + 15])
+            : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16))
+            : "memory");
 }
 
-// GRAD's 32 rows: dh and z (gate in the low half) -> dZ's two halves, packed
-// the same way, and H.
+// Four 8 x 8 matrices of 16 bits, transposed; a lane's address is that of row
+// lane % 8 of matrix lane / 8.
+__device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// GATED: 16 values of act(gate) * up, as fragments of 16 rows packed to bf16.
 template <int ACT>
-__device__ __forceinline__ void gated_grad32(const uint32_t (&dh)[32], const uint32_t (&z)[32], uint32_t (&dz)[32], uint32_t (&h)[16])
+__device__ __forceinline__ void gated_values(const uint32_t (&g)[16], const uint32_t (&u)[16], uint32_t (&h)[8])
 {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-        float hv[2];
+    for (int i = 0; i < 16; i += 2) {
+        float a0, a1, d;
+        act_slope<ACT>(__uint_as_float(g[i]), a0, d);
+        act_slope<ACT>(__uint_as_float(g[i + 1]), a1, d);
+        h[i / 2] = pack_bf16x2(__float_as_uint(a0 * __uint_as_float(u[i])), __float_as_uint(a1 * __uint_as_float(u[i + 1])));
+    }
+}
+
+// GRAD: two rows of a feature: dh and packed z -> packed dZ (in z's place) and H.
+template <int ACT>
+__device__ __forceinline__ uint32_t gated_grad_pair(uint32_t dh0, uint32_t dh1, uint32_t &zg, uint32_t &zu)
+{
+    float dg[2], du[2], h[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float g = __uint_as_float(z[j + e] << 16), u = __uint_as_float(z[j + e] & 0xffff0000u);
-            const float d = __uint_as_float(dh[j + e]);
-            float a, slope;
-            act_slope<ACT>(g, a, slope);
-            dz[j + e] = pack_bf16x2(__float_as_uint(d * u * slope), __float_as_uint(d * a));
-            hv[e] = a * u;
+    for (int e = 0; e < 2; ++e) {
+        const float g = __uint_as_float(e ? zg & 0xffff0000u : zg << 16), u = __uint_as_float(e ? zu & 0xffff0000u : zu << 16);
+        const float dh = __uint_as_float(e ? dh1 : dh0);
+        float a, d;
+        act_slope<ACT>(g, a, d);
+        dg[e] = dh * u * d;
+        du[e] = dh * a;
+        h[e] = a * u;
+    }
+    zg = pack_bf16x2(__float_as_uint(dg[0]), __float_as_uint(dg[1]));
+    zu = pack_bf16x2(__float_as_uint(du[0]), __float_as_uint(du[1]));
+    return pack_bf16x2(__float_as_uint(h[0]), __float_as_uint(h[1]));
+}
+
+// GRAD: one box of 32 rows (addr: this lane's matrix row of its gate half,
+// up_off bytes before that of the up half).
+template <int ACT>
+__device__ __forceinline__ void gated_grad_box(uint32_t addr, uint32_t up_off, const uint32_t (&v)[32], uint32_t (&h)[16])
+{
+#pragma unroll
+    for (int oct = 0; oct < 4; ++oct) {
+        uint32_t zg[4], zu[4];
+        ldmatrix_trans(addr + oct * 1024u, zg);
+        ldmatrix_trans(addr + up_off + oct * 1024u, zu);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const int i = (f >> 1) * 16 + oct * 4 + (f & 1) * 2;
+            h[oct * 4 + f] = gated_grad_pair<ACT>(v[i], v[i + 1], zg[f], zu[f]);
         }
-        h[j / 2] = pack_bf16x2(__float_as_uint(hv[0]), __float_as_uint(hv[1]));
+        stmatrix_trans(addr + oct * 1024u, zg[0], zg[1], zg[2], zg[3]);
+        stmatrix_trans(addr + up_off + oct * 1024u, zu[0], zu[1], zu[2], zu[3]);
     }
 }
 
 template <int MODE, int BN, int STAGES, bool PAIR>
 __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                 const __grid_constant__ CUtensorMap tmV,  // GATED: the up half of W; ADAPT: B
-                 const __grid_constant__ CUtensorMap tmE,  // ADAPT: u's parts
+                 const __grid_constant__ CUtensorMap tmV,  // GATED: the up half of W; GRAD: of Z; ADAPT: B
+                 const __grid_constant__ CUtensorMap tmE,  // GRAD: the gate half of Z; ADAPT: u's parts
                  const __grid_constant__ CUtensorMap tmO,  // H, Y
                  const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU,  // halves of Z, dZ
                  const BlockParams p)
@@ -207,10 +286,9 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     constexpr uint32_t EPI_BOX_BYTES = 4096;                  // 32 rows of 128 bytes
     constexpr uint32_t EPI_WARPS_TOTAL = (PAIR ? 2 : 1) * BLOCK_EPI_WARPS;
     constexpr int EPI_ROWS = 32, EPI_ROW_BYTES = 128;
-    static_assert(BLOCK_EPI_WARPS * EPI_BOX_BYTES <= G::EPI_BYTES, "epilogue boxes");
     static_assert(MODE != BLOCK_SHRINK || !PAIR, "adapters' first products take one-CTA tiles");
     constexpr uint32_t TMEM_ALLOC = static_cast<uint32_t>(G::TMEM_COLS);
-    static_assert(8 * (2 * STAGES + 6) + 20 <= G::BAR_BYTES, "barrier area");
+    static_assert(8 * (2 * STAGES + 14) + 20 <= G::BAR_BYTES, "barrier area");
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -219,13 +297,14 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     const uint32_t sA = raw + pad;
     const uint32_t sB = sA + STAGES * G::A_STAGE;
     const uint32_t sE = sB + STAGES * G::B_STAGE;
-    uint8_t *bar_area = smem + STAGES * G::STAGE + G::EPI_BYTES;
+    uint8_t *bar_area = smem + STAGES * G::STAGE + block_epi_bytes(MODE);
     const uint32_t bar0 = ptx::smem_addr(bar_area);
     // barrier k at bar0 + 8k: [0, S) full, [S, 2S) empty, 2S+{0,1} tfull,
-    // 2S+{2,3} tempty, 2S+4 mma-done, 2S+5 never completed
+    // 2S+{2,3} tempty, 2S+4 mma-done, 2S+5 never completed; GRAD: from 2S+6
+    // two for each team of epilogue warps: z landed in the boxes
     const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
     const uint32_t stall_bar = bar0 + 8u * (2 * STAGES + 5);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (2 * STAGES + 6));
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (2 * STAGES + 14));
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
     volatile int32_t *last_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 2);
     uint32_t *issued_slot = tmem_slot + 3;  // k-blocks this CTA's producer loaded
@@ -233,6 +312,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
     auto tfull_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
     auto tempty_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
+    [[maybe_unused]] auto z_bar = [&](uint32_t duo, uint32_t b) { return bar0 + 8u * (2 * STAGES + 6 + 2 * duo + b); };
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = static_cast<int>(threadIdx.x & 31);
@@ -252,6 +332,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         }
         ptx::mbar_init(done_bar, 1);
         ptx::mbar_init(stall_bar, 1);
+        for (uint32_t i = 0; MODE == BLOCK_GRAD && i < 8; ++i) ptx::mbar_init(z_bar(0, i), 1);
         *abort_flag = 0;
         *issued_slot = 0;
         ptx::fence_barrier_init();
@@ -282,7 +363,12 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     if constexpr (PAIR) ptx::cluster_sync_all();
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    ptx::griddep_wait();
+    // ADAPT starts on the shared weights, and SHRINK on its products, while the
+    // call's kernel before it runs: what that one writes is read behind a
+    // griddep_wait of its own.  (The kernels before that one have completed: it
+    // waited for them, or was launched behind them.)
+    if (MODE == BLOCK_SHRINK) ptx::griddep_launch_dependents();
+    if (MODE == BLOCK_GATED || MODE == BLOCK_GRAD) ptx::griddep_wait();
     const uint32_t peer_abort =
         PAIR ? ptx::map_to_cta(ptx::smem_addr(const_cast<int32_t *>(abort_flag)), rank ^ 1u) : 0u;
     const Watchdog wd{p.timeout_ns, abort_flag, p.err, peer_abort};
@@ -296,7 +382,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         uint32_t it = 0;
         bool ok = true;
         const uint32_t full0 = PAIR ? ptx::map_to_cta(full_bar(0), 0u) : full_bar(0);
-        for (int64_t t = worker; ok && block_walk_to<MODE, BN>(p, t, walk, w); t += n_workers) {
+        for (int64_t t = worker; ok && block_walk_to<BN>(p, t, walk, w); t += n_workers) {
             if (!dbg_ok(w.g >= 0 && w.g < p.groups && w.row0 >= 0 && w.row0 <= w.row1 && w.row1 <= p.S && w.tm >= 0 &&
                             w.tn >= 0 && w.tn < p.tiles_n,
                         CHK_UNIT, wd))
@@ -312,16 +398,19 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 if (from + lane < ad_count) {
                     ad = __ldcg(p.tab.ids + ad_first + from + lane);
                     int32_t bad = 0;
+#pragma unroll
                     for (int i = 0; i < ADAPT_FLAGS; ++i) bad |= __ldcg(p.tab.flags + ad * ADAPT_FLAGS + i);
                     if (bad) ad = -1;
                 }
             };
-            if (MODE == BLOCK_ADAPT && w.kb1 > p.k_blocks) {
-                ad_first = __ldcg(p.tab.first + w.tm);
-                ad_count = __ldcg(p.tab.count + w.tm);
-                ext_row = __ldcg(p.tab.blocks + w.tm) * BN + n_half;
-            }
-            for (int32_t kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+            for (int32_t i = w.kb0; i < w.kb1 + w.e1 - w.e0 || (MODE == BLOCK_ADAPT && i == w.kb1); ++i, ++it) {
+                if (MODE == BLOCK_ADAPT && i == w.kb1) {
+                    ext_range(p, w);
+                    if (w.e0 == w.e1) break;
+                    ad_first = __ldcg(p.tab.first + w.tm);
+                    ad_count = __ldcg(p.tab.count + w.tm);
+                    ext_row = __ldcg(p.tab.blocks + w.tm) * BN + n_half;
+                }
                 const uint32_t s = it % STAGES;
                 const uint32_t ph = (it / STAGES) & 1u;
                 const int r = wait_bounded_warp(empty_bar(s), ph ^ 1u, wd);
@@ -346,36 +435,34 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         ptx::mbar_arrive_expect_tx(full_bar(s), G::STAGE);
                     }
                 };
-                if (MODE == BLOCK_ADAPT && kb >= p.k_blocks) {
-                    const int32_t e = kb - p.k_blocks;
+                if (MODE == BLOCK_ADAPT && i >= w.kb1) {
+                    const int32_t e = w.e0 + i - w.kb1;
                     // the block's first adapter, and for R > 32 the rows of B
                     const int32_t per = p.Rp <= 32 ? 32 / p.Rp : 1;
                     const int32_t bpa = p.Rp <= 32 ? 1 : p.Rp / 32;
                     const int32_t a0 = p.Rp <= 32 ? e * per : e / bpa;
                     const int32_t chunk = p.Rp <= 32 ? 0 : (e % bpa) / 2 * 64;
-                    if (kb == w.kb0 || kb == p.k_blocks || a0 + per > ad0 + 32) adapters(a0);
+                    if (i == w.kb1 || a0 + per > ad0 + 32) adapters(a0);
                     int32_t ids[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ids[i] = __shfl_sync(0xffffffffu, ad, min(31, a0 - ad0 + i));
+                    for (int k = 0; k < 4; ++k) ids[k] = __shfl_sync(0xffffffffu, ad, min(31, a0 - ad0 + k));
                     if (ptx::elect_one()) {
                         expect();
                         const int32_t rows = min(p.Rp, 64);
                         const int32_t subs = 64 / rows;
-                        for (int i = 0; i < subs; ++i) {
-                            const int k = p.Rp <= 32 ? i >> 1 : 0;
-                            int32_t id = ids[0];
-                            if (k == 1) id = ids[1];
-                            if (k == 2) id = ids[2];
-                            if (k == 3) id = ids[3];
+                        for (int j = 0; j < subs; ++j) {
+                            const int k = p.Rp <= 32 ? j >> 1 : 0;
+                            const int32_t id = k == 0 ? ids[0] : k == 1 ? ids[1] : k == 2 ? ids[2] : ids[3];
                             // rows past R read as zeros
                             const int32_t r0 = id < 0 ? p.Rp : chunk, z = p.b_shared ? 0 : max(id, 0);
-                            const uint32_t dst = a_dst + static_cast<uint32_t>(i * rows) * 128u;
+                            const uint32_t dst = a_dst + static_cast<uint32_t>(j * rows) * 128u;
                             load(dst, &tmV, m0, r0, z);
                             load(dst + BOX_BYTES, &tmV, m0 + 64, r0, z);
                         }
                         load(b_dst, &tmE, 0, ext_row + e * BN, 0);
                     }
                 } else if (ptx::elect_one()) {
+                    const int32_t kb = i;
                     expect();
                     const int32_t z = p.w_shared ? 0 : w.g;
                     if constexpr (MODE == BLOCK_GATED) {
@@ -417,8 +504,12 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             const uint64_t desc_k = smem_desc_sw128(0, 16, 1024);
             uint32_t it = 0, n = 0;
             bool ok = true;
-            for (int64_t t = worker; ok && block_walk_to<MODE, BN>(p, t, walk, w); t += n_workers) {
-                if (w.kb0 == w.kb1) continue;  // the epilogue writes an empty sum itself
+            for (int64_t t = worker; ok && block_walk_to<BN>(p, t, walk, w); t += n_workers) {
+                if (w.kb0 == w.kb1) {  // the epilogue writes an empty sum itself
+                    if (MODE != BLOCK_ADAPT) continue;
+                    ext_range(p, w);
+                    if (w.e0 == w.e1) continue;
+                }
                 const uint32_t buf = n & 1u;
                 const uint32_t tph = (n >> 1) & 1u;
                 ++n;
@@ -430,7 +521,11 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + buf * BN;
                 const uint32_t n_field = static_cast<uint32_t>(block_rows_n<BN>(w)) >> 3 << 17;
-                for (int32_t kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                for (int32_t kb = w.kb0; kb < w.kb1 + w.e1 - w.e0 || (MODE == BLOCK_ADAPT && kb == w.kb1); ++kb, ++it) {
+                    if (MODE == BLOCK_ADAPT && kb == w.kb1) {
+                        ext_range(p, w);
+                        if (w.e0 == w.e1) break;
+                    }
                     const uint32_t s = it % STAGES;
                     const uint32_t ph = (it / STAGES) & 1u;
                     r = wait_bounded_warp(full_bar(s), ph, wd);
@@ -441,7 +536,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     }
                     ptx::tc_fence_after();
                     if (ptx::elect_one()) {
-                        const bool mn = !p.w_k || (MODE == BLOCK_ADAPT && kb >= p.k_blocks);
+                        const bool mn = !p.w_k || (MODE == BLOCK_ADAPT && kb >= w.kb1);
                         const uint32_t idesc = ((mn ? idesc_mn : idesc_k) & ~(0x3Fu << 17)) | n_field;
                         const uint64_t a_desc0 = mn ? desc_mn : desc_k;
                         const uint32_t a_step = mn ? 2048u : 32u;
@@ -494,33 +589,43 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         const int team = MODE == BLOCK_GATED ? 4 : MODE == BLOCK_GRAD || p.out_bf16 ? 2 : 1;
         const int sub = q & 1;              // which half of a box row is this warp's
         const int member = MODE == BLOCK_GATED ? q : team == 2 ? sub : 0;
-        const uint32_t team_id = 2u + (MODE == BLOCK_GATED ? turn : (warp - 2) >> 1);
+        const uint32_t duo = static_cast<uint32_t>((warp - 2) >> 1);
+        const uint32_t team_id = 2u + (MODE == BLOCK_GATED ? static_cast<uint32_t>(turn) : duo);
         auto team_sync = [&]() {
             if (team == 1)
                 __syncwarp();
             else
                 ptx::named_barrier_sync(team_id, 32 * team);
         };
-        const bool issues = member == 0 && lane == 0;  // all the team's bulk stores
-        const uint32_t area = sE + (MODE == BLOCK_GATED ? static_cast<uint32_t>(turn) * 4u * EPI_BOX_BYTES
-                                    : team == 2         ? static_cast<uint32_t>((warp - 2) >> 1) * 2u * EPI_BOX_BYTES
-                                                        : static_cast<uint32_t>(warp - 2) * EPI_BOX_BYTES);
-        // Address of 16-byte unit u of row r of the box at `box`.
+        const bool issues = member == 0 && lane == 0;  // all the team's bulk copies
+        const uint32_t area = sE + (MODE == BLOCK_GATED  ? static_cast<uint32_t>(turn) * 4u * EPI_BOX_BYTES
+                                    : MODE == BLOCK_GRAD ? duo * 4u * EPI_BOX_BYTES
+                                    : team == 2          ? duo * 2u * EPI_BOX_BYTES
+                                                         : static_cast<uint32_t>(warp - 2) * EPI_BOX_BYTES);
+        // Address of 16-byte unit u of row r of the box at `box`, and this
+        // lane's matrix row for fragments of the warp's half of a box (rows
+        // 8 oct + lane % 8: 1024 bytes an oct further).
         auto unit_at = [&](uint32_t box, int r, int u) { return box + r * EPI_ROW_BYTES + ((u ^ (r & 7)) << 4); };
-        // This lane's bf16 of 32 rows of a box (r: first row).
-        auto put16 = [&](uint32_t box, int r, uint16_t v) {
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(unit_at(box, r, sub * 4 + (lane >> 3)) + (lane & 7) * 2), "h"(v) : "memory");
+        const uint32_t frag_at = static_cast<uint32_t>((lane & 7) * EPI_ROW_BYTES + (((sub * 4 + (lane >> 3)) ^ (lane & 7)) << 4));
+        // 32 rows of the warp's 32 features -> its half of a bf16 box.
+        auto put_box = [&](uint32_t box, const uint32_t (&v)[32]) {
+#pragma unroll
+            for (int oct = 0; oct < 4; ++oct)
+                stmatrix_trans(box + frag_at + oct * 1024u, pack_bf16x2(v[4 * oct], v[4 * oct + 1]),
+                               pack_bf16x2(v[4 * oct + 2], v[4 * oct + 3]), pack_bf16x2(v[16 + 4 * oct], v[17 + 4 * oct]),
+                               pack_bf16x2(v[18 + 4 * oct], v[19 + 4 * oct]));
         };
-        auto bf16_bits = [](uint32_t v) { return __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v))); };
 
         // The box -> rows row0 .. of an output (those before `limit`), columns
         // col0 ..  `whole`: a TMA store may write all of its rows (the tensor's
         // own end clips a box, a group's end does not).  Called by the team
-        // between team_syncs; true where a bulk store was issued.
+        // behind a team_sync.
         auto flush = [&](uint32_t box, const CUtensorMap *map, const BlockOut &o, int size, int32_t row0, int32_t limit, bool whole,
                          int32_t col0) {
             const int32_t cols = min(EPI_ROW_BYTES / size, p.N - col0);
             if (cols <= 0) return;
+            // (a box that the row's end cuts off its 16 bytes goes out plainly:
+            // a TMA store would write on to the next 16-byte boundary)
             const bool full = cols == EPI_ROW_BYTES / size || p.N % (16 / size) == 0;
             if (o.tma && whole && full) {
                 if (issues) ptx::tma_store_3d(map, box, col0, row0, 0);
@@ -533,10 +638,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 const int per = 16 / size, u = lane & 7, n = min(per, cols - u * per);
                 for (int r = member * 4 + (lane >> 3); r < nrows; r += 4 * team) {
                     uint32_t v[4];
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                                 : "r"(unit_at(box, r, u))
-                                 : "memory");
+                    ld_shared_v4(unit_at(box, r, u), v);
                     uint8_t *d = dst + r * pitch + u * 16;
                     if (n == per) {
                         *reinterpret_cast<uint4 *>(d) = make_uint4(v[0], v[1], v[2], v[3]);
@@ -574,6 +676,32 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     ptx::mbar_arrive(tempty_bar(buf));
             }
         };
+        // SHRINK stores 32 features of a row at a time, the others fragments.
+        auto load_piece = [&](uint32_t taddr, uint32_t (&v)[32]) {
+            if constexpr (MODE == BLOCK_SHRINK)
+                ptx::tmem_load_32cols_async(taddr, v);
+            else
+                load_fragments(taddr, v);
+        };
+
+        // SHRINK: where the parts of row `row` of the group at `place` stand for
+        // ADAPT, in units of 8 values; and zeros in the other adapters' columns
+        // of a tile's rows.
+        [[maybe_unused]] int32_t place = 0;
+        [[maybe_unused]] auto wide_row = [&](int32_t row) {
+            const int32_t tile = row / p.wide_bn, in = row % p.wide_bn;
+            return adapter_unit(place - __ldcg(p.tab.first + tile), __ldcg(p.tab.blocks + tile), in, p.wide_bn, p.Rp);
+        };
+        auto zero_others = [&](const BlockUnit &w, int32_t row_tile, int32_t limit) {
+            if constexpr (MODE == BLOCK_SHRINK) {
+                if (w.tn != 0) return;
+                for (int32_t row = row_tile + (warp - 2); row < limit; row += BLOCK_EPI_WARPS) {
+                    const int32_t tile = row / p.wide_bn;
+                    zero_columns(p, row % p.wide_bn, __ldcg(p.tab.blocks + tile), __ldcg(p.tab.count + tile),
+                                 place - __ldcg(p.tab.first + tile), lane);
+                }
+            }
+        };
 
         bool ok = true;
         if (p.debug_stall) {  // watchdog self-test: a barrier that nothing completes
@@ -581,9 +709,12 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
             ok = agree(r == WAIT_OK, 1, 32 * BLOCK_EPI_WARPS);
         }
+        if (MODE == BLOCK_SHRINK || MODE == BLOCK_ADAPT) ptx::griddep_wait();  // the tables
         uint32_t n = 0;
-        uint32_t flip = 0;  // which of two boxes is next
-        for (int64_t t = worker; ok && block_walk_to<MODE, BN>(p, t, walk, w); t += n_workers) {
+        uint32_t flip = 0;     // which of two boxes (GRAD: pairs of them) is next
+        // GRAD: bit b: parity of z_bar(b)'s next phase; a copy is on its way there
+        uint32_t z_phase = 0, z_out = 0;
+        for (int64_t t = worker; ok && block_walk_to<BN>(p, t, walk, w); t += n_workers) {
             const int32_t f0 = w.tn * TILE_F + static_cast<int32_t>(rank) * LANES;  // the CTA's first feature
             const int32_t f_warp = f0 + 32 * (MODE == BLOCK_GATED ? sub : q);       // the warp's
             const int32_t f_box = MODE == BLOCK_GATED ? f0 : team == 2 ? f_warp - 32 * sub : f_warp;
@@ -592,24 +723,43 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             const int32_t pieces = (limit - row_tile + 31) / 32;
             const bool lanes_in = MODE == BLOCK_SHRINK ? f_warp < p.Rp : f_box < p.N;  // uniform in a team
 
-            // GRAD: 32 rows of z, gate in the low half; rows and features past
-            // the end read the last one's.
-            uint32_t z[32];
-            auto load_z = [&](int c) {
+            if constexpr (MODE == BLOCK_SHRINK) place = __ldcg(p.tab.rank + w.g);
+
+            // GRAD: z of piece c into the pair of boxes `b`, gate and up half.
+            // By TMA where its rows are on 16 bytes; else the team
+            // copies its halves (a warp reads back what it wrote alone).
+            auto load_z = [&](int c, uint32_t b) {
                 if constexpr (MODE == BLOCK_GRAD) {
-                    const uint16_t *at = p.z + min(f_warp + lane, p.N - 1);
+                    if (c >= pieces) return;
+                    const uint32_t box = area + b * 2u * EPI_BOX_BYTES;
                     const int32_t r0 = row_tile + 32 * c;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const uint16_t *row = at + static_cast<int64_t>(min(r0 + j, limit - 1)) * p.ldz;
-                        z[j] = static_cast<uint32_t>(row[0]) | static_cast<uint32_t>(row[p.N]) << 16;
+                    if (issues) ptx::bulk_wait_group_read<0>();  // the boxes' last stores
+                    if (p.z_tma) {
+                        // (the team's reads of them ended before the piece's first barrier)
+                        if (issues) {
+                            ptx::mbar_arrive_expect_tx(z_bar(duo, b), 2u * EPI_BOX_BYTES);
+                            ptx::tma_load_3d(box, &tmE, z_bar(duo, b), f_box, r0, 0);
+                            ptx::tma_load_3d(box + EPI_BOX_BYTES, &tmV, z_bar(duo, b), f_box, r0, 0);
+                        }
+                        z_out |= 1u << b;
+                        return;
                     }
+                    team_sync();
+                    const int32_t f = f_warp + lane, rows = limit - r0;
+                    const uint16_t *at = p.z + static_cast<int64_t>(r0) * p.ldz + min(f, p.N - 1);
+#pragma unroll 8
+                    for (int j = 0; j < 32; ++j, at += j < rows ? p.ldz : 0) {
+                        const uint32_t to = unit_at(box, j, sub * 4 + (lane >> 3)) + (lane & 7) * 2;
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(at[0]) : "memory");
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + EPI_BOX_BYTES), "h"(at[p.N]) : "memory");
+                    }
+                    __syncwarp();
                 }
             };
 
-            // 32 rows of the accumulator (v: row j of this lane's feature) ->
-            // the outputs.  `next` is called once v is used up.
-            auto piece = [&](int c, uint32_t (&v)[32], auto &&next) {
+            // 32 rows of the accumulator -> the outputs.  `next` is called once
+            // v is used up.  false: a wait ran out (GRAD).
+            auto piece = [&](int c, uint32_t (&v)[32], auto &&next) -> bool {
                 const int32_t row0 = row_tile + 32 * c;
                 [[maybe_unused]] const bool whole = row0 + EPI_ROWS <= limit || limit == p.S;
                 if constexpr (MODE == BLOCK_GATED) {
@@ -628,44 +778,42 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     const uint32_t give = area + static_cast<uint32_t>(q) * 2048u + lane * 16u;
                     const uint32_t take = area + static_cast<uint32_t>(q ^ 2) * 2048u + lane * 16u;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 4; ++k) {  // k: half of the features, oct of the 16 rows
+                        const int lo = (k >> 1) * 16 + (k & 1) * 4, hi = lo + 8;
                         if (is_up)
-                            ptx::st_shared_v4(give + k * 512u, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                            ptx::st_shared_v4(give + k * 512u, v[lo], v[lo + 1], v[lo + 2], v[lo + 3]);
                         else
-                            ptx::st_shared_v4(give + k * 512u, v[16 + 4 * k], v[17 + 4 * k], v[18 + 4 * k], v[19 + 4 * k]);
+                            ptx::st_shared_v4(give + k * 512u, v[hi], v[hi + 1], v[hi + 2], v[hi + 3]);
                     }
                     team_sync();
-                    uint32_t o[16], mine[16], h[16];
+                    uint32_t g[16], u[16], h[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(o[4 * k]), "=r"(o[4 * k + 1]), "=r"(o[4 * k + 2]), "=r"(o[4 * k + 3])
-                                     : "r"(take + k * 512u)
-                                     : "memory");
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t o[4];
+                        ld_shared_v4(take + k * 512u, o);
+                        const int lo = (k >> 1) * 16 + (k & 1) * 4;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) mine[j] = is_up ? v[16 + j] : v[j];
+                        for (int e = 0; e < 4; ++e) {
+                            g[4 * k + e] = is_up ? o[e] : v[lo + e];
+                            u[4 * k + e] = is_up ? v[lo + 8 + e] : o[e];
+                        }
+                    }
                     if (p.gate.p) {
                         team_sync();  // the exchange was read
-                        const uint32_t box = zbox + (is_up ? EPI_BOX_BYTES : 0u);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) put16(box, j, bf16_bits(v[j]));
+                        put_box(zbox + (is_up ? EPI_BOX_BYTES : 0u), v);
                     }
                     next();
-                    uint32_t g[16], u[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        g[j] = is_up ? o[j] : mine[j];
-                        u[j] = is_up ? mine[j] : o[j];
-                    }
                     switch (p.act) {
-                        case 1: gated16<1>(g, u, h); break;
-                        case 2: gated16<2>(g, u, h); break;
-                        case 3: gated16<3>(g, u, h); break;
-                        default: gated16<0>(g, u, h); break;
+                        case 1: gated_values<1>(g, u, h); break;
+                        case 2: gated_values<2>(g, u, h); break;
+                        case 3: gated_values<3>(g, u, h); break;
+                        default: gated_values<0>(g, u, h); break;
                     }
-                    const int j0 = is_up ? 16 : 0;
+                    // h[4 half + 2 oct + f8], octs of this warp's 16 rows
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) put16(hbox, j0 + j, bf16_bits(h[j]));
+                    for (int oct = 0; oct < 2; ++oct)
+                        stmatrix_trans(hbox + frag_at + (is_up ? 2048u : 0u) + oct * 1024u, h[2 * oct], h[2 * oct + 1], h[4 + 2 * oct],
+                                       h[5 + 2 * oct]);
                     ptx::fence_proxy_async_smem();
                     team_sync();
                     flush(hbox, &tmO, p.out0, 2, row0, limit, whole, f_box);
@@ -676,29 +824,43 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     // one group a piece, empty where nothing was issued
                     if (issues) ptx::bulk_commit_group();
                 } else if constexpr (MODE == BLOCK_GRAD) {
-                    uint32_t dz[32], h[16];
+                    const uint32_t b = flip;
+                    flip ^= 1u;
+                    const uint32_t box = area + b * 2u * EPI_BOX_BYTES;
+                    if (p.z_tma) {
+                        const int r = wait_bounded(z_bar(duo, b), (z_phase >> b) & 1u, wd);
+                        if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
+                        if (r == WAIT_OK) {
+                            z_phase ^= 1u << b;
+                            z_out &= ~(1u << b);
+                        }
+                        if (!agree(r == WAIT_OK, team_id, 64)) return false;
+                    }
+                    uint32_t h[16];
                     switch (p.act) {
-                        case 1: gated_grad32<1>(v, z, dz, h); break;
-                        case 2: gated_grad32<2>(v, z, dz, h); break;
-                        case 3: gated_grad32<3>(v, z, dz, h); break;
-                        default: gated_grad32<0>(v, z, dz, h); break;
+                        case 1: gated_grad_box<1>(box + frag_at, EPI_BOX_BYTES, v, h); break;
+                        case 2: gated_grad_box<2>(box + frag_at, EPI_BOX_BYTES, v, h); break;
+                        case 3: gated_grad_box<3>(box + frag_at, EPI_BOX_BYTES, v, h); break;
+                        default: gated_grad_box<0>(box + frag_at, EPI_BOX_BYTES, v, h); break;
                     }
                     next();
-                    auto send = [&](const CUtensorMap *map, const BlockOut &out, auto &&value) {
-                        const uint32_t box = area + flip * EPI_BOX_BYTES;
-                        flip ^= 1u;
-                        if (issues) ptx::bulk_wait_group_read<1>();
+                    load_z(c + 2, b ^ 1u);
+                    ptx::fence_proxy_async_smem();
+                    team_sync();
+                    flush(box, &tmG, p.gate, 2, row0, limit, whole, f_box);
+                    flush(box + EPI_BOX_BYTES, &tmU, p.up, 2, row0, limit, whole, f_box);
+                    if (issues) ptx::bulk_commit_group();
+                    if (p.out0.p) {  // H in the gate half's box
+                        if (issues) ptx::bulk_wait_group_read<0>();
                         team_sync();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) put16(box, j, value(j));
+                        for (int oct = 0; oct < 4; ++oct)
+                            stmatrix_trans(box + frag_at + oct * 1024u, h[4 * oct], h[4 * oct + 1], h[4 * oct + 2], h[4 * oct + 3]);
                         ptx::fence_proxy_async_smem();
                         team_sync();
-                        flush(box, map, out, 2, row0, limit, whole, f_box);
+                        flush(box, &tmO, p.out0, 2, row0, limit, whole, f_box);
                         if (issues) ptx::bulk_commit_group();
-                    };
-                    send(&tmG, p.gate, [&](int j) { return static_cast<uint16_t>(dz[j]); });
-                    send(&tmU, p.up, [&](int j) { return static_cast<uint16_t>(dz[j] >> 16); });
-                    if (p.out0.p) send(&tmO, p.out0, [&](int j) { return static_cast<uint16_t>(h[j >> 1] >> (16 * (j & 1))); });
+                    }
                 } else if constexpr (MODE == BLOCK_ADAPT) {
                     const uint32_t box = area + (team == 2 ? flip * EPI_BOX_BYTES : 0u);
                     flip ^= 1u;
@@ -710,12 +872,13 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     }
                     team_sync();
                     if (team == 2) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) put16(box, j, bf16_bits(v[j]));
+                        put_box(box, v);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(unit_at(box, j, lane >> 2) + (lane & 3) * 4), "r"(v[j]) : "memory");
+                        for (int i = 0; i < 32; ++i) {
+                            const int f = frag_feature(i, lane);
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(unit_at(box, frag_row(i, lane), f >> 2) + (f & 3) * 4), "r"(v[i]) : "memory");
+                        }
                     }
                     next();
                     ptx::fence_proxy_async_smem();
@@ -725,52 +888,29 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 } else {  // SHRINK
                     const float scale = p.scales ? __ldg(p.scales + w.g) : 1.0f;
                     const int32_t r = f_warp + lane;
-                    const int32_t place = __ldcg(p.tab.rank + w.g);
+                    const int32_t mine = row0 + lane < limit ? wide_row(row0 + lane) : 0;  // (lane: row)
+                    // its adapter's columns there, and how far lo lies from hi
+                    const int64_t lo_off = p.Rp <= 32 ? p.Rp : static_cast<int64_t>(p.wide_bn) * 64;
+                    const int32_t in_row = p.Rp <= 32 ? r : r / 64 * 2 * p.wide_bn * 64 + (r & 63);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         const int32_t row = row0 + j;
+                        const int32_t at32 = __shfl_sync(0xffffffffu, mine, j);
                         if (row >= limit || r >= p.Rp) continue;
                         // (columns past R meet zeros, whatever X holds)
                         const float x = r < p.R ? __fmul_rn(scale, __uint_as_float(v[j])) : 0.0f;
-                        const __nv_bfloat16 rounded = __float2bfloat16_rn(x);
-                        // u = hi + lo; hi rounds down where rounding would make an infinity
-                        __nv_bfloat16 hi = rounded;
-                        if (fabsf(x) <= 3.402823466e38f && fabsf(__bfloat162float(hi)) > 3.402823466e38f)
-                            hi = __ushort_as_bfloat16(static_cast<uint16_t>(__float_as_uint(x) >> 16));
-                        const __nv_bfloat16 lo = fabsf(x) <= 3.402823466e38f
-                                                     ? __float2bfloat16_rn(__fsub_rn(x, __bfloat162float(hi)))
-                                                     : __ushort_as_bfloat16(0);
-                        const int32_t tile = row / p.wide_bn, in = row % p.wide_bn;
-                        const int32_t i = place - __ldcg(p.tab.first + tile);
-                        const int32_t per = p.Rp <= 32 ? 32 / p.Rp : 1;
-                        const int64_t blk = __ldcg(p.tab.blocks + tile) + (p.Rp <= 32 ? i / per : i * (p.Rp / 32) + r / 64 * 2);
-                        uint16_t *at = p.wide + (blk * p.wide_bn + in) * 64 + (p.Rp <= 32 ? i % per * 2 * p.Rp + r : r & 63);
+                        __nv_bfloat16 hi, lo;
+                        split_parts(x, hi, lo);
+                        uint16_t *at = p.wide + static_cast<int64_t>(at32) * 8 + in_row;
                         at[0] = __bfloat16_as_ushort(hi);
-                        at[p.Rp <= 32 ? p.Rp : static_cast<int64_t>(p.wide_bn) * 64] = __bfloat16_as_ushort(lo);
+                        at[lo_off] = __bfloat16_as_ushort(lo);
                         if (p.out0.p && r < p.R)
-                            static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = __bfloat16_as_ushort(rounded);
+                            static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] =
+                                __bfloat16_as_ushort(__float2bfloat16_rn(x));
                     }
                     next();
                 }
-            };
-            // SHRINK: zeros in the other adapters' columns of this tile's rows.
-            auto zero_others = [&]() {
-                if constexpr (MODE == BLOCK_SHRINK) {
-                    if (w.tn != 0) return;
-                    const int32_t place = __ldcg(p.tab.rank + w.g);
-                    for (int32_t row = row_tile + (warp - 2); row < limit; row += BLOCK_EPI_WARPS) {
-                        const int32_t tile = row / p.wide_bn, in = row % p.wide_bn;
-                        const int32_t blk0 = __ldcg(p.tab.blocks + tile), nb = __ldcg(p.tab.blocks + tile + 1) - blk0;
-                        const int32_t i = place - __ldcg(p.tab.first + tile);
-                        // its own 16-byte units of the tile's blocks: [own, own_end)
-                        const int32_t units = adapter_blocks(1, p.Rp) == 1 ? p.Rp / 4 : p.Rp / 32 * 8;
-                        const int32_t own = i * units, own_end = own + units;
-                        for (int32_t k = lane; k < nb * 8; k += 32)
-                            if (k < own || k >= own_end)
-                                *reinterpret_cast<uint4 *>(p.wide + (static_cast<int64_t>(blk0 + (k >> 3)) * p.wide_bn + in) * 64 + (k & 7) * 8) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
+                return true;
             };
             // ADAPT: adds the adapters whose B holds an infinity or NaN to
             // their own rows.
@@ -790,7 +930,6 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     if (!flagged) return;
                     const int32_t first = __ldcg(p.tab.first + w.tm), most = __ldcg(p.tab.count + w.tm);
                     const int32_t blk0 = __ldcg(p.tab.blocks + w.tm);
-                    const int32_t f = f_warp + lane;
                     const int32_t r0 = row_tile + 32 * c;
                     const int32_t per = p.Rp <= 32 ? 32 / p.Rp : 1;
                     for (int32_t i = 0; i < most; ++i) {
@@ -800,11 +939,11 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         const int32_t lo = max(__ldcg(p.tab.lo + first + i), r0), hi = min(__ldcg(p.tab.hi + first + i), min(limit, r0 + 32));
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            const int32_t row = r0 + j;
-                            if (row < lo || row >= hi) continue;
+                            const int32_t row = r0 + frag_row(j, lane), f = f_warp + frag_feature(j, lane);
+                            if (row < lo || row >= hi || f >= p.N) continue;
                             float sum = 0.0f;
 #pragma unroll 1
-                            for (int32_t r = 0; f < p.N && r < p.R; ++r) {
+                            for (int32_t r = 0; r < p.R; ++r) {
                                 const int64_t blk = blk0 + (p.Rp <= 32 ? i / per : i * (p.Rp / 32) + r / 64 * 2);
                                 const uint16_t *at = p.wide + (blk * BN + (row - row_tile)) * 64 + (p.Rp <= 32 ? i % per * 2 * p.Rp + r : r & 63);
                                 const float u = __uint_as_float(static_cast<uint32_t>(at[0]) << 16) +
@@ -819,18 +958,20 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             };
 
             uint32_t v[32];
-            if (w.k_blocks == 0) {  // the empty sum
-                for (int c = turn; lanes_in && c < pieces; c += 2) {
+            if (MODE == BLOCK_ADAPT) ext_range(p, w);
+            if (w.kb0 == w.kb1 && w.e0 == w.e1) {  // the empty sum
+                if (lanes_in) load_z(turn, flip);
+                for (int c = turn; ok && lanes_in && c < pieces; c += 2) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0u;
-                    load_z(c);
                     add_flagged(c, v);
-                    piece(c, v, [] {});
+                    ok = piece(c, v, [] {});
                 }
-                zero_others();
+                if (!ok) break;
+                zero_others(w, row_tile, limit);
                 continue;
             }
-            if (lanes_in && turn < pieces && w.nparts == 1) load_z(turn);
+            if (lanes_in && w.nparts == 1) load_z(turn, flip);
             const uint32_t buf = n & 1u;
             const uint32_t tph = (n >> 1) & 1u;
             ++n;
@@ -845,14 +986,15 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             ptx::tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
             if (w.nparts > 1) {
-                // The partial tile -> scratch [piece][column quad][lane][4
-                // columns]: 16 coalesced bytes a thread.
+                // The partial tile -> scratch [piece][value quad][lane][4
+                // values]: 16 coalesced bytes a thread.
                 constexpr int64_t PART4 = BM * BN / 4;  // float4s a part
                 const int64_t half = static_cast<int64_t>(w.tile) * (PAIR ? 2 : 1) + rank;
                 float4 *parts = reinterpret_cast<float4 *>(p.partials) + half * p.splits * PART4 + q * 32 + lane;
                 float4 *mine = parts + w.part * PART4;
                 for (int c = turn; lanes_in && c < pieces; c += 2) {
-                    ptx::tmem_load_32cols(taddr + c * 32, v);
+                    load_piece(taddr + c * 32, v);
+                    ptx::tmem_wait_ld(v);
 #pragma unroll
                     for (int j4 = 0; j4 < 8; ++j4)
                         __stcg(mine + (c * 8 + j4) * BM, make_float4(__uint_as_float(v[4 * j4]), __uint_as_float(v[4 * j4 + 1]),
@@ -869,8 +1011,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
                 if (*last_flag) {
                     __threadfence();
-                    for (int c = turn; lanes_in && c < pieces; c += 2) {
-                        load_z(c);
+                    if (lanes_in) load_z(turn, flip);
+                    for (int c = turn; ok && lanes_in && c < pieces; c += 2) {
                         float4 acc[8];
 #pragma unroll
                         for (int j4 = 0; j4 < 8; ++j4) acc[j4] = __ldcg(parts + (c * 8 + j4) * BM);
@@ -893,32 +1035,31 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                             v[4 * j4 + 3] = __float_as_uint(acc[j4].w);
                         }
                         add_flagged(c, v);
-                        piece(c, v, [] {});
+                        ok = piece(c, v, [] {});
                     }
-                    zero_others();
+                    zero_others(w, row_tile, limit);
                 }
-                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);  // the flag may be written again
+                ok = agree(ok, 1, 32 * BLOCK_EPI_WARPS);  // (and the flag may be written again)
                 continue;
             }
             // The next piece's loads are on their way while one is stored.
             int c = turn;
             if (lanes_in && c < pieces)
-                ptx::tmem_load_32cols_async(taddr + c * 32, v);
+                load_piece(taddr + c * 32, v);
             else
                 release_tmem(buf);
-            for (; lanes_in && c < pieces; c += 2) {
+            for (; ok && lanes_in && c < pieces; c += 2) {
                 ptx::tmem_wait_ld(v);
                 add_flagged(c, v);
-                piece(c, v, [&] {
-                    if (c + 2 < pieces) {
-                        ptx::tmem_load_32cols_async(taddr + (c + 2) * 32, v);
-                        load_z(c + 2);
-                    } else {
+                ok = piece(c, v, [&] {
+                    if (c + 2 < pieces)
+                        load_piece(taddr + (c + 2) * 32, v);
+                    else
                         release_tmem(buf);
-                    }
                 });
             }
-            zero_others();
+            if (!ok) break;
+            zero_others(w, row_tile, limit);
         }
         // Rows of no group: zeros (SHRINK: of u and its parts).
         if (p.offsets) {
@@ -944,11 +1085,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 const int64_t row = i < first ? i : end.last + (i - first);
                 if constexpr (MODE == BLOCK_SHRINK) {
                     zero(p.out0, row, p.R);
-                    const int32_t tile = static_cast<int32_t>(row / p.wide_bn), in = static_cast<int32_t>(row % p.wide_bn);
-                    const int32_t blk0 = __ldcg(p.tab.blocks + tile), nb = __ldcg(p.tab.blocks + tile + 1) - blk0;
-                    for (int32_t k = lane; k < nb * 8; k += 32)
-                        *reinterpret_cast<uint4 *>(p.wide + (static_cast<int64_t>(blk0 + (k >> 3)) * p.wide_bn + in) * 64 + (k & 7) * 8) =
-                            make_uint4(0u, 0u, 0u, 0u);
+                    const int32_t tile = static_cast<int32_t>(row / p.wide_bn);
+                    zero_columns(p, static_cast<int32_t>(row % p.wide_bn), __ldcg(p.tab.blocks + tile), __ldcg(p.tab.count + tile), -1, lane);
                 } else {
                     zero(p.out0, row, p.N);
                     zero(p.gate, row, p.N);
@@ -957,6 +1095,10 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             }
         }
         if (lane == 0) ptx::bulk_wait_group_read<0>();
+        if (MODE == BLOCK_GRAD && issues) {  // copies that an abort left on their way
+            for (uint32_t b = 0; b < 2; ++b)
+                if ((z_out >> b) & 1u) wait_drain(z_bar(duo, b), (z_phase >> b) & 1u, wd);
+        }
         __syncwarp();
     }
 

@@ -23,7 +23,7 @@ struct AdapterTables {
     int32_t *rank;     // [groups] place in ids (of groups that have rows)
     int32_t *first;    // [row tiles] place of the tile's first adapter
     int32_t *count;    // [row tiles] adapters of its rows
-    int32_t *blocks;   // [row tiles + 1] blocks before the tile's
+    int32_t *blocks;   // [row tiles] blocks before the tile's
     int32_t *flags;    // [groups][ADAPT_FLAGS] B_g holds an infinity or NaN
 };
 constexpr int ADAPT_FLAGS = 8;
@@ -42,6 +42,7 @@ struct BlockParams {
     BlockOut gate, up;       // halves of Z (GATED) or dZ (GRAD)
     const uint16_t *z;       // GRAD: Z
     int64_t ldz;
+    int32_t z_tma;           // tensor maps of its halves exist
     // SHRINK, ADAPT
     AdapterTables tab;
     const float *scales;     // [groups] or null
@@ -65,6 +66,10 @@ __host__ __device__ inline int32_t adapter_blocks(int32_t count, int32_t Rp)
 {
     return Rp <= 32 ? (count * Rp + 31) / 32 : count * (Rp / 32);
 }
+
+// Staging boxes of 32 rows of 128 bytes: eight, GRAD sixteen (z of two pieces a
+// team of two warps; dZ takes z's place).
+__host__ __device__ constexpr int block_epi_bytes(int mode) { return mode == BLOCK_GRAD ? 65536 : 32768; }
 
 constexpr int BLOCK_EPI_WARPS = 8;
 constexpr int BLOCK_THREADS = 64 + 32 * BLOCK_EPI_WARPS;

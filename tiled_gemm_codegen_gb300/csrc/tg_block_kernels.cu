@@ -12,7 +12,9 @@ namespace {
 template <int BN, int STAGES, bool PAIR>
 BlockShape shape()
 {
-    constexpr int smem = Geometry<BN, PAIR>::smem_bytes(STAGES);
+    using G = Geometry<BN, PAIR>;
+    constexpr int bytes = STAGES * G::STAGE + block_epi_bytes(TG_BLOCK_MODE) + G::BAR_BYTES + G::ALIGN_SLACK;
+    constexpr int smem = bytes > G::ONE_CTA_PER_SM ? bytes : G::ONE_CTA_PER_SM;
     static_assert(smem <= SMEM_LIMIT, "shared memory budget");
     return {block_kernel<TG_BLOCK_MODE, BN, STAGES, PAIR>, BN, smem, PAIR};
 }
@@ -29,10 +31,11 @@ BlockShape block_shape_shrink(BlockTiles t)
 BlockShape block_shape_adapt(BlockTiles t)
 #endif
 {
+    constexpr int STAGES = TG_BLOCK_MODE == BLOCK_GRAD ? 5 : 6;
 #if TG_BLOCK_MODE != 2  // (the adapters' first products have few features)
-    if (t == TILES_PAIR) return shape<256, 6, true>();
+    if (t == TILES_PAIR) return shape<256, STAGES, true>();
 #endif
-    return t == TILES_FEW ? shape<32, 9, false>() : shape<128, 6, false>();
+    return t == TILES_FEW ? shape<32, TG_BLOCK_MODE == BLOCK_GRAD ? 8 : 9, false>() : shape<128, STAGES, false>();
 }
 
 }  // namespace tg
