@@ -94,6 +94,7 @@ __device__ __forceinline__ int32_t write_tables(const BlockParams &p, int32_t ti
     for (int32_t t0 = 0; t0 < tiles; t0 += THREADS) {
         const int32_t t = t0 + tid;
         int32_t n = 0;
+        int4 place = make_int4(0, 0, 0, 0);
         if (t < tiles) {
             const int64_t r0 = static_cast<int64_t>(t) * p.wide_bn, r1 = r0 + p.wide_bn;
             int32_t a = 0, b = used;  // first with hi > r0
@@ -113,12 +114,11 @@ __device__ __forceinline__ int32_t write_tables(const BlockParams &p, int32_t ti
                 else
                     a = m + 1;
             }
-            p.tab.first[t] = first;
-            p.tab.count[t] = a - first;
+            place = make_int4(first, a - first, 0, 0);
             n = stride > 0 ? stride : adapter_blocks(a - first, p.Rp);
         }
-        const int32_t before = blocks + block_scan<THREADS, false>(n, part) - n;
-        if (t < tiles) p.tab.blocks[t] = before;
+        place.z = blocks + block_scan<THREADS, false>(n, part) - n;
+        if (t < tiles) p.tab.tile[t] = place;
         blocks += part[THREADS / 32 - 1];
         __syncthreads();
     }
@@ -145,7 +145,7 @@ __device__ __forceinline__ void write_flag(const BlockParams &p, int32_t g, int3
         for (int32_t i = body * 8 + tid; i < N; i += THREADS) bad |= (row[i] & 0x7f80u) == 0x7f80u;
     }
     bad = __syncthreads_or(bad);
-    if (tid == 0) p.tab.flags[g * ADAPT_FLAGS + c] = bad;
+    if (tid == 0) p.tab.flags[g * ADAPT_FLAGS + c] = bad ? 1 : 0;
 }
 
 constexpr int TABLE_THREADS = 1024;
@@ -183,6 +183,34 @@ __device__ __forceinline__ uint4 load8(const uint16_t *row, int32_t k, int32_t K
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// One warp's whole steps of 32 k: DEPTH steps' loads at a time.
+template <int TILES_R, int DEPTH>
+__device__ __forceinline__ void rows_sums(const uint16_t *x0, const uint16_t *x1, const uint16_t *const (&w)[4], int t, int warp,
+                                          int32_t steps, float (&c)[4][4])
+{
+    constexpr int WARPS = ROWS_THREADS / 32;
+    for (int32_t s = warp; s < steps; s += DEPTH * WARPS) {
+        uint4 xa[DEPTH], xb[DEPTH], wv[DEPTH][TILES_R];
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            const int32_t k = min(s + d * WARPS, steps - 1) * 32 + 8 * t;
+            xa[d] = __ldg(reinterpret_cast<const uint4 *>(x0 + k));
+            xb[d] = __ldg(reinterpret_cast<const uint4 *>(x1 + k));
+#pragma unroll
+            for (int i = 0; i < TILES_R; ++i) wv[d][i] = __ldg(reinterpret_cast<const uint4 *>(w[i] + k));
+        }
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            if (s + d * WARPS >= steps) break;
+#pragma unroll
+            for (int i = 0; i < TILES_R; ++i) {
+                mma_16x8x16(c[i], xa[d].x, xb[d].x, xa[d].y, xb[d].y, wv[d][i].x, wv[d][i].y);
+                mma_16x8x16(c[i], xa[d].z, xb[d].z, xa[d].w, xb[d].w, wv[d][i].z, wv[d][i].w);
+            }
+        }
+    }
+}
+
 // Few rows an adapter (decoding): the tables, the flags and u in one launch, so
 // that ADAPT's shared projection, which starts beside it, waits for
 // little.  Block 0: the tables; blocks 1 .. chunks: 16 rows of one group each,
@@ -206,7 +234,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
         const int32_t first = max(0, min(__ldg(p.offsets), p.S)), last = used > 0 ? p.tab.hi[used - 1] : first;
         for (int32_t i = warp; i < first + p.S - last; i += WARPS) {
             const int32_t row = i < first ? i : last + i - first, tile = row / p.wide_bn;
-            zero_columns(p, row % p.wide_bn, tile * stride, p.tab.count[tile], -1, lane);
+            zero_columns(p, row % p.wide_bn, tile * stride, p.tab.tile[tile].y, -1, lane);
             for (int32_t r = lane; p.out0.p && r < p.R; r += 32)
                 static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = 0;
         }
@@ -291,7 +319,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
     const uint16_t *x0 = X + static_cast<int64_t>(row0 + min(gid, rows - 1)) * ldx;
     const uint16_t *x1 = X + static_cast<int64_t>(row0 + min(gid + 8, rows - 1)) * ldx;
     const float scale = p.scales ? __ldg(p.scales + g) : 1.0f;
-    const int32_t steps = (K + 31) / 32;
+    const int32_t steps = K / 32;  // whole ones
     for (int32_t r0 = 0; r0 < p.R; r0 += 32) {
         const int tiles_r = min(4, (p.R - r0 + 7) / 8);
         float c[4][4];
@@ -302,13 +330,18 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
         const uint16_t *w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = A + g * strideA + static_cast<int64_t>(min(r0 + 8 * i + gid, p.R - 1)) * lda;
-#pragma unroll 4
-        for (int32_t s = warp; s < steps; s += WARPS) {
-            const int32_t k = s * 32 + 8 * t;
+        // (a call each for one, two and four tiles of R keeps the loads free of branches, so that many are under way)
+        if (tiles_r > 2)
+            rows_sums<4, 2>(x0, x1, w, t, warp, steps, c);
+        else if (tiles_r == 2)
+            rows_sums<2, 4>(x0, x1, w, t, warp, steps, c);
+        else
+            rows_sums<1, 4>(x0, x1, w, t, warp, steps, c);
+        if (warp == WARPS - 1 && steps * 32 < K) {  // the last, partial step
+            const int32_t k = steps * 32 + 8 * t;
             const uint4 xa = load8(x0, k, K), xb = load8(x1, k, K);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (i >= tiles_r) break;
                 const uint4 wv = load8(w[i], k, K);
                 mma_16x8x16(c[i], xa.x, xb.x, xa.y, xb.y, wv.x, wv.y);
                 mma_16x8x16(c[i], xa.z, xb.z, xa.w, xb.w, wv.z, wv.w);
@@ -429,6 +462,28 @@ struct Cut {
     size_t part_bytes() const { return static_cast<size_t>(part_tiles()) * splits * BM * bn * 4; }
 };
 
+// How many workers share a tile.  Few rows a group: the weights are the
+// traffic, every worker draws at its own rate, and what counts is how
+// evenly the k-blocks fall on them: the number of shares (12 k-blocks at least)
+// for which the busiest worker has the least, a block added for each share
+// (8192 x 2 * 14336, one row: 224 tiles of 128 k-blocks on 152 workers take 82 us
+// whole, XXX in halves).  Else as grouped rows.
+int64_t split_of(int mode, const Cut &c, int64_t S, int64_t hit, int64_t depth, int sms)
+{
+    if (mode == BLOCK_SHRINK)  // X is the traffic: as many workers as there are, for groups that end in the middle of a tile
+        return std::max<int64_t>(1, std::min<int64_t>(sms / (S / c.bn + (hit + 1) / 2), depth / SPLIT_DEPTH));
+    if (c.tiles == TILES_FEW && c.units >= sms) {
+        int64_t best = 1, least = cdiv(c.units, sms) * depth;
+        for (int64_t s = 2; s <= 8 && depth >= s * SPLIT_DEPTH; ++s) {
+            const int64_t most = cdiv(c.units * s, sms) * (cdiv(depth, s) + 1);
+            if (most < least) best = s, least = most;
+        }
+        return best;
+    }
+    const int64_t share = share_of(false, c.tiles == TILES_PAIR, c.units, depth, sms);
+    return share == 0 ? 1 : std::min(SPLIT_MOST, cdiv(depth, share));
+}
+
 // `lanes`: accumulator lanes a feature takes (GATED: 2).  Tiles as grouped
 // rows choose them (tiles_cost): pairs or one CTA, and 32 rows where
 // groups have few, whose ring is deeper (weights are the traffic).
@@ -446,8 +501,7 @@ Cut cut_rows(int mode, int64_t S, int64_t N, int64_t K, int64_t groups, int sms,
     c.units = (S / c.bn + hit) * cdiv(N, c.features);
     if (groups == 1) c.units = cdiv(S, c.bn) * cdiv(N, c.features);
     const int64_t depth = cdiv(K, BK);
-    const int64_t share = share_of(false, pair, c.units, depth, sms);
-    c.splits = share == 0 ? 1 : std::min(SPLIT_MOST, cdiv(depth, share));
+    c.splits = split_of(mode, c, S, hit, depth, sms);
     return c;
 }
 
@@ -653,17 +707,16 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     Operand *ops[4] = {&x, &w, &a, &b};
     const size_t at[4] = {s.take(pack_bytes(x)), s.take(pack_bytes(w)), s.take(pack_bytes(a)), s.take(pack_bytes(b))};
     const size_t at_wide = s.take(static_cast<size_t>(blocks) * cy.bn * 128);
-    const size_t words[7] = {static_cast<size_t>(hit), static_cast<size_t>(hit), static_cast<size_t>(hit), static_cast<size_t>(groups),
-                             static_cast<size_t>(tiles), static_cast<size_t>(tiles), static_cast<size_t>(tiles)};
-    size_t at_tab[7];
-    for (int i = 0; i < 7; ++i) at_tab[i] = s.take(words[i] * 4);
-    const size_t at_flags = s.take(static_cast<size_t>(groups) * ADAPT_FLAGS * 4);
+    const size_t words[4] = {static_cast<size_t>(hit), static_cast<size_t>(hit), static_cast<size_t>(hit), static_cast<size_t>(groups)};
+    size_t at_tab[4];
+    for (int i = 0; i < 4; ++i) at_tab[i] = s.take(words[i] * 4);
+    const size_t at_tile = s.take(static_cast<size_t>(tiles) * 16), at_flags = s.take(static_cast<size_t>(groups) * ADAPT_FLAGS);
     void *mem = nullptr;
     if ((st = host_arena(hs, s.size, &mem)) != TG_OK) return st;
     uint8_t *arena = static_cast<uint8_t *>(mem);
     auto table = [&](size_t off) { return reinterpret_cast<int32_t *>(arena + off); };
     p.tab = AdapterTables{table(at_tab[0]), table(at_tab[1]), table(at_tab[2]), table(at_tab[3]),
-                          table(at_tab[4]), table(at_tab[5]), table(at_tab[6]), table(at_flags)};
+                          reinterpret_cast<int4 *>(arena + at_tile), arena + at_flags};
     p.wide = reinterpret_cast<uint16_t *>(arena + at_wide);
     p.partials = reinterpret_cast<float *>(arena + at_part);
     const int64_t parts_a = few ? 0 : ca.part_tiles(), parts_y = cy.part_tiles();

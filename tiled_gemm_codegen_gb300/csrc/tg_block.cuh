@@ -47,6 +47,7 @@ struct BlockUnit {
     int32_t g, row0, row1, tm, tn;
     int32_t kb0, kb1;      // this worker's k-blocks of the tile (ADAPT: of X W)
     int32_t e0, e1;        // ADAPT: its blocks of u B, once known (ext_range)
+    AdapterTile ad;
     int32_t part, nparts, tile;
 };
 
@@ -128,6 +129,7 @@ __device__ __forceinline__ bool block_walk_to(const BlockParams &p, int64_t t64,
     u.kb0 = static_cast<int32_t>(static_cast<int64_t>(u.part) * p.k_blocks / u.nparts);
     u.kb1 = static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * p.k_blocks / u.nparts);
     u.e0 = u.e1 = 0;
+    u.ad = {0, 0, 0};
     return true;
 }
 
@@ -135,7 +137,8 @@ __device__ __forceinline__ bool block_walk_to(const BlockParams &p, int64_t t64,
 __device__ __forceinline__ void ext_range(const BlockParams &p, BlockUnit &u)
 {
     ptx::griddep_wait();
-    const int32_t n = adapter_blocks(__ldcg(p.tab.count + u.tm), p.Rp);
+    u.ad = adapter_tile(p, u.tm);
+    const int32_t n = adapter_blocks(u.ad.count, p.Rp);
     u.e0 = static_cast<int32_t>(static_cast<int64_t>(u.part) * n / u.nparts);
     u.e1 = static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * n / u.nparts);
 }
@@ -391,25 +394,16 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             const int32_t n_half = static_cast<int32_t>(rank) * (block_rows_n<BN>(w) / 2);
             const int32_t n0 = w.row0 + w.tm * BN + n_half;
             // ADAPT: lane l holds the tile's adapter ad0 + l (-1: none, or flagged)
-            int32_t ad0 = 0, ad = -1, ad_first = 0, ad_count = 0, ext_row = 0;
+            int32_t ad0 = 0, ad = -1;
             auto adapters = [&](int32_t from) {
                 ad0 = from;
-                ad = -1;
-                if (from + lane < ad_count) {
-                    ad = __ldcg(p.tab.ids + ad_first + from + lane);
-                    int32_t bad = 0;
-#pragma unroll
-                    for (int i = 0; i < ADAPT_FLAGS; ++i) bad |= __ldcg(p.tab.flags + ad * ADAPT_FLAGS + i);
-                    if (bad) ad = -1;
-                }
+                ad = from + lane < w.ad.count ? __ldcg(p.tab.ids + w.ad.first + from + lane) : -1;
+                if (ad >= 0 && adapter_flagged(p, ad)) ad = -1;
             };
             for (int32_t i = w.kb0; i < w.kb1 + w.e1 - w.e0 || (MODE == BLOCK_ADAPT && i == w.kb1); ++i, ++it) {
                 if (MODE == BLOCK_ADAPT && i == w.kb1) {
                     ext_range(p, w);
                     if (w.e0 == w.e1) break;
-                    ad_first = __ldcg(p.tab.first + w.tm);
-                    ad_count = __ldcg(p.tab.count + w.tm);
-                    ext_row = __ldcg(p.tab.blocks + w.tm) * BN + n_half;
                 }
                 const uint32_t s = it % STAGES;
                 const uint32_t ph = (it / STAGES) & 1u;
@@ -443,23 +437,17 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     const int32_t a0 = p.Rp <= 32 ? e * per : e / bpa;
                     const int32_t chunk = p.Rp <= 32 ? 0 : (e % bpa) / 2 * 64;
                     if (i == w.kb1 || a0 + per > ad0 + 32) adapters(a0);
-                    int32_t ids[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) ids[k] = __shfl_sync(0xffffffffu, ad, min(31, a0 - ad0 + k));
-                    if (ptx::elect_one()) {
-                        expect();
-                        const int32_t rows = min(p.Rp, 64);
-                        const int32_t subs = 64 / rows;
-                        for (int j = 0; j < subs; ++j) {
-                            const int k = p.Rp <= 32 ? j >> 1 : 0;
-                            const int32_t id = k == 0 ? ids[0] : k == 1 ? ids[1] : k == 2 ? ids[2] : ids[3];
-                            // rows past R read as zeros
-                            const int32_t r0 = id < 0 ? p.Rp : chunk, z = p.b_shared ? 0 : max(id, 0);
-                            const uint32_t dst = a_dst + static_cast<uint32_t>(j * rows) * 128u;
-                            load(dst, &tmV, m0, r0, z);
-                            load(dst + BOX_BYTES, &tmV, m0 + 64, r0, z);
-                        }
-                        load(b_dst, &tmE, 0, ext_row + e * BN, 0);
+                    if (ptx::elect_one()) expect();
+                    __syncwarp();
+                    // a lane a box (rows of B past R read as zeros), and one for u
+                    const int32_t rows = min(p.Rp, 64), subs = 64 / rows;
+                    const int32_t j = lane >> 1, h = lane & 1;
+                    const int32_t id = __shfl_sync(0xffffffffu, ad, min(31, a0 - ad0 + (p.Rp <= 32 ? j >> 1 : 0)));
+                    if (j < subs) {
+                        const int32_t r0 = id < 0 ? p.Rp : chunk, z = p.b_shared ? 0 : max(id, 0);
+                        load(a_dst + h * BOX_BYTES + static_cast<uint32_t>(j * rows) * 128u, &tmV, m0 + 64 * h, r0, z);
+                    } else if (lane == 31) {
+                        load(b_dst, &tmE, 0, (w.ad.blk0 + e) * BN + n_half, 0);
                     }
                 } else if (ptx::elect_one()) {
                     const int32_t kb = i;
@@ -684,21 +672,25 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 load_fragments(taddr, v);
         };
 
-        // SHRINK: where the parts of row `row` of the group at `place` stand for
-        // ADAPT, in units of 8 values; and zeros in the other adapters' columns
-        // of a tile's rows.
-        [[maybe_unused]] int32_t place = 0;
+        // SHRINK: a unit's rows lie in two of ADAPT's tiles at most (which are
+        // no lower than its own): theirs, and its adapter's place among theirs.
+        [[maybe_unused]] int32_t tile0 = 0, place0 = 0, place1 = 0;
+        [[maybe_unused]] AdapterTile ad0{}, ad1{};
+        // where the parts of a row stand, in units of 8 values
         [[maybe_unused]] auto wide_row = [&](int32_t row) {
-            const int32_t tile = row / p.wide_bn, in = row % p.wide_bn;
-            return adapter_unit(place - __ldcg(p.tab.first + tile), __ldcg(p.tab.blocks + tile), in, p.wide_bn, p.Rp);
+            const int32_t tile = row / p.wide_bn, in = row - tile * p.wide_bn;
+            const bool second = tile != tile0;
+            return adapter_unit(second ? place1 : place0, second ? ad1.blk0 : ad0.blk0, in, p.wide_bn, p.Rp);
         };
+        // zeros in the other adapters' columns of a unit's rows
         auto zero_others = [&](const BlockUnit &w, int32_t row_tile, int32_t limit) {
             if constexpr (MODE == BLOCK_SHRINK) {
                 if (w.tn != 0) return;
                 for (int32_t row = row_tile + (warp - 2); row < limit; row += BLOCK_EPI_WARPS) {
-                    const int32_t tile = row / p.wide_bn;
-                    zero_columns(p, row % p.wide_bn, __ldcg(p.tab.blocks + tile), __ldcg(p.tab.count + tile),
-                                 place - __ldcg(p.tab.first + tile), lane);
+                    const int32_t tile = row / p.wide_bn, in = row - tile * p.wide_bn;
+                    const bool second = tile != tile0;
+                    const int32_t count = second ? ad1.count : ad0.count;
+                    if (count > 1 || p.Rp < 32) zero_columns(p, in, second ? ad1.blk0 : ad0.blk0, count, second ? place1 : place0, lane);
                 }
             }
         };
@@ -715,6 +707,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         // GRAD: bit b: parity of z_bar(b)'s next phase; a copy is on its way there
         uint32_t z_phase = 0, z_out = 0;
         for (int64_t t = worker; ok && block_walk_to<BN>(p, t, walk, w); t += n_workers) {
+            if (MODE == BLOCK_ADAPT) ext_range(p, w);
             const int32_t f0 = w.tn * TILE_F + static_cast<int32_t>(rank) * LANES;  // the CTA's first feature
             const int32_t f_warp = f0 + 32 * (MODE == BLOCK_GATED ? sub : q);       // the warp's
             const int32_t f_box = MODE == BLOCK_GATED ? f0 : team == 2 ? f_warp - 32 * sub : f_warp;
@@ -723,7 +716,14 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             const int32_t pieces = (limit - row_tile + 31) / 32;
             const bool lanes_in = MODE == BLOCK_SHRINK ? f_warp < p.Rp : f_box < p.N;  // uniform in a team
 
-            if constexpr (MODE == BLOCK_SHRINK) place = __ldcg(p.tab.rank + w.g);
+            if constexpr (MODE == BLOCK_SHRINK) {
+                tile0 = row_tile / p.wide_bn;
+                ad0 = adapter_tile(p, tile0);
+                ad1 = adapter_tile(p, (limit - 1) / p.wide_bn);
+                const int32_t place = __ldcg(p.tab.rank + w.g);
+                place0 = place - ad0.first;
+                place1 = place - ad1.first;
+            }
 
             // GRAD: z of piece c into the pair of boxes `b`, gate and up half.
             // By TMA where its rows are on 16 bytes; else the team
@@ -747,11 +747,21 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     team_sync();
                     const int32_t f = f_warp + lane, rows = limit - r0;
                     const uint16_t *at = p.z + static_cast<int64_t>(r0) * p.ldz + min(f, p.N - 1);
-#pragma unroll 8
-                    for (int j = 0; j < 32; ++j, at += j < rows ? p.ldz : 0) {
-                        const uint32_t to = unit_at(box, j, sub * 4 + (lane >> 3)) + (lane & 7) * 2;
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(at[0]) : "memory");
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + EPI_BOX_BYTES), "h"(at[p.N]) : "memory");
+                    // (rows past the group's end: the last one's)
+#pragma unroll
+                    for (int j0 = 0; j0 < 32; j0 += 16) {
+                        uint16_t zg[16], zu[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j, at += j0 + j < rows ? p.ldz : 0) {
+                            zg[j] = at[0];
+                            zu[j] = at[p.N];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const uint32_t to = unit_at(box, j0 + j, sub * 4 + (lane >> 3)) + (lane & 7) * 2;
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(zg[j]) : "memory");
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + EPI_BOX_BYTES), "h"(zu[j]) : "memory");
+                        }
                     }
                     __syncwarp();
                 }
@@ -916,27 +926,19 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             // their own rows.
             bool flagged = false;
             if constexpr (MODE == BLOCK_ADAPT) {
-                const int32_t first = __ldcg(p.tab.first + w.tm), most = __ldcg(p.tab.count + w.tm);
-                int32_t bad = 0;
-                for (int32_t i = lane; i < most; i += 32) {
-                    const int32_t *flag = p.tab.flags + __ldcg(p.tab.ids + first + i) * ADAPT_FLAGS;
-#pragma unroll
-                    for (int k = 0; k < ADAPT_FLAGS; ++k) bad |= __ldcg(flag + k);
-                }
-                flagged = __any_sync(0xffffffffu, bad != 0);
+                bool bad = false;
+                for (int32_t i = lane; i < w.ad.count; i += 32) bad |= adapter_flagged(p, __ldcg(p.tab.ids + w.ad.first + i));
+                flagged = __any_sync(0xffffffffu, bad);
             }
             auto add_flagged = [&](int c, uint32_t (&v)[32]) {
                 if constexpr (MODE == BLOCK_ADAPT) {
                     if (!flagged) return;
-                    const int32_t first = __ldcg(p.tab.first + w.tm), most = __ldcg(p.tab.count + w.tm);
-                    const int32_t blk0 = __ldcg(p.tab.blocks + w.tm);
                     const int32_t r0 = row_tile + 32 * c;
-                    const int32_t per = p.Rp <= 32 ? 32 / p.Rp : 1;
-                    for (int32_t i = 0; i < most; ++i) {
-                        const int32_t id = __ldcg(p.tab.ids + first + i);
-                        const int32_t bad = lane < ADAPT_FLAGS ? __ldcg(p.tab.flags + id * ADAPT_FLAGS + lane) : 0;
-                        if (!__any_sync(0xffffffffu, bad != 0)) continue;
-                        const int32_t lo = max(__ldcg(p.tab.lo + first + i), r0), hi = min(__ldcg(p.tab.hi + first + i), min(limit, r0 + 32));
+                    for (int32_t i = 0; i < w.ad.count; ++i) {
+                        const int32_t id = __ldcg(p.tab.ids + w.ad.first + i);
+                        if (!adapter_flagged(p, id)) continue;
+                        const int32_t lo = max(__ldcg(p.tab.lo + w.ad.first + i), r0);
+                        const int32_t hi = min(__ldcg(p.tab.hi + w.ad.first + i), min(limit, r0 + 32));
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const int32_t row = r0 + frag_row(j, lane), f = f_warp + frag_feature(j, lane);
@@ -944,8 +946,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                             float sum = 0.0f;
 #pragma unroll 1
                             for (int32_t r = 0; r < p.R; ++r) {
-                                const int64_t blk = blk0 + (p.Rp <= 32 ? i / per : i * (p.Rp / 32) + r / 64 * 2);
-                                const uint16_t *at = p.wide + (blk * BN + (row - row_tile)) * 64 + (p.Rp <= 32 ? i % per * 2 * p.Rp + r : r & 63);
+                                const uint16_t *at = p.wide + static_cast<int64_t>(adapter_unit(i, w.ad.blk0, row - row_tile, BN, p.Rp)) * 8 +
+                                                     (p.Rp <= 32 ? r : r / 64 * 2 * BN * 64 + (r & 63));
                                 const float u = __uint_as_float(static_cast<uint32_t>(at[0]) << 16) +
                                                 __uint_as_float(static_cast<uint32_t>(at[p.Rp <= 32 ? p.Rp : BN * 64]) << 16);
                                 const float bv = __uint_as_float(static_cast<uint32_t>(p.b[id * p.strideB + r * p.ldb + f]) << 16);
@@ -958,7 +960,6 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             };
 
             uint32_t v[32];
-            if (MODE == BLOCK_ADAPT) ext_range(p, w);
             if (w.kb0 == w.kb1 && w.e0 == w.e1) {  // the empty sum
                 if (lanes_in) load_z(turn, flip);
                 for (int c = turn; ok && lanes_in && c < pieces; c += 2) {
@@ -1085,8 +1086,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 const int64_t row = i < first ? i : end.last + (i - first);
                 if constexpr (MODE == BLOCK_SHRINK) {
                     zero(p.out0, row, p.R);
-                    const int32_t tile = static_cast<int32_t>(row / p.wide_bn);
-                    zero_columns(p, static_cast<int32_t>(row % p.wide_bn), __ldcg(p.tab.blocks + tile), __ldcg(p.tab.count + tile), -1, lane);
+                    const AdapterTile ad = adapter_tile(p, static_cast<int32_t>(row / p.wide_bn));
+                    zero_columns(p, static_cast<int32_t>(row % p.wide_bn), ad.blk0, ad.count, -1, lane);
                 } else {
                     zero(p.out0, row, p.N);
                     zero(p.gate, row, p.N);

@@ -21,10 +21,8 @@ struct AdapterTables {
     int32_t *ids;      // [min(groups, S)] groups that have rows, in order
     int32_t *lo, *hi;  // [min(groups, S)] their rows
     int32_t *rank;     // [groups] place in ids (of groups that have rows)
-    int32_t *first;    // [row tiles] place of the tile's first adapter
-    int32_t *count;    // [row tiles] adapters of its rows
-    int32_t *blocks;   // [row tiles] blocks before the tile's
-    int32_t *flags;    // [groups][ADAPT_FLAGS] B_g holds an infinity or NaN
+    int4 *tile;        // [row tiles] place of the tile's first adapter, adapters of its rows, first block
+    uint8_t *flags;    // [groups][ADAPT_FLAGS] B_g holds an infinity or NaN
 };
 constexpr int ADAPT_FLAGS = 8;
 
