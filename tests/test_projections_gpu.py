@@ -396,12 +396,13 @@ def test_adapted_pitches_and_guard_bands(pitches, dtype, pair):
     assert bool(torch.isnan(ys).all()) and bool(torch.isnan(us).all())
 
 
-@pytest.mark.parametrize("R", [4, 16, 48])
+@pytest.mark.parametrize("R", [4, 16, 48, 100])
+@pytest.mark.parametrize("K", [96, 3200])  # whole tiles; shared ones
 @pytest.mark.parametrize("pair", [1, 2])
-def test_adapters_stay_in_their_rows(R, pair):
+def test_adapters_stay_in_their_rows(R, K, pair):
     """Infinities and NaN in one adapter's matrices and rows next to others in
     the same tile: the others exact, its own as the formula's."""
-    sizes, K, N = [3, 5, 2, 40, 1, 100, 2], 96, 160
+    sizes, N = [3, 5, 2, 40, 1, 100, 2], 160
     t, v = _adapters(sizes, K, N, R, 80, S=160)
     (X, W, A, B), (xv, wv, av, bv) = t, v
     for arr, val in ((B, bv),):

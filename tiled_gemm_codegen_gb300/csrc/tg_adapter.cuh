@@ -18,13 +18,6 @@ __device__ __forceinline__ AdapterTile adapter_tile(const BlockParams &p, int32_
     return {v.x, v.y, v.z};
 }
 
-// Whether B of adapter `id` holds an infinity or NaN.
-__device__ __forceinline__ bool adapter_flagged(const BlockParams &p, int32_t id)
-{
-    const uint2 f = __ldcg(reinterpret_cast<const uint2 *>(p.tab.flags) + id);
-    return (f.x | f.y) != 0;
-}
-
 // u = hi + lo: rounded to bf16, and what that leaves.  hi rounds down where
 // rounding would make an infinity; an infinity or NaN is hi's alone.
 __device__ __forceinline__ void split_parts(float x, __nv_bfloat16 &hi, __nv_bfloat16 &lo)

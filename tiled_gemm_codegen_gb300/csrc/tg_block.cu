@@ -77,7 +77,7 @@ __device__ __forceinline__ int32_t each_group(const BlockParams &p, int32_t *par
     return used;
 }
 
-// By one block: the tables of AdapterTables but the flags.  stride: blocks of
+// By one block: the tables of AdapterTables.  stride: blocks of
 // a tile (0: as many as it needs, tiles one behind another).  Returns the
 // number of groups that have rows.
 template <int THREADS>
@@ -125,42 +125,14 @@ __device__ __forceinline__ int32_t write_tables(const BlockParams &p, int32_t ti
     return used;
 }
 
-// By one block: share `c` of ADAPT_FLAGS of B_g's rows, flagged if it holds an
-// infinity or NaN (groups without rows are not looked at).
-template <int THREADS>
-__device__ __forceinline__ void write_flag(const BlockParams &p, int32_t g, int32_t c, int32_t N, int32_t vec)
-{
-    const int tid = static_cast<int>(threadIdx.x);
-    if (__ldg(p.offsets + g + 1) <= __ldg(p.offsets + g)) return;
-    int32_t bad = 0;
-    for (int32_t r = c; r < p.R; r += ADAPT_FLAGS) {
-        const uint16_t *row = p.b + g * p.strideB + r * p.ldb;
-        const int32_t body = vec ? N / 8 : 0;
-        for (int32_t i = tid; i < body; i += THREADS) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row) + i);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
-        }
-        for (int32_t i = body * 8 + tid; i < N; i += THREADS) bad |= (row[i] & 0x7f80u) == 0x7f80u;
-    }
-    bad = __syncthreads_or(bad);
-    if (tid == 0) p.tab.flags[g * ADAPT_FLAGS + c] = bad ? 1 : 0;
-}
-
 constexpr int TABLE_THREADS = 1024;
 constexpr int ROWS_THREADS = 512;
 
-// Block 0: the tables.  The others: flags.
-__global__ void __launch_bounds__(TABLE_THREADS) adapter_tables_kernel(const BlockParams p, int32_t tiles, int32_t N, int32_t vec)
+__global__ void __launch_bounds__(TABLE_THREADS) adapter_tables_kernel(const BlockParams p, int32_t tiles)
 {
     ptx::griddep_launch_dependents();
     __shared__ int32_t part[32], his[TABLE_THREADS];
-    if (blockIdx.x == 0)
-        write_tables<TABLE_THREADS>(p, tiles, 0, part, his);
-    else
-        write_flag<TABLE_THREADS>(p, static_cast<int32_t>(blockIdx.x - 1) / ADAPT_FLAGS,
-                                  static_cast<int32_t>(blockIdx.x - 1) % ADAPT_FLAGS, N, vec);
+    write_tables<TABLE_THREADS>(p, tiles, 0, part, his);
 }
 
 // ------------------------------------------------------------ u of few rows
@@ -183,8 +155,9 @@ __device__ __forceinline__ uint4 load8(const uint16_t *row, int32_t k, int32_t K
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One warp's whole steps of 32 k: DEPTH steps' loads at a time.
-template <int TILES_R, int DEPTH>
+// One warp's whole steps of 32 k, DEPTH steps' loads at a time: rows t / 4, and
+// with HIGH rows 8 + t / 4, against TILES_R tiles of 8 of R.
+template <int TILES_R, bool HIGH, int DEPTH>
 __device__ __forceinline__ void rows_sums(const uint16_t *x0, const uint16_t *x1, const uint16_t *const (&w)[4], int t, int warp,
                                           int32_t steps, float (&c)[4][4])
 {
@@ -195,7 +168,7 @@ __device__ __forceinline__ void rows_sums(const uint16_t *x0, const uint16_t *x1
         for (int d = 0; d < DEPTH; ++d) {
             const int32_t k = min(s + d * WARPS, steps - 1) * 32 + 8 * t;
             xa[d] = __ldg(reinterpret_cast<const uint4 *>(x0 + k));
-            xb[d] = __ldg(reinterpret_cast<const uint4 *>(x1 + k));
+            xb[d] = HIGH ? __ldg(reinterpret_cast<const uint4 *>(x1 + k)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int i = 0; i < TILES_R; ++i) wv[d][i] = __ldg(reinterpret_cast<const uint4 *>(w[i] + k));
         }
@@ -211,16 +184,15 @@ __device__ __forceinline__ void rows_sums(const uint16_t *x0, const uint16_t *x1
     }
 }
 
-// Few rows an adapter (decoding): the tables, the flags and u in one launch, so
-// that ADAPT's shared projection, which starts beside it, waits for
-// little.  Block 0: the tables; blocks 1 .. chunks: 16 rows of one group each,
-// K split over the block's 16 warps, 32 R at a time; the rest: flags.  A lane's
-// 16 bytes of X and of A are two MMAs' fragments: any order of k will do where
+// Few rows an adapter (decoding): the tables and u in one launch, so that
+// ADAPT's shared projection, which starts beside it, waits for
+// little.  Block 0: the tables; the others: 16 rows of one group each,
+// K split over the block's 16 warps, 32 R at a time.  A lane's 16 bytes of X and of A are two MMAs' fragments: any order of k will do where
 // both operands have the same.  Bound by latency: offsets, one
 // round of loads, the warps' sums.
 __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockParams p, const uint16_t *X, int64_t ldx, const uint16_t *A,
-                                                                    int64_t lda, int64_t strideA, int32_t K, int32_t chunks,
-                                                                    int32_t tiles, int32_t stride, int32_t N, int32_t vec)
+                                                                    int64_t lda, int64_t strideA, int32_t K, int32_t tiles,
+                                                                    int32_t stride)
 {
     ptx::griddep_launch_dependents();
     constexpr int WARPS = ROWS_THREADS / 32;
@@ -238,11 +210,6 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
             for (int32_t r = lane; p.out0.p && r < p.R; r += 32)
                 static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = 0;
         }
-        return;
-    }
-    if (static_cast<int32_t>(blockIdx.x) > chunks) {
-        const int32_t i = static_cast<int32_t>(blockIdx.x) - 1 - chunks;
-        write_flag<ROWS_THREADS>(p, i / ADAPT_FLAGS, i % ADAPT_FLAGS, N, vec);
         return;
     }
     // the chunk's group: chunks are counted group by group
@@ -330,16 +297,22 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
         const uint16_t *w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = A + g * strideA + static_cast<int64_t>(min(r0 + 8 * i + gid, p.R - 1)) * lda;
-        // (a call each for one, two and four tiles of R keeps the loads free of branches, so that many are under way)
-        if (tiles_r > 2)
-            rows_sums<4, 2>(x0, x1, w, t, warp, steps, c);
-        else if (tiles_r == 2)
-            rows_sums<2, 4>(x0, x1, w, t, warp, steps, c);
-        else
-            rows_sums<1, 4>(x0, x1, w, t, warp, steps, c);
+        // (a call for each number of tiles keeps the loads free of branches, so that all of a round are under way at once)
+        if (rows <= 8) {
+            if (tiles_r > 2)
+                rows_sums<4, false, 4>(x0, x1, w, t, warp, steps, c);
+            else if (tiles_r == 2)
+                rows_sums<2, false, 8>(x0, x1, w, t, warp, steps, c);
+            else
+                rows_sums<1, false, 8>(x0, x1, w, t, warp, steps, c);
+        } else if (tiles_r > 2) {
+            rows_sums<4, true, 4>(x0, x1, w, t, warp, steps, c);
+        } else {
+            rows_sums<2, true, 4>(x0, x1, w, t, warp, steps, c);
+        }
         if (warp == WARPS - 1 && steps * 32 < K) {  // the last, partial step
             const int32_t k = steps * 32 + 8 * t;
-            const uint4 xa = load8(x0, k, K), xb = load8(x1, k, K);
+            const uint4 xa = load8(x0, k, K), xb = rows > 8 ? load8(x1, k, K) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint4 wv = load8(w[i], k, K);
@@ -683,10 +656,6 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     p.Rp = static_cast<int32_t>(Rp);
     p.wide_bn = static_cast<int32_t>(cy.bn);
     p.scales = scales;
-    p.b = static_cast<const uint16_t *>(b.p);
-    p.ldb = b.ld;
-    p.strideB = b.nb > 1 ? b.stride : 0;
-
     const bool force = opt && opt->force_pack;
     const bool a_shared = a.nb > 1 && a.stride == 0;
     if (a_shared) a.nb = 1;
@@ -695,8 +664,7 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
         w.pack = force || !tma_ok(w.p, w.ld, 0, 2);
         a.pack = force || !tma_ok(a.p, a.ld, a.nb > 1 ? a.stride : 0, 2);
     }
-    const bool b_vec = tma_ok(b.p, b.ld, b.nb > 1 ? b.stride : 0, 2);
-    b.pack = force || !b_vec;
+    b.pack = force || !tma_ok(b.p, b.ld, b.nb > 1 ? b.stride : 0, 2);
     if (b.nb > 1 && b.stride == 0) {  // one matrix for every adapter
         b.nb = 1;
         p.b_shared = 1;
@@ -710,13 +678,13 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     const size_t words[4] = {static_cast<size_t>(hit), static_cast<size_t>(hit), static_cast<size_t>(hit), static_cast<size_t>(groups)};
     size_t at_tab[4];
     for (int i = 0; i < 4; ++i) at_tab[i] = s.take(words[i] * 4);
-    const size_t at_tile = s.take(static_cast<size_t>(tiles) * 16), at_flags = s.take(static_cast<size_t>(groups) * ADAPT_FLAGS);
+    const size_t at_tile = s.take(static_cast<size_t>(tiles) * 16);
     void *mem = nullptr;
     if ((st = host_arena(hs, s.size, &mem)) != TG_OK) return st;
     uint8_t *arena = static_cast<uint8_t *>(mem);
     auto table = [&](size_t off) { return reinterpret_cast<int32_t *>(arena + off); };
     p.tab = AdapterTables{table(at_tab[0]), table(at_tab[1]), table(at_tab[2]), table(at_tab[3]),
-                          reinterpret_cast<int4 *>(arena + at_tile), arena + at_flags};
+                          reinterpret_cast<int4 *>(arena + at_tile)};
     p.wide = reinterpret_cast<uint16_t *>(arena + at_wide);
     p.partials = reinterpret_cast<float *>(arena + at_part);
     const int64_t parts_a = few ? 0 : ca.part_tiles(), parts_y = cy.part_tiles();
@@ -725,21 +693,21 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     p.counters = counters + parts_a;
     cudaError_t e = pack_operands(hs, arena, ops, at, 4);
     if (e != cudaSuccess) return host_cuda_status(e);
+    p.b = static_cast<const uint16_t *>(b.p);
+    p.ldb = b.ld;
+    p.strideB = b.nb > 1 ? b.stride : 0;
 
     p.offsets = offsets;
     p.groups = static_cast<int32_t>(groups);
     p.N = static_cast<int32_t>(R);
     p.out0 = BlockOut{U, ldu, 0};
-    const unsigned flag_blocks = static_cast<unsigned>(groups * ADAPT_FLAGS);
-    const int32_t vec = b_vec ? 1 : 0;
     if (few) {
-        const int32_t chunks = static_cast<int32_t>(S / 16 + hit);
-        adapter_rows_kernel<<<1u + chunks + flag_blocks, ROWS_THREADS, 0, hs.stream>>>(
+        adapter_rows_kernel<<<static_cast<unsigned>(1 + S / 16 + hit), ROWS_THREADS, 0, hs.stream>>>(
             p, static_cast<const uint16_t *>(x.p), x.ld, static_cast<const uint16_t *>(a.p), a.ld, a_shared ? 0 : a.stride,
-            static_cast<int32_t>(K), chunks, static_cast<int32_t>(tiles), static_cast<int32_t>(stride), static_cast<int32_t>(N), vec);
+            static_cast<int32_t>(K), static_cast<int32_t>(tiles), static_cast<int32_t>(stride));
         if ((e = cudaGetLastError()) != cudaSuccess) return host_cuda_status(e);
     } else {
-        adapter_tables_kernel<<<1u + flag_blocks, TABLE_THREADS, 0, hs.stream>>>(p, static_cast<int32_t>(tiles), static_cast<int32_t>(N), vec);
+        adapter_tables_kernel<<<1, TABLE_THREADS, 0, hs.stream>>>(p, static_cast<int32_t>(tiles));
         if ((e = cudaGetLastError()) != cudaSuccess) return host_cuda_status(e);
         BlockParams pa = p;
         pa.w_k = 1;

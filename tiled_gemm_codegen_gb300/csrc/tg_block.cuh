@@ -143,6 +143,31 @@ __device__ __forceinline__ void ext_range(const BlockParams &p, BlockUnit &u)
     u.e1 = static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * n / u.nparts);
 }
 
+// ADAPT: the adapters (of the tile's) whose columns lie in a unit's blocks.
+__device__ __forceinline__ int32_t ext_first(const BlockParams &p, const BlockUnit &u)
+{
+    return p.Rp <= 32 ? u.e0 * (32 / p.Rp) : u.e0 / (p.Rp / 32);
+}
+__device__ __forceinline__ int32_t ext_end(const BlockParams &p, const BlockUnit &u)
+{
+    return min(u.ad.count, p.Rp <= 32 ? u.e1 * (32 / p.Rp) : (u.e1 - 1) / (p.Rp / 32) + 1);
+}
+
+// Whether one of the first n of 8 bf16 on 16 bytes is an infinity or NaN.
+__device__ __forceinline__ bool has_non_finite(const uint16_t *b, int32_t n)
+{
+    if (n >= 8) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(b));
+        // exponents of ones: adding the lowest exponent bit carries out of them
+        const uint32_t lo = ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                            ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+        return (lo & 0x80008000u) != 0;
+    }
+    bool bad = false;
+    for (int32_t e = 0; e < n; ++e) bad |= (__ldg(b + e) & 0x7f80u) == 0x7f80u;
+    return bad;
+}
+
 // The MMA's N for a tile: its rows rounded up to 32 (16 a CTA of a pair).
 template <int BN>
 __device__ __forceinline__ int32_t block_rows_n(const BlockUnit &u)
@@ -291,7 +316,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     constexpr int EPI_ROWS = 32, EPI_ROW_BYTES = 128;
     static_assert(MODE != BLOCK_SHRINK || !PAIR, "adapters' first products take one-CTA tiles");
     constexpr uint32_t TMEM_ALLOC = static_cast<uint32_t>(G::TMEM_COLS);
-    static_assert(8 * (2 * STAGES + 14) + 20 <= G::BAR_BYTES, "barrier area");
+    static_assert(8 * (2 * STAGES + 14) + 20 <= 512, "barrier area");
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -304,7 +329,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     const uint32_t bar0 = ptx::smem_addr(bar_area);
     // barrier k at bar0 + 8k: [0, S) full, [S, 2S) empty, 2S+{0,1} tfull,
     // 2S+{2,3} tempty, 2S+4 mma-done, 2S+5 never completed; GRAD: from 2S+6
-    // two for each team of epilogue warps: z landed in the boxes
+    // two for each team of epilogue warps: z landed in the boxes; ADAPT: 2S+6:
+    // every epilogue warp has looked through a unit's B
     const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
     const uint32_t stall_bar = bar0 + 8u * (2 * STAGES + 5);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (2 * STAGES + 14));
@@ -315,6 +341,10 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
     auto tfull_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
     auto tempty_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
+    [[maybe_unused]] const uint32_t flag_bar = bar0 + 8u * (2 * STAGES + 6);
+    // ADAPT: bit a of warp w's 256 for unit n: adapter a (of the unit's, from
+    // its first block's) is flagged
+    [[maybe_unused]] uint32_t *flag_words = reinterpret_cast<uint32_t *>(bar_area + 512);
     [[maybe_unused]] auto z_bar = [&](uint32_t duo, uint32_t b) { return bar0 + 8u * (2 * STAGES + 6 + 2 * duo + b); };
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -336,6 +366,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         ptx::mbar_init(done_bar, 1);
         ptx::mbar_init(stall_bar, 1);
         for (uint32_t i = 0; MODE == BLOCK_GRAD && i < 8; ++i) ptx::mbar_init(z_bar(0, i), 1);
+        if (MODE == BLOCK_ADAPT) ptx::mbar_init(flag_bar, BLOCK_EPI_WARPS);
         *abort_flag = 0;
         *issued_slot = 0;
         ptx::fence_barrier_init();
@@ -383,6 +414,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         uint32_t it = 0;
+        [[maybe_unused]] uint32_t flag_n = 0;  // ADAPT: units with blocks of u B before this one
         bool ok = true;
         const uint32_t full0 = PAIR ? ptx::map_to_cta(full_bar(0), 0u) : full_bar(0);
         for (int64_t t = worker; ok && block_walk_to<BN>(p, t, walk, w); t += n_workers) {
@@ -397,13 +429,23 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             int32_t ad0 = 0, ad = -1;
             auto adapters = [&](int32_t from) {
                 ad0 = from;
-                ad = from + lane < w.ad.count ? __ldcg(p.tab.ids + w.ad.first + from + lane) : -1;
-                if (ad >= 0 && adapter_flagged(p, ad)) ad = -1;
+                ad = from + lane < ext_end(p, w) ? __ldcg(p.tab.ids + w.ad.first + from + lane) : -1;
+                const int32_t a = from + lane - ext_first(p, w);
+                uint32_t bad = 0;
+                for (int k = 0; ad >= 0 && k < BLOCK_EPI_WARPS; ++k)
+                    bad |= flag_words[(flag_n & 1u) * 8 * BLOCK_EPI_WARPS + k * 8 + (a >> 5)] >> (a & 31);
+                if (bad & 1u) ad = -1;
             };
             for (int32_t i = w.kb0; i < w.kb1 + w.e1 - w.e0 || (MODE == BLOCK_ADAPT && i == w.kb1); ++i, ++it) {
                 if (MODE == BLOCK_ADAPT && i == w.kb1) {
                     ext_range(p, w);
                     if (w.e0 == w.e1) break;
+                    const int r = wait_bounded_warp(flag_bar, flag_n & 1u, wd);
+                    if (r != WAIT_OK) {
+                        if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_PRODUCER);
+                        ok = false;
+                        break;
+                    }
                 }
                 const uint32_t s = it % STAGES;
                 const uint32_t ph = (it / STAGES) & 1u;
@@ -471,6 +513,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 }
                 __syncwarp();
             }
+            if (MODE == BLOCK_ADAPT && w.e0 < w.e1) ++flag_n;
         }
         if (lane == 0) {
             *issued_slot = it;
@@ -703,6 +746,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         }
         if (MODE == BLOCK_SHRINK || MODE == BLOCK_ADAPT) ptx::griddep_wait();  // the tables
         uint32_t n = 0;
+        [[maybe_unused]] uint32_t flag_n = 0;  // ADAPT: units with blocks of u B before this one
         uint32_t flip = 0;     // which of two boxes (GRAD: pairs of them) is next
         // GRAD: bit b: parity of z_bar(b)'s next phase; a copy is on its way there
         uint32_t z_phase = 0, z_out = 0;
@@ -764,6 +808,15 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         }
                     }
                     __syncwarp();
+                }
+            };
+
+            // z of a unit's first two pieces (behind the team's last use of the boxes).
+            auto load_two = [&]() {
+                if constexpr (MODE == BLOCK_GRAD) {
+                    if (p.z_tma) team_sync();
+                    load_z(turn, flip);
+                    load_z(turn + 2, flip ^ 1u);
                 }
             };
 
@@ -854,7 +907,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         default: gated_grad_box<0>(box + frag_at, EPI_BOX_BYTES, v, h); break;
                     }
                     next();
-                    load_z(c + 2, b ^ 1u);
+                    if (c != turn) load_z(c + 2, b ^ 1u);  // (the first two came together)
                     ptx::fence_proxy_async_smem();
                     team_sync();
                     flush(box, &tmG, p.gate, 2, row0, limit, whole, f_box);
@@ -922,21 +975,58 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 }
                 return true;
             };
-            // ADAPT: adds the adapters whose B holds an infinity or NaN to
-            // their own rows.
+            // ADAPT: which of the unit's adapters hold an infinity or NaN in this
+            // CTA's features of B; they are added to their own rows below.
+            // Every warp looks through an eighth of each B's rows.
             bool flagged = false;
+            [[maybe_unused]] const uint32_t *flags = flag_words + (flag_n & 1u) * 8 * BLOCK_EPI_WARPS;
             if constexpr (MODE == BLOCK_ADAPT) {
-                bool bad = false;
-                for (int32_t i = lane; i < w.ad.count; i += 32) bad |= adapter_flagged(p, __ldcg(p.tab.ids + w.ad.first + i));
-                flagged = __any_sync(0xffffffffu, bad);
+                if (w.e0 < w.e1) {
+                    const int32_t a0 = ext_first(p, w), a1 = ext_end(p, w);
+                    const int32_t f = f0 + 8 * (lane & 15), r0 = 2 * (warp - 2) + (lane >> 4);
+                    for (int32_t at = a0; at < a1; at += 32) {
+                        const int32_t id = at + lane < a1 ? __ldcg(p.tab.ids + w.ad.first + at + lane) : 0;
+                        uint32_t word = 0;
+                        for (int32_t a = 0; a < min(32, a1 - at); a += 4) {
+                            uint32_t bad[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int32_t g = __shfl_sync(0xffffffffu, id, min(31, a + k));
+                                const uint16_t *b = p.b + g * p.strideB + f;
+                                if (a + k < a1 - at && f < p.N) {
+#pragma unroll 2
+                                    for (int32_t r = r0; r < p.R; r += 2 * BLOCK_EPI_WARPS) bad[k] |= has_non_finite(b + r * p.ldb, p.N - f);
+                                }
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (__any_sync(0xffffffffu, bad[k] != 0)) word |= 1u << ((a + k) & 31);
+                        }
+                        if (lane == 0) const_cast<uint32_t *>(flags)[(warp - 2) * 8 + ((at - a0) >> 5)] = word;
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(flag_bar);
+                    const int r = wait_bounded_warp(flag_bar, flag_n & 1u, wd);
+                    if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
+                    if (!agree(r == WAIT_OK, 1, 32 * BLOCK_EPI_WARPS)) break;
+                    uint32_t any = 0;
+                    for (int32_t k = lane; k < BLOCK_EPI_WARPS * 8; k += 32)
+                        if ((k & 7) * 32 < a1 - a0) any |= flags[k];
+                    flagged = __any_sync(0xffffffffu, any != 0);
+                    ++flag_n;
+                }
             }
             auto add_flagged = [&](int c, uint32_t (&v)[32]) {
                 if constexpr (MODE == BLOCK_ADAPT) {
                     if (!flagged) return;
                     const int32_t r0 = row_tile + 32 * c;
-                    for (int32_t i = 0; i < w.ad.count; ++i) {
+                    const int32_t a0 = ext_first(p, w), a1 = ext_end(p, w);
+                    for (int32_t i = a0; i < a1; ++i) {
                         const int32_t id = __ldcg(p.tab.ids + w.ad.first + i);
-                        if (!adapter_flagged(p, id)) continue;
+                        uint32_t bad = 0;
+                        for (int k = 0; k < BLOCK_EPI_WARPS; ++k) bad |= flags[k * 8 + ((i - a0) >> 5)] >> ((i - a0) & 31);
+                        // (in the share that has its first block)
+                        if (!(bad & 1u) || (p.Rp > 32 && i * (p.Rp / 32) < w.e0)) continue;
                         const int32_t lo = max(__ldcg(p.tab.lo + w.ad.first + i), r0);
                         const int32_t hi = min(__ldcg(p.tab.hi + w.ad.first + i), min(limit, r0 + 32));
 #pragma unroll
@@ -961,18 +1051,17 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
 
             uint32_t v[32];
             if (w.kb0 == w.kb1 && w.e0 == w.e1) {  // the empty sum
-                if (lanes_in) load_z(turn, flip);
+                if (lanes_in) load_two();
                 for (int c = turn; ok && lanes_in && c < pieces; c += 2) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0u;
-                    add_flagged(c, v);
                     ok = piece(c, v, [] {});
                 }
                 if (!ok) break;
                 zero_others(w, row_tile, limit);
                 continue;
             }
-            if (lanes_in && w.nparts == 1) load_z(turn, flip);
+            if (lanes_in && w.nparts == 1) load_two();
             const uint32_t buf = n & 1u;
             const uint32_t tph = (n >> 1) & 1u;
             ++n;
@@ -980,7 +1069,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             const int r = wait_bounded(tfull_bar(buf), tph, wd);
             if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
             const bool here = r == WAIT_OK;
-            if (!(w.nparts > 1 ? agree(here, 1, 32 * BLOCK_EPI_WARPS)
+            if (!(w.nparts > 1 || flagged ? agree(here, 1, 32 * BLOCK_EPI_WARPS)
                   : team == 1  ? __all_sync(0xffffffffu, here) != 0
                                : agree(here, team_id, 32 * team)))
                 break;
@@ -996,6 +1085,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 for (int c = turn; lanes_in && c < pieces; c += 2) {
                     load_piece(taddr + c * 32, v);
                     ptx::tmem_wait_ld(v);
+                    add_flagged(c, v);
 #pragma unroll
                     for (int j4 = 0; j4 < 8; ++j4)
                         __stcg(mine + (c * 8 + j4) * BM, make_float4(__uint_as_float(v[4 * j4]), __uint_as_float(v[4 * j4 + 1]),
@@ -1012,7 +1102,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
                 if (*last_flag) {
                     __threadfence();
-                    if (lanes_in) load_z(turn, flip);
+                    if (lanes_in) load_two();
                     for (int c = turn; ok && lanes_in && c < pieces; c += 2) {
                         float4 acc[8];
 #pragma unroll
@@ -1035,7 +1125,6 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                             v[4 * j4 + 2] = __float_as_uint(acc[j4].z);
                             v[4 * j4 + 3] = __float_as_uint(acc[j4].w);
                         }
-                        add_flagged(c, v);
                         ok = piece(c, v, [] {});
                     }
                     zero_others(w, row_tile, limit);
@@ -1061,6 +1150,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             }
             if (!ok) break;
             zero_others(w, row_tile, limit);
+            if (flagged) ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);  // its flags were read
         }
         // Rows of no group: zeros (SHRINK: of u and its parts).
         if (p.offsets) {

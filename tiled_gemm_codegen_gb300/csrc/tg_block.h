@@ -22,9 +22,7 @@ struct AdapterTables {
     int32_t *lo, *hi;  // [min(groups, S)] their rows
     int32_t *rank;     // [groups] place in ids (of groups that have rows)
     int4 *tile;        // [row tiles] place of the tile's first adapter, adapters of its rows, first block
-    uint8_t *flags;    // [groups][ADAPT_FLAGS] B_g holds an infinity or NaN
 };
-constexpr int ADAPT_FLAGS = 8;
 
 struct BlockParams {
     const int32_t *offsets;  // [groups + 1]; null: one group of all rows
@@ -47,7 +45,7 @@ struct BlockParams {
     uint16_t *wide;          // u's parts: [block][bn rows][64]
     int32_t R, Rp;
     int32_t wide_bn;         // rows of ADAPT's tiles
-    const uint16_t *b;       // B (as the caller gave it), for flagged adapters
+    const uint16_t *b;       // B, rows on 16 bytes: looked through for infinities and NaN
     int64_t ldb, strideB;
     int32_t b_shared;        // 1 = every adapter has the same B
     // shares of tiles
@@ -68,6 +66,10 @@ __host__ __device__ inline int32_t adapter_blocks(int32_t count, int32_t Rp)
 // Staging boxes of 32 rows of 128 bytes: eight, GRAD sixteen (z of two pieces a
 // team of two warps; dZ takes z's place).
 __host__ __device__ constexpr int block_epi_bytes(int mode) { return mode == BLOCK_GRAD ? 65536 : 32768; }
+
+// Barriers, and ADAPT's flagged adapters: for two units in turn a bit an
+// adapter from each epilogue warp.
+__host__ __device__ constexpr int block_bar_bytes(int mode) { return mode == BLOCK_ADAPT ? 1024 : 512; }
 
 constexpr int BLOCK_EPI_WARPS = 8;
 constexpr int BLOCK_THREADS = 64 + 32 * BLOCK_EPI_WARPS;

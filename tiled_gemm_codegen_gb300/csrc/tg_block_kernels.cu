@@ -13,7 +13,7 @@ template <int BN, int STAGES, bool PAIR>
 BlockShape shape()
 {
     using G = Geometry<BN, PAIR>;
-    constexpr int bytes = STAGES * G::STAGE + block_epi_bytes(TG_BLOCK_MODE) + G::BAR_BYTES + G::ALIGN_SLACK;
+    constexpr int bytes = STAGES * G::STAGE + block_epi_bytes(TG_BLOCK_MODE) + block_bar_bytes(TG_BLOCK_MODE) + G::ALIGN_SLACK;
     constexpr int smem = bytes > G::ONE_CTA_PER_SM ? bytes : G::ONE_CTA_PER_SM;
     static_assert(smem <= SMEM_LIMIT, "shared memory budget");
     return {block_kernel<TG_BLOCK_MODE, BN, STAGES, PAIR>, BN, smem, PAIR};
