@@ -31,25 +31,27 @@ __device__ __forceinline__ void split_parts(float x, __nv_bfloat16 &hi, __nv_bfl
     }
 }
 
-// Where a row's parts for adapter i of its tile begin (row `in` of the tile,
-// whose blocks begin at blk0), in units of 8 values.
-__device__ __forceinline__ int32_t adapter_unit(int32_t i, int32_t blk0, int32_t in, int32_t bn, int32_t Rp)
+// Where hi of value r of a row's u stands for adapter i of its tile (row `in`
+// of the tile, whose blocks begin at blk0), in values; lo stands a block,
+// bn * 64 values, behind it.  r a multiple of 8: 16 bytes.
+__device__ __forceinline__ int64_t adapter_at(int32_t i, int32_t r, int32_t blk0, int32_t in, int32_t bn, int32_t Rp)
 {
-    const int32_t per = Rp <= 32 ? 32 / Rp : 1;
-    const int32_t blk = blk0 + (Rp <= 32 ? i / per : i * (Rp / 32));
-    return (blk * bn + in) * 8 + (Rp <= 32 ? i % per * (Rp / 4) : 0);
+    const int32_t col = i * Rp + r;
+    return (static_cast<int64_t>(blk0 + (col >> 6) * 2) * bn + in) * 64 + (col & 63);
 }
 
 // Zeros in row `in` of a tile's blocks (count adapters) but for adapter i's
 // columns (-1: all of them).  A warp a row.
 __device__ __forceinline__ void zero_columns(const BlockParams &p, int32_t in, int32_t blk0, int32_t count, int32_t i, int lane)
 {
-    const int32_t units = p.Rp <= 32 ? p.Rp / 4 : p.Rp / 32 * 8;  // 16 bytes each, an adapter's
-    const int32_t own = i * units, own_end = i < 0 ? own : own + units;
-    for (int32_t k = lane; k < adapter_blocks(count, p.Rp) * 8; k += 32)
-        if (k < own || k >= own_end)
-            *reinterpret_cast<uint4 *>(p.wide + (static_cast<int64_t>(blk0 + (k >> 3)) * p.wide_bn + in) * 64 + (k & 7) * 8) =
-                make_uint4(0u, 0u, 0u, 0u);
+    const int32_t own = i < 0 ? -1 : i * (p.Rp / 8), end = own + p.Rp / 8;  // its 16 bytes of hi
+    const int32_t all = adapter_blocks(count, p.Rp) * 4;
+    for (int32_t k = lane; k < all; k += 32)
+        if (own < 0 || k < own || k >= end) {
+            uint16_t *at = p.wide + adapter_at(0, k * 8, blk0, in, p.wide_bn, 0);
+            *reinterpret_cast<uint4 *>(at) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(at + static_cast<int64_t>(p.wide_bn) * 64) = make_uint4(0u, 0u, 0u, 0u);
+        }
 }
 
 }  // namespace tg

@@ -126,7 +126,8 @@ __device__ __forceinline__ int32_t write_tables(const BlockParams &p, int32_t ti
 }
 
 constexpr int TABLE_THREADS = 1024;
-constexpr int ROWS_THREADS = 512;
+constexpr int ROWS_THREADS = 128;
+constexpr int ROWS_GROUPS = 512;  // groups adapter_rows_kernel takes at most
 
 __global__ void __launch_bounds__(TABLE_THREADS) adapter_tables_kernel(const BlockParams p, int32_t tiles)
 {
@@ -155,18 +156,18 @@ __device__ __forceinline__ uint4 load8(const uint16_t *row, int32_t k, int32_t K
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One warp's whole steps of 32 k, DEPTH steps' loads at a time: rows t / 4, and
-// with HIGH rows 8 + t / 4, against TILES_R tiles of 8 of R.
+// A warp's whole steps of 32 k - from `s` on every `by`-th - DEPTH steps' loads
+// at a time: rows t / 4, and with HIGH rows 8 + t / 4, against TILES_R tiles of 8
+// of R.
 template <int TILES_R, bool HIGH, int DEPTH>
-__device__ __forceinline__ void rows_sums(const uint16_t *x0, const uint16_t *x1, const uint16_t *const (&w)[4], int t, int warp,
-                                          int32_t steps, float (&c)[4][4])
+__device__ __forceinline__ void rows_sums(const uint16_t *x0, const uint16_t *x1, const uint16_t *const (&w)[4], int t, int32_t s,
+                                          int32_t by, int32_t steps, float (&c)[4][4])
 {
-    constexpr int WARPS = ROWS_THREADS / 32;
-    for (int32_t s = warp; s < steps; s += DEPTH * WARPS) {
+    for (; s < steps; s += DEPTH * by) {
         uint4 xa[DEPTH], xb[DEPTH], wv[DEPTH][TILES_R];
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
-            const int32_t k = min(s + d * WARPS, steps - 1) * 32 + 8 * t;
+            const int32_t k = min(s + d * by, steps - 1) * 32 + 8 * t;
             xa[d] = __ldg(reinterpret_cast<const uint4 *>(x0 + k));
             xb[d] = HIGH ? __ldg(reinterpret_cast<const uint4 *>(x1 + k)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
@@ -174,7 +175,7 @@ __device__ __forceinline__ void rows_sums(const uint16_t *x0, const uint16_t *x1
         }
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
-            if (s + d * WARPS >= steps) break;
+            if (s + d * by >= steps) break;
 #pragma unroll
             for (int i = 0; i < TILES_R; ++i) {
                 mma_16x8x16(c[i], xa[d].x, xb[d].x, xa[d].y, xb[d].y, wv[d][i].x, wv[d][i].y);
@@ -184,102 +185,52 @@ __device__ __forceinline__ void rows_sums(const uint16_t *x0, const uint16_t *x1
     }
 }
 
-// Few rows an adapter (decoding): the tables and u in one launch, so that
-// ADAPT's shared projection, which starts beside it, waits for
-// little.  Block 0: the tables; the others: 16 rows of one group each,
-// K split over the block's 16 warps, 32 R at a time.  A lane's 16 bytes of X and of A are two MMAs' fragments: any order of k will do where
-// both operands have the same.  Bound by latency: offsets, one
-// round of loads, the warps' sums.
-__global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockParams p, const uint16_t *X, int64_t ldx, const uint16_t *A,
-                                                                    int64_t lda, int64_t strideA, int32_t K, int32_t tiles,
-                                                                    int32_t stride)
+// One chunk of 16 rows of a group by a cluster (adapter_rows_kernel).  bounds: the
+// groups' ends; chunks: the chunks (low half) and groups with rows up to each.
+__device__ __forceinline__ void rows_chunk(const BlockParams &p, const uint16_t *X, int64_t ldx, const uint16_t *A, int64_t lda,
+                                           int64_t strideA, int32_t K, int32_t stride, int32_t cluster, int32_t rank, int32_t want,
+                                           int32_t first_row, const int32_t *bounds, const int32_t *chunks, int32_t *found,
+                                           float (&sums)[ROWS_THREADS / 32][16][33])
 {
-    ptx::griddep_launch_dependents();
     constexpr int WARPS = ROWS_THREADS / 32;
-    __shared__ int32_t part[32], his[ROWS_THREADS];
-    __shared__ int32_t found[8];  // group, first row, rows, place; adapters before and in the (two) tiles
-    __shared__ float sums[WARPS][16][33];
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-    if (blockIdx.x == 0) {
-        const int32_t used = write_tables<ROWS_THREADS>(p, tiles, stride, part, his);
-        // rows of no group: zeros
-        const int32_t first = max(0, min(__ldg(p.offsets), p.S)), last = used > 0 ? p.tab.hi[used - 1] : first;
-        for (int32_t i = warp; i < first + p.S - last; i += WARPS) {
-            const int32_t row = i < first ? i : last + i - first, tile = row / p.wide_bn;
-            zero_columns(p, row % p.wide_bn, tile * stride, p.tab.tile[tile].y, -1, lane);
-            for (int32_t r = lane; p.out0.p && r < p.R; r += 32)
-                static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = 0;
-        }
-        return;
-    }
-    // the chunk's group: chunks are counted group by group
-    const int32_t want = static_cast<int32_t>(blockIdx.x) - 1;
-    if (tid < 8) found[tid] = tid == 0 ? -1 : 0;
+    __syncthreads();  // the chunk before is done with found
+    if (tid < 8) found[tid] = 0;
     __syncthreads();
-    {
-        int32_t before = 0;  // chunks of the groups before this turn's
-        int32_t last = max(0, min(__ldg(p.offsets), p.S)), used = 0;
-        for (int32_t g0 = 0; g0 < p.groups; g0 += ROWS_THREADS) {
-            const int32_t g = g0 + tid;
-            int32_t hi = g < p.groups ? max(0, min(__ldg(p.offsets + g + 1), p.S)) : 0;
-            hi = block_scan<ROWS_THREADS, true>(max(hi, last), part);
-            his[tid] = hi;
-            __syncthreads();
-            const int32_t lo = tid > 0 ? his[tid - 1] : last;
-            const int32_t rows = g < p.groups ? hi - lo : 0;
-            // chunks in the low bits' place, groups with rows above: one scan
-            const int32_t n = (rows + 15) / 16, has = rows > 0;
-            const int32_t at_n = before + block_scan<ROWS_THREADS, false>(n, part) - n;
-            const int32_t all_n = part[WARPS - 1];
-            const int32_t at = used + block_scan<ROWS_THREADS, false>(has, part) - has;
-            if (want >= at_n && want < at_n + n) {
-                found[0] = g;
-                found[1] = lo + (want - at_n) * 16;
-                found[2] = min(16, hi - found[1]);
-                found[3] = at;
-            }
-            last = his[ROWS_THREADS - 1];
-            before += all_n;
-            used += part[WARPS - 1];
-            __syncthreads();
-        }
+    for (int32_t i = tid; i < p.groups; i += ROWS_THREADS) {
+        const int32_t end = chunks[i], before = i > 0 ? chunks[i - 1] : 0;
+        if (want < (before & 0xffff) || want >= (end & 0xffff)) continue;
+        const int32_t row0 = (i > 0 ? bounds[i - 1] : first_row) + (want - (before & 0xffff)) * 16;
+        found[0] = i;
+        found[1] = row0;
+        found[2] = min(16, bounds[i] - row0);
+        found[3] = before >> 16;
     }
-    const int32_t g = found[0], row0 = found[1], rows = found[2];
-    if (g < 0) return;
+    __syncthreads();
+    const int32_t g = found[0], row0 = found[1], rows = found[2], place = found[3];
     // the adapters before and in the tiles of its rows (two at most)
     const int32_t t0 = row0 / p.wide_bn, t1 = (row0 + rows - 1) / p.wide_bn;
-    if (p.groups <= ROWS_THREADS) {
-        // (every group's bounds are in his, and its own thread counts it)
-        const int32_t first_row = max(0, min(__ldg(p.offsets), p.S));
-        const int32_t hi = his[tid], lo = tid > 0 ? his[tid - 1] : first_row;
-        const bool has = tid < p.groups && hi > lo;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int32_t r0 = (k ? t1 : t0) * p.wide_bn, r1 = r0 + p.wide_bn;
-            const int32_t b = __syncthreads_count(has && hi <= r0), c = __syncthreads_count(has && hi > r0 && lo < r1);
-            if (tid == 0) {
-                found[4 + 2 * k] = b;
-                found[5 + 2 * k] = c;
-            }
-        }
-    } else {
+    {
         int32_t b[2] = {0, 0}, c[2] = {0, 0};
-        each_group<ROWS_THREADS>(p, part, his, [&](int32_t, int32_t lo, int32_t hi, int32_t) {
+        for (int32_t i = tid; i < p.groups; i += ROWS_THREADS) {
+            const int32_t hi = bounds[i], lo = i > 0 ? bounds[i - 1] : first_row;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int32_t r0 = (k ? t1 : t0) * p.wide_bn, r1 = r0 + p.wide_bn;
-                b[k] += hi <= r0;
-                c[k] += hi > r0 && lo < r1;
+                b[k] += hi > lo && hi <= r0;
+                c[k] += hi > lo && hi > r0 && lo < r1;
             }
-        });
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            if (b[k]) atomicAdd(&found[4 + 2 * k], b[k]);
-            if (c[k]) atomicAdd(&found[5 + 2 * k], c[k]);
+            b[k] = __reduce_add_sync(0xffffffffu, b[k]);
+            c[k] = __reduce_add_sync(0xffffffffu, c[k]);
+            if (lane == 0) {
+                atomicAdd(&found[4 + 2 * k], b[k]);
+                atomicAdd(&found[5 + 2 * k], c[k]);
+            }
         }
     }
-    __syncthreads();
-    const int32_t place = found[3];
 
     // sums over this warp's share of K
     const int gid = lane >> 2, t = lane & 3;
@@ -287,6 +238,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
     const uint16_t *x1 = X + static_cast<int64_t>(row0 + min(gid + 8, rows - 1)) * ldx;
     const float scale = p.scales ? __ldg(p.scales + g) : 1.0f;
     const int32_t steps = K / 32;  // whole ones
+    const int32_t me = rank * WARPS + warp, all = cluster * WARPS;
     for (int32_t r0 = 0; r0 < p.R; r0 += 32) {
         const int tiles_r = min(4, (p.R - r0 + 7) / 8);
         float c[4][4];
@@ -298,19 +250,14 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = A + g * strideA + static_cast<int64_t>(min(r0 + 8 * i + gid, p.R - 1)) * lda;
         // (a call for each number of tiles keeps the loads free of branches, so that all of a round are under way at once)
-        if (rows <= 8) {
-            if (tiles_r > 2)
-                rows_sums<4, false, 4>(x0, x1, w, t, warp, steps, c);
-            else if (tiles_r == 2)
-                rows_sums<2, false, 8>(x0, x1, w, t, warp, steps, c);
-            else
-                rows_sums<1, false, 8>(x0, x1, w, t, warp, steps, c);
-        } else if (tiles_r > 2) {
-            rows_sums<4, true, 4>(x0, x1, w, t, warp, steps, c);
-        } else {
-            rows_sums<2, true, 4>(x0, x1, w, t, warp, steps, c);
-        }
-        if (warp == WARPS - 1 && steps * 32 < K) {  // the last, partial step
+        if (rows > 8)
+            rows_sums<4, true, 2>(x0, x1, w, t, me, all, steps, c);
+        else if (tiles_r > 2)
+            rows_sums<4, false, 4>(x0, x1, w, t, me, all, steps, c);
+        else
+            rows_sums<2, false, 4>(x0, x1, w, t, me, all, steps, c);
+        if (r0 + 32 >= p.R) ptx::griddep_launch_dependents();  // (nothing left to draw)
+        if (me == all - 1 && steps * 32 < K) {  // the last, partial step
             const int32_t k = steps * 32 + 8 * t;
             const uint4 xa = load8(x0, k, K), xb = rows > 8 ? load8(x1, k, K) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
@@ -320,42 +267,122 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
                 mma_16x8x16(c[i], xa.z, xb.z, xa.w, xb.w, wv.z, wv.w);
             }
         }
-        __syncthreads();  // the sums of the turn before were read
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) sums[warp][gid + (e >> 1) * 8][8 * i + 2 * t + (e & 1)] = c[i][e];
         __syncthreads();
-        // a thread a value
-        const int32_t in = tid >> 5, r = r0 + lane;
-        if (in < rows && r < p.Rp) {
-            float x = 0.0f;
+        for (int v = tid; v < 512; v += ROWS_THREADS) {
+            float x = sums[0][v >> 5][v & 31];
 #pragma unroll
-            for (int k = 0; k < WARPS; ++k) x = __fadd_rn(x, sums[k][in][lane]);
+            for (int k = 1; k < WARPS; ++k) x = __fadd_rn(x, sums[k][v >> 5][v & 31]);
+            sums[0][v >> 5][v & 31] = x;
+        }
+        if (cluster > 1)
+            ptx::cluster_sync_all();
+        else
+            __syncthreads();
+        // a thread a value (each CTA its share of them), the CTAs' sums in order
+        const int32_t count = 512 / cluster;
+        for (int32_t v = rank * count + tid; v < (rank + 1) * count; v += ROWS_THREADS) {
+            const int32_t in = v >> 5, r = r0 + (v & 31);
+            if (in >= rows || r >= p.Rp) continue;
+            const uint32_t at0 = ptx::smem_addr(&sums[0][in][v & 31]);
+            float x = 0.0f;
+            if (cluster > 1) {
+                float y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = k < cluster ? __uint_as_float(ptx::ld_cluster_u32(ptx::map_to_cta(at0, k))) : 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x = __fadd_rn(x, y[k]);
+            } else {
+                x = sums[0][in][v & 31];
+            }
             x = r < p.R ? __fmul_rn(scale, x) : 0.0f;  // (columns past R meet zeros)
             __nv_bfloat16 hi, lo;
             split_parts(x, hi, lo);
             const int32_t row = row0 + in, tile = row / p.wide_bn, k = tile == t0 ? 0 : 1;
-            const int32_t unit = adapter_unit(place - found[4 + 2 * k], tile * stride, row % p.wide_bn, p.wide_bn, p.Rp);
-            uint16_t *at = p.wide + static_cast<int64_t>(unit) * 8 + (p.Rp <= 32 ? r : r / 64 * 2 * p.wide_bn * 64 + (r & 63));
+            uint16_t *at = p.wide + adapter_at(place - found[4 + 2 * k], r, tile * stride, row % p.wide_bn, p.wide_bn, p.Rp);
             at[0] = __bfloat16_as_ushort(hi);
-            at[p.Rp <= 32 ? p.Rp : static_cast<int64_t>(p.wide_bn) * 64] = __bfloat16_as_ushort(lo);
+            at[static_cast<int64_t>(p.wide_bn) * 64] = __bfloat16_as_ushort(lo);
             if (p.out0.p && r < p.R)
-                static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+                static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = __bfloat16_as_ushort(hi);
         }
+        if (cluster > 1)  // the sums were read
+            ptx::cluster_sync_all();
+        else
+            __syncthreads();
     }
     // columns from R's last 32 to Rp's end, and the other adapters'
-    for (int32_t in = warp; in < rows; in += WARPS) {
+    for (int32_t in = me; in < rows; in += all) {
         const int32_t row = row0 + in, tile = row / p.wide_bn, k = tile == t0 ? 0 : 1;
         const int32_t i = place - found[4 + 2 * k];
         zero_columns(p, row % p.wide_bn, tile * stride, found[5 + 2 * k], i, lane);
         for (int32_t r = (p.R + 31) / 32 * 32 + lane; r < p.Rp; r += 32) {
-            uint16_t *at = p.wide + static_cast<int64_t>(adapter_unit(i, tile * stride, row % p.wide_bn, p.wide_bn, p.Rp)) * 8 +
-                           r / 64 * 2 * p.wide_bn * 64 + (r & 63);
+            uint16_t *at = p.wide + adapter_at(i, r, tile * stride, row % p.wide_bn, p.wide_bn, p.Rp);
             at[0] = 0;
             at[static_cast<int64_t>(p.wide_bn) * 64] = 0;
         }
     }
+}
+
+// Few rows an adapter (decoding): the tables and u in one launch, so that
+// ADAPT's shared projection, which starts beside it, waits for little.  Cluster
+// 0: the tables; the others: 16 rows of one group each, K split over the
+// cluster's warps (an SM alone draws some 50 GB/s: 128 KB of an adapter, R = 16, K =
+// 4096, would take it 3 us), 32 R at a time.  A lane's 16 bytes of X and of A
+// are two MMAs' fragments: any order of k will do where both operands have the
+// same.  Bound by latency: offsets, one round of loads, the warps' and the
+// cluster's sums.  The shared projection starts beside a few blocks (`early`), but
+// behind the loads of many: its own would fill the memory's queues, and each
+// round of theirs would take 2.5 us instead of one.
+__global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockParams p, const uint16_t *X, int64_t ldx, const uint16_t *A,
+                                                                    int64_t lda, int64_t strideA, int32_t K, int32_t tiles,
+                                                                    int32_t stride, int32_t cluster, int32_t early)
+{
+    if (early) ptx::griddep_launch_dependents();
+    constexpr int WARPS = ROWS_THREADS / 32;
+    __shared__ int32_t part[32], bounds[ROWS_GROUPS], chunks[ROWS_GROUPS];
+    __shared__ int32_t found[8];  // group, first row, rows, place; adapters before and in the (two) tiles
+    __shared__ float sums[WARPS][16][33];
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int32_t rank = cluster > 1 ? static_cast<int32_t>(ptx::cluster_ctarank()) : 0;
+    const int32_t cid = static_cast<int32_t>(blockIdx.x) / cluster;
+    if (cid == 0) {
+        if (rank > 0) return;
+        const int32_t used = write_tables<ROWS_THREADS>(p, tiles, stride, part, bounds);
+        // rows of no group: zeros
+        const int32_t first = max(0, min(__ldg(p.offsets), p.S)), last = used > 0 ? p.tab.hi[used - 1] : first;
+        for (int32_t i = warp; i < first + p.S - last; i += WARPS) {
+            const int32_t row = i < first ? i : last + i - first, tile = row / p.wide_bn;
+            zero_columns(p, row % p.wide_bn, tile * stride, p.tab.tile[tile].y, -1, lane);
+            for (int32_t r = lane; p.out0.p && r < p.R; r += 32)
+                static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = 0;
+        }
+        return;
+    }
+    // chunks of 16 rows, counted group by group (with the groups that have rows
+    // above them in one sum: few rows, few groups)
+    const int32_t first_row = max(0, min(__ldg(p.offsets), p.S));
+    int32_t total = 0;
+    {
+        int32_t last = first_row;
+        for (int32_t g0 = 0; g0 < p.groups; g0 += ROWS_THREADS) {
+            const int32_t g = g0 + tid;
+            int32_t hi = g < p.groups ? max(0, min(__ldg(p.offsets + g + 1), p.S)) : 0;
+            hi = block_scan<ROWS_THREADS, true>(max(hi, last), part);
+            last = part[WARPS - 1];
+            bounds[g] = hi;  // (ROWS_GROUPS is a multiple of the block)
+            __syncthreads();
+            const int32_t rows = g < p.groups ? hi - (g > 0 ? bounds[g - 1] : first_row) : 0;
+            chunks[g] = total + block_scan<ROWS_THREADS, false>((rows + 15) / 16 | (rows > 0) << 16, part);
+            total += part[WARPS - 1];
+        }
+        total &= 0xffff;
+    }
+    const int32_t n_clusters = static_cast<int32_t>(gridDim.x) / cluster - 1;
+    for (int32_t want = cid - 1; want < total; want += n_clusters)
+        rows_chunk(p, X, ldx, A, lda, strideA, K, stride, cluster, rank, want, first_row, bounds, chunks, found, sums);
 }
 
 // ------------------------------------------------------------ launches
@@ -641,10 +668,9 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     const int64_t tiles = cdiv(S, cy.bn);
     // Few rows: u by adapter_rows_kernel, a fixed number of blocks a tile.
     const int64_t stride = adapter_blocks(static_cast<int32_t>(std::min(cy.bn, hit)), static_cast<int32_t>(Rp));
-    const bool few = S <= ADAPT_FEW_ROWS && tiles * stride * cy.bn * 128 <= ADAPT_FEW_BYTES;
+    const bool few = S <= ADAPT_FEW_ROWS && groups <= ROWS_GROUPS && tiles * stride * cy.bn * 128 <= ADAPT_FEW_BYTES;
     // Else a tile's blocks round its adapters up; together at most so many.
-    const int64_t blocks = few ? tiles * stride
-                           : Rp <= 32 ? std::min(tiles + hit, tiles + cdiv((tiles + hit) * Rp, 32)) : (tiles + hit) * (Rp / 32);
+    const int64_t blocks = few ? tiles * stride : 2 * (tiles + cdiv((tiles + hit) * Rp, 64));
     if (blocks * cy.bn > INT32_MAX / 8) return TG_ERR_UNSUPPORTED;
 
     BlockParams p{};
@@ -697,43 +723,59 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     p.ldb = b.ld;
     p.strideB = b.nb > 1 ? b.stride : 0;
 
+    // both kernels' arguments first: the second starts beside the first
+    const bool pair = cy.tiles == TILES_PAIR;
+    BlockParams py = p;
+    py.groups = 1;
+    py.N = static_cast<int32_t>(N);
+    py.w_k = w_k ? 1 : 0;
+    py.out_bf16 = out_bf16 ? 1 : 0;
+    py.out0 = output(&m.o, Y, S, N, ldy, out_bf16 ? 2 : 4);
+    set_cut(py, cy, N);
+    const uint32_t rows_box = static_cast<uint32_t>(pair ? cy.bn / 2 : cy.bn);
+    const Operand wide{p.wide, blocks * cy.bn, 64, 64, 1, 0};
+    if ((K > 0 && (!map_operand(&m.x, x, rows_box) || !map_operand(&m.w, w, w_k ? BM : BK))) ||
+        !map_operand(&m.v, b, static_cast<uint32_t>(std::min<int64_t>(Rp, 64))) || !map_operand(&m.e, wide, rows_box))
+        return TG_ERR_CUDA;
     p.offsets = offsets;
     p.groups = static_cast<int32_t>(groups);
     p.N = static_cast<int32_t>(R);
     p.out0 = BlockOut{U, ldu, 0};
     if (few) {
-        adapter_rows_kernel<<<static_cast<unsigned>(1 + S / 16 + hit), ROWS_THREADS, 0, hs.stream>>>(
-            p, static_cast<const uint16_t *>(x.p), x.ld, static_cast<const uint16_t *>(a.p), a.ld, a_shared ? 0 : a.stride,
-            static_cast<int32_t>(K), static_cast<int32_t>(tiles), static_cast<int32_t>(stride));
-        if ((e = cudaGetLastError()) != cudaSuccess) return host_cuda_status(e);
+        // at most four steps of 32 k a warp, and no more blocks than run at once
+        int32_t cluster = 1;
+        const int64_t clusters = std::min<int64_t>(1 + S / 16 + hit, 4 * hs.sms);
+        while (cluster < 8 && K > 512 * cluster && clusters * cluster * 2 <= 4 * hs.sms) cluster *= 2;
+        const bool early = clusters * cluster <= hs.sms / 4;
+        py.ext_first = !early && !pair && cy.units * cy.splits <= hs.sms ? 1 : 0;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
+        cfg.blockDim = dim3(ROWS_THREADS);
+        cfg.stream = hs.stream;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, adapter_rows_kernel, p, static_cast<const uint16_t *>(x.p), x.ld, static_cast<const uint16_t *>(a.p),
+                               a.ld, a_shared ? int64_t(0) : a.stride, static_cast<int32_t>(K), static_cast<int32_t>(tiles),
+                               static_cast<int32_t>(stride), cluster, early ? 1 : 0);
+        if (e != cudaSuccess) return host_cuda_status(e);
     } else {
+        BlockMaps ma;
+        if (K > 0 && (!map_operand(&ma.x, x, static_cast<uint32_t>(ca.bn)) || !map_operand(&ma.w, a, BM))) return TG_ERR_CUDA;
         adapter_tables_kernel<<<1, TABLE_THREADS, 0, hs.stream>>>(p, static_cast<int32_t>(tiles));
         if ((e = cudaGetLastError()) != cudaSuccess) return host_cuda_status(e);
-        BlockParams pa = p;
-        pa.w_k = 1;
-        pa.w_shared = a_shared ? 1 : 0;
-        pa.out_bf16 = 1;
-        pa.partials = reinterpret_cast<float *>(arena + at_part_a);
-        pa.counters = counters;
-        set_cut(pa, ca, R);
-        if (K > 0 && (!map_operand(&m.x, x, static_cast<uint32_t>(ca.bn)) || !map_operand(&m.w, a, BM))) return TG_ERR_CUDA;
-        if ((e = launch_block(BLOCK_SHRINK, ca.tiles, hs, ca.units * ca.splits, m, pa)) != cudaSuccess) return host_cuda_status(e);
+        p.w_k = 1;
+        p.w_shared = a_shared ? 1 : 0;
+        p.out_bf16 = 1;
+        p.partials = reinterpret_cast<float *>(arena + at_part_a);
+        p.counters = counters;
+        set_cut(p, ca, R);
+        if ((e = launch_block(BLOCK_SHRINK, ca.tiles, hs, ca.units * ca.splits, ma, p)) != cudaSuccess) return host_cuda_status(e);
     }
-
-    // Y
-    const bool pair = cy.tiles == TILES_PAIR;
-    p.offsets = nullptr;
-    p.groups = 1;
-    p.N = static_cast<int32_t>(N);
-    p.w_k = w_k ? 1 : 0;
-    p.out_bf16 = out_bf16 ? 1 : 0;
-    p.out0 = output(&m.o, Y, S, N, ldy, out_bf16 ? 2 : 4);
-    set_cut(p, cy, N);
-    const uint32_t rows_box = static_cast<uint32_t>(pair ? cy.bn / 2 : cy.bn);
-    if (K > 0 && (!map_operand(&m.x, x, rows_box) || !map_operand(&m.w, w, w_k ? BM : BK))) return TG_ERR_CUDA;
-    const Operand wide{p.wide, blocks * cy.bn, 64, 64, 1, 0};
-    if (!map_operand(&m.v, b, static_cast<uint32_t>(std::min<int64_t>(Rp, 64))) || !map_operand(&m.e, wide, rows_box)) return TG_ERR_CUDA;
-    return host_cuda_status(launch_block(BLOCK_ADAPT, cy.tiles, hs, cy.units * cy.splits, m, p));
+    return host_cuda_status(launch_block(BLOCK_ADAPT, cy.tiles, hs, cy.units * cy.splits, m, py));
 }
 
 bool act_ok(int32_t act) { return act >= TG_ACT_NONE && act <= TG_ACT_SILU; }

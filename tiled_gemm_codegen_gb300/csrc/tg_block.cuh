@@ -27,14 +27,15 @@
 //
 // ADAPT: rows of several adapters share a tile (decoding: a row or two each).
 // For a row tile with c adapters the contraction is extended by blocks of 64 k
-// in which every adapter has columns of its own; a row's u stands in its
-// adapter's columns and zeros in the others'.  u is fp32 and meets bf16 B, so
-// it goes in as two bf16 parts, hi + lo (17 bits or more): columns [hi | lo] of Rp = R
-// rounded up to 8, 16 or 32 each, both against the same rows of B (32 / Rp
-// adapters a block), or for R > 32 blocks of 64 of hi, then of lo.  The zeros
+// in which every adapter has Rp columns of its own (R rounded up to 8, 16, 32
+// or a multiple of 64); a row's u stands in its adapter's columns and zeros in the
+// others'.  u is fp32 and meets bf16 B, so it goes in as two bf16 parts, hi + lo (17
+// bits or more), two blocks with the same 64 rows of B: a pair of ring slots
+// of which the second holds lo alone, its MMAs reading the first one's B.  The zeros
 // of other adapters' rows must not meet an infinity or NaN in B (0 x NaN is
-// NaN): B_g that hold one are flagged by the table kernel, go in as zeros and
-// are added by the epilogue, row by row of their own.
+// NaN): the epilogue's warps, idle until then, look through the tile's features
+// of each B; those that hold one go in as zeros and are added by the
+// epilogue, to their own rows alone.
 #pragma once
 
 #include "tg_adapter.cuh"
@@ -46,7 +47,8 @@ namespace tg {
 struct BlockUnit {
     int32_t g, row0, row1, tm, tn;
     int32_t kb0, kb1;      // this worker's k-blocks of the tile (ADAPT: of X W)
-    int32_t e0, e1;        // ADAPT: its blocks of u B, once known (ext_range)
+    int32_t mid;           // ADAPT: before this one come its blocks of u B ..
+    int32_t e0, e1;        // .. e0 to e1, once known (ext_range)
     AdapterTile ad;
     int32_t part, nparts, tile;
 };
@@ -128,6 +130,7 @@ __device__ __forceinline__ bool block_walk_to(const BlockParams &p, int64_t t64,
     u.tn = in / rows;
     u.kb0 = static_cast<int32_t>(static_cast<int64_t>(u.part) * p.k_blocks / u.nparts);
     u.kb1 = static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * p.k_blocks / u.nparts);
+    u.mid = p.ext_first ? u.kb0 : u.kb1;
     u.e0 = u.e1 = 0;
     u.ad = {0, 0, 0};
     return true;
@@ -139,18 +142,24 @@ __device__ __forceinline__ void ext_range(const BlockParams &p, BlockUnit &u)
     ptx::griddep_wait();
     u.ad = adapter_tile(p, u.tm);
     const int32_t n = adapter_blocks(u.ad.count, p.Rp);
-    u.e0 = static_cast<int32_t>(static_cast<int64_t>(u.part) * n / u.nparts);
-    u.e1 = static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * n / u.nparts);
+    u.e0 = 2 * static_cast<int32_t>(static_cast<int64_t>(u.part) * (n / 2) / u.nparts);  // pairs stay together
+    u.e1 = 2 * static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * (n / 2) / u.nparts);
 }
 
 // ADAPT: the adapters (of the tile's) whose columns lie in a unit's blocks.
-__device__ __forceinline__ int32_t ext_first(const BlockParams &p, const BlockUnit &u)
-{
-    return p.Rp <= 32 ? u.e0 * (32 / p.Rp) : u.e0 / (p.Rp / 32);
-}
+__device__ __forceinline__ int32_t ext_first(const BlockParams &p, const BlockUnit &u) { return u.e0 * 32 / p.Rp; }
 __device__ __forceinline__ int32_t ext_end(const BlockParams &p, const BlockUnit &u)
 {
-    return min(u.ad.count, p.Rp <= 32 ? u.e1 * (32 / p.Rp) : (u.e1 - 1) / (p.Rp / 32) + 1);
+    return min(u.ad.count, (u.e1 * 32 + p.Rp - 1) / p.Rp);
+}
+
+// Whether one of eight bf16 is an infinity or NaN: adding the lowest bit of an
+// exponent of ones carries out of it.
+__device__ __forceinline__ bool non_finite(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    const uint32_t x = ((a & 0x7f807f80u) + 0x00800080u) | ((b & 0x7f807f80u) + 0x00800080u) | ((c & 0x7f807f80u) + 0x00800080u) |
+                       ((d & 0x7f807f80u) + 0x00800080u);
+    return (x & 0x80008000u) != 0;
 }
 
 // Whether one of the first n of 8 bf16 on 16 bytes is an infinity or NaN.
@@ -158,10 +167,7 @@ __device__ __forceinline__ bool has_non_finite(const uint16_t *b, int32_t n)
 {
     if (n >= 8) {
         const uint4 x = __ldg(reinterpret_cast<const uint4 *>(b));
-        // exponents of ones: adding the lowest exponent bit carries out of them
-        const uint32_t lo = ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
-                            ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
-        return (lo & 0x80008000u) != 0;
+        return non_finite(x.x, x.y, x.z, x.w);
     }
     bool bad = false;
     for (int32_t e = 0; e < n; ++e) bad |= (__ldg(b + e) & 0x7f80u) == 0x7f80u;
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     constexpr int EPI_ROWS = 32, EPI_ROW_BYTES = 128;
     static_assert(MODE != BLOCK_SHRINK || !PAIR, "adapters' first products take one-CTA tiles");
     constexpr uint32_t TMEM_ALLOC = static_cast<uint32_t>(G::TMEM_COLS);
-    static_assert(8 * (2 * STAGES + 14) + 20 <= 512, "barrier area");
+    static_assert(8 * (4 * STAGES + 14) + 24 <= 512, "barrier area");
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -329,22 +335,36 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     const uint32_t bar0 = ptx::smem_addr(bar_area);
     // barrier k at bar0 + 8k: [0, S) full, [S, 2S) empty, 2S+{0,1} tfull,
     // 2S+{2,3} tempty, 2S+4 mma-done, 2S+5 never completed; GRAD: from 2S+6
-    // two for each team of epilogue warps: z landed in the boxes; ADAPT: 2S+6:
-    // every epilogue warp has looked through a unit's B
+    // two for each team of epilogue warps: z landed in the boxes; ADAPT: 2S+6 (a pair):
+    // every epilogue warp has looked through a unit's B; from 2S+7 (one CTA):
+    // they have looked through slot s, from 3S+7: B is on its way there (the
+    // epilogue may be two phases of full[s] ahead, which its parity would not tell)
     const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
     const uint32_t stall_bar = bar0 + 8u * (2 * STAGES + 5);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (2 * STAGES + 14));
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (4 * STAGES + 14));
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
     volatile int32_t *last_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 2);
-    uint32_t *issued_slot = tmem_slot + 3;  // k-blocks this CTA's producer loaded
+    uint32_t *issued_slot = tmem_slot + 3;  // k-blocks this CTA's producer loaded; b_only
     auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
     auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
     auto tfull_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
     auto tempty_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
     [[maybe_unused]] const uint32_t flag_bar = bar0 + 8u * (2 * STAGES + 6);
-    // ADAPT: bit a of warp w's 256 for unit n: adapter a (of the unit's, from
-    // its first block's) is flagged
+    [[maybe_unused]] auto check_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + 7 + s); };
+    [[maybe_unused]] auto coming_bar = [&](uint32_t s) { return bar0 + 8u * (3 * STAGES + 7 + s); };
+    // ADAPT: byte j: of the 64 rows of B of a unit's j-th pair of blocks, which
+    // eights hold an infinity or NaN.  All zero but while a unit has one.
     [[maybe_unused]] uint32_t *flag_words = reinterpret_cast<uint32_t *>(bar_area + 512);
+    // The eights that go in as zeros: those, in a pair of CTAs the whole boxes
+    // that TMA would have loaded with them.
+    [[maybe_unused]] auto flag_byte = [&](int32_t j) {
+        uint32_t byte = flag_words[j >> 2] >> (j & 3) * 8 & 0xffu;
+        for (int32_t per = min(p.Rp, 64) / 8, g = 0; PAIR && byte && g < 8; g += per) {
+            const uint32_t box = ((1u << per) - 1u) << g;
+            if (byte & box) byte |= box;
+        }
+        return byte;
+    };
     [[maybe_unused]] auto z_bar = [&](uint32_t duo, uint32_t b) { return bar0 + 8u * (2 * STAGES + 6 + 2 * duo + b); };
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -366,9 +386,16 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         ptx::mbar_init(done_bar, 1);
         ptx::mbar_init(stall_bar, 1);
         for (uint32_t i = 0; MODE == BLOCK_GRAD && i < 8; ++i) ptx::mbar_init(z_bar(0, i), 1);
-        if (MODE == BLOCK_ADAPT) ptx::mbar_init(flag_bar, BLOCK_EPI_WARPS);
+        if (MODE == BLOCK_ADAPT) {
+            ptx::mbar_init(flag_bar, BLOCK_EPI_WARPS);
+            for (uint32_t s = 0; s < STAGES; ++s) {
+                ptx::mbar_init(check_bar(s), BLOCK_EPI_WARPS);
+                ptx::mbar_init(coming_bar(s), 1);
+            }
+            for (int i = 0; i < (block_bar_bytes(MODE) - 512) / 4; ++i) flag_words[i] = 0;
+        }
         *abort_flag = 0;
-        *issued_slot = 0;
+        issued_slot[0] = issued_slot[1] = 0;
         ptx::fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
@@ -414,6 +441,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         uint32_t it = 0;
+        uint32_t b_only = 0;  // bit s: slot s's last load brought rows alone
         [[maybe_unused]] uint32_t flag_n = 0;  // ADAPT: units with blocks of u B before this one
         bool ok = true;
         const uint32_t full0 = PAIR ? ptx::map_to_cta(full_bar(0), 0u) : full_bar(0);
@@ -425,26 +453,23 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             const int32_t m0 = w.tn * TILE_F + static_cast<int32_t>(rank) * LANES;
             const int32_t n_half = static_cast<int32_t>(rank) * (block_rows_n<BN>(w) / 2);
             const int32_t n0 = w.row0 + w.tm * BN + n_half;
-            // ADAPT: lane l holds the tile's adapter ad0 + l (-1: none, or flagged)
+            // ADAPT: lane l holds the tile's adapter ad0 + l (-1: none)
             int32_t ad0 = 0, ad = -1;
             auto adapters = [&](int32_t from) {
                 ad0 = from;
                 ad = from + lane < ext_end(p, w) ? __ldcg(p.tab.ids + w.ad.first + from + lane) : -1;
-                const int32_t a = from + lane - ext_first(p, w);
-                uint32_t bad = 0;
-                for (int k = 0; ad >= 0 && k < BLOCK_EPI_WARPS; ++k)
-                    bad |= flag_words[(flag_n & 1u) * 8 * BLOCK_EPI_WARPS + k * 8 + (a >> 5)] >> (a & 31);
-                if (bad & 1u) ad = -1;
             };
-            for (int32_t i = w.kb0; i < w.kb1 + w.e1 - w.e0 || (MODE == BLOCK_ADAPT && i == w.kb1); ++i, ++it) {
-                if (MODE == BLOCK_ADAPT && i == w.kb1) {
+            for (int32_t i = w.kb0; i < w.kb1 + w.e1 - w.e0 || (MODE == BLOCK_ADAPT && i == w.mid); ++i, ++it) {
+                if (MODE == BLOCK_ADAPT && i == w.mid) {
                     ext_range(p, w);
-                    if (w.e0 == w.e1) break;
-                    const int r = wait_bounded_warp(flag_bar, flag_n & 1u, wd);
-                    if (r != WAIT_OK) {
-                        if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_PRODUCER);
-                        ok = false;
-                        break;
+                    if (w.kb1 + w.e1 - w.e0 == i) break;
+                    if (PAIR && w.e0 < w.e1) {
+                        const int r = wait_bounded_warp(flag_bar, flag_n & 1u, wd);
+                        if (r != WAIT_OK) {
+                            if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_PRODUCER);
+                            ok = false;
+                            break;
+                        }
                     }
                 }
                 const uint32_t s = it % STAGES;
@@ -471,28 +496,40 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         ptx::mbar_arrive_expect_tx(full_bar(s), G::STAGE);
                     }
                 };
-                if (MODE == BLOCK_ADAPT && i >= w.kb1) {
-                    const int32_t e = w.e0 + i - w.kb1;
-                    // the block's first adapter, and for R > 32 the rows of B
-                    const int32_t per = p.Rp <= 32 ? 32 / p.Rp : 1;
-                    const int32_t bpa = p.Rp <= 32 ? 1 : p.Rp / 32;
-                    const int32_t a0 = p.Rp <= 32 ? e * per : e / bpa;
-                    const int32_t chunk = p.Rp <= 32 ? 0 : (e % bpa) / 2 * 64;
-                    if (i == w.kb1 || a0 + per > ad0 + 32) adapters(a0);
+                if (MODE == BLOCK_ADAPT && i >= w.mid && i - w.mid < w.e1 - w.e0) {
+                    const int32_t e = w.e0 + i - w.mid;
+                    if (e & 1) {  // lo: its MMAs read the slot before's rows of B
+                        b_only |= 1u << s;
+                        if (ptx::elect_one()) {
+                            if constexpr (PAIR) {
+                                if (leader) ptx::mbar_arrive_expect_tx(full_bar(s), 2 * G::B_STAGE);
+                            } else {
+                                ptx::mbar_arrive_expect_tx(full_bar(s), G::B_STAGE);
+                            }
+                            load(b_dst, &tmE, 0, (w.ad.blk0 + e) * BN + n_half, 0);
+                        }
+                        __syncwarp();
+                        continue;
+                    }
+                    b_only &= ~(1u << s);
                     if (ptx::elect_one()) expect();
                     __syncwarp();
-                    // a lane a box (rows of B past R read as zeros), and one for u
-                    const int32_t rows = min(p.Rp, 64), subs = 64 / rows;
-                    const int32_t j = lane >> 1, h = lane & 1;
-                    const int32_t id = __shfl_sync(0xffffffffu, ad, min(31, a0 - ad0 + (p.Rp <= 32 ? j >> 1 : 0)));
+                    // a lane a box (rows of B past R read as zeros), and one for hi
+                    const int32_t rows = min(p.Rp, 64), subs = 64 / rows, j = lane >> 1, h = lane & 1;
+                    const int32_t a0 = e * 32 / p.Rp;
+                    if (i == w.mid || a0 + subs > ad0 + 32) adapters(a0);
+                    int32_t id = __shfl_sync(0xffffffffu, ad, min(31, a0 - ad0 + j));
+                    // (one CTA's epilogue warps zero what they find in the slot instead)
+                    if (PAIR && j < subs && (flag_byte((i - w.mid) >> 1) >> (j * rows / 8) & 1u)) id = -1;
                     if (j < subs) {
-                        const int32_t r0 = id < 0 ? p.Rp : chunk, z = p.b_shared ? 0 : max(id, 0);
+                        const int32_t r0 = id < 0 ? p.Rp : e * 32 % p.Rp, z = p.b_shared ? 0 : max(id, 0);
                         load(a_dst + h * BOX_BYTES + static_cast<uint32_t>(j * rows) * 128u, &tmV, m0 + 64 * h, r0, z);
                     } else if (lane == 31) {
                         load(b_dst, &tmE, 0, (w.ad.blk0 + e) * BN + n_half, 0);
                     }
-                } else if (ptx::elect_one()) {
-                    const int32_t kb = i;
+                    if (!PAIR && lane == 0) ptx::mbar_arrive(coming_bar(s));
+                } else if (b_only &= ~(1u << s); ptx::elect_one()) {
+                    const int32_t kb = i < w.mid ? i : i - (w.e1 - w.e0);
                     expect();
                     const int32_t z = p.w_shared ? 0 : w.g;
                     if constexpr (MODE == BLOCK_GATED) {
@@ -516,7 +553,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             if (MODE == BLOCK_ADAPT && w.e0 < w.e1) ++flag_n;
         }
         if (lane == 0) {
-            *issued_slot = it;
+            issued_slot[0] = it;
+            issued_slot[1] = b_only;
             if constexpr (!PAIR) {
                 const uint32_t first = it > STAGES ? it - STAGES : 0u;
                 for (uint32_t j = first; j < it; ++j)
@@ -534,6 +572,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             const uint64_t desc_mn = smem_desc_sw128(0, BK * 128, 1024);
             const uint64_t desc_k = smem_desc_sw128(0, 16, 1024);
             uint32_t it = 0, n = 0;
+            [[maybe_unused]] uint32_t check_phase = 0;  // ADAPT: bit s: parity of check_bar(s)'s next phase
             bool ok = true;
             for (int64_t t = worker; ok && block_walk_to<BN>(p, t, walk, w); t += n_workers) {
                 if (w.kb0 == w.kb1) {  // the epilogue writes an empty sum itself
@@ -552,14 +591,19 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + buf * BN;
                 const uint32_t n_field = static_cast<uint32_t>(block_rows_n<BN>(w)) >> 3 << 17;
-                for (int32_t kb = w.kb0; kb < w.kb1 + w.e1 - w.e0 || (MODE == BLOCK_ADAPT && kb == w.kb1); ++kb, ++it) {
-                    if (MODE == BLOCK_ADAPT && kb == w.kb1) {
+                for (int32_t kb = w.kb0; kb < w.kb1 + w.e1 - w.e0 || (MODE == BLOCK_ADAPT && kb == w.mid); ++kb, ++it) {
+                    if (MODE == BLOCK_ADAPT && kb == w.mid) {
                         ext_range(p, w);
-                        if (w.e0 == w.e1) break;
+                        if (w.kb1 + w.e1 - w.e0 == kb) break;
                     }
+                    const bool ext = MODE == BLOCK_ADAPT && kb >= w.mid && kb - w.mid < w.e1 - w.e0;
                     const uint32_t s = it % STAGES;
                     const uint32_t ph = (it / STAGES) & 1u;
                     r = wait_bounded_warp(full_bar(s), ph, wd);
+                    if (!PAIR && ext && ((kb - w.mid) & 1) == 0 && r == WAIT_OK) {
+                        r = wait_bounded_warp(check_bar(s), check_phase >> s & 1u, wd);
+                        check_phase ^= 1u << s;
+                    }
                     if (r != WAIT_OK) {
                         if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_MMA);
                         ok = false;
@@ -567,11 +611,14 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     }
                     ptx::tc_fence_after();
                     if (ptx::elect_one()) {
-                        const bool mn = !p.w_k || (MODE == BLOCK_ADAPT && kb >= w.kb1);
+                        const bool mn = !p.w_k || ext;
                         const uint32_t idesc = ((mn ? idesc_mn : idesc_k) & ~(0x3Fu << 17)) | n_field;
                         const uint64_t a_desc0 = mn ? desc_mn : desc_k;
                         const uint32_t a_step = mn ? 2048u : 32u;
-                        const uint32_t a_addr = sA + s * G::A_STAGE;
+                        // u's second part meets the rows of B of the slot before
+                        const bool second = ext && ((kb - w.mid) & 1);
+                        const uint32_t sa = second ? (it - 1) % STAGES : s;
+                        const uint32_t a_addr = sA + sa * G::A_STAGE;
                         const uint32_t b_addr = sB + s * G::B_STAGE;
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk) {
@@ -583,10 +630,15 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                             else
                                 ptx::mma_bf16(d_tmem, ad, bd, idesc, acc);
                         }
-                        if constexpr (PAIR)
-                            ptx::mma_commit_pair_multicast(empty_bar(s), 0x3);
-                        else
-                            ptx::mma_commit(empty_bar(s));
+                        // (the first of a pair is still read by the second's)
+                        const bool keep = ext && !second;
+                        if constexpr (PAIR) {
+                            if (second) ptx::mma_commit_pair_multicast(empty_bar(sa), 0x3);
+                            if (!keep) ptx::mma_commit_pair_multicast(empty_bar(s), 0x3);
+                        } else {
+                            if (second) ptx::mma_commit(empty_bar(sa));
+                            if (!keep) ptx::mma_commit(empty_bar(s));
+                        }
                     }
                     __syncwarp();
                 }
@@ -631,7 +683,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         const bool issues = member == 0 && lane == 0;  // all the team's bulk copies
         const uint32_t area = sE + (MODE == BLOCK_GATED  ? static_cast<uint32_t>(turn) * 4u * EPI_BOX_BYTES
                                     : MODE == BLOCK_GRAD ? duo * 4u * EPI_BOX_BYTES
-                                    : team == 2          ? duo * 2u * EPI_BOX_BYTES
+                                    : MODE == BLOCK_ADAPT && team == 2 ? duo * 2u * EPI_BOX_BYTES
                                                          : static_cast<uint32_t>(warp - 2) * EPI_BOX_BYTES);
         // Address of 16-byte unit u of row r of the box at `box`, and this
         // lane's matrix row for fragments of the warp's half of a box (rows
@@ -683,17 +735,23 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                             if (e < n) reinterpret_cast<uint32_t *>(d)[e] = v[e];
                     }
                 }
+            } else if (size == 2) {  // two elements a lane
+                const int c = 2 * lane;
+                uint8_t *d = dst + c * 2 + member * pitch;
+#pragma unroll 8
+                for (int r = member; r < nrows; r += team, d += team * pitch) {
+                    uint32_t v;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(unit_at(box, r, c >> 3) + (c & 7) * 2) : "memory");
+                    if (c < cols) *reinterpret_cast<uint16_t *>(d) = static_cast<uint16_t>(v);
+                    if (c + 1 < cols) *reinterpret_cast<uint16_t *>(d + 2) = static_cast<uint16_t>(v >> 16);
+                }
             } else {  // an element a lane
                 for (int c = lane; c < cols; c += 32) {
-                    const int u = c * size >> 4, in = c * size & 15;
-                    uint8_t *d = dst + c * size + member * pitch;
-#pragma unroll 4
-                    for (int r = member; r < nrows; r += team, d += team * pitch) {
-                        if (size == 2)
-                            *reinterpret_cast<uint16_t *>(d) = ld_shared_u16(unit_at(box, r, u) + in);
-                        else
-                            *reinterpret_cast<float *>(d) = ld_shared_f32(unit_at(box, r, u) + in);
-                    }
+                    const int u = c >> 2, in = c * 4 & 15;
+                    uint8_t *d = dst + c * 4 + member * pitch;
+#pragma unroll 8
+                    for (int r = member; r < nrows; r += team, d += team * pitch)
+                        *reinterpret_cast<float *>(d) = ld_shared_f32(unit_at(box, r, u) + in);
                 }
             }
         };
@@ -707,23 +765,16 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     ptx::mbar_arrive(tempty_bar(buf));
             }
         };
-        // SHRINK stores 32 features of a row at a time, the others fragments.
-        auto load_piece = [&](uint32_t taddr, uint32_t (&v)[32]) {
-            if constexpr (MODE == BLOCK_SHRINK)
-                ptx::tmem_load_32cols_async(taddr, v);
-            else
-                load_fragments(taddr, v);
-        };
 
         // SHRINK: a unit's rows lie in two of ADAPT's tiles at most (which are
         // no lower than its own): theirs, and its adapter's place among theirs.
         [[maybe_unused]] int32_t tile0 = 0, place0 = 0, place1 = 0;
         [[maybe_unused]] AdapterTile ad0{}, ad1{};
-        // where the parts of a row stand, in units of 8 values
-        [[maybe_unused]] auto wide_row = [&](int32_t row) {
+        // where the first part of value r of a row stands
+        [[maybe_unused]] auto wide_at = [&](int32_t row, int32_t r) {
             const int32_t tile = row / p.wide_bn, in = row - tile * p.wide_bn;
             const bool second = tile != tile0;
-            return adapter_unit(second ? place1 : place0, second ? ad1.blk0 : ad0.blk0, in, p.wide_bn, p.Rp);
+            return p.wide + adapter_at(second ? place1 : place0, r, second ? ad1.blk0 : ad0.blk0, in, p.wide_bn, p.Rp);
         };
         // zeros in the other adapters' columns of a unit's rows
         auto zero_others = [&](const BlockUnit &w, int32_t row_tile, int32_t limit) {
@@ -733,7 +784,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     const int32_t tile = row / p.wide_bn, in = row - tile * p.wide_bn;
                     const bool second = tile != tile0;
                     const int32_t count = second ? ad1.count : ad0.count;
-                    if (count > 1 || p.Rp < 32) zero_columns(p, in, second ? ad1.blk0 : ad0.blk0, count, second ? place1 : place0, lane);
+                    if (count * p.Rp % 64 || count > 1) zero_columns(p, in, second ? ad1.blk0 : ad0.blk0, count, second ? place1 : place0, lane);
                 }
             }
         };
@@ -746,7 +797,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         }
         if (MODE == BLOCK_SHRINK || MODE == BLOCK_ADAPT) ptx::griddep_wait();  // the tables
         uint32_t n = 0;
-        [[maybe_unused]] uint32_t flag_n = 0;  // ADAPT: units with blocks of u B before this one
+        // ADAPT: ring slots of the units before this one; parities of coming_bar
+        [[maybe_unused]] uint32_t at_it = 0, coming_phase = 0;
         uint32_t flip = 0;     // which of two boxes (GRAD: pairs of them) is next
         // GRAD: bit b: parity of z_bar(b)'s next phase; a copy is on its way there
         uint32_t z_phase = 0, z_out = 0;
@@ -899,6 +951,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         }
                         if (!agree(r == WAIT_OK, team_id, 64)) return false;
                     }
+                    if (c != turn) load_z(c + 2, b ^ 1u);  // (the first two came together)
                     uint32_t h[16];
                     switch (p.act) {
                         case 1: gated_grad_box<1>(box + frag_at, EPI_BOX_BYTES, v, h); break;
@@ -907,7 +960,6 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         default: gated_grad_box<0>(box + frag_at, EPI_BOX_BYTES, v, h); break;
                     }
                     next();
-                    if (c != turn) load_z(c + 2, b ^ 1u);  // (the first two came together)
                     ptx::fence_proxy_async_smem();
                     team_sync();
                     flush(box, &tmG, p.gate, 2, row0, limit, whole, f_box);
@@ -949,84 +1001,119 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     flush(box, &tmO, p.out0, p.out_bf16 ? 2 : 4, row0, limit, whole, f_box);
                     if (issues) ptx::bulk_commit_group();
                 } else {  // SHRINK
+                    // parts -> this warp's two boxes of 32 rows x 64 bytes (16-byte units
+                    // swizzled by the row's pair), then 16 bytes of a row a lane
                     const float scale = p.scales ? __ldg(p.scales + w.g) : 1.0f;
-                    const int32_t r = f_warp + lane;
-                    const int32_t mine = row0 + lane < limit ? wide_row(row0 + lane) : 0;  // (lane: row)
-                    // its adapter's columns there, and how far lo lies from hi
-                    const int64_t lo_off = p.Rp <= 32 ? p.Rp : static_cast<int64_t>(p.wide_bn) * 64;
-                    const int32_t in_row = p.Rp <= 32 ? r : r / 64 * 2 * p.wide_bn * 64 + (r & 63);
+                    const uint32_t at = area + static_cast<uint32_t>((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
+                    __syncwarp();  // the boxes were read
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int32_t row = row0 + j;
-                        const int32_t at32 = __shfl_sync(0xffffffffu, mine, j);
+                    for (int oct = 0; oct < 4; ++oct) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const int i = (f >> 1) * 16 + oct * 4 + (f & 1) * 2;
+                            const bool in = f_warp + f * 8 + (lane >> 2) < p.R;  // (columns past R meet zeros, whatever X holds)
+                            __nv_bfloat16 h0, l0, h1, l1;
+                            split_parts(in ? __fmul_rn(scale, __uint_as_float(v[i])) : 0.0f, h0, l0);
+                            split_parts(in ? __fmul_rn(scale, __uint_as_float(v[i + 1])) : 0.0f, h1, l1);
+                            hi[f] = static_cast<uint32_t>(__bfloat16_as_ushort(h0)) | static_cast<uint32_t>(__bfloat16_as_ushort(h1)) << 16;
+                            lo[f] = static_cast<uint32_t>(__bfloat16_as_ushort(l0)) | static_cast<uint32_t>(__bfloat16_as_ushort(l1)) << 16;
+                        }
+                        stmatrix_trans(at + oct * 512u, hi[0], hi[1], hi[2], hi[3]);
+                        stmatrix_trans(at + 2048u + oct * 512u, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    __syncwarp();
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        const int j = (lane >> 2) + 8 * k, u = lane & 3;
+                        const int32_t row = row0 + j, r = f_warp + 8 * u;
+                        uint32_t hi[4], lo[4];
+                        ld_shared_v4(area + j * 64u + ((u ^ ((j >> 1) & 3)) << 4), hi);
+                        ld_shared_v4(area + 2048u + j * 64u + ((u ^ ((j >> 1) & 3)) << 4), lo);
                         if (row >= limit || r >= p.Rp) continue;
-                        // (columns past R meet zeros, whatever X holds)
-                        const float x = r < p.R ? __fmul_rn(scale, __uint_as_float(v[j])) : 0.0f;
-                        __nv_bfloat16 hi, lo;
-                        split_parts(x, hi, lo);
-                        uint16_t *at = p.wide + static_cast<int64_t>(at32) * 8 + in_row;
-                        at[0] = __bfloat16_as_ushort(hi);
-                        at[lo_off] = __bfloat16_as_ushort(lo);
-                        if (p.out0.p && r < p.R)
-                            static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] =
-                                __bfloat16_as_ushort(__float2bfloat16_rn(x));
+                        uint16_t *to = wide_at(row, r);
+                        *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(p.wide_bn) * 64) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        if (p.out0.p) {
+                            uint16_t *o = static_cast<uint16_t *>(p.out0.p) + static_cast<int64_t>(row) * p.out0.ld + r;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (r + e < p.R) o[e] = static_cast<uint16_t>(hi[e >> 1] >> (16 * (e & 1)));
+                        }
                     }
                     next();
                 }
                 return true;
             };
-            // ADAPT: which of the unit's adapters hold an infinity or NaN in this
-            // CTA's features of B; they are added to their own rows below.
-            // Every warp looks through an eighth of each B's rows.
+            // ADAPT: the rows of B that hold an infinity or NaN in this CTA's
+            // features; they go in as zeros and are added to their own adapter's rows
+            // below.  A warp looks through eight rows of each pair of blocks: in
+            // the slot they have landed in, or, where the slot's barrier is the other
+            // CTA's, in memory.
             bool flagged = false;
-            [[maybe_unused]] const uint32_t *flags = flag_words + (flag_n & 1u) * 8 * BLOCK_EPI_WARPS;
+            const int32_t pairs = (w.e1 - w.e0) / 2;
             if constexpr (MODE == BLOCK_ADAPT) {
-                if (w.e0 < w.e1) {
-                    const int32_t a0 = ext_first(p, w), a1 = ext_end(p, w);
-                    const int32_t f = f0 + 8 * (lane & 15), r0 = 2 * (warp - 2) + (lane >> 4);
-                    for (int32_t at = a0; at < a1; at += 32) {
-                        const int32_t id = at + lane < a1 ? __ldcg(p.tab.ids + w.ad.first + at + lane) : 0;
-                        uint32_t word = 0;
-                        for (int32_t a = 0; a < min(32, a1 - at); a += 4) {
-                            uint32_t bad[4] = {0u, 0u, 0u, 0u};
+                at_it += static_cast<uint32_t>(w.mid - w.kb0);
+                bool fine = true;
+                for (int32_t j0 = 0; j0 < pairs && fine; j0 += PAIR ? 4 : 1) {
+                    bool bad[PAIR ? 4 : 1] = {};
+                    [[maybe_unused]] const uint32_t at = at_it + 2u * static_cast<uint32_t>(j0), slot = at % STAGES;
+                    [[maybe_unused]] const uint32_t rows_at = sA + slot * G::A_STAGE + static_cast<uint32_t>(warp - 2) * 1024u + lane * 16u;
+                    if constexpr (PAIR) {
+                        const int32_t f = f0 + 8 * (lane & 15);
+                        const bool ragged = __any_sync(0xffffffffu, f < p.N && p.N - f < 8);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int32_t g = __shfl_sync(0xffffffffu, id, min(31, a + k));
-                                const uint16_t *b = p.b + g * p.strideB + f;
-                                if (a + k < a1 - at && f < p.N) {
-#pragma unroll 2
-                                    for (int32_t r = r0; r < p.R; r += 2 * BLOCK_EPI_WARPS) bad[k] |= has_non_finite(b + r * p.ldb, p.N - f);
-                                }
-                            }
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (__any_sync(0xffffffffu, bad[k] != 0)) word |= 1u << ((a + k) & 31);
+                        for (int k = 0; k < 16; ++k) {
+                            const int32_t col = w.e0 * 32 + (j0 + (k >> 2)) * 64 + 8 * (warp - 2) + 2 * (k & 3) + (lane >> 4);
+                            const int32_t i = col / p.Rp, r = col - i * p.Rp;
+                            const bool in = j0 + (k >> 2) < pairs && i < w.ad.count && r < p.R && f < p.N;
+                            const int32_t id = in && !p.b_shared ? __ldcg(p.tab.ids + w.ad.first + i) : 0;
+                            const uint16_t *b = in ? p.b + id * p.strideB + r * p.ldb + f : p.b;
+                            bad[k >> 2] |= in && (ragged ? has_non_finite(b, p.N - f) : has_non_finite(b, 8));
                         }
-                        if (lane == 0) const_cast<uint32_t *>(flags)[(warp - 2) * 8 + ((at - a0) >> 5)] = word;
+                    } else {
+                        int r = wait_bounded_warp(coming_bar(slot), coming_phase >> slot & 1u, wd);
+                        coming_phase ^= 1u << slot;
+                        if (r == WAIT_OK) r = wait_bounded_warp(full_bar(slot), at / STAGES & 1u, wd);
+                        if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
+                        fine = r == WAIT_OK;
+                        if (!fine) break;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t x[4];
+                            ld_shared_v4(rows_at + (k & 1) * 512u + (k >> 1) * BOX_BYTES, x);
+                            bad[0] |= non_finite(x[0] , x[1], x[2], x[3]);
+                        }
                     }
+#pragma unroll
+                    for (int k = 0; k < (PAIR ? 4 : 1); ++k)
+                        if (__any_sync(0xffffffffu, bad[k])) {
+                            flagged = true;
+                            if (lane == 0) atomicOr(&flag_words[(j0 + k) >> 2], 1u << (((j0 + k) & 3) * 8 + warp - 2));
+                            if constexpr (!PAIR) {
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) ptx::st_shared_v4(rows_at + (z & 1) * 512u + (z >> 1) * BOX_BYTES, 0u, 0u, 0u, 0u);
+                                ptx::fence_proxy_async_smem();
+                            }
+                        }
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(flag_bar);
-                    const int r = wait_bounded_warp(flag_bar, flag_n & 1u, wd);
-                    if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
-                    if (!agree(r == WAIT_OK, 1, 32 * BLOCK_EPI_WARPS)) break;
-                    uint32_t any = 0;
-                    for (int32_t k = lane; k < BLOCK_EPI_WARPS * 8; k += 32)
-                        if ((k & 7) * 32 < a1 - a0) any |= flags[k];
-                    flagged = __any_sync(0xffffffffu, any != 0);
-                    ++flag_n;
+                    if (!PAIR && lane == 0) ptx::mbar_arrive(check_bar(slot));
+                }
+                at_it += static_cast<uint32_t>(w.kb1 - w.mid + w.e1 - w.e0);
+                if (pairs > 0) {
+                    if (PAIR && lane == 0) ptx::mbar_arrive(flag_bar);
+                    if (!agree(fine, 1, 32 * BLOCK_EPI_WARPS)) break;
+                    flagged = !agree(!flagged, 1, 32 * BLOCK_EPI_WARPS);
                 }
             }
             auto add_flagged = [&](int c, uint32_t (&v)[32]) {
                 if constexpr (MODE == BLOCK_ADAPT) {
                     if (!flagged) return;
                     const int32_t r0 = row_tile + 32 * c;
-                    const int32_t a0 = ext_first(p, w), a1 = ext_end(p, w);
-                    for (int32_t i = a0; i < a1; ++i) {
-                        const int32_t id = __ldcg(p.tab.ids + w.ad.first + i);
-                        uint32_t bad = 0;
-                        for (int k = 0; k < BLOCK_EPI_WARPS; ++k) bad |= flags[k * 8 + ((i - a0) >> 5)] >> ((i - a0) & 31);
-                        // (in the share that has its first block)
-                        if (!(bad & 1u) || (p.Rp > 32 && i * (p.Rp / 32) < w.e0)) continue;
+                    for (int32_t e = 0; e < pairs * 8; ++e) {
+                        const int32_t col = w.e0 * 32 + e * 8, i = col / p.Rp, r8 = col - i * p.Rp;
+                        if (!(flag_byte(e >> 3) >> (e & 7) & 1u) || i >= w.ad.count) continue;
+                        const int32_t id = p.b_shared ? 0 : __ldcg(p.tab.ids + w.ad.first + i);
                         const int32_t lo = max(__ldcg(p.tab.lo + w.ad.first + i), r0);
                         const int32_t hi = min(__ldcg(p.tab.hi + w.ad.first + i), min(limit, r0 + 32));
 #pragma unroll
@@ -1035,11 +1122,10 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                             if (row < lo || row >= hi || f >= p.N) continue;
                             float sum = 0.0f;
 #pragma unroll 1
-                            for (int32_t r = 0; r < p.R; ++r) {
-                                const uint16_t *at = p.wide + static_cast<int64_t>(adapter_unit(i, w.ad.blk0, row - row_tile, BN, p.Rp)) * 8 +
-                                                     (p.Rp <= 32 ? r : r / 64 * 2 * BN * 64 + (r & 63));
+                            for (int32_t r = r8; r < min(r8 + 8, p.R); ++r) {
+                                const uint16_t *at = p.wide + adapter_at(i, r, w.ad.blk0, row - row_tile, BN, p.Rp);
                                 const float u = __uint_as_float(static_cast<uint32_t>(at[0]) << 16) +
-                                                __uint_as_float(static_cast<uint32_t>(at[p.Rp <= 32 ? p.Rp : BN * 64]) << 16);
+                                                __uint_as_float(static_cast<uint32_t>(at[BN * 64]) << 16);
                                 const float bv = __uint_as_float(static_cast<uint32_t>(p.b[id * p.strideB + r * p.ldb + f]) << 16);
                                 sum = __fmaf_rn(u, bv, sum);
                             }
@@ -1049,69 +1135,52 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 }
             };
 
-            uint32_t v[32];
-            if (w.kb0 == w.kb1 && w.e0 == w.e1) {  // the empty sum
-                if (lanes_in) load_two();
-                for (int c = turn; ok && lanes_in && c < pieces; c += 2) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0u;
-                    ok = piece(c, v, [] {});
-                }
-                if (!ok) break;
-                zero_others(w, row_tile, limit);
-                continue;
-            }
-            if (lanes_in && w.nparts == 1) load_two();
+            const bool empty = w.kb0 == w.kb1 && w.e0 == w.e1, shared = w.nparts > 1 && !empty;
+            if (lanes_in && !shared) load_two();
             const uint32_t buf = n & 1u;
-            const uint32_t tph = (n >> 1) & 1u;
-            ++n;
-            // (the warps that meet at barriers below leave together)
-            const int r = wait_bounded(tfull_bar(buf), tph, wd);
-            if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
-            const bool here = r == WAIT_OK;
-            if (!(w.nparts > 1 || flagged ? agree(here, 1, 32 * BLOCK_EPI_WARPS)
-                  : team == 1  ? __all_sync(0xffffffffu, here) != 0
-                               : agree(here, team_id, 32 * team)))
-                break;
-            ptx::tc_fence_after();
+            if (!empty) {
+                const uint32_t tph = (n >> 1) & 1u;
+                ++n;
+                // (the warps that meet at barriers below leave together)
+                const int r = wait_bounded(tfull_bar(buf), tph, wd);
+                if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
+                const bool here = r == WAIT_OK;
+                if (!(shared || flagged ? agree(here, 1, 32 * BLOCK_EPI_WARPS)
+                      : team == 1       ? __all_sync(0xffffffffu, here) != 0
+                                        : agree(here, team_id, 32 * team)))
+                    break;
+                ptx::tc_fence_after();
+            }
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
-            if (w.nparts > 1) {
-                // The partial tile -> scratch [piece][value quad][lane][4
-                // values]: 16 coalesced bytes a thread.
-                constexpr int64_t PART4 = BM * BN / 4;  // float4s a part
-                const int64_t half = static_cast<int64_t>(w.tile) * (PAIR ? 2 : 1) + rank;
-                float4 *parts = reinterpret_cast<float4 *>(p.partials) + half * p.splits * PART4 + q * 32 + lane;
-                float4 *mine = parts + w.part * PART4;
-                for (int c = turn; lanes_in && c < pieces; c += 2) {
-                    load_piece(taddr + c * 32, v);
-                    ptx::tmem_wait_ld(v);
-                    add_flagged(c, v);
-#pragma unroll
-                    for (int j4 = 0; j4 < 8; ++j4)
-                        __stcg(mine + (c * 8 + j4) * BM, make_float4(__uint_as_float(v[4 * j4]), __uint_as_float(v[4 * j4 + 1]),
-                                                                     __uint_as_float(v[4 * j4 + 2]), __uint_as_float(v[4 * j4 + 3])));
-                }
-                release_tmem(buf);
-                __threadfence();
-                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
-                if (warp == 2 && lane == 0) {
-                    const int32_t old = atomicAdd(p.counters + half, 1);
-                    *last_flag = old == w.nparts - 1 ? 1 : 0;
-                    if (old == w.nparts - 1) atomicExch(p.counters + half, 0);  // ready for the next call
-                }
-                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
-                if (*last_flag) {
-                    __threadfence();
-                    if (lanes_in) load_two();
-                    for (int c = turn; ok && lanes_in && c < pieces; c += 2) {
+            // Partial tiles in scratch: [piece][value quad][lane][4 values], 16
+            // coalesced bytes a thread.
+            constexpr int64_t PART4 = BM * BN / 4;  // float4s a part
+            const int64_t half = static_cast<int64_t>(w.tile) * (PAIR ? 2 : 1) + rank;
+            float4 *parts = reinterpret_cast<float4 *>(p.partials) + half * p.splits * PART4 + q * 32 + lane;
+            // The accumulator, out or (a share) to scratch; then, by the last
+            // share to arrive, the sum of the shares in the order of k.  One loop
+            // for all of them: short calls run from cold instruction caches.
+            for (bool sum = false;; sum = true) {
+                uint32_t v[32];
+                // The next piece's loads are on their way while one is stored.
+                auto advance = [&](int c) {
+                    if (sum || empty) return;
+                    if (lanes_in && c < pieces)
+                        load_fragments(taddr + c * 32, v);
+                    else
+                        release_tmem(buf);
+                };
+                advance(turn);
+                for (int c = turn; ok && lanes_in && c < pieces; c += 2) {
+                    if (sum) {
                         float4 acc[8];
 #pragma unroll
                         for (int j4 = 0; j4 < 8; ++j4) acc[j4] = __ldcg(parts + (c * 8 + j4) * BM);
 #pragma unroll 2
-                        for (int s = 1; s < w.nparts; ++s) {
+                        for (int k = 1; k < w.nparts; ++k) {
                             float4 t4[8];
 #pragma unroll
-                            for (int j4 = 0; j4 < 8; ++j4) t4[j4] = __ldcg(parts + s * PART4 + (c * 8 + j4) * BM);
+                            for (int j4 = 0; j4 < 8; ++j4) t4[j4] = __ldcg(parts + k * PART4 + (c * 8 + j4) * BM);
 #pragma unroll
                             for (int j4 = 0; j4 < 8; ++j4) {
                                 acc[j4].x += t4[j4].x; acc[j4].y += t4[j4].y;
@@ -1125,32 +1194,45 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                             v[4 * j4 + 2] = __float_as_uint(acc[j4].z);
                             v[4 * j4 + 3] = __float_as_uint(acc[j4].w);
                         }
-                        ok = piece(c, v, [] {});
+                    } else if (empty) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0u;
+                    } else {
+                        ptx::tmem_wait_ld(v);
+                        add_flagged(c, v);
                     }
-                    zero_others(w, row_tile, limit);
+                    if (shared && !sum) {
+                        float4 *mine = parts + w.part * PART4;
+#pragma unroll
+                        for (int j4 = 0; j4 < 8; ++j4)
+                            __stcg(mine + (c * 8 + j4) * BM, make_float4(__uint_as_float(v[4 * j4]), __uint_as_float(v[4 * j4 + 1]),
+                                                                         __uint_as_float(v[4 * j4 + 2]), __uint_as_float(v[4 * j4 + 3])));
+                        advance(c + 2);
+                    } else {
+                        ok = piece(c, v, [&] { advance(c + 2); });
+                    }
                 }
-                ok = agree(ok, 1, 32 * BLOCK_EPI_WARPS);  // (and the flag may be written again)
-                continue;
+                if (!shared || sum) break;
+                __threadfence();
+                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
+                if (warp == 2 && lane == 0) {
+                    const int32_t old = atomicAdd(p.counters + half, 1);
+                    *last_flag = old == w.nparts - 1 ? 1 : 0;
+                    if (old == w.nparts - 1) atomicExch(p.counters + half, 0);  // ready for the next call
+                }
+                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
+                if (!*last_flag) break;
+                __threadfence();
+                if (lanes_in) load_two();
             }
-            // The next piece's loads are on their way while one is stored.
-            int c = turn;
-            if (lanes_in && c < pieces)
-                load_piece(taddr + c * 32, v);
-            else
-                release_tmem(buf);
-            for (; ok && lanes_in && c < pieces; c += 2) {
-                ptx::tmem_wait_ld(v);
-                add_flagged(c, v);
-                ok = piece(c, v, [&] {
-                    if (c + 2 < pieces)
-                        load_piece(taddr + (c + 2) * 32, v);
-                    else
-                        release_tmem(buf);
-                });
-            }
+            if (ok && (!shared || *last_flag)) zero_others(w, row_tile, limit);
+            // (the flags, of the last share and of B, may be written again)
+            if (shared || flagged) ok = agree(ok, 1, 32 * BLOCK_EPI_WARPS);
             if (!ok) break;
-            zero_others(w, row_tile, limit);
-            if (flagged) ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);  // its flags were read
+            if (flagged) {
+                for (int32_t i = (warp - 2) * 32 + lane; i * 4 < pairs; i += 32 * BLOCK_EPI_WARPS) flag_words[i] = 0;
+                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
+            }
         }
         // Rows of no group: zeros (SHRINK: of u and its parts).
         if (p.offsets) {
@@ -1200,16 +1282,19 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         // are settled first
         ptx::cluster_sync_all();
         if (leader && warp == 0 && lane == 0) {
-            const uint32_t i_l = *issued_slot;
+            const uint32_t i_l = issued_slot[0];
             const uint32_t i_p = ptx::ld_cluster_u32(ptx::map_to_cta(ptx::smem_addr(issued_slot), 1u));
             const uint32_t hi = i_l > i_p ? i_l : i_p;
             const uint32_t lo = hi > STAGES ? hi - STAGES : 0u;
+            const uint32_t only_l = issued_slot[1];
+            const uint32_t only_p = ptx::ld_cluster_u32(ptx::map_to_cta(ptx::smem_addr(issued_slot + 1), 1u));
             for (uint32_t j = lo; j < hi; ++j) {
                 const uint32_t s = j % STAGES;
+                const uint32_t bytes = ((j < i_l ? only_l : only_p) >> s) & 1u ? G::B_STAGE : G::STAGE;
                 if (j < i_l && j >= i_p)
-                    ptx::mbar_complete_tx(full_bar(s), G::STAGE);
+                    ptx::mbar_complete_tx(full_bar(s), bytes);
                 else if (j >= i_l && j < i_p)
-                    ptx::mbar_arrive_expect_tx(full_bar(s), G::STAGE);
+                    ptx::mbar_arrive_expect_tx(full_bar(s), bytes);
                 if (!wait_drain(full_bar(s), (j / STAGES) & 1u, wd)) break;
             }
         }

@@ -45,6 +45,9 @@ struct BlockParams {
     uint16_t *wide;          // u's parts: [block][bn rows][64]
     int32_t R, Rp;
     int32_t wide_bn;         // rows of ADAPT's tiles
+    int32_t ext_first;       // ADAPT: a unit's blocks of u B come before those of X W (u is there when the
+                             // kernel starts, and no unit before this one keeps the epilogue from looking
+                             // through B), not behind them
     const uint16_t *b;       // B, rows on 16 bytes: looked through for infinities and NaN
     int64_t ldb, strideB;
     int32_t b_shared;        // 1 = every adapter has the same B
@@ -57,19 +60,17 @@ struct BlockParams {
     int32_t debug_stall;
 };
 
-// Blocks of 64 k that a row tile's adapters take.
-__host__ __device__ inline int32_t adapter_blocks(int32_t count, int32_t Rp)
-{
-    return Rp <= 32 ? (count * Rp + 31) / 32 : count * (Rp / 32);
-}
+// Blocks of 64 k that a row tile's adapters take: for every 64 of their Rp values
+// one of u's first parts and one of its second ones.
+__host__ __device__ inline int32_t adapter_blocks(int32_t count, int32_t Rp) { return (count * Rp + 63) / 64 * 2; }
 
 // Staging boxes of 32 rows of 128 bytes: eight, GRAD sixteen (z of two pieces a
 // team of two warps; dZ takes z's place).
 __host__ __device__ constexpr int block_epi_bytes(int mode) { return mode == BLOCK_GRAD ? 65536 : 32768; }
 
-// Barriers, and ADAPT's flagged adapters: for two units in turn a bit an
-// adapter from each epilogue warp.
-__host__ __device__ constexpr int block_bar_bytes(int mode) { return mode == BLOCK_ADAPT ? 1024 : 512; }
+// Barriers, and ADAPT's flags: a byte for each pair of blocks that a tile may
+// have (256 rows of as many adapters of R = 256 at most).
+__host__ __device__ constexpr int block_bar_bytes(int mode) { return mode == BLOCK_ADAPT ? 2048 : 512; }
 
 constexpr int BLOCK_EPI_WARPS = 8;
 constexpr int BLOCK_THREADS = 64 + 32 * BLOCK_EPI_WARPS;

@@ -31,11 +31,11 @@ BlockShape block_shape_shrink(BlockTiles t)
 BlockShape block_shape_adapt(BlockTiles t)
 #endif
 {
-    constexpr int STAGES = TG_BLOCK_MODE == BLOCK_GRAD ? 5 : 6;
+    constexpr bool GRAD = TG_BLOCK_MODE == BLOCK_GRAD;
 #if TG_BLOCK_MODE != 2  // (the adapters' first products have few features)
-    if (t == TILES_PAIR) return shape<256, STAGES, true>();
+    if (t == TILES_PAIR) return shape<256, GRAD ? 5 : 6, true>();
 #endif
-    return t == TILES_FEW ? shape<32, TG_BLOCK_MODE == BLOCK_GRAD ? 8 : 9, false>() : shape<128, STAGES, false>();
+    return t == TILES_FEW ? shape<32, GRAD ? 8 : 9, false>() : shape<128, GRAD ? 5 : 6, false>();
 }
 
 }  // namespace tg
