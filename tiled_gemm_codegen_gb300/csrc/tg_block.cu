@@ -126,7 +126,6 @@ __device__ __forceinline__ int32_t write_tables(const BlockParams &p, int32_t ti
 }
 
 constexpr int TABLE_THREADS = 1024;
-constexpr int ROWS_THREADS = 128;
 constexpr int ROWS_GROUPS = 512;  // groups adapter_rows_kernel takes at most
 
 __global__ void __launch_bounds__(TABLE_THREADS) adapter_tables_kernel(const BlockParams p, int32_t tiles)
@@ -187,6 +186,7 @@ __device__ __forceinline__ void rows_sums(const uint16_t *x0, const uint16_t *x1
 
 // One chunk of 16 rows of a group by a cluster (adapter_rows_kernel).  bounds: the
 // groups' ends; chunks: the chunks (low half) and groups with rows up to each.
+template <int ROWS_THREADS>
 __device__ __forceinline__ void rows_chunk(const BlockParams &p, const uint16_t *X, int64_t ldx, const uint16_t *A, int64_t lda,
                                            int64_t strideA, int32_t K, int32_t stride, int32_t cluster, int32_t rank, int32_t want,
                                            int32_t first_row, const int32_t *bounds, const int32_t *chunks, int32_t *found,
@@ -333,9 +333,12 @@ __device__ __forceinline__ void rows_chunk(const BlockParams &p, const uint16_t 
 // 4096, would take it 3 us), 32 R at a time.  A lane's 16 bytes of X and of A
 // are two MMAs' fragments: any order of k will do where both operands have the
 // same.  Bound by latency: offsets, one round of loads, the warps' and the
-// cluster's sums.  The shared projection starts beside a few blocks (`early`), but
-// behind the loads of many: its own would fill the memory's queues, and each
-// round of theirs would take 2.5 us instead of one.
+// cluster's sums.  The shared projection starts at once where both kernels'
+// blocks have SMs of their own (512 threads, `early`: 1003 rows, 1400 x 1000, 18
+// us; 24 in small blocks that share SMs); else behind this one's loads: its own
+// would fill the memory's queues, and each round of loads would take 2.5 us
+// instead of one (64 rows of 40 adapters, 4096 x 4096: 34 us; 27 behind them).
+template <int ROWS_THREADS>
 __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockParams p, const uint16_t *X, int64_t ldx, const uint16_t *A,
                                                                     int64_t lda, int64_t strideA, int32_t K, int32_t tiles,
                                                                     int32_t stride, int32_t cluster, int32_t early)
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
     }
     const int32_t n_clusters = static_cast<int32_t>(gridDim.x) / cluster - 1;
     for (int32_t want = cid - 1; want < total; want += n_clusters)
-        rows_chunk(p, X, ldx, A, lda, strideA, K, stride, cluster, rank, want, first_row, bounds, chunks, found, sums);
+        rows_chunk<ROWS_THREADS>(p, X, ldx, A, lda, strideA, K, stride, cluster, rank, want, first_row, bounds, chunks, found, sums);
 }
 
 // ------------------------------------------------------------ launches
@@ -742,15 +745,17 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     p.N = static_cast<int32_t>(R);
     p.out0 = BlockOut{U, ldu, 0};
     if (few) {
-        // at most four steps of 32 k a warp, and no more blocks than run at once
+        const int64_t workers = std::min<int64_t>(cy.units * cy.splits, hs.sms) * (pair ? 2 : 1), wanted = 1 + S / 16 + hit;
+        const bool early = wanted + workers <= hs.sms;
+        const int64_t clusters = early ? wanted : std::min<int64_t>(wanted, 4 * hs.sms);
+        // at most four steps of 32 k a warp of a small block, and no more blocks than run at once
+        const int64_t room = early ? hs.sms - workers : 4 * hs.sms;
         int32_t cluster = 1;
-        const int64_t clusters = std::min<int64_t>(1 + S / 16 + hit, 4 * hs.sms);
-        while (cluster < 8 && K > 512 * cluster && clusters * cluster * 2 <= 4 * hs.sms) cluster *= 2;
-        const bool early = clusters * cluster <= hs.sms / 4;
+        while (cluster < 8 && K > 512 * cluster && clusters * cluster * 2 <= room) cluster *= 2;
         py.ext_first = !early && !pair && cy.units * cy.splits <= hs.sms ? 1 : 0;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
-        cfg.blockDim = dim3(ROWS_THREADS);
+        cfg.blockDim = dim3(early ? 512 : 128);
         cfg.stream = hs.stream;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -758,7 +763,7 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, adapter_rows_kernel, p, static_cast<const uint16_t *>(x.p), x.ld, static_cast<const uint16_t *>(a.p),
+        e = cudaLaunchKernelEx(&cfg, early ? adapter_rows_kernel<512> : adapter_rows_kernel<128>, p, static_cast<const uint16_t *>(x.p), x.ld, static_cast<const uint16_t *>(a.p),
                                a.ld, a_shared ? int64_t(0) : a.stride, static_cast<int32_t>(K), static_cast<int32_t>(tiles),
                                static_cast<int32_t>(stride), cluster, early ? 1 : 0);
         if (e != cudaSuccess) return host_cuda_status(e);

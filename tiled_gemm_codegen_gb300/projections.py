@@ -34,9 +34,15 @@ def _weights(W, offsets, what):
     if W.dtype != _BF16 or not W.is_cuda:
         raise TypeError(f"{what} must be a bf16 CUDA tensor")
     if offsets is None:
-        if W.dim() != 2:
+        shape, st = W.shape, W.stride()
+        if len(shape) != 2:
             raise ValueError(f"{what} must have shape [K, N] (weights of several groups need offsets)")
-        return (None, 1), _matrices(W.unsqueeze(0), what)
+        r, c = shape
+        if c > 1 and st[1] != 1 and (st[0] == 1 or r == 1):
+            return (None, 1), (W.data_ptr(), 1, r, c, _pitch(st[1], c, max(r, 1), what), 0, True)
+        if c > 1 and st[1] != 1 and r:
+            raise ValueError(f"{what} must have unit stride in one of its dimensions")
+        return (None, 1), (W.data_ptr(), 1, r, c, _pitch(st[0], r, c, what), 0, False)
     po, groups = _offsets(offsets)
     m = _matrices(W, what)
     if m[1] != groups:
@@ -53,7 +59,7 @@ def _options(options, col_major):
 def _wanted(t, shape, like, what):
     """(tensor or None, ptr, ld) of an optional bf16 output: None, True (one is
     made) or a tensor."""
-    if t is None or t is False:
+    if t is None:
         return None, None, 0
     if t is True:
         t = torch.empty(shape, dtype=_BF16, device=like.device)
