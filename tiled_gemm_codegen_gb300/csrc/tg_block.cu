@@ -470,7 +470,7 @@ struct Cut {
 // evenly the k-blocks fall on them: the number of shares (12 k-blocks at least)
 // for which the busiest worker has the least, a block added for each share
 // (8192 x 2 * 14336, one row: 224 tiles of 128 k-blocks on 152 workers take 82 us
-// whole, XXX in halves).  Else as grouped rows.
+// whole, 79 in halves).  Else as grouped rows.
 int64_t split_of(int mode, const Cut &c, int64_t S, int64_t hit, int64_t depth, int sms)
 {
     if (mode == BLOCK_SHRINK)  // X is the traffic: as many workers as there are, for groups that end in the middle of a tile
@@ -487,25 +487,50 @@ int64_t split_of(int mode, const Cut &c, int64_t S, int64_t hit, int64_t depth, 
     return share == 0 ? 1 : std::min(SPLIT_MOST, cdiv(depth, share));
 }
 
-// `lanes`: accumulator lanes a feature takes (GATED: 2).  Tiles as grouped
-// rows choose them (tiles_cost): pairs or one CTA, and 32 rows where
-// groups have few, whose ring is deeper (weights are the traffic).
-Cut cut_rows(int mode, int64_t S, int64_t N, int64_t K, int64_t groups, int sms, const tg_options *opt)
+// Tiles of one kind for a product: `lanes` accumulator lanes a feature (GATED: 2).
+Cut cut_tiles(int mode, BlockTiles tiles, int64_t S, int64_t N, int64_t K, int64_t groups, int sms)
 {
     const int64_t lanes = mode == BLOCK_GATED ? 2 : 1, hit = std::min(groups, S);
-    bool pair = N * lanes > 128 && S > 32 * hit &&
-                tiles_cost(false, true, S, 0, N * lanes, K, groups, sms) < tiles_cost(false, false, S, 0, N * lanes, K, groups, sms);
-    if (opt && opt->cta_pair) pair = opt->cta_pair == 2;
-    if (mode == BLOCK_SHRINK) pair = false;
     Cut c;
-    c.tiles = pair ? TILES_PAIR : S <= 32 * hit ? TILES_FEW : TILES_ONE;
-    c.bn = pair ? 256 : c.tiles == TILES_FEW ? 32 : 128;
-    c.features = (pair ? 256 : 128) / lanes;
-    c.units = (S / c.bn + hit) * cdiv(N, c.features);
-    if (groups == 1) c.units = cdiv(S, c.bn) * cdiv(N, c.features);
-    const int64_t depth = cdiv(K, BK);
-    c.splits = split_of(mode, c, S, hit, depth, sms);
+    c.tiles = tiles;
+    c.bn = tiles == TILES_PAIR ? 256 : tiles == TILES_FEW ? 32 : 128;
+    c.features = (tiles == TILES_PAIR ? 256 : 128) / lanes;
+    c.units = (groups == 1 ? cdiv(S, c.bn) : S / c.bn + hit) * cdiv(N, c.features);
+    c.splits = split_of(mode, c, S, hit, cdiv(K, BK), sms);
     return c;
+}
+
+// About what a product takes in such tiles, in microseconds: a start, turns of
+// the workers (over groups that end anywhere in a tile) of so much a k-block or of
+// an epilogue, whichever is longer, the last one's epilogue, and where tiles
+// are shared the adding.  Measured: a k-block 0.29 in 128 x 128 tiles, 0.33 in pairs'
+// 256 x 256; an epilogue 4 and 8 (GRAD, which reads z), 2.5 and 4.  In 26 calls
+// of 300 to 16384 rows, K 256 to 6144, F 512 to 14336, it foretells the quicker
+// of the two but for two calls within 4% (the estimate of the plain grouped
+// GEMM, whose epilogue is short, was up to 40% off: 512 rows, GRAD, 2048 x 2816:
+// 24 us in pairs, 17 in one-CTA tiles).
+double cut_cost(int mode, const Cut &c, int64_t S, int64_t N, int64_t K, int64_t groups, int sms)
+{
+    const bool pair = c.tiles == TILES_PAIR;
+    const double block = pair ? 0.33 : 0.29, out = mode == BLOCK_GRAD ? (pair ? 8 : 4) : pair ? 4 : 2.5;
+    const int64_t hit = std::min(groups, S), workers = pair ? sms / 2 : sms;
+    const int64_t rows = groups == 1 ? cdiv(S, c.bn) : std::max(hit, S / c.bn + (hit + 1) / 2);
+    const int64_t units = rows * cdiv(N, c.features);
+    const double blocks = static_cast<double>(cdiv(K, BK)) / static_cast<double>(c.splits);
+    return 4 + static_cast<double>(cdiv(units * c.splits, workers)) * std::max(blocks * block, c.splits > 1 ? 0.0 : out) + out +
+           (c.splits > 1 ? (pair ? 5 : 3) : 0);
+}
+
+// One-CTA tiles of 32 rows where groups have few (the ring is then deeper:
+// weights are the traffic), else pairs or one CTA, whichever is quicker.
+Cut cut_rows(int mode, int64_t S, int64_t N, int64_t K, int64_t groups, int sms, const tg_options *opt)
+{
+    const bool few = S <= 32 * std::min(groups, S);
+    const Cut one = cut_tiles(mode, few ? TILES_FEW : TILES_ONE, S, N, K, groups, sms);
+    if (mode == BLOCK_SHRINK || (opt && opt->cta_pair == 1)) return one;
+    const Cut pair = cut_tiles(mode, TILES_PAIR, S, N, K, groups, sms);
+    if (opt && opt->cta_pair == 2) return pair;
+    return !few && cut_cost(mode, pair, S, N, K, groups, sms) < cut_cost(mode, one, S, N, K, groups, sms) ? pair : one;
 }
 
 void set_cut(BlockParams &p, const Cut &c, int64_t N)
