@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     const uint32_t sA = raw + pad;
     const uint32_t sB = sA + STAGES * G::A_STAGE;
     const uint32_t sE = sB + STAGES * G::B_STAGE;
-    uint8_t *bar_area = smem + STAGES * G::STAGE + block_epi_bytes(MODE);
+    uint8_t *bar_area = smem + STAGES * G::STAGE + block_epi_bytes(MODE, BN);
     const uint32_t bar0 = ptx::smem_addr(bar_area);
     // barrier k at bar0 + 8k: [0, S) full, [S, 2S) empty, 2S+{0,1} tfull,
     // 2S+{2,3} tempty, 2S+4 mma-done, 2S+5 never completed; GRAD: from 2S+6
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 ptx::named_barrier_sync(team_id, 32 * team);
         };
         const bool issues = member == 0 && lane == 0;  // all the team's bulk copies
-        const uint32_t area = sE + (MODE == BLOCK_GATED  ? static_cast<uint32_t>(turn) * 4u * EPI_BOX_BYTES
+        const uint32_t area = sE + (MODE == BLOCK_GATED  ? static_cast<uint32_t>(turn) * 8u * EPI_BOX_BYTES
                                     : MODE == BLOCK_GRAD ? duo * 4u * EPI_BOX_BYTES
                                     : MODE == BLOCK_ADAPT && team == 2 ? duo * 2u * EPI_BOX_BYTES
                                                          : static_cast<uint32_t>(warp - 2) * EPI_BOX_BYTES);
@@ -878,17 +878,9 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 const int32_t row0 = row_tile + 32 * c;
                 [[maybe_unused]] const bool whole = row0 + EPI_ROWS <= limit || limit == p.S;
                 if constexpr (MODE == BLOCK_GATED) {
-                    const uint32_t zbox = area;  // gate half, up half; also the exchange
-                    const uint32_t hbox = area + (2u + flip) * EPI_BOX_BYTES;
+                    // the exchange, H's boxes of two pieces in turn, z's (gate half, up half)
+                    const uint32_t hbox = area + (2u + flip) * EPI_BOX_BYTES, zbox = area + (4u + 2u * flip) * EPI_BOX_BYTES;
                     flip ^= 1u;
-                    // the boxes' last stores have read them (H's of the piece before may run on)
-                    if (issues) {
-                        if (p.gate.p)
-                            ptx::bulk_wait_group_read<0>();
-                        else
-                            ptx::bulk_wait_group_read<1>();
-                    }
-                    team_sync();
                     const bool is_up = q >= 2;  // computes rows 16 .. 31, else 0 .. 15
                     const uint32_t give = area + static_cast<uint32_t>(q) * 2048u + lane * 16u;
                     const uint32_t take = area + static_cast<uint32_t>(q ^ 2) * 2048u + lane * 16u;
@@ -900,6 +892,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         else
                             ptx::st_shared_v4(give + k * 512u, v[hi], v[hi + 1], v[hi + 2], v[hi + 3]);
                     }
+                    if (issues) ptx::bulk_wait_group_read<1>();  // the boxes' stores of two pieces before
                     team_sync();
                     uint32_t g[16], u[16], h[8];
 #pragma unroll
@@ -913,10 +906,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                             u[4 * k + e] = is_up ? v[lo + 8 + e] : o[e];
                         }
                     }
-                    if (p.gate.p) {
-                        team_sync();  // the exchange was read
-                        put_box(zbox + (is_up ? EPI_BOX_BYTES : 0u), v);
-                    }
+                    if (p.gate.p) put_box(zbox + (is_up ? EPI_BOX_BYTES : 0u), v);
                     next();
                     switch (p.act) {
                         case 1: gated_values<1>(g, u, h); break;

@@ -64,9 +64,14 @@ struct BlockParams {
 // one of u's first parts and one of its second ones.
 __host__ __device__ inline int32_t adapter_blocks(int32_t count, int32_t Rp) { return (count * Rp + 63) / 64 * 2; }
 
-// Staging boxes of 32 rows of 128 bytes: eight, GRAD sixteen (z of two pieces a
-// team of two warps; dZ takes z's place).
-__host__ __device__ constexpr int block_epi_bytes(int mode) { return mode == BLOCK_GRAD ? 65536 : 32768; }
+// Staging boxes of 32 rows of 128 bytes.  GATED: for each half of the epilogue's
+// warps an exchange of two boxes, and those of two pieces in turn (H, z); GRAD: z of
+// two pieces a team of two warps (dZ takes its place); else eight.  Tiles of 32
+// rows have one piece, so one half of the warps.
+__host__ __device__ constexpr int block_epi_bytes(int mode, int bn)
+{
+    return (mode == BLOCK_GATED || mode == BLOCK_GRAD) && bn > 32 ? 65536 : 32768;
+}
 
 // Barriers, and ADAPT's flags: a byte for each pair of blocks that a tile may
 // have (256 rows of as many adapters of R = 256 at most).

@@ -13,7 +13,7 @@ template <int BN, int STAGES, bool PAIR>
 BlockShape shape()
 {
     using G = Geometry<BN, PAIR>;
-    constexpr int bytes = STAGES * G::STAGE + block_epi_bytes(TG_BLOCK_MODE) + block_bar_bytes(TG_BLOCK_MODE) + G::ALIGN_SLACK;
+    constexpr int bytes = STAGES * G::STAGE + block_epi_bytes(TG_BLOCK_MODE, BN) + block_bar_bytes(TG_BLOCK_MODE) + G::ALIGN_SLACK;
     constexpr int smem = bytes > G::ONE_CTA_PER_SM ? bytes : G::ONE_CTA_PER_SM;
     static_assert(smem <= SMEM_LIMIT, "shared memory budget");
     return {block_kernel<TG_BLOCK_MODE, BN, STAGES, PAIR>, BN, smem, PAIR};
@@ -31,11 +31,11 @@ BlockShape block_shape_shrink(BlockTiles t)
 BlockShape block_shape_adapt(BlockTiles t)
 #endif
 {
-    constexpr bool GRAD = TG_BLOCK_MODE == BLOCK_GRAD;
+    constexpr int STAGES = block_epi_bytes(TG_BLOCK_MODE, 256) > 32768 ? 5 : 6;
 #if TG_BLOCK_MODE != 2  // (the adapters' first products have few features)
-    if (t == TILES_PAIR) return shape<256, GRAD ? 5 : 6, true>();
+    if (t == TILES_PAIR) return shape<256, STAGES, true>();
 #endif
-    return t == TILES_FEW ? shape<32, GRAD ? 8 : 9, false>() : shape<128, GRAD ? 5 : 6, false>();
+    return t == TILES_FEW ? shape<32, 9, false>() : shape<128, STAGES, false>();
 }
 
 }  // namespace tg
