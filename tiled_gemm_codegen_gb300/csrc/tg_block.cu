@@ -608,7 +608,6 @@ cudaError_t pack_operands(const HostStream &hs, uint8_t *arena, Operand *const *
 
 void set_common(BlockParams &p, const HostStream &hs, const tg_options *opt)
 {
-    p.group_m = 8;
     p.err = hs.err;
     p.timeout_ns = opt && opt->timeout_ns ? opt->timeout_ns : HOST_TIMEOUT_NS;
     p.debug_stall = opt ? opt->debug_stall : 0;

@@ -53,6 +53,8 @@ struct BlockUnit {
     int32_t part, nparts, tile;
 };
 
+constexpr int32_t GROUP_M = 8;  // tiles of rows a raster strip
+
 // A warp's walk through the tiles (or shares of tiles): grouped_kernel's, for
 // one group (no bounds to read) or many, 32 groups at a time with a lane each.
 struct BlockWalk {
@@ -104,32 +106,46 @@ __device__ __forceinline__ bool block_walk_to(const BlockParams &p, int64_t t64,
 {
     if (t64 > INT32_MAX) return false;
     const int32_t t = static_cast<int32_t>(t64);
-    while (t >= w.before + w.total) {
+    int32_t r = t, before = 0;
+    if (!p.offsets) {
+        if (t >= w.total) return false;
+        u.g = 0;
+        u.row0 = 0;
+        u.row1 = p.S;
+    }
+    while (p.offsets && t >= w.before + w.total) {
         if (w.base + 32 >= p.groups) return false;
         w.before += w.total;
         block_walk_load<BN>(p, w.base + 32, w);
     }
-    const int32_t at = t - w.before;
-    const int idx = __popc(__ballot_sync(0xffffffffu, at >= w.incl));
-    u.g = w.base + idx;
-    u.row0 = __shfl_sync(0xffffffffu, w.lo, idx);
-    u.row1 = __shfl_sync(0xffffffffu, w.hi, idx);
-    int32_t before = __shfl_sync(0xffffffffu, w.incl, idx > 0 ? idx - 1 : 0);
-    if (idx == 0) before = 0;
-    int32_t r = at - before;
+    if (p.offsets) {
+        const int32_t at = t - w.before;
+        const int idx = __popc(__ballot_sync(0xffffffffu, at >= w.incl));
+        u.g = w.base + idx;
+        u.row0 = __shfl_sync(0xffffffffu, w.lo, idx);
+        u.row1 = __shfl_sync(0xffffffffu, w.hi, idx);
+        before = __shfl_sync(0xffffffffu, w.incl, idx > 0 ? idx - 1 : 0);
+        if (idx == 0) before = 0;
+        r = at - before;
+    }
     const int32_t tiles_m = (u.row1 - u.row0 + BN - 1) / BN;
-    const int32_t per = tiles_m * p.tiles_n;
     u.nparts = p.splits;
-    u.part = r / per;
-    r -= u.part * per;
-    u.tile = (w.before + before) / p.splits + r;
-    const int32_t strip = p.group_m * p.tiles_n;
-    const int32_t first = r / strip * p.group_m;
-    const int32_t in = r % strip, rows = min(tiles_m - first, p.group_m);
-    u.tm = first + in % rows;
-    u.tn = in / rows;
-    u.kb0 = static_cast<int32_t>(static_cast<int64_t>(u.part) * p.k_blocks / u.nparts);
-    u.kb1 = static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * p.k_blocks / u.nparts);
+    u.part = 0;
+    u.kb0 = 0;
+    u.kb1 = p.k_blocks;
+    if (p.splits > 1) {
+        const int32_t per = tiles_m * p.tiles_n;
+        u.part = r / per;
+        r -= u.part * per;
+        u.tile = (w.before + before) / p.splits + r;
+        u.kb0 = static_cast<int32_t>(static_cast<int64_t>(u.part) * p.k_blocks / u.nparts);
+        u.kb1 = static_cast<int32_t>(static_cast<int64_t>(u.part + 1) * p.k_blocks / u.nparts);
+    }
+    // strips of 8 tiles of rows (short calls pay for every division here)
+    const int32_t strip = GROUP_M * p.tiles_n, which = r / strip, first = which * GROUP_M;
+    const int32_t in = r - which * strip, rows = min(tiles_m - first, GROUP_M);
+    u.tn = rows == GROUP_M ? in / GROUP_M : in / rows;
+    u.tm = first + in - u.tn * rows;
     u.mid = p.ext_first ? u.kb0 : u.kb1;
     u.e0 = u.e1 = 0;
     u.ad = {0, 0, 0};
@@ -181,9 +197,16 @@ __device__ __forceinline__ int32_t block_rows_n(const BlockUnit &u)
     return min(BN, (u.row1 - u.row0 - u.tm * BN + 31) / 32 * 32);
 }
 
-// 1 / (1 + exp(-g)) by the fast exponential and reciprocal (a few units off:
-// far below a bf16 rounding of what it goes into).
-__device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// 1 / (1 + 2^(-g log2 e)) by the hardware's approximate power and reciprocal
+// (a unit or two off each: far below a bf16 rounding of what it goes into),
+// denormals as zeros.
+__device__ __forceinline__ float fast_sigmoid(float g)
+{
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * g));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
+}
 
 // act(g) and its slope.  tanh(y) = 2 / (1 + exp(-2 y)) - 1.
 template <int ACT>
@@ -318,7 +341,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     constexpr int TILE_F = PAIR ? 2 * LANES : LANES;
     constexpr uint32_t BOX_BYTES = BK * 64 * 2;               // 64 k x 64 features, 8 KB
     constexpr uint32_t EPI_BOX_BYTES = 4096;                  // 32 rows of 128 bytes
-    constexpr uint32_t EPI_WARPS_TOTAL = (PAIR ? 2 : 1) * BLOCK_EPI_WARPS;
+    constexpr int EPI_WARPS = BLOCK_EPI_WARPS, TURNS = EPI_WARPS / 4;  // warps of a quadrant: pieces in turn
+    constexpr uint32_t EPI_WARPS_TOTAL = (PAIR ? 2 : 1) * EPI_WARPS;
     constexpr int EPI_ROWS = 32, EPI_ROW_BYTES = 128;
     static_assert(MODE != BLOCK_SHRINK || !PAIR, "adapters' first products take one-CTA tiles");
     constexpr uint32_t TMEM_ALLOC = static_cast<uint32_t>(G::TMEM_COLS);
@@ -385,11 +409,11 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         }
         ptx::mbar_init(done_bar, 1);
         ptx::mbar_init(stall_bar, 1);
-        for (uint32_t i = 0; MODE == BLOCK_GRAD && i < 8; ++i) ptx::mbar_init(z_bar(0, i), 1);
+        for (uint32_t i = 0; MODE == BLOCK_GRAD && i < EPI_WARPS; ++i) ptx::mbar_init(z_bar(0, i), 1);
         if (MODE == BLOCK_ADAPT) {
-            ptx::mbar_init(flag_bar, BLOCK_EPI_WARPS);
+            ptx::mbar_init(flag_bar, EPI_WARPS);
             for (uint32_t s = 0; s < STAGES; ++s) {
-                ptx::mbar_init(check_bar(s), BLOCK_EPI_WARPS);
+                ptx::mbar_init(check_bar(s), EPI_WARPS);
                 ptx::mbar_init(coming_bar(s), 1);
             }
             for (int i = 0; i < (block_bar_bytes(MODE) - 512) / 4; ++i) flag_words[i] = 0;
@@ -780,7 +804,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         auto zero_others = [&](const BlockUnit &w, int32_t row_tile, int32_t limit) {
             if constexpr (MODE == BLOCK_SHRINK) {
                 if (w.tn != 0) return;
-                for (int32_t row = row_tile + (warp - 2); row < limit; row += BLOCK_EPI_WARPS) {
+                for (int32_t row = row_tile + (warp - 2); row < limit; row += EPI_WARPS) {
                     const int32_t tile = row / p.wide_bn, in = row - tile * p.wide_bn;
                     const bool second = tile != tile0;
                     const int32_t count = second ? ad1.count : ad0.count;
@@ -793,7 +817,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         if (p.debug_stall) {  // watchdog self-test: a barrier that nothing completes
             const int r = wait_bounded(stall_bar, 0, wd);
             if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
-            ok = agree(r == WAIT_OK, 1, 32 * BLOCK_EPI_WARPS);
+            ok = agree(r == WAIT_OK, 1, 32 * EPI_WARPS);
         }
         if (MODE == BLOCK_SHRINK || MODE == BLOCK_ADAPT) ptx::griddep_wait();  // the tables
         uint32_t n = 0;
@@ -864,17 +888,16 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             };
 
             // z of a unit's first two pieces (behind the team's last use of the boxes).
-            auto load_two = [&]() {
+            auto load_first = [&]() {
                 if constexpr (MODE == BLOCK_GRAD) {
                     if (p.z_tma) team_sync();
                     load_z(turn, flip);
-                    load_z(turn + 2, flip ^ 1u);
+                    load_z(turn + TURNS, flip ^ 1u);
                 }
             };
 
-            // 32 rows of the accumulator -> the outputs.  `next` is called once
-            // v is used up.  false: a wait ran out (GRAD).
-            auto piece = [&](int c, uint32_t (&v)[32], auto &&next) -> bool {
+            // 32 rows of the accumulator -> the outputs.  false: a wait ran out (GRAD).
+            auto piece = [&](int c, uint32_t (&v)[32]) -> bool {
                 const int32_t row0 = row_tile + 32 * c;
                 [[maybe_unused]] const bool whole = row0 + EPI_ROWS <= limit || limit == p.S;
                 if constexpr (MODE == BLOCK_GATED) {
@@ -907,7 +930,6 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         }
                     }
                     if (p.gate.p) put_box(zbox + (is_up ? EPI_BOX_BYTES : 0u), v);
-                    next();
                     switch (p.act) {
                         case 1: gated_values<1>(g, u, h); break;
                         case 2: gated_values<2>(g, u, h); break;
@@ -941,7 +963,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         }
                         if (!agree(r == WAIT_OK, team_id, 64)) return false;
                     }
-                    if (c != turn) load_z(c + 2, b ^ 1u);  // (the first two came together)
+                    if (c != turn) load_z(c + TURNS, b ^ 1u);  // (the first two came together)
                     uint32_t h[16];
                     switch (p.act) {
                         case 1: gated_grad_box<1>(box + frag_at, EPI_BOX_BYTES, v, h); break;
@@ -949,7 +971,6 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         case 3: gated_grad_box<3>(box + frag_at, EPI_BOX_BYTES, v, h); break;
                         default: gated_grad_box<0>(box + frag_at, EPI_BOX_BYTES, v, h); break;
                     }
-                    next();
                     ptx::fence_proxy_async_smem();
                     team_sync();
                     flush(box, &tmG, p.gate, 2, row0, limit, whole, f_box);
@@ -985,7 +1006,6 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                             asm volatile("st.shared.u32 [%0], %1;" ::"r"(unit_at(box, frag_row(i, lane), f >> 2) + (f & 3) * 4), "r"(v[i]) : "memory");
                         }
                     }
-                    next();
                     ptx::fence_proxy_async_smem();
                     team_sync();
                     flush(box, &tmO, p.out0, p.out_bf16 ? 2 : 4, row0, limit, whole, f_box);
@@ -1031,7 +1051,6 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                                 if (r + e < p.R) o[e] = static_cast<uint16_t>(hi[e >> 1] >> (16 * (e & 1)));
                         }
                     }
-                    next();
                 }
                 return true;
             };
@@ -1092,8 +1111,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 at_it += static_cast<uint32_t>(w.kb1 - w.mid + w.e1 - w.e0);
                 if (pairs > 0) {
                     if (PAIR && lane == 0) ptx::mbar_arrive(flag_bar);
-                    if (!agree(fine, 1, 32 * BLOCK_EPI_WARPS)) break;
-                    flagged = !agree(!flagged, 1, 32 * BLOCK_EPI_WARPS);
+                    if (!agree(fine, 1, 32 * EPI_WARPS)) break;
+                    flagged = !agree(!flagged, 1, 32 * EPI_WARPS);
                 }
             }
             auto add_flagged = [&](int c, uint32_t (&v)[32]) {
@@ -1126,7 +1145,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             };
 
             const bool empty = w.kb0 == w.kb1 && w.e0 == w.e1, shared = w.nparts > 1 && !empty;
-            if (lanes_in && !shared) load_two();
+            if (lanes_in && !shared) load_first();
             const uint32_t buf = n & 1u;
             if (!empty) {
                 const uint32_t tph = (n >> 1) & 1u;
@@ -1135,7 +1154,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 const int r = wait_bounded(tfull_bar(buf), tph, wd);
                 if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
                 const bool here = r == WAIT_OK;
-                if (!(shared || flagged ? agree(here, 1, 32 * BLOCK_EPI_WARPS)
+                if (!(shared || flagged ? agree(here, 1, 32 * EPI_WARPS)
                       : team == 1       ? __all_sync(0xffffffffu, here) != 0
                                         : agree(here, team_id, 32 * team)))
                     break;
@@ -1152,16 +1171,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             // for all of them: short calls run from cold instruction caches.
             for (bool sum = false;; sum = true) {
                 uint32_t v[32];
-                // The next piece's loads are on their way while one is stored.
-                auto advance = [&](int c) {
-                    if (sum || empty) return;
-                    if (lanes_in && c < pieces)
-                        load_fragments(taddr + c * 32, v);
-                    else
-                        release_tmem(buf);
-                };
-                advance(turn);
-                for (int c = turn; ok && lanes_in && c < pieces; c += 2) {
+                if (!sum && !empty && !(lanes_in && turn < pieces)) release_tmem(buf);
+                for (int c = turn; ok && lanes_in && c < pieces; c += TURNS) {
                     if (sum) {
                         float4 acc[8];
 #pragma unroll
@@ -1188,7 +1199,9 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0u;
                     } else {
+                        load_fragments(taddr + c * 32, v);
                         ptx::tmem_wait_ld(v);
+                        if (c + TURNS >= pieces) release_tmem(buf);
                         add_flagged(c, v);
                     }
                     if (shared && !sum) {
@@ -1197,31 +1210,30 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         for (int j4 = 0; j4 < 8; ++j4)
                             __stcg(mine + (c * 8 + j4) * BM, make_float4(__uint_as_float(v[4 * j4]), __uint_as_float(v[4 * j4 + 1]),
                                                                          __uint_as_float(v[4 * j4 + 2]), __uint_as_float(v[4 * j4 + 3])));
-                        advance(c + 2);
                     } else {
-                        ok = piece(c, v, [&] { advance(c + 2); });
+                        ok = piece(c, v);
                     }
                 }
                 if (!shared || sum) break;
                 __threadfence();
-                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
+                ptx::named_barrier_sync(1, 32 * EPI_WARPS);
                 if (warp == 2 && lane == 0) {
                     const int32_t old = atomicAdd(p.counters + half, 1);
                     *last_flag = old == w.nparts - 1 ? 1 : 0;
                     if (old == w.nparts - 1) atomicExch(p.counters + half, 0);  // ready for the next call
                 }
-                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
+                ptx::named_barrier_sync(1, 32 * EPI_WARPS);
                 if (!*last_flag) break;
                 __threadfence();
-                if (lanes_in) load_two();
+                if (lanes_in) load_first();
             }
             if (ok && (!shared || *last_flag)) zero_others(w, row_tile, limit);
             // (the flags, of the last share and of B, may be written again)
-            if (shared || flagged) ok = agree(ok, 1, 32 * BLOCK_EPI_WARPS);
+            if (shared || flagged) ok = agree(ok, 1, 32 * EPI_WARPS);
             if (!ok) break;
             if (flagged) {
-                for (int32_t i = (warp - 2) * 32 + lane; i * 4 < pairs; i += 32 * BLOCK_EPI_WARPS) flag_words[i] = 0;
-                ptx::named_barrier_sync(1, 32 * BLOCK_EPI_WARPS);
+                for (int32_t i = (warp - 2) * 32 + lane; i * 4 < pairs; i += 32 * EPI_WARPS) flag_words[i] = 0;
+                ptx::named_barrier_sync(1, 32 * EPI_WARPS);
             }
         }
         // Rows of no group: zeros (SHRINK: of u and its parts).
@@ -1232,8 +1244,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 end.before += end.total;
                 block_walk_load<BN>(p, end.base + 32, end);
             }
-            const int64_t w0 = static_cast<int64_t>(blockIdx.x) * BLOCK_EPI_WARPS + (warp - 2);
-            const int64_t nw = static_cast<int64_t>(gridDim.x) * BLOCK_EPI_WARPS;
+            const int64_t w0 = static_cast<int64_t>(blockIdx.x) * EPI_WARPS + (warp - 2);
+            const int64_t nw = static_cast<int64_t>(gridDim.x) * EPI_WARPS;
             auto zero = [&](const BlockOut &o, int64_t row, int32_t cols) {
                 if (!o.p) return;
                 uint8_t *dst = static_cast<uint8_t *>(o.p) + row * o.ld * 2;
