@@ -18,7 +18,6 @@ namespace {
 
 constexpr int64_t ADAPT_GROUPS = 4096;  // adapters a call takes at most
 constexpr int64_t ADAPT_RANK = 256;
-constexpr int64_t ADAPT_FEW_ROWS = 2048;
 constexpr int64_t ADAPT_FEW_BYTES = 32 << 20;
 
 // ------------------------------------------------------------ adapter tables
@@ -606,6 +605,40 @@ cudaError_t pack_operands(const HostStream &hs, uint8_t *arena, Operand *const *
     return e;
 }
 
+// adapter_rows_kernel's launch: blocks of 512 threads beside the projection's
+// `workers` SMs where there are enough, else small ones, no more than run at
+// once; clusters of at most four steps of 32 k a warp of a small block.  cost:
+// about what it takes, in microseconds: for every 32 R the sums, and rounds of
+// loads; beside the projection only the rounds, and what further 32 R add for
+// each adapter's A.  Up to 8 it is quicker than the products by tcgen05, which
+// cost some 10 more whatever they are (in all, rows against products: 1000 rows
+// of 8 adapters, 1024 x 1024, R = 16: 14 us, 24; 250 of 8, 4096 x 4096: 25, 32;
+// 500 of 8: 38, 42; 2000 of 8: 67, 61; R = 64, one row: 18, 21; 8 of 8: 28, 24;
+// 64 of 40: 45, 41).
+struct RowsCut {
+    bool early;
+    int64_t clusters;
+    int32_t cluster;
+    double cost;
+};
+constexpr double ROWS_COST = 8;
+
+RowsCut cut_few_rows(int64_t S, int64_t K, int64_t R, int64_t hit, int64_t workers, int sms)
+{
+    RowsCut c;
+    const int64_t wanted = 1 + S / 16 + hit;
+    c.early = wanted + workers <= sms;
+    c.clusters = std::min<int64_t>(wanted, 4 * sms);
+    const int64_t room = c.early ? sms - workers : 4 * sms;
+    c.cluster = 1;
+    while (c.cluster < 8 && K > 512 * c.cluster && c.clusters * c.cluster * 2 <= room) c.cluster *= 2;
+    const int64_t steps = cdiv(cdiv(K, 32), (c.early ? 16 : 4) * c.cluster), depth = S > 8 * hit ? 2 : 4;
+    const double passes = static_cast<double>(cdiv(R, 32)), rounds = static_cast<double>(cdiv(steps, depth));
+    c.cost = c.early ? passes * 1.5 * rounds + (passes - 1) * static_cast<double>(hit)
+                     : passes * (2.5 + 2.0 * rounds) * static_cast<double>(cdiv(wanted, c.clusters));
+    return c;
+}
+
 void set_common(BlockParams &p, const HostStream &hs, const tg_options *opt)
 {
     p.err = hs.err;
@@ -695,7 +728,8 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     const int64_t tiles = cdiv(S, cy.bn);
     // Few rows: u by adapter_rows_kernel, a fixed number of blocks a tile.
     const int64_t stride = adapter_blocks(static_cast<int32_t>(std::min(cy.bn, hit)), static_cast<int32_t>(Rp));
-    const bool few = S <= ADAPT_FEW_ROWS && groups <= ROWS_GROUPS && tiles * stride * cy.bn * 128 <= ADAPT_FEW_BYTES;
+    const RowsCut cr = cut_few_rows(S, K, R, hit, std::min<int64_t>(cy.units * cy.splits, hs.sms) * (cy.tiles == TILES_PAIR ? 2 : 1), hs.sms);
+    const bool few = cr.cost <= ROWS_COST && groups <= ROWS_GROUPS && tiles * stride * cy.bn * 128 <= ADAPT_FEW_BYTES;
     // Else a tile's blocks round its adapters up; together at most so many.
     const int64_t blocks = few ? tiles * stride : 2 * (tiles + cdiv((tiles + hit) * Rp, 64));
     if (blocks * cy.bn > INT32_MAX / 8) return TG_ERR_UNSUPPORTED;
@@ -769,27 +803,20 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     p.N = static_cast<int32_t>(R);
     p.out0 = BlockOut{U, ldu, 0};
     if (few) {
-        const int64_t workers = std::min<int64_t>(cy.units * cy.splits, hs.sms) * (pair ? 2 : 1), wanted = 1 + S / 16 + hit;
-        const bool early = wanted + workers <= hs.sms;
-        const int64_t clusters = early ? wanted : std::min<int64_t>(wanted, 4 * hs.sms);
-        // at most four steps of 32 k a warp of a small block, and no more blocks than run at once
-        const int64_t room = early ? hs.sms - workers : 4 * hs.sms;
-        int32_t cluster = 1;
-        while (cluster < 8 && K > 512 * cluster && clusters * cluster * 2 <= room) cluster *= 2;
-        py.ext_first = !early && !pair && cy.units * cy.splits <= hs.sms ? 1 : 0;
+        py.ext_first = !cr.early && !pair && cy.units * cy.splits <= hs.sms ? 1 : 0;
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
-        cfg.blockDim = dim3(early ? 512 : 128);
+        cfg.gridDim = dim3(static_cast<unsigned>(cr.clusters * cr.cluster));
+        cfg.blockDim = dim3(cr.early ? 512 : 128);
         cfg.stream = hs.stream;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr.val.clusterDim.x = static_cast<unsigned>(cr.cluster);
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, early ? adapter_rows_kernel<512> : adapter_rows_kernel<128>, p, static_cast<const uint16_t *>(x.p), x.ld, static_cast<const uint16_t *>(a.p),
+        e = cudaLaunchKernelEx(&cfg, cr.early ? adapter_rows_kernel<512> : adapter_rows_kernel<128>, p, static_cast<const uint16_t *>(x.p), x.ld, static_cast<const uint16_t *>(a.p),
                                a.ld, a_shared ? int64_t(0) : a.stride, static_cast<int32_t>(K), static_cast<int32_t>(tiles),
-                               static_cast<int32_t>(stride), cluster, early ? 1 : 0);
+                               static_cast<int32_t>(stride), cr.cluster, cr.early ? 1 : 0);
         if (e != cudaSuccess) return host_cuda_status(e);
     } else {
         BlockMaps ma;
