@@ -1,0 +1,162 @@
+"""A feed-forward block with low-rank adapters on the library's operators: a
+projection beside which each row has its request's adapter, then the gated
+projection and the way down.  The block trains as a whole or, its weights
+frozen, by its adapters alone, and answers single tokens of many requests.
+
+    python examples/gated_block.py [--tokens 4096] [--width 2048] [--hidden 5632] [--adapters 16] [--rank 16]
+
+prints the loss of a few steps of gradient descent of a set length, the time of a step,
+and of one token of each adapter.
+"""
+from __future__ import annotations
+
+import argparse
+import os
+import sys
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+import torch  # noqa: E402
+
+import tiled_gemm_codegen_gb300 as tg  # noqa: E402
+
+BF16 = torch.bfloat16
+
+
+def _product(a, b):
+    return tg.gemm_fused(a, b, out_dtype=BF16)
+
+
+class Gated(torch.autograd.Function):
+    """down(silu(gate(x)) * up(x)) for bf16 x [S, D], gate and up in one matrix
+    [2 F, D] (the gate's rows first) and down [D, F], as linear layers store
+    theirs."""
+
+    @staticmethod
+    def forward(ctx, x, gate_up, down):
+        h, z = tg.gemm_gated(x, gate_up.t(), Z=True)
+        ctx.save_for_backward(x, gate_up, down, z)
+        return _product(h, down.t())
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, gate_up, down, z = ctx.saved_tensors
+        dy = dy.contiguous()
+        dz, h = tg.gemm_gated_grad(dy, down, z, H=True)
+        need = ctx.needs_input_grad
+        return (_product(dz, gate_up) if need[0] else None, _product(dz.t(), x) if need[1] else None,
+                _product(dy.t(), h) if need[2] else None)
+
+
+class Adapted(torch.autograd.Function):
+    """x @ W.T + scales[g] * (x @ A[g].T) @ B[g] for rows in the order of their
+    adapters (offsets); W [N, K] bf16 and frozen, A [groups, R, K] and B [groups,
+    R, N] bf16, scales fp32; rows of no adapter have the first term alone."""
+
+    @staticmethod
+    def forward(ctx, x, W, A, B, scales, offsets):
+        y, u = tg.gemm_adapted(x, W.t(), A, B, offsets, scales=scales, U=True, out_dtype=BF16)
+        ctx.save_for_backward(x, W, A, B, scales, offsets, u)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, W, A, B, scales, offsets, u = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx, du = tg.gemm_adapted(dy, W, B, A, offsets, scales=scales, U=True, out_dtype=BF16)
+        dA = tg.gemm_grouped_wgrad(du, x, offsets, out_dtype=BF16)
+        return dx, None, dA, tg.gemm_grouped_wgrad(u, dy, offsets, out_dtype=BF16), None, None
+
+
+class Rows(torch.autograd.Function):
+    """The rows of bf16 x [S, D] in an order of one id a row, or back from it."""
+
+    @staticmethod
+    def forward(ctx, x, order, back):
+        ctx.order, ctx.back = order, back
+        return tg.expert_combine(x, order) if back else tg.expert_gather(x, order)
+
+    @staticmethod
+    def backward(ctx, dy):
+        dy = dy.contiguous()
+        return (tg.expert_gather(dy, ctx.order) if ctx.back else tg.expert_combine(dy, ctx.order)), None, None
+
+
+def block(x, ids, weights, adapters):
+    """y [S, D] = Gated(Adapted(x)) for rows of adapters ids [S] (-1: of none);
+    weights: (W [D, D], gate_up, down), adapters: (A, B, scales)."""
+    W, gate_up, down = weights
+    A, B, scales = adapters
+    groups = A.shape[0]
+    order = tg.expert_sort(torch.where(ids < 0, groups, ids)[:, None], groups + 1)  # rows of no adapter last
+    p = Adapted.apply(Rows.apply(x, order, False), W, A, B, scales, order.offsets[:-1])
+    return Rows.apply(Gated.apply(p, gate_up, down), order, True)
+
+
+def make(width, hidden, adapters, rank, dev="cuda"):
+    """Random (weights, adapters): B is zero at first, as adapters start."""
+    def r(*s):
+        return (torch.randn(*s, device=dev) * s[-1] ** -0.5).to(BF16)
+
+    return (r(width, width), r(2 * hidden, width), r(width, hidden)), (
+        r(adapters, rank, width), torch.zeros(adapters, rank, width, dtype=BF16, device=dev), torch.full((adapters,), 2.0, device=dev))
+
+
+def _us(f, n=50):
+    for _ in range(5):
+        f()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    for _ in range(n):
+        f()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b) * 1e3 / n
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    for name, value in (("tokens", 4096), ("width", 2048), ("hidden", 5632), ("adapters", 16), ("rank", 16), ("steps", 5)):
+        ap.add_argument(f"--{name}", type=int, default=value)
+    a = ap.parse_args()
+    tg.load()
+    torch.manual_seed(0)
+    weights, (A, B, scales) = make(a.width, a.hidden, a.adapters, a.rank)
+    x = torch.randn(a.tokens, a.width, device="cuda").to(BF16)
+    target = torch.randn(a.tokens, a.width, device="cuda").to(BF16)
+    ids = torch.randint(0, a.adapters, (a.tokens,), device="cuda")
+
+    def step(leaves):
+        y = block(x, ids, weights, (A, B, scales))
+        loss = (y.float() - target.float()).square().mean()
+        for t in leaves:
+            t.grad = None
+        loss.backward()
+        return loss
+
+    for what, leaves in (("adapters", [A, B]), ("all but the frozen projection", [A, B, *weights[1:]])):
+        for t in leaves:
+            t.requires_grad_()
+        for i in range(a.steps):
+            loss = step(leaves)
+            with torch.no_grad():
+                for t in leaves:
+                    t -= 1e-3 * t.grad * (t.numel() ** 0.5 / t.grad.float().norm().clamp(min=1e-20))  # 1e-3 a weight
+            print(f"{what}, step {i}: loss {loss.item():.4f}")
+        print(f"{what}: {_us(lambda: step(leaves), 10):.0f} us a step of {a.tokens} tokens")
+    with torch.no_grad():
+        one, each = x[:a.adapters], torch.arange(a.adapters, device="cuda")
+        each_us = _us(lambda: block(one, each, weights, (A, B, scales)))
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            block(one, each, weights, (A, B, scales))  # workspaces of the stream
+        with torch.cuda.graph(graph, stream=side):
+            block(one, each, weights, (A, B, scales))
+        print(f"a token of each of {a.adapters} adapters: {each_us:.1f} us, in a graph {_us(graph.replay):.1f} us")
+    if tg.device_error() != tg.TG_OK:
+        raise SystemExit("device error")
+
+
+if __name__ == "__main__":
+    main()
