@@ -283,6 +283,28 @@ def test_boxes_stored_plainly_between_boxes_stored_by_tma(size, F, pair):
     assert int(wrong) == 0
 
 
+@pytest.mark.parametrize("activation", ACTS)
+def test_gated_grad_of_huge_gates(activation):
+    """Gates whose square (and cube) pass fp32: the slope is 0 or 1 there, the
+    activation 0 or the gate."""
+    S, K, F = 40, 16, 64
+    dY, yv = _rand((S, K), 45)
+    V, vv = _mats((), K, F, 46, True)
+    Z, zv = _rand((S, 2 * F), 47)
+    for r, g in enumerate((2.0 ** 66, -(2.0 ** 66), 2.0 ** 20, -(2.0 ** 20), 2.0 ** 100, -(2.0 ** 100))):
+        Z[r, :F], zv[r, :F] = g, g
+    dZ, H = tg.gemm_gated_grad(dY, V, Z, H=True, activation=activation)
+    with np.errstate(all="ignore"):
+        dz, h = _grad_ref(activation, yv @ vv, zv, F, in_group(S, [S]))
+        g, u = zv[:, :F], zv[:, F:]
+        # (huge gates: s and 1 - s are exact, and what is left are two products' roundings)
+        e_act = np.where(np.abs(g) > 1e5, 4 * U32 * np.abs(g) * (g > 0), act_error(g))
+        e_slope = np.where(np.abs(g) > 1e5, 4 * U32, slope_error(g))
+    dh = yv @ vv
+    assert within(dZ, dz, np.concatenate((np.abs(dh * u) * (e_slope + 8 * U32), np.abs(dh) * (e_act + 4 * U32 * np.abs(act(activation, g)))), 1), BF)
+    assert within(H, h, np.abs(u) * (e_act + 4 * U32 * np.abs(act(activation, g))), BF)
+
+
 def test_gradients_of_a_block_against_differences():
     """x -> gated -> down, all gradients: each against the central difference
     of the 64-bit formula along a random direction."""
@@ -459,6 +481,60 @@ def test_adapted_gradients_against_differences():
         assert abs(float((_np(got) * step).sum()) - diff) <= 2.0 ** -8 * mag
 
 
+@pytest.mark.parametrize("sizes,lead,S", [([3, 0, 1], 500, 1200), ([0, 0], 0, 700), ([2, 40], 33, 75), ([1] * 40, 1900, 2000)])
+@pytest.mark.parametrize("K,R", [(64, 16), (1000, 20), (640, 100)])
+def test_adapted_mostly_rows_of_no_adapter(sizes, lead, S, K, R):
+    t, v = _adapters(sizes, K, 130, R, 160, S=S)
+    y, u = adapted(*v, sizes, lead=lead)
+    assert np.abs(u).max() < 2 ** 16 and np.abs(y).max() < 2 ** 24
+    for _ in range(2):
+        U = torch.full((S, R), NAN, dtype=BF, device=dev())
+        Y, U = tg.gemm_adapted(*t, _offsets(sizes, lead), U=U)
+        assert np.array_equal(_np(Y), y) and np.array_equal(_np(U), _bf(u))
+
+
+@pytest.mark.parametrize("groups", [511, 512, 513, 1500, 4096])
+@pytest.mark.parametrize("R", [8, 64])
+def test_adapted_many_adapters(groups, R):
+    g = np.random.default_rng(groups)
+    sizes = [int(n) for n in g.integers(0, 3, groups)]
+    K, N, S = 72, 72, sum(sizes) + 20
+    t, v = _adapters(sizes, K, N, R, 170, S=S)
+    Y, U = tg.gemm_adapted(*t, _offsets(sizes, 9), U=True)
+    y, u = adapted(*v, sizes, lead=9)
+    assert np.array_equal(_np(Y), y) and np.array_equal(_np(U), _bf(u))
+
+
+@pytest.mark.parametrize("sizes,S", [([900, 0, 700, 300, 77], 2000), ([1, 1, 3000], 3100), ([40] * 60, 2500)])
+@pytest.mark.parametrize("R", [16, 64])
+@pytest.mark.parametrize("pair", [0, 1, 2])
+def test_adapted_long_products(sizes, S, R, pair):
+    """u by the tensor cores, its contraction shared, in both kinds of tiles."""
+    K, N = 2048, 264
+    t, v = _adapters(sizes, K, N, R, 180, S=S)
+    y, u = adapted(*v, sizes)
+    assert np.abs(u).max() < 2 ** 16 and np.abs(y).max() < 2 ** 24
+    for _ in range(2):
+        Y, U = tg.gemm_adapted(*t, _offsets(sizes), U=True, options=tg.make_options(cta_pair=pair))
+        assert np.array_equal(_np(Y), y) and np.array_equal(_np(U), _bf(u))
+
+
+@pytest.mark.parametrize("sizes", [[3, 1, 0, 7], [300, 500, 20]])
+@pytest.mark.parametrize("R", [16, 40])
+@pytest.mark.parametrize("which", ["A", "B", "both"])
+def test_adapted_one_matrix_for_every_adapter(sizes, R, which):
+    (X, W, A, B), (xv, wv, av, bv) = _adapters(sizes, 72, 136, R, 190)
+    E = len(sizes)
+    if which != "B":
+        A, av = A[:1].expand(E, *A.shape[1:]), np.repeat(av[:1], E, 0)
+    if which != "A":
+        B, bv = B[:1].expand(E, *B.shape[1:]), np.repeat(bv[:1], E, 0)
+    scales = torch.tensor([2.0 ** (i % 3) for i in range(E)], device=dev())
+    Y, U = tg.gemm_adapted(X, W, A, B, _offsets(sizes), scales=scales, U=True)
+    y, u = adapted(xv, wv, av, bv, sizes, _np(scales))
+    assert np.array_equal(_np(Y), y) and np.array_equal(_np(U), _bf(u))
+
+
 # ---------------------------------------------------------------- all of them
 def _calls(S, sizes, seed=100):
     """One call of each operator with preallocated outputs, as functions of
@@ -513,6 +589,13 @@ def test_same_bits_again_graph_and_stream():
         torch.cuda.synchronize()
         got = [t.clone() for t in out]
         assert all(torch.equal(a, b) for a, b in zip(got, run(_offsets(moved)))), moved
+
+
+@pytest.mark.parametrize("S,sizes", [(1045, [300, 0, 45, 700]), (7, [1, 0, 3, 3])])
+def test_packed_operands_give_the_same_bits(S, sizes):
+    off = _offsets(sizes)
+    run, _ = _calls(S, sizes)
+    assert all(torch.equal(a, b) for a, b in zip(run(off), run(off, tg.make_options(force_pack=1))))
 
 
 def test_two_streams_at_once():

@@ -77,10 +77,9 @@ __device__ __forceinline__ int32_t each_group(const BlockParams &p, int32_t *par
 }
 
 // By one block: the tables of AdapterTables.  stride: blocks of
-// a tile (0: as many as it needs, tiles one behind another).  Returns the
-// number of groups that have rows.
+// a tile (0: as many as it needs, tiles one behind another).
 template <int THREADS>
-__device__ __forceinline__ int32_t write_tables(const BlockParams &p, int32_t tiles, int32_t stride, int32_t *part, int32_t *his)
+__device__ __forceinline__ void write_tables(const BlockParams &p, int32_t tiles, int32_t stride, int32_t *part, int32_t *his)
 {
     const int tid = static_cast<int>(threadIdx.x);
     const int32_t used = each_group<THREADS>(p, part, his, [&](int32_t g, int32_t lo, int32_t hi, int32_t place) {
@@ -121,7 +120,6 @@ __device__ __forceinline__ int32_t write_tables(const BlockParams &p, int32_t ti
         blocks += part[THREADS / 32 - 1];
         __syncthreads();
     }
-    return used;
 }
 
 constexpr int TABLE_THREADS = 1024;
@@ -184,10 +182,11 @@ __device__ __forceinline__ void rows_sums(const uint16_t *x0, const uint16_t *x1
 }
 
 // One chunk of 16 rows of a group by a cluster (adapter_rows_kernel).  bounds: the
-// groups' ends; chunks: the chunks (low half) and groups with rows up to each.
+// groups' ends; chunks: the chunks (low half) and groups with rows up to each,
+// total in all; the chunks behind them are rows of no group.
 template <int ROWS_THREADS>
 __device__ __forceinline__ void rows_chunk(const BlockParams &p, const uint16_t *X, int64_t ldx, const uint16_t *A, int64_t lda,
-                                           int64_t strideA, int32_t K, int32_t stride, int32_t cluster, int32_t rank, int32_t want,
+                                           int64_t strideA, int32_t K, int32_t stride, int32_t cluster, int32_t rank, int32_t want, int32_t total,
                                            int32_t first_row, const int32_t *bounds, const int32_t *chunks, int32_t *found,
                                            float (&sums)[ROWS_THREADS / 32][16][33])
 {
@@ -196,6 +195,12 @@ __device__ __forceinline__ void rows_chunk(const BlockParams &p, const uint16_t 
     __syncthreads();  // the chunk before is done with found
     if (tid < 8) found[tid] = 0;
     __syncthreads();
+    if (want >= total && tid == 0) {
+        const int32_t lead = (first_row + 15) / 16, b = want - total, at = b < lead ? b * 16 : bounds[p.groups - 1] + (b - lead) * 16;
+        found[0] = -1;
+        found[1] = at;
+        found[2] = min(16, (b < lead ? first_row : p.S) - at);
+    }
     for (int32_t i = tid; i < p.groups; i += ROWS_THREADS) {
         const int32_t end = chunks[i], before = i > 0 ? chunks[i - 1] : 0;
         if (want < (before & 0xffff) || want >= (end & 0xffff)) continue;
@@ -231,13 +236,25 @@ __device__ __forceinline__ void rows_chunk(const BlockParams &p, const uint16_t 
         }
     }
 
+    const int32_t me = rank * WARPS + warp, all = cluster * WARPS;
+    if (g < 0) {  // zeros
+        ptx::griddep_launch_dependents();
+        __syncthreads();
+        for (int32_t in = me; in < rows; in += all) {
+            const int32_t row = row0 + in, tile = row / p.wide_bn;
+            zero_columns(p, row % p.wide_bn, tile * stride, found[tile == t0 ? 5 : 7], -1, lane);
+            for (int32_t r = lane; p.out0.p && r < p.R; r += 32)
+                static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = 0;
+        }
+        return;
+    }
+
     // sums over this warp's share of K
     const int gid = lane >> 2, t = lane & 3;
     const uint16_t *x0 = X + static_cast<int64_t>(row0 + min(gid, rows - 1)) * ldx;
     const uint16_t *x1 = X + static_cast<int64_t>(row0 + min(gid + 8, rows - 1)) * ldx;
     const float scale = p.scales ? __ldg(p.scales + g) : 1.0f;
     const int32_t steps = K / 32;  // whole ones
-    const int32_t me = rank * WARPS + warp, all = cluster * WARPS;
     for (int32_t r0 = 0; r0 < p.R; r0 += 32) {
         const int tiles_r = min(4, (p.R - r0 + 7) / 8);
         float c[4][4];
@@ -347,20 +364,12 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
     __shared__ int32_t part[32], bounds[ROWS_GROUPS], chunks[ROWS_GROUPS];
     __shared__ int32_t found[8];  // group, first row, rows, place; adapters before and in the (two) tiles
     __shared__ float sums[WARPS][16][33];
-    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int tid = static_cast<int>(threadIdx.x);
     const int32_t rank = cluster > 1 ? static_cast<int32_t>(ptx::cluster_ctarank()) : 0;
     const int32_t cid = static_cast<int32_t>(blockIdx.x) / cluster;
     if (cid == 0) {
         if (rank > 0) return;
-        const int32_t used = write_tables<ROWS_THREADS>(p, tiles, stride, part, bounds);
-        // rows of no group: zeros
-        const int32_t first = max(0, min(__ldg(p.offsets), p.S)), last = used > 0 ? p.tab.hi[used - 1] : first;
-        for (int32_t i = warp; i < first + p.S - last; i += WARPS) {
-            const int32_t row = i < first ? i : last + i - first, tile = row / p.wide_bn;
-            zero_columns(p, row % p.wide_bn, tile * stride, p.tab.tile[tile].y, -1, lane);
-            for (int32_t r = lane; p.out0.p && r < p.R; r += 32)
-                static_cast<uint16_t *>(p.out0.p)[static_cast<int64_t>(row) * p.out0.ld + r] = 0;
-        }
+        write_tables<ROWS_THREADS>(p, tiles, stride, part, bounds);
         return;
     }
     // chunks of 16 rows, counted group by group (with the groups that have rows
@@ -383,8 +392,9 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
         total &= 0xffff;
     }
     const int32_t n_clusters = static_cast<int32_t>(gridDim.x) / cluster - 1;
-    for (int32_t want = cid - 1; want < total; want += n_clusters)
-        rows_chunk<ROWS_THREADS>(p, X, ldx, A, lda, strideA, K, stride, cluster, rank, want, first_row, bounds, chunks, found, sums);
+    const int32_t bare = (first_row + 15) / 16 + (p.S - bounds[p.groups - 1] + 15) / 16;
+    for (int32_t want = cid - 1; want < total + bare; want += n_clusters)
+        rows_chunk<ROWS_THREADS>(p, X, ldx, A, lda, strideA, K, stride, cluster, rank, want, total, first_row, bounds, chunks, found, sums);
 }
 
 // ------------------------------------------------------------ launches
@@ -814,8 +824,9 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, cr.early ? adapter_rows_kernel<512> : adapter_rows_kernel<128>, p, static_cast<const uint16_t *>(x.p), x.ld, static_cast<const uint16_t *>(a.p),
-                               a.ld, a_shared ? int64_t(0) : a.stride, static_cast<int32_t>(K), static_cast<int32_t>(tiles),
+        e = cudaLaunchKernelEx(&cfg, cr.early ? adapter_rows_kernel<512> : adapter_rows_kernel<128>, p,
+                               static_cast<const uint16_t *>(x.p), x.ld, static_cast<const uint16_t *>(a.p), a.ld,
+                               a_shared ? int64_t(0) : a.stride, static_cast<int32_t>(K), static_cast<int32_t>(tiles),
                                static_cast<int32_t>(stride), cr.cluster, cr.early ? 1 : 0);
         if (e != cudaSuccess) return host_cuda_status(e);
     } else {

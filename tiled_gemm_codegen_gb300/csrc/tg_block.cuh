@@ -216,7 +216,7 @@ __device__ __forceinline__ void act_slope(float g, float &a, float &d)
         a = g < 0.0f ? 0.0f : g;  // (NaN stays NaN)
         d = g > 0.0f ? 1.0f : 0.0f;
     } else if (ACT == 2) {  // gelu, tanh form: s = (1 + tanh(c (g + 0.044715 g^3))) / 2
-        const float c = 0.7978845608028654f, g2 = g * g;
+        const float c = 0.7978845608028654f, g2 = fminf(g * g, 1e10f);  // (s is 0 or 1 there; an infinite g2 times 1 - s would be NaN)
         const float s = fast_sigmoid(2.0f * c * g * (1.0f + 0.044715f * g2));
         a = g * s;
         d = s + 2.0f * a * (1.0f - s) * c * (1.0f + 3.0f * 0.044715f * g2);
@@ -1091,7 +1091,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         for (int k = 0; k < 4; ++k) {
                             uint32_t x[4];
                             ld_shared_v4(rows_at + (k & 1) * 512u + (k >> 1) * BOX_BYTES, x);
-                            bad[0] |= non_finite(x[0] , x[1], x[2], x[3]);
+                            bad[0] |= non_finite(x[0], x[1], x[2], x[3]);
                         }
                     }
 #pragma unroll
