@@ -470,6 +470,7 @@ cudaError_t launch_block(int mode, BlockTiles tiles, const HostStream &hs, int64
 struct Cut {
     BlockTiles tiles;
     int64_t bn, features, units, splits;
+    int64_t depth;  // k-blocks of a tile; ADAPT: and of its adapters, in their time, about
     int64_t part_tiles() const { return splits > 1 ? units * (tiles == TILES_PAIR ? 2 : 1) : 0; }
     size_t part_bytes() const { return static_cast<size_t>(part_tiles()) * splits * BM * bn * 4; }
 };
@@ -496,8 +497,13 @@ int64_t split_of(int mode, const Cut &c, int64_t S, int64_t hit, int64_t depth, 
     return share == 0 ? 1 : std::min(SPLIT_MOST, cdiv(depth, share));
 }
 
+// ADAPT: how many adapters have rows, at most, and the columns of each.
+struct Adapters {
+    int64_t hit, Rp;
+};
+
 // Tiles of one kind for a product: `lanes` accumulator lanes a feature (GATED: 2).
-Cut cut_tiles(int mode, BlockTiles tiles, int64_t S, int64_t N, int64_t K, int64_t groups, int sms)
+Cut cut_tiles(int mode, BlockTiles tiles, int64_t S, int64_t N, int64_t K, int64_t groups, const Adapters &ad, int sms)
 {
     const int64_t lanes = mode == BLOCK_GATED ? 2 : 1, hit = std::min(groups, S);
     Cut c;
@@ -505,7 +511,17 @@ Cut cut_tiles(int mode, BlockTiles tiles, int64_t S, int64_t N, int64_t K, int64
     c.bn = tiles == TILES_PAIR ? 256 : tiles == TILES_FEW ? 32 : 128;
     c.features = (tiles == TILES_PAIR ? 256 : 128) / lanes;
     c.units = (groups == 1 ? cdiv(S, c.bn) : S / c.bn + hit) * cdiv(N, c.features);
-    c.splits = split_of(mode, c, S, hit, cdiv(K, BK), sms);
+    c.depth = cdiv(K, BK);
+    int64_t shared = c.depth;
+    if (mode == BLOCK_ADAPT) {
+        // (a tile's rows begin and end inside an adapter's; a block of theirs takes
+        // two of X W's time, and splitting pays for many of them only: u comes
+        // late, and one pair waits for it in any share)
+        const int64_t most = std::min({c.bn, ad.hit, ad.hit * c.bn / S + 1});
+        c.depth += 2 * adapter_blocks(static_cast<int32_t>(most), static_cast<int32_t>(ad.Rp));
+        if (c.depth > 2 * shared) shared = c.depth;
+    }
+    c.splits = split_of(mode, c, S, hit, shared, sms);
     return c;
 }
 
@@ -518,28 +534,35 @@ Cut cut_tiles(int mode, BlockTiles tiles, int64_t S, int64_t N, int64_t K, int64
 // of the two but for two calls within 4% (the estimate of the plain grouped
 // GEMM, whose epilogue is short, was up to 40% off: 512 rows, GRAD, 2048 x 2816:
 // 24 us in pairs, 17 in one-CTA tiles).
-double cut_cost(int mode, const Cut &c, int64_t S, int64_t N, int64_t K, int64_t groups, int sms)
+double cut_cost(int mode, const Cut &c, int64_t S, int64_t N, int64_t groups, int sms)
 {
     const bool pair = c.tiles == TILES_PAIR;
-    const double block = pair ? 0.33 : 0.29, out = mode == BLOCK_GRAD ? (pair ? 8 : 4) : pair ? 4 : 2.5;
+    const double block = pair ? 0.33 : 0.29, out = c.tiles == TILES_FEW ? 1 : mode == BLOCK_GRAD ? (pair ? 8 : 4) : pair ? 4 : 2.5;
     const int64_t hit = std::min(groups, S), workers = pair ? sms / 2 : sms;
     const int64_t rows = groups == 1 ? cdiv(S, c.bn) : std::max(hit, S / c.bn + (hit + 1) / 2);
     const int64_t units = rows * cdiv(N, c.features);
-    const double blocks = static_cast<double>(cdiv(K, BK)) / static_cast<double>(c.splits);
+    const double blocks = static_cast<double>(c.depth) / static_cast<double>(c.splits);
     return 4 + static_cast<double>(cdiv(units * c.splits, workers)) * std::max(blocks * block, c.splits > 1 ? 0.0 : out) + out +
            (c.splits > 1 ? (pair ? 5 : 3) : 0);
 }
 
 // One-CTA tiles of 32 rows where groups have few (the ring is then deeper:
-// weights are the traffic), else pairs or one CTA, whichever is quicker.
-Cut cut_rows(int mode, int64_t S, int64_t N, int64_t K, int64_t groups, int sms, const tg_options *opt)
+// weights are the traffic), else pairs or one CTA, whichever is quicker; ADAPT
+// also 32 rows where adapters have few, as a tile then has fewer of them (258 rows of
+// 64, 320 x 344, R = 16: 19 us in tiles of 128, 13 of 32; 256 of 128, 4096 x 4096:
+// 43 and 71).
+Cut cut_rows(int mode, int64_t S, int64_t N, int64_t K, int64_t groups, const Adapters &ad, int sms, const tg_options *opt)
 {
     const bool few = S <= 32 * std::min(groups, S);
-    const Cut one = cut_tiles(mode, few ? TILES_FEW : TILES_ONE, S, N, K, groups, sms);
+    Cut one = cut_tiles(mode, few ? TILES_FEW : TILES_ONE, S, N, K, groups, ad, sms);
+    if (mode == BLOCK_ADAPT && !few && S <= 32 * ad.hit) {  // (SHRINK's tiles are of 32 rows, too)
+        const Cut low = cut_tiles(mode, TILES_FEW, S, N, K, groups, ad, sms);
+        if (cut_cost(mode, low, S, N, groups, sms) < cut_cost(mode, one, S, N, groups, sms)) one = low;
+    }
     if (mode == BLOCK_SHRINK || (opt && opt->cta_pair == 1)) return one;
-    const Cut pair = cut_tiles(mode, TILES_PAIR, S, N, K, groups, sms);
+    const Cut pair = cut_tiles(mode, TILES_PAIR, S, N, K, groups, ad, sms);
     if (opt && opt->cta_pair == 2) return pair;
-    return !few && cut_cost(mode, pair, S, N, K, groups, sms) < cut_cost(mode, one, S, N, K, groups, sms) ? pair : one;
+    return !few && cut_cost(mode, pair, S, N, groups, sms) < cut_cost(mode, one, S, N, groups, sms) ? pair : one;
 }
 
 void set_cut(BlockParams &p, const Cut &c, int64_t N)
@@ -665,7 +688,7 @@ tg_status run_gated(int mode, Operand x, Operand w, Operand v, bool w_k, uint16_
     HostStream hs;
     tg_status st = host_stream(stream, &hs);
     if (st != TG_OK) return st;
-    const Cut c = cut_rows(mode, S, F, K, groups, hs.sms, opt);
+    const Cut c = cut_rows(mode, S, F, K, groups, Adapters{}, hs.sms, opt);
     if (c.units * c.splits > INT32_MAX) return TG_ERR_UNSUPPORTED;
 
     BlockParams p{};
@@ -732,8 +755,8 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     const int64_t Rp = R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : cdiv(R, 64) * 64;
     const int64_t hit = std::min(groups, S);
     // the adapters' first product, by group; the shared one, all rows
-    const Cut ca = cut_rows(BLOCK_SHRINK, S, R, K, groups, hs.sms, opt);
-    const Cut cy = cut_rows(BLOCK_ADAPT, S, N, K, 1, hs.sms, opt);
+    const Cut ca = cut_rows(BLOCK_SHRINK, S, R, K, groups, Adapters{}, hs.sms, opt);
+    const Cut cy = cut_rows(BLOCK_ADAPT, S, N, K, 1, Adapters{hit, Rp}, hs.sms, opt);
     if (ca.units * ca.splits > INT32_MAX || cy.units * cy.splits > INT32_MAX) return TG_ERR_UNSUPPORTED;
     const int64_t tiles = cdiv(S, cy.bn);
     // Few rows: u by adapter_rows_kernel, a fixed number of blocks a tile.

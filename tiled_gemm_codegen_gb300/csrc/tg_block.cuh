@@ -33,9 +33,9 @@
 // bits or more), two blocks with the same 64 rows of B: a pair of ring slots
 // of which the second holds lo alone, its MMAs reading the first one's B.  The zeros
 // of other adapters' rows must not meet an infinity or NaN in B (0 x NaN is
-// NaN): the epilogue's warps, idle until then, look through the tile's features
-// of each B; those that hold one go in as zeros and are added by the
-// epilogue, to their own rows alone.
+// NaN): the epilogue's warps look through B in the ring slots, before the MMAs
+// read them; rows that hold one are zeroed there and added by the
+// epilogue, to their adapter's rows alone.
 #pragma once
 
 #include "tg_adapter.cuh"
@@ -176,18 +176,6 @@ __device__ __forceinline__ bool non_finite(uint32_t a, uint32_t b, uint32_t c, u
     const uint32_t x = ((a & 0x7f807f80u) + 0x00800080u) | ((b & 0x7f807f80u) + 0x00800080u) | ((c & 0x7f807f80u) + 0x00800080u) |
                        ((d & 0x7f807f80u) + 0x00800080u);
     return (x & 0x80008000u) != 0;
-}
-
-// Whether one of the first n of 8 bf16 on 16 bytes is an infinity or NaN.
-__device__ __forceinline__ bool has_non_finite(const uint16_t *b, int32_t n)
-{
-    if (n >= 8) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(b));
-        return non_finite(x.x, x.y, x.z, x.w);
-    }
-    bool bad = false;
-    for (int32_t e = 0; e < n; ++e) bad |= (__ldg(b + e) & 0x7f80u) == 0x7f80u;
-    return bad;
 }
 
 // The MMA's N for a tile: its rows rounded up to 32 (16 a CTA of a pair).
@@ -359,10 +347,9 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     const uint32_t bar0 = ptx::smem_addr(bar_area);
     // barrier k at bar0 + 8k: [0, S) full, [S, 2S) empty, 2S+{0,1} tfull,
     // 2S+{2,3} tempty, 2S+4 mma-done, 2S+5 never completed; GRAD: from 2S+6
-    // two for each team of epilogue warps: z landed in the boxes; ADAPT: 2S+6 (a pair):
-    // every epilogue warp has looked through a unit's B; from 2S+7 (one CTA):
-    // they have looked through slot s, from 3S+7: B is on its way there (the
-    // epilogue may be two phases of full[s] ahead, which its parity would not tell)
+    // two for each team of epilogue warps: z landed in the boxes; ADAPT: from 2S+6:
+    // rows of B in slot s were looked through (by both CTAs' epilogues, at the
+    // leader), from 3S+6: they have landed (in this CTA)
     const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
     const uint32_t stall_bar = bar0 + 8u * (2 * STAGES + 5);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (4 * STAGES + 14));
@@ -373,22 +360,11 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
     auto tfull_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
     auto tempty_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
-    [[maybe_unused]] const uint32_t flag_bar = bar0 + 8u * (2 * STAGES + 6);
-    [[maybe_unused]] auto check_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + 7 + s); };
-    [[maybe_unused]] auto coming_bar = [&](uint32_t s) { return bar0 + 8u * (3 * STAGES + 7 + s); };
+    [[maybe_unused]] auto check_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + 6 + s); };
+    [[maybe_unused]] auto land_bar = [&](uint32_t s) { return bar0 + 8u * (3 * STAGES + 6 + s); };
     // ADAPT: byte j: of the 64 rows of B of a unit's j-th pair of blocks, which
     // eights hold an infinity or NaN.  All zero but while a unit has one.
     [[maybe_unused]] uint32_t *flag_words = reinterpret_cast<uint32_t *>(bar_area + 512);
-    // The eights that go in as zeros: those, in a pair of CTAs the whole boxes
-    // that TMA would have loaded with them.
-    [[maybe_unused]] auto flag_byte = [&](int32_t j) {
-        uint32_t byte = flag_words[j >> 2] >> (j & 3) * 8 & 0xffu;
-        for (int32_t per = min(p.Rp, 64) / 8, g = 0; PAIR && byte && g < 8; g += per) {
-            const uint32_t box = ((1u << per) - 1u) << g;
-            if (byte & box) byte |= box;
-        }
-        return byte;
-    };
     [[maybe_unused]] auto z_bar = [&](uint32_t duo, uint32_t b) { return bar0 + 8u * (2 * STAGES + 6 + 2 * duo + b); };
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -411,10 +387,9 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         ptx::mbar_init(stall_bar, 1);
         for (uint32_t i = 0; MODE == BLOCK_GRAD && i < EPI_WARPS; ++i) ptx::mbar_init(z_bar(0, i), 1);
         if (MODE == BLOCK_ADAPT) {
-            ptx::mbar_init(flag_bar, EPI_WARPS);
             for (uint32_t s = 0; s < STAGES; ++s) {
-                ptx::mbar_init(check_bar(s), EPI_WARPS);
-                ptx::mbar_init(coming_bar(s), 1);
+                ptx::mbar_init(check_bar(s), EPI_WARPS_TOTAL);
+                ptx::mbar_init(land_bar(s), 1);
             }
             for (int i = 0; i < (block_bar_bytes(MODE) - 512) / 4; ++i) flag_words[i] = 0;
         }
@@ -466,7 +441,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         // ------------------------------------------------ TMA producer
         uint32_t it = 0;
         uint32_t b_only = 0;  // bit s: slot s's last load brought rows alone
-        [[maybe_unused]] uint32_t flag_n = 0;  // ADAPT: units with blocks of u B before this one
+        [[maybe_unused]] uint32_t land_used = 0, land_phase = 0;  // bit s: land_bar(s) was used, parity of its next phase
         bool ok = true;
         const uint32_t full0 = PAIR ? ptx::map_to_cta(full_bar(0), 0u) : full_bar(0);
         for (int64_t t = worker; ok && block_walk_to<BN>(p, t, walk, w); t += n_workers) {
@@ -487,14 +462,6 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 if (MODE == BLOCK_ADAPT && i == w.mid) {
                     ext_range(p, w);
                     if (w.kb1 + w.e1 - w.e0 == i) break;
-                    if (PAIR && w.e0 < w.e1) {
-                        const int r = wait_bounded_warp(flag_bar, flag_n & 1u, wd);
-                        if (r != WAIT_OK) {
-                            if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_PRODUCER);
-                            ok = false;
-                            break;
-                        }
-                    }
                 }
                 const uint32_t s = it % STAGES;
                 const uint32_t ph = (it / STAGES) & 1u;
@@ -513,48 +480,45 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     else
                         ptx::tma_load_3d(dst, map, fb, c0, c1, c2);
                 };
-                auto expect = [&]() {
+                auto expect = [&](uint32_t bytes) {
                     if constexpr (PAIR) {
-                        if (leader) ptx::mbar_arrive_expect_tx(full_bar(s), 2 * G::STAGE);
+                        if (leader) ptx::mbar_arrive_expect_tx(full_bar(s), 2 * bytes);
                     } else {
-                        ptx::mbar_arrive_expect_tx(full_bar(s), G::STAGE);
+                        ptx::mbar_arrive_expect_tx(full_bar(s), bytes);
                     }
                 };
                 if (MODE == BLOCK_ADAPT && i >= w.mid && i - w.mid < w.e1 - w.e0) {
                     const int32_t e = w.e0 + i - w.mid;
-                    if (e & 1) {  // lo: its MMAs read the slot before's rows of B
-                        b_only |= 1u << s;
+                    b_only |= 1u << s;  // (the rows of B land on a barrier of their own)
+                    if (e & 1) {        // lo: its MMAs read the slot before's rows of B
                         if (ptx::elect_one()) {
-                            if constexpr (PAIR) {
-                                if (leader) ptx::mbar_arrive_expect_tx(full_bar(s), 2 * G::B_STAGE);
-                            } else {
-                                ptx::mbar_arrive_expect_tx(full_bar(s), G::B_STAGE);
-                            }
+                            expect(G::B_STAGE);
                             load(b_dst, &tmE, 0, (w.ad.blk0 + e) * BN + n_half, 0);
                         }
                         __syncwarp();
                         continue;
                     }
-                    b_only &= ~(1u << s);
-                    if (ptx::elect_one()) expect();
+                    if (ptx::elect_one()) {
+                        expect(G::B_STAGE);
+                        ptx::mbar_arrive_expect_tx(land_bar(s), G::A_STAGE);
+                    }
+                    land_used |= 1u << s;
+                    land_phase ^= 1u << s;
                     __syncwarp();
                     // a lane a box (rows of B past R read as zeros), and one for hi
                     const int32_t rows = min(p.Rp, 64), subs = 64 / rows, j = lane >> 1, h = lane & 1;
                     const int32_t a0 = e * 32 / p.Rp;
                     if (i == w.mid || a0 + subs > ad0 + 32) adapters(a0);
-                    int32_t id = __shfl_sync(0xffffffffu, ad, min(31, a0 - ad0 + j));
-                    // (one CTA's epilogue warps zero what they find in the slot instead)
-                    if (PAIR && j < subs && (flag_byte((i - w.mid) >> 1) >> (j * rows / 8) & 1u)) id = -1;
+                    const int32_t id = __shfl_sync(0xffffffffu, ad, min(31, a0 - ad0 + j));
                     if (j < subs) {
                         const int32_t r0 = id < 0 ? p.Rp : e * 32 % p.Rp, z = p.b_shared ? 0 : max(id, 0);
-                        load(a_dst + h * BOX_BYTES + static_cast<uint32_t>(j * rows) * 128u, &tmV, m0 + 64 * h, r0, z);
+                        ptx::tma_load_3d(a_dst + h * BOX_BYTES + static_cast<uint32_t>(j * rows) * 128u, &tmV, land_bar(s), m0 + 64 * h, r0, z);
                     } else if (lane == 31) {
                         load(b_dst, &tmE, 0, (w.ad.blk0 + e) * BN + n_half, 0);
                     }
-                    if (!PAIR && lane == 0) ptx::mbar_arrive(coming_bar(s));
                 } else if (b_only &= ~(1u << s); ptx::elect_one()) {
                     const int32_t kb = i < w.mid ? i : i - (w.e1 - w.e0);
-                    expect();
+                    expect(G::STAGE);
                     const int32_t z = p.w_shared ? 0 : w.g;
                     if constexpr (MODE == BLOCK_GATED) {
                         if (!p.w_k) {
@@ -574,7 +538,6 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 }
                 __syncwarp();
             }
-            if (MODE == BLOCK_ADAPT && w.e0 < w.e1) ++flag_n;
         }
         if (lane == 0) {
             issued_slot[0] = it;
@@ -584,6 +547,8 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 for (uint32_t j = first; j < it; ++j)
                     if (!wait_drain(full_bar(j % STAGES), (j / STAGES) & 1u, wd)) break;
             }
+            for (uint32_t s = 0; MODE == BLOCK_ADAPT && s < STAGES; ++s)
+                if ((land_used >> s & 1u) && !wait_drain(land_bar(s), (land_phase >> s & 1u) ^ 1u, wd)) break;
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -624,9 +589,10 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     const uint32_t s = it % STAGES;
                     const uint32_t ph = (it / STAGES) & 1u;
                     r = wait_bounded_warp(full_bar(s), ph, wd);
-                    if (!PAIR && ext && ((kb - w.mid) & 1) == 0 && r == WAIT_OK) {
+                    if (ext && ((kb - w.mid) & 1) == 0 && r == WAIT_OK) {
                         r = wait_bounded_warp(check_bar(s), check_phase >> s & 1u, wd);
                         check_phase ^= 1u << s;
+                        if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");  // (the other CTA's zeros)
                     }
                     if (r != WAIT_OK) {
                         if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_MMA);
@@ -821,8 +787,9 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         }
         if (MODE == BLOCK_SHRINK || MODE == BLOCK_ADAPT) ptx::griddep_wait();  // the tables
         uint32_t n = 0;
-        // ADAPT: ring slots of the units before this one; parities of coming_bar
-        [[maybe_unused]] uint32_t at_it = 0, coming_phase = 0;
+        // ADAPT: ring slots of the units before this one; parities of land_bar
+        [[maybe_unused]] uint32_t at_it = 0, land_phase = 0;
+        [[maybe_unused]] const uint32_t check_leader0 = PAIR ? ptx::map_to_cta(check_bar(0), 0u) : check_bar(0);
         uint32_t flip = 0;     // which of two boxes (GRAD: pairs of them) is next
         // GRAD: bit b: parity of z_bar(b)'s next phase; a copy is on its way there
         uint32_t z_phase = 0, z_out = 0;
@@ -1056,61 +1023,45 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             };
             // ADAPT: the rows of B that hold an infinity or NaN in this CTA's
             // features; they go in as zeros and are added to their own adapter's rows
-            // below.  A warp looks through eight rows of each pair of blocks: in
-            // the slot they have landed in, or, where the slot's barrier is the other
-            // CTA's, in memory.
+            // below.  A warp looks through eight rows of each pair of blocks, in the
+            // slot they have landed in.
             bool flagged = false;
             const int32_t pairs = (w.e1 - w.e0) / 2;
             if constexpr (MODE == BLOCK_ADAPT) {
                 at_it += static_cast<uint32_t>(w.mid - w.kb0);
                 bool fine = true;
-                for (int32_t j0 = 0; j0 < pairs && fine; j0 += PAIR ? 4 : 1) {
-                    bool bad[PAIR ? 4 : 1] = {};
-                    [[maybe_unused]] const uint32_t at = at_it + 2u * static_cast<uint32_t>(j0), slot = at % STAGES;
-                    [[maybe_unused]] const uint32_t rows_at = sA + slot * G::A_STAGE + static_cast<uint32_t>(warp - 2) * 1024u + lane * 16u;
-                    if constexpr (PAIR) {
-                        const int32_t f = f0 + 8 * (lane & 15);
-                        const bool ragged = __any_sync(0xffffffffu, f < p.N && p.N - f < 8);
+                for (int32_t j = 0; j < pairs; ++j) {
+                    const uint32_t slot = (at_it + 2u * static_cast<uint32_t>(j)) % STAGES;
+                    const uint32_t rows_at = sA + slot * G::A_STAGE + static_cast<uint32_t>(warp - 2) * 1024u + lane * 16u;
+                    const int r = wait_bounded_warp(land_bar(slot), land_phase >> slot & 1u, wd);
+                    land_phase ^= 1u << slot;
+                    if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
+                    fine = r == WAIT_OK;
+                    if (!fine) break;
+                    bool bad = false;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int32_t col = w.e0 * 32 + (j0 + (k >> 2)) * 64 + 8 * (warp - 2) + 2 * (k & 3) + (lane >> 4);
-                            const int32_t i = col / p.Rp, r = col - i * p.Rp;
-                            const bool in = j0 + (k >> 2) < pairs && i < w.ad.count && r < p.R && f < p.N;
-                            const int32_t id = in && !p.b_shared ? __ldcg(p.tab.ids + w.ad.first + i) : 0;
-                            const uint16_t *b = in ? p.b + id * p.strideB + r * p.ldb + f : p.b;
-                            bad[k >> 2] |= in && (ragged ? has_non_finite(b, p.N - f) : has_non_finite(b, 8));
-                        }
-                    } else {
-                        int r = wait_bounded_warp(coming_bar(slot), coming_phase >> slot & 1u, wd);
-                        coming_phase ^= 1u << slot;
-                        if (r == WAIT_OK) r = wait_bounded_warp(full_bar(slot), at / STAGES & 1u, wd);
-                        if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
-                        fine = r == WAIT_OK;
-                        if (!fine) break;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t x[4];
-                            ld_shared_v4(rows_at + (k & 1) * 512u + (k >> 1) * BOX_BYTES, x);
-                            bad[0] |= non_finite(x[0], x[1], x[2], x[3]);
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t x[4];
+                        ld_shared_v4(rows_at + (k & 1) * 512u + (k >> 1) * BOX_BYTES, x);
+                        bad |= non_finite(x[0], x[1], x[2], x[3]);
                     }
+                    if (__any_sync(0xffffffffu, bad)) {
+                        flagged = true;
+                        if (lane == 0) atomicOr(&flag_words[j >> 2], 1u << ((j & 3) * 8 + warp - 2));
 #pragma unroll
-                    for (int k = 0; k < (PAIR ? 4 : 1); ++k)
-                        if (__any_sync(0xffffffffu, bad[k])) {
-                            flagged = true;
-                            if (lane == 0) atomicOr(&flag_words[(j0 + k) >> 2], 1u << (((j0 + k) & 3) * 8 + warp - 2));
-                            if constexpr (!PAIR) {
-#pragma unroll
-                                for (int z = 0; z < 4; ++z) ptx::st_shared_v4(rows_at + (z & 1) * 512u + (z >> 1) * BOX_BYTES, 0u, 0u, 0u, 0u);
-                                ptx::fence_proxy_async_smem();
-                            }
-                        }
+                        for (int k = 0; k < 4; ++k) ptx::st_shared_v4(rows_at + (k & 1) * 512u + (k >> 1) * BOX_BYTES, 0u, 0u, 0u, 0u);
+                        ptx::fence_proxy_async_smem();
+                    }
                     __syncwarp();
-                    if (!PAIR && lane == 0) ptx::mbar_arrive(check_bar(slot));
+                    if (lane == 0) {
+                        if constexpr (PAIR)
+                            ptx::mbar_arrive_cluster(check_leader0 + 8u * slot);
+                        else
+                            ptx::mbar_arrive(check_bar(slot));
+                    }
                 }
                 at_it += static_cast<uint32_t>(w.kb1 - w.mid + w.e1 - w.e0);
                 if (pairs > 0) {
-                    if (PAIR && lane == 0) ptx::mbar_arrive(flag_bar);
                     if (!agree(fine, 1, 32 * EPI_WARPS)) break;
                     flagged = !agree(!flagged, 1, 32 * EPI_WARPS);
                 }
@@ -1121,7 +1072,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     const int32_t r0 = row_tile + 32 * c;
                     for (int32_t e = 0; e < pairs * 8; ++e) {
                         const int32_t col = w.e0 * 32 + e * 8, i = col / p.Rp, r8 = col - i * p.Rp;
-                        if (!(flag_byte(e >> 3) >> (e & 7) & 1u) || i >= w.ad.count) continue;
+                        if (!(flag_words[e >> 5] >> (e & 31) & 1u) || i >= w.ad.count) continue;
                         const int32_t id = p.b_shared ? 0 : __ldcg(p.tab.ids + w.ad.first + i);
                         const int32_t lo = max(__ldcg(p.tab.lo + w.ad.first + i), r0);
                         const int32_t hi = min(__ldcg(p.tab.hi + w.ad.first + i), min(limit, r0 + 32));
@@ -1144,7 +1095,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 }
             };
 
-            const bool empty = w.kb0 == w.kb1 && w.e0 == w.e1, shared = w.nparts > 1 && !empty;
+            const bool empty = w.kb0 == w.kb1 && w.e0 == w.e1, shared = w.nparts > 1;  // (a share may be empty: zeros)
             if (lanes_in && !shared) load_first();
             const uint32_t buf = n & 1u;
             if (!empty) {
