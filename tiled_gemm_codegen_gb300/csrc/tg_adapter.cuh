@@ -54,4 +54,20 @@ __device__ __forceinline__ void zero_columns(const BlockParams &p, int32_t in, i
         }
 }
 
+// The same for `rows` rows of a tile from `in` on, by `threads` threads of which this
+// is `id`.
+__device__ __forceinline__ void zero_rows(const BlockParams &p, const AdapterTile &ad, int32_t i, int32_t in, int32_t rows, int32_t id,
+                                          int32_t threads)
+{
+    const int32_t own = i * (p.Rp / 8), end = own + p.Rp / 8, all = adapter_blocks(ad.count, p.Rp) * 4;
+    if (all == end - own) return;
+    for (int32_t k = id; k < rows * all; k += threads) {
+        const int32_t row = k / all, u = k - row * all;
+        if (u >= own && u < end) continue;
+        uint16_t *at = p.wide + adapter_at(0, u * 8, ad.blk0, in + row, p.wide_bn, 0);
+        *reinterpret_cast<uint4 *>(at) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(at + static_cast<int64_t>(p.wide_bn) * 64) = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
 }  // namespace tg

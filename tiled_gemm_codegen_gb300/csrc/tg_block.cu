@@ -421,11 +421,11 @@ const BlockShape &shape_of(int mode, BlockTiles tiles, BlockShapeState **state)
     return shapes[mode][tiles];
 }
 
-cudaLaunchConfig_t block_config(const BlockShape &k, int grid, cudaStream_t s, cudaLaunchAttribute (&attr)[2])
+cudaLaunchConfig_t block_config(int mode, const BlockShape &k, int grid, cudaStream_t s, cudaLaunchAttribute (&attr)[2])
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(BLOCK_THREADS);
+    cfg.blockDim = dim3(static_cast<unsigned>(block_threads(mode, k.pair)));
     cfg.dynamicSmemBytes = static_cast<size_t>(k.smem);
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -450,7 +450,7 @@ cudaError_t launch_block(int mode, BlockTiles tiles, const HostStream &hs, int64
         cudaError_t e = cudaFuncSetAttribute(k.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
         if (e != cudaSuccess) return e;
         if (k.pair) {
-            cudaLaunchConfig_t cfg = block_config(k, 2, hs.stream, attr);
+            cudaLaunchConfig_t cfg = block_config(mode, k, 2, hs.stream, attr);
             cfg.numAttrs = 1;
             e = cudaOccupancyMaxActiveClusters(&pairs, k.kern, &cfg);
             if (e != cudaSuccess) return e;
@@ -462,7 +462,7 @@ cudaError_t launch_block(int mode, BlockTiles tiles, const HostStream &hs, int64
         }
     }
     const int64_t workers = std::max<int64_t>(1, std::min<int64_t>(units, k.pair ? pairs : hs.sms));
-    const cudaLaunchConfig_t cfg = block_config(k, static_cast<int>(workers) * (k.pair ? 2 : 1), hs.stream, attr);
+    const cudaLaunchConfig_t cfg = block_config(mode, k, static_cast<int>(workers) * (k.pair ? 2 : 1), hs.stream, attr);
     return cudaLaunchKernelEx(&cfg, k.kern, m.x, m.w, m.v, m.e, m.o, m.g, m.u, p);
 }
 
@@ -560,6 +560,7 @@ Cut cut_rows(int mode, int64_t S, int64_t N, int64_t K, int64_t groups, const Ad
         if (cut_cost(mode, low, S, N, groups, sms) < cut_cost(mode, one, S, N, groups, sms)) one = low;
     }
     if (mode == BLOCK_SHRINK || (opt && opt->cta_pair == 1)) return one;
+    if (mode == BLOCK_ADAPT && std::min<int64_t>(256, ad.hit) * ad.Rp > 64 * BLOCK_PAIRS) return one;
     const Cut pair = cut_tiles(mode, TILES_PAIR, S, N, K, groups, ad, sms);
     if (opt && opt->cta_pair == 2) return pair;
     return !few && cut_cost(mode, pair, S, N, groups, sms) < cut_cost(mode, one, S, N, groups, sms) ? pair : one;
@@ -834,7 +835,7 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     p.offsets = offsets;
     p.groups = static_cast<int32_t>(groups);
     p.N = static_cast<int32_t>(R);
-    p.out0 = BlockOut{U, ldu, 0};
+    p.out0 = BlockOut{U, ldu, U && tma_ok(U, ldu, 0, 2) ? 1 : 0};
     if (few) {
         py.ext_first = !cr.early && !pair && cy.units * cy.splits <= hs.sms ? 1 : 0;
         cudaLaunchConfig_t cfg{};

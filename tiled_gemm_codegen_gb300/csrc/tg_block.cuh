@@ -33,9 +33,12 @@
 // bits or more), two blocks with the same 64 rows of B: a pair of ring slots
 // of which the second holds lo alone, its MMAs reading the first one's B.  The zeros
 // of other adapters' rows must not meet an infinity or NaN in B (0 x NaN is
-// NaN): the epilogue's warps look through B in the ring slots, before the MMAs
-// read them; rows that hold one are zeroed there and added by the
-// epilogue, to their adapter's rows alone.
+// NaN): B is looked through in the ring slots, before the MMAs read them; rows
+// that hold one are zeroed there and added by the epilogue, to their
+// adapter's rows alone.  One CTA's epilogue warps look themselves; a pair has
+// two warps a CTA for it, as its tiles follow one another (12813 rows, 480 x 3984:
+// 83 us; 99 where the epilogue looks between two tiles, 151 where it looks in
+// memory; in one CTA the two warps cost the shortest calls 1 us of 16).
 #pragma once
 
 #include "tg_adapter.cuh"
@@ -167,6 +170,15 @@ __device__ __forceinline__ int32_t ext_first(const BlockParams &p, const BlockUn
 __device__ __forceinline__ int32_t ext_end(const BlockParams &p, const BlockUnit &u)
 {
     return min(u.ad.count, (u.e1 * 32 + p.Rp - 1) / p.Rp);
+}
+
+// A completed phase's arrivals from the other CTA, acquired (a fence of that
+// scope instead took the issuing warp a microsecond).
+__device__ __forceinline__ void acquire_cluster(uint32_t bar, uint32_t parity)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar),
+                 "r"(parity)
+                 : "memory");
 }
 
 // Whether one of eight bf16 is an infinity or NaN: adding the lowest bit of an
@@ -316,7 +328,7 @@ __device__ __forceinline__ void gated_grad_box(uint32_t addr, uint32_t up_off, c
 }
 
 template <int MODE, int BN, int STAGES, bool PAIR>
-__global__ void __launch_bounds__(BLOCK_THREADS, 1)
+__global__ void __launch_bounds__(block_threads(MODE, PAIR), 1)
     block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                  const __grid_constant__ CUtensorMap tmV,  // GATED: the up half of W; GRAD: of Z; ADAPT: B
                  const __grid_constant__ CUtensorMap tmE,  // GRAD: the gate half of Z; ADAPT: u's parts
@@ -348,8 +360,9 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     // barrier k at bar0 + 8k: [0, S) full, [S, 2S) empty, 2S+{0,1} tfull,
     // 2S+{2,3} tempty, 2S+4 mma-done, 2S+5 never completed; GRAD: from 2S+6
     // two for each team of epilogue warps: z landed in the boxes; ADAPT: from 2S+6:
-    // rows of B in slot s were looked through (by both CTAs' epilogues, at the
-    // leader), from 3S+6: they have landed (in this CTA)
+    // rows of B in slot s were looked through (in both CTAs, at the leader), from
+    // 3S+6: they have landed (in this CTA); a pair's: 4S+6+b: flags b of a unit are
+    // there, 4S+8+b: they may be written again
     const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
     const uint32_t stall_bar = bar0 + 8u * (2 * STAGES + 5);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_area + 8 * (4 * STAGES + 14));
@@ -362,9 +375,43 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
     auto tempty_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
     [[maybe_unused]] auto check_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + 6 + s); };
     [[maybe_unused]] auto land_bar = [&](uint32_t s) { return bar0 + 8u * (3 * STAGES + 6 + s); };
-    // ADAPT: byte j: of the 64 rows of B of a unit's j-th pair of blocks, which
-    // eights hold an infinity or NaN.  All zero but while a unit has one.
+    [[maybe_unused]] auto flag_bar = [&](uint32_t b) { return bar0 + 8u * (4 * STAGES + 6 + b); };
+    [[maybe_unused]] auto free_bar = [&](uint32_t b) { return bar0 + 8u * (4 * STAGES + 8 + b); };
+    // ADAPT: of the 64 rows of B of a unit's j-th pair of blocks, which eights
+    // hold an infinity or NaN.  One CTA: byte j, all zero but while a unit has one.  A
+    // pair, for its units in turn: four bits by each warp that looks, two j a byte.
     [[maybe_unused]] uint32_t *flag_words = reinterpret_cast<uint32_t *>(bar_area + 512);
+    [[maybe_unused]] auto flags_of = [&](uint32_t b, int who) {
+        return reinterpret_cast<volatile uint8_t *>(bar_area + 512 + (2 * b + who) * (BLOCK_PAIRS / 2));
+    };
+    // Looks through a warp's eights of rows, from `eight` on, in slot s and zeroes
+    // those that hold one: a bit for each.  (Behind land_bar(s).)
+    [[maybe_unused]] auto look = [&](uint32_t s, int eight) -> uint32_t {
+        constexpr int N = PAIR ? 8 / BLOCK_LOOK_WARPS : 8 / EPI_WARPS;
+        const uint32_t rows_at = sA + s * G::A_STAGE + static_cast<uint32_t>(eight) * 1024u + (threadIdx.x & 31) * 16u;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t x[4];
+                ld_shared_v4(rows_at + e * 1024u + (k & 1) * 512u + (k >> 1) * BOX_BYTES, x);
+                bad |= non_finite(x[0], x[1], x[2], x[3]);
+            }
+            if (bad) bits |= 1u << e;
+        }
+        bits = __reduce_or_sync(0xffffffffu, bits);
+        if (bits) {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                for (int k = 0; k < 4 && (bits >> e & 1u); ++k)
+                    ptx::st_shared_v4(rows_at + e * 1024u + (k & 1) * 512u + (k >> 1) * BOX_BYTES, 0u, 0u, 0u, 0u);
+            ptx::fence_proxy_async_smem();
+        }
+        __syncwarp();
+        return bits;
+    };
     [[maybe_unused]] auto z_bar = [&](uint32_t duo, uint32_t b) { return bar0 + 8u * (2 * STAGES + 6 + 2 * duo + b); };
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -388,8 +435,12 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         for (uint32_t i = 0; MODE == BLOCK_GRAD && i < EPI_WARPS; ++i) ptx::mbar_init(z_bar(0, i), 1);
         if (MODE == BLOCK_ADAPT) {
             for (uint32_t s = 0; s < STAGES; ++s) {
-                ptx::mbar_init(check_bar(s), EPI_WARPS_TOTAL);
+                ptx::mbar_init(check_bar(s), PAIR ? 2 * BLOCK_LOOK_WARPS : EPI_WARPS);
                 ptx::mbar_init(land_bar(s), 1);
+            }
+            for (uint32_t b = 0; PAIR && b < 2; ++b) {
+                ptx::mbar_init(flag_bar(b), BLOCK_LOOK_WARPS);
+                ptx::mbar_init(free_bar(b), EPI_WARPS);
             }
             for (int i = 0; i < (block_bar_bytes(MODE) - 512) / 4; ++i) flag_words[i] = 0;
         }
@@ -592,7 +643,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     if (ext && ((kb - w.mid) & 1) == 0 && r == WAIT_OK) {
                         r = wait_bounded_warp(check_bar(s), check_phase >> s & 1u, wd);
                         check_phase ^= 1u << s;
-                        if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");  // (the other CTA's zeros)
+                        if (PAIR) acquire_cluster(check_bar(s), (check_phase >> s & 1u) ^ 1u);  // (the other CTA's zeros)
                     }
                     if (r != WAIT_OK) {
                         if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_MMA);
@@ -650,7 +701,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             }
             __syncwarp();
         }
-    } else {
+    } else if (warp < 2 + EPI_WARPS) {
         // ------------------------------------------------ epilogue
         const int q = warp & 3;             // tensor-memory lane quadrant of this warp
         const int turn = (warp - 2) >> 2;   // which of the quadrant's two warps
@@ -757,27 +808,11 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         };
 
         // SHRINK: a unit's rows lie in two of ADAPT's tiles at most (which are
-        // no lower than its own): theirs, and its adapter's place among theirs.
-        [[maybe_unused]] int32_t tile0 = 0, place0 = 0, place1 = 0;
-        [[maybe_unused]] AdapterTile ad0{}, ad1{};
-        // where the first part of value r of a row stands
-        [[maybe_unused]] auto wide_at = [&](int32_t row, int32_t r) {
-            const int32_t tile = row / p.wide_bn, in = row - tile * p.wide_bn;
-            const bool second = tile != tile0;
-            return p.wide + adapter_at(second ? place1 : place0, r, second ? ad1.blk0 : ad0.blk0, in, p.wide_bn, p.Rp);
-        };
-        // zeros in the other adapters' columns of a unit's rows
-        auto zero_others = [&](const BlockUnit &w, int32_t row_tile, int32_t limit) {
-            if constexpr (MODE == BLOCK_SHRINK) {
-                if (w.tn != 0) return;
-                for (int32_t row = row_tile + (warp - 2); row < limit; row += EPI_WARPS) {
-                    const int32_t tile = row / p.wide_bn, in = row - tile * p.wide_bn;
-                    const bool second = tile != tile0;
-                    const int32_t count = second ? ad1.count : ad0.count;
-                    if (count * p.Rp % 64 || count > 1) zero_columns(p, in, second ? ad1.blk0 : ad0.blk0, count, second ? place1 : place0, lane);
-                }
-            }
-        };
+        // no lower than its own), the second from row `bound`: where the first parts of
+        // this lane's 8 values of row 0 would stand.
+        [[maybe_unused]] int32_t bound = 0;
+        [[maybe_unused]] uint16_t *wide0 = nullptr, *wide1 = nullptr;
+        [[maybe_unused]] float scale = 1.0f;
 
         bool ok = true;
         if (p.debug_stall) {  // watchdog self-test: a barrier that nothing completes
@@ -787,9 +822,9 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
         }
         if (MODE == BLOCK_SHRINK || MODE == BLOCK_ADAPT) ptx::griddep_wait();  // the tables
         uint32_t n = 0;
-        // ADAPT: ring slots of the units before this one; parities of land_bar
-        [[maybe_unused]] uint32_t at_it = 0, land_phase = 0;
-        [[maybe_unused]] const uint32_t check_leader0 = PAIR ? ptx::map_to_cta(check_bar(0), 0u) : check_bar(0);
+        // ADAPT: one CTA: ring slots of the units before this one, parities of
+        // land_bar; a pair: units with blocks of u B before this one
+        [[maybe_unused]] uint32_t at_it = 0, land_phase = 0, flag_n = 0;
         uint32_t flip = 0;     // which of two boxes (GRAD: pairs of them) is next
         // GRAD: bit b: parity of z_bar(b)'s next phase; a copy is on its way there
         uint32_t z_phase = 0, z_out = 0;
@@ -804,12 +839,19 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             const bool lanes_in = MODE == BLOCK_SHRINK ? f_warp < p.Rp : f_box < p.N;  // uniform in a team
 
             if constexpr (MODE == BLOCK_SHRINK) {
-                tile0 = row_tile / p.wide_bn;
-                ad0 = adapter_tile(p, tile0);
-                ad1 = adapter_tile(p, (limit - 1) / p.wide_bn);
+                const int32_t tile0 = row_tile / p.wide_bn, tile1 = (limit - 1) / p.wide_bn, r = f_warp + 8 * (lane & 3);
+                const AdapterTile ad0 = adapter_tile(p, tile0), ad1 = adapter_tile(p, tile1);
                 const int32_t place = __ldcg(p.tab.rank + w.g);
-                place0 = place - ad0.first;
-                place1 = place - ad1.first;
+                if (p.scales) scale = __ldg(p.scales + w.g);
+                bound = (tile0 + 1) * p.wide_bn;
+                wide0 = p.wide + adapter_at(place - ad0.first, r, ad0.blk0, -tile0 * p.wide_bn, p.wide_bn, p.Rp);
+                wide1 = p.wide + adapter_at(place - ad1.first, r, ad1.blk0, -tile1 * p.wide_bn, p.wide_bn, p.Rp);
+                // zeros in the other adapters' columns, while the product is made
+                if (w.tn == 0 && w.part == 0) {
+                    const int32_t mid = min(limit, bound), id = (warp - 2) * 32 + lane;
+                    zero_rows(p, ad0, place - ad0.first, row_tile - tile0 * p.wide_bn, mid - row_tile, id, 32 * EPI_WARPS);
+                    zero_rows(p, ad1, place - ad1.first, mid - tile1 * p.wide_bn, limit - mid, id, 32 * EPI_WARPS);
+                }
             }
 
             // GRAD: z of piece c into the pair of boxes `b`, gate and up half.
@@ -980,7 +1022,6 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 } else {  // SHRINK
                     // parts -> this warp's two boxes of 32 rows x 64 bytes (16-byte units
                     // swizzled by the row's pair), then 16 bytes of a row a lane
-                    const float scale = p.scales ? __ldg(p.scales + w.g) : 1.0f;
                     const uint32_t at = area + static_cast<uint32_t>((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
                     __syncwarp();  // the boxes were read
 #pragma unroll
@@ -1000,7 +1041,7 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         stmatrix_trans(at + 2048u + oct * 512u, lo[0], lo[1], lo[2], lo[3]);
                     }
                     __syncwarp();
-#pragma unroll 1
+#pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int j = (lane >> 2) + 8 * k, u = lane & 3;
                         const int32_t row = row0 + j, r = f_warp + 8 * u;
@@ -1008,14 +1049,18 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                         ld_shared_v4(area + j * 64u + ((u ^ ((j >> 1) & 3)) << 4), hi);
                         ld_shared_v4(area + 2048u + j * 64u + ((u ^ ((j >> 1) & 3)) << 4), lo);
                         if (row >= limit || r >= p.Rp) continue;
-                        uint16_t *to = wide_at(row, r);
+                        uint16_t *to = (row < bound ? wide0 : wide1) + static_cast<int64_t>(row) * 64;
                         *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(p.wide_bn) * 64) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         if (p.out0.p) {
                             uint16_t *o = static_cast<uint16_t *>(p.out0.p) + static_cast<int64_t>(row) * p.out0.ld + r;
+                            if (p.out0.tma && r + 8 <= p.R) {  // (rows on 16 bytes)
+                                *reinterpret_cast<uint4 *>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (r + e < p.R) o[e] = static_cast<uint16_t>(hi[e >> 1] >> (16 * (e & 1)));
+                                for (int e = 0; e < 8; ++e)
+                                    if (r + e < p.R) o[e] = static_cast<uint16_t>(hi[e >> 1] >> (16 * (e & 1)));
+                            }
                         }
                     }
                 }
@@ -1023,42 +1068,24 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
             };
             // ADAPT: the rows of B that hold an infinity or NaN in this CTA's
             // features; they go in as zeros and are added to their own adapter's rows
-            // below.  A warp looks through eight rows of each pair of blocks, in the
-            // slot they have landed in.
+            // below.  A warp looks through eight rows of each pair of blocks.
             bool flagged = false;
             const int32_t pairs = (w.e1 - w.e0) / 2;
-            if constexpr (MODE == BLOCK_ADAPT) {
+            if constexpr (MODE == BLOCK_ADAPT && !PAIR) {
                 at_it += static_cast<uint32_t>(w.mid - w.kb0);
                 bool fine = true;
                 for (int32_t j = 0; j < pairs; ++j) {
                     const uint32_t slot = (at_it + 2u * static_cast<uint32_t>(j)) % STAGES;
-                    const uint32_t rows_at = sA + slot * G::A_STAGE + static_cast<uint32_t>(warp - 2) * 1024u + lane * 16u;
                     const int r = wait_bounded_warp(land_bar(slot), land_phase >> slot & 1u, wd);
                     land_phase ^= 1u << slot;
                     if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
                     fine = r == WAIT_OK;
                     if (!fine) break;
-                    bool bad = false;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t x[4];
-                        ld_shared_v4(rows_at + (k & 1) * 512u + (k >> 1) * BOX_BYTES, x);
-                        bad |= non_finite(x[0], x[1], x[2], x[3]);
-                    }
-                    if (__any_sync(0xffffffffu, bad)) {
+                    if (look(slot, warp - 2)) {
                         flagged = true;
                         if (lane == 0) atomicOr(&flag_words[j >> 2], 1u << ((j & 3) * 8 + warp - 2));
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) ptx::st_shared_v4(rows_at + (k & 1) * 512u + (k >> 1) * BOX_BYTES, 0u, 0u, 0u, 0u);
-                        ptx::fence_proxy_async_smem();
                     }
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (PAIR)
-                            ptx::mbar_arrive_cluster(check_leader0 + 8u * slot);
-                        else
-                            ptx::mbar_arrive(check_bar(slot));
-                    }
+                    if (lane == 0) ptx::mbar_arrive(check_bar(slot));
                 }
                 at_it += static_cast<uint32_t>(w.kb1 - w.mid + w.e1 - w.e0);
                 if (pairs > 0) {
@@ -1066,13 +1093,19 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                     flagged = !agree(!flagged, 1, 32 * EPI_WARPS);
                 }
             }
+            auto is_flagged = [&](int32_t e) {
+                if constexpr (PAIR)
+                    return (flags_of(flag_n & 1u, e >> 2 & 1)[e >> 4] >> ((e >> 3 & 1) * 4 + (e & 3)) & 1) != 0;
+                else
+                    return (flag_words[e >> 5] >> (e & 31) & 1u) != 0;
+            };
             auto add_flagged = [&](int c, uint32_t (&v)[32]) {
                 if constexpr (MODE == BLOCK_ADAPT) {
                     if (!flagged) return;
                     const int32_t r0 = row_tile + 32 * c;
                     for (int32_t e = 0; e < pairs * 8; ++e) {
                         const int32_t col = w.e0 * 32 + e * 8, i = col / p.Rp, r8 = col - i * p.Rp;
-                        if (!(flag_words[e >> 5] >> (e & 31) & 1u) || i >= w.ad.count) continue;
+                        if (!is_flagged(e) || i >= w.ad.count) continue;
                         const int32_t id = p.b_shared ? 0 : __ldcg(p.tab.ids + w.ad.first + i);
                         const int32_t lo = max(__ldcg(p.tab.lo + w.ad.first + i), r0);
                         const int32_t hi = min(__ldcg(p.tab.hi + w.ad.first + i), min(limit, r0 + 32));
@@ -1102,10 +1135,16 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 const uint32_t tph = (n >> 1) & 1u;
                 ++n;
                 // (the warps that meet at barriers below leave together)
-                const int r = wait_bounded(tfull_bar(buf), tph, wd);
+                int r = wait_bounded(tfull_bar(buf), tph, wd);
+                if (MODE == BLOCK_ADAPT && PAIR && pairs > 0 && r == WAIT_OK) {
+                    r = wait_bounded(flag_bar(flag_n & 1u), flag_n >> 1 & 1u, wd);
+                    for (int32_t i = lane; r == WAIT_OK && i < (pairs + 1) / 2; i += 32)
+                        flagged |= (flags_of(flag_n & 1u, 0)[i] | flags_of(flag_n & 1u, 1)[i]) != 0;
+                    flagged = __any_sync(0xffffffffu, flagged);
+                }
                 if (r == WAIT_TIMEOUT) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
                 const bool here = r == WAIT_OK;
-                if (!(shared || flagged ? agree(here, 1, 32 * EPI_WARPS)
+                if (!(shared || (flagged && !PAIR) ? agree(here, 1, 32 * EPI_WARPS)
                       : team == 1       ? __all_sync(0xffffffffu, here) != 0
                                         : agree(here, team_id, 32 * team)))
                     break;
@@ -1178,11 +1217,15 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 __threadfence();
                 if (lanes_in) load_first();
             }
-            if (ok && (!shared || *last_flag)) zero_others(w, row_tile, limit);
+            if (MODE == BLOCK_ADAPT && PAIR && pairs > 0) {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(free_bar(flag_n & 1u));
+                ++flag_n;
+            }
             // (the flags, of the last share and of B, may be written again)
-            if (shared || flagged) ok = agree(ok, 1, 32 * EPI_WARPS);
+            if (shared || (flagged && !PAIR)) ok = agree(ok, 1, 32 * EPI_WARPS);
             if (!ok) break;
-            if (flagged) {
+            if (flagged && !PAIR) {
                 for (int32_t i = (warp - 2) * 32 + lane; i * 4 < pairs; i += 32 * EPI_WARPS) flag_words[i] = 0;
                 ptx::named_barrier_sync(1, 32 * EPI_WARPS);
             }
@@ -1226,6 +1269,39 @@ __global__ void __launch_bounds__(BLOCK_THREADS, 1)
                 if ((z_out >> b) & 1u) wait_drain(z_bar(duo, b), (z_phase >> b) & 1u, wd);
         }
         __syncwarp();
+    } else if constexpr (MODE == BLOCK_ADAPT && PAIR) {
+        // ------------------------------------------------ B's infinities and NaN
+        const int who = warp - 2 - EPI_WARPS;
+        const uint32_t check_leader0 = ptx::map_to_cta(check_bar(0), 0u);
+        uint32_t at_it = 0, land_phase = 0, n = 0;  // ring slots and units with blocks of u B before this one
+        bool ok = true;
+        for (int64_t t = worker; ok && block_walk_to<BN>(p, t, walk, w); t += n_workers) {
+            ext_range(p, w);
+            const int32_t pairs = (w.e1 - w.e0) / 2;
+            at_it += static_cast<uint32_t>(w.mid - w.kb0);
+            if (pairs > 0) {
+                const uint32_t b = n & 1u;
+                int r = wait_bounded_warp(free_bar(b), (n >> 1 & 1u) ^ 1u, wd);
+                uint32_t bits = 0;
+                for (int32_t j = 0; j < pairs && r == WAIT_OK; ++j) {
+                    const uint32_t slot = (at_it + 2u * static_cast<uint32_t>(j)) % STAGES;
+                    r = wait_bounded_warp(land_bar(slot), land_phase >> slot & 1u, wd);
+                    land_phase ^= 1u << slot;
+                    if (r != WAIT_OK) break;
+                    bits |= look(slot, 4 * who) << (j & 1) * 4;
+                    if (lane == 0) {
+                        ptx::mbar_arrive_cluster(check_leader0 + 8u * slot);
+                        flags_of(b, who)[j >> 1] = static_cast<uint8_t>(bits);
+                    }
+                    if (j & 1) bits = 0;
+                }
+                if (r == WAIT_TIMEOUT && lane == 0) raise_abort(wd, ERR_TIMEOUT_EPILOGUE);
+                ok = r == WAIT_OK;
+                if (ok && lane == 0) ptx::mbar_arrive(flag_bar(b));
+                ++n;
+            }
+            at_it += static_cast<uint32_t>(w.kb1 - w.mid + w.e1 - w.e0);
+        }
     }
 
     __syncthreads();

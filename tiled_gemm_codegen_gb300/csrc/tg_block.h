@@ -72,14 +72,20 @@ __host__ __device__ constexpr int block_epi_bytes(int mode, int bn)
     return (mode == BLOCK_GATED || mode == BLOCK_GRAD) && bn > 32 ? 65536 : 32768;
 }
 
-// Barriers, and ADAPT's flags: a byte for each pair of blocks that a tile may
-// have (256 rows of as many adapters of R = 256 at most).
-__host__ __device__ constexpr int block_bar_bytes(int mode) { return mode == BLOCK_ADAPT ? 2048 : 512; }
+// Barriers, and ADAPT's flags: a byte for each pair of blocks that a unit may have (a
+// tile of 128 rows of as many adapters of R = 256: 512), in a pair of CTAs for two
+// units (its tiles of 256 rows are not taken for more).
+constexpr int BLOCK_PAIRS = 768;
+__host__ __device__ constexpr int block_bar_bytes(int mode) { return mode == BLOCK_ADAPT ? 512 + 2 * BLOCK_PAIRS : 512; }
 
 // (12 or 16 epilogue warps take up to 10% less time for K = 256, where the epilogue
 // is most of a tile, and up to 3% more for K = 4096.)
 constexpr int BLOCK_EPI_WARPS = 8;
-constexpr int BLOCK_THREADS = 64 + 32 * BLOCK_EPI_WARPS;
+constexpr int BLOCK_LOOK_WARPS = 2;  // ADAPT, a pair
+__host__ __device__ constexpr int block_threads(int mode, bool pair)
+{
+    return 64 + 32 * (BLOCK_EPI_WARPS + (mode == BLOCK_ADAPT && pair ? BLOCK_LOOK_WARPS : 0));
+}
 
 using BlockKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
                              const CUtensorMap, const CUtensorMap, const BlockParams);
