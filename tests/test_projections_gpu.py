@@ -598,6 +598,16 @@ def test_packed_operands_give_the_same_bits(S, sizes):
     assert all(torch.equal(a, b) for a, b in zip(run(off), run(off, tg.make_options(force_pack=1))))
 
 
+@pytest.mark.parametrize("bounds", [[0, 30, 30, 100], [0, 0, 0, 100], [5, 30, 2 ** 31 - 1, 2 ** 31 - 1], [-5, 30, 20, 400], [0, 30, 100, -2 ** 31],
+                                    [100, 0, 50, 100], [0, 0, 0, 0]])
+def test_packed_operands_of_groups_without_rows(bounds):
+    """Matrices that meet no rows are not copied: whatever the bounds are, those
+    that the product reads are."""
+    run, _ = _calls(100, [30, 70, 0])
+    off = torch.tensor(bounds, dtype=torch.int32, device=dev())
+    assert all(torch.equal(a, b) for a, b in zip(run(off), run(off, tg.make_options(force_pack=1))))
+
+
 def test_two_streams_at_once():
     runs = [_calls(S, sizes, seed) for S, sizes, seed in ((700, [300, 400], 110), (900, [1, 899], 120))]
     offs = [_offsets([300, 400]), _offsets([1, 899])]

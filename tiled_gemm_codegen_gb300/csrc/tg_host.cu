@@ -58,6 +58,7 @@ struct PackJob {
     uint16_t *dst;
     int64_t rows, cols, ld_src, s_src, ld_dst, chunks;
     uintptr_t span_begin, span_end;  // bytes of the source this job may read
+    const int32_t *offsets = nullptr;  // where given: matrices of groups without rows are left out
 };
 
 __device__ __forceinline__ uint32_t pack_pair(uint16_t lo, uint16_t hi)
@@ -101,9 +102,20 @@ __global__ void pack_bf16_kernel(PackJob ja, PackJob jb, int blocks_a)
     const int64_t nblocks = is_a ? blocks_a : gridDim.x - blocks_a;
     const int64_t chunks_per_row = j.ld_dst / 8;
     for (int64_t c = bid * blockDim.x + threadIdx.x; c < j.chunks; c += nblocks * blockDim.x) {
-        const int64_t row_g = c / chunks_per_row;
+        int64_t row_g, b;
+        if (j.chunks <= UINT32_MAX) {  // (divisions of 64 bits are what leaving matrices out costs)
+            row_g = static_cast<uint32_t>(c) / static_cast<uint32_t>(chunks_per_row);
+            b = static_cast<uint32_t>(row_g) / static_cast<uint32_t>(j.rows);
+        } else {
+            row_g = c / chunks_per_row;
+            b = row_g / j.rows;
+        }
+        if (j.offsets && __ldg(j.offsets + b + 1) <= __ldg(j.offsets + b)) {  // on to the last chunk of this thread's here
+            const int64_t step = nblocks * blockDim.x, rest = (b + 1) * j.rows * chunks_per_row - 1 - c;
+            if (rest >= step) c += rest / step * step;
+            continue;
+        }
         const int64_t col0 = (c - row_g * chunks_per_row) * 8;
-        const int64_t b = row_g / j.rows;
         const int64_t r = row_g - b * j.rows;
         const uint16_t *s = j.src + b * j.s_src + r * j.ld_src + col0;
         uint4 out;
@@ -1040,6 +1052,8 @@ cudaError_t host_pack(const HostStream &hs, const HostPack *a, const HostPack *b
     PackJob ja{}, jb{};
     if (a) ja = pack_job(a->src, static_cast<uint16_t *>(a->dst), a->rows, a->cols, a->ld, a->nb, a->stride);
     if (b) jb = pack_job(b->src, static_cast<uint16_t *>(b->dst), b->rows, b->cols, b->ld, b->nb, b->stride);
+    if (a) ja.offsets = a->offsets;
+    if (b) jb.offsets = b->offsets;
     const int blocks_a = a ? grid_for(ja.chunks, hs.sms) : 0;
     const int blocks_b = b ? grid_for(jb.chunks, hs.sms) : 0;
     pack_bf16_kernel<<<blocks_a + blocks_b, 256, 0, hs.stream>>>(ja, jb, blocks_a);

@@ -50,10 +50,13 @@ bool host_encode_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, ui
 
 // One operand of a realign pass: nb matrices of rows x cols bf16 (row pitch
 // ld, `stride` elements between matrices) -> dst, rows pack_pitch(cols) apart.
+// offsets (int32 [nb + 1] on the device, or null): a matrix g with offsets[g + 1] <=
+// offsets[g] meets no rows and is left out.
 struct HostPack {
     const void *src = nullptr;
     void *dst = nullptr;
     int64_t rows = 0, cols = 0, ld = 0, nb = 0, stride = 0;
+    const int32_t *offsets = nullptr;
 };
 cudaError_t host_pack(const HostStream &hs, const HostPack *a, const HostPack *b);  // either may be null
 
