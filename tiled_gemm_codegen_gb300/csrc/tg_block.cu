@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) adapter_rows_kernel(const BlockP
                                                                     int64_t lda, int64_t strideA, int32_t K, int32_t tiles,
                                                                     int32_t stride, int32_t cluster, int32_t early)
 {
+    ptx::griddep_wait();  // (before the kernel behind this one may start: it reads the call's inputs at once)
     if (early) ptx::griddep_launch_dependents();
     constexpr int WARPS = ROWS_THREADS / 32;
     __shared__ int32_t part[32], bounds[ROWS_GROUPS], chunks[ROWS_GROUPS];
@@ -776,6 +777,7 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
     p.k_blocks = static_cast<int32_t>(cdiv(K, BK));
     p.R = static_cast<int32_t>(R);
     p.Rp = static_cast<int32_t>(Rp);
+    p.used_most = static_cast<int32_t>(hit);
     p.wide_bn = static_cast<int32_t>(cy.bn);
     p.scales = scales;
     const bool force = opt && opt->force_pack;
@@ -843,12 +845,14 @@ tg_status run_adapted(Operand x, Operand w, bool w_k, Operand a, Operand b, void
         cfg.gridDim = dim3(static_cast<unsigned>(cr.clusters * cr.cluster));
         cfg.blockDim = dim3(cr.early ? 512 : 128);
         cfg.stream = hs.stream;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = static_cast<unsigned>(cr.cluster);
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(cr.cluster);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
         e = cudaLaunchKernelEx(&cfg, cr.early ? adapter_rows_kernel<512> : adapter_rows_kernel<128>, p,
                                static_cast<const uint16_t *>(x.p), x.ld, static_cast<const uint16_t *>(a.p), a.ld,
                                a_shared ? int64_t(0) : a.stride, static_cast<int32_t>(K), static_cast<int32_t>(tiles),

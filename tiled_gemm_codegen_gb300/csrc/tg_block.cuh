@@ -505,12 +505,15 @@ __global__ void __launch_bounds__(block_threads(MODE, PAIR), 1)
             const int32_t n0 = w.row0 + w.tm * BN + n_half;
             // ADAPT: lane l holds the tile's adapter ad0 + l (-1: none)
             int32_t ad0 = 0, ad = -1;
+            [[maybe_unused]] int32_t early_id = 0;  // of adapter `lane`: the first tile's begin with the first
             auto adapters = [&](int32_t from) {
                 ad0 = from;
-                ad = from + lane < ext_end(p, w) ? __ldcg(p.tab.ids + w.ad.first + from + lane) : -1;
+                ad = from + lane < ext_end(p, w) ? !PAIR && w.tm == 0 && from == 0 ? early_id : __ldcg(p.tab.ids + w.ad.first + from + lane) : -1;
             };
             for (int32_t i = w.kb0; i < w.kb1 + w.e1 - w.e0 || (MODE == BLOCK_ADAPT && i == w.mid); ++i, ++it) {
                 if (MODE == BLOCK_ADAPT && i == w.mid) {
+                    ptx::griddep_wait();
+                    if (!PAIR && w.tm == 0) early_id = __ldcg(p.tab.ids + min(lane, p.used_most - 1));  // beside the tile's entry
                     ext_range(p, w);
                     if (w.kb1 + w.e1 - w.e0 == i) break;
                 }

@@ -43,6 +43,7 @@ struct BlockParams {
     const float *scales;     // [groups] or null
     uint16_t *wide;          // u's parts: [block][bn rows][64]
     int32_t R, Rp;
+    int32_t used_most;       // min(groups, S): the length of the tables of adapters with rows
     int32_t wide_bn;         // rows of ADAPT's tiles
     int32_t ext_first;       // ADAPT: a unit's blocks of u B come before those of X W (u is there when the
                              // kernel starts, and no unit before this one keeps the epilogue from looking
