@@ -530,15 +530,16 @@ Cut cut_tiles(int mode, BlockTiles tiles, int64_t S, int64_t N, int64_t K, int64
 // the workers (over groups that end anywhere in a tile) of so much a k-block or of
 // an epilogue, whichever is longer, the last one's epilogue, and where tiles
 // are shared the adding.  Measured: a k-block 0.29 in 128 x 128 tiles, 0.33 in pairs'
-// 256 x 256; an epilogue 4 and 8 (GRAD, which reads z), 2.5 and 4.  In 26 calls
-// of 300 to 16384 rows, K 256 to 6144, F 512 to 14336, it foretells the quicker
-// of the two but for two calls within 4% (the estimate of the plain grouped
-// GEMM, whose epilogue is short, was up to 40% off: 512 rows, GRAD, 2048 x 2816:
-// 24 us in pairs, 17 in one-CTA tiles).
+// 256 x 256; the epilogues' are fitted to the choice in 130 calls of 200 to 32768
+// rows, K 128 to 8192, 64 to 14336 features: the tiles chosen take 0.1% longer than the
+// better ones on average, ADAPT's 1.1% (the estimate of the plain grouped GEMM,
+// whose epilogue is short, was up to 40% off: 512 rows, GRAD, 2048 x 2816: 24 us in
+// pairs, 17 in one-CTA tiles).
 double cut_cost(int mode, const Cut &c, int64_t S, int64_t N, int64_t groups, int sms)
 {
     const bool pair = c.tiles == TILES_PAIR;
-    const double block = pair ? 0.33 : 0.29, out = c.tiles == TILES_FEW ? 1 : mode == BLOCK_GRAD ? (pair ? 8 : 4) : pair ? 4 : 2.5;
+    const double block = pair ? 0.33 : 0.29;
+    const double out = c.tiles == TILES_FEW ? 1 : mode == BLOCK_ADAPT ? (pair ? 5 : 3) : pair ? 6 : mode == BLOCK_GRAD ? 3.5 : 2.5;
     const int64_t hit = std::min(groups, S), workers = pair ? sms / 2 : sms;
     const int64_t rows = groups == 1 ? cdiv(S, c.bn) : std::max(hit, S / c.bn + (hit + 1) / 2);
     const int64_t units = rows * cdiv(N, c.features);

@@ -39,6 +39,13 @@
 // two warps a CTA for it, as its tiles follow one another (12813 rows, 480 x 3984:
 // 83 us; 99 where the epilogue looks between two tiles, 151 where it looks in
 // memory; in one CTA the two warps cost the shortest calls 1 us of 16).
+//
+// Measured (one GB300, calls in a captured graph): bound by the tensor pipe in
+// batches (GATED, 8192 rows, 4096 x 2 * 8192, z kept: 546-570 us, 1.93-2.01 PFLOP/s,
+// pipe 91% active; GRAD of it: 345 us, 74%), by HBM in decoding (one row, 8192 x 2 *
+// 14336: 78 us, 6.0 TB/s), by the epilogue's instructions where contractions are
+// short (16384 rows, 256 x 2 * 2048: 71 us, 81 with z), and by a chain of dependent
+// steps in small ADAPT calls (one row, 4096 x 4096, R = 16: 15 us; 64 rows of 40: 25).
 #pragma once
 
 #include "tg_adapter.cuh"
