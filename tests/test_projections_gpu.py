@@ -441,6 +441,55 @@ def test_adapters_stay_in_their_rows(R, K, pair):
     assert np.array_equal(Y, y, equal_nan=True)
 
 
+@pytest.mark.parametrize("R", [8, 24])
+@pytest.mark.parametrize("pair", [1, 2])
+def test_an_infinite_row_beside_infinities_of_its_adapter(R, pair):
+    """u of a row is infinite and its B holds an infinity: the other
+    features are the formula's infinities, no NaN of a zeroed product."""
+    sizes, K, N = [4, 6, 3], 72, 200
+    (X, W, A, B), (xv, wv, av, bv) = _adapters(sizes, K, N, R, 87)
+    B[B == 0], bv[bv == 0] = 1, 1  # (0 x infinity is the formula's NaN)
+    A[1], av[1] = 1, 1
+    X[6], xv[6] = 1, 1
+    X[6, 3], xv[6, 3] = float("inf"), np.inf
+    B[1, 2, 9], bv[1, 2, 9] = NAN, np.nan
+    B[1, 5, 140], bv[1, 5, 140] = float("inf"), np.inf
+    W[:], wv[:] = 0, 0
+    W[3], wv[3] = 1, 1
+    B[1], bv[1] = B[1].abs(), np.abs(bv[1])
+    Y = _np(tg.gemm_adapted(X, W, A, B, _offsets(sizes), options=tg.make_options(cta_pair=pair)))
+    with np.errstate(all="ignore"):
+        y, _ = adapted(xv, wv, av, bv, sizes)
+    both = np.zeros_like(y, bool)
+    both[6, 140] = True  # an infinite u on an infinity of B: NaN here
+    assert np.array_equal(np.where(both, 0, Y), np.where(both, 0, y), equal_nan=True)
+    assert not np.isfinite(Y[6]).any() and np.isnan(Y[6]).sum() == 2
+
+
+@pytest.mark.parametrize("R", [8, 16, 40])
+@pytest.mark.parametrize("K,N", [(64, 1500), (500, 520), (0, 1500)])
+@pytest.mark.parametrize("pair", [1, 2])
+def test_adapters_stay_in_their_rows_of_many_tiles(R, K, N, pair):
+    """The same over several tiles a worker, one behind another: some have an
+    infinity, some none, all are what the formula gives."""
+    sizes = [(37 * i) % 450 for i in range(40)]
+    S = sum(sizes) + 300
+    (X, W, A, B), _ = _adapters(sizes, K, N, R, 85, S=S)
+    g = np.random.default_rng(3)
+    for val in (float("inf"), NAN, float("-inf")):
+        for _ in range(8):
+            B[int(g.integers(40)), int(g.integers(R)), int(g.integers(N))] = val
+    want = X.double() @ W.double()
+    at = 0
+    for i, n in enumerate(sizes):
+        want[at:at + n] += (X[at:at + n].double() @ A[i].double().t()) @ B[i].double()
+        at += n
+    for _ in range(3):
+        Y = tg.gemm_adapted(X, W, A, B, _offsets(sizes), options=tg.make_options(cta_pair=pair))
+        assert torch.equal(torch.isnan(Y), torch.isnan(want))
+        assert torch.equal(torch.nan_to_num(Y.double(), 0, 1e30, -1e30), torch.nan_to_num(want, 0, 1e30, -1e30))
+
+
 @pytest.mark.parametrize("sizes,K,N,R", [([0, 300, 17, 1000, 256], 1024, 640, 16), ([2] * 40 + [0] * 9, 2048, 200, 64), ([700], 520, 392, 100)])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_adapted_random_values(sizes, K, N, R, dtype):

@@ -33,9 +33,9 @@
 // bits or more), two blocks with the same 64 rows of B: a pair of ring slots
 // of which the second holds lo alone, its MMAs reading the first one's B.  The zeros
 // of other adapters' rows must not meet an infinity or NaN in B (0 x NaN is
-// NaN): B is looked through in the ring slots, before the MMAs read them; rows
-// that hold one are zeroed there and added by the epilogue, to their
-// adapter's rows alone.  One CTA's epilogue warps look themselves; a pair has
+// NaN): B is looked through in the ring slots, before the MMAs read them; what is
+// not finite is zeroed there and added by the epilogue, to its
+// adapter's rows alone (an infinite u on an infinity of B makes NaN).  One CTA's epilogue warps look themselves; a pair has
 // two warps a CTA for it, as its tiles follow one another (12813 rows, 480 x 3984:
 // 83 us; 99 where the epilogue looks between two tiles, 151 where it looks in
 // memory; in one CTA the two warps cost the shortest calls 1 us of 16).
@@ -195,6 +195,14 @@ __device__ __forceinline__ bool non_finite(uint32_t a, uint32_t b, uint32_t c, u
     const uint32_t x = ((a & 0x7f807f80u) + 0x00800080u) | ((b & 0x7f807f80u) + 0x00800080u) | ((c & 0x7f807f80u) + 0x00800080u) |
                        ((d & 0x7f807f80u) + 0x00800080u);
     return (x & 0x80008000u) != 0;
+}
+
+// Two bf16, infinities and NaN as zeros.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t x)
+{
+    if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+    if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+    return x;
 }
 
 // The MMA's N for a tile: its rows rounded up to 32 (16 a CTA of a pair).
@@ -391,8 +399,8 @@ __global__ void __launch_bounds__(block_threads(MODE, PAIR), 1)
     [[maybe_unused]] auto flags_of = [&](uint32_t b, int who) {
         return reinterpret_cast<volatile uint8_t *>(bar_area + 512 + (2 * b + who) * (BLOCK_PAIRS / 2));
     };
-    // Looks through a warp's eights of rows, from `eight` on, in slot s and zeroes
-    // those that hold one: a bit for each.  (Behind land_bar(s).)
+    // Looks through a warp's eights of rows, from `eight` on, in slot s, and zeroes the
+    // infinities and NaN: a bit for each eight that held one.  (Behind land_bar(s).)
     [[maybe_unused]] auto look = [&](uint32_t s, int eight) -> uint32_t {
         constexpr int N = PAIR ? 8 / BLOCK_LOOK_WARPS : 8 / EPI_WARPS;
         const uint32_t rows_at = sA + s * G::A_STAGE + static_cast<uint32_t>(eight) * 1024u + (threadIdx.x & 31) * 16u;
@@ -412,8 +420,12 @@ __global__ void __launch_bounds__(block_threads(MODE, PAIR), 1)
         if (bits) {
 #pragma unroll
             for (int e = 0; e < N; ++e)
-                for (int k = 0; k < 4 && (bits >> e & 1u); ++k)
-                    ptx::st_shared_v4(rows_at + e * 1024u + (k & 1) * 512u + (k >> 1) * BOX_BYTES, 0u, 0u, 0u, 0u);
+                for (int k = 0; k < 4 && (bits >> e & 1u); ++k) {
+                    const uint32_t at = rows_at + e * 1024u + (k & 1) * 512u + (k >> 1) * BOX_BYTES;
+                    uint32_t x[4];
+                    ld_shared_v4(at, x);
+                    ptx::st_shared_v4(at, finite_halves(x[0]), finite_halves(x[1]), finite_halves(x[2]), finite_halves(x[3]));
+                }
             ptx::fence_proxy_async_smem();
         }
         __syncwarp();
@@ -1076,9 +1088,9 @@ __global__ void __launch_bounds__(block_threads(MODE, PAIR), 1)
                 }
                 return true;
             };
-            // ADAPT: the rows of B that hold an infinity or NaN in this CTA's
-            // features; they go in as zeros and are added to their own adapter's rows
-            // below.  A warp looks through eight rows of each pair of blocks.
+            // ADAPT: infinities and NaN of B in this CTA's features; they go in as
+            // zeros and are added to their own adapter's rows below.  A warp looks
+            // through eight rows of each pair of blocks.
             bool flagged = false;
             const int32_t pairs = (w.e1 - w.e0) / 2;
             if constexpr (MODE == BLOCK_ADAPT && !PAIR) {
@@ -1126,11 +1138,12 @@ __global__ void __launch_bounds__(block_threads(MODE, PAIR), 1)
                             float sum = 0.0f;
 #pragma unroll 1
                             for (int32_t r = r8; r < min(r8 + 8, p.R); ++r) {
+                                const uint32_t bits = p.b[id * p.strideB + r * p.ldb + f];
+                                if ((bits & 0x7f80u) != 0x7f80u) continue;
                                 const uint16_t *at = p.wide + adapter_at(i, r, w.ad.blk0, row - row_tile, BN, p.Rp);
                                 const float u = __uint_as_float(static_cast<uint32_t>(at[0]) << 16) +
                                                 __uint_as_float(static_cast<uint32_t>(at[BN * 64]) << 16);
-                                const float bv = __uint_as_float(static_cast<uint32_t>(p.b[id * p.strideB + r * p.ldb + f]) << 16);
-                                sum = __fmaf_rn(u, bv, sum);
+                                sum = __fmaf_rn(u, __uint_as_float(bits << 16), sum);
                             }
                             v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), sum));
                         }
