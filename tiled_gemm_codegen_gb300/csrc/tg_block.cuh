@@ -418,14 +418,13 @@ __global__ void __launch_bounds__(block_threads(MODE, PAIR), 1)
         }
         bits = __reduce_or_sync(0xffffffffu, bits);
         if (bits) {
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                for (int k = 0; k < 4 && (bits >> e & 1u); ++k) {
-                    const uint32_t at = rows_at + e * 1024u + (k & 1) * 512u + (k >> 1) * BOX_BYTES;
-                    uint32_t x[4];
-                    ld_shared_v4(at, x);
-                    ptx::st_shared_v4(at, finite_halves(x[0]), finite_halves(x[1]), finite_halves(x[2]), finite_halves(x[3]));
-                }
+#pragma unroll 1
+            for (int k = 0; k < 4 * N; ++k) {
+                const uint32_t at = rows_at + (k >> 2) * 1024u + (k & 1) * 512u + (k >> 1 & 1) * BOX_BYTES;
+                uint32_t x[4];
+                ld_shared_v4(at, x);
+                ptx::st_shared_v4(at, finite_halves(x[0]), finite_halves(x[1]), finite_halves(x[2]), finite_halves(x[3]));
+            }
             ptx::fence_proxy_async_smem();
         }
         __syncwarp();
