@@ -34,9 +34,9 @@
 // of which the second holds lo alone, its MMAs reading the first one's B.  The zeros
 // of other adapters' rows must not meet an infinity or NaN in B (0 x NaN is
 // NaN): B is looked through in the ring slots, before the MMAs read them; what is
-// not finite is zeroed there and added by the epilogue, to its
-// adapter's rows alone (an infinite u on an infinity of B makes NaN).  One CTA's epilogue warps look themselves; a pair has
-// two warps a CTA for it, as its tiles follow one another (12813 rows, 480 x 3984:
+// not finite is zeroed there and added by the epilogue, to its adapter's rows
+// alone (an infinite u on an infinity of B makes NaN).  One CTA's epilogue warps
+// look themselves; a pair has two warps a CTA for it, as its tiles follow one another (12813 rows, 480 x 3984:
 // 83 us; 99 where the epilogue looks between two tiles, 151 where it looks in
 // memory; in one CTA the two warps cost the shortest calls 1 us of 16).
 //
